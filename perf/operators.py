@@ -89,7 +89,7 @@ def _blocks(k):
 
 def _weights(g, lead, k):
     """MX weights: rows of `lead`, K values each.  Codes as quantised normal values have them, scales spread over some octaves, the last
-    block's codes zero past K, one block in 64 all zero.  Scale rows are padded to whole 4-byte words."""
+    block's codes zero past K, one block in 64 all zero.  Scale rows are padded to whole 16 bytes."""
     nb = _blocks(k)
     nib = (torch.randn(lead + (nb * BLOCK,), generator=g, device="cuda") * 2.4).round_().abs_().clamp_(max=7).to(torch.uint8)
     nib += torch.randint(0, 2, nib.shape, generator=g, device="cuda", dtype=torch.uint8) * 8
@@ -97,7 +97,7 @@ def _weights(g, lead, k):
     rare = torch.rand(lead + (nb, 1), generator=g, device="cuda") < 1 / 64
     nib = nib.reshape(lead + (nb, BLOCK)).masked_fill_(rare, 0).reshape(lead + (nb * BLOCK,))
     codes = nib[..., 0::2] | (nib[..., 1::2] << 4)
-    scales = torch.zeros(lead + (4 * ((nb + 3) // 4),), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(lead + (16 * ((nb + 15) // 16),), dtype=torch.uint8, device="cuda")
     mid = 126 - int(round(math.log2(max(k, 4)) / 2))
     scales[..., :nb] = torch.randint(mid - 2, mid + 2, lead + (nb,), generator=g, device="cuda", dtype=torch.uint8)
     return codes.contiguous(), scales
