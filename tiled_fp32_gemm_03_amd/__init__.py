@@ -23,6 +23,12 @@ Raw C-ABI mirrors (same names and argument order as ``include/gemm_f32.h``):
   gemm_mixed(M, N, K, A, lda, B, ldb, C, ldc, format, config, stream)
   gemm_mixed_tile(config, M, N, K) -> dict, gemm_mixed_num_configs()
                                                         (include/gemm_mixed.h)
+  gemm_mx_quantize(rows, K, X, ldx, format, along, codes, ld, scales, lds, stream)
+  gemm_mx_dequantize(rows, K, codes, ld, scales, lds, Y, ldy, format, along, stream)
+  gemm_mx(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, c_format, config, stream)
+  gemm_mx_tile(config, M, N, K) -> dict, gemm_mx_num_configs()
+  gemm_mx_a16(M, N, K, A, lda, a_format, B, ldb, SB, ldsb, C, ldc, c_format, stream)
+  gemm_mx_code_bytes(K), gemm_mx_scale_bytes(K)         (include/gemm_mx.h)
 Pointers are device addresses (ints); ``stream`` is a hipStream_t as int
 (0 = null stream).  A non-zero status raises ``GemmError``.
 
@@ -34,6 +40,14 @@ result); ``format`` names the 16-bit format when A and B hold raw codes
 (int16 / uint16).  ``matmul_splitk(A, B, out=None, config=-1, splits=0,
 workspace=None)`` runs the split-K form; it allocates the workspace as a torch
 tensor when none is given.
+
+4-bit microscaled (MX) matrices are ``MxTensor``s, rows of K values in blocks
+of 32 along K.  ``mx_quantize(X, along="rows")`` makes one from a float32,
+bfloat16 or float16 matrix; ``along="columns"`` takes its columns as the rows
+(a product's right operand).  ``mx_dequantize(q, dtype, along)`` reads the
+values back.  ``matmul_mx(A, B, dtype=torch.float32)`` is the product of the
+rows of A (an ``MxTensor``, or a bfloat16 or float16 matrix) with the rows of
+the ``MxTensor`` B, C[i][j] = sum_k A[i][k] B[j][k].
 """
 from __future__ import annotations
 
@@ -54,6 +68,9 @@ __all__ = [
     "NOALLOC_SCRATCH_BYTES",
     "gemm_mixed", "gemm_mixed_tile", "gemm_mixed_num_configs", "matmul_mixed", "MIXED_FORMATS",
     "mixed_config_name",
+    "MxTensor", "MX_FORMATS", "MX_ALONG", "mx_quantize", "mx_dequantize", "matmul_mx",
+    "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx", "gemm_mx_tile", "gemm_mx_num_configs",
+    "gemm_mx_a16", "gemm_mx_code_bytes", "gemm_mx_scale_bytes",
     "library_path",
     "exported_symbols",
 ]
@@ -101,6 +118,14 @@ _SIGS = {
     "gemm_mixed": ([_i, _i, _i, _p, _i, _p, _i, _p, _i, _i, _i, _p], _i),
     "gemm_mixed_num_configs": ([], _i),
     "gemm_mixed_tile": ([_i, _i, _i, _i, _ip, _ip, _ip, _ip, _ip], _i),
+    "gemm_mx_code_bytes": ([_i], _ll),
+    "gemm_mx_scale_bytes": ([_i], _ll),
+    "gemm_mx_quantize": ([_i, _i, _p, _i, _i, _i, _p, _i, _p, _i, _p], _i),
+    "gemm_mx_dequantize": ([_i, _i, _p, _i, _p, _i, _p, _i, _i, _i, _p], _i),
+    "gemm_mx": ([_i, _i, _i, _p, _i, _p, _i, _p, _i, _p, _i, _p, _i, _i, _i, _p], _i),
+    "gemm_mx_num_configs": ([], _i),
+    "gemm_mx_tile": ([_i, _i, _i, _i, _ip, _ip, _ip, _ip, _ip], _i),
+    "gemm_mx_a16": ([_i, _i, _i, _p, _i, _i, _p, _i, _p, _i, _p, _i, _i, _p], _i),
     "gemm_f32_probe_lds_bytes": ([_i, _i], _ll),
     "gemm_f32_device_props": ([_i, _ip, _ip, _ip, _ip, _ip], _i),
     "gemm_f32_probe_fused": ([_i, _i, _i, _p, _ll, _p, _p], _i),
@@ -122,6 +147,10 @@ FUSED_BOTH, FUSED_MFMA, FUSED_STORE = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 64 << 20
 # Input formats of include/gemm_mixed.h.
 MIXED_FORMATS = {"bf16": 0, "f16": 1}
+# Formats of unquantised matrices and the ways blocks run (include/gemm_mx.h).
+MX_FORMATS = {"bf16": 0, "f16": 1, "f32": 2}
+MX_ALONG = {"rows": 0, "columns": 1}
+_MX_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class GemmError(RuntimeError):
@@ -306,6 +335,70 @@ def gemm_mixed_tile(config, M, N, K) -> dict:
     return {"BM": bm, "BN": bn, "BK": bk, "threads": nt, "config": chosen}
 
 
+def _mx_format(fmt) -> int:
+    if isinstance(fmt, str):
+        try:
+            return MX_FORMATS[fmt]
+        except KeyError:
+            raise ValueError(f"unknown format {fmt!r}; one of {sorted(MX_FORMATS)}") from None
+    return int(fmt)
+
+
+def _along(along) -> int:
+    if isinstance(along, str):
+        try:
+            return MX_ALONG[along]
+        except KeyError:
+            raise ValueError(f"unknown direction {along!r}; one of {sorted(MX_ALONG)}") from None
+    return int(along)
+
+
+def gemm_mx_code_bytes(K) -> int:
+    return int(_lib.gemm_mx_code_bytes(int(K)))
+
+
+def gemm_mx_scale_bytes(K) -> int:
+    return int(_lib.gemm_mx_scale_bytes(int(K)))
+
+
+def gemm_mx_quantize(rows, K, X, ldx, format, along, codes, ld, scales, lds, stream=0) -> None:
+    _check(_lib.gemm_mx_quantize(rows, K, X or None, ldx, _mx_format(format), _along(along),
+                                 codes or None, ld, scales or None, lds, stream or None),
+           "gemm_mx_quantize")
+
+
+def gemm_mx_dequantize(rows, K, codes, ld, scales, lds, Y, ldy, format, along, stream=0) -> None:
+    _check(_lib.gemm_mx_dequantize(rows, K, codes or None, ld, scales or None, lds, Y or None, ldy,
+                                   _mx_format(format), _along(along), stream or None),
+           "gemm_mx_dequantize")
+
+
+def gemm_mx(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, c_format, config=-1,
+            stream=0) -> None:
+    _check(_lib.gemm_mx(M, N, K, A or None, lda, SA or None, ldsa, B or None, ldb, SB or None,
+                        ldsb, C or None, ldc, _mx_format(c_format), int(config), stream or None),
+           "gemm_mx")
+
+
+def gemm_mx_num_configs() -> int:
+    return int(_lib.gemm_mx_num_configs())
+
+
+def gemm_mx_tile(config, M, N, K) -> dict:
+    vals = [ctypes.c_int(0) for _ in range(5)]
+    rc = _lib.gemm_mx_tile(int(config), M, N, K, *[ctypes.byref(v) for v in vals])
+    _check(rc, "gemm_mx_tile")
+    bm, bn, bk, nt, chosen = (v.value for v in vals)
+    return {"BM": bm, "BN": bn, "BK": bk, "threads": nt, "config": chosen}
+
+
+def gemm_mx_a16(M, N, K, A, lda, a_format, B, ldb, SB, ldsb, C, ldc, c_format, stream=0) -> None:
+    _check(_lib.gemm_mx_a16(M, N, K, A or None, lda, _format(a_format), B or None, ldb,
+                            SB or None, ldsb, C or None, ldc, _mx_format(c_format),
+                            stream or None),
+           "gemm_mx_a16")
+
+
 def config_name(variant, config: int = -1, M: int = 1, N: int = 1, K: int = 1) -> str:
     """Readable name of a launch-table entry, e.g. "prod#0:128x128x32/256t"."""
     t = gemm_f32_tile(variant, config, M, N, K)
@@ -426,4 +519,161 @@ def matmul_splitk(A, B, out=None, config: int = -1, splits: int = 0, workspace=N
     ldc = max(_ld(out), max(1, N))
     gemm_f32_splitk(M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, out.data_ptr(), ldc, config,
                     splits, ws_ptr, ws_bytes, stream)
+    return out
+
+
+class MxTensor:
+    """A matrix in 4-bit microscaled form (include/gemm_mx.h): ``codes`` and
+    ``scales`` are uint8 tensors of ``rows`` rows (more leading dimensions for a
+    stack of matrices), each row 16 ceil(K / 32) bytes of codes and
+    16 ceil(K / 512) bytes of scales."""
+
+    __slots__ = ("codes", "scales", "K")
+
+    def __init__(self, codes, scales, K: int):
+        K = int(K)
+        if K < 0:
+            raise ValueError("K must be >= 0")
+        blocks = (K + 31) // 32
+        for name, t, need in (("codes", codes, 16 * blocks), ("scales", scales, 16 * ((blocks + 15) // 16))):
+            if t.dtype != torch.uint8:
+                raise TypeError(f"{name} must be uint8")
+            if t.dim() < 2 or t.shape[-1] < need:
+                raise ValueError(f"{name} must have rows of at least {need} bytes for K = {K}")
+        if codes.shape[:-1] != scales.shape[:-1]:
+            raise ValueError("codes and scales must have the same rows")
+        self.codes, self.scales, self.K = codes, scales, K
+
+    @property
+    def shape(self):
+        """(rows, K), after any leading dimensions."""
+        return (*self.codes.shape[:-1], self.K)
+
+    @classmethod
+    def empty(cls, rows: int, K: int, device) -> "MxTensor":
+        return cls(torch.empty((rows, gemm_mx_code_bytes(K)), dtype=torch.uint8, device=device),
+                   torch.empty((rows, gemm_mx_scale_bytes(K)), dtype=torch.uint8, device=device), K)
+
+
+def _row_pitch(t) -> int:
+    """Row pitch in bytes of a 2-D uint8 tensor with contiguous rows."""
+    rows, width = t.shape
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError("rows must be contiguous (last stride 1)")
+    if rows > 1:
+        if t.stride(0) < width:
+            raise ValueError("rows overlap (row stride smaller than the row length)")
+        return t.stride(0)
+    return max(16, (width + 15) // 16 * 16)
+
+
+def _mx_args(q, name: str, device):
+    if not isinstance(q, MxTensor):
+        raise TypeError(f"{name} must be an MxTensor")
+    if q.codes.dim() != 2:
+        raise ValueError(f"{name} must be one matrix (2-D codes and scales)")
+    if not q.codes.is_cuda or q.codes.device != device or q.scales.device != device:
+        raise TypeError(f"{name} must be on {device} like the other operands")
+    return (q.codes.data_ptr(), max(16, _row_pitch(q.codes)),
+            q.scales.data_ptr(), max(16, _row_pitch(q.scales)))
+
+
+def _on(device):
+    """Makes `device` the current one for a launch (cheap when it is)."""
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else _SAME
+
+
+class _Same:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_SAME = _Same()
+
+
+def _mx_out(out, shape, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.dtype != dtype or tuple(out.shape) != tuple(shape) or out.device != device:
+        raise TypeError(f"out must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out
+
+
+def mx_quantize(X, along: str = "rows", out=None, stream=None):
+    """The MX form of a float32, bfloat16 or float16 CUDA matrix with unit last
+    stride: of its rows, or (``along="columns"``) of its columns."""
+    if X.dtype not in _MX_DTYPES or not X.is_cuda:
+        raise TypeError("X must be a float32, bfloat16 or float16 CUDA tensor")
+    ldx = _ld(X)
+    way = _along(along)
+    rows, K = X.shape if way == 0 else (X.shape[1], X.shape[0])
+    if out is None:
+        out = MxTensor.empty(rows, K, X.device)
+    elif out.shape != (rows, K):
+        raise ValueError(f"out must be an MxTensor of shape {(rows, K)}")
+    codes, ld, scales, lds = _mx_args(out, "out", X.device)
+    if stream is None:
+        stream = torch.cuda.current_stream(X.device).cuda_stream
+    with _on(X.device):
+        gemm_mx_quantize(rows, K, X.data_ptr(), ldx, _MX_DTYPES[X.dtype], way, codes, ld, scales,
+                         lds, stream)
+    return out
+
+
+def mx_dequantize(q, dtype=torch.float32, along: str = "rows", out=None, stream=None):
+    """The values of an MxTensor as a matrix of ``dtype``: its rows as rows, or
+    (``along="columns"``) as columns."""
+    if dtype not in _MX_DTYPES:
+        raise TypeError("dtype must be float32, bfloat16 or float16")
+    device = q.codes.device
+    codes, ld, scales, lds = _mx_args(q, "q", device)
+    way = _along(along)
+    rows, K = q.shape
+    out = _mx_out(out, (rows, K) if way == 0 else (K, rows), dtype, device)
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    with _on(device):
+        gemm_mx_dequantize(rows, K, codes, ld, scales, lds, out.data_ptr(), _ld(out),
+                           _MX_DTYPES[dtype], way, stream)
+    return out
+
+
+def matmul_mx(A, B, dtype=torch.float32, out=None, config: int = -1, stream=None):
+    """C[i][j] = sum_k A[i][k] B[j][k] for the rows of A and of the MxTensor B.
+
+    A is an MxTensor, or a bfloat16 or float16 CUDA matrix with unit last
+    stride (whose values enter as they are; ``config`` is then not taken).
+    ``dtype`` is the result's: float32, bfloat16 or float16.
+    """
+    if dtype not in _MX_DTYPES:
+        raise TypeError("dtype must be float32, bfloat16 or float16")
+    if not isinstance(B, MxTensor):
+        raise TypeError("B must be an MxTensor")
+    device = B.codes.device
+    b = _mx_args(B, "B", device)
+    N, K = B.shape
+    mx = isinstance(A, MxTensor)
+    if mx:
+        a = _mx_args(A, "A", device)
+    else:
+        if A.dtype not in (torch.bfloat16, torch.float16) or A.device != device:
+            raise TypeError(f"A must be an MxTensor, or a bfloat16 or float16 tensor on {device}")
+        if config != -1:
+            raise ValueError("config is for products of two MxTensors")
+        a = (A.data_ptr(), _ld(A), _MX_DTYPES[A.dtype])
+    M, K2 = A.shape
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} and {tuple(B.shape)}")
+    out = _mx_out(out, (M, N), dtype, device)
+    ldc = _ld(out)
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    with _on(device):
+        if mx:
+            gemm_mx(M, N, K, *a, *b, out.data_ptr(), ldc, _MX_DTYPES[dtype], config, stream)
+        else:
+            gemm_mx_a16(M, N, K, *a, *b, out.data_ptr(), ldc, _MX_DTYPES[dtype], stream)
     return out

@@ -22,10 +22,10 @@ LIB = os.path.join(HERE, "libgemm_f32.so")
 ARCH = "gfx950"
 
 SOURCES = ["gemm_f32_abi.hip", "naive_tiled.hip", "prod.hip", "w16_vgpr.hip", "valu.hip", "mixed.hip",
-           "mixed16.hip", "probes.hip"]
+           "mixed16.hip", "probes.hip", "mx_abi.hip", "mx_quant.hip", "mx_gemm.hip", "mx_a16.hip"]
 
 # Host-only C++ (no device code): argument checks, launch table, choice model.
-HOST_SOURCES = ["host_plan.cpp"]
+HOST_SOURCES = ["host_plan.cpp", "mx_plan.cpp"]
 HOST_FLAGS = ["-std=c++17", "-O2", "-fPIC", "-Wall", "-Wextra", "-I", CSRC]
 
 # Per-source flags: the kernels of w16_vgpr.hip keep their accumulators in

@@ -24,13 +24,6 @@ constexpr int kTiledT[GEMM_F32_NUM_VARIANTS] = {0, 16, 0, 32, 4, 32, 0};
 
 thread_local char t_last_error[256] = "";
 
-int launch_status(hipError_t err, const char *what) {
-  if (err == hipSuccess) return GEMM_F32_OK;
-  std::snprintf(t_last_error, sizeof(t_last_error), "%s: %s (%s)", what,
-                hipGetErrorName(err), hipGetErrorString(err));
-  return GEMM_F32_LAUNCH_FAILED;
-}
-
 int num_configs(int variant) {
   if (variant < 0 || variant >= GEMM_F32_NUM_VARIANTS) return 0;
   if (variant == GEMM_F32_PROD) return prod_num_configs();
@@ -78,6 +71,13 @@ int splitk_validate(int M, int N, int K, const float *A, int lda, const float *B
 }
 
 }  // namespace
+
+int gemm_f32_impl::launch_status(hipError_t err, const char *what) {
+  if (err == hipSuccess) return GEMM_F32_OK;
+  std::snprintf(t_last_error, sizeof(t_last_error), "%s: %s (%s)", what,
+                hipGetErrorName(err), hipGetErrorString(err));
+  return GEMM_F32_LAUNCH_FAILED;
+}
 
 extern "C" int gemm_f32_ex(int M, int N, int K, const float *A, int lda,
                            const float *B, int ldb, float *C, int ldc,
@@ -305,7 +305,7 @@ extern "C" const char *gemm_f32_status_string(int status) {
       return "launch-table index out of range or not valid for this shape";
     case GEMM_F32_BAD_ARG: return "invalid argument";
     case GEMM_F32_BAD_WORKSPACE:
-      return "split-K workspace missing, smaller than the plan needs, or not 4-byte aligned";
+      return "workspace missing, smaller than the call needs, or misaligned";
     case GEMM_F32_SCRATCH_TOO_SMALL:
       return "the split-K plan needs more than the library's fixed scratch array holds";
     default: return "unknown status";

@@ -10,6 +10,10 @@
 
 namespace gemm_f32_impl {
 
+// The status code of a launch; an error's text is kept for
+// gemm_f32_last_error (gemm_f32_abi.hip).
+int launch_status(hipError_t err, const char *what);
+
 // One product C = A x B, row-major with leading dimensions (elements).
 struct Problem {
   int M, N, K;

@@ -1,0 +1,60 @@
+// Internal declarations of the MX operators: what the C-ABI front end
+// (mx_abi.hip) hands to the kernels' translation units.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "mx_plan.hpp"
+
+namespace gemm_f32_impl {
+
+// An MX matrix: codes and scales, row pitches in bytes.
+struct MxMatrix {
+  const unsigned char *codes;
+  long long ld;
+  const unsigned char *scales;
+  long long lds;
+};
+
+// One conversion between a row-major matrix (pitch in elements) and an MX
+// matrix of `rows` rows of K values.
+struct MxConvert {
+  int rows, K;
+  const void *x;  // quantise: source
+  void *y;        // dequantise: destination
+  long long ldx;
+  unsigned char *codes;
+  long long ld;
+  unsigned char *scales;
+  long long lds;
+};
+hipError_t launch_mx_quantize(int format, int along, const MxConvert &c, hipStream_t s);
+hipError_t launch_mx_dequantize(int format, int along, const MxConvert &c, hipStream_t s);
+
+// C = A B^T with both operands MX; C in `c_format`, pitch in elements.
+struct MxProblem {
+  int M, N, K;
+  MxMatrix A, B;
+  void *C;
+  long long ldc;
+  int c_format;
+};
+hipError_t launch_mx_gemm(int entry, const MxProblem &p, hipStream_t s);
+
+// C = A B^T with A in 16 bits (pitch in elements) and B MX.
+struct MxA16Problem {
+  int M, N, K;
+  const uint16_t *A;
+  long long lda;
+  int a_format;
+  MxMatrix B;
+  void *C;
+  long long ldc;
+  int c_format;
+};
+hipError_t launch_mx_a16(const MxA16Problem &p, hipStream_t s);
+
+// C = 0 in any format.
+hipError_t launch_mx_zero(void *C, int M, int N, long long ldc, int c_format, hipStream_t s);
+
+}  // namespace gemm_f32_impl

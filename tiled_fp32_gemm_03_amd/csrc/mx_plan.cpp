@@ -1,0 +1,45 @@
+// Host-only planning of the MX operators (see mx_plan.hpp).
+#include "mx_plan.hpp"
+
+#include <cstdint>
+
+namespace gemm_f32_impl {
+
+namespace {
+
+bool misaligned(const void *p, int align) {
+  return (reinterpret_cast<std::uintptr_t>(p) & static_cast<std::uintptr_t>(align - 1)) != 0;
+}
+
+}  // namespace
+
+int check_mx_ld(int K, int ld, int lds) {
+  const long long c = mx_code_bytes(K), s = mx_scale_bytes(K);
+  if (ld < (c > 16 ? c : 16) || lds < (s > 16 ? s : 16)) return kInvalidLd;
+  return (ld % 16 || lds % 16) ? kMisaligned : kOk;
+}
+
+int check_mx_pointers(const void *codes, const void *scales) {
+  if (codes == nullptr || scales == nullptr) return kNullPtr;
+  return misaligned(codes, 16) || misaligned(scales, 16) ? kMisaligned : kOk;
+}
+
+int check_plain_pointer(const void *p, int format) {
+  if (p == nullptr) return kNullPtr;
+  return misaligned(p, format_bytes(format)) ? kMisaligned : kOk;
+}
+
+namespace {
+
+// Index = launch-table entry of gemm_mx.
+const MxEntry kMxEntries[] = {
+    {64, 64, 128, 256},  // operands straight from memory, any size
+};
+
+}  // namespace
+
+int mx_num_entries() { return (int)(sizeof(kMxEntries) / sizeof(kMxEntries[0])); }
+const MxEntry &mx_entry(int index) { return kMxEntries[index]; }
+int mx_choose(int, int, int) { return 0; }
+
+}  // namespace gemm_f32_impl
