@@ -134,6 +134,55 @@ def test_binding_refusals_on_host_tensors():
         g.matmul_mx(q, q, dtype=torch.int32)
 
 
+# ---- the mixture-of-experts layer ------------------------------------------------
+
+
+def _moe(T=2, E=4, top=2, H=64, I=32, X=256, ldx=64, R=256, ldr=64, fmt=0, W1=256, ld1=64, S1=0,
+         lds1=0, W2=256, ld2=32, S2=0, lds2=0, weights=0, renorm=1, Y=256, ldy=64, yf=0, ids=0,
+         gates=0, ws=256, ws_bytes=1 << 20):
+    p = lambda v: v or None  # noqa: E731
+    return L.gemm_moe(T, E, top, H, I, p(X), ldx, p(R), ldr, fmt, p(W1), ld1, p(S1), lds1, p(W2),
+                      ld2, p(S2), lds2, weights, renorm, p(Y), ldy, yf, p(ids), p(gates), p(ws),
+                      ws_bytes, None)
+
+
+def test_moe_refusals():
+    workspace = 9
+    for kw in (dict(T=-1), dict(E=-1), dict(top=-1), dict(H=0), dict(I=0), dict(H=-5)):
+        assert _moe(**kw) == DIM, kw
+    for kw in (dict(T=257), dict(E=513), dict(top=0), dict(top=5), dict(E=32, top=17),
+               dict(H=(1 << 24) + 1), dict(fmt=2), dict(yf=1), dict(weights=2), dict(yf=3)):
+        assert _moe(**kw) == ARG, kw
+    for kw in (dict(ldx=63), dict(ldr=63), dict(ldy=63), dict(ld1=63), dict(ld2=31)):
+        assert _moe(**kw) == LD, kw
+    mx_kw = dict(weights=1, ld1=32, lds1=16, ld2=16, lds2=16, S1=256, S2=256)
+    for kw in (dict(ld1=16), dict(lds1=0), dict(ld2=0), dict(lds2=0)):
+        assert _moe(**{**mx_kw, **kw}) == LD, kw
+    for kw in (dict(ld1=40), dict(lds1=24), dict(W1=264), dict(S2=264)):
+        assert _moe(**{**mx_kw, **kw}) == MISALIGNED, kw
+    for name in ("X", "R", "W1", "W2", "Y"):
+        assert _moe(**{name: 0}) == NULL, name
+        assert _moe(**{name: 257}) == MISALIGNED, name
+    assert _moe(**{**mx_kw, "S1": 0}) == NULL
+    assert _moe(yf=2, Y=258) == MISALIGNED
+    assert _moe(ids=258) == MISALIGNED and _moe(gates=258) == MISALIGNED
+    need = g.gemm_moe_workspace_bytes(2, 4, 2, 64, 32)
+    assert need > 0 and need % 16 == 0
+    assert _moe(ws=0) == workspace and _moe(ws=264) == workspace and _moe(ws_bytes=need - 1) == workspace
+    assert _moe(T=0, X=0, R=0, W1=0, W2=0, Y=0, ws=0) == OK
+    assert g.gemm_moe_workspace_bytes(257, 4, 2, 64, 32) == -1
+    assert g.gemm_moe_workspace_bytes(1, 4, 5, 64, 32) == -1
+
+
+def test_moe_binding_refusals_on_host_tensors():
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        g.moe_layer(x, torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 64, 64),
+                    torch.zeros(4, 64, 32), 2)
+    with pytest.raises(TypeError):
+        g.moe_layer(x.float(), x, x, x, 1)
+
+
 # ---- the oracle's own pins -----------------------------------------------------
 
 

@@ -29,6 +29,9 @@ Raw C-ABI mirrors (same names and argument order as ``include/gemm_f32.h``):
   gemm_mx_tile(config, M, N, K) -> dict, gemm_mx_num_configs()
   gemm_mx_a16(M, N, K, A, lda, a_format, B, ldb, SB, ldsb, C, ldc, c_format, stream)
   gemm_mx_code_bytes(K), gemm_mx_scale_bytes(K)         (include/gemm_mx.h)
+  gemm_moe(T, E, top, H, I, X, ldx, R, ldr, format, W1, ld1, S1, lds1, W2, ld2, S2, lds2, weights,
+           renormalize, Y, ldy, y_format, ids, gates, workspace, workspace_bytes, stream),
+  gemm_moe_workspace_bytes(T, E, top, H, I)             (include/gemm_moe.h)
 Pointers are device addresses (ints); ``stream`` is a hipStream_t as int
 (0 = null stream).  A non-zero status raises ``GemmError``.
 
@@ -48,6 +51,10 @@ bfloat16 or float16 matrix; ``along="columns"`` takes its columns as the rows
 values back.  ``matmul_mx(A, B, dtype=torch.float32)`` is the product of the
 rows of A (an ``MxTensor``, or a bfloat16 or float16 matrix) with the rows of
 the ``MxTensor`` B, C[i][j] = sum_k A[i][k] B[j][k].
+
+``moe_layer(X, router, w1, w2, top)`` is a mixture-of-experts layer for a few
+tokens, the experts' weights being 16-bit tensors or stacks of MX matrices; it
+returns the result, the chosen experts and their gates.
 """
 from __future__ import annotations
 
@@ -71,6 +78,7 @@ __all__ = [
     "MxTensor", "MX_FORMATS", "MX_ALONG", "mx_quantize", "mx_dequantize", "matmul_mx",
     "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx", "gemm_mx_tile", "gemm_mx_num_configs",
     "gemm_mx_a16", "gemm_mx_code_bytes", "gemm_mx_scale_bytes",
+    "gemm_moe", "gemm_moe_workspace_bytes", "moe_layer", "MOE_WEIGHTS",
     "library_path",
     "exported_symbols",
 ]
@@ -126,6 +134,9 @@ _SIGS = {
     "gemm_mx_num_configs": ([], _i),
     "gemm_mx_tile": ([_i, _i, _i, _i, _ip, _ip, _ip, _ip, _ip], _i),
     "gemm_mx_a16": ([_i, _i, _i, _p, _i, _i, _p, _i, _p, _i, _p, _i, _i, _p], _i),
+    "gemm_moe_workspace_bytes": ([_i, _i, _i, _i, _i], _ll),
+    "gemm_moe": ([_i, _i, _i, _i, _i, _p, _i, _p, _i, _i, _p, _i, _p, _i, _p, _i, _p, _i, _i, _i,
+                  _p, _i, _i, _p, _p, _p, _ll, _p], _i),
     "gemm_f32_probe_lds_bytes": ([_i, _i], _ll),
     "gemm_f32_device_props": ([_i, _ip, _ip, _ip, _ip, _ip], _i),
     "gemm_f32_probe_fused": ([_i, _i, _i, _p, _ll, _p, _p], _i),
@@ -150,6 +161,8 @@ MIXED_FORMATS = {"bf16": 0, "f16": 1}
 # Formats of unquantised matrices and the ways blocks run (include/gemm_mx.h).
 MX_FORMATS = {"bf16": 0, "f16": 1, "f32": 2}
 MX_ALONG = {"rows": 0, "columns": 1}
+# Kinds of expert weights (include/gemm_moe.h).
+MOE_WEIGHTS = {"w16": 0, "mx": 1}
 _MX_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
@@ -397,6 +410,22 @@ def gemm_mx_a16(M, N, K, A, lda, a_format, B, ldb, SB, ldsb, C, ldc, c_format, s
                             SB or None, ldsb, C or None, ldc, _mx_format(c_format),
                             stream or None),
            "gemm_mx_a16")
+
+
+def gemm_moe_workspace_bytes(T, E, top, H, I) -> int:
+    return int(_lib.gemm_moe_workspace_bytes(int(T), int(E), int(top), int(H), int(I)))
+
+
+def gemm_moe(T, E, top, H, I, X, ldx, R, ldr, format, W1, ld1, S1, lds1, W2, ld2, S2, lds2, weights,
+             renormalize, Y, ldy, y_format, ids, gates, workspace, workspace_bytes,
+             stream=0) -> None:
+    weights = MOE_WEIGHTS[weights] if isinstance(weights, str) else int(weights)
+    _check(_lib.gemm_moe(T, E, top, H, I, X or None, ldx, R or None, ldr, _format(format),
+                         W1 or None, ld1, S1 or None, lds1, W2 or None, ld2, S2 or None, lds2,
+                         weights, int(renormalize), Y or None, ldy, _mx_format(y_format),
+                         ids or None, gates or None, workspace or None, int(workspace_bytes),
+                         stream or None),
+           "gemm_moe")
 
 
 def config_name(variant, config: int = -1, M: int = 1, N: int = 1, K: int = 1) -> str:
@@ -677,3 +706,86 @@ def matmul_mx(A, B, dtype=torch.float32, out=None, config: int = -1, stream=None
         else:
             gemm_mx_a16(M, N, K, *a, *b, out.data_ptr(), ldc, _MX_DTYPES[dtype], stream)
     return out
+
+
+def _expert_rows(w, name: str, dtype, device, E: int, rows: int, K: int):
+    """Pointers and pitches of stacked expert matrices (E, rows, K): (weights,
+    pitch, scales, scale pitch), the experts' rows following one another."""
+    def pitch(t, width, what):
+        if t.dim() != 3 or t.device != device:
+            raise TypeError(f"{what} must be a 3-D tensor on {device}")
+        if tuple(t.shape[:2]) != (E, rows):
+            raise ValueError(f"{what} must have {E} experts of {rows} rows, not {tuple(t.shape)}")
+        if t.shape[2] > 1 and t.stride(2) != 1:
+            raise ValueError(f"{what} must have contiguous rows (last stride 1)")
+        if rows > 1 and t.stride(1) < t.shape[2]:
+            raise ValueError(f"{what}: rows overlap")
+        step = t.stride(1) if rows > 1 else (t.stride(0) if E > 1 else width)
+        if E > 1 and t.stride(0) != rows * step:
+            raise ValueError(f"{what}: experts must follow one another (stride {rows * step})")
+        return step
+
+    if isinstance(w, MxTensor):
+        if w.K != K:
+            raise ValueError(f"{name} must have rows of {K} values, not {w.K}")
+        c = pitch(w.codes, gemm_mx_code_bytes(K), name + ".codes")
+        s = pitch(w.scales, gemm_mx_scale_bytes(K), name + ".scales")
+        return w.codes.data_ptr(), c, w.scales.data_ptr(), s
+    if w.dtype != dtype:
+        raise TypeError(f"{name} must be an MxTensor, or {dtype} like the tokens")
+    if w.dim() == 3 and w.shape[2] != K:
+        raise ValueError(f"{name} must have rows of {K} values, not {w.shape[2]}")
+    return w.data_ptr(), pitch(w, K, name), 0, 0
+
+
+def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None, out=None,
+              workspace=None, stream=None):
+    """A mixture-of-experts layer for a few tokens (include/gemm_moe.h): (Y, ids, gates).
+
+    X is (T, H), router (E, H), both bfloat16 or float16; w1 is (E, 2 I, H) with
+    each expert's gate rows first and w2 (E, H, I), tensors of the same dtype or
+    stacks of MX matrices (MxTensor with 3-D codes and scales).  Y is (T, H) in
+    ``dtype`` (X's, or float32), ids (T, top) int32 and gates (T, top) float32.
+    ``workspace`` is a uint8 CUDA tensor of at least gemm_moe_workspace_bytes;
+    when None, one is allocated with torch for this call.
+    """
+    if X.dtype not in (torch.bfloat16, torch.float16) or not X.is_cuda:
+        raise TypeError("X must be a bfloat16 or float16 CUDA tensor")
+    device = X.device
+    if router.dtype != X.dtype or router.device != device:
+        raise TypeError(f"router must be a {X.dtype} tensor on {device}")
+    ldx, ldr = _ld(X), _ld(router)
+    T, H = X.shape
+    E = router.shape[0]
+    if router.shape[1] != H:
+        raise ValueError(f"router must have rows of {H} values, not {router.shape[1]}")
+    if isinstance(w1, MxTensor) != isinstance(w2, MxTensor):
+        raise TypeError("w1 and w2 must both be MxTensors or both tensors")
+    mx = isinstance(w2, MxTensor)
+    I = w2.K if mx else w2.shape[-1]
+    a1 = _expert_rows(w1, "w1", X.dtype, device, E, 2 * I, H)
+    a2 = _expert_rows(w2, "w2", X.dtype, device, E, H, I)
+    dtype = X.dtype if dtype is None else dtype
+    if dtype not in (X.dtype, torch.float32):
+        raise TypeError(f"dtype must be {X.dtype} or float32")
+    top = int(top)
+    need = gemm_moe_workspace_bytes(T, E, top, H, I)
+    if need < 0:
+        raise ValueError(f"sizes outside the layer's bounds: {T} tokens, {E} experts, top {top}, "
+                         f"widths {H} and {I}")
+    out = _mx_out(out, (T, H), dtype, device)
+    ldy = _ld(out)
+    ids = torch.empty((T, top), dtype=torch.int32, device=device)
+    gates = torch.empty((T, top), dtype=torch.float32, device=device)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise TypeError(f"workspace must be a contiguous tensor on {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    with _on(device):
+        gemm_moe(T, E, top, H, I, X.data_ptr(), ldx, router.data_ptr(), ldr, _MX_DTYPES[X.dtype],
+                 *a1, *a2, int(mx), renormalize, out.data_ptr(), ldy, _MX_DTYPES[dtype],
+                 ids.data_ptr(), gates.data_ptr(), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), stream)
+    return out, ids, gates

@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libgemm_f32.so")
 ARCH = "gfx950"
 
 SOURCES = ["gemm_f32_abi.hip", "naive_tiled.hip", "prod.hip", "w16_vgpr.hip", "valu.hip", "mixed.hip",
-           "mixed16.hip", "probes.hip", "mx_abi.hip", "mx_quant.hip", "mx_gemm.hip", "mx_a16.hip"]
+           "mixed16.hip", "probes.hip", "mx_abi.hip", "mx_quant.hip", "mx_gemm.hip", "mx_a16.hip", "moe.hip"]
 
 # Host-only C++ (no device code): argument checks, launch table, choice model.
 HOST_SOURCES = ["host_plan.cpp", "mx_plan.cpp"]

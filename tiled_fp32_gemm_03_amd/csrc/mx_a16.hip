@@ -7,16 +7,6 @@
 namespace gemm_f32_impl {
 namespace {
 
-// 8 values of an activation row from k, the first `n` of them (others 0).
-__device__ inline u32x4 load_act(const uint16_t *row, long long k, long long n) {
-  if (n >= 8) return *reinterpret_cast<const u32x4h *>(row + k);
-  u32x4 w{0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) w[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
-  return w;
-}
-
 template <int AF, int MB, int W>
 __global__ void __launch_bounds__(64 * W) mx_a16_kernel(MxA16Problem p) {
   __shared__ f32x4 part[W][MB][64];
@@ -24,8 +14,8 @@ __global__ void __launch_bounds__(64 * W) mx_a16_kernel(MxA16Problem p) {
   const int l16 = lane & 15, g = lane >> 4;
   const long long n0 = 16LL * blockIdx.x;
   const long long rb = n0 + l16 < p.N ? n0 + l16 : p.N - 1;
-  const unsigned char *codes = p.B.codes + rb * p.B.ld, *scales = p.B.scales + rb * p.B.lds;
-  const int nb = (int)mx_blocks(p.K);
+  const WRow row{p.B.codes + rb * p.B.ld, p.B.scales + rb * p.B.lds};
+  const int steps = (int)ceil_div(p.K, 128);
   for (long long m0 = 16LL * MB * blockIdx.y; m0 < p.M; m0 += 16LL * MB * gridDim.y) {
     const uint16_t *arow[MB];
 #pragma unroll
@@ -34,30 +24,15 @@ __global__ void __launch_bounds__(64 * W) mx_a16_kernel(MxA16Problem p) {
       arow[i] = p.A + (m < p.M ? m : p.M - 1) * p.lda;
     }
     f32x4 acc[MB] = {};
-    for (int kb0 = 4 * wave; kb0 < nb; kb0 += 4 * W) {
-      const int kb = kb0 + g;
-      u32x4 c{0, 0, 0, 0};
-      uint32_t sb = 127;
-      if (kb < nb) {
-        c = *reinterpret_cast<const u32x4 *>(codes + 16LL * kb);
-        sb = scales[kb];
-      }
-      bf16x8 w[4];
-      widen_block(c, sb, w);
+    for (int step = wave; step < steps; step += W) {
+      u32x4 w[4];
+      load_weights<kWMx>(row, step, g, p.K, w);
 #pragma unroll
       for (int i = 0; i < MB; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const long long k = 32LL * kb + 8 * j;
-          const u32x4 a = load_act(arow[i], k, p.K - k);
-          if constexpr (AF == kBf16) {
-            acc[i] = mfma_bf16(w[j], __builtin_bit_cast(bf16x8, a), acc[i]);
-          } else {
-            bf16x8 hi, lo;
-            split_f16(__builtin_bit_cast(f16x8, a), hi, lo);
-            acc[i] = mfma_bf16(w[j], hi, acc[i]);
-            acc[i] = mfma_bf16(w[j], lo, acc[i]);
-          }
+          const long long k = 128LL * step + thin_k<kWMx>(g, j);
+          acc[i] = thin_mfma<kWMx, AF>(w[j], load_act(arow[i], k, p.K - k), acc[i]);
         }
     }
 #pragma unroll

@@ -4,6 +4,7 @@
 #include "gemm_f32.h"
 #include "gemm_internal.hpp"
 #include "gemm_mixed.h"
+#include "gemm_moe.h"
 #include "gemm_mx.h"
 #include "mx_internal.hpp"
 
@@ -12,6 +13,9 @@ using namespace gemm_f32_impl;
 static_assert(kBf16 == GEMM_MIXED_BF16 && kF16 == GEMM_MIXED_F16 && kF32 == GEMM_MX_F32 &&
                   kAlongRows == GEMM_MX_ROWS && kAlongColumns == GEMM_MX_COLUMNS,
               "constants of mx_plan.hpp and the headers differ");
+static_assert(kMoeMaxTokens == GEMM_MOE_MAX_TOKENS && kMoeMaxExperts == GEMM_MOE_MAX_EXPERTS &&
+                  kMoeMaxTop == GEMM_MOE_MAX_TOP && kMoeMaxWidth == GEMM_MOE_MAX_WIDTH,
+              "bounds of mx_plan.hpp and gemm_moe.h differ");
 
 extern "C" long long gemm_mx_code_bytes(int K) { return K < 0 ? 0 : mx_code_bytes(K); }
 extern "C" long long gemm_mx_scale_bytes(int K) { return K < 0 ? 0 : mx_scale_bytes(K); }
@@ -128,4 +132,52 @@ extern "C" int gemm_mx_a16(int M, int N, int K, const void *A, int lda, int a_fo
   const MxA16Problem p{M, N, K, static_cast<const uint16_t *>(A), lda, a_format,
                        {B, ldb, SB, ldsb}, C, ldc, c_format};
   return launch_status(launch_mx_a16(p, s), "mx 16-bit product");
+}
+
+// ---- the mixture-of-experts layer ----------------------------------------------
+
+extern "C" long long gemm_moe_workspace_bytes(int T, int E, int top, int H, int I) {
+  return moe_check_sizes(T, E, top, H, I) == kOk ? moe_space(T, E, top, I).bytes : -1;
+}
+
+extern "C" int gemm_moe(int T, int E, int top, int H, int I, const void *X, int ldx,
+                        const void *R, int ldr, int format, const void *W1, int ld1,
+                        const unsigned char *S1, int lds1, const void *W2, int ld2,
+                        const unsigned char *S2, int lds2, int weights, int renormalize, void *Y,
+                        int ldy, int y_format, int *ids, float *gates, void *workspace,
+                        long long workspace_bytes, void *stream) {
+  int rc = moe_check_sizes(T, E, top, H, I);
+  if (rc != kOk) return rc;
+  if ((format != kBf16 && format != kF16) || (y_format != format && y_format != kF32) ||
+      (weights != GEMM_MOE_W16 && weights != GEMM_MOE_MX))
+    return kBadArg;
+  const bool mx = weights == GEMM_MOE_MX;
+  if (ldx < H || ldr < H || ldy < H) return kInvalidLd;
+  if (mx) {
+    rc = check_mx_ld(H, ld1, lds1);
+    if (rc == kOk) rc = check_mx_ld(I, ld2, lds2);
+    if (rc != kOk) return rc;
+  } else if (ld1 < H || ld2 < I) {
+    return kInvalidLd;
+  }
+  if (T == 0) return kOk;
+  rc = check_plain_pointer(X, format);
+  if (rc == kOk) rc = check_plain_pointer(R, format);
+  if (rc == kOk) rc = check_plain_pointer(Y, y_format);
+  if (rc == kOk) rc = mx ? check_mx_pointers(W1, S1) : check_plain_pointer(W1, format);
+  if (rc == kOk) rc = mx ? check_mx_pointers(W2, S2) : check_plain_pointer(W2, format);
+  if (rc == kOk && ids != nullptr) rc = check_plain_pointer(ids, kF32);
+  if (rc == kOk && gates != nullptr) rc = check_plain_pointer(gates, kF32);
+  if (rc != kOk) return rc;
+  const MoeSpace at = moe_space(T, E, top, I);
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15) != 0 ||
+      workspace_bytes < at.bytes)
+    return GEMM_F32_BAD_WORKSPACE;
+  const MoeProblem p{T, E, top, H, I, static_cast<const uint16_t *>(X), ldx,
+                     static_cast<const uint16_t *>(R), ldr, format,
+                     static_cast<const unsigned char *>(W1), mx ? ld1 : 2LL * ld1, S1, lds1,
+                     static_cast<const unsigned char *>(W2), mx ? ld2 : 2LL * ld2, S2, lds2,
+                     mx, renormalize != 0, Y, ldy, y_format, ids, gates,
+                     static_cast<unsigned char *>(workspace), at};
+  return launch_status(launch_moe(p, static_cast<hipStream_t>(stream)), "moe");
 }

@@ -54,6 +54,33 @@ struct MxA16Problem {
 };
 hipError_t launch_mx_a16(const MxA16Problem &p, hipStream_t s);
 
+// The mixture-of-experts layer (gemm_moe.h).
+struct MoeProblem {
+  int T, E, top, H, I;
+  const uint16_t *X;
+  long long ldx;
+  const uint16_t *R;
+  long long ldr;
+  int format;
+  const unsigned char *W1;  // rows of 2-byte values or of codes
+  long long ld1;            // bytes
+  const unsigned char *S1;
+  long long lds1;
+  const unsigned char *W2;
+  long long ld2;
+  const unsigned char *S2;
+  long long lds2;
+  int mx, renormalize;
+  void *Y;
+  long long ldy;
+  int y_format;
+  int *ids;  // may be null
+  float *gates;
+  unsigned char *ws;
+  MoeSpace at;
+};
+hipError_t launch_moe(const MoeProblem &p, hipStream_t s);
+
 // C = 0 in any format.
 hipError_t launch_mx_zero(void *C, int M, int N, long long ldc, int c_format, hipStream_t s);
 

@@ -42,4 +42,34 @@ int mx_num_entries() { return (int)(sizeof(kMxEntries) / sizeof(kMxEntries[0]));
 const MxEntry &mx_entry(int index) { return kMxEntries[index]; }
 int mx_choose(int, int, int) { return 0; }
 
+int moe_check_sizes(int T, int E, int top, int H, int I) {
+  if (T < 0 || E < 0 || top < 0 || H < 1 || I < 1) return kInvalidDim;
+  if (T > kMoeMaxTokens || E > kMoeMaxExperts || top < 1 || top > kMoeMaxTop || top > E ||
+      H > kMoeMaxWidth || I > kMoeMaxWidth)
+    return kBadArg;
+  return kOk;
+}
+
+MoeSpace moe_space(int T, int E, int top, int I) {
+  MoeSpace w;
+  long long at = 0;
+  const long long pairs = (long long)T * top;
+  auto take = [&at](long long bytes) {
+    const long long from = at;
+    at += ceil_div(bytes, 16) * 16;
+    return from;
+  };
+  w.pitch = ceil_div(I, 128) * 128;
+  w.logits = take(8LL * T * E);
+  w.ids = take(4 * pairs);
+  w.gates = take(4 * pairs);
+  w.start = take(4LL * (E + 1));
+  w.list = take(4 * pairs);
+  w.active = take(4LL * (E + 1));
+  w.hi = take(2 * pairs * w.pitch);
+  w.lo = take(2 * pairs * w.pitch);
+  w.bytes = at;
+  return w;
+}
+
 }  // namespace gemm_f32_impl
