@@ -86,7 +86,7 @@ int gemm_mx_dequantize(int rows, int K, const unsigned char *codes, int ld,
  *   C, ldc    M x N row-major in `c_format`, element-aligned, ldc in elements.
  *   config    -1 picks a launch-table entry for the shape, otherwise an index
  *             below gemm_mx_num_configs() (else GEMM_F32_BAD_CONFIG); an
- *             entry whose address range the operands exceed runs entry 0.
+ *             entry that the sizes or pitches do not fit runs entry 0.
  * Products of two elements and their block sums are formed by the scaled
  * matrix instruction, v_mfma_scale_f32_16x16x128_f8f6f4.
  */
