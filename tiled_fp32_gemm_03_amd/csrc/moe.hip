@@ -206,45 +206,32 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(MoeProblem p) 
 constexpr int kUpWaves = 8;
 
 template <int W, int AF, int MB>
-__device__ inline void moe_up_rows(const MoeProblem &p, const WRow (&row)[2], int first, int n,
+__device__ inline void moe_up_rows(const MoeProblem &p, const Row (&w)[2], int first, int n,
                                    int i0, f32x4 (*part)[2][2][64]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-  const int steps = (int)ceil_div(p.H, 128);
   const int *list = ws_at<int>(p, p.at.list) + first;
-  const uint16_t *x[MB];
+  Row x[MB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     const int m = 16 * i + l16 < n ? 16 * i + l16 : n - 1;
-    x[i] = p.X + list[m] / p.top * p.ldx;
+    x[i] = {reinterpret_cast<const unsigned char *>(p.X + list[m] / p.top * p.ldx), nullptr};
   }
-  f32x4 acc[MB][2] = {};
-  for (int step = wave; step < steps; step += kUpWaves) {
-    u32x4 w[2][4];
-    load_weights<W>(row[0], step, g, p.H, w[0]);
-    load_weights<W>(row[1], step, g, p.H, w[1]);
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long long k = 128LL * step + thin_k<W>(g, j);
-        const u32x4 a = load_act(x[i], k, p.H - k);
-        acc[i][0] = thin_mfma<W, AF>(w[0][j], a, acc[i][0]);
-        acc[i][1] = thin_mfma<W, AF>(w[1][j], a, acc[i][1]);
-      }
-  }
+  Thin<W, AF, MB, 2> t;
+  t.clear();
+  t.run(x, w, wave, kUpWaves, (int)ceil_div(p.H, kPieceK<W>), p.H, g);
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
-    part[wave][i][0][lane] = acc[i][0];
-    part[wave][i][1][lane] = acc[i][1];
+    part[wave][i][0][lane] = t.acc[i][0];
+    part[wave][i][1][lane] = t.acc[i][1];
   }
   __syncthreads();
   if (wave < MB) {
     f32x4 a = part[0][wave][0][lane], b = part[0][wave][1][lane];
 #pragma unroll
-    for (int w = 1; w < kUpWaves; ++w) {
-      a += part[w][wave][0][lane];
-      b += part[w][wave][1][lane];
+    for (int q = 1; q < kUpWaves; ++q) {
+      a += part[q][wave][0][lane];
+      b += part[q][wave][1][lane];
     }
     const int m = 16 * wave + l16;
     if (m < n) {
@@ -277,47 +264,39 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeProblem p) {
   const int i0 = 16 * blockIdx.x, l16 = threadIdx.x & 15;
   const int i = i0 + l16 < p.I ? i0 + l16 : p.I - 1;
   const long long r0 = 2LL * p.I * e + i, r1 = r0 + p.I;
-  WRow row[2] = {{p.W1 + r0 * p.ld1, nullptr}, {p.W1 + r1 * p.ld1, nullptr}};
-  if constexpr (W == kWMx) row[0].scales = p.S1 + r0 * p.lds1, row[1].scales = p.S1 + r1 * p.lds1;
+  Row w[2] = {{p.W1 + r0 * p.ld1, nullptr}, {p.W1 + r1 * p.ld1, nullptr}};
+  if constexpr (W == kMx) w[0].q = p.S1 + r0 * p.lds1, w[1].q = p.S1 + r1 * p.lds1;
   if (n <= 16) {
-    moe_up_rows<W, AF, 1>(p, row, first, n, i0, part);
+    moe_up_rows<W, AF, 1>(p, w, first, n, i0, part);
   } else {
-    for (int m = 0; m < n; m += 32) moe_up_rows<W, AF, 2>(p, row, first + m, n - m, i0, part);
+    for (int m = 0; m < n; m += 32) moe_up_rows<W, AF, 2>(p, w, first + m, n - m, i0, part);
   }
 }
 
 // ---- second product and the weighted sum -----------------------------------------
 // A workgroup owns 16 columns of Y for all tokens.  Its waves take pieces of
-// 512 of an expert's inner columns in turn, over all chosen experts, and add
-// each piece's rows, times their gates, to a sum of their own in LDS; the
-// waves' sums are added in wave order at the end.
+// an expert's inner columns in turn, over all chosen experts, and add each
+// run of pieces, times the gates, to a sum of their own in LDS; the waves'
+// sums are added in wave order at the end.
 constexpr int kDownWaves = 8;
-constexpr int kPiece = 4;  // 128-deep steps per piece
+template <int W>
+constexpr int kRunPieces = W == kMx ? 1 : 4;  // 512 k
 
 template <int W, int MB>
-__device__ inline void moe_down_piece(const MoeProblem &p, const WRow &row, int first, int n,
-                                      int s0, int s1, float *sum) {
+__device__ inline void moe_down_run(const MoeProblem &p, const Row &row, int first, int n, int p0,
+                                    int p1, float *sum) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const uint16_t *hi[MB], *lo[MB];
+  Row u[MB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
     const int m = 16 * i + l16 < n ? 16 * i + l16 : n - 1;
-    hi[i] = ws_at<uint16_t>(p, p.at.hi) + (first + m) * p.at.pitch;
-    lo[i] = ws_at<uint16_t>(p, p.at.lo) + (first + m) * p.at.pitch;
+    u[i] = {p.ws + p.at.hi + 2 * (first + m) * p.at.pitch,
+            p.ws + p.at.lo + 2 * (first + m) * p.at.pitch};
   }
-  f32x4 acc[MB] = {};
-  for (int step = s0; step < s1; ++step) {
-    u32x4 w[4];
-    load_weights<W>(row, step, g, p.I, w);
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long long k = 128LL * step + thin_k<W>(g, j);
-        acc[i] = thin_mfma_split<W>(w[j], *reinterpret_cast<const u32x4 *>(hi[i] + k),
-                                    *reinterpret_cast<const u32x4 *>(lo[i] + k), acc[i]);
-      }
-  }
+  Thin<W, kSplit, MB, 1> t;
+  t.clear();
+  const Row w[1] = {row};
+  t.run(u, w, p0, 1, p1, p.I, g);
   const int *list = ws_at<int>(p, p.at.list) + first;
   const float *gates = ws_at<float>(p, p.at.gates);
 #pragma unroll
@@ -326,7 +305,7 @@ __device__ inline void moe_down_piece(const MoeProblem &p, const WRow &row, int 
     if (m < n) {
       const int pair = list[m];
       f32x4 *to = reinterpret_cast<f32x4 *>(sum + 16 * (pair / p.top) + 4 * g);
-      *to += gates[pair] * acc[i];
+      *to += gates[pair] * t.acc[i][0];
     }
   }
 }
@@ -341,19 +320,20 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeProblem p)
   const int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
   const int n0 = 16 * blockIdx.x, l16 = lane & 15;
   const int col = n0 + l16 < p.H ? n0 + l16 : p.H - 1;
-  const int steps = (int)ceil_div(p.I, 128), pieces = (int)ceil_div(steps, kPiece);
-  const int units = active[0] * pieces;
-  for (int u = wave; u < units; u += kDownWaves) {
-    const int e = active[1 + u / pieces], piece = u % pieces;
+  const int pieces = (int)ceil_div(p.I, kPieceK<W>), runs = (int)ceil_div(pieces, kRunPieces<W>);
+  const int units = active[0] * runs;
+  for (int v = wave; v < units; v += kDownWaves) {
+    const int e = active[1 + v / runs], run = v % runs;
     const int first = start[e], n = start[e + 1] - first;
     const long long r = (long long)p.H * e + col;
-    const WRow row{p.W2 + r * p.ld2, W == kWMx ? p.S2 + r * p.lds2 : nullptr};
-    const int s0 = piece * kPiece, s1 = s0 + kPiece < steps ? s0 + kPiece : steps;
+    const Row row{p.W2 + r * p.ld2, W == kMx ? p.S2 + r * p.lds2 : nullptr};
+    const int p0 = run * kRunPieces<W>;
+    const int p1 = p0 + kRunPieces<W> < pieces ? p0 + kRunPieces<W> : pieces;
     if (n <= 16) {
-      moe_down_piece<W, 1>(p, row, first, n, s0, s1, sum);
+      moe_down_run<W, 1>(p, row, first, n, p0, p1, sum);
     } else {
       for (int m = 0; m < n; m += 32)
-        moe_down_piece<W, 2>(p, row, first + m, n - m, s0, s1, sum);
+        moe_down_run<W, 2>(p, row, first + m, n - m, p0, p1, sum);
     }
   }
   __syncthreads();
@@ -377,13 +357,13 @@ hipError_t launch_moe(const MoeProblem &p, hipStream_t s) {
   e = launch_kernel(moe_route_kernel, dim3(1), dim3(kRouteThreads), s, p);
   if (e != hipSuccess) return e;
   const dim3 ugrid((unsigned)(p.at.pitch / 16), (unsigned)(p.E < pairs ? p.E : pairs));
-  auto up = p.mx ? (p.format == kBf16 ? moe_up_kernel<kWMx, kBf16> : moe_up_kernel<kWMx, kF16>)
-                 : (p.format == kBf16 ? moe_up_kernel<kWBf16, kBf16> : moe_up_kernel<kWF16, kF16>);
+  auto up = p.mx ? (p.format == kBf16 ? moe_up_kernel<kMx, kBf16> : moe_up_kernel<kMx, kF16>)
+                 : (p.format == kBf16 ? moe_up_kernel<kBf16, kBf16> : moe_up_kernel<kF16, kF16>);
   e = launch_kernel(up, ugrid, dim3(64 * kUpWaves), s, p);
   if (e != hipSuccess) return e;
-  auto down = p.mx                ? moe_down_kernel<kWMx>
-              : p.format == kBf16 ? moe_down_kernel<kWBf16>
-                                  : moe_down_kernel<kWF16>;
+  auto down = p.mx                ? moe_down_kernel<kMx>
+              : p.format == kBf16 ? moe_down_kernel<kBf16>
+                                  : moe_down_kernel<kF16>;
   MoeProblem q = p;
   void *args[] = {&q};
   return hipLaunchKernel(reinterpret_cast<const void *>(down), dim3((unsigned)ceil_div(p.H, 16)),

@@ -1,70 +1,118 @@
-// 16-bit activations times MX weights (gemm_mx_a16): see mx_thin.hpp for the
-// operands.  The workgroup's waves take 128-deep steps of K in turn and their
-// sums are added in a fixed order through LDS.
+// Thin products with MX weights: 16-bit activations (gemm_mx_a16) and the
+// few-row form of gemm_mx.  See mx_thin.hpp for the operands.  A workgroup
+// takes 16 NB columns of C and up to 16 MB rows; its waves take the pieces of
+// K in turn and their sums are added in wave order through LDS.
 #include "mx_internal.hpp"
 #include "mx_thin.hpp"
 
 namespace gemm_f32_impl {
 namespace {
 
-template <int AF, int MB, int W>
-__global__ void __launch_bounds__(64 * W) mx_a16_kernel(MxA16Problem p) {
-  __shared__ f32x4 part[W][MB][64];
+// C's blocks [i][b] of all waves, summed and stored, four blocks at a time.
+template <int WAVES, int MB, int NB>
+__device__ __forceinline__ void thin_store(const f32x4 (&acc)[MB][NB], f32x4 (*part)[4][64],
+                                           long long m0, long long n0, int M, int N, void *C,
+                                           long long ldc, int c_format) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int l16 = lane & 15, g = lane >> 4;
-  const long long n0 = 16LL * blockIdx.x;
-  const long long rb = n0 + l16 < p.N ? n0 + l16 : p.N - 1;
-  const WRow row{p.B.codes + rb * p.B.ld, p.B.scales + rb * p.B.lds};
-  const int steps = (int)ceil_div(p.K, 128);
-  for (long long m0 = 16LL * MB * blockIdx.y; m0 < p.M; m0 += 16LL * MB * gridDim.y) {
-    const uint16_t *arow[MB];
+  constexpr int kBlocks = MB * NB, kRound = kBlocks < 4 ? kBlocks : 4;
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const long long m = m0 + 16 * i + l16;
-      arow[i] = p.A + (m < p.M ? m : p.M - 1) * p.lda;
-    }
-    f32x4 acc[MB] = {};
-    for (int step = wave; step < steps; step += W) {
-      u32x4 w[4];
-      load_weights<kWMx>(row, step, g, p.K, w);
+  for (int r = 0; r < kBlocks; r += kRound) {
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const long long k = 128LL * step + thin_k<kWMx>(g, j);
-          acc[i] = thin_mfma<kWMx, AF>(w[j], load_act(arow[i], k, p.K - k), acc[i]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i) part[wave][i][lane] = acc[i];
+    for (int q = 0; q < kRound; ++q) part[wave][q][lane] = acc[(r + q) / NB][(r + q) % NB];
     __syncthreads();
-    for (int i = wave; i < MB; i += W) {
-      f32x4 sum = part[0][i][lane];
+    if (wave < kRound) {
+      f32x4 sum = part[0][wave][lane];
 #pragma unroll
-      for (int w = 1; w < W; ++w) sum += part[w][i][lane];
-      const long long m = m0 + 16 * i + l16, n = n0 + 4 * g, left = p.N - n;
-      if (m < p.M) store4_fmt(p.c_format, p.C, m * p.ldc + n, (int)(left < 4 ? left : 4), sum);
+      for (int w = 1; w < WAVES; ++w) sum += part[w][wave][lane];
+      const long long m = m0 + 16 * ((r + wave) / NB) + (lane & 15);
+      const long long n = n0 + 16 * ((r + wave) % NB) + 4 * (lane >> 4), left = N - n;
+      if (m < M) store4_fmt(c_format, C, m * ldc + n, (int)(left < 4 ? left : 4), sum);
     }
     __syncthreads();
   }
 }
 
-template <int AF>
-hipError_t launch_a16(const MxA16Problem &p, hipStream_t s) {
-  constexpr int W = 8;
+// A's rows: 16-bit values, or MX rows (a_scales not null).
+struct ThinProblem {
+  int M, N, K;
+  const unsigned char *A;
+  long long lda;  // bytes
+  const unsigned char *SA;
+  long long ldsa;
+  MxMatrix B;
+  void *C;
+  long long ldc;
+  int c_format;
+};
+
+template <int A, int MB, int NB, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) mx_thin_kernel(ThinProblem p) {
+  __shared__ f32x4 part[WAVES][4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, g = lane >> 4;
+  const long long n0 = 16LL * NB * blockIdx.x;
+  Row w[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const long long n = n0 + 16 * b + l16 < p.N ? n0 + 16 * b + l16 : p.N - 1;
+    w[b] = {p.B.codes + n * p.B.ld, p.B.scales + n * p.B.lds};
+  }
+  const int pieces = (int)ceil_div(p.K, kPieceK<kMx>);
+  for (long long m0 = 16LL * MB * blockIdx.y; m0 < p.M; m0 += 16LL * MB * gridDim.y) {
+    Row a[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const long long m = m0 + 16 * i + l16 < p.M ? m0 + 16 * i + l16 : p.M - 1;
+      a[i] = {p.A + m * p.lda, A == kMx ? p.SA + m * p.ldsa : nullptr};
+    }
+    Thin<kMx, A, MB, NB> t;
+    t.clear();
+    t.run(a, w, wave, WAVES, pieces, p.K, g);
+    thin_store<WAVES, MB, NB>(t.acc, part, m0, n0, p.M, p.N, p.C, p.ldc, p.c_format);
+  }
+}
+
+template <int A, int MB, int NB>
+hipError_t launch_thin_blocks(const ThinProblem &p, hipStream_t s) {
+  const long long gy = ceil_div(p.M, 16 * MB);
+  const dim3 grid((unsigned)ceil_div(p.N, 16 * NB), (unsigned)(gy < kMaxGridY ? gy : kMaxGridY));
+  constexpr bool kLarge = MB * NB == 16;  // its registers allow one wave per SIMD
+  if (kLarge || p.K <= 4 * kPieceK<kMx>)
+    return launch_kernel(mx_thin_kernel<A, MB, NB, 4>, grid, dim3(256), s, p);
+  return launch_kernel(mx_thin_kernel<A, MB, NB, kLarge ? 4 : 8>, grid, dim3(512), s, p);
+}
+
+template <int A>
+hipError_t launch_thin(const ThinProblem &p, hipStream_t s) {
   const int mb = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
-  const long long gy = ceil_div(p.M, 16 * mb);
-  const dim3 grid((unsigned)ceil_div(p.N, 16), (unsigned)(gy < kMaxGridY ? gy : kMaxGridY));
-  auto kern = mb == 1   ? mx_a16_kernel<AF, 1, W>
-              : mb == 2 ? mx_a16_kernel<AF, 2, W>
-                        : mx_a16_kernel<AF, 4, W>;
-  return launch_kernel(kern, grid, dim3(64 * W), s, p);
+  // Columns per workgroup: as many as leave a workgroup per compute unit.
+  const long long cols = ceil_div(p.N, 16);
+  const int nb = cols >= 4 * 256 ? 4 : cols >= 2 * 256 ? 2 : 1;
+  if (mb == 1)
+    return nb == 4   ? launch_thin_blocks<A, 1, 4>(p, s)
+           : nb == 2 ? launch_thin_blocks<A, 1, 2>(p, s)
+                     : launch_thin_blocks<A, 1, 1>(p, s);
+  if (mb == 2)
+    return nb == 4   ? launch_thin_blocks<A, 2, 4>(p, s)
+           : nb == 2 ? launch_thin_blocks<A, 2, 2>(p, s)
+                     : launch_thin_blocks<A, 2, 1>(p, s);
+  return nb == 4   ? launch_thin_blocks<A, 4, 4>(p, s)
+         : nb == 2 ? launch_thin_blocks<A, 4, 2>(p, s)
+                   : launch_thin_blocks<A, 4, 1>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_mx_a16(const MxA16Problem &p, hipStream_t s) {
-  return p.a_format == kBf16 ? launch_a16<kBf16>(p, s) : launch_a16<kF16>(p, s);
+  const ThinProblem t{p.M, p.N, p.K, reinterpret_cast<const unsigned char *>(p.A), 2 * p.lda,
+                      nullptr, 0, p.B, p.C, p.ldc, p.c_format};
+  return p.a_format == kBf16 ? launch_thin<kBf16>(t, s) : launch_thin<kF16>(t, s);
+}
+
+hipError_t launch_mx_thin(const MxProblem &p, hipStream_t s) {
+  const ThinProblem t{p.M, p.N, p.K, p.A.codes, p.A.ld, p.A.scales, p.A.lds, p.B, p.C, p.ldc,
+                      p.c_format};
+  return launch_thin<kMx>(t, s);
 }
 
 }  // namespace gemm_f32_impl

@@ -337,6 +337,7 @@ hipError_t launch_mx_zero(void *C, int M, int N, long long ldc, int c_format, hi
 }
 
 hipError_t launch_mx_gemm(int entry, const MxProblem &p, hipStream_t s) {
+  if (entry == 3) return launch_mx_thin(p, s);
   if (entry == 1 && mx_tile_fits<128>(p)) return launch_mx_tiles<128>(p, s);
   if (entry == 2 && mx_tile_fits<64>(p)) return launch_mx_tiles<64>(p, s);
   const long long tiles_m = ceil_div(p.M, 64), tiles_n = ceil_div(p.N, 64);

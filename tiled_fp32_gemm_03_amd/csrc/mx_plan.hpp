@@ -48,7 +48,7 @@ int moe_check_sizes(int T, int E, int top, int H, int I);
 // The workspace of one call, as byte offsets (each a multiple of 16) and the
 // pitch of u in elements.  u is kept as two planes of bf16, hi and lo, a row
 // per (token, choice) pair in the order of `list`; its rows are padded with
-// zeros to whole 128-deep steps.
+// zeros to whole 512 values.
 struct MoeSpace {
   long long logits;  // double [T][E]
   long long ids;     // int [T top], as chosen
