@@ -580,47 +580,56 @@ class MxTensor:
 
     @classmethod
     def empty(cls, rows: int, K: int, device) -> "MxTensor":
-        return cls(torch.empty((rows, gemm_mx_code_bytes(K)), dtype=torch.uint8, device=device),
-                   torch.empty((rows, gemm_mx_scale_bytes(K)), dtype=torch.uint8, device=device), K)
+        blocks = (K + 31) // 32
+        return cls(torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=device),
+                   torch.empty((rows, (blocks + 15) // 16 * 16), dtype=torch.uint8, device=device), K)
 
 
 def _row_pitch(t) -> int:
-    """Row pitch in bytes of a 2-D uint8 tensor with contiguous rows."""
+    """Row pitch in bytes of a 2-D uint8 tensor with contiguous rows, at least 16."""
     rows, width = t.shape
+    if width > 0 and width % 16 == 0 and t.is_contiguous():
+        return width
     if width > 1 and t.stride(1) != 1:
         raise ValueError("rows must be contiguous (last stride 1)")
     if rows > 1:
         if t.stride(0) < width:
             raise ValueError("rows overlap (row stride smaller than the row length)")
-        return t.stride(0)
+        return max(16, t.stride(0))
     return max(16, (width + 15) // 16 * 16)
 
 
 def _mx_args(q, name: str, device):
     if not isinstance(q, MxTensor):
         raise TypeError(f"{name} must be an MxTensor")
-    if q.codes.dim() != 2:
+    codes, scales = q.codes, q.scales
+    if codes.dim() != 2:
         raise ValueError(f"{name} must be one matrix (2-D codes and scales)")
-    if not q.codes.is_cuda or q.codes.device != device or q.scales.device != device:
+    if not codes.is_cuda or codes.device != device or scales.device != device:
         raise TypeError(f"{name} must be on {device} like the other operands")
-    return (q.codes.data_ptr(), max(16, _row_pitch(q.codes)),
-            q.scales.data_ptr(), max(16, _row_pitch(q.scales)))
+    return codes.data_ptr(), _row_pitch(codes), scales.data_ptr(), _row_pitch(scales)
 
 
-def _on(device):
-    """Makes `device` the current one for a launch (cheap when it is)."""
-    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else _SAME
+def _pitch(t) -> int:
+    """_ld, without its checks where a matrix is contiguous."""
+    if t.dim() == 2 and t.is_contiguous():
+        return t.shape[1] or 1
+    return _ld(t)
 
 
-class _Same:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_SAME = _Same()
+def _launch(fn, where: str, device, stream, args) -> None:
+    """Calls an entry of the library with `device` current, on `stream` or, when
+    it is None, on the device's current stream."""
+    index = device.index
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, stream or None)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream or None)
+    if rc != 0:
+        raise GemmError(rc, where)
 
 
 def _mx_out(out, shape, dtype, device):
@@ -634,39 +643,34 @@ def _mx_out(out, shape, dtype, device):
 def mx_quantize(X, along: str = "rows", out=None, stream=None):
     """The MX form of a float32, bfloat16 or float16 CUDA matrix with unit last
     stride: of its rows, or (``along="columns"``) of its columns."""
-    if X.dtype not in _MX_DTYPES or not X.is_cuda:
+    fmt = _MX_DTYPES.get(X.dtype)
+    if fmt is None or not X.is_cuda:
         raise TypeError("X must be a float32, bfloat16 or float16 CUDA tensor")
-    ldx = _ld(X)
-    way = _along(along)
-    rows, K = X.shape if way == 0 else (X.shape[1], X.shape[0])
+    ldx, device, way = _pitch(X), X.device, _along(along)
+    rows, K = X.shape
+    if way == 1:
+        rows, K = K, rows
     if out is None:
-        out = MxTensor.empty(rows, K, X.device)
+        out = MxTensor.empty(rows, K, device)
     elif out.shape != (rows, K):
         raise ValueError(f"out must be an MxTensor of shape {(rows, K)}")
-    codes, ld, scales, lds = _mx_args(out, "out", X.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(X.device).cuda_stream
-    with _on(X.device):
-        gemm_mx_quantize(rows, K, X.data_ptr(), ldx, _MX_DTYPES[X.dtype], way, codes, ld, scales,
-                         lds, stream)
+    _launch(_lib.gemm_mx_quantize, "gemm_mx_quantize", device, stream,
+            (rows, K, X.data_ptr(), ldx, fmt, way, *_mx_args(out, "out", device)))
     return out
 
 
 def mx_dequantize(q, dtype=torch.float32, along: str = "rows", out=None, stream=None):
     """The values of an MxTensor as a matrix of ``dtype``: its rows as rows, or
     (``along="columns"``) as columns."""
-    if dtype not in _MX_DTYPES:
+    fmt = _MX_DTYPES.get(dtype)
+    if fmt is None:
         raise TypeError("dtype must be float32, bfloat16 or float16")
-    device = q.codes.device
-    codes, ld, scales, lds = _mx_args(q, "q", device)
-    way = _along(along)
+    device, way = q.codes.device, _along(along)
+    args = _mx_args(q, "q", device)
     rows, K = q.shape
     out = _mx_out(out, (rows, K) if way == 0 else (K, rows), dtype, device)
-    if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    with _on(device):
-        gemm_mx_dequantize(rows, K, codes, ld, scales, lds, out.data_ptr(), _ld(out),
-                           _MX_DTYPES[dtype], way, stream)
+    _launch(_lib.gemm_mx_dequantize, "gemm_mx_dequantize", device, stream,
+            (rows, K, *args, out.data_ptr(), _pitch(out), fmt, way))
     return out
 
 
@@ -677,7 +681,8 @@ def matmul_mx(A, B, dtype=torch.float32, out=None, config: int = -1, stream=None
     stride (whose values enter as they are; ``config`` is then not taken).
     ``dtype`` is the result's: float32, bfloat16 or float16.
     """
-    if dtype not in _MX_DTYPES:
+    fmt = _MX_DTYPES.get(dtype)
+    if fmt is None:
         raise TypeError("dtype must be float32, bfloat16 or float16")
     if not isinstance(B, MxTensor):
         raise TypeError("B must be an MxTensor")
@@ -692,19 +697,16 @@ def matmul_mx(A, B, dtype=torch.float32, out=None, config: int = -1, stream=None
             raise TypeError(f"A must be an MxTensor, or a bfloat16 or float16 tensor on {device}")
         if config != -1:
             raise ValueError("config is for products of two MxTensors")
-        a = (A.data_ptr(), _ld(A), _MX_DTYPES[A.dtype])
+        a = (A.data_ptr(), _pitch(A), _MX_DTYPES[A.dtype])
     M, K2 = A.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} and {tuple(B.shape)}")
     out = _mx_out(out, (M, N), dtype, device)
-    ldc = _ld(out)
-    if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    with _on(device):
-        if mx:
-            gemm_mx(M, N, K, *a, *b, out.data_ptr(), ldc, _MX_DTYPES[dtype], config, stream)
-        else:
-            gemm_mx_a16(M, N, K, *a, *b, out.data_ptr(), ldc, _MX_DTYPES[dtype], stream)
+    c = (out.data_ptr(), _pitch(out), fmt)
+    if mx:
+        _launch(_lib.gemm_mx, "gemm_mx", device, stream, (M, N, K, *a, *b, *c, config))
+    else:
+        _launch(_lib.gemm_mx_a16, "gemm_mx_a16", device, stream, (M, N, K, *a, *b, *c))
     return out
 
 
@@ -754,7 +756,7 @@ def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None,
     device = X.device
     if router.dtype != X.dtype or router.device != device:
         raise TypeError(f"router must be a {X.dtype} tensor on {device}")
-    ldx, ldr = _ld(X), _ld(router)
+    ldx, ldr = _pitch(X), _pitch(router)
     T, H = X.shape
     E = router.shape[0]
     if router.shape[1] != H:
@@ -774,18 +776,15 @@ def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None,
         raise ValueError(f"sizes outside the layer's bounds: {T} tokens, {E} experts, top {top}, "
                          f"widths {H} and {I}")
     out = _mx_out(out, (T, H), dtype, device)
-    ldy = _ld(out)
     ids = torch.empty((T, top), dtype=torch.int32, device=device)
     gates = torch.empty((T, top), dtype=torch.float32, device=device)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise TypeError(f"workspace must be a contiguous tensor on {device}")
-    if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    with _on(device):
-        gemm_moe(T, E, top, H, I, X.data_ptr(), ldx, router.data_ptr(), ldr, _MX_DTYPES[X.dtype],
-                 *a1, *a2, int(mx), renormalize, out.data_ptr(), ldy, _MX_DTYPES[dtype],
-                 ids.data_ptr(), gates.data_ptr(), workspace.data_ptr(),
-                 workspace.numel() * workspace.element_size(), stream)
+    _launch(_lib.gemm_moe, "gemm_moe", device, stream,
+            (T, E, top, H, I, X.data_ptr(), ldx, router.data_ptr(), ldr, _MX_DTYPES[X.dtype],
+             *a1, *a2, int(mx), int(renormalize), out.data_ptr(), _pitch(out), _MX_DTYPES[dtype],
+             ids.data_ptr(), gates.data_ptr(), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size()))
     return out, ids, gates

@@ -1,8 +1,10 @@
-// The mixture-of-experts layer for a few tokens (gemm_moe.h), in four
-// launches: the router's logits, the choice of experts, and the two products
-// over the chosen experts' weights.  The products read each chosen expert's
-// weights once, straight into the matrix instructions' operands
-// (mx_thin.hpp); the tokens of one expert share them, 16 rows at a time.
+// The mixture-of-experts layer for a few tokens (gemm_moe.h): the router's
+// logits, the choice of experts, and the two products over the chosen
+// experts' weights.  The products read each chosen expert's weights once,
+// straight into the matrix instructions' operands (mx_thin.hpp); the tokens
+// of one expert share them, 16 rows at a time.  Three launches for up to 8
+// tokens (the choice is made again by each workgroup of the first product),
+// four for more.
 #include "mx_internal.hpp"
 #include "mx_thin.hpp"
 
@@ -14,360 +16,493 @@ __device__ inline T *ws_at(const MoeProblem &p, long long off) {
   return reinterpret_cast<T *>(p.ws + off);
 }
 
+// ---- reductions over a wave, by lane rotations inside rows of 16 lanes -----
+
+template <int CTRL>
+__device__ inline double dpp_f64(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(
+      double, u32x2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)b[0], CTRL, 0xf, 0xf, false),
+                    (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b[1], CTRL, 0xf, 0xf, false)});
+}
+__device__ inline double lane_f64(double v, int lane) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double,
+                            u32x2{(uint32_t)__builtin_amdgcn_readlane((int)b[0], lane),
+                                  (uint32_t)__builtin_amdgcn_readlane((int)b[1], lane)});
+}
+constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;
+__device__ inline double wave_max(double v) {
+  v = __builtin_fmax(v, dpp_f64<kRor8>(v));
+  v = __builtin_fmax(v, dpp_f64<kRor4>(v));
+  v = __builtin_fmax(v, dpp_f64<kRor2>(v));
+  v = __builtin_fmax(v, dpp_f64<kRor1>(v));
+  return __builtin_fmax(__builtin_fmax(lane_f64(v, 0), lane_f64(v, 16)),
+                        __builtin_fmax(lane_f64(v, 32), lane_f64(v, 48)));
+}
+__device__ inline double wave_sum(double v) {
+  v += dpp_f64<kRor8>(v);
+  v += dpp_f64<kRor4>(v);
+  v += dpp_f64<kRor2>(v);
+  v += dpp_f64<kRor1>(v);
+  return (lane_f64(v, 0) + lane_f64(v, 16)) + (lane_f64(v, 32) + lane_f64(v, 48));
+}
+
 // ---- router logits -------------------------------------------------------
-// A wave takes one expert and 4 tokens; a lane 8 consecutive h at a time.
+// A wave takes one expert and TB tokens; a lane 8 consecutive h of each 512.
 // Products and sums in 64 bits, so that the order of experts next to a tie
 // does not depend on the order of the sum.
-constexpr int kLogitTokens = 4;
 
-template <int FMT>
+template <int FMT, int TB>
 __global__ void __launch_bounds__(256) moe_logits_kernel(MoeProblem p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_id();
   const int e = 4 * blockIdx.x + wave;
   if (e >= p.E) return;
-  const int t0 = kLogitTokens * blockIdx.y;
-  double acc[kLogitTokens] = {};
-  for (long long h = 8 * lane; h < p.H; h += 512) {
-    float r[8];
-    load8<FMT>(p.R, e * p.ldr + h, (int)(p.H - h < 8 ? p.H - h : 8), r);
+  const int t0 = TB * blockIdx.y;
+  double acc[TB] = {};
+  const uint16_t *row = p.R + e * p.ldr, *x[TB];
 #pragma unroll
-    for (int i = 0; i < kLogitTokens; ++i) {
-      const int t = t0 + i < p.T ? t0 + i : p.T - 1;
-      float x[8];
-      load8<FMT>(p.X, t * p.ldx + h, (int)(p.H - h < 8 ? p.H - h : 8), x);
+  for (int i = 0; i < TB; ++i) x[i] = p.X + (t0 + i < p.T ? t0 + i : p.T - 1) * p.ldx;
+  auto add = [&](const u32x4 &rw, const u32x4 (&xw)[TB]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i] = fma((double)r[j], (double)x[j], acc[i]);
+    for (int j = 0; j < 8; ++j) {
+      const double r = to_f32<FMT>((uint16_t)(rw[j >> 1] >> (16 * (j & 1))));
+#pragma unroll
+      for (int i = 0; i < TB; ++i)
+        acc[i] = fma(r, (double)to_f32<FMT>((uint16_t)(xw[i][j >> 1] >> (16 * (j & 1)))), acc[i]);
     }
+  };
+  const int whole = p.H & ~511;
+#pragma unroll 4
+  for (int h = 8 * lane; h < whole; h += 512) {
+    u32x4 xw[TB];
+    const u32x4 rw = *reinterpret_cast<const u32x4h *>(row + h);
+#pragma unroll
+    for (int i = 0; i < TB; ++i) xw[i] = *reinterpret_cast<const u32x4h *>(x[i] + h);
+    add(rw, xw);
+  }
+  if (whole + 8 * lane < p.H) {
+    const int h = whole + 8 * lane;
+    u32x4 xw[TB];
+    const u32x4 rw = load_guarded(reinterpret_cast<const unsigned char *>(row), h, p.H - h);
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+      xw[i] = load_guarded(reinterpret_cast<const unsigned char *>(x[i]), h, p.H - h);
+    add(rw, xw);
   }
 #pragma unroll
-  for (int i = 0; i < kLogitTokens; ++i) {
-    double v = acc[i];
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    if (lane == 0 && t0 + i < p.T) ws_at<double>(p, p.at.logits)[(long long)(t0 + i) * p.E + e] = v;
+  for (int i = 0; i < TB; ++i) {
+    const double v = wave_sum(acc[i]);
+    if (lane == 0 && t0 + i < p.T) ws_at<double>(p, p.at.logits)[(t0 + i) * p.E + e] = v;
   }
 }
 
 // ---- the choice of experts --------------------------------------------------
-// One workgroup.  A wave takes a token: `top` times the largest of the logits
-// not yet taken (ties to the lower index), then the gates.  Then the pairs
-// (token, choice) are listed by expert: ranks inside 64 pairs by ballots,
-// added to the counts of the 64-pair chunks before.
-constexpr int kRouteThreads = 1024;
-constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTop;
+// A wave takes a token: `top` times the largest logit not yet taken (ties to
+// the lower index; a NaN counts as -infinity), then the gates.  Then the
+// pairs (token, choice) are listed by expert: ranks inside 64 pairs by
+// ballots, added to the counts of the 64-pair chunks before.
+
 constexpr int kPerLane = kMoeMaxExperts / 64;
+constexpr int kFusedTokens = 8;
 
-// Doubles as integers of the same order; NaN as -infinity, so that every
-// expert can be chosen and INT64_MIN is below all.
-__device__ inline long long order_key(double v) {
-  if (v != v) v = -__builtin_inf();
-  const long long b = __builtin_bit_cast(long long, v);
-  return b >= 0 ? b : b ^ 0x7fffffffffffffffLL;
-}
+template <int MAX_PAIRS>
+struct Route {
+  float gate[MAX_PAIRS];               // by pair
+  unsigned short chosen[MAX_PAIRS];    // by pair
+  unsigned short list[MAX_PAIRS];      // pairs by expert
+  unsigned short count[(MAX_PAIRS + 63) / 64][kMoeMaxExperts];
+  unsigned short start[kMoeMaxExperts + 1];
+  unsigned short active[kMoeMaxExperts];
+  int nactive;
+};
 
-__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(MoeProblem p) {
-  __shared__ unsigned short chosen[kMaxPairs];
-  __shared__ unsigned short count[kMaxPairs / 64][kMoeMaxExperts];
-  __shared__ int first[kMoeMaxExperts + 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int kWaves = kRouteThreads / 64;
-  const int pairs = p.T * p.top, chunks = (pairs + 63) / 64;
-  const double *logits = ws_at<double>(p, p.at.logits);
-  int *ids = ws_at<int>(p, p.at.ids);
-  float *gates = ws_at<float>(p, p.at.gates);
-
-  for (int i = threadIdx.x; i < chunks * kMoeMaxExperts; i += kRouteThreads)
-    (&count[0][0])[i] = 0;
-
-  for (int t = wave; t < p.T; t += kWaves) {
-    double z[kPerLane];
-    long long key[kPerLane];
+template <int MAX_PAIRS>
+__device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, int t) {
+  const int lane = threadIdx.x & 63;
+  const double *logits = ws_at<double>(p, p.at.logits) + t * p.E;
+  const double low = -__builtin_inf();
+  double z[kPerLane], key[kPerLane];
+  unsigned taken = 0;  // bit i: expert lane + 64 i is taken, or past E
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int e = lane + 64 * i;
+    const bool in = e < p.E;
+    z[i] = in ? logits[e] : low;
+    taken |= in ? 0u : 1u << i;
+    nan |= z[i] != z[i];
+    key[i] = z[i] != z[i] ? low : z[i];
+  }
+  int id = 0;          // lane s: choice s,
+  double value = 0.0;  // its logit
+  for (int s = 0; s < p.top; ++s) {
+    double best = low;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (64 * i < p.E && !(taken >> i & 1)) best = __builtin_fmax(best, key[i]);
+    best = wave_max(best);
+    bool found = false;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
-      const int e = lane + 64 * i;
-      z[i] = e < p.E ? logits[(long long)t * p.E + e] : 0.0;
-      key[i] = e < p.E ? order_key(z[i]) : (long long)0x8000000000000000ULL;
-    }
-    double zmax = 0.0, total = 0.0, mine = 0.0;
-    for (int s = 0; s < p.top; ++s) {
-      long long best = key[0];
-      int at = lane;
-#pragma unroll
-      for (int i = 1; i < kPerLane; ++i)
-        if (key[i] > best) best = key[i], at = lane + 64 * i;
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) {
-        const long long ob = __shfl_xor(best, d);
-        const int oa = __shfl_xor(at, d);
-        if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
-      }
-      double v = 0.0;  // the chosen logit, from the lane that holds it
-#pragma unroll
-      for (int i = 0; i < kPerLane; ++i)
-        if (at == lane + 64 * i) {
-          v = z[i];
-          key[i] = (long long)0x8000000000000000ULL;
-        }
-      v = __shfl(v, at & 63);
-      if (s == 0) {
-        // The largest logit; a NaN among the logits makes every gate NaN.
-        zmax = v;
-        double part = 0.0;
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
-          if (lane + 64 * i < p.E) {
-            nan |= z[i] != z[i];
-            if (!p.renormalize) part += exp(z[i] - zmax);
-          }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) part += __shfl_xor(part, d);
-        total = __any(nan) ? __builtin_nan("") : part;
-      }
-      const double w = exp(v - zmax);
-      if (p.renormalize) total += w;
-      if (lane == s) mine = w;
-      if (lane == 0) {
-        chosen[t * p.top + s] = (unsigned short)at;
-        ids[t * p.top + s] = at;
-        if (p.ids) p.ids[t * p.top + s] = at;
-      }
-    }
-    if (lane < p.top) {
-      const float gate = (float)(mine / total);
-      gates[t * p.top + lane] = gate;
-      if (p.gates) p.gates[t * p.top + lane] = gate;
+      if (found || 64 * i >= p.E) continue;  // uniform
+      const unsigned long long m = __ballot(!(taken >> i & 1) && key[i] == best);
+      if (m == 0) continue;
+      found = true;
+      const int at = __builtin_ctzll(m);
+      if (lane == at) taken |= 1u << i;
+      if (lane == s) id = 64 * i + at, value = best;
     }
   }
-  __syncthreads();
-
-  // Counts per chunk of 64 pairs, and each pair's rank in its chunk.
-  for (int c = wave; c < chunks; c += kWaves) {
-    const int i = 64 * c + lane;
-    const int e = i < pairs ? chosen[i] : kMoeMaxExperts;
-    unsigned long long same = __ballot(1);
+  // Gates: a NaN among the logits makes every one NaN.
+  const double zmax = lane_f64(value, 0);
+  double w = lane < p.top ? exp(value - zmax) : 0.0, part = w;
+  if (!p.renormalize) {
+    part = 0.0;
 #pragma unroll
-    for (int b = 0; b < 10; ++b) {
-      const unsigned long long m = __ballot((e >> b) & 1);
-      same &= (e >> b) & 1 ? m : ~m;
-    }
-    if (i < pairs && (same & ((1ULL << lane) - 1)) == 0)
-      count[c][e] = (unsigned short)__popcll(same);
+    for (int i = 0; i < kPerLane; ++i)
+      if (64 * i < p.E) part += lane + 64 * i < p.E ? exp(z[i] - zmax) : 0.0;
+  }
+  const double total = __any(nan) ? __builtin_nan("") : wave_sum(part);
+  if (lane < p.top) {
+    r.chosen[t * p.top + lane] = (unsigned short)id;
+    r.gate[t * p.top + lane] = (float)(w / total);
+  }
+}
+
+// Lanes of the wave whose pair has the same expert as this lane's.
+__device__ inline unsigned long long same_expert(int e) {
+  unsigned long long same = ~0ULL;
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {
+    const unsigned long long m = __ballot((e >> b) & 1);
+    same &= (e >> b) & 1 ? m : ~m;
+  }
+  return same;
+}
+
+template <int THREADS, int MAX_PAIRS>
+__device__ inline void route_all(const MoeProblem &p, Route<MAX_PAIRS> &r) {
+  constexpr int kWaves = THREADS / 64;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int pairs = p.T * p.top, chunks = (pairs + 63) / 64;
+  const unsigned long long before = (1ULL << lane) - 1;
+  for (int c = 0; c < chunks; ++c)
+    for (int e = threadIdx.x; e < p.E; e += THREADS) r.count[c][e] = 0;
+  for (int t = wave; t < p.T; t += kWaves) choose_experts(p, r, t);
+  __syncthreads();
+  for (int c = wave; c < chunks; c += kWaves) {
+    const int i = 64 * c + lane, e = i < pairs ? r.chosen[i] : kMoeMaxExperts;
+    const unsigned long long same = same_expert(e);
+    if (i < pairs && (same & before) == 0) r.count[c][e] = (unsigned short)__popcll(same);
   }
   __syncthreads();
   if (wave == 0) {  // where each expert's pairs begin, and the chosen experts
     int base = 0, nact = 0;
-    int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
     for (int e0 = 0; e0 < p.E; e0 += 64) {
       const int e = e0 + lane;
       int n = 0;
       if (e < p.E)
-        for (int c = 0; c < chunks; ++c) n += count[c][e];
+        for (int c = 0; c < chunks; ++c) n += r.count[c][e];
       int upto = n;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const int v = __shfl_up(upto, d);
         if (lane >= d) upto += v;
       }
-      if (e < p.E) first[e] = start[e] = base + upto - n;
+      if (e < p.E) r.start[e] = (unsigned short)(base + upto - n);
       const unsigned long long on = __ballot(n > 0);
-      if (n > 0) active[1 + nact + __popcll(on & ((1ULL << lane) - 1))] = e;
+      if (n > 0) r.active[nact + __popcll(on & before)] = (unsigned short)e;
       base += __shfl(upto, 63);
       nact += __popcll(on);
     }
     if (lane == 0) {
-      active[0] = nact;
-      start[p.E] = pairs;
+      r.nactive = nact;
+      r.start[p.E] = (unsigned short)pairs;
     }
   }
   __syncthreads();
-  int *list = ws_at<int>(p, p.at.list);
   for (int c = wave; c < chunks; c += kWaves) {
-    const int i = 64 * c + lane;
-    const int e = i < pairs ? chosen[i] : kMoeMaxExperts;
-    unsigned long long same = __ballot(1);
-#pragma unroll
-    for (int b = 0; b < 10; ++b) {
-      const unsigned long long m = __ballot((e >> b) & 1);
-      same &= (e >> b) & 1 ? m : ~m;
-    }
+    const int i = 64 * c + lane, e = i < pairs ? r.chosen[i] : kMoeMaxExperts;
+    const unsigned long long same = same_expert(e);
     if (i < pairs) {
-      int at = first[e] + __popcll(same & ((1ULL << lane) - 1));
-      for (int q = 0; q < c; ++q) at += count[q][e];
-      list[at] = i;
+      int at = r.start[e] + __popcll(same & before);
+      for (int q = 0; q < c; ++q) at += r.count[q][e];
+      r.list[at] = (unsigned short)i;
     }
   }
+  __syncthreads();
+}
+
+// The route in the workspace, for the kernels that follow, and the caller's
+// ids and gates.
+template <int THREADS, int MAX_PAIRS>
+__device__ inline void write_route(const MoeProblem &p, const Route<MAX_PAIRS> &r) {
+  const int pairs = p.T * p.top;
+  int *list = ws_at<int>(p, p.at.list), *start = ws_at<int>(p, p.at.start);
+  int *active = ws_at<int>(p, p.at.active);
+  float *gates = ws_at<float>(p, p.at.gates);
+  for (int i = threadIdx.x; i < pairs; i += THREADS) {
+    list[i] = r.list[i];
+    gates[i] = r.gate[i];
+    if (p.ids) p.ids[i] = r.chosen[i];
+    if (p.gates) p.gates[i] = r.gate[i];
+  }
+  for (int e = threadIdx.x; e <= p.E; e += THREADS) start[e] = r.start[e];
+  for (int a = threadIdx.x; a < r.nactive; a += THREADS) active[1 + a] = r.active[a];
+  if (threadIdx.x == 0) active[0] = r.nactive;
+}
+
+constexpr int kRouteThreads = 1024;
+__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(MoeProblem p) {
+  __shared__ Route<kMoeMaxTokens * kMoeMaxTop> r;
+  route_all<kRouteThreads>(p, r);
+  write_route<kRouteThreads>(p, r);
 }
 
 // ---- first product: u = silu(gate) * other ------------------------------------
-// A workgroup takes one chosen expert and 16 of its inner columns, both
-// factors; its waves take 128-deep steps of H in turn.
+// A unit is one chosen expert and 16 of its inner columns, both factors.  `ks`
+// waves share a unit, taking the pieces of H in turn: one wave per unit where
+// there are units enough to fill the chip, more where there are few.
 
-constexpr int kUpWaves = 8;
+constexpr int kUpWaves = 4;
+typedef f32x4 UpPart[2][2][64];  // [block of rows][factor][lane]
 
 template <int W, int AF, int MB>
-__device__ inline void moe_up_rows(const MoeProblem &p, const Row (&w)[2], int first, int n,
-                                   int i0, f32x4 (*part)[2][2][64]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int l16 = lane & 15, g = lane >> 4;
-  const int *list = ws_at<int>(p, p.at.list) + first;
-  Row x[MB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int m = 16 * i + l16 < n ? 16 * i + l16 : n - 1;
-    x[i] = {reinterpret_cast<const unsigned char *>(p.X + list[m] / p.top * p.ldx), nullptr};
-  }
+__device__ __forceinline__ void moe_up_rows(const MoeProblem &p, const Row (&w)[2],
+                                            const Row (&x)[MB], int first, int n, int i0, int ks,
+                                            bool any, UpPart *part) {
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int l16 = lane & 15, g = lane >> 4, kw = wave & (ks - 1);
   Thin<W, AF, MB, 2> t;
   t.clear();
-  t.run(x, w, wave, kUpWaves, (int)ceil_div(p.H, kPieceK<W>), p.H, g);
+  if (any) t.run(x, w, kw, ks, (int)ceil_div(p.H, kPieceK<W>), p.H, g);
+  if (ks > 1) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      part[wave][i][0][lane] = t.acc[i][0];
+      part[wave][i][1][lane] = t.acc[i][1];
+    }
+    __syncthreads();
+    if (kw == 0)
+      for (int q = 1; q < ks; ++q)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          t.acc[i][0] += part[wave + q][i][0][lane];
+          t.acc[i][1] += part[wave + q][i][1][lane];
+        }
+    __syncthreads();
+  }
+  if (kw != 0 || !any) return;
 #pragma unroll
   for (int i = 0; i < MB; ++i) {
-    part[wave][i][0][lane] = t.acc[i][0];
-    part[wave][i][1][lane] = t.acc[i][1];
-  }
-  __syncthreads();
-  if (wave < MB) {
-    f32x4 a = part[0][wave][0][lane], b = part[0][wave][1][lane];
+    const int m = 16 * i + l16;
+    if (m >= n) continue;
+    uint16_t hi[4], lo[4];
 #pragma unroll
-    for (int q = 1; q < kUpWaves; ++q) {
-      a += part[q][wave][0][lane];
-      b += part[q][wave][1][lane];
+    for (int j = 0; j < 4; ++j) {
+      const float a = t.acc[i][0][j], b = t.acc[i][1][j];
+      const float u = a / (1.f + expf(-a)) * b;
+      const float v = i0 + 4 * g + j < p.I ? u : 0.f;  // rows are padded with zeros
+      hi[j] = from_f32<kBf16>(v);
+      const float h = to_f32<kBf16>(hi[j]);
+      lo[j] = mag_bits(h) < 0x7f800000u ? from_f32<kBf16>(v - h) : (uint16_t)0;
     }
-    const int m = 16 * wave + l16;
-    if (m < n) {
-      uint16_t hi[4], lo[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float u = a[j] / (1.f + expf(-a[j])) * b[j];
-        const float v = i0 + 4 * g + j < p.I ? u : 0.f;  // rows are padded with zeros
-        hi[j] = from_f32<kBf16>(v);
-        const float h = to_f32<kBf16>(hi[j]);
-        lo[j] = mag_bits(h) < 0x7f800000u ? from_f32<kBf16>(v - h) : (uint16_t)0;
-      }
-      const long long at = (first + m) * p.at.pitch + i0 + 4 * g;
-      *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.hi) + at) =
-          u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
-      *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.lo) + at) =
-          u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
-    }
+    const long long at = (first + m) * p.at.pitch + i0 + 4 * g;
+    *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.hi) + at) =
+        u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
+    *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.lo) + at) =
+        u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
   }
-  __syncthreads();
 }
 
-template <int W, int AF>
-__global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeProblem p) {
-  __shared__ f32x4 part[kUpWaves][2][2][64];
-  const int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
-  if ((int)blockIdx.y >= active[0]) return;
-  const int e = active[1 + blockIdx.y];
-  const int first = start[e], n = start[e + 1] - first;
-  const int i0 = 16 * blockIdx.x, l16 = threadIdx.x & 15;
+// FUSED: at most kFusedTokens tokens, each workgroup makes the choice itself.
+template <int W, int AF, bool FUSED>
+__global__ void __launch_bounds__(64 * kUpWaves, W == kMx ? 3 : 4) moe_up_kernel(MoeProblem p, int ks) {
+  __shared__ UpPart part[kUpWaves];
+  __shared__ Route<FUSED ? kFusedTokens * kMoeMaxTop : 1> route;
+  const int wave = wave_id(), l16 = threadIdx.x & 15;
+  int e, first, n;
+  if constexpr (FUSED) {
+    route_all<64 * kUpWaves>(p, route);
+    if (blockIdx.x == 0 && blockIdx.y == 0) write_route<64 * kUpWaves>(p, route);
+    if ((int)blockIdx.y >= route.nactive) return;
+    e = __builtin_amdgcn_readfirstlane(route.active[blockIdx.y]);
+    first = __builtin_amdgcn_readfirstlane(route.start[e]);
+    n = __builtin_amdgcn_readfirstlane(route.start[e + 1]) - first;
+  } else {
+    const int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
+    if ((int)blockIdx.y >= active[0]) return;
+    e = active[1 + blockIdx.y];
+    first = start[e];
+    n = start[e + 1] - first;
+  }
+  auto token_row = [&](int m) __attribute__((always_inline)) {
+    const int at = first + (m < n ? m : n - 1);
+    const int pair = FUSED ? (int)route.list[at] : ws_at<int>(p, p.at.list)[at];
+    return Row{reinterpret_cast<const unsigned char *>(p.X + pair / p.top * p.ldx), nullptr};
+  };
+  const int units = kUpWaves / ks;
+  const int i0 = 16 * (int)(blockIdx.x * units + wave / ks);
+  const bool any = i0 < p.at.pitch;  // the last workgroup may have units too many
   const int i = i0 + l16 < p.I ? i0 + l16 : p.I - 1;
   const long long r0 = 2LL * p.I * e + i, r1 = r0 + p.I;
   Row w[2] = {{p.W1 + r0 * p.ld1, nullptr}, {p.W1 + r1 * p.ld1, nullptr}};
   if constexpr (W == kMx) w[0].q = p.S1 + r0 * p.lds1, w[1].q = p.S1 + r1 * p.lds1;
   if (n <= 16) {
-    moe_up_rows<W, AF, 1>(p, w, first, n, i0, part);
+    const Row x[1] = {token_row(l16)};
+    moe_up_rows<W, AF, 1>(p, w, x, first, n, i0, ks, any, part);
   } else {
-    for (int m = 0; m < n; m += 32) moe_up_rows<W, AF, 2>(p, w, first + m, n - m, i0, part);
+    for (int m = 0; m < n; m += 32) {
+      const Row x[2] = {token_row(m + l16), token_row(m + 16 + l16)};
+      moe_up_rows<W, AF, 2>(p, w, x, first + m, n - m, i0, ks, any, part);
+    }
   }
 }
 
 // ---- second product and the weighted sum -----------------------------------------
-// A workgroup owns 16 columns of Y for all tokens.  Its waves take pieces of
-// an expert's inner columns in turn, over all chosen experts, and add each
-// run of pieces, times the gates, to a sum of their own in LDS; the waves'
-// sums are added in wave order at the end.
-constexpr int kDownWaves = 8;
-template <int W>
-constexpr int kRunPieces = W == kMx ? 1 : 4;  // 512 k
+// A workgroup owns 16 columns of Y for all tokens.  The pieces of all chosen
+// experts' inner columns, one expert after the other, are dealt to its waves
+// in equal runs; a wave loads the next piece's weights while it uses one, and
+// adds each piece's rows, times their gates, to a sum of its own in LDS.  The
+// waves' sums are added in wave order at the end.
 
-template <int W, int MB>
-__device__ inline void moe_down_run(const MoeProblem &p, const Row &row, int first, int n, int p0,
-                                    int p1, float *sum) {
-  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  Row u[MB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int m = 16 * i + l16 < n ? 16 * i + l16 : n - 1;
-    u[i] = {p.ws + p.at.hi + 2 * (first + m) * p.at.pitch,
-            p.ws + p.at.lo + 2 * (first + m) * p.at.pitch};
-  }
-  Thin<W, kSplit, MB, 1> t;
-  t.clear();
-  const Row w[1] = {row};
-  t.run(u, w, p0, 1, p1, p.I, g);
-  const int *list = ws_at<int>(p, p.at.list) + first;
-  const float *gates = ws_at<float>(p, p.at.gates);
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int m = 16 * i + l16;
-    if (m < n) {
-      const int pair = list[m];
-      f32x4 *to = reinterpret_cast<f32x4 *>(sum + 16 * (pair / p.top) + 4 * g);
-      *to += gates[pair] * t.acc[i][0];
-    }
-  }
+// LDS of the second product: sums [wave][token][16], then the route.
+struct DownLds {
+  int gates, start, active, tokens, bytes;
+};
+constexpr DownLds down_lds(int waves, int T, int E, int top) {
+  const int pairs = T * top;
+  const int gates = waves * T * 64, start = gates + 4 * pairs, active = start + 2 * (E + 1),
+            tokens = active + 2 * E;
+  return {gates, start, active, tokens, tokens + 2 * pairs};
 }
 
-template <int W>
-__global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeProblem p) {
-  extern __shared__ __attribute__((aligned(16))) float sums[];  // [wave][token][16]
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  float *sum = sums + wave * 16 * p.T;
-  for (int i = lane; i < 4 * p.T; i += 64) reinterpret_cast<f32x4 *>(sum)[i] = f32x4{0, 0, 0, 0};
+template <int W, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) moe_down_kernel(MoeProblem p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  constexpr int kThreads = 64 * WAVES;
+  const DownLds at = down_lds(WAVES, p.T, p.E, p.top);
+  float *gate = reinterpret_cast<float *>(lds + at.gates);  // by place in the list
+  unsigned short *start = reinterpret_cast<unsigned short *>(lds + at.start);
+  unsigned short *active = reinterpret_cast<unsigned short *>(lds + at.active);
+  unsigned short *token = reinterpret_cast<unsigned short *>(lds + at.tokens);  // by place
+  const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int nact = ws_at<int>(p, p.at.active)[0], pairs = p.T * p.top;
+  for (int i = threadIdx.x; i < 4 * p.T * WAVES; i += kThreads)
+    reinterpret_cast<f32x4 *>(lds)[i] = f32x4{0, 0, 0, 0};
+  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+    const int pair = ws_at<int>(p, p.at.list)[i];
+    gate[i] = ws_at<float>(p, p.at.gates)[pair];
+    token[i] = (unsigned short)(pair / p.top);
+  }
+  for (int i = threadIdx.x; i <= p.E; i += kThreads)
+    start[i] = (unsigned short)ws_at<int>(p, p.at.start)[i];
+  for (int i = threadIdx.x; i < nact; i += kThreads)
+    active[i] = (unsigned short)ws_at<int>(p, p.at.active)[1 + i];
   __syncthreads();
-  const int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
-  const int n0 = 16 * blockIdx.x, l16 = lane & 15;
+
+  float *sum = reinterpret_cast<float *>(lds) + wave * 16 * p.T;
+  const int n0 = 16 * blockIdx.x, nb = (int)mx_blocks(p.I);
   const int col = n0 + l16 < p.H ? n0 + l16 : p.H - 1;
-  const int pieces = (int)ceil_div(p.I, kPieceK<W>), runs = (int)ceil_div(pieces, kRunPieces<W>);
-  const int units = active[0] * runs;
-  for (int v = wave; v < units; v += kDownWaves) {
-    const int e = active[1 + v / runs], run = v % runs;
-    const int first = start[e], n = start[e + 1] - first;
+  const int pieces = (int)ceil_div(p.I, kPieceK<W>), whole = p.I / kPieceK<W>;
+  const long long all = (long long)nact * pieces;
+  const int from = (int)(all * wave / WAVES), to = (int)(all * (wave + 1) / WAVES);
+  typedef Thin<W, kSplit, 1, 1> Product;
+  auto load = [&](typename Product::Piece &x, int v) __attribute__((always_inline)) {
+    const int e = __builtin_amdgcn_readfirstlane(active[v / pieces]);
     const long long r = (long long)p.H * e + col;
     const Row row{p.W2 + r * p.ld2, W == kMx ? p.S2 + r * p.lds2 : nullptr};
-    const int p0 = run * kRunPieces<W>;
-    const int p1 = p0 + kRunPieces<W> < pieces ? p0 + kRunPieces<W> : pieces;
-    if (n <= 16) {
-      moe_down_run<W, 1>(p, row, first, n, p0, p1, sum);
-    } else {
-      for (int m = 0; m < n; m += 32)
-        moe_down_run<W, 2>(p, row, first + m, n - m, p0, p1, sum);
+    const int piece = v % pieces;
+    if constexpr (W == kMx) x = load_mx_piece(row, piece, g, nb);
+    else if (piece < whole) x = load_half_piece(row, piece, g);
+    else x = load_half_guarded(row, piece, g, p.I);
+  };
+  auto use = [&](typename Product::Piece (&x)[1], int v) __attribute__((always_inline)) {
+    const int e = __builtin_amdgcn_readfirstlane(active[v / pieces]), piece = v % pieces;
+    const int first = __builtin_amdgcn_readfirstlane(start[e]);
+    const int last = __builtin_amdgcn_readfirstlane(start[e + 1]);
+    if constexpr (W == kMx)
+      if (piece >= whole) mask_mx_piece(x[0], piece, g, nb);
+    for (int m0 = first; m0 < last; m0 += 16) {
+      const int m = m0 + l16 < last ? m0 + l16 : last - 1;
+      const Row u[1] = {{p.ws + p.at.hi + 2 * m * p.at.pitch, p.ws + p.at.lo + 2 * m * p.at.pitch}};
+      Product t;
+      t.clear();
+      t.template use<false>(x, u, piece, g, p.I, nb);
+      if (m0 + l16 < last) {
+        f32x4 *y = reinterpret_cast<f32x4 *>(sum + 16 * token[m] + 4 * g);
+        *y += gate[m] * t.acc[0][0];
+      }
     }
+  };
+  typename Product::Piece x[1], y[1];  // by turns
+  if (from < to) load(x[0], from);
+  for (int v = from; v < to; v += 2) {
+    load(y[0], v + 1 < to ? v + 1 : v);
+    use(x, v);
+    if (v + 1 >= to) break;
+    load(x[0], v + 2 < to ? v + 2 : v + 1);
+    use(y, v + 1);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 4 * p.T; i += 64 * kDownWaves) {
-    f32x4 v = reinterpret_cast<const f32x4 *>(sums)[i];
+  for (int i = threadIdx.x; i < 4 * p.T; i += kThreads) {
+    const f32x4 *s = reinterpret_cast<const f32x4 *>(lds) + i;
+    f32x4 v = s[0];
 #pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) v += reinterpret_cast<const f32x4 *>(sums + w * 16 * p.T)[i];
+    for (int w = 1; w < WAVES; ++w) v += s[w * 4 * p.T];
     const int t = i / 4, n = n0 + 4 * (i % 4);
     store4_fmt(p.y_format, p.Y, t * p.ldy + n, p.H - n < 4 ? p.H - n : 4, v);
   }
 }
 
+template <int FMT>
+hipError_t launch_logits(const MoeProblem &p, hipStream_t s) {
+  const unsigned gx = (unsigned)ceil_div(p.E, 4);
+  if (p.T == 1) return launch_kernel(moe_logits_kernel<FMT, 1>, dim3(gx), dim3(256), s, p);
+  return launch_kernel(moe_logits_kernel<FMT, 4>, dim3(gx, (unsigned)ceil_div(p.T, 4)), dim3(256),
+                       s, p);
+}
+
+template <int W, int AF>
+hipError_t launch_up(const MoeProblem &p, hipStream_t s) {
+  const int pairs = p.T * p.top;
+  const long long experts = p.E < pairs ? p.E : pairs, cols = p.at.pitch / 16;
+  // Waves per unit: until 16 waves per compute unit, or a piece for each.
+  int ks = 1;
+  while (ks < kUpWaves && cols * experts * ks < 16 * 256 && 2 * ks * kPieceK<W> <= p.H) ks *= 2;
+  const dim3 grid((unsigned)ceil_div(cols * ks, kUpWaves), (unsigned)experts);
+  return launch_kernel(p.T <= kFusedTokens ? moe_up_kernel<W, AF, true> : moe_up_kernel<W, AF, false>,
+                       grid, dim3(64 * kUpWaves), s, p, ks);
+}
+
+template <int W, int WAVES>
+hipError_t launch_down_waves(const MoeProblem &p, hipStream_t s) {
+  MoeProblem q = p;
+  void *args[] = {&q};
+  return hipLaunchKernel(reinterpret_cast<const void *>(moe_down_kernel<W, WAVES>),
+                         dim3((unsigned)ceil_div(p.H, 16)), dim3(64 * WAVES), args,
+                         (size_t)down_lds(WAVES, p.T, p.E, p.top).bytes, s);
+}
+template <int W>
+hipError_t launch_down(const MoeProblem &p, hipStream_t s) {
+  return p.T <= 64 ? launch_down_waves<W, 16>(p, s) : launch_down_waves<W, 8>(p, s);
+}
+
 }  // namespace
 
 hipError_t launch_moe(const MoeProblem &p, hipStream_t s) {
-  const int pairs = p.T * p.top;
-  const dim3 lgrid((unsigned)ceil_div(p.E, 4), (unsigned)ceil_div(p.T, kLogitTokens));
-  hipError_t e = launch_kernel(
-      p.format == kBf16 ? moe_logits_kernel<kBf16> : moe_logits_kernel<kF16>, lgrid, dim3(256), s, p);
+  const bool bf16 = p.format == kBf16;
+  hipError_t e = bf16 ? launch_logits<kBf16>(p, s) : launch_logits<kF16>(p, s);
   if (e != hipSuccess) return e;
-  e = launch_kernel(moe_route_kernel, dim3(1), dim3(kRouteThreads), s, p);
+  if (p.T > kFusedTokens) {
+    e = launch_kernel(moe_route_kernel, dim3(1), dim3(kRouteThreads), s, p);
+    if (e != hipSuccess) return e;
+  }
+  e = p.mx ? (bf16 ? launch_up<kMx, kBf16>(p, s) : launch_up<kMx, kF16>(p, s))
+           : (bf16 ? launch_up<kBf16, kBf16>(p, s) : launch_up<kF16, kF16>(p, s));
   if (e != hipSuccess) return e;
-  const dim3 ugrid((unsigned)(p.at.pitch / 16), (unsigned)(p.E < pairs ? p.E : pairs));
-  auto up = p.mx ? (p.format == kBf16 ? moe_up_kernel<kMx, kBf16> : moe_up_kernel<kMx, kF16>)
-                 : (p.format == kBf16 ? moe_up_kernel<kBf16, kBf16> : moe_up_kernel<kF16, kF16>);
-  e = launch_kernel(up, ugrid, dim3(64 * kUpWaves), s, p);
-  if (e != hipSuccess) return e;
-  auto down = p.mx                ? moe_down_kernel<kMx>
-              : p.format == kBf16 ? moe_down_kernel<kBf16>
-                                  : moe_down_kernel<kF16>;
-  MoeProblem q = p;
-  void *args[] = {&q};
-  return hipLaunchKernel(reinterpret_cast<const void *>(down), dim3((unsigned)ceil_div(p.H, 16)),
-                         dim3(64 * kDownWaves), args, (size_t)kDownWaves * 64 * p.T, s);
+  return p.mx ? launch_down<kMx>(p, s) : bf16 ? launch_down<kBf16>(p, s) : launch_down<kF16>(p, s);
 }
 
 }  // namespace gemm_f32_impl

@@ -13,7 +13,7 @@ template <int WAVES, int MB, int NB>
 __device__ __forceinline__ void thin_store(const f32x4 (&acc)[MB][NB], f32x4 (*part)[4][64],
                                            long long m0, long long n0, int M, int N, void *C,
                                            long long ldc, int c_format) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_id();
   constexpr int kBlocks = MB * NB, kRound = kBlocks < 4 ? kBlocks : 4;
 #pragma unroll
   for (int r = 0; r < kBlocks; r += kRound) {
@@ -48,7 +48,7 @@ struct ThinProblem {
 template <int A, int MB, int NB, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES) mx_thin_kernel(ThinProblem p) {
   __shared__ f32x4 part[WAVES][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_id();
   const int l16 = lane & 15, g = lane >> 4;
   const long long n0 = 16LL * NB * blockIdx.x;
   Row w[NB];

@@ -187,6 +187,9 @@ __device__ inline int piece_k(int g, int s, int j) {
   return W == kMx ? 128 * s + 32 * g + 8 * j : 32 * j + 8 * g;
 }
 
+// The wave's number in its workgroup, as a scalar.
+__device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // One product of thin operands: MB blocks of 16 rows of kind A by NB blocks
 // of 16 rows of weights of kind W.  `mine` says which pieces this wave takes:
 // first, first + step, ... below `pieces`.
@@ -254,7 +257,7 @@ struct Thin {
   __device__ __forceinline__ void multiply(const Piece (&x)[NB], const Row (&a)[MB], int piece,
                                            int g, int K) {
 #pragma unroll
-    for (int s = 0; s < kPieceSteps<W>; ++s)
+    for (int s = 0; s < kPieceSteps<W>; ++s) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         u32x4 w[NB];
@@ -295,6 +298,10 @@ struct Thin {
           }
         }
       }
+      // One step's activations at a time: hoisted all together their
+      // registers would cost the waves that hide their latency.
+      if constexpr (kPieceSteps<W> > 1) __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   // Adds this wave's pieces first, first + step, ... below `end` of the K
@@ -306,16 +313,23 @@ struct Thin {
     int p = first;
     Piece x[NB];
     if (p < last) load(x, w, p, g, K, nb);
-    for (; p < last; p += step) {
-      if constexpr (NB >= 4) {  // 16 KB per piece: in flight enough, and no registers for two
+    if constexpr (W == kMx && NB > 1) {  // 8 KB or more in flight; registers for waves instead
+      for (; p < last; p += step) {
         use<false>(x, a, p, g, K, nb);
         load(x, w, p + step < last ? p + step : p, g, K, nb);
-      } else {
-        Piece next[NB];
-        load(next, w, p + step < last ? p + step : p, g, K, nb);
+      }
+    } else {
+      // Two pieces by turns: handing the loaded one on in registers would
+      // wait for it.
+      Piece y[NB];
+      while (p < last) {
+        load(y, w, p + step < last ? p + step : p, g, K, nb);
         use<false>(x, a, p, g, K, nb);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) x[b] = next[b];
+        p += step;
+        if (p >= last) break;
+        load(x, w, p + step < last ? p + step : p, g, K, nb);
+        use<false>(y, a, p, g, K, nb);
+        p += step;
       }
     }
     if (p < end) {  // the piece that reaches past K
