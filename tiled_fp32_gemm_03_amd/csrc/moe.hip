@@ -266,17 +266,20 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(MoeProblem p) 
 // there are units enough to fill the chip, more where there are few.
 
 constexpr int kUpWaves = 4;
-typedef f32x4 UpPart[2][2][64];  // [block of rows][factor][lane]
+typedef f32x4 UpPart[1][2][64];  // [block of rows][factor][lane]
 
-template <int W, int AF, int MB>
+template <int W, int AF, int MB, bool ODD>
 __device__ __forceinline__ void moe_up_rows(const MoeProblem &p, const Row (&w)[2],
                                             const Row (&x)[MB], int first, int n, int i0, int ks,
                                             bool any, UpPart *part) {
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int l16 = lane & 15, g = lane >> 4, kw = wave & (ks - 1);
-  Thin<W, AF, MB, 2> t;
+  bool valid[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) valid[i] = 16 * i + l16 < n;
+  Thin<W, AF, MB, 2, ODD> t;
   t.clear();
-  if (any) t.run(x, w, kw, ks, (int)ceil_div(p.H, kPieceK<W>), p.H, g);
+  if (any) t.run(x, valid, w, kw, ks, p.H, g);
   if (ks > 1) {
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
@@ -317,8 +320,8 @@ __device__ __forceinline__ void moe_up_rows(const MoeProblem &p, const Row (&w)[
 }
 
 // FUSED: at most kFusedTokens tokens, each workgroup makes the choice itself.
-template <int W, int AF, bool FUSED>
-__global__ void __launch_bounds__(64 * kUpWaves, W == kMx ? 3 : 4) moe_up_kernel(MoeProblem p, int ks) {
+template <int W, int AF, bool FUSED, bool ODD>
+__global__ void __launch_bounds__(64 * kUpWaves, 3) moe_up_kernel(MoeProblem p, int ks) {
   __shared__ UpPart part[kUpWaves];
   __shared__ Route<FUSED ? kFusedTokens * kMoeMaxTop : 1> route;
   const int wave = wave_id(), l16 = threadIdx.x & 15;
@@ -349,14 +352,9 @@ __global__ void __launch_bounds__(64 * kUpWaves, W == kMx ? 3 : 4) moe_up_kernel
   const long long r0 = 2LL * p.I * e + i, r1 = r0 + p.I;
   Row w[2] = {{p.W1 + r0 * p.ld1, nullptr}, {p.W1 + r1 * p.ld1, nullptr}};
   if constexpr (W == kMx) w[0].q = p.S1 + r0 * p.lds1, w[1].q = p.S1 + r1 * p.lds1;
-  if (n <= 16) {
-    const Row x[1] = {token_row(l16)};
-    moe_up_rows<W, AF, 1>(p, w, x, first, n, i0, ks, any, part);
-  } else {
-    for (int m = 0; m < n; m += 32) {
-      const Row x[2] = {token_row(m + l16), token_row(m + 16 + l16)};
-      moe_up_rows<W, AF, 2>(p, w, x, first + m, n - m, i0, ks, any, part);
-    }
+  for (int m = 0; m < n; m += 16) {
+    const Row x[1] = {token_row(m + l16)};
+    moe_up_rows<W, AF, 1, ODD>(p, w, x, first + m, n - m, i0, ks, any, part);
   }
 }
 
@@ -378,7 +376,7 @@ constexpr DownLds down_lds(int waves, int T, int E, int top) {
   return {gates, start, active, tokens, tokens + 2 * pairs};
 }
 
-template <int W, int WAVES>
+template <int W, int WAVES, bool ODD>
 __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) moe_down_kernel(MoeProblem p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   constexpr int kThreads = 64 * WAVES;
@@ -408,42 +406,29 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) moe_down_kern
   const int pieces = (int)ceil_div(p.I, kPieceK<W>), whole = p.I / kPieceK<W>;
   const long long all = (long long)nact * pieces;
   const int from = (int)(all * wave / WAVES), to = (int)(all * (wave + 1) / WAVES);
-  typedef Thin<W, kSplit, 1, 1> Product;
-  auto load = [&](typename Product::Piece &x, int v) __attribute__((always_inline)) {
-    const int e = __builtin_amdgcn_readfirstlane(active[v / pieces]);
-    const long long r = (long long)p.H * e + col;
-    const Row row{p.W2 + r * p.ld2, W == kMx ? p.S2 + r * p.lds2 : nullptr};
-    const int piece = v % pieces;
-    if constexpr (W == kMx) x = load_mx_piece(row, piece, g, nb);
-    else if (piece < whole) x = load_half_piece(row, piece, g);
-    else x = load_half_guarded(row, piece, g, p.I);
-  };
-  auto use = [&](typename Product::Piece (&x)[1], int v) __attribute__((always_inline)) {
+  typedef Thin<W, kSplit, 1, 1, ODD> Product;
+#pragma unroll 1
+  for (int v = from; v < to; ++v) {
     const int e = __builtin_amdgcn_readfirstlane(active[v / pieces]), piece = v % pieces;
     const int first = __builtin_amdgcn_readfirstlane(start[e]);
     const int last = __builtin_amdgcn_readfirstlane(start[e + 1]);
-    if constexpr (W == kMx)
-      if (piece >= whole) mask_mx_piece(x[0], piece, g, nb);
+    const long long r = (long long)p.H * e + col;
+    const Row w[1] = {{p.W2 + r * p.ld2, W == kMx ? p.S2 + r * p.lds2 : nullptr}};
+    typename Product::Weights x;
+    if (piece < whole) Product::template load_weights<false>(x, w, piece, g, p.I, nb);
+    else Product::template load_weights<true>(x, w, piece, g, p.I, nb);
     for (int m0 = first; m0 < last; m0 += 16) {
-      const int m = m0 + l16 < last ? m0 + l16 : last - 1;
+      const bool valid[1] = {m0 + l16 < last};
+      const int m = valid[0] ? m0 + l16 : first;
       const Row u[1] = {{p.ws + p.at.hi + 2 * m * p.at.pitch, p.ws + p.at.lo + 2 * m * p.at.pitch}};
       Product t;
       t.clear();
-      t.template use<false>(x, u, piece, g, p.I, nb);
-      if (m0 + l16 < last) {
+      t.template use<false>(x, w, u, valid, piece, g, p.I, nb);
+      if (valid[0]) {
         f32x4 *y = reinterpret_cast<f32x4 *>(sum + 16 * token[m] + 4 * g);
         *y += gate[m] * t.acc[0][0];
       }
     }
-  };
-  typename Product::Piece x[1], y[1];  // by turns
-  if (from < to) load(x[0], from);
-  for (int v = from; v < to; v += 2) {
-    load(y[0], v + 1 < to ? v + 1 : v);
-    use(x, v);
-    if (v + 1 >= to) break;
-    load(x[0], v + 2 < to ? v + 2 : v + 1);
-    use(y, v + 1);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 4 * p.T; i += kThreads) {
@@ -464,29 +449,48 @@ hipError_t launch_logits(const MoeProblem &p, hipStream_t s) {
                        s, p);
 }
 
-template <int W, int AF>
+template <int W, int AF, bool ODD>
 hipError_t launch_up(const MoeProblem &p, hipStream_t s) {
   const int pairs = p.T * p.top;
   const long long experts = p.E < pairs ? p.E : pairs, cols = p.at.pitch / 16;
-  // Waves per unit: until 16 waves per compute unit, or a piece for each.
+  // Waves per unit: neighbours read neighbouring pieces of the same rows.
   int ks = 1;
-  while (ks < kUpWaves && cols * experts * ks < 16 * 256 && 2 * ks * kPieceK<W> <= p.H) ks *= 2;
+  while (ks < kUpWaves && 2 * ks * kPieceK<W> <= p.H) ks *= 2;
   const dim3 grid((unsigned)ceil_div(cols * ks, kUpWaves), (unsigned)experts);
-  return launch_kernel(p.T <= kFusedTokens ? moe_up_kernel<W, AF, true> : moe_up_kernel<W, AF, false>,
+  return launch_kernel(p.T <= kFusedTokens ? moe_up_kernel<W, AF, true, ODD>
+                                           : moe_up_kernel<W, AF, false, ODD>,
                        grid, dim3(64 * kUpWaves), s, p, ks);
 }
 
-template <int W, int WAVES>
+template <int W, int WAVES, bool ODD>
 hipError_t launch_down_waves(const MoeProblem &p, hipStream_t s) {
   MoeProblem q = p;
   void *args[] = {&q};
-  return hipLaunchKernel(reinterpret_cast<const void *>(moe_down_kernel<W, WAVES>),
+  return hipLaunchKernel(reinterpret_cast<const void *>(moe_down_kernel<W, WAVES, ODD>),
                          dim3((unsigned)ceil_div(p.H, 16)), dim3(64 * WAVES), args,
                          (size_t)down_lds(WAVES, p.T, p.E, p.top).bytes, s);
 }
-template <int W>
+template <int W, bool ODD>
 hipError_t launch_down(const MoeProblem &p, hipStream_t s) {
-  return p.T <= 64 ? launch_down_waves<W, 16>(p, s) : launch_down_waves<W, 8>(p, s);
+  return p.T <= 64 ? launch_down_waves<W, 16, ODD>(p, s) : launch_down_waves<W, 8, ODD>(p, s);
+}
+
+// Whether a product's 16-bit rows are to be read by whole words (Eight<true>):
+// some start in the middle of one, and both matrices start on one.
+bool odd_rows(const void *a, long long a_pitch, const void *b, long long b_pitch) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 3) == 0 &&
+         ((a_pitch | b_pitch) & 3) != 0;
+}
+
+template <int W, int AF>
+hipError_t launch_products(const MoeProblem &p, hipStream_t s) {
+  constexpr bool kHalf = W != kMx;
+  const hipError_t e = odd_rows(p.X, 2 * p.ldx, kHalf ? p.W1 : nullptr, kHalf ? p.ld1 : 0)
+                           ? launch_up<W, AF, true>(p, s)
+                           : launch_up<W, AF, false>(p, s);
+  if (e != hipSuccess) return e;
+  if (kHalf && odd_rows(p.W2, p.ld2, nullptr, 0)) return launch_down<W, kHalf>(p, s);
+  return launch_down<W, false>(p, s);
 }
 
 }  // namespace
@@ -499,10 +503,8 @@ hipError_t launch_moe(const MoeProblem &p, hipStream_t s) {
     e = launch_kernel(moe_route_kernel, dim3(1), dim3(kRouteThreads), s, p);
     if (e != hipSuccess) return e;
   }
-  e = p.mx ? (bf16 ? launch_up<kMx, kBf16>(p, s) : launch_up<kMx, kF16>(p, s))
-           : (bf16 ? launch_up<kBf16, kBf16>(p, s) : launch_up<kF16, kF16>(p, s));
-  if (e != hipSuccess) return e;
-  return p.mx ? launch_down<kMx>(p, s) : bf16 ? launch_down<kBf16>(p, s) : launch_down<kF16>(p, s);
+  if (p.mx) return bf16 ? launch_products<kMx, kBf16>(p, s) : launch_products<kMx, kF16>(p, s);
+  return bf16 ? launch_products<kBf16, kBf16>(p, s) : launch_products<kF16, kF16>(p, s);
 }
 
 }  // namespace gemm_f32_impl

@@ -45,7 +45,7 @@ struct ThinProblem {
   int c_format;
 };
 
-template <int A, int MB, int NB, int WAVES>
+template <int A, int MB, int NB, int WAVES, bool ODD>
 __global__ void __launch_bounds__(64 * WAVES) mx_thin_kernel(ThinProblem p) {
   __shared__ f32x4 part[WAVES][4][64];
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -57,48 +57,48 @@ __global__ void __launch_bounds__(64 * WAVES) mx_thin_kernel(ThinProblem p) {
     const long long n = n0 + 16 * b + l16 < p.N ? n0 + 16 * b + l16 : p.N - 1;
     w[b] = {p.B.codes + n * p.B.ld, p.B.scales + n * p.B.lds};
   }
-  const int pieces = (int)ceil_div(p.K, kPieceK<kMx>);
   for (long long m0 = 16LL * MB * blockIdx.y; m0 < p.M; m0 += 16LL * MB * gridDim.y) {
     Row a[MB];
+    bool valid[MB];
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      const long long m = m0 + 16 * i + l16 < p.M ? m0 + 16 * i + l16 : p.M - 1;
-      a[i] = {p.A + m * p.lda, A == kMx ? p.SA + m * p.ldsa : nullptr};
+      const long long m = m0 + 16 * i + l16;
+      valid[i] = m < p.M;
+      a[i] = {p.A + (valid[i] ? m : 0) * p.lda, A == kMx ? p.SA + (valid[i] ? m : 0) * p.ldsa : nullptr};
     }
-    Thin<kMx, A, MB, NB> t;
+    Thin<kMx, A, MB, NB, ODD> t;
     t.clear();
-    t.run(a, w, wave, WAVES, pieces, p.K, g);
+    t.run(a, valid, w, wave, WAVES, p.K, g);
     thin_store<WAVES, MB, NB>(t.acc, part, m0, n0, p.M, p.N, p.C, p.ldc, p.c_format);
   }
 }
 
-template <int A, int MB, int NB>
+template <int A, int MB, int NB, bool ODD>
 hipError_t launch_thin_blocks(const ThinProblem &p, hipStream_t s) {
   const long long gy = ceil_div(p.M, 16 * MB);
   const dim3 grid((unsigned)ceil_div(p.N, 16 * NB), (unsigned)(gy < kMaxGridY ? gy : kMaxGridY));
-  constexpr bool kLarge = MB * NB == 16;  // its registers allow one wave per SIMD
-  if (kLarge || p.K <= 4 * kPieceK<kMx>)
-    return launch_kernel(mx_thin_kernel<A, MB, NB, 4>, grid, dim3(256), s, p);
-  return launch_kernel(mx_thin_kernel<A, MB, NB, kLarge ? 4 : 8>, grid, dim3(512), s, p);
+  if (p.K <= 4 * kPieceK<kMx>)
+    return launch_kernel(mx_thin_kernel<A, MB, NB, 4, ODD>, grid, dim3(256), s, p);
+  return launch_kernel(mx_thin_kernel<A, MB, NB, 8, ODD>, grid, dim3(512), s, p);
 }
 
-template <int A>
+template <int A, bool ODD>
 hipError_t launch_thin(const ThinProblem &p, hipStream_t s) {
-  const int mb = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
   // Columns per workgroup: as many as leave a workgroup per compute unit.
   const long long cols = ceil_div(p.N, 16);
   const int nb = cols >= 4 * 256 ? 4 : cols >= 2 * 256 ? 2 : 1;
-  if (mb == 1)
-    return nb == 4   ? launch_thin_blocks<A, 1, 4>(p, s)
-           : nb == 2 ? launch_thin_blocks<A, 1, 2>(p, s)
-                     : launch_thin_blocks<A, 1, 1>(p, s);
-  if (mb == 2)
-    return nb == 4   ? launch_thin_blocks<A, 2, 4>(p, s)
-           : nb == 2 ? launch_thin_blocks<A, 2, 2>(p, s)
-                     : launch_thin_blocks<A, 2, 1>(p, s);
-  return nb == 4   ? launch_thin_blocks<A, 4, 4>(p, s)
-         : nb == 2 ? launch_thin_blocks<A, 4, 2>(p, s)
-                   : launch_thin_blocks<A, 4, 1>(p, s);
+  if (p.M <= 16)
+    return nb == 4   ? launch_thin_blocks<A, 1, 4, ODD>(p, s)
+           : nb == 2 ? launch_thin_blocks<A, 1, 2, ODD>(p, s)
+                     : launch_thin_blocks<A, 1, 1, ODD>(p, s);
+  return nb == 4   ? launch_thin_blocks<A, 2, 4, ODD>(p, s)
+         : nb == 2 ? launch_thin_blocks<A, 2, 2, ODD>(p, s)
+                   : launch_thin_blocks<A, 2, 1, ODD>(p, s);
+}
+
+// Rows that start in the middle of a word, of a matrix that starts on one.
+bool odd_rows(const void *base, long long pitch_bytes) {
+  return (reinterpret_cast<uintptr_t>(base) & 3) == 0 && (pitch_bytes & 3) != 0;
 }
 
 }  // namespace
@@ -106,13 +106,15 @@ hipError_t launch_thin(const ThinProblem &p, hipStream_t s) {
 hipError_t launch_mx_a16(const MxA16Problem &p, hipStream_t s) {
   const ThinProblem t{p.M, p.N, p.K, reinterpret_cast<const unsigned char *>(p.A), 2 * p.lda,
                       nullptr, 0, p.B, p.C, p.ldc, p.c_format};
-  return p.a_format == kBf16 ? launch_thin<kBf16>(t, s) : launch_thin<kF16>(t, s);
+  if (odd_rows(p.A, 2 * p.lda) && p.M > 1)
+    return p.a_format == kBf16 ? launch_thin<kBf16, true>(t, s) : launch_thin<kF16, true>(t, s);
+  return p.a_format == kBf16 ? launch_thin<kBf16, false>(t, s) : launch_thin<kF16, false>(t, s);
 }
 
 hipError_t launch_mx_thin(const MxProblem &p, hipStream_t s) {
   const ThinProblem t{p.M, p.N, p.K, p.A.codes, p.A.ld, p.A.scales, p.A.lds, p.B, p.C, p.ldc,
                       p.c_format};
-  return launch_thin<kMx>(t, s);
+  return launch_thin<kMx, false>(t, s);
 }
 
 }  // namespace gemm_f32_impl

@@ -36,7 +36,7 @@ const MxEntry kMxEntries[] = {
     {64, 64, 128, 256},    // operands straight from memory, any size
     {256, 256, 256, 256},  // direct-load tiles, 128 x 128 per wave
     {128, 128, 256, 256},  // direct-load tiles, 64 x 64 per wave
-    {64, 16, 512, 512},    // few rows: K shared by the waves, B read once
+    {32, 16, 256, 512},    // few rows: K shared by the waves, B read once
 };
 
 }  // namespace
@@ -45,7 +45,7 @@ int mx_num_entries() { return (int)(sizeof(kMxEntries) / sizeof(kMxEntries[0]));
 const MxEntry &mx_entry(int index) { return kMxEntries[index]; }
 int mx_choose(int M, int N, int) {
   if (M >= 256 && N >= 256 && ceil_div(M, 256) * ceil_div(N, 256) >= 192) return 1;
-  return M <= 64 ? 3 : M >= 128 && N >= 128 ? 2 : 0;
+  return M <= 32 ? 3 : M >= 128 && N >= 128 ? 2 : 0;
 }
 
 int moe_check_sizes(int T, int E, int top, int H, int I) {

@@ -1,20 +1,22 @@
 // Pieces of the thin products (few rows of gemm_mx, gemm_mx_a16, the
-// mixture-of-experts layer): up to 64 rows of activations against weights
+// mixture-of-experts layer): up to 32 rows of activations against weights
 // read once from memory, which is what bounds them.
 //
 // A wave multiplies blocks of 16 activation rows with blocks of 16 weight
-// rows ("columns" of C) and takes K in pieces of four 16-byte loads per
-// weight row: 512 k of MX weights, 128 k of 16-bit ones.  A piece's weights
-// are loaded whole before any is used and the next piece's while it is used,
-// so a wave keeps 4 KB or more per 16 weight rows in flight.
+// rows ("columns" of C) and takes K in pieces of four 128-deep steps (MX
+// weights) or one (16-bit ones).  A piece's weights are loaded at once, the
+// activations step by step, a step ahead of their use.  Rows past the last
+// are not loaded: with the usual few rows most lanes are spared the L1
+// traffic, of which 16-bit activations need four times what MX weights do.
 //
 // Lane l holds row l % 16 of each operand; which k a lane holds is free as
 // long as both operands agree, so it follows how the weights are stored, with
 // g = l / 16:
-//   MX weights: load s of a piece is block 4 s + g of the row; MFMA j of the
-//     128-deep step s takes its values 8 j .. 8 j + 7, widened with their
-//     scale (exact: an element has two significant bits);
-//   16-bit weights: load j is k = 32 j + 8 g .. + 7, the operand of MFMA j.
+//   MX weights: load s of a piece is block 4 s + g of it; MFMA j of step s
+//     takes its values 8 j .. 8 j + 7, widened with their scale (exact: an
+//     element has two significant bits);
+//   16-bit weights: load j of a step is k = 32 j + 8 g .. + 7, the operand of
+//     MFMA j.
 #pragma once
 
 #include "mx_values.hpp"
@@ -75,25 +77,63 @@ __device__ inline u32x4 load_guarded(const unsigned char *row, long long k, long
   return w;
 }
 
+// 8 values of a row of 16-bit codes.  ODD: rows that may start in the middle
+// of a 4-byte word, where a 16-byte load costs a multiple of an aligned one:
+// the words around them are loaded, from 2 bytes before the first value on
+// (the row before, or its padding: only rows after the first can be odd,
+// because the matrix starts on a word), with the last value on its own.
+template <bool ODD>
+struct Eight {
+  u32x4 v;
+  __device__ __forceinline__ void load(const unsigned char *at) {
+    v = *reinterpret_cast<const u32x4h *>(at);
+  }
+  __device__ __forceinline__ u32x4 get(const unsigned char *) const { return v; }
+  __device__ __forceinline__ void set(u32x4 x, const unsigned char *) { v = x; }
+};
+template <>
+struct Eight<true> {
+  u32x4 v;
+  uint32_t last;
+  static __device__ __forceinline__ uint32_t shift(const unsigned char *at) {
+    return ((uint32_t)(uintptr_t)at & 2u) * 8u;
+  }
+  __device__ __forceinline__ void load(const unsigned char *at) {
+    const uintptr_t odd = reinterpret_cast<uintptr_t>(at) & 2;
+    v = *reinterpret_cast<const u32x4w *>(at - odd);
+    last = *reinterpret_cast<const uint16_t *>(at + 14);
+  }
+  __device__ __forceinline__ void set(u32x4 x, const unsigned char *at) {
+    const bool odd = shift(at) != 0;
+    v = odd ? u32x4{x[0] << 16, x[0] >> 16 | x[1] << 16, x[1] >> 16 | x[2] << 16,
+                    x[2] >> 16 | x[3] << 16}
+            : x;
+    last = x[3] >> 16;
+  }
+  // `at`: any address of the row, for its alignment.
+  __device__ __forceinline__ u32x4 get(const unsigned char *at) const {
+    const uint32_t s = shift(at);
+    return u32x4{__builtin_amdgcn_alignbit(v[1], v[0], s), __builtin_amdgcn_alignbit(v[2], v[1], s),
+                 __builtin_amdgcn_alignbit(v[3], v[2], s), __builtin_amdgcn_alignbit(last, v[3], s)};
+  }
+};
+
 // A piece of an MX row as it is stored: blocks 16 piece + 4 s + g and the 16
-// scales.  Blocks past the row's are read from its last and made zeros with
-// scale 1.
+// scales.  Blocks past the row's are read from its last; mask_mx_piece makes
+// them zeros with scale 1.
 struct MxPiece {
   u32x4 c[4];
   u32x4 s;
 };
-__device__ inline MxPiece load_mx_piece(const Row &r, int piece, int g, int nb) {
-  MxPiece x;
-  const int kb0 = 16 * piece + g;
+__device__ __forceinline__ void load_mx_piece(MxPiece &x, const Row &r, int piece, int g, int nb) {
   x.s = *reinterpret_cast<const u32x4 *>(r.q + 16LL * piece);
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const int kb = kb0 + 4 * s < nb ? kb0 + 4 * s : nb - 1;
+    const int kb = 16 * piece + 4 * s + g < nb ? 16 * piece + 4 * s + g : nb - 1;
     x.c[s] = *reinterpret_cast<const u32x4 *>(r.p + 16LL * kb);
   }
-  return x;
 }
-__device__ inline void mask_mx_piece(MxPiece &x, int piece, int g, int nb) {
+__device__ __forceinline__ void mask_mx_piece(MxPiece &x, int piece, int g, int nb) {
 #pragma unroll
   for (int s = 0; s < 4; ++s)
     if (16 * piece + 4 * s + g >= nb) {
@@ -137,7 +177,7 @@ __device__ inline u32x4 widen(uint32_t codes, uint32_t sb) {
                  pack2<kBf16>(v[6], v[7])};
   }
 }
-// Whether all of a lane's four blocks allow it (blocks of zeros allow any).
+// Whether all of a lane's blocks allow it (blocks of zeros allow any).
 template <uint32_t LOW, uint32_t HIGH>
 __device__ inline bool scales_within(const MxPiece &x, int g) {
   bool ok = true;
@@ -150,52 +190,31 @@ __device__ inline bool scales_within(const MxPiece &x, int g) {
   return ok;
 }
 
-// A piece of 16-bit weights: operands of MFMA 0 .. 3.
-struct HalfPiece {
-  u32x4 c[4];
-};
-__device__ inline HalfPiece load_half_piece(const Row &r, int piece, int g) {
-  HalfPiece x;
-  const uint16_t *p = reinterpret_cast<const uint16_t *>(r.p) + 128LL * piece + 8 * g;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x.c[j] = *reinterpret_cast<const u32x4h *>(p + 32 * j);
-  return x;
-}
-__device__ inline HalfPiece load_half_guarded(const Row &r, int piece, int g, int K) {
-  HalfPiece x;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const long long k = 128LL * piece + 32 * j + 8 * g;
-    x.c[j] = load_guarded(r.p, k, K - k);
-  }
-  return x;
-}
-
-template <int W>
-struct PieceOf {
-  typedef HalfPiece type;
-};
-template <>
-struct PieceOf<kMx> {
-  typedef MxPiece type;
-};
+// The wave's number in its workgroup, as a scalar.
+__device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // First k (from the piece's first) of lane group g's operand of MFMA j of
 // step s.
 template <int W>
 __device__ inline int piece_k(int g, int s, int j) {
-  return W == kMx ? 128 * s + 32 * g + 8 * j : 32 * j + 8 * g;
+  return 128 * s + (W == kMx ? 32 * g + 8 * j : 32 * j + 8 * g);
 }
 
-// The wave's number in its workgroup, as a scalar.
-__device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
-
 // One product of thin operands: MB blocks of 16 rows of kind A by NB blocks
-// of 16 rows of weights of kind W.  `mine` says which pieces this wave takes:
-// first, first + step, ... below `pieces`.
-template <int W, int A, int MB, int NB>
+// of 16 rows of weights of kind W.
+template <int W, int A, int MB, int NB, bool ODD = false>
 struct Thin {
-  typedef typename PieceOf<W>::type Piece;
+  static constexpr int kK = kPieceK<W>, kSteps = kPieceSteps<W>;
+  struct Weights {
+    MxPiece mx[W == kMx ? NB : 1];
+    Eight<ODD> half[W == kMx ? 1 : NB][4];
+  };
+  // Activations of one step (16-bit or split), or of a piece (MX).
+  struct Acts {
+    MxPiece mx[A == kMx ? MB : 1];
+    Eight<ODD && A != kSplit> v[A == kMx ? 1 : MB][4];
+    Eight<false> lo[A == kSplit ? MB : 1][4];
+  };
   f32x4 acc[MB][NB];
 
   __device__ __forceinline__ void clear() {
@@ -205,140 +224,146 @@ struct Thin {
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  static __device__ __forceinline__ void load(Piece (&x)[NB], const Row (&w)[NB], int piece, int g,
-                                              int K, int nb) {
+  // A piece's weights; with TAIL it reaches past K: zeros there.
+  template <bool TAIL>
+  static __device__ __forceinline__ void load_weights(Weights &x, const Row (&w)[NB], int piece,
+                                                      int g, int K, int nb) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      if constexpr (W == kMx) x[b] = load_mx_piece(w[b], piece, g, nb);
-      else x[b] = load_half_piece(w[b], piece, g);
+      if constexpr (W == kMx) {
+        load_mx_piece(x.mx[b], w[b], piece, g, nb);
+        if constexpr (TAIL) mask_mx_piece(x.mx[b], piece, g, nb);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const long long k = (long long)kK * piece + piece_k<W>(g, 0, j);
+          if constexpr (TAIL) x.half[b][j].set(load_guarded(w[b].p, k, K - k), w[b].p);
+          else x.half[b][j].load(w[b].p + 2 * k);
+        }
+      }
     }
   }
-
-  // The products of one piece.  With GUARD it may reach past K.
-  template <bool GUARD>
-  __device__ __forceinline__ void use(Piece (&x)[NB], const Row (&a)[MB], int piece, int g, int K,
-                                      int nb) {
-    if constexpr (W == kMx && GUARD) {
+  // Step s of a piece's activations.  Rows that `valid` leaves out are not
+  // loaded: their results are not used.  Split ones are padded with zeros to
+  // whole pieces.
+  template <bool TAIL>
+  static __device__ __forceinline__ void load_acts(Acts &y, const Row (&a)[MB],
+                                                   const bool (&valid)[MB], int piece, int s,
+                                                   int g, int K, int nb) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) mask_mx_piece(x[b], piece, g, nb);
-    }
-    if constexpr (A == kMx) {
-      MxPiece y[MB];
+    for (int i = 0; i < MB; ++i)
+      if (valid[i]) {
+        if constexpr (A == kMx) {
+          load_mx_piece(y.mx[i], a[i], piece, g, nb);
+          if constexpr (TAIL) mask_mx_piece(y.mx[i], piece, g, nb);
+        } else {
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        y[i] = load_mx_piece(a[i], piece, g, nb);
-        if constexpr (GUARD) mask_mx_piece(y[i], piece, g, nb);
+          for (int j = 0; j < 4; ++j) {
+            const long long k = (long long)kK * piece + piece_k<W>(g, s, j);
+            if constexpr (A == kSplit) {
+              y.v[i][j].load(a[i].p + 2 * k);
+              y.lo[i][j].load(a[i].q + 2 * k);
+            } else if constexpr (TAIL) {
+              y.v[i][j].set(load_guarded(a[i].p, k, K - k), a[i].p);
+            } else {
+              y.v[i][j].load(a[i].p + 2 * k);
+            }
+          }
+        }
       }
+  }
+
+  // The products of a piece whose weights are loaded.
+  template <bool TAIL>
+  __device__ __forceinline__ void use(const Weights &x, const Row (&w)[NB], const Row (&a)[MB],
+                                      const bool (&valid)[MB], int piece, int g, int K, int nb) {
+    if constexpr (A == kMx) {
+      Acts y;
+      load_acts<TAIL>(y, a, valid, piece, 0, g, K, nb);
 #pragma unroll
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            acc[i][b] = mfma_mx(x[b].c[s], (int)piece_scale(x[b], s, g), y[i].c[s],
-                                (int)piece_scale(y[i], s, g), acc[i][b]);
-    } else if constexpr (W == kMx) {
-      bool wide = true, half = A == kF16;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        wide &= scales_within<1, 254>(x[b], g);
-        if constexpr (A == kF16) half &= scales_within<104, 140>(x[b], g);
-      }
-      if (A == kF16 && __all(half)) multiply<GUARD, kToF16>(x, a, piece, g, K);
-      else if (A != kF16 && __all(wide)) multiply<GUARD, kToBf16>(x, a, piece, g, K);
-      else multiply<GUARD, kThroughF32>(x, a, piece, g, K);
+            acc[i][b] = mfma_mx(x.mx[b].c[s], (int)piece_scale(x.mx[b], s, g), y.mx[i].c[s],
+                                (int)piece_scale(y.mx[i], s, g), acc[i][b]);
     } else {
-      multiply<GUARD, W == kF16 ? kToF16 : kToBf16>(x, a, piece, g, K);
+      Acts y[2];
+      load_acts<TAIL>(y[0], a, valid, piece, 0, g, K, nb);
+      bool ok = true;
+      if constexpr (W == kMx) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          ok &= A == kF16 ? scales_within<104, 140>(x.mx[b], g) : scales_within<1, 254>(x.mx[b], g);
+        ok = __all(ok);
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        if (s + 1 < kSteps) load_acts<TAIL>(y[(s + 1) & 1], a, valid, piece, s + 1, g, K, nb);
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr Widen kHow = W == kF16 || (W == kMx && A == kF16) ? kToF16 : kToBf16;
+        if (W != kMx || ok) multiply<kHow>(x, y[s & 1], w, a, s, g);
+        else multiply<kThroughF32>(x, y[s & 1], w, a, s, g);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
 
-  // HOW: the format the weights come in or are brought to.
-  template <bool GUARD, Widen HOW>
-  __device__ __forceinline__ void multiply(const Piece (&x)[NB], const Row (&a)[MB], int piece,
-                                           int g, int K) {
+  // One step's products.  HOW: the format the weights come in or are brought to.
+  template <Widen HOW>
+  __device__ __forceinline__ void multiply(const Weights &x, const Acts &y, const Row (&w)[NB],
+                                           const Row (&a)[MB], int s, int g) {
 #pragma unroll
-    for (int s = 0; s < kPieceSteps<W>; ++s) {
+    for (int j = 0; j < 4; ++j) {
+      u32x4 wv[NB];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u32x4 w[NB];
+      for (int b = 0; b < NB; ++b) {
+        if constexpr (W == kMx) wv[b] = widen<HOW>(x.mx[b].c[s][j], piece_scale(x.mx[b], s, g));
+        else wv[b] = x.half[b][j].get(w[b].p);
+      }
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        u32x4 v = y.v[i][j].get(a[i].p), lo{};
+        if constexpr (A == kSplit) lo = y.lo[i][j].get(a[i].q);
+        constexpr bool kSplitHere = A == kF16 && HOW != kToF16;
+        if constexpr (kSplitHere) split_f16(v, v, lo);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          if constexpr (W == kMx) w[b] = widen<HOW>(x[b].c[s][j], piece_scale(x[b], s, g));
-          else w[b] = x[b].c[j];
-        }
-        const long long k = (long long)kPieceK<W> * piece + piece_k<W>(g, s, j);
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          u32x4 v, lo;
-          if constexpr (A == kSplit) {  // rows padded with zeros to whole 512 k
-            v = *reinterpret_cast<const u32x4 *>(a[i].p + 2 * k);
-            lo = *reinterpret_cast<const u32x4 *>(a[i].q + 2 * k);
+          if constexpr (A == kSplit && HOW == kToF16) {
+            // fp16 weights are split too; the product of the two low parts,
+            // 2^-18 of the whole, is left out
+            u32x4 wh, wl;
+            split_f16(wv[b], wh, wl);
+            acc[i][b] = mfma_bf16(wh, v, acc[i][b]);
+            acc[i][b] = mfma_bf16(wh, lo, acc[i][b]);
+            acc[i][b] = mfma_bf16(wl, v, acc[i][b]);
+          } else if constexpr (HOW == kToF16) {
+            acc[i][b] = mfma_f16(wv[b], v, acc[i][b]);
           } else {
-            if constexpr (GUARD) v = load_guarded(a[i].p, k, K - k);
-            else v = *reinterpret_cast<const u32x4h *>(a[i].p + 2 * k);
-            if constexpr (A == kF16 && HOW != kToF16) split_f16(v, v, lo);
-          }
-          constexpr bool kTwo = A == kSplit || (A == kF16 && HOW != kToF16);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            if constexpr (kTwo && HOW == kToF16) {
-              // fp16 weights are split too; the product of the two low
-              // parts, 2^-18 of the whole, is left out
-              u32x4 wh, wl;
-              split_f16(w[b], wh, wl);
-              acc[i][b] = mfma_bf16(wh, v, acc[i][b]);
-              acc[i][b] = mfma_bf16(wh, lo, acc[i][b]);
-              acc[i][b] = mfma_bf16(wl, v, acc[i][b]);
-            } else if constexpr (HOW == kToF16) {
-              acc[i][b] = mfma_f16(w[b], v, acc[i][b]);
-            } else {
-              acc[i][b] = mfma_bf16(w[b], v, acc[i][b]);
-              if constexpr (kTwo) acc[i][b] = mfma_bf16(w[b], lo, acc[i][b]);
-            }
+            acc[i][b] = mfma_bf16(wv[b], v, acc[i][b]);
+            if constexpr (A == kSplit || kSplitHere) acc[i][b] = mfma_bf16(wv[b], lo, acc[i][b]);
           }
         }
       }
-      // One step's activations at a time: hoisted all together their
-      // registers would cost the waves that hide their latency.
-      if constexpr (kPieceSteps<W> > 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-  // Adds this wave's pieces first, first + step, ... below `end` of the K
-  // values of rows `a` and `w`.
-  __device__ __forceinline__ void run(const Row (&a)[MB], const Row (&w)[NB], int first, int step,
-                                      int end, int K, int g) {
-    const int nb = (int)mx_blocks(K), whole = K / kPieceK<W>;
-    const int last = end < whole ? end : whole;  // whole pieces below `end`
+  // Adds the products of pieces first, first + step, ... of the K values.
+  __device__ __forceinline__ void run(const Row (&a)[MB], const bool (&valid)[MB],
+                                      const Row (&w)[NB], int first, int step, int K, int g) {
+    const int nb = (int)mx_blocks(K), last = K / kK;  // whole pieces
     int p = first;
-    Piece x[NB];
-    if (p < last) load(x, w, p, g, K, nb);
-    if constexpr (W == kMx && NB > 1) {  // 8 KB or more in flight; registers for waves instead
-      for (; p < last; p += step) {
-        use<false>(x, a, p, g, K, nb);
-        load(x, w, p + step < last ? p + step : p, g, K, nb);
-      }
-    } else {
-      // Two pieces by turns: handing the loaded one on in registers would
-      // wait for it.
-      Piece y[NB];
-      while (p < last) {
-        load(y, w, p + step < last ? p + step : p, g, K, nb);
-        use<false>(x, a, p, g, K, nb);
-        p += step;
-        if (p >= last) break;
-        load(x, w, p + step < last ? p + step : p, g, K, nb);
-        use<false>(y, a, p, g, K, nb);
-        p += step;
-      }
+#pragma unroll 1
+    for (; p < last; p += step) {
+      Weights x;
+      load_weights<false>(x, w, p, g, K, nb);
+      use<false>(x, w, a, valid, p, g, K, nb);
     }
-    if (p < end) {  // the piece that reaches past K
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if constexpr (W == kMx) x[b] = load_mx_piece(w[b], p, g, nb);
-        else x[b] = load_half_guarded(w[b], p, g, K);
-      }
-      use<true>(x, a, p, g, K, nb);
+    if (p == last && (long long)last * kK < K) {
+      Weights x;
+      load_weights<true>(x, w, p, g, K, nb);
+      use<true>(x, w, a, valid, p, g, K, nb);
     }
   }
 };

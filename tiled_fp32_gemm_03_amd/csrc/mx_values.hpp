@@ -25,6 +25,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4h __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4w __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32h __attribute__((aligned(2)));
 typedef f32x2 f32x2u __attribute__((aligned(4)));
 
