@@ -113,6 +113,7 @@ struct Route {
   unsigned short list[MAX_PAIRS];      // pairs by expert
   unsigned short count[(MAX_PAIRS + 63) / 64][kMoeMaxExperts];
   unsigned short start[kMoeMaxExperts + 1];
+  unsigned short ufirst[kMoeMaxExperts];
   unsigned short active[kMoeMaxExperts];
   int nactive;
 };
@@ -198,22 +199,27 @@ __device__ inline void route_all(const MoeProblem &p, Route<MAX_PAIRS> &r) {
   }
   __syncthreads();
   if (wave == 0) {  // where each expert's pairs begin, and the chosen experts
-    int base = 0, nact = 0;
+    int base = 0, ubase = 0, nact = 0;
     for (int e0 = 0; e0 < p.E; e0 += 64) {
       const int e = e0 + lane;
       int n = 0;
       if (e < p.E)
         for (int c = 0; c < chunks; ++c) n += r.count[c][e];
-      int upto = n;
+      const int u = (n + 3) & ~3;  // rows of u
+      int upto = n, uupto = u;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(upto, d);
-        if (lane >= d) upto += v;
+        const int v = __shfl_up(upto, d), uv = __shfl_up(uupto, d);
+        if (lane >= d) upto += v, uupto += uv;
       }
-      if (e < p.E) r.start[e] = (unsigned short)(base + upto - n);
+      if (e < p.E) {
+        r.start[e] = (unsigned short)(base + upto - n);
+        r.ufirst[e] = (unsigned short)(ubase + uupto - u);
+      }
       const unsigned long long on = __ballot(n > 0);
       if (n > 0) r.active[nact + __popcll(on & before)] = (unsigned short)e;
       base += __shfl(upto, 63);
+      ubase += __shfl(uupto, 63);
       nact += __popcll(on);
     }
     if (lane == 0) {
@@ -240,7 +246,7 @@ template <int THREADS, int MAX_PAIRS>
 __device__ inline void write_route(const MoeProblem &p, const Route<MAX_PAIRS> &r) {
   const int pairs = p.T * p.top;
   int *list = ws_at<int>(p, p.at.list), *start = ws_at<int>(p, p.at.start);
-  int *active = ws_at<int>(p, p.at.active);
+  int *active = ws_at<int>(p, p.at.active), *ufirst = ws_at<int>(p, p.at.ufirst);
   float *gates = ws_at<float>(p, p.at.gates);
   for (int i = threadIdx.x; i < pairs; i += THREADS) {
     list[i] = r.list[i];
@@ -249,6 +255,7 @@ __device__ inline void write_route(const MoeProblem &p, const Route<MAX_PAIRS> &
     if (p.gates) p.gates[i] = r.gate[i];
   }
   for (int e = threadIdx.x; e <= p.E; e += THREADS) start[e] = r.start[e];
+  for (int e = threadIdx.x; e < p.E; e += THREADS) ufirst[e] = r.ufirst[e];
   for (int a = threadIdx.x; a < r.nactive; a += THREADS) active[1 + a] = r.active[a];
   if (threadIdx.x == 0) active[0] = r.nactive;
 }
@@ -269,8 +276,8 @@ constexpr int kUpWaves = 4;
 typedef f32x4 UpPart[1][2][64];  // [block of rows][factor][lane]
 
 template <int W, int AF, int MB, bool ODD>
-__device__ __forceinline__ void moe_up_rows(const MoeProblem &p, const Row (&w)[2],
-                                            const Row (&x)[MB], int first, int n, int i0, int ks,
+__device__ __forceinline__ void moe_up_rows(const MoeProblem &p, const Rows (&w)[2],
+                                            const Row (&x)[MB], int ufirst, int n, int i0, int ks,
                                             bool any, UpPart *part) {
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int l16 = lane & 15, g = lane >> 4, kw = wave & (ks - 1);
@@ -279,7 +286,7 @@ __device__ __forceinline__ void moe_up_rows(const MoeProblem &p, const Row (&w)[
   for (int i = 0; i < MB; ++i) valid[i] = 16 * i + l16 < n;
   Thin<W, AF, MB, 2, ODD> t;
   t.clear();
-  if (any) t.run(x, valid, w, kw, ks, p.H, g);
+  if (any) t.run(x, valid, w, kw, ks, p.H, lane);
   if (ks > 1) {
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
@@ -311,10 +318,10 @@ __device__ __forceinline__ void moe_up_rows(const MoeProblem &p, const Row (&w)[
       const float h = to_f32<kBf16>(hi[j]);
       lo[j] = mag_bits(h) < 0x7f800000u ? from_f32<kBf16>(v - h) : (uint16_t)0;
     }
-    const long long at = (first + m) * p.at.pitch + i0 + 4 * g;
-    *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.hi) + at) =
+    const long long at = split_at<W>(ufirst + m, i0 + 4 * g, p.at.pitch);
+    *reinterpret_cast<u32x2 *>(p.ws + p.at.hi + at) =
         u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
-    *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.lo) + at) =
+    *reinterpret_cast<u32x2 *>(p.ws + p.at.lo + at) =
         u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
   }
 }
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(64 * kUpWaves, 3) moe_up_kernel(MoeProblem p, 
   __shared__ UpPart part[kUpWaves];
   __shared__ Route<FUSED ? kFusedTokens * kMoeMaxTop : 1> route;
   const int wave = wave_id(), l16 = threadIdx.x & 15;
-  int e, first, n;
+  int e, first, n, ufirst;
   if constexpr (FUSED) {
     route_all<64 * kUpWaves>(p, route);
     if (blockIdx.x == 0 && blockIdx.y == 0) write_route<64 * kUpWaves>(p, route);
@@ -333,28 +340,36 @@ __global__ void __launch_bounds__(64 * kUpWaves, 3) moe_up_kernel(MoeProblem p, 
     e = __builtin_amdgcn_readfirstlane(route.active[blockIdx.y]);
     first = __builtin_amdgcn_readfirstlane(route.start[e]);
     n = __builtin_amdgcn_readfirstlane(route.start[e + 1]) - first;
+    ufirst = __builtin_amdgcn_readfirstlane(route.ufirst[e]);
   } else {
     const int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
     if ((int)blockIdx.y >= active[0]) return;
     e = active[1 + blockIdx.y];
     first = start[e];
     n = start[e + 1] - first;
+    ufirst = ws_at<int>(p, p.at.ufirst)[e];
   }
-  auto token_row = [&](int m) __attribute__((always_inline)) {
-    const int at = first + (m < n ? m : n - 1);
-    const int pair = FUSED ? (int)route.list[at] : ws_at<int>(p, p.at.list)[at];
-    return Row{reinterpret_cast<const unsigned char *>(p.X + pair / p.top * p.ldx), nullptr};
-  };
+  const int lane = threadIdx.x & 63;
   const int units = kUpWaves / ks;
   const int i0 = 16 * (int)(blockIdx.x * units + wave / ks);
   const bool any = i0 < p.at.pitch;  // the last workgroup may have units too many
-  const int i = i0 + l16 < p.I ? i0 + l16 : p.I - 1;
-  const long long r0 = 2LL * p.I * e + i, r1 = r0 + p.I;
-  Row w[2] = {{p.W1 + r0 * p.ld1, nullptr}, {p.W1 + r1 * p.ld1, nullptr}};
-  if constexpr (W == kMx) w[0].q = p.S1 + r0 * p.lds1, w[1].q = p.S1 + r1 * p.lds1;
+  auto inner = [&](int r) { return 2LL * p.I * e + (i0 + r < p.I ? i0 + r : p.I - 1); };
+  Rows w[2];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const long long r = inner(load_row(lane, t));
+    w[0].p[t] = p.W1 + r * p.ld1;
+    w[1].p[t] = p.W1 + (r + p.I) * p.ld1;
+  }
+  if constexpr (W == kMx) {
+    w[0].q = p.S1 + inner(l16) * p.lds1;
+    w[1].q = p.S1 + (inner(l16) + p.I) * p.lds1;
+  }
   for (int m = 0; m < n; m += 16) {
-    const Row x[1] = {token_row(m + l16)};
-    moe_up_rows<W, AF, 1, ODD>(p, w, x, first + m, n - m, i0, ks, any, part);
+    const int at = first + (m + l16 < n ? m + l16 : n - 1);
+    const int pair = FUSED ? (int)route.list[at] : ws_at<int>(p, p.at.list)[at];
+    const Row x[1] = {{reinterpret_cast<const unsigned char *>(p.X + pair / p.top * p.ldx), nullptr}};
+    moe_up_rows<W, AF, 1, ODD>(p, w, x, ufirst + m, n - m, i0, ks, any, part);
   }
 }
 
@@ -367,13 +382,13 @@ __global__ void __launch_bounds__(64 * kUpWaves, 3) moe_up_kernel(MoeProblem p, 
 
 // LDS of the second product: sums [wave][token][16], then the route.
 struct DownLds {
-  int gates, start, active, tokens, bytes;
+  int gates, start, ufirst, active, tokens, bytes;
 };
 constexpr DownLds down_lds(int waves, int T, int E, int top) {
   const int pairs = T * top;
-  const int gates = waves * T * 64, start = gates + 4 * pairs, active = start + 2 * (E + 1),
-            tokens = active + 2 * E;
-  return {gates, start, active, tokens, tokens + 2 * pairs};
+  const int gates = waves * T * 64, start = gates + 4 * pairs, ufirst = start + 2 * (E + 1),
+            active = ufirst + 2 * E, tokens = active + 2 * E;
+  return {gates, start, ufirst, active, tokens, tokens + 2 * pairs};
 }
 
 template <int W, int WAVES, bool ODD>
@@ -383,6 +398,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) moe_down_kern
   const DownLds at = down_lds(WAVES, p.T, p.E, p.top);
   float *gate = reinterpret_cast<float *>(lds + at.gates);  // by place in the list
   unsigned short *start = reinterpret_cast<unsigned short *>(lds + at.start);
+  unsigned short *ufirst = reinterpret_cast<unsigned short *>(lds + at.ufirst);
   unsigned short *active = reinterpret_cast<unsigned short *>(lds + at.active);
   unsigned short *token = reinterpret_cast<unsigned short *>(lds + at.tokens);  // by place
   const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
@@ -396,13 +412,14 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) moe_down_kern
   }
   for (int i = threadIdx.x; i <= p.E; i += kThreads)
     start[i] = (unsigned short)ws_at<int>(p, p.at.start)[i];
+  for (int i = threadIdx.x; i < p.E; i += kThreads)
+    ufirst[i] = (unsigned short)ws_at<int>(p, p.at.ufirst)[i];
   for (int i = threadIdx.x; i < nact; i += kThreads)
     active[i] = (unsigned short)ws_at<int>(p, p.at.active)[1 + i];
   __syncthreads();
 
   float *sum = reinterpret_cast<float *>(lds) + wave * 16 * p.T;
   const int n0 = 16 * blockIdx.x, nb = (int)mx_blocks(p.I);
-  const int col = n0 + l16 < p.H ? n0 + l16 : p.H - 1;
   const int pieces = (int)ceil_div(p.I, kPieceK<W>), whole = p.I / kPieceK<W>;
   const long long all = (long long)nact * pieces;
   const int from = (int)(all * wave / WAVES), to = (int)(all * (wave + 1) / WAVES);
@@ -412,18 +429,28 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) moe_down_kern
     const int e = __builtin_amdgcn_readfirstlane(active[v / pieces]), piece = v % pieces;
     const int first = __builtin_amdgcn_readfirstlane(start[e]);
     const int last = __builtin_amdgcn_readfirstlane(start[e + 1]);
-    const long long r = (long long)p.H * e + col;
-    const Row w[1] = {{p.W2 + r * p.ld2, W == kMx ? p.S2 + r * p.lds2 : nullptr}};
+    auto row = [&](int r) { return (long long)p.H * e + (n0 + r < p.H ? n0 + r : p.H - 1); };
+    Rows w[1];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) w[0].p[t] = p.W2 + row(load_row(lane, t)) * p.ld2;
+    if constexpr (W == kMx) w[0].q = p.S2 + row(l16) * p.lds2;
     typename Product::Weights x;
-    if (piece < whole) Product::template load_weights<false>(x, w, piece, g, p.I, nb);
-    else Product::template load_weights<true>(x, w, piece, g, p.I, nb);
+    if (piece < whole) {
+      Product::template load_weights<false>(x, w, piece, lane, p.I, nb);
+      Product::template turn_weights<false>(x, w, piece, lane, nb);
+    } else {
+      Product::template load_weights<true>(x, w, piece, lane, p.I, nb);
+      Product::template turn_weights<true>(x, w, piece, lane, nb);
+    }
+    const int u0 = __builtin_amdgcn_readfirstlane(ufirst[e]);
     for (int m0 = first; m0 < last; m0 += 16) {
-      const bool valid[1] = {m0 + l16 < last};
-      const int m = valid[0] ? m0 + l16 : first;
-      const Row u[1] = {{p.ws + p.at.hi + 2 * m * p.at.pitch, p.ws + p.at.lo + 2 * m * p.at.pitch}};
+      const int m = m0 + l16;
+      const bool valid[1] = {m < last};
+      const long long at_u = split_at<W>(u0 + m - first, 0, p.at.pitch) + 64 * g;
+      const Row u[1] = {{p.ws + p.at.hi + at_u, p.ws + p.at.lo + at_u}};
       Product t;
       t.clear();
-      t.template use<false>(x, w, u, valid, piece, g, p.I, nb);
+      t.template use<false>(x, u, valid, piece, lane, p.I, nb);
       if (valid[0]) {
         f32x4 *y = reinterpret_cast<f32x4 *>(sum + 16 * token[m] + 4 * g);
         *y += gate[m] * t.acc[0][0];

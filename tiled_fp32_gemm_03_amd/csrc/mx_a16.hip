@@ -49,26 +49,35 @@ template <int A, int MB, int NB, int WAVES, bool ODD>
 __global__ void __launch_bounds__(64 * WAVES) mx_thin_kernel(ThinProblem p) {
   __shared__ f32x4 part[WAVES][4][64];
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const int l16 = lane & 15, g = lane >> 4;
+  const int l16 = lane & 15;
   const long long n0 = 16LL * NB * blockIdx.x;
-  Row w[NB];
+  Rows w[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    const long long n = n0 + 16 * b + l16 < p.N ? n0 + 16 * b + l16 : p.N - 1;
-    w[b] = {p.B.codes + n * p.B.ld, p.B.scales + n * p.B.lds};
+    auto row = [&](int r) { return n0 + 16 * b + r < p.N ? n0 + 16 * b + r : p.N - 1; };
+#pragma unroll
+    for (int t = 0; t < 4; ++t) w[b].p[t] = p.B.codes + row(load_row(lane, t)) * p.B.ld;
+    w[b].q = p.B.scales + row(l16) * p.B.lds;
   }
   for (long long m0 = 16LL * MB * blockIdx.y; m0 < p.M; m0 += 16LL * MB * gridDim.y) {
-    Row a[MB];
+    typename ActRow<A>::type a[MB];
     bool valid[MB];
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      const long long m = m0 + 16 * i + l16;
-      valid[i] = m < p.M;
-      a[i] = {p.A + (valid[i] ? m : 0) * p.lda, A == kMx ? p.SA + (valid[i] ? m : 0) * p.ldsa : nullptr};
+      auto row = [&](int r) { return m0 + 16 * i + r < p.M ? m0 + 16 * i + r : p.M - 1; };
+      if constexpr (A == kMx) {
+        valid[i] = m0 + 16 * i + load_row(lane, 0) < p.M;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) a[i].p[t] = p.A + row(load_row(lane, t)) * p.lda;
+        a[i].q = p.SA + row(l16) * p.ldsa;
+      } else {
+        valid[i] = m0 + 16 * i + l16 < p.M;
+        a[i] = {p.A + row(l16) * p.lda, nullptr};
+      }
     }
     Thin<kMx, A, MB, NB, ODD> t;
     t.clear();
-    t.run(a, valid, w, wave, WAVES, p.K, g);
+    t.run(a, valid, w, wave, WAVES, p.K, lane);
     thin_store<WAVES, MB, NB>(t.acc, part, m0, n0, p.M, p.N, p.C, p.ldc, p.c_format);
   }
 }

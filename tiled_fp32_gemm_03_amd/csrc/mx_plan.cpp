@@ -67,13 +67,15 @@ MoeSpace moe_space(int T, int E, int top, int I) {
   };
   w.pitch = ceil_div(I, 512) * 512;
   w.logits = take(8LL * T * E);
-  w.ids = take(4 * pairs);
   w.gates = take(4 * pairs);
   w.start = take(4LL * (E + 1));
+  w.ufirst = take(4LL * E);
   w.list = take(4 * pairs);
   w.active = take(4LL * (E + 1));
-  w.hi = take(2 * pairs * w.pitch);
-  w.lo = take(2 * pairs * w.pitch);
+  const long long chosen = E < pairs ? E : pairs;  // at most
+  const long long urows = ceil_div(pairs + 3 * chosen, 4) * 4;
+  w.hi = take(2 * urows * w.pitch);
+  w.lo = take(2 * urows * w.pitch);
   w.bytes = at;
   return w;
 }

@@ -3,23 +3,32 @@
 // read once from memory, which is what bounds them.
 //
 // A wave multiplies blocks of 16 activation rows with blocks of 16 weight
-// rows ("columns" of C) and takes K in pieces of four 128-deep steps (MX
-// weights) or one (16-bit ones).  A piece's weights are loaded at once, the
-// activations step by step, a step ahead of their use.  Rows past the last
-// are not loaded: with the usual few rows most lanes are spared the L1
-// traffic, of which 16-bit activations need four times what MX weights do.
+// rows ("columns" of C) and takes K in pieces of 256 bytes of weight row:
+// four 128-deep steps of MX weights, one of 16-bit ones.  A piece's weights
+// are loaded at once, the activations step by step, a step ahead of their
+// use.
 //
-// Lane l holds row l % 16 of each operand; which k a lane holds is free as
-// long as both operands agree, so it follows how the weights are stored, with
-// g = l / 16:
-//   MX weights: load s of a piece is block 4 s + g of it; MFMA j of step s
-//     takes its values 8 j .. 8 j + 7, widened with their scale (exact: an
+// The matrix instructions want lane l to hold row l % 16, but four
+// neighbouring lanes that read four rows cost the L1 four accesses where
+// four that read 64 bytes of one row cost it one, and the L1's accesses were
+// what bounded these kernels (a second product of 143 MB took 70 us with 21
+// accesses per load).  So lane l loads 16 bytes number l % 4 (of group g = l /
+// 16) of rows 4 (l / 4 % 4) + t, t = 0 .. 3, and a 4 x 4 transpose inside each
+// four lanes brings row l % 16's four into the lane: 32 ALU operations per
+// 4 KB.  Lane l then holds 64 consecutive bytes of its row, which decides the
+// order of k (any order is as good as both operands agree):
+//   MX weights: blocks 4 g + s of a piece's 16, s its step; MFMA j takes the
+//     block's values 8 j .. 8 j + 7, widened with their scale (exact: an
 //     element has two significant bits);
-//   16-bit weights: load j of a step is k = 32 j + 8 g .. + 7, the operand of
-//     MFMA j.
+//   16-bit weights: MFMA j takes k = 32 g + 8 j .. + 7.
+// The activations are read as their lanes hold them, valid rows alone; with
+// few rows that is few accesses.  The layer's inner values, which its first
+// product writes for its second, are kept in the order of these loads.
 #pragma once
 
 #include "mx_values.hpp"
+
+#include <type_traits>
 
 namespace gemm_f32_impl {
 namespace {
@@ -28,12 +37,28 @@ namespace {
 // kept as a sum of two bf16 terms.
 constexpr int kMx = 3, kSplit = 4;
 
-// One row of an operand: 2-byte values or MX codes; scales of an MX row; the
-// second term of a split one.
+// Where lane l loads 16 rows of weights: rows 4 (l / 4 % 4) + t, as 2-byte
+// values or MX codes, and the scales of row l % 16 (MX).
+struct Rows {
+  const unsigned char *p[4];
+  const unsigned char *q;
+};
+// Activations: the lane's row l % 16 of 2-byte values; of MX rows as weights;
+// of a split operand the lane's place in its two planes.
 struct Row {
   const unsigned char *p;
   const unsigned char *q;
 };
+template <int A>
+struct ActRow {
+  typedef Row type;
+};
+template <>
+struct ActRow<kMx> {
+  typedef Rows type;
+};
+// Row t of those that this lane loads, and the row it holds.
+__device__ inline int load_row(int lane, int t) { return (lane & 12) + t; }
 
 template <int W>
 constexpr int kPieceK = W == kMx ? 512 : 128;
@@ -64,6 +89,31 @@ __device__ inline void split_f16(u32x4 x, u32x4 &hi, u32x4 &lo) {
   }
   hi = __builtin_bit_cast(u32x4, h);
   lo = __builtin_bit_cast(u32x4, l);
+}
+
+// The 4 x 4 transpose inside each four lanes: lane i's r[t] goes to lane t's
+// r[i].
+template <int CTRL>
+__device__ inline uint32_t quad(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
+__device__ __forceinline__ void quad_transpose(u32x4 (&r)[4], int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+#pragma unroll
+    for (int t = 0; t < 4; t += 2) {  // lanes i, i ^ 1 and registers t, t + 1
+      const uint32_t a = r[t][d], b = r[t + 1][d], fa = quad<0xB1>(a), fb = quad<0xB1>(b);
+      r[t][d] = odd ? fb : a;
+      r[t + 1][d] = odd ? b : fa;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {  // lanes i, i ^ 2 and registers t, t + 2
+      const uint32_t a = r[t][d], b = r[t + 2][d], fa = quad<0x4E>(a), fb = quad<0x4E>(b);
+      r[t][d] = high ? fb : a;
+      r[t + 2][d] = high ? b : fa;
+    }
+  }
 }
 
 // 8 values of a row of 16-bit codes from k, the first `n` of them (others 0).
@@ -118,33 +168,29 @@ struct Eight<true> {
   }
 };
 
-// A piece of an MX row as it is stored: blocks 16 piece + 4 s + g and the 16
-// scales.  Blocks past the row's are read from its last; mask_mx_piece makes
-// them zeros with scale 1.
+// A piece of 16 MX rows: after `turn`, lane l holds blocks 16 piece + 4 g + s of
+// row l % 16 and their scales, byte s of the word.  Blocks past the row's are
+// read from its last; mask makes them zeros with scale 1.
 struct MxPiece {
   u32x4 c[4];
-  u32x4 s;
-};
-__device__ __forceinline__ void load_mx_piece(MxPiece &x, const Row &r, int piece, int g, int nb) {
-  x.s = *reinterpret_cast<const u32x4 *>(r.q + 16LL * piece);
+  uint32_t s;
+  __device__ __forceinline__ void load(const Rows &r, int piece, int lane, int nb) {
+    const int kb = 16 * piece + 4 * (lane >> 4) + (lane & 3), in = kb < nb ? kb : nb - 1;
+    s = *reinterpret_cast<const uint32_t *>(r.q + 16LL * piece + 4 * (lane >> 4));
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int kb = 16 * piece + 4 * s + g < nb ? 16 * piece + 4 * s + g : nb - 1;
-    x.c[s] = *reinterpret_cast<const u32x4 *>(r.p + 16LL * kb);
+    for (int t = 0; t < 4; ++t) c[t] = *reinterpret_cast<const u32x4 *>(r.p[t] + 16LL * in);
   }
-}
-__device__ __forceinline__ void mask_mx_piece(MxPiece &x, int piece, int g, int nb) {
+  __device__ __forceinline__ void turn(int lane) { quad_transpose(c, lane); }
+  __device__ __forceinline__ void mask(int piece, int lane, int nb) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
-    if (16 * piece + 4 * s + g >= nb) {
-      x.c[s] = u32x4{0, 0, 0, 0};
-      x.s[s] = 0x7f7f7f7fu;
-    }
-}
-// Lane group g's scale byte of step s.
-__device__ inline uint32_t piece_scale(const MxPiece &x, int s, int g) {
-  return (x.s[s] >> (8 * g)) & 255u;
-}
+    for (int i = 0; i < 4; ++i)
+      if (16 * piece + 4 * (lane >> 4) + i >= nb) {
+        c[i] = u32x4{0, 0, 0, 0};
+        s = (s & ~(255u << (8 * i))) | 127u << (8 * i);
+      }
+  }
+  __device__ __forceinline__ uint32_t scale(int i) const { return (s >> (8 * i)) & 255u; }
+};
 
 // How the values of MX weights become matrix operands.  As bf16 or fp16 by
 // one conversion per two values where every scale of the piece allows it:
@@ -179,12 +225,12 @@ __device__ inline u32x4 widen(uint32_t codes, uint32_t sb) {
 }
 // Whether all of a lane's blocks allow it (blocks of zeros allow any).
 template <uint32_t LOW, uint32_t HIGH>
-__device__ inline bool scales_within(const MxPiece &x, int g) {
+__device__ inline bool scales_within(const MxPiece &x) {
   bool ok = true;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const u32x4 c = x.c[s];
-    const uint32_t sb = piece_scale(x, s, g);
+    const uint32_t sb = x.scale(s);
     ok &= sb - LOW <= HIGH - LOW || (sb != 255 && (c[0] | c[1] | c[2] | c[3]) == 0);
   }
   return ok;
@@ -193,11 +239,39 @@ __device__ inline bool scales_within(const MxPiece &x, int g) {
 // The wave's number in its workgroup, as a scalar.
 __device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// First k (from the piece's first) of lane group g's operand of MFMA j of
-// step s.
+// Four 16-byte parts of 16-bit rows: 64 consecutive bytes of row l % 16 after
+// `turn`, from byte `at` of group g = 0 on.
+template <bool ODD>
+struct Half {
+  Eight<ODD> e[4];
+  u32x4 v[4];
+  __device__ __forceinline__ void load(const unsigned char *const (&p)[4], long long at) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) e[t].load(p[t] + at);
+  }
+  // Values k .. k + 7 of each row as far as they are below K, else 0.
+  __device__ __forceinline__ void load_tail(const unsigned char *const (&p)[4], long long k, int K) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) e[t].set(load_guarded(p[t], k, K - k), p[t]);
+  }
+  __device__ __forceinline__ void turn(const unsigned char *const (&p)[4], int lane) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = e[t].get(p[t]);
+    quad_transpose(v, lane);
+  }
+};
+
+// Split activations (two bf16 planes, hi and lo): 4 rows together, in the
+// order of the second product's loads.  For a load (piece, step, MFMA j) and
+// 4 rows: 256 bytes, lane group g's 64 at 64 g, row r's 16 at 16 (r % 4).
+// Values per row are padded with zeros to whole pieces (`pitch`).
 template <int W>
-__device__ inline int piece_k(int g, int s, int j) {
-  return 128 * s + (W == kMx ? 32 * g + 8 * j : 32 * j + 8 * g);
+__device__ inline long long split_at(int row, int k, long long pitch) {
+  const int kSteps = kPieceSteps<W>;
+  const int piece = k / kPieceK<W>, in = k % kPieceK<W>;
+  const int g = in / (32 * kSteps), s = in / 32 % kSteps, j = in / 8 % 4, b = in % 8;
+  return 2 * ((row >> 2) * 4 * pitch) + ((piece * kSteps + s) * 4 + j) * 256LL + 64 * g +
+         16 * (row & 3) + 2 * b;
 }
 
 // One product of thin operands: MB blocks of 16 rows of kind A by NB blocks
@@ -205,15 +279,10 @@ __device__ inline int piece_k(int g, int s, int j) {
 template <int W, int A, int MB, int NB, bool ODD = false>
 struct Thin {
   static constexpr int kK = kPieceK<W>, kSteps = kPieceSteps<W>;
+  typedef typename ActRow<A>::type Act;
   struct Weights {
     MxPiece mx[W == kMx ? NB : 1];
-    Eight<ODD> half[W == kMx ? 1 : NB][4];
-  };
-  // Activations of one step (16-bit or split), or of a piece (MX).
-  struct Acts {
-    MxPiece mx[A == kMx ? MB : 1];
-    Eight<ODD && A != kSplit> v[A == kMx ? 1 : MB][4];
-    Eight<false> lo[A == kSplit ? MB : 1][4];
+    Half<ODD> half[W == kMx ? 1 : NB];
   };
   f32x4 acc[MB][NB];
 
@@ -224,146 +293,152 @@ struct Thin {
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // A piece's weights; with TAIL it reaches past K: zeros there.
+  // A piece's weights; with TAIL it may reach past K.
   template <bool TAIL>
-  static __device__ __forceinline__ void load_weights(Weights &x, const Row (&w)[NB], int piece,
-                                                      int g, int K, int nb) {
+  static __device__ __forceinline__ void load_weights(Weights &x, const Rows (&w)[NB], int piece,
+                                                      int lane, int K, int nb) {
+    const long long k = (long long)kK * piece + 32 * (lane >> 4) + 8 * (lane & 3);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if constexpr (W == kMx) x.mx[b].load(w[b], piece, lane, nb);
+      else if constexpr (TAIL) x.half[b].load_tail(w[b].p, k, K);
+      else x.half[b].load(w[b].p, 2 * k);
+    }
+  }
+  template <bool TAIL>
+  static __device__ __forceinline__ void turn_weights(Weights &x, const Rows (&w)[NB], int piece,
+                                                      int lane, int nb) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if constexpr (W == kMx) {
-        load_mx_piece(x.mx[b], w[b], piece, g, nb);
-        if constexpr (TAIL) mask_mx_piece(x.mx[b], piece, g, nb);
+        x.mx[b].turn(lane);
+        if constexpr (TAIL) x.mx[b].mask(piece, lane, nb);
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const long long k = (long long)kK * piece + piece_k<W>(g, 0, j);
-          if constexpr (TAIL) x.half[b][j].set(load_guarded(w[b].p, k, K - k), w[b].p);
-          else x.half[b][j].load(w[b].p + 2 * k);
-        }
+        x.half[b].turn(w[b].p, lane);
       }
     }
   }
-  // Step s of a piece's activations.  Rows that `valid` leaves out are not
-  // loaded: their results are not used.  Split ones are padded with zeros to
-  // whole pieces.
-  template <bool TAIL>
-  static __device__ __forceinline__ void load_acts(Acts &y, const Row (&a)[MB],
-                                                   const bool (&valid)[MB], int piece, int s,
-                                                   int g, int K, int nb) {
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-      if (valid[i]) {
-        if constexpr (A == kMx) {
-          load_mx_piece(y.mx[i], a[i], piece, g, nb);
-          if constexpr (TAIL) mask_mx_piece(y.mx[i], piece, g, nb);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const long long k = (long long)kK * piece + piece_k<W>(g, s, j);
-            if constexpr (A == kSplit) {
-              y.v[i][j].load(a[i].p + 2 * k);
-              y.lo[i][j].load(a[i].q + 2 * k);
-            } else if constexpr (TAIL) {
-              y.v[i][j].set(load_guarded(a[i].p, k, K - k), a[i].p);
-            } else {
-              y.v[i][j].load(a[i].p + 2 * k);
-            }
-          }
-        }
-      }
-  }
 
-  // The products of a piece whose weights are loaded.
+  // The products of a piece whose weights are loaded and turned, with the
+  // activation rows that `valid` has.
   template <bool TAIL>
-  __device__ __forceinline__ void use(const Weights &x, const Row (&w)[NB], const Row (&a)[MB],
-                                      const bool (&valid)[MB], int piece, int g, int K, int nb) {
+  __device__ __forceinline__ void use(const Weights &x, const Act (&a)[MB],
+                                      const bool (&valid)[MB], int piece, int lane, int K, int nb) {
     if constexpr (A == kMx) {
-      Acts y;
-      load_acts<TAIL>(y, a, valid, piece, 0, g, K, nb);
+      MxPiece y[MB];
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int i = 0; i < MB; ++i) {
+        if (valid[i]) y[i].load(a[i], piece, lane, nb);
+        y[i].turn(lane);
+        if constexpr (TAIL) y[i].mask(piece, lane, nb);
+      }
+      auto step = [&](auto sel) __attribute__((always_inline)) {
+        constexpr int s = decltype(sel)::value;
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            acc[i][b] = mfma_mx(x.mx[b].c[s], (int)piece_scale(x.mx[b], s, g), y.mx[i].c[s],
-                                (int)piece_scale(y.mx[i], s, g), acc[i][b]);
+            acc[i][b] = mfma_mx<s>(x.mx[b].c[s], (int)x.mx[b].s, y[i].c[s], (int)y[i].s, acc[i][b]);
+      };
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{});
+      step(std::integral_constant<int, 3>{});
     } else {
-      Acts y[2];
-      load_acts<TAIL>(y[0], a, valid, piece, 0, g, K, nb);
+      constexpr Widen kHow = W == kF16 || (W == kMx && A == kF16) ? kToF16 : kToBf16;
       bool ok = true;
       if constexpr (W == kMx) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          ok &= A == kF16 ? scales_within<104, 140>(x.mx[b], g) : scales_within<1, 254>(x.mx[b], g);
+          ok &= A == kF16 ? scales_within<104, 140>(x.mx[b]) : scales_within<1, 254>(x.mx[b]);
         ok = __all(ok);
       }
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if (s + 1 < kSteps) load_acts<TAIL>(y[(s + 1) & 1], a, valid, piece, s + 1, g, K, nb);
-        __builtin_amdgcn_sched_barrier(0);
-        constexpr Widen kHow = W == kF16 || (W == kMx && A == kF16) ? kToF16 : kToBf16;
-        if (W != kMx || ok) multiply<kHow>(x, y[s & 1], w, a, s, g);
-        else multiply<kThroughF32>(x, y[s & 1], w, a, s, g);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      if (W != kMx || ok) multiply<TAIL, kHow>(x, a, valid, piece, lane, K);
+      else multiply<TAIL, kThroughF32>(x, a, valid, piece, lane, K);
     }
   }
 
-  // One step's products.  HOW: the format the weights come in or are brought to.
-  template <Widen HOW>
-  __device__ __forceinline__ void multiply(const Weights &x, const Acts &y, const Row (&w)[NB],
-                                           const Row (&a)[MB], int s, int g) {
+  // HOW: the format the weights come in or are brought to.
+  template <bool TAIL, Widen HOW>
+  __device__ __forceinline__ void multiply(const Weights &x, const Act (&a)[MB],
+                                           const bool (&valid)[MB], int piece, int lane, int K) {
+    constexpr bool kSplitHere = A == kF16 && HOW != kToF16;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u32x4 wv[NB];
+    for (int s = 0; s < kSteps; ++s) {
+      Eight<ODD && A != kSplit> y[MB][4];
+      u32x4 z[A == kSplit ? MB : 1][4];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if constexpr (W == kMx) wv[b] = widen<HOW>(x.mx[b].c[s][j], piece_scale(x.mx[b], s, g));
-        else wv[b] = x.half[b][j].get(w[b].p);
-      }
+      for (int i = 0; i < MB; ++i)
+        if (valid[i]) {
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        u32x4 v = y.v[i][j].get(a[i].p), lo{};
-        if constexpr (A == kSplit) lo = y.lo[i][j].get(a[i].q);
-        constexpr bool kSplitHere = A == kF16 && HOW != kToF16;
-        if constexpr (kSplitHere) split_f16(v, v, lo);
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (A == kSplit) {
+              const long long at = ((piece * kSteps + s) * 4 + j) * 256LL;
+              y[i][j].load(a[i].p + at);
+              z[i][j] = *reinterpret_cast<const u32x4 *>(a[i].q + at);
+            } else {
+              const long long k =
+                  (long long)kK * piece + 32 * kSteps * (lane >> 4) + 32 * s + 8 * j;
+              if constexpr (TAIL) y[i][j].set(load_guarded(a[i].p, k, K - k), a[i].p);
+              else y[i][j].load(a[i].p + 2 * k);
+            }
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u32x4 wv[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          if constexpr (A == kSplit && HOW == kToF16) {
-            // fp16 weights are split too; the product of the two low parts,
-            // 2^-18 of the whole, is left out
-            u32x4 wh, wl;
-            split_f16(wv[b], wh, wl);
-            acc[i][b] = mfma_bf16(wh, v, acc[i][b]);
-            acc[i][b] = mfma_bf16(wh, lo, acc[i][b]);
-            acc[i][b] = mfma_bf16(wl, v, acc[i][b]);
-          } else if constexpr (HOW == kToF16) {
-            acc[i][b] = mfma_f16(wv[b], v, acc[i][b]);
-          } else {
-            acc[i][b] = mfma_bf16(wv[b], v, acc[i][b]);
-            if constexpr (A == kSplit || kSplitHere) acc[i][b] = mfma_bf16(wv[b], lo, acc[i][b]);
+          if constexpr (W == kMx) wv[b] = widen<HOW>(x.mx[b].c[s][j], x.mx[b].scale(s));
+          else wv[b] = x.half[b].v[j];
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          u32x4 v = y[i][j].get(a[i].p), lo{};
+          if constexpr (A == kSplit) lo = z[i][j];
+          if constexpr (kSplitHere) split_f16(v, v, lo);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            if constexpr (A == kSplit && HOW == kToF16) {
+              // fp16 weights are split too; the product of the two low parts,
+              // 2^-18 of the whole, is left out
+              u32x4 wh, wl;
+              split_f16(wv[b], wh, wl);
+              acc[i][b] = mfma_bf16(wh, v, acc[i][b]);
+              acc[i][b] = mfma_bf16(wh, lo, acc[i][b]);
+              acc[i][b] = mfma_bf16(wl, v, acc[i][b]);
+            } else if constexpr (HOW == kToF16) {
+              acc[i][b] = mfma_f16(wv[b], v, acc[i][b]);
+            } else {
+              acc[i][b] = mfma_bf16(wv[b], v, acc[i][b]);
+              if constexpr (A == kSplit || kSplitHere) acc[i][b] = mfma_bf16(wv[b], lo, acc[i][b]);
+            }
           }
         }
       }
+      // One step's activations at a time: all of them together would cost the
+      // registers of the waves that hide their latency.
+      if constexpr (kSteps > 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
 
   // Adds the products of pieces first, first + step, ... of the K values.
-  __device__ __forceinline__ void run(const Row (&a)[MB], const bool (&valid)[MB],
-                                      const Row (&w)[NB], int first, int step, int K, int g) {
+  __device__ __forceinline__ void run(const Act (&a)[MB], const bool (&valid)[MB],
+                                      const Rows (&w)[NB], int first, int step, int K, int lane) {
     const int nb = (int)mx_blocks(K), last = K / kK;  // whole pieces
     int p = first;
 #pragma unroll 1
     for (; p < last; p += step) {
       Weights x;
-      load_weights<false>(x, w, p, g, K, nb);
-      use<false>(x, w, a, valid, p, g, K, nb);
+      load_weights<false>(x, w, p, lane, K, nb);
+      turn_weights<false>(x, w, p, lane, nb);
+      use<false>(x, a, valid, p, lane, K, nb);
     }
     if (p == last && (long long)last * kK < K) {
       Weights x;
-      load_weights<true>(x, w, p, g, K, nb);
-      use<true>(x, w, a, valid, p, g, K, nb);
+      load_weights<true>(x, w, p, lane, K, nb);
+      turn_weights<true>(x, w, p, lane, nb);
+      use<true>(x, a, valid, p, lane, K, nb);
     }
   }
 };

@@ -168,12 +168,13 @@ __device__ inline void store4_fmt(int fmt, void *p, long long i, int n, f32x4 v)
 
 // One v_mfma_scale_f32_16x16x128_f8f6f4 on 4-bit elements: lane l holds 32
 // values (one block) of row l % 16 of each operand, the k of block l / 16,
-// with that block's scale byte.  The accumulator's 4 values are row l % 16
+// with that block's scale byte: byte SEL of the words sb and sa.  The accumulator's 4 values are row l % 16
 // of `a` (C's row) and rows 4 (l / 16) .. + 3 of `b` (C's columns).
+template <int SEL = 0>
 __device__ inline f32x4 mfma_mx(u32x4 b, int sb, u32x4 a, int sa, f32x4 acc) {
   const i32x8 x{(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
   const i32x8 y{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 4, 4, 0, sb, 0, sa);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 4, 4, SEL, sb, SEL, sa);
 }
 
 }  // namespace
