@@ -2,9 +2,9 @@
 // logits, the choice of experts, and the two products over the chosen
 // experts' weights.  The products read each chosen expert's weights once,
 // straight into the matrix instructions' operands (mx_thin.hpp); the tokens
-// of one expert share them, 16 rows at a time.  Three launches for up to 8
-// tokens (the choice is made again by each workgroup of the first product),
-// four for more.
+// of one expert share them, 16 rows at a time.  Four launches for up to 8
+// tokens (logits, first product, second product, sum; the choice is made again
+// by each workgroup of the first product), six for more.
 #include "mx_internal.hpp"
 #include "mx_thin.hpp"
 
@@ -84,10 +84,10 @@ __global__ void __launch_bounds__(256) moe_logits_kernel(MoeProblem p) {
   if (whole + 8 * lane < p.H) {
     const int h = whole + 8 * lane;
     u32x4 xw[TB];
-    const u32x4 rw = load_guarded(reinterpret_cast<const unsigned char *>(row), h, p.H - h);
+    const u32x4 rw = load_guarded(reinterpret_cast<const unsigned char *>(row), h, p.H);
 #pragma unroll
     for (int i = 0; i < TB; ++i)
-      xw[i] = load_guarded(reinterpret_cast<const unsigned char *>(x[i]), h, p.H - h);
+      xw[i] = load_guarded(reinterpret_cast<const unsigned char *>(x[i]), h, p.H);
     add(rw, xw);
   }
 #pragma unroll
@@ -113,13 +113,13 @@ struct Route {
   unsigned short list[MAX_PAIRS];      // pairs by expert
   unsigned short count[(MAX_PAIRS + 63) / 64][kMoeMaxExperts];
   unsigned short start[kMoeMaxExperts + 1];
-  unsigned short ufirst[kMoeMaxExperts];
   unsigned short active[kMoeMaxExperts];
   int nactive;
 };
 
+// Token t, as number `slot` of `r`.
 template <int MAX_PAIRS>
-__device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, int t) {
+__device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, int slot, int t) {
   const int lane = threadIdx.x & 63;
   const double *logits = ws_at<double>(p, p.at.logits) + t * p.E;
   const double low = -__builtin_inf();
@@ -166,8 +166,8 @@ __device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, 
   }
   const double total = __any(nan) ? __builtin_nan("") : wave_sum(part);
   if (lane < p.top) {
-    r.chosen[t * p.top + lane] = (unsigned short)id;
-    r.gate[t * p.top + lane] = (float)(w / total);
+    r.chosen[slot * p.top + lane] = (unsigned short)id;
+    r.gate[slot * p.top + lane] = (float)(w / total);
   }
 }
 
@@ -182,15 +182,15 @@ __device__ inline unsigned long long same_expert(int e) {
   return same;
 }
 
+// The lists of chosen pairs, from r.chosen.
 template <int THREADS, int MAX_PAIRS>
-__device__ inline void route_all(const MoeProblem &p, Route<MAX_PAIRS> &r) {
+__device__ inline void list_pairs(const MoeProblem &p, Route<MAX_PAIRS> &r) {
   constexpr int kWaves = THREADS / 64;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int pairs = p.T * p.top, chunks = (pairs + 63) / 64;
   const unsigned long long before = (1ULL << lane) - 1;
   for (int c = 0; c < chunks; ++c)
     for (int e = threadIdx.x; e < p.E; e += THREADS) r.count[c][e] = 0;
-  for (int t = wave; t < p.T; t += kWaves) choose_experts(p, r, t);
   __syncthreads();
   for (int c = wave; c < chunks; c += kWaves) {
     const int i = 64 * c + lane, e = i < pairs ? r.chosen[i] : kMoeMaxExperts;
@@ -199,27 +199,22 @@ __device__ inline void route_all(const MoeProblem &p, Route<MAX_PAIRS> &r) {
   }
   __syncthreads();
   if (wave == 0) {  // where each expert's pairs begin, and the chosen experts
-    int base = 0, ubase = 0, nact = 0;
+    int base = 0, nact = 0;
     for (int e0 = 0; e0 < p.E; e0 += 64) {
       const int e = e0 + lane;
       int n = 0;
       if (e < p.E)
         for (int c = 0; c < chunks; ++c) n += r.count[c][e];
-      const int u = (n + 3) & ~3;  // rows of u
-      int upto = n, uupto = u;
+      int upto = n;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(upto, d), uv = __shfl_up(uupto, d);
-        if (lane >= d) upto += v, uupto += uv;
+        const int v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
       }
-      if (e < p.E) {
-        r.start[e] = (unsigned short)(base + upto - n);
-        r.ufirst[e] = (unsigned short)(ubase + uupto - u);
-      }
+      if (e < p.E) r.start[e] = (unsigned short)(base + upto - n);
       const unsigned long long on = __ballot(n > 0);
       if (n > 0) r.active[nact + __popcll(on & before)] = (unsigned short)e;
       base += __shfl(upto, 63);
-      ubase += __shfl(uupto, 63);
       nact += __popcll(on);
     }
     if (lane == 0) {
@@ -240,232 +235,216 @@ __device__ inline void route_all(const MoeProblem &p, Route<MAX_PAIRS> &r) {
   __syncthreads();
 }
 
-// The route in the workspace, for the kernels that follow, and the caller's
-// ids and gates.
+// Chosen experts and gates, to the workspace and the caller.
 template <int THREADS, int MAX_PAIRS>
-__device__ inline void write_route(const MoeProblem &p, const Route<MAX_PAIRS> &r) {
-  const int pairs = p.T * p.top;
-  int *list = ws_at<int>(p, p.at.list), *start = ws_at<int>(p, p.at.start);
-  int *active = ws_at<int>(p, p.at.active), *ufirst = ws_at<int>(p, p.at.ufirst);
+__device__ inline void write_choice(const MoeProblem &p, const Route<MAX_PAIRS> &r, int from,
+                                    int to) {
+  int *ids = ws_at<int>(p, p.at.ids);
   float *gates = ws_at<float>(p, p.at.gates);
-  for (int i = threadIdx.x; i < pairs; i += THREADS) {
-    list[i] = r.list[i];
-    gates[i] = r.gate[i];
-    if (p.ids) p.ids[i] = r.chosen[i];
-    if (p.gates) p.gates[i] = r.gate[i];
+  for (int i = from + threadIdx.x; i < to; i += THREADS) {
+    ids[i] = r.chosen[i - from];
+    gates[i] = r.gate[i - from];
+    if (p.ids) p.ids[i] = r.chosen[i - from];
+    if (p.gates) p.gates[i] = r.gate[i - from];
   }
+}
+// The lists, to the workspace.
+template <int THREADS, int MAX_PAIRS>
+__device__ inline void write_lists(const MoeProblem &p, const Route<MAX_PAIRS> &r) {
+  int *list = ws_at<int>(p, p.at.list), *start = ws_at<int>(p, p.at.start);
+  int *active = ws_at<int>(p, p.at.active);
+  for (int i = threadIdx.x; i < p.T * p.top; i += THREADS) list[i] = r.list[i];
   for (int e = threadIdx.x; e <= p.E; e += THREADS) start[e] = r.start[e];
-  for (int e = threadIdx.x; e < p.E; e += THREADS) ufirst[e] = r.ufirst[e];
   for (int a = threadIdx.x; a < r.nactive; a += THREADS) active[1 + a] = r.active[a];
   if (threadIdx.x == 0) active[0] = r.nactive;
 }
 
-constexpr int kRouteThreads = 1024;
-__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(MoeProblem p) {
+// More than kFusedTokens tokens: the choice, four tokens to a workgroup, and
+// the lists, by one.
+constexpr int kChooseTokens = 4;
+__global__ void __launch_bounds__(64 * kChooseTokens) moe_choose_kernel(MoeProblem p) {
+  __shared__ Route<kChooseTokens * kMoeMaxTop> r;
+  const int t0 = kChooseTokens * blockIdx.x;
+  const int last = t0 + kChooseTokens < p.T ? t0 + kChooseTokens : p.T;
+  if (t0 + wave_id() < last) choose_experts(p, r, wave_id(), t0 + wave_id());
+  __syncthreads();
+  write_choice<64 * kChooseTokens>(p, r, t0 * p.top, last * p.top);
+}
+constexpr int kListThreads = 1024;
+__global__ void __launch_bounds__(kListThreads) moe_list_kernel(MoeProblem p) {
   __shared__ Route<kMoeMaxTokens * kMoeMaxTop> r;
-  route_all<kRouteThreads>(p, r);
-  write_route<kRouteThreads>(p, r);
+  for (int i = threadIdx.x; i < p.T * p.top; i += kListThreads)
+    r.chosen[i] = (unsigned short)ws_at<int>(p, p.at.ids)[i];
+  list_pairs<kListThreads>(p, r);
+  write_lists<kListThreads>(p, r);
 }
 
-// ---- first product: u = silu(gate) * other ------------------------------------
-// A unit is one chosen expert and 16 of its inner columns, both factors.  `ks`
-// waves share a unit, taking the pieces of H in turn: one wave per unit where
-// there are units enough to fill the chip, more where there are few.
+// ---- the two products ---------------------------------------------------------
+// A workgroup takes one chosen expert and some groups of 16 columns; `ks` of
+// its waves share a group, taking the pieces of K in turn: one where there
+// are groups enough to fill the chip, more where there are few.  A wave goes
+// through `each` groups, its weights loaded ahead across them.
 
-constexpr int kUpWaves = 4;
-typedef f32x4 UpPart[1][2][64];  // [block of rows][factor][lane]
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
-template <int W, int AF, int MB, bool ODD>
-__device__ __forceinline__ void moe_up_rows(const MoeProblem &p, const Rows (&w)[2],
-                                            const Row (&x)[MB], int ufirst, int n, int i0, int ks,
-                                            bool any, UpPart *part) {
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  const int l16 = lane & 15, g = lane >> 4, kw = wave & (ks - 1);
-  bool valid[MB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) valid[i] = 16 * i + l16 < n;
-  Thin<W, AF, MB, 2, ODD> t;
-  t.clear();
-  if (any) t.run(x, valid, w, kw, ks, p.H, lane);
-  if (ks > 1) {
-#pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      part[wave][i][0][lane] = t.acc[i][0];
-      part[wave][i][1][lane] = t.acc[i][1];
-    }
-    __syncthreads();
-    if (kw == 0)
-      for (int q = 1; q < ks; ++q)
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          t.acc[i][0] += part[wave + q][i][0][lane];
-          t.acc[i][1] += part[wave + q][i][1][lane];
-        }
-    __syncthreads();
-  }
-  if (kw != 0 || !any) return;
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int m = 16 * i + l16;
-    if (m >= n) continue;
-    uint16_t hi[4], lo[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = t.acc[i][0][j], b = t.acc[i][1][j];
-      const float u = a / (1.f + expf(-a)) * b;
-      const float v = i0 + 4 * g + j < p.I ? u : 0.f;  // rows are padded with zeros
-      hi[j] = from_f32<kBf16>(v);
-      const float h = to_f32<kBf16>(hi[j]);
-      lo[j] = mag_bits(h) < 0x7f800000u ? from_f32<kBf16>(v - h) : (uint16_t)0;
-    }
-    const long long at = split_at<W>(ufirst + m, i0 + 4 * g, p.at.pitch);
-    *reinterpret_cast<u32x2 *>(p.ws + p.at.hi + at) =
-        u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
-    *reinterpret_cast<u32x2 *>(p.ws + p.at.lo + at) =
-        u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
-  }
-}
-
-// FUSED: at most kFusedTokens tokens, each workgroup makes the choice itself.
-template <int W, int AF, bool FUSED, bool ODD>
-__global__ void __launch_bounds__(64 * kUpWaves, 3) moe_up_kernel(MoeProblem p, int ks) {
-  __shared__ UpPart part[kUpWaves];
-  __shared__ Route<FUSED ? kFusedTokens * kMoeMaxTop : 1> route;
-  const int wave = wave_id(), l16 = threadIdx.x & 15;
-  int e, first, n, ufirst;
-  if constexpr (FUSED) {
-    route_all<64 * kUpWaves>(p, route);
-    if (blockIdx.x == 0 && blockIdx.y == 0) write_route<64 * kUpWaves>(p, route);
-    if ((int)blockIdx.y >= route.nactive) return;
-    e = __builtin_amdgcn_readfirstlane(route.active[blockIdx.y]);
-    first = __builtin_amdgcn_readfirstlane(route.start[e]);
-    n = __builtin_amdgcn_readfirstlane(route.start[e + 1]) - first;
-    ufirst = __builtin_amdgcn_readfirstlane(route.ufirst[e]);
-  } else {
-    const int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
-    if ((int)blockIdx.y >= active[0]) return;
-    e = active[1 + blockIdx.y];
-    first = start[e];
-    n = start[e + 1] - first;
-    ufirst = ws_at<int>(p, p.at.ufirst)[e];
-  }
-  const int lane = threadIdx.x & 63;
-  const int units = kUpWaves / ks;
-  const int i0 = 16 * (int)(blockIdx.x * units + wave / ks);
-  const bool any = i0 < p.at.pitch;  // the last workgroup may have units too many
-  auto inner = [&](int r) { return 2LL * p.I * e + (i0 + r < p.I ? i0 + r : p.I - 1); };
-  Rows w[2];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const long long r = inner(load_row(lane, t));
-    w[0].p[t] = p.W1 + r * p.ld1;
-    w[1].p[t] = p.W1 + (r + p.I) * p.ld1;
-  }
-  if constexpr (W == kMx) {
-    w[0].q = p.S1 + inner(l16) * p.lds1;
-    w[1].q = p.S1 + (inner(l16) + p.I) * p.lds1;
-  }
-  for (int m = 0; m < n; m += 16) {
-    const int at = first + (m + l16 < n ? m + l16 : n - 1);
-    const int pair = FUSED ? (int)route.list[at] : ws_at<int>(p, p.at.list)[at];
-    const Row x[1] = {{reinterpret_cast<const unsigned char *>(p.X + pair / p.top * p.ldx), nullptr}};
-    moe_up_rows<W, AF, 1, ODD>(p, w, x, ufirst + m, n - m, i0, ks, any, part);
-  }
-}
-
-// ---- second product and the weighted sum -----------------------------------------
-// A workgroup owns 16 columns of Y for all tokens.  The pieces of all chosen
-// experts' inner columns, one expert after the other, are dealt to its waves
-// in equal runs; a wave loads the next piece's weights while it uses one, and
-// adds each piece's rows, times their gates, to a sum of its own in LDS.  The
-// waves' sums are added in wave order at the end.
-
-// LDS of the second product: sums [wave][token][16], then the route.
-struct DownLds {
-  int gates, start, ufirst, active, tokens, bytes;
+// What the launch chose: waves per group, groups per wave, and the LDS for
+// activations.
+struct MoeShape {
+  int ks, each, lds;
 };
-constexpr DownLds down_lds(int waves, int T, int E, int top) {
-  const int pairs = T * top;
-  const int gates = waves * T * 64, start = gates + 4 * pairs, ufirst = start + 2 * (E + 1),
-            active = ufirst + 2 * E, tokens = active + 2 * E;
-  return {gates, start, ufirst, active, tokens, tokens + 2 * pairs};
+
+// An expert's part in a launch.
+struct Expert {
+  int e, first, n;  // its number, its first place in the list, its pairs
+};
+__device__ inline bool expert_of(const MoeProblem &p, int a, Expert &x) {
+  const int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
+  if (a >= active[0]) return false;
+  x.e = active[1 + a];
+  x.first = start[x.e];
+  x.n = start[x.e + 1] - x.first;
+  return true;
 }
 
-template <int W, int WAVES, bool ODD>
-__global__ void __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : 2) moe_down_kernel(MoeProblem p) {
-  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  constexpr int kThreads = 64 * WAVES;
-  const DownLds at = down_lds(WAVES, p.T, p.E, p.top);
-  float *gate = reinterpret_cast<float *>(lds + at.gates);  // by place in the list
-  unsigned short *start = reinterpret_cast<unsigned short *>(lds + at.start);
-  unsigned short *ufirst = reinterpret_cast<unsigned short *>(lds + at.ufirst);
-  unsigned short *active = reinterpret_cast<unsigned short *>(lds + at.active);
-  unsigned short *token = reinterpret_cast<unsigned short *>(lds + at.tokens);  // by place
-  const int wave = wave_id(), lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const int nact = ws_at<int>(p, p.at.active)[0], pairs = p.T * p.top;
-  for (int i = threadIdx.x; i < 4 * p.T * WAVES; i += kThreads)
-    reinterpret_cast<f32x4 *>(lds)[i] = f32x4{0, 0, 0, 0};
-  for (int i = threadIdx.x; i < pairs; i += kThreads) {
-    const int pair = ws_at<int>(p, p.at.list)[i];
-    gate[i] = ws_at<float>(p, p.at.gates)[pair];
-    token[i] = (unsigned short)(pair / p.top);
+// Columns 16 c .. 16 c + 15 of the product of up to 16 rows, NB factors each,
+// for each group c of this wave: `weights(c)` gives the lane's rows,
+// `done(c, acc)` takes the sums of the group's first wave.
+template <int W, int A, int NB, bool ODD, class RowOf, class WeightsOf, class Done>
+__device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, int n, int K,
+                                               int groups, const MoeShape &sh,
+                                               WeightsOf weights, Done done) {
+  typedef Thin<W, A, 1, NB, ODD> Product;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  // As much of K as the launch's LDS holds of this many rows.
+  const int round = sh.ks * kPieceK<W>;
+  const int keep = n <= 4 ? 4 : 16;
+  const Tile tile{keep, tile_values<A>(keep, K, round, sh.lds)};
+  const bool whole = tile.kc >= K;
+  const int per = kWaves / sh.ks;  // groups side by side
+  int c = (int)blockIdx.x * per * sh.each + wave / sh.ks;
+  typename Product::Walk at{wave & (sh.ks - 1), sh.ks, c < groups, false};
+  Row w[NB], next[NB];
+  weights(c < groups ? c : groups - 1, w);
+  typename Product::Weights x;
+  Product::load_first(x, w, at, K, lane);
+  for (int i = 0; i < sh.each; ++i, c += per) {
+    at.any = c < groups;
+    at.staged = whole && i > 0;
+    weights(i + 1 < sh.each && c + per < groups ? c + per : at.any ? c : groups - 1, next);
+    Product t;
+    t.clear();
+    t.template run<kThreads>(lds, tile, row, n, w, next, x, at, K, lane);
+    if (sh.ks > 1) {  // the waves' sums, added in wave order
+      __shared__ f32x4 part[kWaves][NB][64];
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < NB; ++b) part[wave][b][lane] = t.acc[0][b];
+      __syncthreads();
+      if (at.first == 0)
+        for (int q = 1; q < sh.ks; ++q)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) t.acc[0][b] += part[wave + q][b][lane];
+    }
+    if (at.any && at.first == 0 && (lane & 15) < n) done(c, t.acc[0]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) w[b] = next[b];
   }
-  for (int i = threadIdx.x; i <= p.E; i += kThreads)
-    start[i] = (unsigned short)ws_at<int>(p, p.at.start)[i];
-  for (int i = threadIdx.x; i < p.E; i += kThreads)
-    ufirst[i] = (unsigned short)ws_at<int>(p, p.at.ufirst)[i];
-  for (int i = threadIdx.x; i < nact; i += kThreads)
-    active[i] = (unsigned short)ws_at<int>(p, p.at.active)[1 + i];
-  __syncthreads();
+}
 
-  float *sum = reinterpret_cast<float *>(lds) + wave * 16 * p.T;
-  const int n0 = 16 * blockIdx.x, nb = (int)mx_blocks(p.I);
-  const int pieces = (int)ceil_div(p.I, kPieceK<W>), whole = p.I / kPieceK<W>;
-  const long long all = (long long)nact * pieces;
-  const int from = (int)(all * wave / WAVES), to = (int)(all * (wave + 1) / WAVES);
-  typedef Thin<W, kSplit, 1, 1, ODD> Product;
-#pragma unroll 1
-  for (int v = from; v < to; ++v) {
-    const int e = __builtin_amdgcn_readfirstlane(active[v / pieces]), piece = v % pieces;
-    const int first = __builtin_amdgcn_readfirstlane(start[e]);
-    const int last = __builtin_amdgcn_readfirstlane(start[e + 1]);
-    auto row = [&](int r) { return (long long)p.H * e + (n0 + r < p.H ? n0 + r : p.H - 1); };
-    Rows w[1];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) w[0].p[t] = p.W2 + row(load_row(lane, t)) * p.ld2;
-    if constexpr (W == kMx) w[0].q = p.S2 + row(l16) * p.lds2;
-    typename Product::Weights x;
-    if (piece < whole) {
-      Product::template load_weights<false>(x, w, piece, lane, p.I, nb);
-      Product::template turn_weights<false>(x, w, piece, lane, nb);
-    } else {
-      Product::template load_weights<true>(x, w, piece, lane, p.I, nb);
-      Product::template turn_weights<true>(x, w, piece, lane, nb);
+// First product: u = silu(gate) * other.  FUSED: at most kFusedTokens tokens,
+// each workgroup makes the choice itself.
+template <int W, int AF, bool FUSED, bool ODD>
+__global__ void __launch_bounds__(kThreads, 3) moe_up_kernel(MoeProblem p, MoeShape sh) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ Route<FUSED ? kFusedTokens * kMoeMaxTop : 1> route;
+  __shared__ long long starts[16];  // of the tokens' rows
+  Expert x;
+  if constexpr (FUSED) {
+    for (int t = wave_id(); t < p.T; t += kWaves) choose_experts(p, route, t, t);
+    __syncthreads();
+    list_pairs<kThreads>(p, route);
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+      write_choice<kThreads>(p, route, 0, p.T * p.top);
+      write_lists<kThreads>(p, route);
     }
-    const int u0 = __builtin_amdgcn_readfirstlane(ufirst[e]);
-    for (int m0 = first; m0 < last; m0 += 16) {
-      const int m = m0 + l16;
-      const bool valid[1] = {m < last};
-      const long long at_u = split_at<W>(u0 + m - first, 0, p.at.pitch) + 64 * g;
-      const Row u[1] = {{p.ws + p.at.hi + at_u, p.ws + p.at.lo + at_u}};
-      Product t;
-      t.clear();
-      t.template use<false>(x, u, valid, piece, lane, p.I, nb);
-      if (valid[0]) {
-        f32x4 *y = reinterpret_cast<f32x4 *>(sum + 16 * token[m] + 4 * g);
-        *y += gate[m] * t.acc[0][0];
-      }
+    if ((int)blockIdx.y >= route.nactive) return;
+    x.e = __builtin_amdgcn_readfirstlane(route.active[blockIdx.y]);
+    x.first = __builtin_amdgcn_readfirstlane(route.start[x.e]);
+    x.n = __builtin_amdgcn_readfirstlane(route.start[x.e + 1]) - x.first;
+  } else if (!expert_of(p, blockIdx.y, x)) {
+    return;
+  }
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  auto weights = [&](int c, Row (&w)[2]) __attribute__((always_inline)) {
+    const long long i = 16LL * c + l16 < p.I ? 16LL * c + l16 : p.I - 1, r = 2LL * p.I * x.e + i;
+    w[0] = {p.W1 + r * p.ld1, p.S1 + r * p.lds1};
+    w[1] = {p.W1 + (r + p.I) * p.ld1, p.S1 + (r + p.I) * p.lds1};
+  };
+  for (int m0 = 0; m0 < x.n; m0 += 16) {
+    const int n = x.n - m0 < 16 ? x.n - m0 : 16;
+    if ((int)threadIdx.x < n) {
+      const int at = x.first + m0 + threadIdx.x;
+      const int pair = FUSED ? (int)route.list[at] : ws_at<int>(p, p.at.list)[at];
+      starts[threadIdx.x] = pair / p.top * p.ldx;
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 4 * p.T; i += kThreads) {
-    const f32x4 *s = reinterpret_cast<const f32x4 *>(lds) + i;
-    f32x4 v = s[0];
+    auto row = [&](int r) __attribute__((always_inline)) {
+      return Row{reinterpret_cast<const unsigned char *>(p.X + starts[r]), nullptr};
+    };
+    auto done = [&](int c, const f32x4 (&acc)[2]) __attribute__((always_inline)) {
+      f32x4 u;
+      const long long i = 16LL * c + 4 * g;
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) v += s[w * 4 * p.T];
-    const int t = i / 4, n = n0 + 4 * (i % 4);
-    store4_fmt(p.y_format, p.Y, t * p.ldy + n, p.H - n < 4 ? p.H - n : 4, v);
+      for (int j = 0; j < 4; ++j)  // zeros from I to the pitch
+        u[j] = i + j < p.I ? acc[0][j] / (1.f + expf(-acc[0][j])) * acc[1][j] : 0.f;
+      if (i < p.at.upitch)
+        *reinterpret_cast<f32x4 *>(ws_at<float>(p, p.at.u) + (x.first + m0 + l16) * p.at.upitch + i) = u;
+    };
+    const int groups = (int)ceil_div(p.I, 16);
+    expert_columns<W, AF, 2, ODD>(lds, row, n, p.H, groups, sh, weights, done);
+    __syncthreads();
   }
+}
+
+// Second product: each pair's result, before its gate.
+template <int W, bool ODD>
+__global__ void __launch_bounds__(kThreads, 3) moe_down_kernel(MoeProblem p, MoeShape sh) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  Expert x;
+  if (!expert_of(p, blockIdx.y, x)) return;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  auto weights = [&](int c, Row (&w)[1]) __attribute__((always_inline)) {
+    const long long h = 16LL * c + l16 < p.H ? 16LL * c + l16 : p.H - 1, r = (long long)p.H * x.e + h;
+    w[0] = {p.W2 + r * p.ld2, p.S2 + r * p.lds2};
+  };
+  for (int m0 = 0; m0 < x.n; m0 += 16) {
+    const int n = x.n - m0 < 16 ? x.n - m0 : 16;
+    auto row = [&](int r) __attribute__((always_inline)) {
+      return Row{p.ws + p.at.u + 4 * (x.first + m0 + r) * p.at.upitch, nullptr};
+    };
+    auto done = [&](int c, const f32x4 (&acc)[1]) __attribute__((always_inline)) {
+      const int pair = ws_at<int>(p, p.at.list)[x.first + m0 + l16];
+      const long long h = 16LL * c + 4 * g, left = p.H - h;
+      store4<kF32>(ws_at<float>(p, p.at.part), pair * p.at.ypitch + h, (int)(left < 4 ? left : 4),
+                   acc[0]);
+    };
+    const int groups = (int)ceil_div(p.H, 16);
+    expert_columns<W, kF32, 1, ODD>(lds, row, n, p.I, groups, sh, weights, done);
+    __syncthreads();
+  }
+}
+
+// Y: each token's results times their gates, in the order of the choice.
+__global__ void __launch_bounds__(256) moe_sum_kernel(MoeProblem p) {
+  const int t = blockIdx.y;
+  const long long h = 4LL * (blockIdx.x * 256 + threadIdx.x), left = p.H - h;
+  if (left <= 0) return;
+  const float *gates = ws_at<float>(p, p.at.gates) + t * p.top;
+  const float *part = ws_at<float>(p, p.at.part) + (long long)t * p.top * p.at.ypitch + h;
+  f32x4 y{0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < p.top; ++s)
+    y += gates[s] * *reinterpret_cast<const f32x4 *>(part + s * p.at.ypitch);
+  store4_fmt(p.y_format, p.Y, t * p.ldy + h, (int)(left < 4 ? left : 4), y);
 }
 
 template <int FMT>
@@ -476,30 +455,44 @@ hipError_t launch_logits(const MoeProblem &p, hipStream_t s) {
                        s, p);
 }
 
-template <int W, int AF, bool ODD>
-hipError_t launch_up(const MoeProblem &p, hipStream_t s) {
+// The shape of a product over `experts` experts, `columns` columns and K, of
+// at most `rows` rows each.
+template <int W, int A>
+MoeShape shape_of(long long experts, int columns, int K, int rows) {
+  const long long groups = experts * ceil_div(columns, 16);
+  MoeShape sh;
+  sh.ks = waves_per_group(groups, K, kPieceK<W>, kWaves, 8 * 256);
+  // Groups per wave: while workgroups are left for three on each compute unit.
+  sh.each = 1;
+  while (sh.each < 8 && groups * sh.ks / kWaves / (2 * sh.each) >= 3 * 256) sh.each *= 2;
+  const int round = sh.ks * kPieceK<W>;
+  const int keep = rows <= 4 ? 4 : 16;
+  sh.lds = act_bytes<A>(Tile{keep, tile_values<A>(keep, K, round, 48 * 1024)});
+  return sh;
+}
+template <class Kernel>
+hipError_t launch_experts(Kernel kern, const MoeProblem &p, MoeShape sh, int columns, hipStream_t s) {
   const int pairs = p.T * p.top;
-  const long long experts = p.E < pairs ? p.E : pairs, cols = p.at.pitch / 16;
-  // Waves per unit: neighbours read neighbouring pieces of the same rows.
-  int ks = 1;
-  while (ks < kUpWaves && 2 * ks * kPieceK<W> <= p.H) ks *= 2;
-  const dim3 grid((unsigned)ceil_div(cols * ks, kUpWaves), (unsigned)experts);
-  return launch_kernel(p.T <= kFusedTokens ? moe_up_kernel<W, AF, true, ODD>
-                                           : moe_up_kernel<W, AF, false, ODD>,
-                       grid, dim3(64 * kUpWaves), s, p, ks);
+  MoeProblem q = p;
+  void *args[] = {&q, &sh};
+  const dim3 grid((unsigned)ceil_div(ceil_div(columns, 16), kWaves / sh.ks * sh.each),
+                  (unsigned)(p.E < pairs ? p.E : pairs));
+  return hipLaunchKernel(reinterpret_cast<const void *>(kern), grid, dim3(kThreads), args,
+                         (size_t)sh.lds, s);
 }
 
-template <int W, int WAVES, bool ODD>
-hipError_t launch_down_waves(const MoeProblem &p, hipStream_t s) {
-  MoeProblem q = p;
-  void *args[] = {&q};
-  return hipLaunchKernel(reinterpret_cast<const void *>(moe_down_kernel<W, WAVES, ODD>),
-                         dim3((unsigned)ceil_div(p.H, 16)), dim3(64 * WAVES), args,
-                         (size_t)down_lds(WAVES, p.T, p.E, p.top).bytes, s);
+template <int W, int AF, bool ODD>
+hipError_t launch_up(const MoeProblem &p, hipStream_t s) {
+  const long long experts = p.E < p.T * p.top ? p.E : p.T * p.top;
+  return launch_experts(p.T <= kFusedTokens ? moe_up_kernel<W, AF, true, ODD>
+                                            : moe_up_kernel<W, AF, false, ODD>,
+                        p, shape_of<W, AF>(experts, p.I, p.H, p.T), p.I, s);
 }
 template <int W, bool ODD>
 hipError_t launch_down(const MoeProblem &p, hipStream_t s) {
-  return p.T <= 64 ? launch_down_waves<W, 16, ODD>(p, s) : launch_down_waves<W, 8, ODD>(p, s);
+  const long long experts = p.E < p.T * p.top ? p.E : p.T * p.top;
+  return launch_experts(moe_down_kernel<W, ODD>, p, shape_of<W, kF32>(experts, p.H, p.I, p.T), p.H,
+                        s);
 }
 
 // Whether a product's 16-bit rows are to be read by whole words (Eight<true>):
@@ -527,11 +520,16 @@ hipError_t launch_moe(const MoeProblem &p, hipStream_t s) {
   hipError_t e = bf16 ? launch_logits<kBf16>(p, s) : launch_logits<kF16>(p, s);
   if (e != hipSuccess) return e;
   if (p.T > kFusedTokens) {
-    e = launch_kernel(moe_route_kernel, dim3(1), dim3(kRouteThreads), s, p);
+    e = launch_kernel(moe_choose_kernel, dim3((unsigned)ceil_div(p.T, kChooseTokens)),
+                      dim3(64 * kChooseTokens), s, p);
+    if (e == hipSuccess) e = launch_kernel(moe_list_kernel, dim3(1), dim3(kListThreads), s, p);
     if (e != hipSuccess) return e;
   }
-  if (p.mx) return bf16 ? launch_products<kMx, kBf16>(p, s) : launch_products<kMx, kF16>(p, s);
-  return bf16 ? launch_products<kBf16, kBf16>(p, s) : launch_products<kF16, kF16>(p, s);
+  e = p.mx ? (bf16 ? launch_products<kMx, kBf16>(p, s) : launch_products<kMx, kF16>(p, s))
+           : (bf16 ? launch_products<kBf16, kBf16>(p, s) : launch_products<kF16, kF16>(p, s));
+  if (e != hipSuccess) return e;
+  return launch_kernel(moe_sum_kernel, dim3((unsigned)ceil_div(p.H, 1024), (unsigned)p.T), dim3(256),
+                       s, p);
 }
 
 }  // namespace gemm_f32_impl

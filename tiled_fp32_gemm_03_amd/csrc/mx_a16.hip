@@ -8,30 +8,6 @@
 namespace gemm_f32_impl {
 namespace {
 
-// C's blocks [i][b] of all waves, summed and stored, four blocks at a time.
-template <int WAVES, int MB, int NB>
-__device__ __forceinline__ void thin_store(const f32x4 (&acc)[MB][NB], f32x4 (*part)[4][64],
-                                           long long m0, long long n0, int M, int N, void *C,
-                                           long long ldc, int c_format) {
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  constexpr int kBlocks = MB * NB, kRound = kBlocks < 4 ? kBlocks : 4;
-#pragma unroll
-  for (int r = 0; r < kBlocks; r += kRound) {
-#pragma unroll
-    for (int q = 0; q < kRound; ++q) part[wave][q][lane] = acc[(r + q) / NB][(r + q) % NB];
-    __syncthreads();
-    if (wave < kRound) {
-      f32x4 sum = part[0][wave][lane];
-#pragma unroll
-      for (int w = 1; w < WAVES; ++w) sum += part[w][wave][lane];
-      const long long m = m0 + 16 * ((r + wave) / NB) + (lane & 15);
-      const long long n = n0 + 16 * ((r + wave) % NB) + 4 * (lane >> 4), left = N - n;
-      if (m < M) store4_fmt(c_format, C, m * ldc + n, (int)(left < 4 ? left : 4), sum);
-    }
-    __syncthreads();
-  }
-}
-
 // A's rows: 16-bit values, or MX rows (a_scales not null).
 struct ThinProblem {
   int M, N, K;
@@ -45,64 +21,78 @@ struct ThinProblem {
   int c_format;
 };
 
-template <int A, int MB, int NB, int WAVES, bool ODD>
-__global__ void __launch_bounds__(64 * WAVES) mx_thin_kernel(ThinProblem p) {
-  __shared__ f32x4 part[WAVES][4][64];
+// LDS for activations: what leaves room for two workgroups, and the most that
+// one round of pieces may take.
+constexpr int kThinLds = 64 * 1024, kThinMostLds = 140 * 1024;
+
+// ks: the waves that share 16 columns.
+template <int A, int MB, int WAVES, bool ODD>
+__global__ void __launch_bounds__(64 * WAVES) mx_thin_kernel(ThinProblem p, Tile tile, int ks) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  typedef Thin<kMx, A, MB, 1, ODD> Product;
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const int l16 = lane & 15;
-  const long long n0 = 16LL * NB * blockIdx.x;
-  Rows w[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    auto row = [&](int r) { return n0 + 16 * b + r < p.N ? n0 + 16 * b + r : p.N - 1; };
-#pragma unroll
-    for (int t = 0; t < 4; ++t) w[b].p[t] = p.B.codes + row(load_row(lane, t)) * p.B.ld;
-    w[b].q = p.B.scales + row(l16) * p.B.lds;
-  }
+  const int l16 = lane & 15, g = lane >> 4;
+  const long long n0 = 16LL * (blockIdx.x * (WAVES / ks) + wave / ks);
+  const long long n = n0 + l16 < p.N ? n0 + l16 : p.N - 1;
+  const Row w[1] = {{p.B.codes + n * p.B.ld, p.B.scales + n * p.B.lds}};
+  const typename Product::Walk at{wave & (ks - 1), ks, n0 < p.N, false};
+  typename Product::Weights x;
+  Product::load_first(x, w, at, p.K, lane);
   for (long long m0 = 16LL * MB * blockIdx.y; m0 < p.M; m0 += 16LL * MB * gridDim.y) {
-    typename ActRow<A>::type a[MB];
-    bool valid[MB];
+    Product t;
+    t.clear();
+    const int rows = (int)(p.M - m0 < 16 * MB ? p.M - m0 : 16 * MB);
+    t.template run<64 * WAVES>(
+        lds, tile, [&](int r) { return Row{p.A + (m0 + r) * p.lda, p.SA + (m0 + r) * p.ldsa}; },
+        rows, w, w, x, at, p.K, lane);
+    if (ks > 1) {  // the waves' sums, added in wave order
+      f32x4 *part = reinterpret_cast<f32x4 *>(lds);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < MB; ++i) part[(i * WAVES + wave) * 64 + lane] = t.acc[i][0];
+      __syncthreads();
+      if (at.first == 0)
+        for (int q = 1; q < ks; ++q)
+#pragma unroll
+          for (int i = 0; i < MB; ++i) t.acc[i][0] += part[(i * WAVES + wave + q) * 64 + lane];
+    }
+    if (at.first != 0 || !at.any) continue;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      auto row = [&](int r) { return m0 + 16 * i + r < p.M ? m0 + 16 * i + r : p.M - 1; };
-      if constexpr (A == kMx) {
-        valid[i] = m0 + 16 * i + load_row(lane, 0) < p.M;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) a[i].p[t] = p.A + row(load_row(lane, t)) * p.lda;
-        a[i].q = p.SA + row(l16) * p.ldsa;
-      } else {
-        valid[i] = m0 + 16 * i + l16 < p.M;
-        a[i] = {p.A + row(l16) * p.lda, nullptr};
-      }
+      const int r = 16 * i + l16;
+      if (r >= rows) continue;
+      const long long col = n0 + 4 * g, left = p.N - col;
+      store4_fmt(p.c_format, p.C, (m0 + r) * p.ldc + col, (int)(left < 4 ? left : 4), t.acc[i][0]);
     }
-    Thin<kMx, A, MB, NB, ODD> t;
-    t.clear();
-    t.run(a, valid, w, wave, WAVES, p.K, lane);
-    thin_store<WAVES, MB, NB>(t.acc, part, m0, n0, p.M, p.N, p.C, p.ldc, p.c_format);
   }
 }
 
-template <int A, int MB, int NB, bool ODD>
-hipError_t launch_thin_blocks(const ThinProblem &p, hipStream_t s) {
-  const long long gy = ceil_div(p.M, 16 * MB);
-  const dim3 grid((unsigned)ceil_div(p.N, 16 * NB), (unsigned)(gy < kMaxGridY ? gy : kMaxGridY));
-  if (p.K <= 4 * kPieceK<kMx>)
-    return launch_kernel(mx_thin_kernel<A, MB, NB, 4, ODD>, grid, dim3(256), s, p);
-  return launch_kernel(mx_thin_kernel<A, MB, NB, 8, ODD>, grid, dim3(512), s, p);
+template <int A, int MB, int WAVES, bool ODD>
+hipError_t launch_thin_waves(const ThinProblem &p, int ks, int keep, hipStream_t s) {
+  const long long groups = ceil_div(p.N, 16), gy = ceil_div(p.M, 16 * MB);
+  Tile tile{keep, tile_values<A>(keep, p.K, ks * kPieceK<kMx>, kThinLds / MB)};
+  const int bytes = MB * act_bytes<A>(tile), parts = ks > 1 ? MB * WAVES * 1024 : 0;
+  const dim3 grid((unsigned)ceil_div(groups * ks, WAVES),
+                  (unsigned)(gy < kMaxGridY ? gy : kMaxGridY));
+  ThinProblem q = p;
+  void *args[] = {&q, &tile, &ks};
+  return hipLaunchKernel(reinterpret_cast<const void *>(mx_thin_kernel<A, MB, WAVES, ODD>), grid,
+                         dim3(64 * WAVES), args, (size_t)(bytes > parts ? bytes : parts), s);
+}
+
+template <int A, int MB, bool ODD>
+hipError_t launch_thin_rows(const ThinProblem &p, hipStream_t s) {
+  const long long groups = ceil_div(p.N, 16);
+  const int keep = p.M <= 4 ? 4 : 16;
+  int ks = waves_per_group(groups, p.K, kPieceK<kMx>, 8, 8 * 256);
+  while (ks > 1 && MB * act_bytes<A>(Tile{keep, ks * kPieceK<kMx>}) > kThinMostLds) ks /= 2;
+  return ks == 8 || groups * ks >= 8 * 256 ? launch_thin_waves<A, MB, 8, ODD>(p, ks, keep, s)
+                                           : launch_thin_waves<A, MB, 4, ODD>(p, ks, keep, s);
 }
 
 template <int A, bool ODD>
 hipError_t launch_thin(const ThinProblem &p, hipStream_t s) {
-  // Columns per workgroup: as many as leave a workgroup per compute unit.
-  const long long cols = ceil_div(p.N, 16);
-  const int nb = cols >= 4 * 256 ? 4 : cols >= 2 * 256 ? 2 : 1;
-  if (p.M <= 16)
-    return nb == 4   ? launch_thin_blocks<A, 1, 4, ODD>(p, s)
-           : nb == 2 ? launch_thin_blocks<A, 1, 2, ODD>(p, s)
-                     : launch_thin_blocks<A, 1, 1, ODD>(p, s);
-  return nb == 4   ? launch_thin_blocks<A, 2, 4, ODD>(p, s)
-         : nb == 2 ? launch_thin_blocks<A, 2, 2, ODD>(p, s)
-                   : launch_thin_blocks<A, 2, 1, ODD>(p, s);
+  return p.M <= 16 ? launch_thin_rows<A, 1, ODD>(p, s) : launch_thin_rows<A, 2, ODD>(p, s);
 }
 
 // Rows that start in the middle of a word, of a matrix that starts on one.

@@ -137,7 +137,7 @@ extern "C" int gemm_mx_a16(int M, int N, int K, const void *A, int lda, int a_fo
 // ---- the mixture-of-experts layer ----------------------------------------------
 
 extern "C" long long gemm_moe_workspace_bytes(int T, int E, int top, int H, int I) {
-  return moe_check_sizes(T, E, top, H, I) == kOk ? moe_space(T, E, top, I).bytes : -1;
+  return moe_check_sizes(T, E, top, H, I) == kOk ? moe_space(T, E, top, H, I).bytes : -1;
 }
 
 extern "C" int gemm_moe(int T, int E, int top, int H, int I, const void *X, int ldx,
@@ -169,7 +169,7 @@ extern "C" int gemm_moe(int T, int E, int top, int H, int I, const void *X, int 
   if (rc == kOk && ids != nullptr) rc = check_plain_pointer(ids, kF32);
   if (rc == kOk && gates != nullptr) rc = check_plain_pointer(gates, kF32);
   if (rc != kOk) return rc;
-  const MoeSpace at = moe_space(T, E, top, I);
+  const MoeSpace at = moe_space(T, E, top, H, I);
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15) != 0 ||
       workspace_bytes < at.bytes)
     return GEMM_F32_BAD_WORKSPACE;

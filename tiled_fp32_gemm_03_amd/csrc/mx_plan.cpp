@@ -56,7 +56,7 @@ int moe_check_sizes(int T, int E, int top, int H, int I) {
   return kOk;
 }
 
-MoeSpace moe_space(int T, int E, int top, int I) {
+MoeSpace moe_space(int T, int E, int top, int H, int I) {
   MoeSpace w;
   long long at = 0;
   const long long pairs = (long long)T * top;
@@ -65,17 +65,16 @@ MoeSpace moe_space(int T, int E, int top, int I) {
     at += ceil_div(bytes, 16) * 16;
     return from;
   };
-  w.pitch = ceil_div(I, 512) * 512;
+  w.upitch = ceil_div(I, 8) * 8;
+  w.ypitch = ceil_div(H, 4) * 4;
   w.logits = take(8LL * T * E);
+  w.ids = take(4 * pairs);
   w.gates = take(4 * pairs);
   w.start = take(4LL * (E + 1));
-  w.ufirst = take(4LL * E);
   w.list = take(4 * pairs);
   w.active = take(4LL * (E + 1));
-  const long long chosen = E < pairs ? E : pairs;  // at most
-  const long long urows = ceil_div(pairs + 3 * chosen, 4) * 4;
-  w.hi = take(2 * urows * w.pitch);
-  w.lo = take(2 * urows * w.pitch);
+  w.u = take(4 * pairs * w.upitch);
+  w.part = take(4 * pairs * w.ypitch);
   w.bytes = at;
   return w;
 }

@@ -45,21 +45,21 @@ constexpr int kMoeMaxTokens = 256, kMoeMaxExperts = 512, kMoeMaxTop = 16,
               kMoeMaxWidth = 1 << 24;
 int moe_check_sizes(int T, int E, int top, int H, int I);
 
-// The workspace of one call, as byte offsets (each a multiple of 16).  The
-// inner values u are kept as two planes of bf16, hi and lo, with a row per
-// (token, choice) pair: an expert's rows in the order of `list`, its first on
-// a multiple of 4 (`ufirst`), `pitch` values each, zeros past I.
+// The workspace of one call, as byte offsets (each a multiple of 16).  A pair
+// is a token's choice, number token * top + choice; `list` has the pairs by
+// expert, then by number.
 struct MoeSpace {
   long long logits;  // double [T][E]
+  long long ids;     // int [T top]
   long long gates;   // float [T top]
   long long start;   // int [E + 1]: expert e's pairs are list[start[e]] .. list[start[e + 1] - 1]
-  long long ufirst;  // int [E]
-  long long list;    // int [T top]: pairs (token * top + choice), by expert, then by pair
+  long long list;    // int [T top]
   long long active;  // int [1 + E]: how many experts were chosen, and which, rising
-  long long hi, lo;  // bf16 [urows][pitch]
+  long long u;       // float [T top][upitch], by place in the list: the inner values
+  long long part;    // float [T top][ypitch], by pair: the experts' results
   long long bytes;
-  long long pitch;
+  long long upitch, ypitch;
 };
-MoeSpace moe_space(int T, int E, int top, int I);
+MoeSpace moe_space(int T, int E, int top, int H, int I);
 
 }  // namespace gemm_f32_impl

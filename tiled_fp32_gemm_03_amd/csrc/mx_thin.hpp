@@ -4,26 +4,21 @@
 //
 // A wave multiplies blocks of 16 activation rows with blocks of 16 weight
 // rows ("columns" of C) and takes K in pieces of 256 bytes of weight row:
-// four 128-deep steps of MX weights, one of 16-bit ones.  A piece's weights
-// are loaded at once, the activations step by step, a step ahead of their
-// use.
+// four 128-deep steps of MX weights, one of 16-bit ones.  The weights go from
+// memory into registers, the next piece's while one is used; the activations,
+// which a workgroup's waves share, wait in LDS.  Loads complete in order, so
+// activations loaded from memory between the pieces would make each wave wait
+// for the next piece's weights as well (measured: twice the time), and four
+// lanes that read four rows cost the L1 four accesses, of which 16-bit
+// activations would need four times what MX weights do.
 //
-// The matrix instructions want lane l to hold row l % 16, but four
-// neighbouring lanes that read four rows cost the L1 four accesses where
-// four that read 64 bytes of one row cost it one, and the L1's accesses were
-// what bounded these kernels (a second product of 143 MB took 70 us with 21
-// accesses per load).  So lane l loads 16 bytes number l % 4 (of group g = l /
-// 16) of rows 4 (l / 4 % 4) + t, t = 0 .. 3, and a 4 x 4 transpose inside each
-// four lanes brings row l % 16's four into the lane: 32 ALU operations per
-// 4 KB.  Lane l then holds 64 consecutive bytes of its row, which decides the
-// order of k (any order is as good as both operands agree):
-//   MX weights: blocks 4 g + s of a piece's 16, s its step; MFMA j takes the
-//     block's values 8 j .. 8 j + 7, widened with their scale (exact: an
+// Lane l holds row l % 16 of each operand; which k a lane holds is free as
+// long as both operands agree, so it follows how the weights are stored, with
+// g = l / 16:
+//   MX weights: load s of a piece is block 4 s + g of it; MFMA j of step s
+//     takes its values 8 j .. 8 j + 7, widened with their scale (exact: an
 //     element has two significant bits);
-//   16-bit weights: MFMA j takes k = 32 g + 8 j .. + 7.
-// The activations are read as their lanes hold them, valid rows alone; with
-// few rows that is few accesses.  The layer's inner values, which its first
-// product writes for its second, are kept in the order of these loads.
+//   16-bit weights: load j is k = 32 j + 8 g .. + 7, the operand of MFMA j.
 #pragma once
 
 #include "mx_values.hpp"
@@ -33,32 +28,9 @@
 namespace gemm_f32_impl {
 namespace {
 
-// Kinds of operands: the formats of mx_plan.hpp, MX rows, and activations
-// kept as a sum of two bf16 terms.
-constexpr int kMx = 3, kSplit = 4;
-
-// Where lane l loads 16 rows of weights: rows 4 (l / 4 % 4) + t, as 2-byte
-// values or MX codes, and the scales of row l % 16 (MX).
-struct Rows {
-  const unsigned char *p[4];
-  const unsigned char *q;
-};
-// Activations: the lane's row l % 16 of 2-byte values; of MX rows as weights;
-// of a split operand the lane's place in its two planes.
-struct Row {
-  const unsigned char *p;
-  const unsigned char *q;
-};
-template <int A>
-struct ActRow {
-  typedef Row type;
-};
-template <>
-struct ActRow<kMx> {
-  typedef Rows type;
-};
-// Row t of those that this lane loads, and the row it holds.
-__device__ inline int load_row(int lane, int t) { return (lane & 12) + t; }
+// Kinds of operands: the formats of mx_plan.hpp (kF32: activations split into
+// two bf16 terms, hi + lo, 16 significant bits), and MX rows.
+constexpr int kMx = 3;
 
 template <int W>
 constexpr int kPieceK = W == kMx ? 512 : 128;
@@ -91,40 +63,53 @@ __device__ inline void split_f16(u32x4 x, u32x4 &hi, u32x4 &lo) {
   lo = __builtin_bit_cast(u32x4, l);
 }
 
-// The 4 x 4 transpose inside each four lanes: lane i's r[t] goes to lane t's
-// r[i].
-template <int CTRL>
-__device__ inline uint32_t quad(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
-}
-__device__ __forceinline__ void quad_transpose(u32x4 (&r)[4], int lane) {
-  const bool odd = lane & 1, high = lane & 2;
+// hi + lo of 8 fp32 values, 16 significant bits; an infinity or a NaN is hi
+// alone.
+__device__ inline void split_f32(u32x4 a, u32x4 b, u32x4 &hi, u32x4 &lo) {
 #pragma unroll
-  for (int d = 0; d < 4; ++d) {
+  for (int i = 0; i < 4; ++i) {
+    float h[2], l[2];
 #pragma unroll
-    for (int t = 0; t < 4; t += 2) {  // lanes i, i ^ 1 and registers t, t + 1
-      const uint32_t a = r[t][d], b = r[t + 1][d], fa = quad<0xB1>(a), fb = quad<0xB1>(b);
-      r[t][d] = odd ? fb : a;
-      r[t + 1][d] = odd ? b : fa;
+    for (int q = 0; q < 2; ++q) {
+      const float v = __builtin_bit_cast(float, i < 2 ? a[2 * i + q] : b[2 * i + q - 4]);
+      h[q] = (float)(__bf16)v;
+      l[q] = mag_bits(h[q]) < 0x7f800000u ? v - h[q] : 0.f;
     }
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {  // lanes i, i ^ 2 and registers t, t + 2
-      const uint32_t a = r[t][d], b = r[t + 2][d], fa = quad<0x4E>(a), fb = quad<0x4E>(b);
-      r[t][d] = high ? fb : a;
-      r[t + 2][d] = high ? b : fa;
-    }
+    hi[i] = pack2<kBf16>(h[0], h[1]);
+    lo[i] = pack2<kBf16>(l[0], l[1]);
   }
 }
 
-// 8 values of a row of 16-bit codes from k, the first `n` of them (others 0).
-__device__ inline u32x4 load_guarded(const unsigned char *row, long long k, long long n) {
-  const uint16_t *p = reinterpret_cast<const uint16_t *>(row) + k;
-  if (n >= 8) return *reinterpret_cast<const u32x4h *>(p);
-  u32x4 w{0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-  return w;
+// Values k .. k + 7 of a row of K 16-bit codes, zeros past K: the eight that
+// end at K at the latest, moved into place.  (One load and a shift: guarded
+// element loads, inlined everywhere, made kernels of 60 KB that spent their
+// time on fetching instructions.)
+__device__ inline u32x4 load_guarded(const unsigned char *row, long long k, int K) {
+  const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
+  uint64_t lo = 0, hi = 0;
+  if (K >= 8) {
+    const long long from = k < K - 8 ? k : K - 8;
+    const u32x4 v = *reinterpret_cast<const u32x4h *>(p + from);
+    lo = v[0] | (uint64_t)v[1] << 32;
+    hi = v[2] | (uint64_t)v[3] << 32;
+    const long long drop = k - from;  // values before k
+    const int bits = drop < 8 ? (int)drop * 16 : 128;
+    if (bits >= 64) {
+      lo = bits < 128 ? hi >> (bits - 64) : 0;
+      hi = 0;
+    } else if (bits > 0) {
+      lo = lo >> bits | hi << (64 - bits);
+      hi >>= bits;
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; k + i < K; ++i) {
+      const uint64_t v = (uint64_t)p[k + i] << (16 * (i & 3));
+      if (i < 4) lo |= v;
+      else hi |= v;
+    }
+  }
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 // 8 values of a row of 16-bit codes.  ODD: rows that may start in the middle
@@ -168,30 +153,6 @@ struct Eight<true> {
   }
 };
 
-// A piece of 16 MX rows: after `turn`, lane l holds blocks 16 piece + 4 g + s of
-// row l % 16 and their scales, byte s of the word.  Blocks past the row's are
-// read from its last; mask makes them zeros with scale 1.
-struct MxPiece {
-  u32x4 c[4];
-  uint32_t s;
-  __device__ __forceinline__ void load(const Rows &r, int piece, int lane, int nb) {
-    const int kb = 16 * piece + 4 * (lane >> 4) + (lane & 3), in = kb < nb ? kb : nb - 1;
-    s = *reinterpret_cast<const uint32_t *>(r.q + 16LL * piece + 4 * (lane >> 4));
-#pragma unroll
-    for (int t = 0; t < 4; ++t) c[t] = *reinterpret_cast<const u32x4 *>(r.p[t] + 16LL * in);
-  }
-  __device__ __forceinline__ void turn(int lane) { quad_transpose(c, lane); }
-  __device__ __forceinline__ void mask(int piece, int lane, int nb) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (16 * piece + 4 * (lane >> 4) + i >= nb) {
-        c[i] = u32x4{0, 0, 0, 0};
-        s = (s & ~(255u << (8 * i))) | 127u << (8 * i);
-      }
-  }
-  __device__ __forceinline__ uint32_t scale(int i) const { return (s >> (8 * i)) & 255u; }
-};
-
 // How the values of MX weights become matrix operands.  As bf16 or fp16 by
 // one conversion per two values where every scale of the piece allows it:
 // bf16 holds every element under scale bytes 1 to 254 (0.5 2^-126 is a
@@ -223,66 +184,169 @@ __device__ inline u32x4 widen(uint32_t codes, uint32_t sb) {
                  pack2<kBf16>(v[6], v[7])};
   }
 }
-// Whether all of a lane's blocks allow it (blocks of zeros allow any).
-template <uint32_t LOW, uint32_t HIGH>
-__device__ inline bool scales_within(const MxPiece &x) {
-  bool ok = true;
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const u32x4 c = x.c[s];
-    const uint32_t sb = x.scale(s);
-    ok &= sb - LOW <= HIGH - LOW || (sb != 255 && (c[0] | c[1] | c[2] | c[3]) == 0);
-  }
-  return ok;
-}
 
 // The wave's number in its workgroup, as a scalar.
 __device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// Four 16-byte parts of 16-bit rows: 64 consecutive bytes of row l % 16 after
-// `turn`, from byte `at` of group g = 0 on.
-template <bool ODD>
-struct Half {
-  Eight<ODD> e[4];
-  u32x4 v[4];
-  __device__ __forceinline__ void load(const unsigned char *const (&p)[4], long long at) {
+// ---- weights -----------------------------------------------------------------
+
+// The lane's row of weights: 2-byte values or MX codes, and MX scales.
+struct Row {
+  const unsigned char *p;
+  const unsigned char *q;
+};
+
+// A piece of an MX row as it is stored: blocks 16 piece + 4 s + g and the 16
+// scales.  Blocks past the row's are read from its last; mask makes them
+// zeros with scale 1.
+struct MxPiece {
+  u32x4 c[4];
+  u32x4 s;
+  __device__ __forceinline__ void load(const Row &r, int piece, int g, int nb) {
+    s = *reinterpret_cast<const u32x4 *>(r.q + 16LL * piece);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) e[t].load(p[t] + at);
+    for (int i = 0; i < 4; ++i) {
+      const int kb = 16 * piece + 4 * i + g < nb ? 16 * piece + 4 * i + g : nb - 1;
+      c[i] = *reinterpret_cast<const u32x4 *>(r.p + 16LL * kb);
+    }
   }
-  // Values k .. k + 7 of each row as far as they are below K, else 0.
-  __device__ __forceinline__ void load_tail(const unsigned char *const (&p)[4], long long k, int K) {
+  __device__ __forceinline__ void mask(int piece, int g, int nb) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) e[t].set(load_guarded(p[t], k, K - k), p[t]);
+    for (int i = 0; i < 4; ++i)
+      if (16 * piece + 4 * i + g >= nb) {
+        c[i] = u32x4{0, 0, 0, 0};
+        s[i] = 0x7f7f7f7fu;
+      }
   }
-  __device__ __forceinline__ void turn(const unsigned char *const (&p)[4], int lane) {
+  // Lane group g's scale byte of step i.
+  __device__ __forceinline__ uint32_t scale(int i, int g) const { return (s[i] >> (8 * g)) & 255u; }
+  // Whether all of the lane's blocks have scales within (blocks of zeros allow any).
+  template <uint32_t LOW, uint32_t HIGH>
+  __device__ __forceinline__ bool within(int g) const {
+    bool ok = true;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) v[t] = e[t].get(p[t]);
-    quad_transpose(v, lane);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t sb = scale(i, g);
+      ok &= sb - LOW <= HIGH - LOW || (sb != 255 && (c[i][0] | c[i][1] | c[i][2] | c[i][3]) == 0);
+    }
+    return ok;
   }
 };
 
-// Split activations (two bf16 planes, hi and lo): 4 rows together, in the
-// order of the second product's loads.  For a load (piece, step, MFMA j) and
-// 4 rows: 256 bytes, lane group g's 64 at 64 g, row r's 16 at 16 (r % 4).
-// Values per row are padded with zeros to whole pieces (`pitch`).
-template <int W>
-__device__ inline long long split_at(int row, int k, long long pitch) {
-  const int kSteps = kPieceSteps<W>;
-  const int piece = k / kPieceK<W>, in = k % kPieceK<W>;
-  const int g = in / (32 * kSteps), s = in / 32 % kSteps, j = in / 8 % 4, b = in % 8;
-  return 2 * ((row >> 2) * 4 * pitch) + ((piece * kSteps + s) * 4 + j) * 256LL + 64 * g +
-         16 * (row & 3) + 2 * b;
+// ---- activations in LDS --------------------------------------------------------
+//
+// Blocks of up to 16 rows, `rows` of them kept (4 or 16), of kc values: for
+// each operand of a matrix instruction (piece, step, MFMA j) and lane group,
+// the rows' 16 bytes one after the other, and 16 bytes of padding, so that
+// neither the writes (neighbouring threads take neighbouring k of a row) nor
+// the reads (16 lanes take 16 rows) meet on a bank.  kF32: a second such
+// plane for lo.  MX rows: one operand is a block; the scales follow, a byte
+// per block and row.
+
+struct Tile {
+  int rows, kc;
+  __host__ __device__ int group() const { return 16 * rows + 16; }
+};
+// LDS bytes of a block of rows of kind A: linear in kc (whole pieces).
+template <int A>
+__host__ __device__ inline int act_bytes(const Tile &t) {
+  return A == kMx ? t.kc / 32 * (t.group() + t.rows)
+                  : t.kc / 8 * t.group() * (A == kF32 ? 2 : 1);
 }
 
-// One product of thin operands: MB blocks of 16 rows of kind A by NB blocks
-// of 16 rows of weights of kind W.
-template <int W, int A, int MB, int NB, bool ODD = false>
+// Fills a block with values k0 .. k0 + kc - 1 of rows 0 .. n - 1, zeros past K;
+// `row(r)` gives row r's start (for MX its codes and scales).  All THREADS
+// threads of the workgroup take part; each issues four loads before it writes
+// any (one at a time, their latencies alone took 30 us of a first product).
+// Rows of kind kF32 hold zeros from K to a multiple of 8.
+template <int A, int W, bool ODD, int THREADS, class RowOf>
+__device__ __forceinline__ void stage_acts(unsigned char *lds, const Tile &t, RowOf row, int n,
+                                           int k0, int K) {
+  constexpr int kBatch = 4;
+  const int G = t.group();
+  const int per = t.kc / (A == kMx ? 32 : 8), all = n * per;
+  const int nb = (int)mx_blocks(K), eights = (int)ceil_div(K, 8);
+  unsigned char *scales = lds + per * G;  // kMx
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < all; i0 += kBatch * THREADS) {
+    u32x4 c[kBatch], d[kBatch];
+    unsigned char sb[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * THREADS < all ? i0 + u * THREADS : all - 1;
+      const int r = i / per, x = i % per;
+      const Row src = row(r);
+      if constexpr (A == kMx) {
+        const int kb = k0 / 32 + x, in = kb < nb ? kb : nb - 1;
+        c[u] = *reinterpret_cast<const u32x4 *>(src.p + 16LL * in);
+        sb[u] = src.q[in];
+      } else if constexpr (A == kF32) {
+        const int e = k0 / 8 + x, in = e < eights ? e : eights - 1;
+        const u32x4w *q = reinterpret_cast<const u32x4w *>(src.p + 32LL * in);
+        c[u] = q[0];
+        d[u] = q[1];
+      } else {
+        const long long k = k0 + 8LL * x;
+        if constexpr (ODD) {
+          if (k + 8 <= K) {
+            Eight<true> v;
+            v.load(src.p + 2 * k);
+            c[u] = v.v;
+            d[u][0] = v.last;
+          }
+        } else if (k + 8 <= K) {
+          c[u] = *reinterpret_cast<const u32x4h *>(src.p + 2 * k);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * THREADS;
+      if (i >= all) continue;
+      const int r = i / per, x = i % per;
+      if constexpr (A == kMx) {
+        const bool in = k0 / 32 + x < nb;
+        *reinterpret_cast<u32x4 *>(lds + x * G + 16 * r) = in ? c[u] : u32x4{0, 0, 0, 0};
+        scales[x * t.rows + r] = in ? sb[u] : 127;
+      } else {
+        // Operand and lane group of values 8 x .. 8 x + 7: the MX order of k
+        // is (step, g, j), the 16-bit one (j, g).
+        const int group = W == kMx ? (x & ~15) | (x & 3) << 2 | (x >> 2 & 3) : x;
+        u32x4 *to = reinterpret_cast<u32x4 *>(lds + group * G + 16 * r);
+        if constexpr (A == kF32) {
+          const bool in = k0 / 8 + x < eights;
+          u32x4 hi, lo;
+          split_f32(c[u], d[u], hi, lo);
+          *to = in ? hi : u32x4{0, 0, 0, 0};
+          *reinterpret_cast<u32x4 *>(lds + per * G + group * G + 16 * r) =
+              in ? lo : u32x4{0, 0, 0, 0};
+        } else {
+          const long long k = k0 + 8LL * x;
+          if (k + 8 > K) {
+            c[u] = load_guarded(row(r).p, k < K ? k : K, K);
+          } else if constexpr (ODD) {
+            Eight<true> v;
+            v.v = c[u];
+            v.last = d[u][0];
+            c[u] = v.get(row(r).p);
+          }
+          *to = c[u];
+        }
+      }
+    }
+  }
+}
+
+// ---- the product -----------------------------------------------------------------
+
+// MB blocks of rows of kind A in LDS by NB blocks of 16 rows of weights of
+// kind W in registers.
+template <int W, int A, int MB, int NB, bool ODD>
 struct Thin {
   static constexpr int kK = kPieceK<W>, kSteps = kPieceSteps<W>;
-  typedef typename ActRow<A>::type Act;
   struct Weights {
     MxPiece mx[W == kMx ? NB : 1];
-    Half<ODD> half[W == kMx ? 1 : NB];
+    Eight<ODD> half[W == kMx ? 1 : NB][4];
   };
   f32x4 acc[MB][NB];
 
@@ -293,155 +357,188 @@ struct Thin {
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // A piece's weights; with TAIL it may reach past K.
-  template <bool TAIL>
-  static __device__ __forceinline__ void load_weights(Weights &x, const Rows (&w)[NB], int piece,
-                                                      int lane, int K, int nb) {
-    const long long k = (long long)kK * piece + 32 * (lane >> 4) + 8 * (lane & 3);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if constexpr (W == kMx) x.mx[b].load(w[b], piece, lane, nb);
-      else if constexpr (TAIL) x.half[b].load_tail(w[b].p, k, K);
-      else x.half[b].load(w[b].p, 2 * k);
-    }
-  }
-  template <bool TAIL>
-  static __device__ __forceinline__ void turn_weights(Weights &x, const Rows (&w)[NB], int piece,
-                                                      int lane, int nb) {
+  // A piece's weights, zeros past K.
+  static __device__ __forceinline__ void load(Weights &x, const Row (&w)[NB], int piece, int g,
+                                              int K) {
+    const int nb = (int)mx_blocks(K);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if constexpr (W == kMx) {
-        x.mx[b].turn(lane);
-        if constexpr (TAIL) x.mx[b].mask(piece, lane, nb);
+        x.mx[b].load(w[b], piece, g, nb);
       } else {
-        x.half[b].turn(w[b].p, lane);
+        const long long k0 = (long long)kK * piece + 8 * g;
+        if (piece < K / kK) {  // uniform
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x.half[b][j].load(w[b].p + 2 * (k0 + 32 * j));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const long long k = k0 + 32 * j;
+            x.half[b][j].set(load_guarded(w[b].p, k < K ? k : K, K), w[b].p);
+          }
+        }
       }
     }
   }
 
-  // The products of a piece whose weights are loaded and turned, with the
-  // activation rows that `valid` has.
-  template <bool TAIL>
-  __device__ __forceinline__ void use(const Weights &x, const Act (&a)[MB],
-                                      const bool (&valid)[MB], int piece, int lane, int K, int nb) {
-    if constexpr (A == kMx) {
-      MxPiece y[MB];
+  // The products of a loaded piece, number `local` of the tile.
+  __device__ __forceinline__ void use(Weights &x, const Row (&w)[NB], const unsigned char *lds,
+                                      const Tile &t, int local, int piece, int lane, int K) {
+    const int g = lane >> 4, r = lane & (t.rows - 1), G = t.group(), block = act_bytes<A>(t);
+    if constexpr (W == kMx) {
+      if ((long long)kK * (piece + 1) > K) {  // uniform
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        if (valid[i]) y[i].load(a[i], piece, lane, nb);
-        y[i].turn(lane);
-        if constexpr (TAIL) y[i].mask(piece, lane, nb);
+        for (int b = 0; b < NB; ++b) x.mx[b].mask(piece, g, (int)mx_blocks(K));
       }
-      auto step = [&](auto sel) __attribute__((always_inline)) {
-        constexpr int s = decltype(sel)::value;
+    }
+    if constexpr (A == kMx) {
+      const unsigned char *scales = lds + t.kc / 32 * G;
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          const int at = (4 * local + s) * 4 + g;
+          const u32x4 a = *reinterpret_cast<const u32x4 *>(lds + i * block + at * G + 16 * r);
+          const int sa = scales[i * block + at * t.rows + r];
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            acc[i][b] = mfma_mx<s>(x.mx[b].c[s], (int)x.mx[b].s, y[i].c[s], (int)y[i].s, acc[i][b]);
-      };
-      step(std::integral_constant<int, 0>{});
-      step(std::integral_constant<int, 1>{});
-      step(std::integral_constant<int, 2>{});
-      step(std::integral_constant<int, 3>{});
+            acc[i][b] = mfma_mx(x.mx[b].c[s], (int)x.mx[b].scale(s, g), a, sa, acc[i][b]);
+        }
     } else {
       constexpr Widen kHow = W == kF16 || (W == kMx && A == kF16) ? kToF16 : kToBf16;
+      const unsigned char *from = lds + (local * kSteps * 16 + g) * G + 16 * r;
+      const int lo = t.kc / 8 * G;
       bool ok = true;
       if constexpr (W == kMx) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          ok &= A == kF16 ? scales_within<104, 140>(x.mx[b]) : scales_within<1, 254>(x.mx[b]);
+          ok &= A == kF16 ? x.mx[b].template within<104, 140>(g) : x.mx[b].template within<1, 254>(g);
         ok = __all(ok);
       }
-      if (W != kMx || ok) multiply<TAIL, kHow>(x, a, valid, piece, lane, K);
-      else multiply<TAIL, kThroughF32>(x, a, valid, piece, lane, K);
-    }
-  }
-
-  // HOW: the format the weights come in or are brought to.
-  template <bool TAIL, Widen HOW>
-  __device__ __forceinline__ void multiply(const Weights &x, const Act (&a)[MB],
-                                           const bool (&valid)[MB], int piece, int lane, int K) {
-    constexpr bool kSplitHere = A == kF16 && HOW != kToF16;
+      if (W != kMx || ok) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      Eight<ODD && A != kSplit> y[MB][4];
-      u32x4 z[A == kSplit ? MB : 1][4];
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-        if (valid[i]) {
+        for (int s = 0; s < kSteps; ++s)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if constexpr (A == kSplit) {
-              const long long at = ((piece * kSteps + s) * 4 + j) * 256LL;
-              y[i][j].load(a[i].p + at);
-              z[i][j] = *reinterpret_cast<const u32x4 *>(a[i].q + at);
-            } else {
-              const long long k =
-                  (long long)kK * piece + 32 * kSteps * (lane >> 4) + 32 * s + 8 * j;
-              if constexpr (TAIL) y[i][j].set(load_guarded(a[i].p, k, K - k), a[i].p);
-              else y[i][j].load(a[i].p + 2 * k);
+            u32x4 wv[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              if constexpr (W == kMx) wv[b] = widen<kHow>(x.mx[b].c[s][j], x.mx[b].scale(s, g));
+              else wv[b] = x.half[b][j].get(w[b].p);
             }
+            multiply<kHow>(wv, from + (4 * s + j) * 4 * G, block, lo);
           }
-        }
+      } else if constexpr (W == kMx) {
+        // Rare, and kept short: a loop over the piece's words.
+        const Weights y = x;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+          u32x4 wv[NB];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u32x4 wv[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          if constexpr (W == kMx) wv[b] = widen<HOW>(x.mx[b].c[s][j], x.mx[b].scale(s));
-          else wv[b] = x.half[b].v[j];
-        }
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          u32x4 v = y[i][j].get(a[i].p), lo{};
-          if constexpr (A == kSplit) lo = z[i][j];
-          if constexpr (kSplitHere) split_f16(v, v, lo);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            if constexpr (A == kSplit && HOW == kToF16) {
-              // fp16 weights are split too; the product of the two low parts,
-              // 2^-18 of the whole, is left out
-              u32x4 wh, wl;
-              split_f16(wv[b], wh, wl);
-              acc[i][b] = mfma_bf16(wh, v, acc[i][b]);
-              acc[i][b] = mfma_bf16(wh, lo, acc[i][b]);
-              acc[i][b] = mfma_bf16(wl, v, acc[i][b]);
-            } else if constexpr (HOW == kToF16) {
-              acc[i][b] = mfma_f16(wv[b], v, acc[i][b]);
-            } else {
-              acc[i][b] = mfma_bf16(wv[b], v, acc[i][b]);
-              if constexpr (A == kSplit || kSplitHere) acc[i][b] = mfma_bf16(wv[b], lo, acc[i][b]);
-            }
-          }
+          for (int b = 0; b < NB; ++b)
+            wv[b] = widen<kThroughF32>(y.mx[b].c[i >> 2][i & 3], y.mx[b].scale(i >> 2, g));
+          multiply<kThroughF32>(wv, from + i * 4 * G, block, lo);
         }
       }
-      // One step's activations at a time: all of them together would cost the
-      // registers of the waves that hide their latency.
-      if constexpr (kSteps > 1) __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-  // Adds the products of pieces first, first + step, ... of the K values.
-  __device__ __forceinline__ void run(const Act (&a)[MB], const bool (&valid)[MB],
-                                      const Rows (&w)[NB], int first, int step, int K, int lane) {
-    const int nb = (int)mx_blocks(K), last = K / kK;  // whole pieces
-    int p = first;
-#pragma unroll 1
-    for (; p < last; p += step) {
-      Weights x;
-      load_weights<false>(x, w, p, lane, K, nb);
-      turn_weights<false>(x, w, p, lane, nb);
-      use<false>(x, a, valid, p, lane, K, nb);
-    }
-    if (p == last && (long long)last * kK < K) {
-      Weights x;
-      load_weights<true>(x, w, p, lane, K, nb);
-      turn_weights<true>(x, w, p, lane, nb);
-      use<true>(x, a, valid, p, lane, K, nb);
+  // One matrix operand's products; `at`: the lane's activations in LDS.  HOW:
+  // the format that the weights come in or were brought to.
+  template <Widen HOW>
+  __device__ __forceinline__ void multiply(const u32x4 (&wv)[NB], const unsigned char *at,
+                                           int block, int lo_plane) {
+    constexpr bool kSplitHere = A == kF16 && HOW != kToF16;
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      u32x4 v = *reinterpret_cast<const u32x4 *>(at + i * block), lo{};
+      if constexpr (A == kF32) lo = *reinterpret_cast<const u32x4 *>(at + i * block + lo_plane);
+      if constexpr (kSplitHere) split_f16(v, v, lo);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if constexpr (A == kF32 && HOW == kToF16) {
+          // fp16 weights are split too; the product of the two low parts,
+          // 2^-18 of the whole, is left out
+          u32x4 wh, wl;
+          split_f16(wv[b], wh, wl);
+          acc[i][b] = mfma_bf16(wh, v, acc[i][b]);
+          acc[i][b] = mfma_bf16(wh, lo, acc[i][b]);
+          acc[i][b] = mfma_bf16(wl, v, acc[i][b]);
+        } else if constexpr (HOW == kToF16) {
+          acc[i][b] = mfma_f16(wv[b], v, acc[i][b]);
+        } else {
+          acc[i][b] = mfma_bf16(wv[b], v, acc[i][b]);
+          if constexpr (A == kF32 || kSplitHere) acc[i][b] = mfma_bf16(wv[b], lo, acc[i][b]);
+        }
+      }
     }
   }
+
+  // How a workgroup's waves go through K.
+  struct Walk {
+    int first, ks;  // this wave takes pieces first, first + ks, ...
+    bool any;       // whether this wave has columns at all
+    bool staged;    // the tile already holds all of K
+  };
+  // Adds all K values, from `x`, which holds the wave's first piece, on.  At
+  // the end `x` holds the first piece of the rows `next`.  `row(r)` gives row
+  // r of n activations.  Every wave of the workgroup makes the call.
+  template <int THREADS, class RowOf>
+  __device__ __forceinline__ void run(unsigned char *lds, const Tile &t, RowOf row, int n,
+                                      const Row (&w)[NB], const Row (&next)[NB], Weights &x,
+                                      const Walk &at, int K, int lane) {
+    const int g = lane >> 4, pieces = (int)ceil_div(K, kK);
+    const int rounds = (int)ceil_div(pieces, at.ks), per = t.kc / (kK * at.ks);
+    const int block = act_bytes<A>(t);
+#pragma unroll 1
+    for (int i0 = 0; i0 < rounds; i0 += per) {
+      if (!at.staged) {
+        __syncthreads();
+#pragma unroll 1
+        for (int m = 0; m < MB && n > 16 * m; ++m)
+          stage_acts<A, W, ODD, THREADS>(
+              lds + m * block, t, [&](int r) { return row(16 * m + r); },
+              n - 16 * m < 16 ? n - 16 * m : 16, i0 * at.ks * kK, K);
+        __syncthreads();
+      }
+      if (!at.any) continue;
+      const int end = i0 + per < rounds ? i0 + per : rounds;
+#pragma unroll 1
+      for (int i = i0; i < end; ++i) {
+        const int p = at.first + i * at.ks;
+        const bool last = i + 1 == rounds;
+        const int q = last ? (at.first < pieces ? at.first : 0) : p + at.ks < pieces ? p + at.ks : 0;
+        Row from[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) from[b] = last ? next[b] : w[b];
+        Weights y;
+        load(y, from, q, g, K);
+        if (p < pieces) use(x, w, lds, t, (i - i0) * at.ks + at.first, p, lane, K);
+        x = y;  // the next piece, needed at once
+      }
+    }
+  }
+  static __device__ __forceinline__ void load_first(Weights &x, const Row (&w)[NB], const Walk &at,
+                                                    int K, int lane) {
+    const int pieces = (int)ceil_div(K, kK);
+    if (at.any) load(x, w, at.first < pieces ? at.first : 0, lane >> 4, K);
+  }
 };
+
+// Waves per group of columns: until the groups' waves fill the chip (`want`),
+// or each has a piece.
+inline int waves_per_group(long long groups, int K, int piece, int most, int want) {
+  int ks = 1;
+  while (ks < most && groups * ks < want && (long long)2 * ks * piece <= K) ks *= 2;
+  return ks;
+}
+// Values of the activations' tile: all of K where it fits `bytes`, else as many
+// whole rounds (pieces of all waves that share columns) as do, one at least.
+template <int A>
+__host__ __device__ inline int tile_values(int rows, int K, int round, int bytes) {
+  const int all = (int)ceil_div(K, round), fit = bytes / act_bytes<A>(Tile{rows, round});
+  return round * (all < fit ? all : fit > 1 ? fit : 1);
+}
 
 }  // namespace
 }  // namespace gemm_f32_impl
