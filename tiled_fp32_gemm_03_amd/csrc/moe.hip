@@ -2,9 +2,9 @@
 // logits, the choice of experts, and the two products over the chosen
 // experts' weights.  The products read each chosen expert's weights once,
 // straight into the matrix instructions' operands (mx_thin.hpp); the tokens
-// of one expert share them, 16 rows at a time.  Four launches for up to 8
-// tokens (logits, first product, second product, sum; the choice is made again
-// by each workgroup of the first product), six for more.
+// of one expert share them, 16 rows at a time.  Four launches for one token
+// (logits, first product, second product, sum), one or two more for the choice
+// of experts of several.
 #include "mx_internal.hpp"
 #include "mx_thin.hpp"
 
@@ -104,7 +104,6 @@ __global__ void __launch_bounds__(256) moe_logits_kernel(MoeProblem p) {
 // ballots, added to the counts of the 64-pair chunks before.
 
 constexpr int kPerLane = kMoeMaxExperts / 64;
-constexpr int kFusedTokens = 8;
 
 template <int MAX_PAIRS>
 struct Route {
@@ -118,7 +117,7 @@ struct Route {
 };
 
 // Token t, as number `slot` of `r`.
-template <int MAX_PAIRS>
+template <bool GATES, int MAX_PAIRS>
 __device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, int slot, int t) {
   const int lane = threadIdx.x & 63;
   const double *logits = ws_at<double>(p, p.at.logits) + t * p.E;
@@ -155,6 +154,8 @@ __device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, 
       if (lane == s) id = 64 * i + at, value = best;
     }
   }
+  if (lane < p.top) r.chosen[slot * p.top + lane] = (unsigned short)id;
+  if (!GATES) return;
   // Gates: a NaN among the logits makes every one NaN.
   const double zmax = lane_f64(value, 0);
   double w = lane < p.top ? exp(value - zmax) : 0.0, part = w;
@@ -165,10 +166,7 @@ __device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, 
       if (64 * i < p.E) part += lane + 64 * i < p.E ? exp(z[i] - zmax) : 0.0;
   }
   const double total = __any(nan) ? __builtin_nan("") : wave_sum(part);
-  if (lane < p.top) {
-    r.chosen[slot * p.top + lane] = (unsigned short)id;
-    r.gate[slot * p.top + lane] = (float)(w / total);
-  }
+  if (lane < p.top) r.gate[slot * p.top + lane] = (float)(w / total);
 }
 
 // Lanes of the wave whose pair has the same expert as this lane's.
@@ -259,14 +257,24 @@ __device__ inline void write_lists(const MoeProblem &p, const Route<MAX_PAIRS> &
   if (threadIdx.x == 0) active[0] = r.nactive;
 }
 
-// More than kFusedTokens tokens: the choice, four tokens to a workgroup, and
-// the lists, by one.
+// Up to kRouteTokens tokens: choice and lists by one workgroup, a wave to a
+// token.  More: the choice, four tokens to a workgroup, then the lists.  (One
+// token: the first product's workgroups choose for themselves.)
+constexpr int kRouteTokens = 16;
+__global__ void __launch_bounds__(64 * kRouteTokens) moe_route_kernel(MoeProblem p) {
+  __shared__ Route<kRouteTokens * kMoeMaxTop> r;
+  if (wave_id() < p.T) choose_experts<true>(p, r, wave_id(), wave_id());
+  __syncthreads();
+  write_choice<64 * kRouteTokens>(p, r, 0, p.T * p.top);
+  list_pairs<64 * kRouteTokens>(p, r);
+  write_lists<64 * kRouteTokens>(p, r);
+}
 constexpr int kChooseTokens = 4;
 __global__ void __launch_bounds__(64 * kChooseTokens) moe_choose_kernel(MoeProblem p) {
   __shared__ Route<kChooseTokens * kMoeMaxTop> r;
   const int t0 = kChooseTokens * blockIdx.x;
   const int last = t0 + kChooseTokens < p.T ? t0 + kChooseTokens : p.T;
-  if (t0 + wave_id() < last) choose_experts(p, r, wave_id(), t0 + wave_id());
+  if (t0 + wave_id() < last) choose_experts<true>(p, r, wave_id(), t0 + wave_id());
   __syncthreads();
   write_choice<64 * kChooseTokens>(p, r, t0 * p.top, last * p.top);
 }
@@ -301,8 +309,8 @@ __device__ inline bool expert_of(const MoeProblem &p, int a, Expert &x) {
   const int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
   if (a >= active[0]) return false;
   x.e = active[1 + a];
-  x.first = start[x.e];
-  x.n = start[x.e + 1] - x.first;
+  x.first = p.T == 1 ? a : start[x.e];  // one token: in the order of the choice
+  x.n = p.T == 1 ? 1 : start[x.e + 1] - x.first;
   return true;
 }
 
@@ -351,32 +359,36 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
   }
 }
 
-// First product: u = silu(gate) * other.  FUSED: at most kFusedTokens tokens,
-// each workgroup makes the choice itself.
-template <int W, int AF, bool FUSED, bool ODD>
+// First product: u = silu(gate) * other.  ONE: a single token; each workgroup
+// makes the choice itself, one of them writes it, and the pairs are listed in
+// the order of the choice.
+template <int W, int AF, bool ONE, bool ODD>
 __global__ void __launch_bounds__(kThreads, 3) moe_up_kernel(MoeProblem p, MoeShape sh) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ Route<FUSED ? kFusedTokens * kMoeMaxTop : 1> route;
+  __shared__ Route<kMoeMaxTop> route;
   __shared__ long long starts[16];  // of the tokens' rows
   Expert x;
-  if constexpr (FUSED) {
-    for (int t = wave_id(); t < p.T; t += kWaves) choose_experts(p, route, t, t);
+  if constexpr (ONE) {
+    const bool writes = blockIdx.x == 0 && blockIdx.y == 0;
+    if (wave_id() == 0) choose_experts<false>(p, route, 0, 0);
+    if (writes && wave_id() == 1) choose_experts<true>(p, route, 0, 0);  // the same, and the gates
     __syncthreads();
-    list_pairs<kThreads>(p, route);
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-      write_choice<kThreads>(p, route, 0, p.T * p.top);
-      write_lists<kThreads>(p, route);
+    if (writes) {
+      write_choice<kThreads>(p, route, 0, p.top);
+      if ((int)threadIdx.x < p.top) {
+        ws_at<int>(p, p.at.list)[threadIdx.x] = threadIdx.x;
+        ws_at<int>(p, p.at.active)[1 + threadIdx.x] = route.chosen[threadIdx.x];
+      }
+      if (threadIdx.x == 0) ws_at<int>(p, p.at.active)[0] = p.top;
     }
-    if ((int)blockIdx.y >= route.nactive) return;
-    x.e = __builtin_amdgcn_readfirstlane(route.active[blockIdx.y]);
-    x.first = __builtin_amdgcn_readfirstlane(route.start[x.e]);
-    x.n = __builtin_amdgcn_readfirstlane(route.start[x.e + 1]) - x.first;
+    x = {__builtin_amdgcn_readfirstlane(route.chosen[blockIdx.y]), (int)blockIdx.y, 1};
   } else if (!expert_of(p, blockIdx.y, x)) {
     return;
   }
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   auto weights = [&](int c, Row (&w)[2]) __attribute__((always_inline)) {
-    const long long i = 16LL * c + l16 < p.I ? 16LL * c + l16 : p.I - 1, r = 2LL * p.I * x.e + i;
+    const long long i = 16LL * c + (lane >> 2) < p.I ? 16LL * c + (lane >> 2) : p.I - 1;
+    const long long r = 2LL * p.I * x.e + i;
     w[0] = {p.W1 + r * p.ld1, p.S1 + r * p.lds1};
     w[1] = {p.W1 + (r + p.I) * p.ld1, p.S1 + (r + p.I) * p.lds1};
   };
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 3) moe_up_kernel(MoeProblem p, MoeSh
     const int n = x.n - m0 < 16 ? x.n - m0 : 16;
     if ((int)threadIdx.x < n) {
       const int at = x.first + m0 + threadIdx.x;
-      const int pair = FUSED ? (int)route.list[at] : ws_at<int>(p, p.at.list)[at];
+      const int pair = ONE ? at : ws_at<int>(p, p.at.list)[at];
       starts[threadIdx.x] = pair / p.top * p.ldx;
     }
     auto row = [&](int r) __attribute__((always_inline)) {
@@ -413,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, 3) moe_down_kernel(MoeProblem p, Moe
   if (!expert_of(p, blockIdx.y, x)) return;
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   auto weights = [&](int c, Row (&w)[1]) __attribute__((always_inline)) {
-    const long long h = 16LL * c + l16 < p.H ? 16LL * c + l16 : p.H - 1, r = (long long)p.H * x.e + h;
+    const long long h = 16LL * c + (lane >> 2) < p.H ? 16LL * c + (lane >> 2) : p.H - 1;
+    const long long r = (long long)p.H * x.e + h;
     w[0] = {p.W2 + r * p.ld2, p.S2 + r * p.lds2};
   };
   for (int m0 = 0; m0 < x.n; m0 += 16) {
@@ -484,8 +497,8 @@ hipError_t launch_experts(Kernel kern, const MoeProblem &p, MoeShape sh, int col
 template <int W, int AF, bool ODD>
 hipError_t launch_up(const MoeProblem &p, hipStream_t s) {
   const long long experts = p.E < p.T * p.top ? p.E : p.T * p.top;
-  return launch_experts(p.T <= kFusedTokens ? moe_up_kernel<W, AF, true, ODD>
-                                            : moe_up_kernel<W, AF, false, ODD>,
+  return launch_experts(p.T == 1 ? moe_up_kernel<W, AF, true, ODD>
+                                 : moe_up_kernel<W, AF, false, ODD>,
                         p, shape_of<W, AF>(experts, p.I, p.H, p.T), p.I, s);
 }
 template <int W, bool ODD>
@@ -519,7 +532,10 @@ hipError_t launch_moe(const MoeProblem &p, hipStream_t s) {
   const bool bf16 = p.format == kBf16;
   hipError_t e = bf16 ? launch_logits<kBf16>(p, s) : launch_logits<kF16>(p, s);
   if (e != hipSuccess) return e;
-  if (p.T > kFusedTokens) {
+  if (p.T > 1 && p.T <= kRouteTokens) {
+    e = launch_kernel(moe_route_kernel, dim3(1), dim3(64 * kRouteTokens), s, p);
+    if (e != hipSuccess) return e;
+  } else if (p.T > 1) {
     e = launch_kernel(moe_choose_kernel, dim3((unsigned)ceil_div(p.T, kChooseTokens)),
                       dim3(64 * kChooseTokens), s, p);
     if (e == hipSuccess) e = launch_kernel(moe_list_kernel, dim3(1), dim3(kListThreads), s, p);

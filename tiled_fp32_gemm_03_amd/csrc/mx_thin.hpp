@@ -1,6 +1,6 @@
-// Pieces of the thin products (few rows of gemm_mx, gemm_mx_a16, the
-// mixture-of-experts layer): up to 32 rows of activations against weights
-// read once from memory, which is what bounds them.
+// Pieces of the products of few rows of activations with weights that are read
+// once from memory, which is what bounds them (gemm_mx_a16, the
+// mixture-of-experts layer).
 //
 // A wave multiplies blocks of 16 activation rows with blocks of 16 weight
 // rows ("columns" of C) and takes K in pieces of 256 bytes of weight row:
@@ -8,16 +8,14 @@
 // memory into registers, the next piece's while one is used; the activations,
 // which a workgroup's waves share, wait in LDS.  Loads complete in order, so
 // activations loaded from memory between the pieces would make each wave wait
-// for the next piece's weights as well (measured: twice the time), and four
-// lanes that read four rows cost the L1 four accesses, of which 16-bit
-// activations would need four times what MX weights do.
+// for the next piece's weights as well (measured: twice the time).
 //
-// Lane l holds row l % 16 of each operand; which k a lane holds is free as
-// long as both operands agree, so it follows how the weights are stored, with
-// g = l / 16:
-//   MX weights: load s of a piece is block 4 s + g of it; MFMA j of step s
-//     takes its values 8 j .. 8 j + 7, widened with their scale (exact: an
-//     element has two significant bits);
+// Lane l multiplies row l % 16 of each operand; which k a lane holds is free
+// as long as both operands agree, so it follows how the weights are stored,
+// with g = l / 16:
+//   MX weights: block 4 s + g of a piece in step s; MFMA j of the step takes
+//     its values 8 j .. 8 j + 7, widened with their scale (exact: an element
+//     has two significant bits);
 //   16-bit weights: load j is k = 32 j + 8 g .. + 7, the operand of MFMA j.
 #pragma once
 
@@ -80,34 +78,36 @@ __device__ inline void split_f32(u32x4 a, u32x4 b, u32x4 &hi, u32x4 &lo) {
   }
 }
 
+// The 16-bit codes of x from number `drop` on, then zeros.
+__device__ inline u32x4 drop_first(u32x4 x, long long drop) {
+  uint64_t lo = x[0] | (uint64_t)x[1] << 32, hi = x[2] | (uint64_t)x[3] << 32;
+  const int bits = drop < 8 ? (int)drop * 16 : 128;
+  if (bits >= 64) {
+    lo = bits < 128 ? hi >> (bits - 64) : 0;
+    hi = 0;
+  } else if (bits > 0) {
+    lo = lo >> bits | hi << (64 - bits);
+    hi >>= bits;
+  }
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 // Values k .. k + 7 of a row of K 16-bit codes, zeros past K: the eight that
 // end at K at the latest, moved into place.  (One load and a shift: guarded
 // element loads, inlined everywhere, made kernels of 60 KB that spent their
 // time on fetching instructions.)
 __device__ inline u32x4 load_guarded(const unsigned char *row, long long k, int K) {
   const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
-  uint64_t lo = 0, hi = 0;
   if (K >= 8) {
     const long long from = k < K - 8 ? k : K - 8;
-    const u32x4 v = *reinterpret_cast<const u32x4h *>(p + from);
-    lo = v[0] | (uint64_t)v[1] << 32;
-    hi = v[2] | (uint64_t)v[3] << 32;
-    const long long drop = k - from;  // values before k
-    const int bits = drop < 8 ? (int)drop * 16 : 128;
-    if (bits >= 64) {
-      lo = bits < 128 ? hi >> (bits - 64) : 0;
-      hi = 0;
-    } else if (bits > 0) {
-      lo = lo >> bits | hi << (64 - bits);
-      hi >>= bits;
-    }
-  } else {
+    return drop_first(*reinterpret_cast<const u32x4h *>(p + from), k - from);
+  }
+  uint64_t lo = 0, hi = 0;
 #pragma unroll 1
-    for (int i = 0; k + i < K; ++i) {
-      const uint64_t v = (uint64_t)p[k + i] << (16 * (i & 3));
-      if (i < 4) lo |= v;
-      else hi |= v;
-    }
+  for (int i = 0; k + i < K; ++i) {
+    const uint64_t v = (uint64_t)p[k + i] << (16 * (i & 3));
+    if (i < 4) lo |= v;
+    else hi |= v;
   }
   return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
@@ -189,46 +189,71 @@ __device__ inline u32x4 widen(uint32_t codes, uint32_t sb) {
 __device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // ---- weights -----------------------------------------------------------------
+//
+// Lane l loads 16 bytes number l % 4 of 64 of row l / 4: lanes that each read
+// the row they need, l % 16, cost the L1 an access each, four that read one
+// line of a row one between them (gemm_mx_a16, 32 x 16384 x 8192: 27.7 us
+// against 21.7).  What lane l needs, number l / 16 of row l % 16, then comes
+// from lane 4 (l % 16) + l / 16.
 
-// The lane's row of weights: 2-byte values or MX codes, and MX scales.
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_ds_bpermute(4 * lane, (int)v);
+}
+__device__ __forceinline__ u32x4 from_lane(u32x4 v, int lane) {
+  return u32x4{from_lane(v[0], lane), from_lane(v[1], lane), from_lane(v[2], lane),
+               from_lane(v[3], lane)};
+}
+// The lane whose load holds this lane's operand.
+__device__ __forceinline__ int loader(int lane) { return 4 * (lane & 15) + (lane >> 4); }
+
+// Row l / 4 of a block of 16 rows: 2-byte values or MX codes, and MX scales.
 struct Row {
   const unsigned char *p;
   const unsigned char *q;
 };
 
-// A piece of an MX row as it is stored: blocks 16 piece + 4 s + g and the 16
-// scales.  Blocks past the row's are read from its last; mask makes them
-// zeros with scale 1.
+// A piece of 16 MX rows as loaded: blocks 16 piece + 4 i + l % 4, and scales
+// 4 (l % 4) .. + 3 of the piece.  Blocks past the row's are read from its last.
 struct MxPiece {
   u32x4 c[4];
-  u32x4 s;
-  __device__ __forceinline__ void load(const Row &r, int piece, int g, int nb) {
-    s = *reinterpret_cast<const u32x4 *>(r.q + 16LL * piece);
+  uint32_t s;
+  __device__ __forceinline__ void load(const Row &r, int piece, int lane, int nb) {
+    s = *reinterpret_cast<const uint32_t *>(r.q + 16LL * piece + 4 * (lane & 3));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int kb = 16 * piece + 4 * i + g < nb ? 16 * piece + 4 * i + g : nb - 1;
-      c[i] = *reinterpret_cast<const u32x4 *>(r.p + 16LL * kb);
+      const int kb = 16 * piece + 4 * i + (lane & 3);
+      c[i] = *reinterpret_cast<const u32x4 *>(r.p + 16LL * (kb < nb ? kb : nb - 1));
     }
   }
-  __device__ __forceinline__ void mask(int piece, int g, int nb) {
+};
+// Its operands: blocks 16 piece + 4 i + l / 16 of row l % 16 and their scales;
+// blocks past the row's are zeros with scale 1.
+struct MxBlocks {
+  u32x4 c[4];
+  uint32_t s[4];
+  __device__ __forceinline__ MxBlocks(const MxPiece &x, int piece, int lane, int nb) {
+    const int g = lane >> 4, from = loader(lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (16 * piece + 4 * i + g >= nb) {
-        c[i] = u32x4{0, 0, 0, 0};
-        s[i] = 0x7f7f7f7fu;
-      }
+    for (int i = 0; i < 4; ++i) {
+      c[i] = from_lane(x.c[i], from);
+      s[i] = from_lane(x.s, 4 * (lane & 15) + i) >> (8 * g) & 255u;
+    }
+    if (16 * (piece + 1) > nb) {  // uniform
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (16 * piece + 4 * i + g >= nb) {
+          c[i] = u32x4{0, 0, 0, 0};
+          s[i] = 127u;
+        }
+    }
   }
-  // Lane group g's scale byte of step i.
-  __device__ __forceinline__ uint32_t scale(int i, int g) const { return (s[i] >> (8 * g)) & 255u; }
   // Whether all of the lane's blocks have scales within (blocks of zeros allow any).
   template <uint32_t LOW, uint32_t HIGH>
-  __device__ __forceinline__ bool within(int g) const {
+  __device__ __forceinline__ bool within() const {
     bool ok = true;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t sb = scale(i, g);
-      ok &= sb - LOW <= HIGH - LOW || (sb != 255 && (c[i][0] | c[i][1] | c[i][2] | c[i][3]) == 0);
-    }
+    for (int i = 0; i < 4; ++i)
+      ok &= s[i] - LOW <= HIGH - LOW || (s[i] != 255 && (c[i][0] | c[i][1] | c[i][2] | c[i][3]) == 0);
     return ok;
   }
 };
@@ -240,8 +265,7 @@ struct MxPiece {
 // the rows' 16 bytes one after the other, and 16 bytes of padding, so that
 // neither the writes (neighbouring threads take neighbouring k of a row) nor
 // the reads (16 lanes take 16 rows) meet on a bank.  kF32: a second such
-// plane for lo.  MX rows: one operand is a block; the scales follow, a byte
-// per block and row.
+// plane for lo.
 
 struct Tile {
   int rows, kc;
@@ -250,12 +274,11 @@ struct Tile {
 // LDS bytes of a block of rows of kind A: linear in kc (whole pieces).
 template <int A>
 __host__ __device__ inline int act_bytes(const Tile &t) {
-  return A == kMx ? t.kc / 32 * (t.group() + t.rows)
-                  : t.kc / 8 * t.group() * (A == kF32 ? 2 : 1);
+  return t.kc / 8 * t.group() * (A == kF32 ? 2 : 1);
 }
 
 // Fills a block with values k0 .. k0 + kc - 1 of rows 0 .. n - 1, zeros past K;
-// `row(r)` gives row r's start (for MX its codes and scales).  All THREADS
+// `row(r)` gives row r's start.  All THREADS
 // threads of the workgroup take part; each issues four loads before it writes
 // any (one at a time, their latencies alone took 30 us of a first product).
 // Rows of kind kF32 hold zeros from K to a multiple of 8.
@@ -264,23 +287,16 @@ __device__ __forceinline__ void stage_acts(unsigned char *lds, const Tile &t, Ro
                                            int k0, int K) {
   constexpr int kBatch = 4;
   const int G = t.group();
-  const int per = t.kc / (A == kMx ? 32 : 8), all = n * per;
-  const int nb = (int)mx_blocks(K), eights = (int)ceil_div(K, 8);
-  unsigned char *scales = lds + per * G;  // kMx
+  const int per = t.kc / 8, all = n * per, eights = (int)ceil_div(K, 8);
 #pragma unroll 1
   for (int i0 = threadIdx.x; i0 < all; i0 += kBatch * THREADS) {
     u32x4 c[kBatch], d[kBatch];
-    unsigned char sb[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int i = i0 + u * THREADS < all ? i0 + u * THREADS : all - 1;
       const int r = i / per, x = i % per;
       const Row src = row(r);
-      if constexpr (A == kMx) {
-        const int kb = k0 / 32 + x, in = kb < nb ? kb : nb - 1;
-        c[u] = *reinterpret_cast<const u32x4 *>(src.p + 16LL * in);
-        sb[u] = src.q[in];
-      } else if constexpr (A == kF32) {
+      if constexpr (A == kF32) {
         const int e = k0 / 8 + x, in = e < eights ? e : eights - 1;
         const u32x4w *q = reinterpret_cast<const u32x4w *>(src.p + 32LL * in);
         c[u] = q[0];
@@ -304,11 +320,7 @@ __device__ __forceinline__ void stage_acts(unsigned char *lds, const Tile &t, Ro
       const int i = i0 + u * THREADS;
       if (i >= all) continue;
       const int r = i / per, x = i % per;
-      if constexpr (A == kMx) {
-        const bool in = k0 / 32 + x < nb;
-        *reinterpret_cast<u32x4 *>(lds + x * G + 16 * r) = in ? c[u] : u32x4{0, 0, 0, 0};
-        scales[x * t.rows + r] = in ? sb[u] : 127;
-      } else {
+      {
         // Operand and lane group of values 8 x .. 8 x + 7: the MX order of k
         // is (step, g, j), the 16-bit one (j, g).
         const int group = W == kMx ? (x & ~15) | (x & 3) << 2 | (x >> 2 & 3) : x;
@@ -358,15 +370,15 @@ struct Thin {
   }
 
   // A piece's weights, zeros past K.
-  static __device__ __forceinline__ void load(Weights &x, const Row (&w)[NB], int piece, int g,
+  static __device__ __forceinline__ void load(Weights &x, const Row (&w)[NB], int piece, int lane,
                                               int K) {
     const int nb = (int)mx_blocks(K);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if constexpr (W == kMx) {
-        x.mx[b].load(w[b], piece, g, nb);
+        x.mx[b].load(w[b], piece, lane, nb);
       } else {
-        const long long k0 = (long long)kK * piece + 8 * g;
+        const long long k0 = (long long)kK * piece + 8 * (lane & 3);
         if (piece < K / kK) {  // uniform
 #pragma unroll
           for (int j = 0; j < 4; ++j) x.half[b][j].load(w[b].p + 2 * (k0 + 32 * j));
@@ -382,61 +394,54 @@ struct Thin {
   }
 
   // The products of a loaded piece, number `local` of the tile.
-  __device__ __forceinline__ void use(Weights &x, const Row (&w)[NB], const unsigned char *lds,
-                                      const Tile &t, int local, int piece, int lane, int K) {
+  __device__ __forceinline__ void use(const Weights &x, const Row (&w)[NB],
+                                      const unsigned char *lds, const Tile &t, int local, int piece,
+                                      int lane, int K) {
     const int g = lane >> 4, r = lane & (t.rows - 1), G = t.group(), block = act_bytes<A>(t);
-    if constexpr (W == kMx) {
-      if ((long long)kK * (piece + 1) > K) {  // uniform
+    constexpr Widen kHow = W == kF16 || (W == kMx && A == kF16) ? kToF16 : kToBf16;
+    const unsigned char *from = lds + (local * kSteps * 16 + g) * G + 16 * r;
+    const int lo = t.kc / 8 * G;
+    if constexpr (W != kMx) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) x.mx[b].mask(piece, g, (int)mx_blocks(K));
+      for (int j = 0; j < 4; ++j) {
+        u32x4 wv[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) wv[b] = from_lane(x.half[b][j].get(w[b].p), loader(lane));
+        multiply<kHow>(wv, from + j * 4 * G, block, lo);
       }
-    }
-    if constexpr (A == kMx) {
-      const unsigned char *scales = lds + t.kc / 32 * G;
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          const int at = (4 * local + s) * 4 + g;
-          const u32x4 a = *reinterpret_cast<const u32x4 *>(lds + i * block + at * G + 16 * r);
-          const int sa = scales[i * block + at * t.rows + r];
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            acc[i][b] = mfma_mx(x.mx[b].c[s], (int)x.mx[b].scale(s, g), a, sa, acc[i][b]);
-        }
     } else {
-      constexpr Widen kHow = W == kF16 || (W == kMx && A == kF16) ? kToF16 : kToBf16;
-      const unsigned char *from = lds + (local * kSteps * 16 + g) * G + 16 * r;
-      const int lo = t.kc / 8 * G;
+      const MxBlocks y0(x.mx[0], piece, lane, (int)mx_blocks(K));
+      const MxBlocks y1(x.mx[NB - 1], piece, lane, (int)mx_blocks(K));
+      const MxBlocks *y[2] = {&y0, &y1};
       bool ok = true;
-      if constexpr (W == kMx) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          ok &= A == kF16 ? x.mx[b].template within<104, 140>(g) : x.mx[b].template within<1, 254>(g);
-        ok = __all(ok);
-      }
-      if (W != kMx || ok) {
+      for (int b = 0; b < NB; ++b)
+        ok &= A == kF16 ? y[b]->template within<104, 140>() : y[b]->template within<1, 254>();
+      if (__all(ok)) {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             u32x4 wv[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              if constexpr (W == kMx) wv[b] = widen<kHow>(x.mx[b].c[s][j], x.mx[b].scale(s, g));
-              else wv[b] = x.half[b][j].get(w[b].p);
-            }
+            for (int b = 0; b < NB; ++b) wv[b] = widen<kHow>(y[b]->c[s][j], y[b]->s[s]);
             multiply<kHow>(wv, from + (4 * s + j) * 4 * G, block, lo);
           }
-      } else if constexpr (W == kMx) {
+      } else {
         // Rare, and kept short: a loop over the piece's words.
-        const Weights y = x;
 #pragma unroll 1
         for (int i = 0; i < 16; ++i) {
           u32x4 wv[NB];
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-            wv[b] = widen<kThroughF32>(y.mx[b].c[i >> 2][i & 3], y.mx[b].scale(i >> 2, g));
+          for (int b = 0; b < NB; ++b) {
+            uint32_t c = 0, sb = 0;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              if (q == i) c = y[b]->c[q >> 2][q & 3];
+              if (q == i) sb = y[b]->s[q >> 2];
+            }
+            wv[b] = widen<kThroughF32>(c, sb);
+          }
           multiply<kThroughF32>(wv, from + i * 4 * G, block, lo);
         }
       }
@@ -487,7 +492,7 @@ struct Thin {
   __device__ __forceinline__ void run(unsigned char *lds, const Tile &t, RowOf row, int n,
                                       const Row (&w)[NB], const Row (&next)[NB], Weights &x,
                                       const Walk &at, int K, int lane) {
-    const int g = lane >> 4, pieces = (int)ceil_div(K, kK);
+    const int pieces = (int)ceil_div(K, kK);
     const int rounds = (int)ceil_div(pieces, at.ks), per = t.kc / (kK * at.ks);
     const int block = act_bytes<A>(t);
 #pragma unroll 1
@@ -512,7 +517,7 @@ struct Thin {
 #pragma unroll
         for (int b = 0; b < NB; ++b) from[b] = last ? next[b] : w[b];
         Weights y;
-        load(y, from, q, g, K);
+        load(y, from, q, lane, K);
         if (p < pieces) use(x, w, lds, t, (i - i0) * at.ks + at.first, p, lane, K);
         x = y;  // the next piece, needed at once
       }
@@ -521,7 +526,73 @@ struct Thin {
   static __device__ __forceinline__ void load_first(Weights &x, const Row (&w)[NB], const Walk &at,
                                                     int K, int lane) {
     const int pieces = (int)ceil_div(K, kK);
-    if (at.any) load(x, w, at.first < pieces ? at.first : 0, lane >> 4, K);
+    if (at.any) load(x, w, at.first < pieces ? at.first : 0, lane, K);
+  }
+};
+
+// The same product of one block of rows with the activations straight from
+// memory, for products so small that what counts is the latency: a piece's
+// weights and activations are asked for together, both by four lanes to a
+// line.  MFMA m of step s takes block 4 s + m of the piece here, lane l its
+// values 8 (l / 16) .. + 7, so that one lane's load holds one lane's operand.
+template <int A, bool ODD>
+struct Direct {
+  f32x4 acc;
+  // The products of 8 values per lane, of MX words that allow `kHow` or not.
+  template <Widen HOW>
+  __device__ __forceinline__ void add(uint32_t codes, uint32_t sb, u32x4 v) {
+    const u32x4 wv = widen<HOW>(codes, sb);
+    if constexpr (HOW == kToF16) {
+      acc = mfma_f16(wv, v, acc);
+    } else {
+      u32x4 lo{};
+      if constexpr (A == kF16) split_f16(v, v, lo);
+      acc = mfma_bf16(wv, v, acc);
+      if constexpr (A == kF16) acc = mfma_bf16(wv, lo, acc);
+    }
+  }
+  // `w`, `a`: rows l / 4 of the weights and the activations.
+  __device__ __forceinline__ void piece(const Row &w, const unsigned char *a, int piece, int lane,
+                                        int K) {
+    const int from = loader(lane), part = lane & 3, nb = (int)mx_blocks(K);
+    const uint32_t s = *reinterpret_cast<const uint32_t *>(w.q + 16LL * piece + 4 * part);
+    if (512LL * (piece + 1) <= K) {  // uniform
+      uint32_t c[16], sc[4];
+      Eight<ODD> v[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        c[q] = *reinterpret_cast<const uint32_t *>(w.p + 16 * (16LL * piece + q) + 4 * part);
+        v[q].load(a + 2 * (32 * (16LL * piece + q) + 8 * part));
+      }
+      bool ok = true;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sc[i] = from_lane(s, 4 * (lane & 15) + i);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t sb = sc[i] >> (8 * m) & 255u;
+          ok &= A == kF16 ? sb - 104u <= 140u - 104u : sb - 1u <= 253u;
+        }
+      }
+      if (__all(ok)) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          add<A == kF16 ? kToF16 : kToBf16>(from_lane(c[q], from), sc[q >> 2] >> (8 * (q & 3)) & 255u,
+                                            from_lane(v[q].get(a), from));
+        return;
+      }
+    }
+    // K's end, or scales far from 1: block by block, through fp32.
+#pragma unroll 1
+    for (int q = 0; q < 16; ++q) {
+      const int kb = 16 * piece + q;
+      if (kb >= nb) break;
+      const uint32_t c = *reinterpret_cast<const uint32_t *>(w.p + 16LL * kb + 4 * part);
+      const long long k = 32LL * kb + 8 * part;
+      add<kThroughF32>(from_lane(c, from),
+                       from_lane(s, 4 * (lane & 15) + (q >> 2)) >> (8 * (q & 3)) & 255u,
+                       from_lane(load_guarded(a, k < K ? k : K, K), from));
+    }
   }
 };
 
