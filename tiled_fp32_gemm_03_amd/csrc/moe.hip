@@ -316,53 +316,94 @@ __device__ inline bool expert_of(const MoeProblem &p, int a, Expert &x) {
 
 // Columns 16 c .. 16 c + 15 of the product of up to 16 rows, NB factors each,
 // for each group c of this wave: `weights(c)` gives the lane's rows,
-// `done(c, acc)` takes the sums of the group's first wave.
-template <int W, int A, int NB, bool ODD, class RowOf, class WeightsOf, class Done>
+// `done(c, acc)` takes the sums of the group's first wave.  The weights of two
+// pieces are on their way while a third is used.
+template <int W, int A, int NB, int ROWS, class RowOf, class WeightsOf, class Done>
 __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, int n, int K,
                                                int groups, const MoeShape &sh,
                                                WeightsOf weights, Done done) {
-  typedef Thin<W, A, 1, NB, ODD> Product;
+  typedef Thin<W, A, NB, ROWS> Product;
+  constexpr int kK = Product::kK;
+  __shared__ f32x4 part[kWaves][NB][64];
   const int lane = threadIdx.x & 63, wave = wave_id();
   // As much of K as the launch's LDS holds of this many rows.
-  const int round = sh.ks * kPieceK<W>;
-  const int keep = n <= 4 ? 4 : 16;
-  const Tile tile{keep, tile_values<A>(keep, K, round, sh.lds)};
+  const int ks = sh.ks, keep = n <= 4 ? 4 : 16;
+  const Tile tile{keep, tile_values<A>(keep, K, ks * kK, sh.lds)};
   const bool whole = tile.kc >= K;
-  const int per = kWaves / sh.ks;  // groups side by side
-  int c = (int)blockIdx.x * per * sh.each + wave / sh.ks;
-  typename Product::Walk at{wave & (sh.ks - 1), sh.ks, c < groups, false};
-  Row w[NB], next[NB];
-  weights(c < groups ? c : groups - 1, w);
-  typename Product::Weights x;
-  Product::load_first(x, w, at, K, lane);
-  for (int i = 0; i < sh.each; ++i, c += per) {
-    at.any = c < groups;
-    at.staged = whole && i > 0;
-    weights(i + 1 < sh.each && c + per < groups ? c + per : at.any ? c : groups - 1, next);
-    Product t;
-    t.clear();
-    t.template run<kThreads>(lds, tile, row, n, w, next, x, at, K, lane);
-    if (sh.ks > 1) {  // the waves' sums, added in wave order
-      __shared__ f32x4 part[kWaves][NB][64];
-      __syncthreads();
-#pragma unroll
-      for (int b = 0; b < NB; ++b) part[wave][b][lane] = t.acc[0][b];
-      __syncthreads();
-      if (at.first == 0)
-        for (int q = 1; q < sh.ks; ++q)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) t.acc[0][b] += part[wave + q][b][lane];
+  const int side = kWaves / ks;  // groups side by side
+  const int c0 = (int)blockIdx.x * side * sh.each + wave / ks, first = wave & (ks - 1);
+  // A wave's turns: for each of its groups, pieces first, first + ks, ...
+  const int pieces = (int)ceil_div(K, kK), rounds = (int)ceil_div(pieces, ks);
+  const int per = tile.kc / (kK * ks);  // rounds in a tile
+  struct Turn {
+    int group, round;
+  };
+  auto step = [&](Turn &t) __attribute__((always_inline)) {
+    if (++t.round == rounds) t = {t.group + 1, 0};
+  };
+  auto piece = [&](const Turn &t) __attribute__((always_inline)) { return first + t.round * ks; };
+  typename Product::Weights x[2];
+  Row w[NB];
+  int at = -1;  // whose group's rows w are
+  auto load = [&](typename Product::Weights &x, const Turn &t) __attribute__((always_inline)) {
+    if (t.group != at) {
+      at = t.group;
+      const int c = c0 + at * side;
+      weights(at < sh.each && c < groups ? c : groups - 1, w);
     }
-    if (at.any && at.first == 0 && (lane & 15) < n) done(c, t.acc[0]);
+    Product::load(x, w, piece(t) < pieces ? piece(t) : pieces - 1, lane, K);
+  };
+  Turn ahead{0, 0}, now{0, 0};
+  // The first tile before the weights, which it would wait for otherwise.
+  stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, 0, K);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) w[b] = next[b];
+  for (int u = 0; u < 2; ++u) {
+    load(x[u], ahead);
+    step(ahead);
+    __builtin_amdgcn_sched_barrier(0);  // in order of use, or the first wait is for both
+  }
+  __syncthreads();
+  Product t;
+  t.clear();
+#pragma unroll 1
+  while (now.group < sh.each) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {  // a turn past the end multiplies nothing
+      if (now.group < sh.each) {
+        if (now.round % per == 0 && now.round + now.group > 0 && !whole) {
+          __syncthreads();
+          stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, now.round * ks * kK, K);
+          __syncthreads();
+        }
+        const int c = c0 + now.group * side;
+        if (c < groups && piece(now) < pieces)
+          t.use(x[u], [&](Row (&w)[NB]) { weights(c, w); }, lds, tile, now.round % per * ks + first, piece(now), lane, K);
+        if (now.round == rounds - 1) {
+          if (ks > 1) {  // the waves' sums, added in wave order
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < NB; ++b) part[wave][b][lane] = t.acc[b];
+            __syncthreads();
+            if (first == 0)
+              for (int q = 1; q < ks; ++q)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) t.acc[b] += part[wave + q][b][lane];
+          }
+          if (c < groups && first == 0 && (lane & 15) < n) done(c, t.acc);
+          t.clear();
+        }
+      }
+      step(now);
+      load(x[u], ahead);
+      step(ahead);
+    }
   }
 }
 
 // First product: u = silu(gate) * other.  ONE: a single token; each workgroup
 // makes the choice itself, one of them writes it, and the pairs are listed in
 // the order of the choice.
-template <int W, int AF, bool ONE, bool ODD>
+template <int W, int AF, bool ONE, int ROWS>
 __global__ void __launch_bounds__(kThreads, 3) moe_up_kernel(MoeProblem p, MoeShape sh) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ Route<kMoeMaxTop> route;
@@ -399,8 +440,9 @@ __global__ void __launch_bounds__(kThreads, 3) moe_up_kernel(MoeProblem p, MoeSh
       const int pair = ONE ? at : ws_at<int>(p, p.at.list)[at];
       starts[threadIdx.x] = pair / p.top * p.ldx;
     }
+    __syncthreads();
     auto row = [&](int r) __attribute__((always_inline)) {
-      return Row{reinterpret_cast<const unsigned char *>(p.X + starts[r]), nullptr};
+      return reinterpret_cast<const unsigned char *>(p.X + starts[r]);
     };
     auto done = [&](int c, const f32x4 (&acc)[2]) __attribute__((always_inline)) {
       f32x4 u;
@@ -412,13 +454,13 @@ __global__ void __launch_bounds__(kThreads, 3) moe_up_kernel(MoeProblem p, MoeSh
         *reinterpret_cast<f32x4 *>(ws_at<float>(p, p.at.u) + (x.first + m0 + l16) * p.at.upitch + i) = u;
     };
     const int groups = (int)ceil_div(p.I, 16);
-    expert_columns<W, AF, 2, ODD>(lds, row, n, p.H, groups, sh, weights, done);
+    expert_columns<W, AF, 2, ROWS>(lds, row, n, p.H, groups, sh, weights, done);
     __syncthreads();
   }
 }
 
 // Second product: each pair's result, before its gate.
-template <int W, bool ODD>
+template <int W, int ROWS>
 __global__ void __launch_bounds__(kThreads, 3) moe_down_kernel(MoeProblem p, MoeShape sh) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   Expert x;
@@ -432,16 +474,16 @@ __global__ void __launch_bounds__(kThreads, 3) moe_down_kernel(MoeProblem p, Moe
   for (int m0 = 0; m0 < x.n; m0 += 16) {
     const int n = x.n - m0 < 16 ? x.n - m0 : 16;
     auto row = [&](int r) __attribute__((always_inline)) {
-      return Row{p.ws + p.at.u + 4 * (x.first + m0 + r) * p.at.upitch, nullptr};
+      return p.ws + p.at.u + 4 * (x.first + m0 + r) * p.at.upitch;
     };
+    const int pair = ws_at<int>(p, p.at.list)[x.first + m0 + (l16 < n ? l16 : 0)];
     auto done = [&](int c, const f32x4 (&acc)[1]) __attribute__((always_inline)) {
-      const int pair = ws_at<int>(p, p.at.list)[x.first + m0 + l16];
       const long long h = 16LL * c + 4 * g, left = p.H - h;
       store4<kF32>(ws_at<float>(p, p.at.part), pair * p.at.ypitch + h, (int)(left < 4 ? left : 4),
                    acc[0]);
     };
     const int groups = (int)ceil_div(p.H, 16);
-    expert_columns<W, kF32, 1, ODD>(lds, row, n, p.I, groups, sh, weights, done);
+    expert_columns<W, kF32, 1, ROWS>(lds, row, n, p.I, groups, sh, weights, done);
     __syncthreads();
   }
 }
@@ -494,21 +536,21 @@ hipError_t launch_experts(Kernel kern, const MoeProblem &p, MoeShape sh, int col
                          (size_t)sh.lds, s);
 }
 
-template <int W, int AF, bool ODD>
+template <int W, int AF, int ROWS>
 hipError_t launch_up(const MoeProblem &p, hipStream_t s) {
   const long long experts = p.E < p.T * p.top ? p.E : p.T * p.top;
-  return launch_experts(p.T == 1 ? moe_up_kernel<W, AF, true, ODD>
-                                 : moe_up_kernel<W, AF, false, ODD>,
+  return launch_experts(p.T == 1 ? moe_up_kernel<W, AF, true, ROWS>
+                                 : moe_up_kernel<W, AF, false, ROWS>,
                         p, shape_of<W, AF>(experts, p.I, p.H, p.T), p.I, s);
 }
-template <int W, bool ODD>
+template <int W, int ROWS>
 hipError_t launch_down(const MoeProblem &p, hipStream_t s) {
   const long long experts = p.E < p.T * p.top ? p.E : p.T * p.top;
-  return launch_experts(moe_down_kernel<W, ODD>, p, shape_of<W, kF32>(experts, p.H, p.I, p.T), p.H,
+  return launch_experts(moe_down_kernel<W, ROWS>, p, shape_of<W, kF32>(experts, p.H, p.I, p.T), p.H,
                         s);
 }
 
-// Whether a product's 16-bit rows are to be read by whole words (Eight<true>):
+// Whether a product's 16-bit rows are to be read by whole words (Eight<kOdd>):
 // some start in the middle of one, and both matrices start on one.
 bool odd_rows(const void *a, long long a_pitch, const void *b, long long b_pitch) {
   return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 3) == 0 &&
@@ -518,12 +560,19 @@ bool odd_rows(const void *a, long long a_pitch, const void *b, long long b_pitch
 template <int W, int AF>
 hipError_t launch_products(const MoeProblem &p, hipStream_t s) {
   constexpr bool kHalf = W != kMx;
-  const hipError_t e = odd_rows(p.X, 2 * p.ldx, kHalf ? p.W1 : nullptr, kHalf ? p.ld1 : 0)
-                           ? launch_up<W, AF, true>(p, s)
-                           : launch_up<W, AF, false>(p, s);
+  hipError_t e;
+  if (p.H < 8)
+    e = launch_up<W, AF, kShort>(p, s);
+  else if (odd_rows(p.X, 2 * p.ldx, kHalf ? p.W1 : nullptr, kHalf ? p.ld1 : 0))
+    e = launch_up<W, AF, kOdd>(p, s);
+  else
+    e = launch_up<W, AF, kWords>(p, s);
   if (e != hipSuccess) return e;
-  if (kHalf && odd_rows(p.W2, p.ld2, nullptr, 0)) return launch_down<W, kHalf>(p, s);
-  return launch_down<W, false>(p, s);
+  if constexpr (kHalf) {
+    if (p.I < 8) return launch_down<W, kShort>(p, s);
+    if (odd_rows(p.W2, p.ld2, nullptr, 0)) return launch_down<W, kOdd>(p, s);
+  }
+  return launch_down<W, kWords>(p, s);
 }
 
 }  // namespace

@@ -36,7 +36,7 @@ hipError_t in_grid_rows(ThinProblem p, int rows, Launch launch) {
 
 // Few columns: 16 to a workgroup, whose waves share K, WAVES / MB to each of
 // its blocks of 16 rows, with activations straight from memory.
-template <int A, int MB, int WAVES, bool ODD>
+template <int A, int MB, int WAVES, int ROWS>
 __global__ void __launch_bounds__(64 * WAVES) mx_small_kernel(ThinProblem p) {
   constexpr int kShares = WAVES / MB;
   __shared__ f32x4 part[WAVES][64];
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(64 * WAVES) mx_small_kernel(ThinProblem p) {
   const Row w{p.B.codes + n * p.B.ld, p.B.scales + n * p.B.lds};
   const long long m0 = 16LL * (MB * blockIdx.y + wave % MB), m = m0 + l16, mr = m0 + (lane >> 2);
   const unsigned char *a = p.A + (mr < p.M ? mr : p.M - 1) * p.lda;
-  Direct<A, ODD> t;
+  Direct<A, ROWS> t;
   t.acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
   for (int q = wave / MB; q < pieces; q += kShares) t.piece(w, a, q, lane, p.K);
@@ -61,13 +61,13 @@ __global__ void __launch_bounds__(64 * WAVES) mx_small_kernel(ThinProblem p) {
   store4_fmt(p.c_format, p.C, m * p.ldc + col, left < 4 ? left : 4, sum);
 }
 
-template <int A, int MB, bool ODD>
+template <int A, int MB, int ROWS>
 hipError_t launch_small(const ThinProblem &p, hipStream_t s) {
   return in_grid_rows(p, 16 * MB, [&](const ThinProblem &q, unsigned gy) {
     const dim3 grid((unsigned)ceil_div(q.N, 16), gy);
     if (q.K <= 4 / MB * 512)
-      return launch_kernel(mx_small_kernel<A, MB, 4, ODD>, grid, dim3(256), s, q);
-    return launch_kernel(mx_small_kernel<A, MB, 8, ODD>, grid, dim3(512), s, q);
+      return launch_kernel(mx_small_kernel<A, MB, 4, ROWS>, grid, dim3(256), s, q);
+    return launch_kernel(mx_small_kernel<A, MB, 8, ROWS>, grid, dim3(512), s, q);
   });
 }
 
@@ -81,7 +81,7 @@ hipError_t launch_small(const ThinProblem &p, hipStream_t s) {
 // in order: activations waited for behind weights, 64 x 16384 x 8192 took
 // 37.7 us.
 constexpr int kWideWaves = 16, kWideThreads = 64 * kWideWaves, kWideK = 512;
-template <int A, int MB, bool ODD>
+template <int A, int MB, int ROWS>
 struct Wide {
   static constexpr int kRows = 16 * MB, kGroup = 16 * kRows + 16;
   static constexpr int kStage = kWideK / 8 * kGroup, kLoads = kRows / 8;
@@ -97,30 +97,24 @@ struct Wide {
     const unsigned char *codes[2];  // row l / 4
     const unsigned char *scales;
   };
-  typedef Eight<ODD> Acts[kLoads];
+  typedef Eight<ROWS> Acts[kLoads];
 
-  // The staging lane's 16-byte units: number `lane` of rows r0 + 8 i, or where
-  // that passes K the last 8 values (of 8 or more), moved into place later.  No
-  // branch: loads behind one would be waited for as if it had not been taken.
-  static __device__ __forceinline__ long long first(long long k, int K) {
-    return k < K - 8 ? k : K - 8;
-  }
+  // The staging lane's 16-byte units: number `lane` of rows r0 + 8 i.  (No
+  // load behind a branch, here and below: it would be waited for as if it had
+  // not been taken.)
   static __device__ __forceinline__ void load(Acts &v, const unsigned char *const (&row)[kLoads],
                                               long long k0, int lane, int K) {
-    const long long from = 2 * first(k0 + 8 * lane, K);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) v[i].load(row[i] + from);
+    for (int i = 0; i < kLoads; ++i) v[i].load(row[i], k0 + 8 * lane, K);
   }
   // `to`: the place of row r0 in LDS.
-  static __device__ __forceinline__ void keep(unsigned char *to, const Acts &v,
-                                              const unsigned char *const (&row)[kLoads],
-                                              long long k0, int lane, int K) {
+  static __device__ __forceinline__ void keep(unsigned char *to, const Acts &v, long long k0,
+                                              int lane, int K) {
     const int group = (lane & ~15) | (lane & 3) << 2 | (lane >> 2 & 3);
-    const long long k = k0 + 8 * lane, from = first(k, K);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      u32x4 x = v[i].get(row[i] + 2 * from);
-      if (k0 + kWideK > K) x = drop_first(x, k - from);  // uniform
+      u32x4 x = v[i].get();
+      if (k0 + kWideK > K) x = v[i].end(x, k0 + 8 * lane, K);  // uniform
       *reinterpret_cast<u32x4 *>(to + group * kGroup + 16 * 8 * i) = x;
     }
   }
@@ -189,9 +183,9 @@ struct Wide {
   }
 };
 
-template <int A, int MB, bool ODD>
+template <int A, int MB, int ROWS>
 __global__ void __launch_bounds__(kWideThreads) mx_wide_kernel(ThinProblem p) {
-  typedef Wide<A, MB, ODD> Product;
+  typedef Wide<A, MB, ROWS> Product;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];  // two stages
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int l16 = lane & 15, g = lane >> 4, nb = (int)mx_blocks(p.K);
@@ -220,7 +214,7 @@ __global__ void __launch_bounds__(kWideThreads) mx_wide_kernel(ThinProblem p) {
       for (int u = 0; u < 2; ++u) {
         const int now = c + u;
         if (now < chunks)
-          Product::keep(to + u * Product::kStage, v[u], row, (long long)now * kWideK, lane, p.K);
+          Product::keep(to + u * Product::kStage, v[u], (long long)now * kWideK, lane, p.K);
         Product::load(v[u], row, (now + 2LL) * kWideK, lane, p.K);
         __syncthreads();
       }
@@ -280,13 +274,13 @@ __global__ void __launch_bounds__(kWideThreads) mx_wide_kernel(ThinProblem p) {
   }
 }
 
-template <int A, int MB, bool ODD>
+template <int A, int MB, int ROWS>
 hipError_t launch_wide(const ThinProblem &p, hipStream_t s) {
   return in_grid_rows(p, 16 * MB, [&](ThinProblem q, unsigned gy) {
     void *args[] = {&q};
-    return hipLaunchKernel(reinterpret_cast<const void *>(mx_wide_kernel<A, MB, ODD>),
+    return hipLaunchKernel(reinterpret_cast<const void *>(mx_wide_kernel<A, MB, ROWS>),
                            dim3((unsigned)ceil_div(q.N, 64), gy), dim3(kWideThreads), args,
-                           2 * Wide<A, MB, ODD>::kStage, s);
+                           2 * Wide<A, MB, ROWS>::kStage, s);
   });
 }
 
@@ -295,13 +289,13 @@ hipError_t launch_wide(const ThinProblem &p, hipStream_t s) {
 // its start.  Small and wide, us: 64 x 4096 x 8192 25.0 and 26.7, 64 x 6144 x
 // 8192 35.9 and 27.7, 64 x 8192 x 512 5.0 and 6.1, x 1024 7.7 and 7.4, 16 x 8192
 // x 8192 16.3 and 17.6, 16 x 16384 x 8192 28.3 and 20.4.
-template <int A, bool ODD>
+template <int A, int ROWS>
 hipError_t launch_a16(const ThinProblem &p, hipStream_t s) {
   const long long groups = ceil_div(p.N, 64) * ceil_div(p.M, 64);
   const bool wide = groups >= (p.M <= 16 ? 192 : 96) && p.K >= 8 &&
                     ceil_div(p.N, 16) * ceil_div(p.M, 32) * p.K >= 1 << 20;
-  if (wide) return p.M <= 32 ? launch_wide<A, 2, ODD>(p, s) : launch_wide<A, 4, ODD>(p, s);
-  return p.M <= 16 ? launch_small<A, 1, ODD>(p, s) : launch_small<A, 2, ODD>(p, s);
+  if (wide) return p.M <= 32 ? launch_wide<A, 2, ROWS>(p, s) : launch_wide<A, 4, ROWS>(p, s);
+  return p.M <= 16 ? launch_small<A, 1, ROWS>(p, s) : launch_small<A, 2, ROWS>(p, s);
 }
 
 // ---- few rows of MX by MX ------------------------------------------------------
@@ -446,8 +440,8 @@ hipError_t launch_mx_a16(const MxA16Problem &p, hipStream_t s) {
   const ThinProblem t{p.M, p.N, p.K, reinterpret_cast<const unsigned char *>(p.A), 2 * p.lda,
                       p.B, p.C, p.ldc, p.c_format};
   if (odd_rows(p.A, 2 * p.lda) && p.M > 1)
-    return p.a_format == kBf16 ? launch_a16<kBf16, true>(t, s) : launch_a16<kF16, true>(t, s);
-  return p.a_format == kBf16 ? launch_a16<kBf16, false>(t, s) : launch_a16<kF16, false>(t, s);
+    return p.a_format == kBf16 ? launch_a16<kBf16, kOdd>(t, s) : launch_a16<kF16, kOdd>(t, s);
+  return p.a_format == kBf16 ? launch_a16<kBf16, kWords>(t, s) : launch_a16<kF16, kWords>(t, s);
 }
 
 hipError_t launch_mx_thin(const MxProblem &p, hipStream_t s) {

@@ -112,45 +112,55 @@ __device__ inline u32x4 load_guarded(const unsigned char *row, long long k, int 
   return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
-// 8 values of a row of 16-bit codes.  ODD: rows that may start in the middle
-// of a 4-byte word, where a 16-byte load costs a multiple of an aligned one:
-// the words around them are loaded, from 2 bytes before the first value on
-// (the row before, or its padding: only rows after the first can be odd,
-// because the matrix starts on a word), with the last value on its own.
-template <bool ODD>
+// How the rows of 16-bit codes lie: kWords: a 16-byte load of 8 of them is
+// cheap, or as cheap as any.  kOdd: rows that may start in the middle of a 4-byte
+// word, where a 16-byte load costs a multiple of an aligned one.  kShort: of
+// fewer than 8 codes.
+enum { kWords, kOdd, kShort };
+
+// Values k .. k + 7 of a row of K codes, or the last 8 where those pass K:
+// `end` then moves them into place and adds the zeros.
+template <int ROWS>
 struct Eight {
   u32x4 v;
-  __device__ __forceinline__ void load(const unsigned char *at) {
-    v = *reinterpret_cast<const u32x4h *>(at);
+  static __device__ __forceinline__ long long first(long long k, int K) {
+    return k < K - 8 ? k : K - 8;
   }
-  __device__ __forceinline__ u32x4 get(const unsigned char *) const { return v; }
-  __device__ __forceinline__ void set(u32x4 x, const unsigned char *) { v = x; }
+  __device__ __forceinline__ void load(const unsigned char *row, long long k, int K) {
+    v = *reinterpret_cast<const u32x4h *>(row + 2 * first(k, K));
+  }
+  __device__ __forceinline__ u32x4 get() const { return v; }
+  static __device__ __forceinline__ u32x4 end(u32x4 x, long long k, int K) {
+    return drop_first(x, k - first(k, K));
+  }
 };
+// The words around the values, from 2 bytes before the first on where that is
+// in the middle of one (the row before, or its padding: only rows after the
+// first can be odd, because the matrix starts on a word), with the last value on
+// its own.
 template <>
-struct Eight<true> {
-  u32x4 v;
-  uint32_t last;
-  static __device__ __forceinline__ uint32_t shift(const unsigned char *at) {
-    return ((uint32_t)(uintptr_t)at & 2u) * 8u;
-  }
-  __device__ __forceinline__ void load(const unsigned char *at) {
+struct Eight<kOdd> : Eight<kWords> {
+  uint32_t last, shift;
+  __device__ __forceinline__ void load(const unsigned char *row, long long k, int K) {
+    const unsigned char *at = row + 2 * first(k, K);
     const uintptr_t odd = reinterpret_cast<uintptr_t>(at) & 2;
     v = *reinterpret_cast<const u32x4w *>(at - odd);
     last = *reinterpret_cast<const uint16_t *>(at + 14);
+    shift = 8 * (uint32_t)odd;
   }
-  __device__ __forceinline__ void set(u32x4 x, const unsigned char *at) {
-    const bool odd = shift(at) != 0;
-    v = odd ? u32x4{x[0] << 16, x[0] >> 16 | x[1] << 16, x[1] >> 16 | x[2] << 16,
-                    x[2] >> 16 | x[3] << 16}
-            : x;
-    last = x[3] >> 16;
+  __device__ __forceinline__ u32x4 get() const {
+    return u32x4{__builtin_amdgcn_alignbit(v[1], v[0], shift),
+                 __builtin_amdgcn_alignbit(v[2], v[1], shift),
+                 __builtin_amdgcn_alignbit(v[3], v[2], shift),
+                 __builtin_amdgcn_alignbit(last, v[3], shift)};
   }
-  // `at`: any address of the row, for its alignment.
-  __device__ __forceinline__ u32x4 get(const unsigned char *at) const {
-    const uint32_t s = shift(at);
-    return u32x4{__builtin_amdgcn_alignbit(v[1], v[0], s), __builtin_amdgcn_alignbit(v[2], v[1], s),
-                 __builtin_amdgcn_alignbit(v[3], v[2], s), __builtin_amdgcn_alignbit(last, v[3], s)};
+};
+template <>
+struct Eight<kShort> : Eight<kWords> {
+  __device__ __forceinline__ void load(const unsigned char *row, long long k, int K) {
+    v = load_guarded(row, k < K ? k : K, K);
   }
+  static __device__ __forceinline__ u32x4 end(u32x4 x, long long, int) { return x; }
 };
 
 // How the values of MX weights become matrix operands.  As bf16 or fp16 by
@@ -258,6 +268,65 @@ struct MxBlocks {
   }
 };
 
+// A piece of 16 rows of 16-bit weights as loaded: values 32 j + 8 (l % 4) ..
+// + 7 of it, j = 0 .. 3; or the last 8 of the row where those pass K.
+template <int ROWS>
+struct HalfPiece {
+  Eight<ROWS> x[4];
+  static __device__ __forceinline__ long long at(int piece, int j, int lane) {
+    return 128LL * piece + 32 * j + 8 * (lane & 3);
+  }
+  __device__ __forceinline__ void load(const unsigned char *row, int piece, int lane, int K) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j].load(row, at(piece, j, lane), K);
+  }
+  // For the piece that passes K: moves what it holds into place.
+  __device__ __forceinline__ void end(const unsigned char *, int piece, int lane, int K) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j].v = x[j].end(x[j].v, at(piece, j, lane), K);
+  }
+  __device__ __forceinline__ u32x4 get(int j, int) const { return x[j].get(); }
+};
+// The words around the values, as in Eight<kOdd>; the last value is the first
+// of the next lane's words, and the piece's last a load of its own (one of each
+// lane's: 71 us for the loads of a first product of 268 MB, against 53 of even
+// rows).
+template <>
+struct HalfPiece<kOdd> {
+  u32x4 v[4];
+  uint32_t last, shift;
+  __device__ __forceinline__ void load(const unsigned char *row, int piece, int lane, int K) {
+    const uintptr_t odd = reinterpret_cast<uintptr_t>(row) & 2;
+    shift = 8 * (uint32_t)odd;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const long long k = HalfPiece<kWords>::at(piece, j, lane), most = (K - 8) & ~1;
+      v[j] = *reinterpret_cast<const u32x4w *>(row - odd + 2 * (k < most ? k : most));
+    }
+    const long long k = 128LL * piece + 127;
+    last = *reinterpret_cast<const uint16_t *>(row + 2 * (k < K ? k : K - 1));
+  }
+  // What it holds is of no use there, but its lines are at hand.
+  __device__ __forceinline__ void end(const unsigned char *row, int piece, int lane, int K) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const long long k = HalfPiece<kWords>::at(piece, j, lane);
+      v[j] = load_guarded(row, k < K ? k : K, K);
+    }
+    shift = 0;
+  }
+  __device__ __forceinline__ u32x4 get(int j, int lane) const {
+    const uint32_t next = j < 3 ? v[j < 3 ? j + 1 : j][0] : last;
+    const uint32_t word = (lane & 3) == 0 ? next : v[j][0];
+    // of lane + 1, in each four
+    const uint32_t w4 = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)word, 0x39, 0xf, 0xf, false);
+    return u32x4{__builtin_amdgcn_alignbit(v[j][1], v[j][0], shift),
+                 __builtin_amdgcn_alignbit(v[j][2], v[j][1], shift),
+                 __builtin_amdgcn_alignbit(v[j][3], v[j][2], shift),
+                 __builtin_amdgcn_alignbit(w4, v[j][3], shift)};
+  }
+};
+
 // ---- activations in LDS --------------------------------------------------------
 //
 // Blocks of up to 16 rows, `rows` of them kept (4 or 16), of kc values: for
@@ -278,41 +347,31 @@ __host__ __device__ inline int act_bytes(const Tile &t) {
 }
 
 // Fills a block with values k0 .. k0 + kc - 1 of rows 0 .. n - 1, zeros past K;
-// `row(r)` gives row r's start.  All THREADS
-// threads of the workgroup take part; each issues four loads before it writes
-// any (one at a time, their latencies alone took 30 us of a first product).
-// Rows of kind kF32 hold zeros from K to a multiple of 8.
-template <int A, int W, bool ODD, int THREADS, class RowOf>
+// `row(r)` gives row r's start.  All THREADS threads of the workgroup take
+// part; each issues eight loads before it writes any (one at a time, their
+// latencies alone took 30 us of a first product).  Rows of kind kF32 hold
+// zeros from K to a multiple of 8.
+template <int A, int W, int ROWS, int THREADS, class RowOf>
 __device__ __forceinline__ void stage_acts(unsigned char *lds, const Tile &t, RowOf row, int n,
                                            int k0, int K) {
-  constexpr int kBatch = 4;
+  constexpr int kBatch = A == kF32 ? 4 : 8;
   const int G = t.group();
   const int per = t.kc / 8, all = n * per, eights = (int)ceil_div(K, 8);
 #pragma unroll 1
   for (int i0 = threadIdx.x; i0 < all; i0 += kBatch * THREADS) {
-    u32x4 c[kBatch], d[kBatch];
+    Eight<ROWS> c[kBatch];
+    u32x4 d[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int i = i0 + u * THREADS < all ? i0 + u * THREADS : all - 1;
       const int r = i / per, x = i % per;
-      const Row src = row(r);
       if constexpr (A == kF32) {
         const int e = k0 / 8 + x, in = e < eights ? e : eights - 1;
-        const u32x4w *q = reinterpret_cast<const u32x4w *>(src.p + 32LL * in);
-        c[u] = q[0];
+        const u32x4w *q = reinterpret_cast<const u32x4w *>(row(r) + 32LL * in);
+        c[u].v = q[0];
         d[u] = q[1];
       } else {
-        const long long k = k0 + 8LL * x;
-        if constexpr (ODD) {
-          if (k + 8 <= K) {
-            Eight<true> v;
-            v.load(src.p + 2 * k);
-            c[u] = v.v;
-            d[u][0] = v.last;
-          }
-        } else if (k + 8 <= K) {
-          c[u] = *reinterpret_cast<const u32x4h *>(src.p + 2 * k);
-        }
+        c[u].load(row(r), k0 + 8LL * x, K);
       }
     }
 #pragma unroll
@@ -320,30 +379,22 @@ __device__ __forceinline__ void stage_acts(unsigned char *lds, const Tile &t, Ro
       const int i = i0 + u * THREADS;
       if (i >= all) continue;
       const int r = i / per, x = i % per;
-      {
-        // Operand and lane group of values 8 x .. 8 x + 7: the MX order of k
-        // is (step, g, j), the 16-bit one (j, g).
-        const int group = W == kMx ? (x & ~15) | (x & 3) << 2 | (x >> 2 & 3) : x;
-        u32x4 *to = reinterpret_cast<u32x4 *>(lds + group * G + 16 * r);
-        if constexpr (A == kF32) {
-          const bool in = k0 / 8 + x < eights;
-          u32x4 hi, lo;
-          split_f32(c[u], d[u], hi, lo);
-          *to = in ? hi : u32x4{0, 0, 0, 0};
-          *reinterpret_cast<u32x4 *>(lds + per * G + group * G + 16 * r) =
-              in ? lo : u32x4{0, 0, 0, 0};
-        } else {
-          const long long k = k0 + 8LL * x;
-          if (k + 8 > K) {
-            c[u] = load_guarded(row(r).p, k < K ? k : K, K);
-          } else if constexpr (ODD) {
-            Eight<true> v;
-            v.v = c[u];
-            v.last = d[u][0];
-            c[u] = v.get(row(r).p);
-          }
-          *to = c[u];
-        }
+      // Operand and lane group of values 8 x .. 8 x + 7: the MX order of k
+      // is (step, g, j), the 16-bit one (j, g).
+      const int group = W == kMx ? (x & ~15) | (x & 3) << 2 | (x >> 2 & 3) : x;
+      u32x4 *to = reinterpret_cast<u32x4 *>(lds + group * G + 16 * r);
+      if constexpr (A == kF32) {
+        const bool in = k0 / 8 + x < eights;
+        u32x4 hi, lo;
+        split_f32(c[u].v, d[u], hi, lo);
+        *to = in ? hi : u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4 *>(lds + per * G + group * G + 16 * r) =
+            in ? lo : u32x4{0, 0, 0, 0};
+      } else {
+        const long long k = k0 + 8LL * x;
+        u32x4 v = c[u].get();
+        if (k + 8 > K) v = c[u].end(v, k, K);
+        *to = v;
       }
     }
   }
@@ -351,25 +402,24 @@ __device__ __forceinline__ void stage_acts(unsigned char *lds, const Tile &t, Ro
 
 // ---- the product -----------------------------------------------------------------
 
-// MB blocks of rows of kind A in LDS by NB blocks of 16 rows of weights of
-// kind W in registers.
-template <int W, int A, int MB, int NB, bool ODD>
+// A block of rows of kind A in LDS by NB blocks of 16 rows of weights of kind
+// W in registers.  No load stands behind a branch: one that may or may not
+// have been issued makes the compiler wait for all, the next piece's too.
+template <int W, int A, int NB, int ROWS>
 struct Thin {
   static constexpr int kK = kPieceK<W>, kSteps = kPieceSteps<W>;
   struct Weights {
     MxPiece mx[W == kMx ? NB : 1];
-    Eight<ODD> half[W == kMx ? 1 : NB][4];
+    HalfPiece<ROWS> half[W == kMx ? 1 : NB];
   };
-  f32x4 acc[MB][NB];
+  f32x4 acc[NB];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < NB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // A piece's weights, zeros past K.
+  // A piece's weights.
   static __device__ __forceinline__ void load(Weights &x, const Row (&w)[NB], int piece, int lane,
                                               int K) {
     const int nb = (int)mx_blocks(K);
@@ -378,36 +428,33 @@ struct Thin {
       if constexpr (W == kMx) {
         x.mx[b].load(w[b], piece, lane, nb);
       } else {
-        const long long k0 = (long long)kK * piece + 8 * (lane & 3);
-        if (piece < K / kK) {  // uniform
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x.half[b][j].load(w[b].p + 2 * (k0 + 32 * j));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const long long k = k0 + 32 * j;
-            x.half[b][j].set(load_guarded(w[b].p, k < K ? k : K, K), w[b].p);
-          }
-        }
+        x.half[b].load(w[b].p, piece, lane, K);
       }
     }
   }
 
-  // The products of a loaded piece, number `local` of the tile.
-  __device__ __forceinline__ void use(const Weights &x, const Row (&w)[NB],
-                                      const unsigned char *lds, const Tile &t, int local, int piece,
-                                      int lane, int K) {
-    const int g = lane >> 4, r = lane & (t.rows - 1), G = t.group(), block = act_bytes<A>(t);
+  // The products of a loaded piece, number `local` of the tile; zeros past K.
+  // `rows` gives the rows w once more.
+  template <class RowsOf>
+  __device__ __forceinline__ void use(Weights &x, RowsOf rows, const unsigned char *lds,
+                                      const Tile &t, int local, int piece, int lane, int K) {
+    const int g = lane >> 4, r = lane & (t.rows - 1), G = t.group();
     constexpr Widen kHow = W == kF16 || (W == kMx && A == kF16) ? kToF16 : kToBf16;
     const unsigned char *from = lds + (local * kSteps * 16 + g) * G + 16 * r;
     const int lo = t.kc / 8 * G;
     if constexpr (W != kMx) {
+      if (piece >= K / kK) {  // uniform
+        Row w[NB];
+        rows(w);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) x.half[b].end(w[b].p, piece, lane, K);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         u32x4 wv[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) wv[b] = from_lane(x.half[b][j].get(w[b].p), loader(lane));
-        multiply<kHow>(wv, from + j * 4 * G, block, lo);
+        for (int b = 0; b < NB; ++b) wv[b] = from_lane(x.half[b].get(j, lane), loader(lane));
+        multiply<kHow>(wv, from + j * 4 * G, lo);
       }
     } else {
       const MxBlocks y0(x.mx[0], piece, lane, (int)mx_blocks(K));
@@ -425,7 +472,7 @@ struct Thin {
             u32x4 wv[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) wv[b] = widen<kHow>(y[b]->c[s][j], y[b]->s[s]);
-            multiply<kHow>(wv, from + (4 * s + j) * 4 * G, block, lo);
+            multiply<kHow>(wv, from + (4 * s + j) * 4 * G, lo);
           }
       } else {
         // Rare, and kept short: a loop over the piece's words.
@@ -442,7 +489,7 @@ struct Thin {
             }
             wv[b] = widen<kThroughF32>(c, sb);
           }
-          multiply<kThroughF32>(wv, from + i * 4 * G, block, lo);
+          multiply<kThroughF32>(wv, from + i * 4 * G, lo);
         }
       }
     }
@@ -452,81 +499,28 @@ struct Thin {
   // the format that the weights come in or were brought to.
   template <Widen HOW>
   __device__ __forceinline__ void multiply(const u32x4 (&wv)[NB], const unsigned char *at,
-                                           int block, int lo_plane) {
+                                           int lo_plane) {
     constexpr bool kSplitHere = A == kF16 && HOW != kToF16;
+    u32x4 v = *reinterpret_cast<const u32x4 *>(at), lo{};
+    if constexpr (A == kF32) lo = *reinterpret_cast<const u32x4 *>(at + lo_plane);
+    if constexpr (kSplitHere) split_f16(v, v, lo);
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      u32x4 v = *reinterpret_cast<const u32x4 *>(at + i * block), lo{};
-      if constexpr (A == kF32) lo = *reinterpret_cast<const u32x4 *>(at + i * block + lo_plane);
-      if constexpr (kSplitHere) split_f16(v, v, lo);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if constexpr (A == kF32 && HOW == kToF16) {
-          // fp16 weights are split too; the product of the two low parts,
-          // 2^-18 of the whole, is left out
-          u32x4 wh, wl;
-          split_f16(wv[b], wh, wl);
-          acc[i][b] = mfma_bf16(wh, v, acc[i][b]);
-          acc[i][b] = mfma_bf16(wh, lo, acc[i][b]);
-          acc[i][b] = mfma_bf16(wl, v, acc[i][b]);
-        } else if constexpr (HOW == kToF16) {
-          acc[i][b] = mfma_f16(wv[b], v, acc[i][b]);
-        } else {
-          acc[i][b] = mfma_bf16(wv[b], v, acc[i][b]);
-          if constexpr (A == kF32 || kSplitHere) acc[i][b] = mfma_bf16(wv[b], lo, acc[i][b]);
-        }
+    for (int b = 0; b < NB; ++b) {
+      if constexpr (A == kF32 && HOW == kToF16) {
+        // fp16 weights are split too; the product of the two low parts,
+        // 2^-18 of the whole, is left out
+        u32x4 wh, wl;
+        split_f16(wv[b], wh, wl);
+        acc[b] = mfma_bf16(wh, v, acc[b]);
+        acc[b] = mfma_bf16(wh, lo, acc[b]);
+        acc[b] = mfma_bf16(wl, v, acc[b]);
+      } else if constexpr (HOW == kToF16) {
+        acc[b] = mfma_f16(wv[b], v, acc[b]);
+      } else {
+        acc[b] = mfma_bf16(wv[b], v, acc[b]);
+        if constexpr (A == kF32 || kSplitHere) acc[b] = mfma_bf16(wv[b], lo, acc[b]);
       }
     }
-  }
-
-  // How a workgroup's waves go through K.
-  struct Walk {
-    int first, ks;  // this wave takes pieces first, first + ks, ...
-    bool any;       // whether this wave has columns at all
-    bool staged;    // the tile already holds all of K
-  };
-  // Adds all K values, from `x`, which holds the wave's first piece, on.  At
-  // the end `x` holds the first piece of the rows `next`.  `row(r)` gives row
-  // r of n activations.  Every wave of the workgroup makes the call.
-  template <int THREADS, class RowOf>
-  __device__ __forceinline__ void run(unsigned char *lds, const Tile &t, RowOf row, int n,
-                                      const Row (&w)[NB], const Row (&next)[NB], Weights &x,
-                                      const Walk &at, int K, int lane) {
-    const int pieces = (int)ceil_div(K, kK);
-    const int rounds = (int)ceil_div(pieces, at.ks), per = t.kc / (kK * at.ks);
-    const int block = act_bytes<A>(t);
-#pragma unroll 1
-    for (int i0 = 0; i0 < rounds; i0 += per) {
-      if (!at.staged) {
-        __syncthreads();
-#pragma unroll 1
-        for (int m = 0; m < MB && n > 16 * m; ++m)
-          stage_acts<A, W, ODD, THREADS>(
-              lds + m * block, t, [&](int r) { return row(16 * m + r); },
-              n - 16 * m < 16 ? n - 16 * m : 16, i0 * at.ks * kK, K);
-        __syncthreads();
-      }
-      if (!at.any) continue;
-      const int end = i0 + per < rounds ? i0 + per : rounds;
-#pragma unroll 1
-      for (int i = i0; i < end; ++i) {
-        const int p = at.first + i * at.ks;
-        const bool last = i + 1 == rounds;
-        const int q = last ? (at.first < pieces ? at.first : 0) : p + at.ks < pieces ? p + at.ks : 0;
-        Row from[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) from[b] = last ? next[b] : w[b];
-        Weights y;
-        load(y, from, q, lane, K);
-        if (p < pieces) use(x, w, lds, t, (i - i0) * at.ks + at.first, p, lane, K);
-        x = y;  // the next piece, needed at once
-      }
-    }
-  }
-  static __device__ __forceinline__ void load_first(Weights &x, const Row (&w)[NB], const Walk &at,
-                                                    int K, int lane) {
-    const int pieces = (int)ceil_div(K, kK);
-    if (at.any) load(x, w, at.first < pieces ? at.first : 0, lane, K);
   }
 };
 
@@ -535,7 +529,7 @@ struct Thin {
 // weights and activations are asked for together, both by four lanes to a
 // line.  MFMA m of step s takes block 4 s + m of the piece here, lane l its
 // values 8 (l / 16) .. + 7, so that one lane's load holds one lane's operand.
-template <int A, bool ODD>
+template <int A, int ROWS>
 struct Direct {
   f32x4 acc;
   // The products of 8 values per lane, of MX words that allow `kHow` or not.
@@ -558,11 +552,11 @@ struct Direct {
     const uint32_t s = *reinterpret_cast<const uint32_t *>(w.q + 16LL * piece + 4 * part);
     if (512LL * (piece + 1) <= K) {  // uniform
       uint32_t c[16], sc[4];
-      Eight<ODD> v[16];
+      Eight<ROWS> v[16];
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         c[q] = *reinterpret_cast<const uint32_t *>(w.p + 16 * (16LL * piece + q) + 4 * part);
-        v[q].load(a + 2 * (32 * (16LL * piece + q) + 8 * part));
+        v[q].load(a, 32 * (16LL * piece + q) + 8 * part, K);
       }
       bool ok = true;
 #pragma unroll
@@ -578,7 +572,7 @@ struct Direct {
 #pragma unroll
         for (int q = 0; q < 16; ++q)
           add<A == kF16 ? kToF16 : kToBf16>(from_lane(c[q], from), sc[q >> 2] >> (8 * (q & 3)) & 255u,
-                                            from_lane(v[q].get(a), from));
+                                            from_lane(v[q].get(), from));
         return;
       }
     }
