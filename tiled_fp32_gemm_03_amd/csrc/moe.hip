@@ -295,8 +295,14 @@ __global__ void __launch_bounds__(kListThreads) moe_list_kernel(MoeProblem p) {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
-// What the launch chose: waves per group, groups per wave, and the LDS for
-// activations.
+// Two workgroups to a compute unit: one streams while the other stages its
+// activations; the LDS that leaves each for its tile, and the most that a tile
+// which needs more may take.
+template <int A>
+constexpr int kTileLds = A == kF32 ? 48 * 1024 : 74 * 1024;
+constexpr int kMostLds = 140 * 1024;
+
+// What the launch chose: waves per group, groups per wave, the tile's LDS.
 struct MoeShape {
   int ks, each, lds;
 };
@@ -324,16 +330,16 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
                                                WeightsOf weights, Done done) {
   typedef Thin<W, A, NB, ROWS> Product;
   constexpr int kK = Product::kK;
-  __shared__ f32x4 part[kWaves][NB][64];
   const int lane = threadIdx.x & 63, wave = wave_id();
-  // As much of K as the launch's LDS holds of this many rows.
-  const int ks = sh.ks, keep = n <= 4 ? 4 : 16;
-  const Tile tile{keep, tile_values<A>(keep, K, ks * kK, sh.lds)};
+  const int ks = sh.ks;
+  const Tile tile = tile_of<A>(tile_rows(n), K, ks * kK, kTileLds<A>);
   const bool whole = tile.kc >= K;
+  f32x4 *part = reinterpret_cast<f32x4 *>(lds + sh.lds);  // [kWaves][NB][64], if ks > 1
   const int side = kWaves / ks;  // groups side by side
   const int c0 = (int)blockIdx.x * side * sh.each + wave / ks, first = wave & (ks - 1);
-  // A wave's turns: for each of its groups, pieces first, first + ks, ...
-  const int pieces = (int)ceil_div(K, kK), rounds = (int)ceil_div(pieces, ks);
+  // A wave's turns: for each of its groups, pieces first, first + ks, ... (an even number of rounds, and of rounds in a tile, unless it holds all).
+  const int pieces = (int)ceil_div(K, kK), need = (int)ceil_div(pieces, ks);
+  const int rounds = whole ? need : (need + 1) & ~1;
   const int per = tile.kc / (kK * ks);  // rounds in a tile
   struct Turn {
     int group, round;
@@ -367,14 +373,14 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
   t.clear();
 #pragma unroll 1
   while (now.group < sh.each) {
+    if (!whole && now.round % per == 0 && now.round + now.group > 0) {
+      __syncthreads();
+      stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, now.round * ks * kK, K);
+      __syncthreads();
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {  // a turn past the end multiplies nothing
       if (now.group < sh.each) {
-        if (now.round % per == 0 && now.round + now.group > 0 && !whole) {
-          __syncthreads();
-          stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, now.round * ks * kK, K);
-          __syncthreads();
-        }
         const int c = c0 + now.group * side;
         if (c < groups && piece(now) < pieces)
           t.use(x[u], [&](Row (&w)[NB]) { weights(c, w); }, lds, tile, now.round % per * ks + first, piece(now), lane, K);
@@ -382,12 +388,12 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
           if (ks > 1) {  // the waves' sums, added in wave order
             __syncthreads();
 #pragma unroll
-            for (int b = 0; b < NB; ++b) part[wave][b][lane] = t.acc[b];
+            for (int b = 0; b < NB; ++b) part[(wave * NB + b) * 64 + lane] = t.acc[b];
             __syncthreads();
             if (first == 0)
               for (int q = 1; q < ks; ++q)
 #pragma unroll
-                for (int b = 0; b < NB; ++b) t.acc[b] += part[wave + q][b][lane];
+                for (int b = 0; b < NB; ++b) t.acc[b] += part[((wave + q) * NB + b) * 64 + lane];
           }
           if (c < groups && first == 0 && (lane & 15) < n) done(c, t.acc);
           t.clear();
@@ -404,7 +410,7 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
 // makes the choice itself, one of them writes it, and the pairs are listed in
 // the order of the choice.
 template <int W, int AF, bool ONE, int ROWS>
-__global__ void __launch_bounds__(kThreads, 3) moe_up_kernel(MoeProblem p, MoeShape sh) {
+__global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeProblem p, MoeShape sh) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ Route<kMoeMaxTop> route;
   __shared__ long long starts[16];  // of the tokens' rows
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 3) moe_up_kernel(MoeProblem p, MoeSh
 
 // Second product: each pair's result, before its gate.
 template <int W, int ROWS>
-__global__ void __launch_bounds__(kThreads, 3) moe_down_kernel(MoeProblem p, MoeShape sh) {
+__global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(MoeProblem p, MoeShape sh) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   Expert x;
   if (!expert_of(p, blockIdx.y, x)) return;
@@ -510,6 +516,16 @@ hipError_t launch_logits(const MoeProblem &p, hipStream_t s) {
                        s, p);
 }
 
+// The LDS of a product of up to `rows` rows to an expert.
+template <int W, int A>
+int tile_bytes(int rows, int K, int ks) {
+  int most = 0;
+  for (int keep = 4; keep <= tile_rows(rows); keep *= 2) {
+    const int bytes = act_bytes<A>(tile_of<A>(keep, K, ks * kPieceK<W>, kTileLds<A>));
+    most = most < bytes ? bytes : most;
+  }
+  return most;
+}
 // The shape of a product over `experts` experts, `columns` columns and K, of
 // at most `rows` rows each.
 template <int W, int A>
@@ -517,37 +533,34 @@ MoeShape shape_of(long long experts, int columns, int K, int rows) {
   const long long groups = experts * ceil_div(columns, 16);
   MoeShape sh;
   sh.ks = waves_per_group(groups, K, kPieceK<W>, kWaves, 8 * 256);
-  // Groups per wave: while workgroups are left for three on each compute unit.
+  while (sh.ks > 1 && tile_bytes<W, A>(rows, K, sh.ks) > kMostLds) sh.ks /= 2;
+  // Groups per wave: while workgroups are left for two on each compute unit.
   sh.each = 1;
-  while (sh.each < 8 && groups * sh.ks / kWaves / (2 * sh.each) >= 3 * 256) sh.each *= 2;
-  const int round = sh.ks * kPieceK<W>;
-  const int keep = rows <= 4 ? 4 : 16;
-  sh.lds = act_bytes<A>(Tile{keep, tile_values<A>(keep, K, round, 48 * 1024)});
+  while (groups * sh.ks / kWaves / (2 * sh.each) >= 2 * 256) sh.each *= 2;
+  sh.lds = tile_bytes<W, A>(rows, K, sh.ks);
   return sh;
 }
-template <class Kernel>
-hipError_t launch_experts(Kernel kern, const MoeProblem &p, MoeShape sh, int columns, hipStream_t s) {
-  const int pairs = p.T * p.top;
+template <int W, int A, int NB, class Kernel>
+hipError_t launch_experts(Kernel kern, const MoeProblem &p, int columns, int K, hipStream_t s) {
+  const int experts = p.E < p.T * p.top ? p.E : p.T * p.top;
+  MoeShape sh = shape_of<W, A>(experts, columns, K, p.T);
   MoeProblem q = p;
   void *args[] = {&q, &sh};
   const dim3 grid((unsigned)ceil_div(ceil_div(columns, 16), kWaves / sh.ks * sh.each),
-                  (unsigned)(p.E < pairs ? p.E : pairs));
+                  (unsigned)experts);
   return hipLaunchKernel(reinterpret_cast<const void *>(kern), grid, dim3(kThreads), args,
-                         (size_t)sh.lds, s);
+                         (size_t)(sh.lds + (sh.ks > 1 ? kWaves * NB * 1024 : 0)), s);
 }
 
 template <int W, int AF, int ROWS>
 hipError_t launch_up(const MoeProblem &p, hipStream_t s) {
-  const long long experts = p.E < p.T * p.top ? p.E : p.T * p.top;
-  return launch_experts(p.T == 1 ? moe_up_kernel<W, AF, true, ROWS>
-                                 : moe_up_kernel<W, AF, false, ROWS>,
-                        p, shape_of<W, AF>(experts, p.I, p.H, p.T), p.I, s);
+  return launch_experts<W, AF, 2>(p.T == 1 ? moe_up_kernel<W, AF, true, ROWS>
+                                        : moe_up_kernel<W, AF, false, ROWS>,
+                               p, p.I, p.H, s);
 }
 template <int W, int ROWS>
 hipError_t launch_down(const MoeProblem &p, hipStream_t s) {
-  const long long experts = p.E < p.T * p.top ? p.E : p.T * p.top;
-  return launch_experts(moe_down_kernel<W, ROWS>, p, shape_of<W, kF32>(experts, p.H, p.I, p.T), p.H,
-                        s);
+  return launch_experts<W, kF32, 1>(moe_down_kernel<W, ROWS>, p, p.H, p.I, s);
 }
 
 // Whether a product's 16-bit rows are to be read by whole words (Eight<kOdd>):

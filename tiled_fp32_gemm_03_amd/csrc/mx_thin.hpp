@@ -329,7 +329,7 @@ struct HalfPiece<kOdd> {
 
 // ---- activations in LDS --------------------------------------------------------
 //
-// Blocks of up to 16 rows, `rows` of them kept (4 or 16), of kc values: for
+// Blocks of up to 16 rows, `rows` of them kept (4, 8 or 16), of kc values: for
 // each operand of a matrix instruction (piece, step, MFMA j) and lane group,
 // the rows' 16 bytes one after the other, and 16 bytes of padding, so that
 // neither the writes (neighbouring threads take neighbouring k of a row) nor
@@ -597,12 +597,14 @@ inline int waves_per_group(long long groups, int K, int piece, int most, int wan
   while (ks < most && groups * ks < want && (long long)2 * ks * piece <= K) ks *= 2;
   return ks;
 }
-// Values of the activations' tile: all of K where it fits `bytes`, else as many
-// whole rounds (pieces of all waves that share columns) as do, one at least.
+// Rows of the tile for n rows.
+__host__ __device__ inline int tile_rows(int n) { return n <= 4 ? 4 : n <= 8 ? 8 : 16; }
+// The activations' tile: all of K where it fits `bytes`, else as many pairs of
+// rounds (pieces of all waves that share columns) as do, one at least.
 template <int A>
-__host__ __device__ inline int tile_values(int rows, int K, int round, int bytes) {
+__host__ __device__ inline Tile tile_of(int rows, int K, int round, int bytes) {
   const int all = (int)ceil_div(K, round), fit = bytes / act_bytes<A>(Tile{rows, round});
-  return round * (all < fit ? all : fit > 1 ? fit : 1);
+  return Tile{rows, round * (all <= fit ? all : fit > 3 ? fit & ~1 : all < 2 ? all : 2)};
 }
 
 }  // namespace
