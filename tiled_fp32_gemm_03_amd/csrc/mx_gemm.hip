@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxProblem p, int tiles_m, 
 #pragma unroll
           for (int j = 0; j < TB; ++j)
             acc[i][j] = mfma_mx(fb[z][j], xb[z][j], fa[z][i], xa[z][i], acc[i][j]);
-          constexpr int kPerRow = (2 * W::DMA + TB * W::KG - 1) / (TB * W::KG);
+          constexpr int kPerRow = 2;  // 8192 cubed: 289 us, one by one 302, four 309
           const int row = kg * TB + i;
           if (row * kPerRow < 2 * W::DMA) {
             __builtin_amdgcn_sched_barrier(0);
@@ -338,7 +338,25 @@ hipError_t launch_mx_zero(void *C, int M, int N, long long ldc, int c_format, hi
 
 hipError_t launch_mx_gemm(int entry, const MxProblem &p, hipStream_t s) {
   if (entry == 3) return launch_mx_thin(p, s);
-  if (entry == 1 && mx_tile_fits<128>(p)) return launch_mx_tiles<128>(p, s);
+  if (entry == 1 && mx_tile_fits<128>(p)) {
+    // A few rows past whole tiles would cost every column of tiles one more:
+    // where that is another round of tiles, the few-row form takes them.
+    const int rest = p.M % 256;
+    const long long tn = ceil_div(p.N, 256), rounds = ceil_div(ceil_div(p.M, 256) * tn, 256);
+    if (rest != 0 && rest <= 32 && ceil_div(p.M / 256 * tn, 256) < rounds) {
+      MxProblem q = p;
+      q.M -= rest;
+      const hipError_t e = launch_mx_tiles<128>(q, s);
+      if (e != hipSuccess) return e;
+      const size_t size = p.c_format == kF32 ? 4 : 2;
+      q.A.codes += q.M * p.A.ld;
+      q.A.scales += q.M * p.A.lds;
+      q.C = static_cast<char *>(p.C) + q.M * p.ldc * size;
+      q.M = rest;
+      return launch_mx_thin(q, s);
+    }
+    return launch_mx_tiles<128>(p, s);
+  }
   if (entry == 2 && mx_tile_fits<64>(p)) return launch_mx_tiles<64>(p, s);
   const long long tiles_m = ceil_div(p.M, 64), tiles_n = ceil_div(p.N, 64);
   if (tiles_m * tiles_n > 0x7fffffffLL) return hipErrorInvalidValue;
