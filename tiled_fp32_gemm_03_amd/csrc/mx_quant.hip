@@ -7,6 +7,7 @@
 // 256 k: a lane reads two adjacent columns' 32 values each (coalesced along
 // the rows of X), the codes are turned through LDS, and each MX row's 128
 // bytes leave as 16-byte stores of 8 neighbouring lanes.
+#include "addr_math.hpp"
 #include "mx_internal.hpp"
 #include "mx_values.hpp"
 
@@ -106,6 +107,14 @@ __device__ inline void store2(void *p, long long i, int n, float a, float b) {
   }
 }
 
+// A workgroup's first column and first tile of k.  Neighbours share the lines
+// that X's rows have at the edge between them, so they go to one XCD (its L2).
+__device__ inline long long cols_of(int &kt) {
+  const int lid = xcd_remap((int)(blockIdx.x + gridDim.x * blockIdx.y), (int)(gridDim.x * gridDim.y));
+  kt = lid / (int)gridDim.x;
+  return (long long)(lid % (int)gridDim.x) * kColRows;
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) quant_cols_kernel(MxConvert c, int ktiles) {
   __shared__ __attribute__((aligned(16))) unsigned char tile[kColRows * kColPitch];
@@ -113,9 +122,10 @@ __global__ void __launch_bounds__(kThreads) quant_cols_kernel(MxConvert c, int k
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int nb = (int)mx_blocks(c.K);
   const int scale_row = (int)mx_scale_bytes(c.K);
-  const long long r0 = (long long)blockIdx.x * kColRows;
+  int kt0;
+  const long long r0 = cols_of(kt0);
   const int ncol = (int)(c.rows - r0 < kColRows ? c.rows - r0 : kColRows);
-  for (int kt = blockIdx.y; kt < ktiles; kt += gridDim.y) {
+  for (int kt = kt0; kt < ktiles; kt += gridDim.y) {
     const int kb0 = kt * kColBlocks;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -123,15 +133,29 @@ __global__ void __launch_bounds__(kThreads) quant_cols_kernel(MxConvert c, int k
       const long long k0 = 32LL * (kb0 + blk), left = c.K - k0;
       float v[2][4][8];
       uint32_t m0 = 0, m1 = 0;
+      // All 32 loads together where none needs a check (each behind its own, they
+      // were waited for one by one: 8191 x 16383 fp32 235 us).
+      if (left >= 32 && ncol == kColRows) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const f32x2 x = load2<FMT>(c.x, (k0 + k) * c.ldx + r0 + 2 * lane, 2);
+          v[0][k >> 3][k & 7] = x[0];
+          v[1][k >> 3][k & 7] = x[1];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          f32x2 x{0.f, 0.f};
+          if (k < left)
+            x = load2<FMT>(c.x, (k0 + k) * c.ldx + r0 + 2 * lane, ncol - 2 * lane);
+          v[0][k >> 3][k & 7] = x[0];
+          v[1][k >> 3][k & 7] = x[1];
+        }
+      }
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        f32x2 x{0.f, 0.f};
-        if (k < left)
-          x = load2<FMT>(c.x, (k0 + k) * c.ldx + r0 + 2 * lane, ncol - 2 * lane);
-        v[0][k >> 3][k & 7] = x[0];
-        v[1][k >> 3][k & 7] = x[1];
-        m0 = umax(m0, mag_bits(x[0]));
-        m1 = umax(m1, mag_bits(x[1]));
+        m0 = umax(m0, mag_bits(v[0][k >> 3][k & 7]));
+        m1 = umax(m1, mag_bits(v[1][k >> 3][k & 7]));
       }
       const uint32_t s0 = scale_byte(m0), s1 = scale_byte(m1);
       u32x4 w0, w1;
@@ -167,9 +191,10 @@ __global__ void __launch_bounds__(kThreads) dequant_cols_kernel(MxConvert c, int
   __shared__ __attribute__((aligned(16))) unsigned char sc[kColRows * kColBlocks];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int nb = (int)mx_blocks(c.K);
-  const long long r0 = (long long)blockIdx.x * kColRows;
+  int kt0;
+  const long long r0 = cols_of(kt0);
   const int ncol = (int)(c.rows - r0 < kColRows ? c.rows - r0 : kColRows);
-  for (int kt = blockIdx.y; kt < ktiles; kt += gridDim.y) {
+  for (int kt = kt0; kt < ktiles; kt += gridDim.y) {
     const int kb0 = kt * kColBlocks;
 #pragma unroll
     for (int i = 0; i < kColRows * kColBlocks / kThreads; ++i) {
@@ -215,8 +240,9 @@ dim3 rows_grid(long long groups, int rows, int &lg) {
   return dim3((unsigned)ceil_div(groups, 1LL << lg), (unsigned)(gy < kMaxGridY ? gy : kMaxGridY));
 }
 dim3 cols_grid(long long ktiles, int rows) {
-  return dim3((unsigned)ceil_div(rows, kColRows),
-              (unsigned)(ktiles < kMaxGridY ? ktiles : kMaxGridY));
+  const long long gx = ceil_div(rows, kColRows), most = (1LL << 30) / gx;  // < 2^31 together
+  const long long gy = ktiles < kMaxGridY ? ktiles : kMaxGridY;
+  return dim3((unsigned)gx, (unsigned)(gy < most ? gy : most));
 }
 
 }  // namespace
