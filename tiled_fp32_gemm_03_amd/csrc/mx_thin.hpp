@@ -61,6 +61,22 @@ __device__ inline void split_f16(u32x4 x, u32x4 &hi, u32x4 &lo) {
   lo = __builtin_bit_cast(u32x4, l);
 }
 
+// The same of finite weights, by truncation, which leaves lo's bits where the
+// packing takes them (an infinity's lo is a NaN).
+__device__ inline void split_f16_weights(u32x4 x, u32x4 &hi, u32x4 &lo) {
+  const f16x8 v = __builtin_bit_cast(f16x8, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = (float)v[2 * i], b = (float)v[2 * i + 1];
+    const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);
+    const float la = a - __builtin_bit_cast(float, ua & 0xffff0000u);
+    const float lb = b - __builtin_bit_cast(float, ub & 0xffff0000u);
+    hi[i] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+    lo[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, lb), __builtin_bit_cast(uint32_t, la),
+                                  0x07060302u);
+  }
+}
+
 // hi + lo of 8 fp32 values, 16 significant bits; an infinity or a NaN is hi
 // alone.
 __device__ inline void split_f32(u32x4 a, u32x4 b, u32x4 &hi, u32x4 &lo) {
@@ -510,7 +526,7 @@ struct Thin {
         // fp16 weights are split too; the product of the two low parts,
         // 2^-18 of the whole, is left out
         u32x4 wh, wl;
-        split_f16(wv[b], wh, wl);
+        split_f16_weights(wv[b], wh, wl);
         acc[b] = mfma_bf16(wh, v, acc[b]);
         acc[b] = mfma_bf16(wh, lo, acc[b]);
         acc[b] = mfma_bf16(wl, v, acc[b]);
