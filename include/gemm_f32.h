@@ -46,13 +46,14 @@ extern "C" {
 #define GEMM_F32_NULL_PTR 3      /* a needed matrix pointer is NULL         */
 #define GEMM_F32_BAD_VARIANT 4   /* unknown variant                         */
 #define GEMM_F32_LAUNCH_FAILED 5 /* the HIP runtime rejected the launch     */
-#define GEMM_F32_MISALIGNED 6    /* a pointer is not 4-byte aligned         */
+#define GEMM_F32_MISALIGNED 6    /* a pointer is not 4-byte aligned (or as the
+                                    entry's header asks)                    */
 #define GEMM_F32_BAD_CONFIG 7    /* config outside the launch table, or not
                                     valid for this shape (small-K entries
                                     need K <= their BK)                      */
 #define GEMM_F32_BAD_ARG 8       /* other invalid argument (query helpers)  */
-#define GEMM_F32_BAD_WORKSPACE 9 /* split-K workspace NULL, too small or not
-                                    4-byte aligned                          */
+#define GEMM_F32_BAD_WORKSPACE 9 /* workspace NULL, too small or not aligned
+                                    (split-K: 4 bytes)                      */
 #define GEMM_F32_SCRATCH_TOO_SMALL 10 /* the plan's slabs exceed the fixed
                                          scratch of gemm_f32_splitk_noalloc */
 

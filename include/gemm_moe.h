@@ -16,7 +16,8 @@
  * Sums are held in fp32; u enters the second product with 16 significant
  * bits or more; y is rounded once to its format.  Results do not depend on
  * timing.  A token whose row holds an infinity or a NaN may give NaN in its
- * own row of Y and gates, and no other's.
+ * own row of Y and gates, and no other's; an infinity among W2's 16-bit
+ * weights may give NaN where it enters.
  *
  * Memory, streams and errors are as for gemm_f32 (gemm_f32.h): device
  * pointers owned by the caller, nothing allocated, asynchronous on `stream`,

@@ -292,12 +292,21 @@ __global__ void __launch_bounds__(kListThreads) moe_list_kernel(MoeProblem p) {
 // its waves share a group, taking the pieces of K in turn: one where there
 // are groups enough to fill the chip, more where there are few.  A wave goes
 // through `each` groups, its weights loaded ahead across them.
+//
+// Memory bounds them: the chosen experts' weights once.  First products run at
+// 4.3 to 4.4 TB/s (268 MB of fp16 weights with odd rows 63 us, the same loads
+// alone 59; 285 MB of MX weights 65 us, alone 58), second ones at 3.3 to 3.6 (134
+// MB of fp16 weights 41 us, alone 37: 16 rows of 64 bytes at a time; 142 MB of
+// MX weights 40 us, alone 32: their activations are twice as large).
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
-// Two workgroups to a compute unit: one streams while the other stages its
-// activations; the LDS that leaves each for its tile, and the most that a tile
-// which needs more may take.
+// Two workgroups to a compute unit in the first product, three in the second:
+// one streams while another stages its activations.  The LDS that leaves each
+// for its tile (64 tokens on 64 experts, 285 MB: 65 us with whole tiles of 8
+// rows, 78 with three workgroups whose tiles did not hold them; 16 tokens on
+// 134 MB of W2: 48 us with three, 64 with two), and the most that a tile which
+// needs more may take.
 template <int A>
 constexpr int kTileLds = A == kF32 ? 48 * 1024 : 74 * 1024;
 constexpr int kMostLds = 140 * 1024;

@@ -34,8 +34,12 @@ hipError_t in_grid_rows(ThinProblem p, int rows, Launch launch) {
   return hipSuccess;
 }
 
-// Few columns: 16 to a workgroup, whose waves share K, WAVES / MB to each of
-// its blocks of 16 rows, with activations straight from memory.
+// Little work: 16 columns to a workgroup, whose waves share K, WAVES / MB to
+// each of its blocks of 16 rows, with activations straight from memory.  One
+// round of loads and one exchange of sums, so the latency of both bounds it:
+// 17 x 4095 x 2049 takes 6.0 us with its launch (19 us with each lane
+// reading its own rows, the end of K behind guarded loads), 1 x 4096 x 4096
+// 4.6 us.
 template <int A, int MB, int WAVES, int ROWS>
 __global__ void __launch_bounds__(64 * WAVES) mx_small_kernel(ThinProblem p) {
   constexpr int kShares = WAVES / MB;
@@ -71,15 +75,20 @@ hipError_t launch_small(const ThinProblem &p, hipStream_t s) {
   });
 }
 
-// More than 16 rows: 16 MB of them by 64 columns to a workgroup.  K is taken
-// 512 values at a time; of the first eight waves, wave (c, s) multiplies
-// columns 32 c .. + 31 with the s-th 128 of them, so that an operand read from
-// LDS serves two products and a weight is widened for all rows.  It loads its
-// own weights, kAhead chunks ahead.  The other eight waves bring the activations
-// to LDS, whose two halves take the chunks in turn, and have asked for those
-// of the three chunks after it.  Waves of their own, because a wave's loads complete
-// in order: activations waited for behind weights, 64 x 16384 x 8192 took
-// 37.7 us.
+// Many columns: 16 MB rows by 64 columns to a workgroup.  K is taken 512
+// values at a time; of the first eight waves, wave (c, s) multiplies columns
+// 32 c .. + 31 with the s-th 128 of them, so that an operand read from LDS
+// serves two products and a weight is widened for all rows.  It loads its own
+// weights, kAhead chunks ahead.  The other eight waves bring the activations to
+// LDS, whose two halves take the chunks in turn, and have asked for the two
+// after the one they write.  Waves of their own, because a wave's loads complete
+// in order and activations would be waited for behind weights.
+//
+// 64 x 16384 x 8192 takes 28 us (76 MB, 2.7 TB/s).  What bounds it: a chunk's
+// 64 KB of activations cross the L1 (1,024 cycles), are written to LDS and
+// read twice (1,500 cycles) next to 1,024 cycles of matrix work.  With lanes
+// that each read their own row of weights it took 41 us, with the rows of 32 in
+// registers (the thin products' form) 61.
 constexpr int kWideWaves = 16, kWideThreads = 64 * kWideWaves, kWideK = 512;
 template <int A, int MB, int ROWS>
 struct Wide {

@@ -86,6 +86,13 @@ __global__ void __launch_bounds__(256) mx_direct_kernel(MxProblem p, int tiles_m
 // 255 among it: with TAIL they are replaced by 127 before use.  The offsets
 // of a tile are 32-bit from its first row (the launcher checks the pitch).
 // C is at least one tile each way; edge tiles are moved back inside it.
+//
+// 8192 cubed takes 289 us (3.8 PFLOP/s; 4096 cubed with fp32 C 51 us, of which
+// 16 are its launch, first loads and stores).  The matrix unit is busy 0.38 of
+// the time at 2.2 GHz.  Timing copies: without the direct loads 253 us,
+// without the operand reads 296, without both 217.  Measured and not kept: the
+// 32x32x64 instruction (308 us), the next step's first operands read before
+// the barrier (316), non-temporal stores (319).
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr int kOutside = (int)0x80000000u;  // an offset past every record count
