@@ -563,13 +563,13 @@ class MxTensor:
         K = int(K)
         if K < 0:
             raise ValueError("K must be >= 0")
-        blocks = (K + 31) // 32
-        for name, t, need in (("codes", codes, 16 * blocks), ("scales", scales, 16 * ((blocks + 15) // 16))):
-            if t.dtype != torch.uint8:
-                raise TypeError(f"{name} must be uint8")
-            if t.dim() < 2 or t.shape[-1] < need:
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("codes and scales must be uint8")
+        c, s = codes.shape, scales.shape
+        for name, shape, need in (("codes", c, (K + 31) // 32 * 16), ("scales", s, (K + 511) // 512 * 16)):
+            if len(shape) < 2 or shape[-1] < need:
                 raise ValueError(f"{name} must have rows of at least {need} bytes for K = {K}")
-        if codes.shape[:-1] != scales.shape[:-1]:
+        if c[0] != s[0] or (len(c) != 2 or len(s) != 2) and c[:-1] != s[:-1]:
             raise ValueError("codes and scales must have the same rows")
         self.codes, self.scales, self.K = codes, scales, K
 
@@ -603,7 +603,7 @@ def _mx_args(q, name: str, device):
     if not isinstance(q, MxTensor):
         raise TypeError(f"{name} must be an MxTensor")
     codes, scales = q.codes, q.scales
-    if codes.dim() != 2:
+    if len(codes.shape) != 2:
         raise ValueError(f"{name} must be one matrix (2-D codes and scales)")
     if not codes.is_cuda or codes.device != device or scales.device != device:
         raise TypeError(f"{name} must be on {device} like the other operands")
@@ -623,7 +623,7 @@ def _launch(fn, where: str, device, stream, args) -> None:
     index = device.index
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():  # CUDA tensors exist, so torch's state does
         rc = fn(*args, stream or None)
     else:
         with torch.cuda.device(device):
@@ -651,11 +651,17 @@ def mx_quantize(X, along: str = "rows", out=None, stream=None):
     if way == 1:
         rows, K = K, rows
     if out is None:
-        out = MxTensor.empty(rows, K, device)
-    elif out.shape != (rows, K):
-        raise ValueError(f"out must be an MxTensor of shape {(rows, K)}")
+        c, s = (K + 31) // 32 * 16, (K + 511) // 512 * 16
+        codes = torch.empty((rows, c), dtype=torch.uint8, device=device)
+        scales = torch.empty((rows, s), dtype=torch.uint8, device=device)
+        out = MxTensor(codes, scales, K)
+        args = codes.data_ptr(), c or 16, scales.data_ptr(), s or 16
+    else:
+        args = _mx_args(out, "out", device)
+        if out.shape != (rows, K):
+            raise ValueError(f"out must be an MxTensor of shape {(rows, K)}")
     _launch(_lib.gemm_mx_quantize, "gemm_mx_quantize", device, stream,
-            (rows, K, X.data_ptr(), ldx, fmt, way, *_mx_args(out, "out", device)))
+            (rows, K, X.data_ptr(), ldx, fmt, way, *args))
     return out
 
 
@@ -667,7 +673,7 @@ def mx_dequantize(q, dtype=torch.float32, along: str = "rows", out=None, stream=
         raise TypeError("dtype must be float32, bfloat16 or float16")
     device, way = q.codes.device, _along(along)
     args = _mx_args(q, "q", device)
-    rows, K = q.shape
+    rows, K = q.codes.shape[0], q.K
     out = _mx_out(out, (rows, K) if way == 0 else (K, rows), dtype, device)
     _launch(_lib.gemm_mx_dequantize, "gemm_mx_dequantize", device, stream,
             (rows, K, *args, out.data_ptr(), _pitch(out), fmt, way))
@@ -688,25 +694,32 @@ def matmul_mx(A, B, dtype=torch.float32, out=None, config: int = -1, stream=None
         raise TypeError("B must be an MxTensor")
     device = B.codes.device
     b = _mx_args(B, "B", device)
-    N, K = B.shape
+    N, K = B.codes.shape[0], B.K
     mx = isinstance(A, MxTensor)
     if mx:
         a = _mx_args(A, "A", device)
+        M, K2 = A.codes.shape[0], A.K
     else:
         if A.dtype not in (torch.bfloat16, torch.float16) or A.device != device:
             raise TypeError(f"A must be an MxTensor, or a bfloat16 or float16 tensor on {device}")
         if config != -1:
             raise ValueError("config is for products of two MxTensors")
-        a = (A.data_ptr(), _pitch(A), _MX_DTYPES[A.dtype])
-    M, K2 = A.shape
+        a = A.data_ptr(), _pitch(A), _MX_DTYPES[A.dtype]
+        M, K2 = A.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} and {tuple(B.shape)}")
-    out = _mx_out(out, (M, N), dtype, device)
-    c = (out.data_ptr(), _pitch(out), fmt)
-    if mx:
-        _launch(_lib.gemm_mx, "gemm_mx", device, stream, (M, N, K, *a, *b, *c, config))
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=device)
+        ldc = N or 1
     else:
-        _launch(_lib.gemm_mx_a16, "gemm_mx_a16", device, stream, (M, N, K, *a, *b, *c))
+        _mx_out(out, (M, N), dtype, device)
+        ldc = _pitch(out)
+    if mx:
+        _launch(_lib.gemm_mx, "gemm_mx", device, stream,
+                (M, N, K, *a, *b, out.data_ptr(), ldc, fmt, config))
+    else:
+        _launch(_lib.gemm_mx_a16, "gemm_mx_a16", device, stream,
+                (M, N, K, *a, *b, out.data_ptr(), ldc, fmt))
     return out
 
 
