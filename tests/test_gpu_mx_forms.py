@@ -141,3 +141,26 @@ def test_layer_with_odd_pitches(g, H, I):
                                padded(w2, extra[0]), top, dtype=torch.float32)
         assert np.array_equal(gi.cpu().numpy(), ids)
         _check(y, ref, bar, "f32", (H, I, extra))
+
+
+def test_a16_more_rows_than_one_grid_holds(g):
+    """65,535 grid rows of 64 or 32 rows, and some: exact on small integers."""
+    for M, N, K in ((65535 * 64 + 70, 16, 32), (65535 * 32 + 33, 3, 7)):
+        rng = np.random.default_rng(N)
+        b, sb = mx.random_rows(rng, N, K, 127, 128)
+        bv = torch.from_numpy(mx.values(b, sb, K)).to(_dev(), torch.float32)
+        gen = torch.Generator(device=_dev()).manual_seed(N)
+        a = torch.randint(-4, 5, (M, K), device=_dev(), dtype=torch.int8, generator=gen).to(torch.bfloat16)
+        got = g.matmul_mx(a, _mx(g, b, sb, K))
+        # halves of at most 6 * 4 * 32: exact in fp32 in any order
+        assert torch.equal(got, a.float() @ bv.T), (M, N, K)
+
+
+def test_quantize_into_an_empty_matrix(g):
+    x = torch.randn(5, 70, device=_dev())
+    q = g.MxTensor.empty(5, 70, x.device)
+    assert g.mx_quantize(x, out=q) is q
+    ref = g.mx_quantize(x)
+    assert torch.equal(q.codes, ref.codes) and torch.equal(q.scales, ref.scales)
+    with pytest.raises(ValueError):
+        g.mx_quantize(x, out=g.MxTensor.empty(5, 71, x.device))

@@ -332,8 +332,9 @@ __device__ inline bool expert_of(const MoeProblem &p, int a, Expert &x) {
 // Columns 16 c .. 16 c + 15 of the product of up to 16 rows, NB factors each,
 // for each group c of this wave: `weights(c)` gives the lane's rows,
 // `done(c, acc)` takes the sums of the group's first wave.  The weights of two
-// pieces are on their way while a third is used.
-template <int W, int A, int NB, int ROWS, class RowOf, class WeightsOf, class Done>
+// pieces are on their way while a third is used.  STAGED: the first tile is in
+// LDS, or on its way there, already.
+template <int W, int A, int NB, int ROWS, bool STAGED, class RowOf, class WeightsOf, class Done>
 __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, int n, int K,
                                                int groups, const MoeShape &sh,
                                                WeightsOf weights, Done done) {
@@ -370,7 +371,7 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
   };
   Turn ahead{0, 0}, now{0, 0};
   // The first tile before the weights, which it would wait for otherwise.
-  stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, 0, K);
+  if constexpr (!STAGED) stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, 0, K, threadIdx.x);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     load(x[u], ahead);
@@ -384,7 +385,7 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
   while (now.group < sh.each) {
     if (!whole && now.round % per == 0 && now.round + now.group > 0) {
       __syncthreads();
-      stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, now.round * ks * kK, K);
+      stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, now.round * ks * kK, K, threadIdx.x);
       __syncthreads();
     }
 #pragma unroll
@@ -428,6 +429,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeProblem p, MoeSh
     const bool writes = blockIdx.x == 0 && blockIdx.y == 0;
     if (wave_id() == 0) choose_experts<false>(p, route, 0, 0);
     if (writes && wave_id() == 1) choose_experts<true>(p, route, 0, 0);  // the same, and the gates
+    if (wave_id() >= 2)  // meanwhile the token's first tile
+      stage_acts<AF, W, ROWS, kThreads - 128>(
+          lds, tile_of<AF>(tile_rows(1), p.H, sh.ks * kPieceK<W>, kTileLds<AF>),
+          [&](int) { return reinterpret_cast<const unsigned char *>(p.X); }, 1, 0, p.H,
+          threadIdx.x - 128);
     __syncthreads();
     if (writes) {
       write_choice<kThreads>(p, route, 0, p.top);
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeProblem p, MoeSh
         *reinterpret_cast<f32x4 *>(ws_at<float>(p, p.at.u) + (x.first + m0 + l16) * p.at.upitch + i) = u;
     };
     const int groups = (int)ceil_div(p.I, 16);
-    expert_columns<W, AF, 2, ROWS>(lds, row, n, p.H, groups, sh, weights, done);
+    expert_columns<W, AF, 2, ROWS, ONE>(lds, row, n, p.H, groups, sh, weights, done);
     __syncthreads();
   }
 }
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(MoeProblem p, Moe
                    acc[0]);
     };
     const int groups = (int)ceil_div(p.H, 16);
-    expert_columns<W, kF32, 1, ROWS>(lds, row, n, p.I, groups, sh, weights, done);
+    expert_columns<W, kF32, 1, ROWS, false>(lds, row, n, p.I, groups, sh, weights, done);
     __syncthreads();
   }
 }

@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(256) mx_direct_kernel(MxProblem p, int tiles_m
 // the time at 2.2 GHz.  Timing copies: without the direct loads 253 us,
 // without the operand reads 296, without both 217.  Measured and not kept: the
 // 32x32x64 instruction (308 us), the next step's first operands read before
-// the barrier (316), non-temporal stores (319).
+// the barrier (316), non-temporal stores (319), eight waves of 128 x 64 (287; a
+// fifth fewer cycles at a lower clock, and 4096 cubed 57).
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr int kOutside = (int)0x80000000u;  // an offset past every record count

@@ -363,18 +363,18 @@ __host__ __device__ inline int act_bytes(const Tile &t) {
 }
 
 // Fills a block with values k0 .. k0 + kc - 1 of rows 0 .. n - 1, zeros past K;
-// `row(r)` gives row r's start.  All THREADS threads of the workgroup take
-// part; each issues eight loads before it writes any (one at a time, their
+// `row(r)` gives row r's start.  Threads 0 .. THREADS - 1 (`tid`) take part; each
+// issues eight loads before it writes any (one at a time, their
 // latencies alone took 30 us of a first product).  Rows of kind kF32 hold
 // zeros from K to a multiple of 8.
 template <int A, int W, int ROWS, int THREADS, class RowOf>
 __device__ __forceinline__ void stage_acts(unsigned char *lds, const Tile &t, RowOf row, int n,
-                                           int k0, int K) {
+                                           int k0, int K, int tid) {
   constexpr int kBatch = A == kF32 ? 4 : 8;
   const int G = t.group();
   const int per = t.kc / 8, all = n * per, eights = (int)ceil_div(K, 8);
 #pragma unroll 1
-  for (int i0 = threadIdx.x; i0 < all; i0 += kBatch * THREADS) {
+  for (int i0 = tid; i0 < all; i0 += kBatch * THREADS) {
     Eight<ROWS> c[kBatch];
     u32x4 d[kBatch];
 #pragma unroll
