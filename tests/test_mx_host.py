@@ -222,3 +222,12 @@ def test_oracle_bf16_rounding_is_torch_s():
     x = np.concatenate([x, np.float32([0, -0.0, np.inf, -np.inf, 3.4e38, 1e-45])])
     want = torch.from_numpy(x).bfloat16().double().numpy()
     assert np.array_equal(mx.round_to(x.astype(np.float64), "bf16"), want)
+
+
+def test_the_choice_of_entry_by_size():
+    """Sizes where every entry was timed: the fastest, or one within a tenth."""
+    for (M, N, K), want in {(17, 64, 16384): 3, (33, 8192, 512): 0, (64, 2048, 16384): 3,
+                            (128, 8192, 4096): 2, (256, 512, 16384): 3, (256, 2048, 4096): 2,
+                            (256, 8192, 512): 2, (300, 300, 300): 0, (700, 1000, 8000): 2,
+                            (1024, 8192, 4096): 2, (4096, 4096, 4096): 1}.items():
+        assert g.gemm_mx_tile(-1, M, N, K)["config"] == want, (M, N, K)

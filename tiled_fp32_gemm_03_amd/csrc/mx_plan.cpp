@@ -43,9 +43,28 @@ const MxEntry kMxEntries[] = {
 
 int mx_num_entries() { return (int)(sizeof(kMxEntries) / sizeof(kMxEntries[0])); }
 const MxEntry &mx_entry(int index) { return kMxEntries[index]; }
-int mx_choose(int M, int N, int) {
+// 256 x 256 tiles where they fill most of the chip; otherwise the entry with
+// the least modelled time in ns, from rounds of workgroups on 256 compute
+// units and a straight line in K through measured times, us (entries 0, 2 and
+// 3): 64 x 2048 x 16384 113, -, 12.0; 100 x 8192 x 4096 31, -, 35; 128 x 8192 x
+// 4096 31, 17, 37; 256 x 512 x 16384 113, 51, 12; 256 x 2048 x 4096 31, 13.4,
+// 18.6; 256 x 8192 x 512 8.7, 6.3, 19; 512 x 8192 x 16384 448, 60, -; 33 x 8192 x
+// 512 4.9, -, 6.0.
+int mx_choose(int M, int N, int K) {
   if (M >= 256 && N >= 256 && ceil_div(M, 256) * ceil_div(N, 256) >= 192) return 1;
-  return M <= 32 ? 3 : M >= 128 && N >= 128 ? 2 : 0;
+  if (M <= 32) return 3;
+  const double k = K / 1024.0;
+  auto rounds = [&](int bm, int bn) { return ceil_div(ceil_div(M, bm) * ceil_div(N, bn), 256); };
+  const double direct = 2000 + (300 + 6850 * k) * (double)rounds(64, 64);
+  const double few = 2400 + (900 + 530 * k) * (double)rounds(32, 16);
+  int best = few < direct ? 3 : 0;
+  if (M >= 128 && N >= 128) {
+    const double filled = (double)(ceil_div(M, 128) * ceil_div(N, 128)) * 0.95 / 256;
+    double tiles = 1500 + (1000 + 2950 * k) * (filled > 1 ? filled : 1);
+    if (tiles < 5300) tiles = 5300;  // its start and end alone
+    if (tiles < (best == 3 ? few : direct)) best = 2;
+  }
+  return best;
 }
 
 int moe_check_sizes(int T, int E, int top, int H, int I) {
