@@ -727,10 +727,13 @@ def _expert_rows(w, name: str, dtype, device, E: int, rows: int, K: int):
     """Pointers and pitches of stacked expert matrices (E, rows, K): (weights,
     pitch, scales, scale pitch), the experts' rows following one another."""
     def pitch(t, width, what):
-        if t.dim() != 3 or t.device != device:
+        shape = t.shape
+        if len(shape) != 3 or t.device != device:
             raise TypeError(f"{what} must be a 3-D tensor on {device}")
-        if tuple(t.shape[:2]) != (E, rows):
-            raise ValueError(f"{what} must have {E} experts of {rows} rows, not {tuple(t.shape)}")
+        if shape[0] != E or shape[1] != rows:
+            raise ValueError(f"{what} must have {E} experts of {rows} rows, not {tuple(shape)}")
+        if E * rows > 1 and t.is_contiguous():
+            return shape[2]
         if t.shape[2] > 1 and t.stride(2) != 1:
             raise ValueError(f"{what} must have contiguous rows (last stride 1)")
         if rows > 1 and t.stride(1) < t.shape[2]:
@@ -743,8 +746,8 @@ def _expert_rows(w, name: str, dtype, device, E: int, rows: int, K: int):
     if isinstance(w, MxTensor):
         if w.K != K:
             raise ValueError(f"{name} must have rows of {K} values, not {w.K}")
-        c = pitch(w.codes, gemm_mx_code_bytes(K), name + ".codes")
-        s = pitch(w.scales, gemm_mx_scale_bytes(K), name + ".scales")
+        c = pitch(w.codes, (K + 31) // 32 * 16, name + ".codes")
+        s = pitch(w.scales, (K + 511) // 512 * 16, name + ".scales")
         return w.codes.data_ptr(), c, w.scales.data_ptr(), s
     if w.dtype != dtype:
         raise TypeError(f"{name} must be an MxTensor, or {dtype} like the tokens")
@@ -784,11 +787,16 @@ def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None,
     if dtype not in (X.dtype, torch.float32):
         raise TypeError(f"dtype must be {X.dtype} or float32")
     top = int(top)
-    need = gemm_moe_workspace_bytes(T, E, top, H, I)
+    need = _lib.gemm_moe_workspace_bytes(T, E, top, H, I)
     if need < 0:
         raise ValueError(f"sizes outside the layer's bounds: {T} tokens, {E} experts, top {top}, "
                          f"widths {H} and {I}")
-    out = _mx_out(out, (T, H), dtype, device)
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=device)
+        ldy = H
+    else:
+        _mx_out(out, (T, H), dtype, device)
+        ldy = _pitch(out)
     ids = torch.empty((T, top), dtype=torch.int32, device=device)
     gates = torch.empty((T, top), dtype=torch.float32, device=device)
     if workspace is None:
@@ -797,7 +805,7 @@ def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None,
         raise TypeError(f"workspace must be a contiguous tensor on {device}")
     _launch(_lib.gemm_moe, "gemm_moe", device, stream,
             (T, E, top, H, I, X.data_ptr(), ldx, router.data_ptr(), ldr, _MX_DTYPES[X.dtype],
-             *a1, *a2, int(mx), int(renormalize), out.data_ptr(), _pitch(out), _MX_DTYPES[dtype],
+             *a1, *a2, int(mx), int(renormalize), out.data_ptr(), ldy, _MX_DTYPES[dtype],
              ids.data_ptr(), gates.data_ptr(), workspace.data_ptr(),
              workspace.numel() * workspace.element_size()))
     return out, ids, gates
