@@ -550,7 +550,15 @@ template <int W, int A>
 MoeShape shape_of(long long experts, int columns, int K, int rows) {
   const long long groups = experts * ceil_div(columns, 16);
   MoeShape sh;
-  sh.ks = waves_per_group(groups, K, kPieceK<W>, kWaves, 8 * 256);
+  // Waves per group: until they are four to a compute unit, or eight where each
+  // keeps 16 pieces; more only stage the same activations more often.  Eight
+  // against four, us: 16 tokens on fp16 W2 rows of 4095 119 and 133; 16 tokens on
+  // 8 experts, MX rows of 4096 41 and 36, bf16 rows of 4096 64 and 62.
+  const long long pieces = ceil_div(K, kPieceK<W>);
+  sh.ks = 1;
+  while (sh.ks < kWaves && 2 * sh.ks <= pieces &&
+         (groups * sh.ks < 4 * 256 || (groups * sh.ks < 8 * 256 && pieces >= 32 * sh.ks)))
+    sh.ks *= 2;
   while (sh.ks > 1 && tile_bytes<W, A>(rows, K, sh.ks) > kMostLds) sh.ks /= 2;
   // Groups per wave: while workgroups are left for two on each compute unit.
   sh.each = 1;

@@ -34,16 +34,18 @@ hipError_t in_grid_rows(ThinProblem p, int rows, Launch launch) {
   return hipSuccess;
 }
 
-// Little work: 16 columns to a workgroup, whose waves share K, WAVES / MB to
+// Little work: 16 columns to a workgroup, whose waves share K, 8 / MB to
 // each of its blocks of 16 rows, with activations straight from memory.  One
-// round of loads and one exchange of sums, so the latency of both bounds it:
+// round of loads and one exchange of sums (eight waves: four took 5.5 us for 24
+// x 1024 x 2048, eight 4.6), so the latency of both bounds it:
 // 17 x 4095 x 2049 takes 6.0 us with its launch (19 us with each lane
 // reading its own rows, the end of K behind guarded loads), 1 x 4096 x 4096
 // 4.6 us.
-template <int A, int MB, int WAVES, int ROWS>
-__global__ void __launch_bounds__(64 * WAVES) mx_small_kernel(ThinProblem p) {
-  constexpr int kShares = WAVES / MB;
-  __shared__ f32x4 part[WAVES][64];
+constexpr int kSmallWaves = 8;
+template <int A, int MB, int ROWS>
+__global__ void __launch_bounds__(64 * kSmallWaves) mx_small_kernel(ThinProblem p) {
+  constexpr int kShares = kSmallWaves / MB;
+  __shared__ f32x4 part[kSmallWaves][64];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int l16 = lane & 15, g = lane >> 4;
   const int n0 = 16 * blockIdx.x, pieces = (int)ceil_div(p.K, 512);
@@ -69,9 +71,7 @@ template <int A, int MB, int ROWS>
 hipError_t launch_small(const ThinProblem &p, hipStream_t s) {
   return in_grid_rows(p, 16 * MB, [&](const ThinProblem &q, unsigned gy) {
     const dim3 grid((unsigned)ceil_div(q.N, 16), gy);
-    if (q.K <= 4 / MB * 512)
-      return launch_kernel(mx_small_kernel<A, MB, 4, ROWS>, grid, dim3(256), s, q);
-    return launch_kernel(mx_small_kernel<A, MB, 8, ROWS>, grid, dim3(512), s, q);
+    return launch_kernel(mx_small_kernel<A, MB, ROWS>, grid, dim3(64 * kSmallWaves), s, q);
   });
 }
 
@@ -374,8 +374,12 @@ struct FewPiece {
   }
 };
 
-template <int MB, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES) mx_few_kernel(MxProblem p) {
+// Four waves, so that two workgroups share a compute unit: 32 x 8192 x 4096 8.8
+// us, with eight 11.0; 32 x 4096 x 16384 12.3 and 13.5.
+constexpr int kFewWaves = 4;
+template <int MB>
+__global__ void __launch_bounds__(64 * kFewWaves) mx_few_kernel(MxProblem p) {
+  constexpr int WAVES = kFewWaves;
   __shared__ f32x4 part[WAVES][MB][64];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int l16 = lane & 15, g = lane >> 4, nb = (int)mx_blocks(p.K);
@@ -434,8 +438,7 @@ template <int MB>
 hipError_t launch_few(const MxProblem &p, hipStream_t s) {
   const long long gy = ceil_div(p.M, 16 * MB);
   const dim3 grid((unsigned)ceil_div(p.N, 16), (unsigned)(gy < kMaxGridY ? gy : kMaxGridY));
-  if (p.K <= 4 * 512) return launch_kernel(mx_few_kernel<MB, 4>, grid, dim3(256), s, p);
-  return launch_kernel(mx_few_kernel<MB, 8>, grid, dim3(512), s, p);
+  return launch_kernel(mx_few_kernel<MB>, grid, dim3(64 * kFewWaves), s, p);
 }
 
 // Rows that start in the middle of a word, of a matrix that starts on one.

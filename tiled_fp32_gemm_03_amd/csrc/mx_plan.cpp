@@ -36,7 +36,7 @@ const MxEntry kMxEntries[] = {
     {64, 64, 128, 256},    // operands straight from memory, any size
     {256, 256, 256, 256},  // direct-load tiles, 128 x 128 per wave
     {128, 128, 256, 256},  // direct-load tiles, 64 x 64 per wave
-    {32, 16, 256, 512},    // few rows: K shared by the waves, B read once
+    {32, 16, 256, 256},    // few rows: K shared by the waves, B read once
 };
 
 }  // namespace

@@ -5,7 +5,7 @@
 // A wave multiplies blocks of 16 activation rows with blocks of 16 weight
 // rows ("columns" of C) and takes K in pieces of 256 bytes of weight row:
 // four 128-deep steps of MX weights, one of 16-bit ones.  The weights go from
-// memory into registers, the next piece's while one is used; the activations,
+// memory into registers, the next two pieces' while one is used; the activations,
 // which a workgroup's waves share, wait in LDS.  Loads complete in order, so
 // activations loaded from memory between the pieces would make each wave wait
 // for the next piece's weights as well (measured: twice the time).
@@ -606,13 +606,6 @@ struct Direct {
   }
 };
 
-// Waves per group of columns: until the groups' waves fill the chip (`want`),
-// or each has a piece.
-inline int waves_per_group(long long groups, int K, int piece, int most, int want) {
-  int ks = 1;
-  while (ks < most && groups * ks < want && (long long)2 * ks * piece <= K) ks *= 2;
-  return ks;
-}
 // Rows of the tile for n rows.
 __host__ __device__ inline int tile_rows(int n) { return n <= 4 ? 4 : n <= 8 ? 8 : 16; }
 // The activations' tile: all of K where it fits `bytes`, else as many pairs of
