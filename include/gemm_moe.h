@@ -13,8 +13,8 @@
  *   y       = sum_s gate[s] W2[e_s] u,   u[i] = silu(W1[e_s][i] . x) *
  *             (W1[e_s][I + i] . x),      silu(v) = v / (1 + exp(-v))
  *
- * Sums are held in fp32; u enters the second product with 16 significant
- * bits or more; y is rounded once to its format.  Results do not depend on
+ * Sums and u are held in fp32, and all of u's bits enter the second product;
+ * y is rounded once to its format.  Results do not depend on
  * timing.  A token whose row holds an infinity or a NaN may give NaN in its
  * own row of Y and gates, and no other's; an infinity among W2's 16-bit
  * weights may give NaN where it enters.

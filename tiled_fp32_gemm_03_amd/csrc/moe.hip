@@ -299,21 +299,20 @@ __global__ void __launch_bounds__(kListThreads) moe_list_kernel(MoeProblem p) {
 // MB of fp16 weights 41 us, alone 37: 16 rows of 64 bytes at a time; 142 MB of
 // MX weights 40 us, alone 32: their activations are twice as large).
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kWaves = 4, kThreads = 64 * kWaves;  // of the first product's workgroups
+constexpr int kMostWaves = 8;                      // of the second one's: 4 or 8
 
-// Two workgroups to a compute unit in the first product, three in the second:
-// one streams while another stages its activations.  The LDS that leaves each
-// for its tile (64 tokens on 64 experts, 285 MB: 65 us with whole tiles of 8
-// rows, 78 with three workgroups whose tiles did not hold them; 16 tokens on
-// 134 MB of W2: 48 us with three, 64 with two), and the most that a tile which
-// needs more may take.
-template <int A>
-constexpr int kTileLds = A == kF32 ? 48 * 1024 : 74 * 1024;
-constexpr int kMostLds = 140 * 1024;
+// Two workgroups of four waves to a compute unit: one streams while another
+// stages its activations.  The LDS that leaves each for its tile, and the most that
+// a tile which needs more may take; then the second product's workgroups have
+// eight waves, where there are groups for them.
+constexpr int kTileLds = 74 * 1024;
+constexpr int kMostLds = 140 * 1024, kCuLds = 160 * 1024;
 
-// What the launch chose: waves per group, groups per wave, the tile's LDS.
+// What the launch chose: waves, waves per group, groups per wave, the tile's LDS.
 struct MoeShape {
-  int ks, each, lds;
+  int waves, ks, each, lds;
+  __host__ __device__ int threads() const { return 64 * waves; }
 };
 
 // An expert's part in a launch.
@@ -342,12 +341,13 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
   constexpr int kK = Product::kK;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int ks = sh.ks;
-  const Tile tile = tile_of<A>(tile_rows(n), K, ks * kK, kTileLds<A>);
+  const Tile tile = tile_of<A>(tile_rows(n), K, ks * kK, kTileLds);
   const bool whole = tile.kc >= K;
-  f32x4 *part = reinterpret_cast<f32x4 *>(lds + sh.lds);  // [kWaves][NB][64], if ks > 1
-  const int side = kWaves / ks;  // groups side by side
+  f32x4 *part = reinterpret_cast<f32x4 *>(lds + sh.lds);  // [waves][NB][64], if ks > 1
+  const int side = sh.waves / ks;  // groups side by side
   const int c0 = (int)blockIdx.x * side * sh.each + wave / ks, first = wave & (ks - 1);
-  // A wave's turns: for each of its groups, pieces first, first + ks, ... (an even number of rounds, and of rounds in a tile, unless it holds all).
+  // A wave's turns: for each of its groups, pieces first, first + ks, ... (an even
+  // number of rounds, and of rounds in a tile, unless it holds all).
   const int pieces = (int)ceil_div(K, kK), need = (int)ceil_div(pieces, ks);
   const int rounds = whole ? need : (need + 1) & ~1;
   const int per = tile.kc / (kK * ks);  // rounds in a tile
@@ -371,7 +371,7 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
   };
   Turn ahead{0, 0}, now{0, 0};
   // The first tile before the weights, which it would wait for otherwise.
-  if constexpr (!STAGED) stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, 0, K, threadIdx.x);
+  if constexpr (!STAGED) stage_acts<A, W, ROWS>(lds, tile, row, n, 0, K, threadIdx.x, sh.threads());
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     load(x[u], ahead);
@@ -385,7 +385,8 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
   while (now.group < sh.each) {
     if (!whole && now.round % per == 0 && now.round + now.group > 0) {
       __syncthreads();
-      stage_acts<A, W, ROWS, kThreads>(lds, tile, row, n, now.round * ks * kK, K, threadIdx.x);
+      stage_acts<A, W, ROWS>(lds, tile, row, n, now.round * ks * kK, K, threadIdx.x,
+                             sh.threads());
       __syncthreads();
     }
 #pragma unroll
@@ -393,7 +394,8 @@ __device__ __forceinline__ void expert_columns(unsigned char *lds, RowOf row, in
       if (now.group < sh.each) {
         const int c = c0 + now.group * side;
         if (c < groups && piece(now) < pieces)
-          t.use(x[u], [&](Row (&w)[NB]) { weights(c, w); }, lds, tile, now.round % per * ks + first, piece(now), lane, K);
+          t.use(x[u], [&](Row (&w)[NB]) { weights(c, w); }, lds, tile, now.round % per * ks + first,
+                piece(now), lane, K);
         if (now.round == rounds - 1) {
           if (ks > 1) {  // the waves' sums, added in wave order
             __syncthreads();
@@ -430,10 +432,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeProblem p, MoeSh
     if (wave_id() == 0) choose_experts<false>(p, route, 0, 0);
     if (writes && wave_id() == 1) choose_experts<true>(p, route, 0, 0);  // the same, and the gates
     if (wave_id() >= 2)  // meanwhile the token's first tile
-      stage_acts<AF, W, ROWS, kThreads - 128>(
-          lds, tile_of<AF>(tile_rows(1), p.H, sh.ks * kPieceK<W>, kTileLds<AF>),
+      stage_acts<AF, W, ROWS>(
+          lds, tile_of<AF>(tile_rows(1), p.H, sh.ks * kPieceK<W>, kTileLds),
           [&](int) { return reinterpret_cast<const unsigned char *>(p.X); }, 1, 0, p.H,
-          threadIdx.x - 128);
+          threadIdx.x - 128, kThreads - 128);
     __syncthreads();
     if (writes) {
       write_choice<kThreads>(p, route, 0, p.top);
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeProblem p, MoeSh
 
 // Second product: each pair's result, before its gate.
 template <int W, int ROWS>
-__global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(MoeProblem p, MoeShape sh) {
+__global__ void __launch_bounds__(64 * kMostWaves, 2) moe_down_kernel(MoeProblem p, MoeShape sh) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   Expert x;
   if (!expert_of(p, blockIdx.y, x)) return;
@@ -539,7 +541,7 @@ template <int W, int A>
 int tile_bytes(int rows, int K, int ks) {
   int most = 0;
   for (int keep = 4; keep <= tile_rows(rows); keep *= 2) {
-    const int bytes = act_bytes<A>(tile_of<A>(keep, K, ks * kPieceK<W>, kTileLds<A>));
+    const int bytes = act_bytes<A>(tile_of<A>(keep, K, ks * kPieceK<W>, kTileLds));
     most = most < bytes ? bytes : most;
   }
   return most;
@@ -555,6 +557,7 @@ MoeShape shape_of(long long experts, int columns, int K, int rows) {
   // against four, us: 16 tokens on fp16 W2 rows of 4095 119 and 133; 16 tokens on
   // 8 experts, MX rows of 4096 41 and 36, bf16 rows of 4096 64 and 62.
   const long long pieces = ceil_div(K, kPieceK<W>);
+  sh.waves = kWaves;
   sh.ks = 1;
   while (sh.ks < kWaves && 2 * sh.ks <= pieces &&
          (groups * sh.ks < 4 * 256 || (groups * sh.ks < 8 * 256 && pieces >= 32 * sh.ks)))
@@ -564,8 +567,17 @@ MoeShape shape_of(long long experts, int columns, int K, int rows) {
   // (three, us: 33 tokens, 8 of 64 experts, 2048 / 1024, MX 83 against 76; 8
   // tokens, 1024 / 2816 76 against 82).
   sh.each = 1;
-  while (groups * sh.ks / kWaves / (2 * sh.each) >= 2 * 256) sh.each *= 2;
+  while (groups * sh.ks / (2 * sh.each) >= 2 * 256 * kWaves) sh.each *= 2;
+  // Eight waves to a workgroup of the second product where those of four do not
+  // all fit the chip and those of eight do (four and eight, us: 64 tokens on 64
+  // experts, 4096 / 1024, MX 149 and 128; 16 tokens on fp16 W2 rows of 4095 136
+  // and 127; on bf16 ones of 4096, which fit, 184 and 192).
   sh.lds = tile_bytes<W, A>(rows, K, sh.ks);
+  auto rounds = [&](int waves) {
+    const long long all = experts * ceil_div(ceil_div(columns, 16), waves / sh.ks * sh.each);
+    return ceil_div(all, 256 * (kCuLds / (sh.lds + (sh.ks > 1 ? waves * 1024 : 0))));
+  };
+  if (A == kF32 && rounds(kMostWaves) < rounds(kWaves)) sh.waves = kMostWaves;
   return sh;
 }
 template <int W, int A, int NB, class Kernel>
@@ -574,10 +586,11 @@ hipError_t launch_experts(Kernel kern, const MoeProblem &p, int columns, int K, 
   MoeShape sh = shape_of<W, A>(experts, columns, K, p.T);
   MoeProblem q = p;
   void *args[] = {&q, &sh};
-  const dim3 grid((unsigned)ceil_div(ceil_div(columns, 16), kWaves / sh.ks * sh.each),
+  const dim3 grid((unsigned)ceil_div(ceil_div(columns, 16), sh.waves / sh.ks * sh.each),
                   (unsigned)experts);
-  return hipLaunchKernel(reinterpret_cast<const void *>(kern), grid, dim3(kThreads), args,
-                         (size_t)(sh.lds + (sh.ks > 1 ? kWaves * NB * 1024 : 0)), s);
+  return hipLaunchKernel(reinterpret_cast<const void *>(kern), grid,
+                         dim3(sh.threads()), args,
+                         (size_t)(sh.lds + (sh.ks > 1 ? sh.waves * NB * 1024 : 0)), s);
 }
 
 template <int W, int AF, int ROWS>

@@ -26,8 +26,8 @@
 namespace gemm_f32_impl {
 namespace {
 
-// Kinds of operands: the formats of mx_plan.hpp (kF32: activations split into
-// two bf16 terms, hi + lo, 16 significant bits), and MX rows.
+// Kinds of operands: the formats of mx_plan.hpp (kF32: activations that enter
+// as three bf16 terms, all their 24 bits), and MX rows.
 constexpr int kMx = 3;
 
 template <int W>
@@ -77,20 +77,24 @@ __device__ inline void split_f16_weights(u32x4 x, u32x4 &hi, u32x4 &lo) {
   }
 }
 
-// hi + lo of 8 fp32 values, 16 significant bits; an infinity or a NaN is hi
-// alone.
-__device__ inline void split_f32(u32x4 a, u32x4 b, u32x4 &hi, u32x4 &lo) {
+// Three bf16 terms whose sum is each of 8 fp32 values: exact (each takes the
+// next 8 of 24 bits, by truncation).  An infinity or a NaN is the first alone.
+__device__ inline void split_f32(u32x4 a, u32x4 b, u32x4 (&term)[3]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float h[2], l[2];
+    uint32_t u[3][2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const float v = __builtin_bit_cast(float, i < 2 ? a[2 * i + q] : b[2 * i + q - 4]);
-      h[q] = (float)(__bf16)v;
-      l[q] = mag_bits(h[q]) < 0x7f800000u ? v - h[q] : 0.f;
+      float v = __builtin_bit_cast(float, i < 2 ? a[2 * i + q] : b[2 * i + q - 4]);
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        u[t][q] = __builtin_bit_cast(uint32_t, v);
+        const float rest = v - __builtin_bit_cast(float, u[t][q] & 0xffff0000u);
+        v = mag_bits(v) < 0x7f800000u ? rest : 0.f;
+      }
     }
-    hi[i] = pack2<kBf16>(h[0], h[1]);
-    lo[i] = pack2<kBf16>(l[0], l[1]);
+#pragma unroll
+    for (int t = 0; t < 3; ++t) term[t][i] = __builtin_amdgcn_perm(u[t][1], u[t][0], 0x07060302u);
   }
 }
 
@@ -349,8 +353,9 @@ struct HalfPiece<kOdd> {
 // each operand of a matrix instruction (piece, step, MFMA j) and lane group,
 // the rows' 16 bytes one after the other, and 16 bytes of padding, so that
 // neither the writes (neighbouring threads take neighbouring k of a row) nor
-// the reads (16 lanes take 16 rows) meet on a bank.  kF32: a second such
-// plane for lo.
+// the reads (16 lanes take 16 rows) meet on a bank.  kF32: three such planes,
+// one for each term (splitting the values where they are used, by every wave that
+// does, took 64 tokens on 64 experts from 117 to 159 us).
 
 struct Tile {
   int rows, kc;
@@ -359,27 +364,27 @@ struct Tile {
 // LDS bytes of a block of rows of kind A: linear in kc (whole pieces).
 template <int A>
 __host__ __device__ inline int act_bytes(const Tile &t) {
-  return t.kc / 8 * t.group() * (A == kF32 ? 2 : 1);
+  return t.kc / 8 * t.group() * (A == kF32 ? 3 : 1);
 }
 
 // Fills a block with values k0 .. k0 + kc - 1 of rows 0 .. n - 1, zeros past K;
-// `row(r)` gives row r's start.  Threads 0 .. THREADS - 1 (`tid`) take part; each
+// `row(r)` gives row r's start.  Threads 0 .. threads - 1 (`tid`) take part; each
 // issues eight loads before it writes any (one at a time, their
 // latencies alone took 30 us of a first product).  Rows of kind kF32 hold
 // zeros from K to a multiple of 8.
-template <int A, int W, int ROWS, int THREADS, class RowOf>
+template <int A, int W, int ROWS, class RowOf>
 __device__ __forceinline__ void stage_acts(unsigned char *lds, const Tile &t, RowOf row, int n,
-                                           int k0, int K, int tid) {
+                                           int k0, int K, int tid, int threads) {
   constexpr int kBatch = A == kF32 ? 4 : 8;
   const int G = t.group();
   const int per = t.kc / 8, all = n * per, eights = (int)ceil_div(K, 8);
 #pragma unroll 1
-  for (int i0 = tid; i0 < all; i0 += kBatch * THREADS) {
+  for (int i0 = tid; i0 < all; i0 += kBatch * threads) {
     Eight<ROWS> c[kBatch];
     u32x4 d[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + u * THREADS < all ? i0 + u * THREADS : all - 1;
+      const int i = i0 + u * threads < all ? i0 + u * threads : all - 1;
       const int r = i / per, x = i % per;
       if constexpr (A == kF32) {
         const int e = k0 / 8 + x, in = e < eights ? e : eights - 1;
@@ -392,25 +397,25 @@ __device__ __forceinline__ void stage_acts(unsigned char *lds, const Tile &t, Ro
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + u * THREADS;
+      const int i = i0 + u * threads;
       if (i >= all) continue;
       const int r = i / per, x = i % per;
       // Operand and lane group of values 8 x .. 8 x + 7: the MX order of k
       // is (step, g, j), the 16-bit one (j, g).
       const int group = W == kMx ? (x & ~15) | (x & 3) << 2 | (x >> 2 & 3) : x;
-      u32x4 *to = reinterpret_cast<u32x4 *>(lds + group * G + 16 * r);
       if constexpr (A == kF32) {
         const bool in = k0 / 8 + x < eights;
-        u32x4 hi, lo;
-        split_f32(c[u].v, d[u], hi, lo);
-        *to = in ? hi : u32x4{0, 0, 0, 0};
-        *reinterpret_cast<u32x4 *>(lds + per * G + group * G + 16 * r) =
-            in ? lo : u32x4{0, 0, 0, 0};
+        u32x4 term[3];
+        split_f32(c[u].v, d[u], term);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          *reinterpret_cast<u32x4 *>(lds + (q * per + group) * G + 16 * r) =
+              in ? term[q] : u32x4{0, 0, 0, 0};
       } else {
         const long long k = k0 + 8LL * x;
         u32x4 v = c[u].get();
         if (k + 8 > K) v = c[u].end(v, k, K);
-        *to = v;
+        *reinterpret_cast<u32x4 *>(lds + group * G + 16 * r) = v;
       }
     }
   }
@@ -457,7 +462,7 @@ struct Thin {
     const int g = lane >> 4, r = lane & (t.rows - 1), G = t.group();
     constexpr Widen kHow = W == kF16 || (W == kMx && A == kF16) ? kToF16 : kToBf16;
     const unsigned char *from = lds + (local * kSteps * 16 + g) * G + 16 * r;
-    const int lo = t.kc / 8 * G;
+    const int plane = t.kc / 8 * G;
     if constexpr (W != kMx) {
       if (piece >= K / kK) {  // uniform
         Row w[NB];
@@ -470,7 +475,7 @@ struct Thin {
         u32x4 wv[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) wv[b] = from_lane(x.half[b].get(j, lane), loader(lane));
-        multiply<kHow>(wv, from + j * 4 * G, lo);
+        multiply<kHow>(wv, from + j * 4 * G, plane);
       }
     } else {
       const MxBlocks y0(x.mx[0], piece, lane, (int)mx_blocks(K));
@@ -488,7 +493,7 @@ struct Thin {
             u32x4 wv[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) wv[b] = widen<kHow>(y[b]->c[s][j], y[b]->s[s]);
-            multiply<kHow>(wv, from + (4 * s + j) * 4 * G, lo);
+            multiply<kHow>(wv, from + (4 * s + j) * 4 * G, plane);
           }
       } else {
         // Rare, and kept short: a loop over the piece's words.
@@ -505,7 +510,7 @@ struct Thin {
             }
             wv[b] = widen<kThroughF32>(c, sb);
           }
-          multiply<kThroughF32>(wv, from + i * 4 * G, lo);
+          multiply<kThroughF32>(wv, from + i * 4 * G, plane);
         }
       }
     }
@@ -515,26 +520,35 @@ struct Thin {
   // the format that the weights come in or were brought to.
   template <Widen HOW>
   __device__ __forceinline__ void multiply(const u32x4 (&wv)[NB], const unsigned char *at,
-                                           int lo_plane) {
-    constexpr bool kSplitHere = A == kF16 && HOW != kToF16;
-    u32x4 v = *reinterpret_cast<const u32x4 *>(at), lo{};
-    if constexpr (A == kF32) lo = *reinterpret_cast<const u32x4 *>(at + lo_plane);
-    if constexpr (kSplitHere) split_f16(v, v, lo);
+                                           int plane) {
+    u32x4 v = *reinterpret_cast<const u32x4 *>(at);
+    if constexpr (A == kF32) {
+      const u32x4 term[3] = {v, *reinterpret_cast<const u32x4 *>(at + plane),
+                             *reinterpret_cast<const u32x4 *>(at + 2 * plane)};
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if constexpr (A == kF32 && HOW == kToF16) {
-        // fp16 weights are split too; the product of the two low parts,
-        // 2^-18 of the whole, is left out
-        u32x4 wh, wl;
-        split_f16_weights(wv[b], wh, wl);
-        acc[b] = mfma_bf16(wh, v, acc[b]);
-        acc[b] = mfma_bf16(wh, lo, acc[b]);
-        acc[b] = mfma_bf16(wl, v, acc[b]);
-      } else if constexpr (HOW == kToF16) {
-        acc[b] = mfma_f16(wv[b], v, acc[b]);
-      } else {
-        acc[b] = mfma_bf16(wv[b], v, acc[b]);
-        if constexpr (A == kF32 || kSplitHere) acc[b] = mfma_bf16(wv[b], lo, acc[b]);
+      for (int b = 0; b < NB; ++b) {
+        u32x4 w = wv[b];
+        if constexpr (HOW == kToF16) {  // fp16 weights are split too
+          u32x4 rest;
+          split_f16_weights(wv[b], w, rest);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) acc[b] = mfma_bf16(rest, term[i], acc[b]);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) acc[b] = mfma_bf16(w, term[i], acc[b]);
+      }
+    } else {
+      constexpr bool kSplitHere = A == kF16 && HOW != kToF16;
+      u32x4 lo{};
+      if constexpr (kSplitHere) split_f16(v, v, lo);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if constexpr (HOW == kToF16) {
+          acc[b] = mfma_f16(wv[b], v, acc[b]);
+        } else {
+          acc[b] = mfma_bf16(wv[b], v, acc[b]);
+          if constexpr (kSplitHere) acc[b] = mfma_bf16(wv[b], lo, acc[b]);
+        }
       }
     }
   }
