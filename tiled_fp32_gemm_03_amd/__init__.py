@@ -44,6 +44,10 @@ result); ``format`` names the 16-bit format when A and B hold raw codes
 workspace=None)`` runs the split-K form; it allocates the workspace as a torch
 tensor when none is given.
 
+Every one of these and of the calls below takes ``stream``, a hipStream_t as int,
+in place of torch's current stream; results and workspaces that the call allocates
+then belong to that stream, as inside ``torch.cuda.stream``.
+
 4-bit microscaled (MX) matrices are ``MxTensor``s, rows of K values in blocks
 of 32 along K.  ``mx_quantize(X, along="rows")`` makes one from a float32,
 bfloat16 or float16 matrix; ``along="columns"`` takes its columns as the rows
@@ -453,6 +457,19 @@ def _ld(t) -> int:
     return max(1, t.stride(0) if t.shape[0] > 1 else t.shape[1])
 
 
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor of torch's allocator that belongs to ``stream`` (None:
+    the current one).  The allocator reuses a tensor's memory in the order of the
+    stream that it belongs to, so one that is used on another would be handed out
+    while it is still in use, and taken while earlier work still uses it."""
+    if stream is None or stream == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    owner = (torch.cuda.ExternalStream(stream, device=device) if stream
+             else torch.cuda.default_stream(device))
+    with torch.cuda.stream(owner):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def matmul(A, B, out=None, variant="prod", config: int = -1, stream=None):
     """C = A x B on the GPU for float32 tensors (row-major views with unit last stride)."""
     import torch
@@ -465,7 +482,7 @@ def matmul(A, B, out=None, variant="prod", config: int = -1, stream=None):
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)}")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=A.device)
+        out = _empty((M, N), torch.float32, A.device, stream)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M, N) or not out.is_cuda:
         raise TypeError("out must be a float32 CUDA tensor of shape (M, N)")
     if stream is None:
@@ -504,7 +521,7 @@ def matmul_mixed(A, B, out=None, config: int = -1, stream=None, format=None):
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)}")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=A.device)
+        out = _empty((M, N), torch.float32, A.device, stream)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M, N) or not out.is_cuda:
         raise TypeError("out must be a float32 CUDA tensor of shape (M, N)")
     if stream is None:
@@ -533,12 +550,12 @@ def matmul_splitk(A, B, out=None, config: int = -1, splits: int = 0, workspace=N
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)}")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=A.device)
+        out = _empty((M, N), torch.float32, A.device, stream)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M, N) or not out.is_cuda:
         raise TypeError("out must be a float32 CUDA tensor of shape (M, N)")
     plan = gemm_f32_splitk_plan(M, N, K, config, splits)
     if workspace is None and plan["workspace_bytes"] > 0:
-        workspace = torch.empty(plan["workspace_bytes"] // 4, dtype=torch.float32, device=A.device)
+        workspace = _empty((plan["workspace_bytes"] // 4,), torch.float32, A.device, stream)
     ws_ptr = workspace.data_ptr() if workspace is not None else 0
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if stream is None:
@@ -632,9 +649,9 @@ def _launch(fn, where: str, device, stream, args) -> None:
         raise GemmError(rc, where)
 
 
-def _mx_out(out, shape, dtype, device):
+def _mx_out(out, shape, dtype, device, stream):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, device, stream)
     if out.dtype != dtype or tuple(out.shape) != tuple(shape) or out.device != device:
         raise TypeError(f"out must be a {dtype} tensor of shape {tuple(shape)} on {device}")
     return out
@@ -652,8 +669,8 @@ def mx_quantize(X, along: str = "rows", out=None, stream=None):
         rows, K = K, rows
     if out is None:
         c, s = (K + 31) // 32 * 16, (K + 511) // 512 * 16
-        codes = torch.empty((rows, c), dtype=torch.uint8, device=device)
-        scales = torch.empty((rows, s), dtype=torch.uint8, device=device)
+        codes = _empty((rows, c), torch.uint8, device, stream)
+        scales = _empty((rows, s), torch.uint8, device, stream)
         out = MxTensor(codes, scales, K)
         args = codes.data_ptr(), c or 16, scales.data_ptr(), s or 16
     else:
@@ -674,7 +691,7 @@ def mx_dequantize(q, dtype=torch.float32, along: str = "rows", out=None, stream=
     device, way = q.codes.device, _along(along)
     args = _mx_args(q, "q", device)
     rows, K = q.codes.shape[0], q.K
-    out = _mx_out(out, (rows, K) if way == 0 else (K, rows), dtype, device)
+    out = _mx_out(out, (rows, K) if way == 0 else (K, rows), dtype, device, stream)
     _launch(_lib.gemm_mx_dequantize, "gemm_mx_dequantize", device, stream,
             (rows, K, *args, out.data_ptr(), _pitch(out), fmt, way))
     return out
@@ -709,10 +726,10 @@ def matmul_mx(A, B, dtype=torch.float32, out=None, config: int = -1, stream=None
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} and {tuple(B.shape)}")
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=device)
+        out = _empty((M, N), dtype, device, stream)
         ldc = N or 1
     else:
-        _mx_out(out, (M, N), dtype, device)
+        _mx_out(out, (M, N), dtype, device, stream)
         ldc = _pitch(out)
     if mx:
         _launch(_lib.gemm_mx, "gemm_mx", device, stream,
@@ -792,15 +809,15 @@ def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None,
         raise ValueError(f"sizes outside the layer's bounds: {T} tokens, {E} experts, top {top}, "
                          f"widths {H} and {I}")
     if out is None:
-        out = torch.empty((T, H), dtype=dtype, device=device)
+        out = _empty((T, H), dtype, device, stream)
         ldy = H
     else:
-        _mx_out(out, (T, H), dtype, device)
+        _mx_out(out, (T, H), dtype, device, stream)
         ldy = _pitch(out)
-    ids = torch.empty((T, top), dtype=torch.int32, device=device)
-    gates = torch.empty((T, top), dtype=torch.float32, device=device)
+    ids = _empty((T, top), torch.int32, device, stream)
+    gates = _empty((T, top), torch.float32, device, stream)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _empty((need,), torch.uint8, device, stream)
     elif workspace.device != device or not workspace.is_contiguous():
         raise TypeError(f"workspace must be a contiguous tensor on {device}")
     _launch(_lib.gemm_moe, "gemm_moe", device, stream,
