@@ -7,7 +7,7 @@
  * For each of T tokens (rows x of X):
  *   z[e]    = sum_h x[h] R[e][h]                      e < E, summed in 64 bits
  *   chosen  = the `top` experts of largest z, in falling order; of equal z the
- *             lower index first; a NaN counts as the lowest z
+ *             lower index first; a NaN counts as the lowest z here
  *   gate[s] = exp(z[chosen s]) / sum over all E of exp(z), or, with
  *             `renormalize`, over the chosen ones alone
  *   y       = sum_s gate[s] W2[e_s] u,   u[i] = silu(W1[e_s][i] . x) *
@@ -16,7 +16,9 @@
  * Sums and u are held in fp32, and all of u's bits enter the second product;
  * y is rounded once to its format.  Results do not depend on
  * timing.  A token whose row holds an infinity or a NaN may give NaN in its
- * own row of Y and gates, and no other's; an infinity among W2's 16-bit
+ * own row of Y and gates, and no other's (a NaN in a row of R: in the rows of
+ * the tokens whose sum of exp(z) has it, with `renormalize` those that choose
+ * its expert); an infinity among W2's 16-bit
  * weights may give NaN where it enters.
  *
  * Memory, streams and errors are as for gemm_f32 (gemm_f32.h): device

@@ -124,18 +124,16 @@ __device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, 
   const double low = -__builtin_inf();
   double z[kPerLane], key[kPerLane];
   unsigned taken = 0;  // bit i: expert lane + 64 i is taken, or past E
-  bool nan = false;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int e = lane + 64 * i;
     const bool in = e < p.E;
     z[i] = in ? logits[e] : low;
     taken |= in ? 0u : 1u << i;
-    nan |= z[i] != z[i];
     key[i] = z[i] != z[i] ? low : z[i];
   }
   int id = 0;          // lane s: choice s,
-  double value = 0.0;  // its logit
+  double value = 0.0;  // its logit (a NaN stays one)
   for (int s = 0; s < p.top; ++s) {
     double best = low;
 #pragma unroll
@@ -151,12 +149,13 @@ __device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, 
       found = true;
       const int at = __builtin_ctzll(m);
       if (lane == at) taken |= 1u << i;
-      if (lane == s) id = 64 * i + at, value = best;
+      const double logit = lane_f64(z[i], at);
+      if (lane == s) id = 64 * i + at, value = logit;
     }
   }
   if (lane < p.top) r.chosen[slot * p.top + lane] = (unsigned short)id;
   if (!GATES) return;
-  // Gates: a NaN among the logits makes every one NaN.
+  // Gates: a NaN among the logits that the sum takes makes every one NaN.
   const double zmax = lane_f64(value, 0);
   double w = lane < p.top ? exp(value - zmax) : 0.0, part = w;
   if (!p.renormalize) {
@@ -165,7 +164,7 @@ __device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, 
     for (int i = 0; i < kPerLane; ++i)
       if (64 * i < p.E) part += lane + 64 * i < p.E ? exp(z[i] - zmax) : 0.0;
   }
-  const double total = __any(nan) ? __builtin_nan("") : wave_sum(part);
+  const double total = wave_sum(part);
   if (lane < p.top) r.gate[slot * p.top + lane] = (float)(w / total);
 }
 
