@@ -688,6 +688,8 @@ def mx_dequantize(q, dtype=torch.float32, along: str = "rows", out=None, stream=
     fmt = _MX_DTYPES.get(dtype)
     if fmt is None:
         raise TypeError("dtype must be float32, bfloat16 or float16")
+    if not isinstance(q, MxTensor):
+        raise TypeError("q must be an MxTensor")
     device, way = q.codes.device, _along(along)
     args = _mx_args(q, "q", device)
     rows, K = q.codes.shape[0], q.K
