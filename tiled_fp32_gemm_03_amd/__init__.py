@@ -352,6 +352,12 @@ def gemm_mixed_tile(config, M, N, K) -> dict:
     return {"BM": bm, "BN": bn, "BK": bk, "threads": nt, "config": chosen}
 
 
+def _fits(*sizes) -> None:
+    """Refuses what the C interface's int does not hold (ctypes would cut it)."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"sizes and pitches must be below 2^31: {max(sizes, key=abs)}")
+
+
 def _mx_format(fmt) -> int:
     if isinstance(fmt, str):
         try:
@@ -371,20 +377,24 @@ def _along(along) -> int:
 
 
 def gemm_mx_code_bytes(K) -> int:
+    _fits(int(K))
     return int(_lib.gemm_mx_code_bytes(int(K)))
 
 
 def gemm_mx_scale_bytes(K) -> int:
+    _fits(int(K))
     return int(_lib.gemm_mx_scale_bytes(int(K)))
 
 
 def gemm_mx_quantize(rows, K, X, ldx, format, along, codes, ld, scales, lds, stream=0) -> None:
+    _fits(rows, K, ldx, ld, lds)
     _check(_lib.gemm_mx_quantize(rows, K, X or None, ldx, _mx_format(format), _along(along),
                                  codes or None, ld, scales or None, lds, stream or None),
            "gemm_mx_quantize")
 
 
 def gemm_mx_dequantize(rows, K, codes, ld, scales, lds, Y, ldy, format, along, stream=0) -> None:
+    _fits(rows, K, ld, lds, ldy)
     _check(_lib.gemm_mx_dequantize(rows, K, codes or None, ld, scales or None, lds, Y or None, ldy,
                                    _mx_format(format), _along(along), stream or None),
            "gemm_mx_dequantize")
@@ -392,6 +402,7 @@ def gemm_mx_dequantize(rows, K, codes, ld, scales, lds, Y, ldy, format, along, s
 
 def gemm_mx(M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, c_format, config=-1,
             stream=0) -> None:
+    _fits(M, N, K, lda, ldsa, ldb, ldsb, ldc, int(config))
     _check(_lib.gemm_mx(M, N, K, A or None, lda, SA or None, ldsa, B or None, ldb, SB or None,
                         ldsb, C or None, ldc, _mx_format(c_format), int(config), stream or None),
            "gemm_mx")
@@ -403,6 +414,7 @@ def gemm_mx_num_configs() -> int:
 
 def gemm_mx_tile(config, M, N, K) -> dict:
     vals = [ctypes.c_int(0) for _ in range(5)]
+    _fits(int(config), M, N, K)
     rc = _lib.gemm_mx_tile(int(config), M, N, K, *[ctypes.byref(v) for v in vals])
     _check(rc, "gemm_mx_tile")
     bm, bn, bk, nt, chosen = (v.value for v in vals)
@@ -410,6 +422,7 @@ def gemm_mx_tile(config, M, N, K) -> dict:
 
 
 def gemm_mx_a16(M, N, K, A, lda, a_format, B, ldb, SB, ldsb, C, ldc, c_format, stream=0) -> None:
+    _fits(M, N, K, lda, ldb, ldsb, ldc)
     _check(_lib.gemm_mx_a16(M, N, K, A or None, lda, _format(a_format), B or None, ldb,
                             SB or None, ldsb, C or None, ldc, _mx_format(c_format),
                             stream or None),
@@ -417,6 +430,7 @@ def gemm_mx_a16(M, N, K, A, lda, a_format, B, ldb, SB, ldsb, C, ldc, c_format, s
 
 
 def gemm_moe_workspace_bytes(T, E, top, H, I) -> int:
+    _fits(int(T), int(E), int(top), int(H), int(I))
     return int(_lib.gemm_moe_workspace_bytes(int(T), int(E), int(top), int(H), int(I)))
 
 
@@ -424,6 +438,7 @@ def gemm_moe(T, E, top, H, I, X, ldx, R, ldr, format, W1, ld1, S1, lds1, W2, ld2
              renormalize, Y, ldy, y_format, ids, gates, workspace, workspace_bytes,
              stream=0) -> None:
     weights = MOE_WEIGHTS[weights] if isinstance(weights, str) else int(weights)
+    _fits(T, E, top, H, I, ldx, ldr, ld1, lds1, ld2, lds2, weights, ldy)
     _check(_lib.gemm_moe(T, E, top, H, I, X or None, ldx, R or None, ldr, _format(format),
                          W1 or None, ld1, S1 or None, lds1, W2 or None, ld2, S2 or None, lds2,
                          weights, int(renormalize), Y or None, ldy, _mx_format(y_format),
@@ -667,6 +682,7 @@ def mx_quantize(X, along: str = "rows", out=None, stream=None):
     rows, K = X.shape
     if way == 1:
         rows, K = K, rows
+    _fits(rows, K, ldx)
     if out is None:
         c, s = (K + 31) // 32 * 16, (K + 511) // 512 * 16
         codes = _empty((rows, c), torch.uint8, device, stream)
@@ -677,6 +693,7 @@ def mx_quantize(X, along: str = "rows", out=None, stream=None):
         args = _mx_args(out, "out", device)
         if out.shape != (rows, K):
             raise ValueError(f"out must be an MxTensor of shape {(rows, K)}")
+        _fits(args[1], args[3])
     _launch(_lib.gemm_mx_quantize, "gemm_mx_quantize", device, stream,
             (rows, K, X.data_ptr(), ldx, fmt, way, *args))
     return out
@@ -693,9 +710,12 @@ def mx_dequantize(q, dtype=torch.float32, along: str = "rows", out=None, stream=
     device, way = q.codes.device, _along(along)
     args = _mx_args(q, "q", device)
     rows, K = q.codes.shape[0], q.K
+    _fits(rows, K, args[1], args[3])
     out = _mx_out(out, (rows, K) if way == 0 else (K, rows), dtype, device, stream)
+    ldy = _pitch(out)
+    _fits(ldy)
     _launch(_lib.gemm_mx_dequantize, "gemm_mx_dequantize", device, stream,
-            (rows, K, *args, out.data_ptr(), _pitch(out), fmt, way))
+            (rows, K, *args, out.data_ptr(), ldy, fmt, way))
     return out
 
 
@@ -727,12 +747,14 @@ def matmul_mx(A, B, dtype=torch.float32, out=None, config: int = -1, stream=None
         M, K2 = A.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} and {tuple(B.shape)}")
+    _fits(M, N, K, config, a[1], b[1], b[3], a[3] if mx else 0)
     if out is None:
         out = _empty((M, N), dtype, device, stream)
         ldc = N or 1
     else:
         _mx_out(out, (M, N), dtype, device, stream)
         ldc = _pitch(out)
+        _fits(ldc)
     if mx:
         _launch(_lib.gemm_mx, "gemm_mx", device, stream,
                 (M, N, K, *a, *b, out.data_ptr(), ldc, fmt, config))
@@ -806,6 +828,7 @@ def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None,
     if dtype not in (X.dtype, torch.float32):
         raise TypeError(f"dtype must be {X.dtype} or float32")
     top = int(top)
+    _fits(T, E, top, H, I, ldx, ldr, a1[1], a1[3], a2[1], a2[3])
     need = _lib.gemm_moe_workspace_bytes(T, E, top, H, I)
     if need < 0:
         raise ValueError(f"sizes outside the layer's bounds: {T} tokens, {E} experts, top {top}, "
@@ -816,6 +839,7 @@ def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None,
     else:
         _mx_out(out, (T, H), dtype, device, stream)
         ldy = _pitch(out)
+        _fits(ldy)
     ids = _empty((T, top), torch.int32, device, stream)
     gates = _empty((T, top), torch.float32, device, stream)
     if workspace is None:
