@@ -18,20 +18,22 @@ struct ThinProblem {
 };
 
 // The launches of a kernel that takes `rows` rows in each grid row: several
-// where one cannot have as many grid rows.
+// where one cannot have as many grid rows, or columns.
 template <class Launch>
-hipError_t in_grid_rows(ThinProblem p, int rows, Launch launch) {
-  const long long most = (long long)rows * kMaxGridY;
-  const int M = p.M;
-  const size_t size = p.c_format == kF32 ? 4 : 2;
-  for (long long m = 0; m < M; m += most) {
-    p.M = (int)(M - m < most ? M - m : most);
-    const hipError_t e = launch(p, (unsigned)ceil_div(p.M, rows));
-    if (e != hipSuccess) return e;
-    p.A += p.M * p.lda;
-    p.C = static_cast<char *>(p.C) + (size_t)p.M * p.ldc * size;
-  }
-  return hipSuccess;
+hipError_t in_grid_rows(const ThinProblem &all, int rows, Launch launch) {
+  return in_columns(all, [&](ThinProblem p) {
+    const long long most = (long long)rows * kMaxGridY;
+    const int M = p.M;
+    const size_t size = p.c_format == kF32 ? 4 : 2;
+    for (long long m = 0; m < M; m += most) {
+      p.M = (int)(M - m < most ? M - m : most);
+      const hipError_t e = launch(p, (unsigned)ceil_div(p.M, rows));
+      if (e != hipSuccess) return e;
+      p.A += p.M * p.lda;
+      p.C = static_cast<char *>(p.C) + (size_t)p.M * p.ldc * size;
+    }
+    return hipSuccess;
+  });
 }
 
 // Little work: 16 columns to a workgroup, whose waves share K, 8 / MB to
@@ -436,9 +438,11 @@ __global__ void __launch_bounds__(64 * kFewWaves) mx_few_kernel(MxProblem p) {
 
 template <int MB>
 hipError_t launch_few(const MxProblem &p, hipStream_t s) {
-  const long long gy = ceil_div(p.M, 16 * MB);
-  const dim3 grid((unsigned)ceil_div(p.N, 16), (unsigned)(gy < kMaxGridY ? gy : kMaxGridY));
-  return launch_kernel(mx_few_kernel<MB>, grid, dim3(64 * kFewWaves), s, p);
+  return in_columns(p, [&](const MxProblem &q) {
+    const long long gy = ceil_div(q.M, 16 * MB);
+    const dim3 grid((unsigned)ceil_div(q.N, 16), (unsigned)(gy < kMaxGridY ? gy : kMaxGridY));
+    return launch_kernel(mx_few_kernel<MB>, grid, dim3(64 * kFewWaves), s, q);
+  });
 }
 
 // Rows that start in the middle of a word, of a matrix that starts on one.

@@ -328,6 +328,27 @@ hipError_t launch_mx_tiles(const MxProblem &p, hipStream_t s) {
   }
 }
 
+// Entry 0, in launches of at most 2^23 tiles (a grid has fewer than 2^32
+// threads): columns 2^26 at a time, then as many rows as those leave.
+hipError_t launch_mx_direct(const MxProblem &p, hipStream_t s) {
+  return in_columns(p, [&](const MxProblem &part) {
+    const long long tiles_n = ceil_div(part.N, 64), most = 64 * ((1LL << 23) / tiles_n);
+    const long long size = format_bytes(p.c_format);
+    for (long long m = 0; m < p.M; m += most) {
+      MxProblem q = part;
+      q.M = (int)(p.M - m < most ? p.M - m : most);
+      q.A.codes += m * p.A.ld;
+      q.A.scales += m * p.A.lds;
+      q.C = static_cast<char *>(part.C) + m * p.ldc * size;
+      const long long tiles_m = ceil_div(q.M, 64);
+      const hipError_t e = launch_kernel(mx_direct_kernel, dim3((unsigned)(tiles_m * tiles_n)),
+                                         dim3(256), s, q, (int)tiles_m, (int)tiles_n);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  });
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(256) mx_zero_kernel(void *C, int M, int N, long long ldc) {
   for (long long m = blockIdx.y; m < M; m += gridDim.y)
@@ -366,10 +387,7 @@ hipError_t launch_mx_gemm(int entry, const MxProblem &p, hipStream_t s) {
     return launch_mx_tiles<128>(p, s);
   }
   if (entry == 2 && mx_tile_fits<64>(p)) return launch_mx_tiles<64>(p, s);
-  const long long tiles_m = ceil_div(p.M, 64), tiles_n = ceil_div(p.N, 64);
-  if (tiles_m * tiles_n > 0x7fffffffLL) return hipErrorInvalidValue;
-  return launch_kernel(mx_direct_kernel, dim3((unsigned)(tiles_m * tiles_n)), dim3(256), s, p,
-                       (int)tiles_m, (int)tiles_n);
+  return launch_mx_direct(p, s);
 }
 
 }  // namespace gemm_f32_impl

@@ -82,6 +82,26 @@ struct MoeProblem {
 };
 hipError_t launch_moe(const MoeProblem &p, hipStream_t s);
 
+// The launches of a product whose grid's x goes along columns, 16 of them to
+// a workgroup of up to 512 threads or more to more: several where one grid
+// cannot have as many workgroups (a grid has fewer than 2^32 threads in x; past that
+// the runtime takes their number modulo 2^32, without an error).
+constexpr long long kMostColumns = 1LL << 26;
+template <class P, class Launch>
+hipError_t in_columns(const P &p, Launch launch) {
+  const long long size = format_bytes(p.c_format);
+  for (long long n = 0; n < p.N; n += kMostColumns) {
+    P q = p;
+    q.N = (int)(p.N - n < kMostColumns ? p.N - n : kMostColumns);
+    q.B.codes += n * p.B.ld;
+    q.B.scales += n * p.B.lds;
+    q.C = static_cast<char *>(p.C) + n * size;
+    const hipError_t e = launch(q);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // C = 0 in any format.
 hipError_t launch_mx_zero(void *C, int M, int N, long long ldc, int c_format, hipStream_t s);
 

@@ -244,6 +244,23 @@ dim3 cols_grid(long long ktiles, int rows) {
   const long long gy = ktiles < kMaxGridY ? ktiles : kMaxGridY;
   return dim3((unsigned)gx, (unsigned)(gy < most ? gy : most));
 }
+// The launches of a conversion down columns: two where one would have 2^32
+// threads in x.
+template <class Kernel>
+hipError_t in_cols(Kernel kern, const MxConvert &c, int format, long long ktiles, hipStream_t s) {
+  constexpr int kMostCols = 1 << 30;
+  for (long long r = 0; r < c.rows; r += kMostCols) {
+    MxConvert q = c;
+    q.rows = (int)(c.rows - r < kMostCols ? c.rows - r : kMostCols);
+    if (c.x) q.x = static_cast<const char *>(c.x) + r * format_bytes(format);
+    if (c.y) q.y = static_cast<char *>(c.y) + r * format_bytes(format);
+    q.codes += r * c.ld;
+    q.scales += r * c.lds;
+    const hipError_t e = launch_kernel(kern, cols_grid(ktiles, q.rows), dim3(kThreads), s, q, (int)ktiles);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 }  // namespace
 
@@ -261,7 +278,7 @@ hipError_t launch_mx_quantize(int format, int along, const MxConvert &c, hipStre
               : format == kF16 ? quant_cols_kernel<kF16>
                                : quant_cols_kernel<kF32>;
   const long long ktiles = mx_scale_bytes(c.K) / kColBlocks;  // whole scale rows are written
-  return launch_kernel(kern, cols_grid(ktiles, c.rows), dim3(kThreads), s, c, (int)ktiles);
+  return in_cols(kern, c, format, ktiles, s);
 }
 
 hipError_t launch_mx_dequantize(int format, int along, const MxConvert &c, hipStream_t s) {
@@ -278,7 +295,7 @@ hipError_t launch_mx_dequantize(int format, int along, const MxConvert &c, hipSt
               : format == kF16 ? dequant_cols_kernel<kF16>
                                : dequant_cols_kernel<kF32>;
   const long long ktiles = ceil_div(mx_blocks(c.K), kColBlocks);
-  return launch_kernel(kern, cols_grid(ktiles, c.rows), dim3(kThreads), s, c, (int)ktiles);
+  return in_cols(kern, c, format, ktiles, s);
 }
 
 }  // namespace gemm_f32_impl
