@@ -142,8 +142,8 @@ struct Wide {
   // `at`: the lane's operands of the wave's 128 values.
   template <Widen HOW>
   __device__ __forceinline__ void words(const unsigned char *at, int j, const uint32_t (&c)[2],
-                                        const uint32_t (&sb)[2]) {
-    const u32x4 w0 = widen<HOW>(c[0], sb[0]), w1 = widen<HOW>(c[1], sb[1]);
+                                        const uint32_t (&sb)[2], int down = 0) {
+    const u32x4 w0 = widen<HOW>(c[0], sb[0], down), w1 = widen<HOW>(c[1], sb[1], down);
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       u32x4 a = *reinterpret_cast<const u32x4 *>(at + 4 * j * kGroup + 256 * i), lo{};
@@ -165,7 +165,7 @@ struct Wide {
   // that hold the chunk's scales.
   __device__ __forceinline__ void use(const Weights &x, uint32_t scales, int half,
                                       const unsigned char *at, int lane, int kb, int nb) {
-    constexpr uint32_t kLow = A == kF16 ? 104 : 1, kHigh = A == kF16 ? 140 : 254;
+    constexpr uint32_t kLow = A == kF16 ? 104 : 1, kHigh = A == kF16 ? 140 : kTopScale;
     const int from = loader(lane);
     bool ok = true;
     uint32_t sb[2], c[4][2];
@@ -184,12 +184,17 @@ struct Wide {
 #pragma unroll
       for (int j = 0; j < 4; ++j) words<A == kF16 ? kToF16 : kToBf16>(at, j, c[j], sb);
     } else {  // rare, and kept short
+      const Quartered quarter(top_scale(sb[0]) || top_scale(sb[1]));
+#pragma unroll
+      for (int i = 0; i < MB; ++i) quarter.before(acc[i][0]), quarter.before(acc[i][1]);
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         const uint32_t d[2] = {j < 2 ? (j ? c[1][0] : c[0][0]) : j == 2 ? c[2][0] : c[3][0],
                                j < 2 ? (j ? c[1][1] : c[0][1]) : j == 2 ? c[2][1] : c[3][1]};
-        words<kThroughF32>(at, j, d, sb);
+        words<kThroughF32>(at, j, d, sb, quarter.down());
       }
+#pragma unroll
+      for (int i = 0; i < MB; ++i) quarter.after(acc[i][0]), quarter.after(acc[i][1]);
     }
   }
 };

@@ -185,12 +185,13 @@ struct Eight<kShort> : Eight<kWords> {
 
 // How the values of MX weights become matrix operands.  As bf16 or fp16 by
 // one conversion per two values where every scale of the piece allows it:
-// bf16 holds every element under scale bytes 1 to 254 (0.5 2^-126 is a
-// subnormal that it holds exactly), fp16 under 104 to 140 (0.5 2^-23 is its
-// smallest step, 6 2^13 below its largest value).  Otherwise through fp32.
+// bf16 holds every element under scale bytes 1 to 252 (0.5 2^-126 is a
+// subnormal that it holds exactly, 6 2^125 below its largest value), fp16 under
+// 104 to 140 (0.5 2^-23 is its smallest step, 6 2^13 below its largest value).
+// Otherwise through fp32, over 2^down (see Quartered).
 enum Widen { kToBf16, kToF16, kThroughF32 };
 template <Widen HOW>
-__device__ inline u32x4 widen(uint32_t codes, uint32_t sb) {
+__device__ inline u32x4 widen(uint32_t codes, uint32_t sb, int down = 0) {
   if constexpr (HOW == kToBf16) {
     const float unit = __builtin_bit_cast(float, sb << 23);
     const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, unit, 0);
@@ -209,11 +210,25 @@ __device__ inline u32x4 widen(uint32_t codes, uint32_t sb) {
                  __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3)};
   } else {
     float v[8];
-    decode8(codes, sb, v);
+    decode8(codes, sb, v, down);
     return u32x4{pack2<kBf16>(v[0], v[1]), pack2<kBf16>(v[2], v[3]), pack2<kBf16>(v[4], v[5]),
                  pack2<kBf16>(v[6], v[7])};
   }
 }
+
+// Elements under scale bytes 253 and 254 can be past bf16's largest value, their
+// products need not be.  A piece that has such a byte (`top`: the lane's do) is
+// multiplied at a quarter of its size, which bf16 holds of the smallest elements
+// too, onto a quarter of the sums so far.
+constexpr uint32_t kTopScale = 252;
+__device__ inline bool top_scale(uint32_t sb) { return sb - (kTopScale + 1) <= 1u; }
+struct Quartered {
+  bool on;
+  __device__ __forceinline__ explicit Quartered(bool top) : on(__any(top)) {}
+  __device__ __forceinline__ int down() const { return on ? 2 : 0; }
+  __device__ __forceinline__ void before(f32x4 &acc) const { acc *= on ? 0.25f : 1.f; }
+  __device__ __forceinline__ void after(f32x4 &acc) const { acc *= on ? 4.f : 1.f; }
+};
 
 // The wave's number in its workgroup, as a scalar.
 __device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
@@ -484,7 +499,7 @@ struct Thin {
       bool ok = true;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        ok &= A == kF16 ? y[b]->template within<104, 140>() : y[b]->template within<1, 254>();
+        ok &= A == kF16 ? y[b]->template within<104, 140>() : y[b]->template within<1, kTopScale>();
       if (__all(ok)) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
@@ -497,6 +512,14 @@ struct Thin {
           }
       } else {
         // Rare, and kept short: a loop over the piece's words.
+        bool top = false;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) top |= top_scale(y[b]->s[s]);
+        const Quartered quarter(top);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) quarter.before(acc[b]);
 #pragma unroll 1
         for (int i = 0; i < 16; ++i) {
           u32x4 wv[NB];
@@ -508,10 +531,12 @@ struct Thin {
               if (q == i) c = y[b]->c[q >> 2][q & 3];
               if (q == i) sb = y[b]->s[q >> 2];
             }
-            wv[b] = widen<kThroughF32>(c, sb);
+            wv[b] = widen<kThroughF32>(c, sb, quarter.down());
           }
           multiply<kThroughF32>(wv, from + i * 4 * G, plane);
         }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) quarter.after(acc[b]);
       }
     }
   }
@@ -564,8 +589,8 @@ struct Direct {
   f32x4 acc;
   // The products of 8 values per lane, of MX words that allow `kHow` or not.
   template <Widen HOW>
-  __device__ __forceinline__ void add(uint32_t codes, uint32_t sb, u32x4 v) {
-    const u32x4 wv = widen<HOW>(codes, sb);
+  __device__ __forceinline__ void add(uint32_t codes, uint32_t sb, u32x4 v, int down = 0) {
+    const u32x4 wv = widen<HOW>(codes, sb, down);
     if constexpr (HOW == kToF16) {
       acc = mfma_f16(wv, v, acc);
     } else {
@@ -595,7 +620,7 @@ struct Direct {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const uint32_t sb = sc[i] >> (8 * m) & 255u;
-          ok &= A == kF16 ? sb - 104u <= 140u - 104u : sb - 1u <= 253u;
+          ok &= A == kF16 ? sb - 104u <= 140u - 104u : sb - 1u < kTopScale;
         }
       }
       if (__all(ok)) {
@@ -613,9 +638,12 @@ struct Direct {
       if (kb >= nb) break;
       const uint32_t c = *reinterpret_cast<const uint32_t *>(w.p + 16LL * kb + 4 * part);
       const long long k = 32LL * kb + 8 * part;
-      add<kThroughF32>(from_lane(c, from),
-                       from_lane(s, 4 * (lane & 15) + (q >> 2)) >> (8 * (q & 3)) & 255u,
-                       from_lane(load_guarded(a, k < K ? k : K, K), from));
+      const uint32_t sb = from_lane(s, 4 * (lane & 15) + (q >> 2)) >> (8 * (q & 3)) & 255u;
+      const Quartered quarter(top_scale(sb));
+      quarter.before(acc);
+      add<kThroughF32>(from_lane(c, from), sb, from_lane(load_guarded(a, k < K ? k : K, K), from),
+                       quarter.down());
+      quarter.after(acc);
     }
   }
 };

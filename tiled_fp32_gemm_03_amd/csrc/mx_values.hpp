@@ -145,14 +145,14 @@ __device__ inline uint32_t encode8(const float (&v)[8], uint32_t sb) {
 
 // The 8 values of a word of codes under scale byte `sb`: the elements, then
 // one exact scaling by v_ldexp_f32 (rounded only below fp32's subnormals,
-// which no element reaches; past its range an infinity).
-__device__ inline void decode8(uint32_t w, uint32_t sb, float (&v)[8]) {
+// which no element reaches; past its range an infinity), over 2^down.
+__device__ inline void decode8(uint32_t w, uint32_t sb, float (&v)[8], int down = 0) {
   f32x2 p[4];
   p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 0);
   p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 1);
   p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 2);
   p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 3);
-  const int e = (int)sb - 127;
+  const int e = (int)sb - 127 - down;
   const float nan = __builtin_nanf("");
 #pragma unroll
   for (int j = 0; j < 8; ++j)
