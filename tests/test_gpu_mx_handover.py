@@ -96,3 +96,18 @@ def test_one_token_in_several_tiles(g, H, fmt, weights):
         y, gi, _ = g.moe_layer(x.to(_dev()), r.to(_dev()), g1, g2, top, dtype=torch.float32)
         assert np.array_equal(gi.cpu().numpy(), ids)
         _check(y, ref, bar, "f32", (H, fmt, weights))
+
+
+@pytest.mark.parametrize("weights", ["w16", "mx"])
+@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [4, 50])
+def test_two_waves_to_a_group(g, T, fmt, weights):
+    """8 experts of 129 and 131 groups, which 16-bit weights' waves share by twos."""
+    E, top, H, I = 8, 2, 2057, 2090
+    rng = np.random.default_rng(T)
+    x, r, w1, w2 = _make(rng, T, E, H, I, fmt, weights)
+    g1, g2, v1, v2 = _on_gpu(g, w1, w2, E, H, I)
+    ref, bar, ids, _ = _layer(x.double().numpy(), r.double().numpy(), v1, v2, top, True)
+    y, gi, _ = g.moe_layer(x.to(_dev()), r.to(_dev()), g1, g2, top, dtype=torch.float32)
+    assert np.array_equal(gi.cpu().numpy(), ids)
+    _check(y, ref, bar, "f32", (T, fmt, weights))

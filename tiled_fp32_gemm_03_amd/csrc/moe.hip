@@ -551,16 +551,18 @@ template <int W, int A>
 MoeShape shape_of(long long experts, int columns, int K, int rows) {
   const long long groups = experts * ceil_div(columns, 16);
   MoeShape sh;
-  // Waves per group: until they are four to a compute unit, or eight where each
-  // keeps 16 pieces; more only stage the same activations more often.  Eight
-  // against four, us: 16 tokens on fp16 W2 rows of 4095 119 and 133; 16 tokens on
-  // 8 experts, MX rows of 4096 41 and 36, bf16 rows of 4096 64 and 62.
+  // Waves per group: until they are four to a compute unit; and two where groups
+  // are fewer than eight to one and 16-bit rows have 16 pieces or more.  One and
+  // two, us (experts' pairs, H / I, weights): 2, 2049 / 2049, bf16 88 and 82; 2,
+  // 2048 / 2048, bf16 62 and 64; 16, 2048 / 2048, bf16 95 and 88; 16, 3501 / 3501, fp16
+  // 256 and 230; 16, 2101 / 8001, fp16 389 and 322; but MX, 16, 8000 / 2100 193 and
+  // 211.  Two and four, where two make more than four to a compute unit: 20, 4001 / 2501,
+  // bf16 160 and 168; 2, 4000 / 2500, bf16 70 and 67; 20, 8000 / 2100, fp16 202 and 219.
   const long long pieces = ceil_div(K, kPieceK<W>);
   sh.waves = kWaves;
   sh.ks = 1;
-  while (sh.ks < kWaves && 2 * sh.ks <= pieces &&
-         (groups * sh.ks < 4 * 256 || (groups * sh.ks < 8 * 256 && pieces >= 32 * sh.ks)))
-    sh.ks *= 2;
+  while (sh.ks < kWaves && 2 * sh.ks <= pieces && groups * sh.ks < 4 * 256) sh.ks *= 2;
+  if (W != kMx && sh.ks == 1 && groups < 8 * 256 && pieces >= 16) sh.ks = 2;
   while (sh.ks > 1 && tile_bytes<W, A>(rows, K, sh.ks) > kMostLds) sh.ks /= 2;
   // Groups per wave: while workgroups are left for two on each compute unit
   // (three, us: 33 tokens, 8 of 64 experts, 2048 / 1024, MX 83 against 76; 8
