@@ -184,14 +184,14 @@ struct Wide {
 #pragma unroll
       for (int j = 0; j < 4; ++j) words<A == kF16 ? kToF16 : kToBf16>(at, j, c[j], sb);
     } else {  // rare, and kept short
-      const Quartered quarter(top_scale(sb[0]) || top_scale(sb[1]));
+      const Quartered quarter(top_scale(sb[0]) | top_scale(sb[1]));
 #pragma unroll
       for (int i = 0; i < MB; ++i) quarter.before(acc[i][0]), quarter.before(acc[i][1]);
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         const uint32_t d[2] = {j < 2 ? (j ? c[1][0] : c[0][0]) : j == 2 ? c[2][0] : c[3][0],
                                j < 2 ? (j ? c[1][1] : c[0][1]) : j == 2 ? c[2][1] : c[3][1]};
-        words<kThroughF32>(at, j, d, sb, quarter.down());
+        words<kThroughF32>(at, j, d, sb, quarter.down);
       }
 #pragma unroll
       for (int i = 0; i < MB; ++i) quarter.after(acc[i][0]), quarter.after(acc[i][1]);

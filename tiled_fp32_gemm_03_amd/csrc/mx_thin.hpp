@@ -217,17 +217,21 @@ __device__ inline u32x4 widen(uint32_t codes, uint32_t sb, int down = 0) {
 }
 
 // Elements under scale bytes 253 and 254 can be past bf16's largest value, their
-// products need not be.  A piece that has such a byte (`top`: the lane's do) is
-// multiplied at a quarter of its size, which bf16 holds of the smallest elements
-// too, onto a quarter of the sums so far.
+// products need not be.  A piece that has such a byte is multiplied at a quarter of
+// its size, which bf16 holds of the smallest elements too, onto a quarter of the sums
+// so far.  `bytes`: the lane's, through top_scale, or'ed (255, a NaN, counts too,
+// and stays one).
 constexpr uint32_t kTopScale = 252;
-__device__ inline bool top_scale(uint32_t sb) { return sb - (kTopScale + 1) <= 1u; }
+__device__ inline uint32_t top_scale(uint32_t sb) { return sb + (255 - kTopScale); }  // bit 8: past it
 struct Quartered {
-  bool on;
-  __device__ __forceinline__ explicit Quartered(bool top) : on(__any(top)) {}
-  __device__ __forceinline__ int down() const { return on ? 2 : 0; }
-  __device__ __forceinline__ void before(f32x4 &acc) const { acc *= on ? 0.25f : 1.f; }
-  __device__ __forceinline__ void after(f32x4 &acc) const { acc *= on ? 4.f : 1.f; }
+  int down;
+  __device__ __forceinline__ explicit Quartered(uint32_t bytes) : down(__any((bytes & 256) != 0) ? 2 : 0) {}
+  __device__ __forceinline__ void before(f32x4 &acc) const { scale(acc, -down); }
+  __device__ __forceinline__ void after(f32x4 &acc) const { scale(acc, down); }
+  static __device__ __forceinline__ void scale(f32x4 &acc, int e) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_amdgcn_ldexpf(acc[i], e);
+  }
 };
 
 // The wave's number in its workgroup, as a scalar.
@@ -500,7 +504,7 @@ struct Thin {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         ok &= A == kF16 ? y[b]->template within<104, 140>() : y[b]->template within<1, kTopScale>();
-      if (__all(ok)) {
+      if (__builtin_expect(__all(ok), 1)) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -512,7 +516,7 @@ struct Thin {
           }
       } else {
         // Rare, and kept short: a loop over the piece's words.
-        bool top = false;
+        uint32_t top = 0;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -531,7 +535,7 @@ struct Thin {
               if (q == i) c = y[b]->c[q >> 2][q & 3];
               if (q == i) sb = y[b]->s[q >> 2];
             }
-            wv[b] = widen<kThroughF32>(c, sb, quarter.down());
+            wv[b] = widen<kThroughF32>(c, sb, quarter.down);
           }
           multiply<kThroughF32>(wv, from + i * 4 * G, plane);
         }
@@ -642,7 +646,7 @@ struct Direct {
       const Quartered quarter(top_scale(sb));
       quarter.before(acc);
       add<kThroughF32>(from_lane(c, from), sb, from_lane(load_guarded(a, k < K ? k : K, K), from),
-                       quarter.down());
+                       quarter.down);
       quarter.after(acc);
     }
   }
