@@ -165,7 +165,6 @@ struct Wide {
   // that hold the chunk's scales.
   __device__ __forceinline__ void use(const Weights &x, uint32_t scales, int half,
                                       const unsigned char *at, int lane, int kb, int nb) {
-    constexpr uint32_t kLow = A == kF16 ? 104 : 1, kHigh = A == kF16 ? 140 : kTopScale;
     const int from = loader(lane);
     bool ok = true;
     uint32_t sb[2], c[4][2];
@@ -173,12 +172,14 @@ struct Wide {
     for (int b = 0; b < 2; ++b) {
       const uint32_t s = from_lane(scales, 32 * half + 16 * b + (lane & 15));
       sb[b] = kb < nb ? s >> (8 * (lane >> 4)) & 255u : 127u;
-      ok &= sb[b] - kLow <= kHigh - kLow;
+      uint32_t any = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t v = from_lane(x.c[b][j], from);
         c[j][b] = kb < nb ? v : 0u;
+        any |= c[j][b];
       }
+      ok &= widens_fast<A>(sb[b], any);
     }
     if (__all(ok)) {
 #pragma unroll
@@ -323,10 +324,6 @@ hipError_t launch_a16(const ThinProblem &p, hipStream_t s) {
 // rows.  A lane then holds blocks 4 g + s of a piece's 16 (g = l / 16) and
 // their scales as the bytes of a word, which the matrix instruction picks.
 
-template <int CTRL>
-__device__ inline uint32_t quad(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
-}
 // Lane i's r[t] goes to lane t's r[i], in each four lanes.
 __device__ __forceinline__ void quad_transpose(u32x4 (&r)[4], int lane) {
   const bool odd = lane & 1, high = lane & 2;

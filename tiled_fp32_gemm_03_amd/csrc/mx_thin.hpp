@@ -185,10 +185,12 @@ struct Eight<kShort> : Eight<kWords> {
 
 // How the values of MX weights become matrix operands.  As bf16 or fp16 by
 // one conversion per two values where every scale of the piece allows it:
-// bf16 holds every element under scale bytes 1 to 252 (0.5 2^-126 is a
-// subnormal that it holds exactly, 6 2^125 below its largest value), fp16 under
-// 104 to 140 (0.5 2^-23 is its smallest step, 6 2^13 below its largest value).
-// Otherwise through fp32, over 2^down (see Quartered).
+// bf16 holds every element under scale bytes 0 to 252 (0.5 2^-127 is a
+// subnormal that it holds exactly, 6 2^125 below its largest value; the conversion
+// takes a scale's exponent bits alone, 0 as 2^-127), fp16 under 104 to 140 (0.5
+// 2^-23 is its smallest step, 6 2^13 below its largest value) and zeros under all
+// but 255: a block of them has byte 0.  Otherwise through fp32, over 2^down (see
+// Quartered).
 enum Widen { kToBf16, kToF16, kThroughF32 };
 template <Widen HOW>
 __device__ inline u32x4 widen(uint32_t codes, uint32_t sb, int down = 0) {
@@ -234,6 +236,13 @@ struct Quartered {
   }
 };
 
+// Whether codes under scale byte `sb` can be widened to bf16, or to fp16 (A ==
+// kF16), by conversion.
+template <int A>
+__device__ inline bool widens_fast(uint32_t sb, uint32_t codes) {
+  return A == kF16 ? sb - 104u <= 140u - 104u || (codes == 0 && sb != 255) : sb <= kTopScale;
+}
+
 // The wave's number in its workgroup, as a scalar.
 __device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
@@ -251,6 +260,11 @@ __device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {
 __device__ __forceinline__ u32x4 from_lane(u32x4 v, int lane) {
   return u32x4{from_lane(v[0], lane), from_lane(v[1], lane), from_lane(v[2], lane),
                from_lane(v[3], lane)};
+}
+// Exchanges inside each four lanes.
+template <int CTRL>
+__device__ inline uint32_t quad(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
 }
 // The lane whose load holds this lane's operand.
 __device__ __forceinline__ int loader(int lane) { return 4 * (lane & 15) + (lane >> 4); }
@@ -296,13 +310,12 @@ struct MxBlocks {
         }
     }
   }
-  // Whether all of the lane's blocks have scales within (blocks of zeros allow any).
-  template <uint32_t LOW, uint32_t HIGH>
-  __device__ __forceinline__ bool within() const {
+  template <int A>
+  __device__ __forceinline__ bool widens_fast() const {
     bool ok = true;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      ok &= s[i] - LOW <= HIGH - LOW || (s[i] != 255 && (c[i][0] | c[i][1] | c[i][2] | c[i][3]) == 0);
+      ok &= gemm_f32_impl::widens_fast<A>(s[i], c[i][0] | c[i][1] | c[i][2] | c[i][3]);
     return ok;
   }
 };
@@ -503,7 +516,7 @@ struct Thin {
       bool ok = true;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        ok &= A == kF16 ? y[b]->template within<104, 140>() : y[b]->template within<1, kTopScale>();
+        ok &= y[b]->template widens_fast<A>();
       if (__builtin_expect(__all(ok), 1)) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
@@ -617,16 +630,15 @@ struct Direct {
         c[q] = *reinterpret_cast<const uint32_t *>(w.p + 16 * (16LL * piece + q) + 4 * part);
         v[q].load(a, 32 * (16LL * piece + q) + 8 * part, K);
       }
+      // Looked at as loaded: the lane's codes are of row l / 4, whose scales the
+      // quad's lanes have (with the operands' codes, 1 x 4096 x 4096 took 0.4 us more).
       bool ok = true;
+      const uint32_t row[4] = {quad<0x00>(s), quad<0x55>(s), quad<0xAA>(s), quad<0xFF>(s)};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sc[i] = from_lane(s, 4 * (lane & 15) + i);
+      for (int q = 0; q < 16; ++q)
+        ok &= widens_fast<A>(row[q >> 2] >> (8 * (q & 3)) & 255u, c[q]);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint32_t sb = sc[i] >> (8 * m) & 255u;
-          ok &= A == kF16 ? sb - 104u <= 140u - 104u : sb - 1u < kTopScale;
-        }
-      }
+      for (int i = 0; i < 4; ++i) sc[i] = from_lane(s, 4 * (lane & 15) + i);
       if (__all(ok)) {
 #pragma unroll
         for (int q = 0; q < 16; ++q)
