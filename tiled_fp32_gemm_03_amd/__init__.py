@@ -352,10 +352,13 @@ def gemm_mixed_tile(config, M, N, K) -> dict:
     return {"BM": bm, "BN": bn, "BK": bk, "threads": nt, "config": chosen}
 
 
+_INT_MAX = 0x7fffffff
+
+
 def _fits(*sizes) -> None:
     """Refuses what the C interface's int does not hold (ctypes would cut it)."""
-    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
-        raise ValueError(f"sizes and pitches must be below 2^31: {max(sizes, key=abs)}")
+    if max(sizes) > _INT_MAX or min(sizes) < -_INT_MAX - 1:
+        raise ValueError(f"sizes and pitches must be below 2^31, not {max(sizes, key=abs)}")
 
 
 def _mx_format(fmt) -> int:
@@ -472,17 +475,21 @@ def _ld(t) -> int:
     return max(1, t.stride(0) if t.shape[0] > 1 else t.shape[1])
 
 
-def _empty(shape, dtype, device, stream):
-    """An uninitialised tensor of torch's allocator that belongs to ``stream`` (None:
-    the current one).  The allocator reuses a tensor's memory in the order of the
-    stream that it belongs to, so one that is used on another would be handed out
-    while it is still in use, and taken while earlier work still uses it."""
+def _empty(device, stream):
+    """torch.empty for tensors that belong to ``stream`` (None: the current one).  The
+    allocator reuses a tensor's memory in the order of the stream that it belongs to,
+    so one that is used on another would be handed out while it is still in use, and
+    taken while earlier work still uses it."""
     if stream is None or stream == torch._C._cuda_getCurrentRawStream(device.index):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty
     owner = (torch.cuda.ExternalStream(stream, device=device) if stream
              else torch.cuda.default_stream(device))
-    with torch.cuda.stream(owner):
-        return torch.empty(shape, dtype=dtype, device=device)
+
+    def empty(*args, **kw):
+        with torch.cuda.stream(owner):
+            return torch.empty(*args, **kw)
+
+    return empty
 
 
 def matmul(A, B, out=None, variant="prod", config: int = -1, stream=None):
@@ -497,7 +504,7 @@ def matmul(A, B, out=None, variant="prod", config: int = -1, stream=None):
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)}")
     if out is None:
-        out = _empty((M, N), torch.float32, A.device, stream)
+        out = _empty(A.device, stream)((M, N), dtype=torch.float32, device=A.device)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M, N) or not out.is_cuda:
         raise TypeError("out must be a float32 CUDA tensor of shape (M, N)")
     if stream is None:
@@ -536,7 +543,7 @@ def matmul_mixed(A, B, out=None, config: int = -1, stream=None, format=None):
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)}")
     if out is None:
-        out = _empty((M, N), torch.float32, A.device, stream)
+        out = _empty(A.device, stream)((M, N), dtype=torch.float32, device=A.device)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M, N) or not out.is_cuda:
         raise TypeError("out must be a float32 CUDA tensor of shape (M, N)")
     if stream is None:
@@ -565,12 +572,13 @@ def matmul_splitk(A, B, out=None, config: int = -1, splits: int = 0, workspace=N
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} x {tuple(B.shape)}")
     if out is None:
-        out = _empty((M, N), torch.float32, A.device, stream)
+        out = _empty(A.device, stream)((M, N), dtype=torch.float32, device=A.device)
     elif out.dtype != torch.float32 or tuple(out.shape) != (M, N) or not out.is_cuda:
         raise TypeError("out must be a float32 CUDA tensor of shape (M, N)")
     plan = gemm_f32_splitk_plan(M, N, K, config, splits)
     if workspace is None and plan["workspace_bytes"] > 0:
-        workspace = _empty((plan["workspace_bytes"] // 4,), torch.float32, A.device, stream)
+        workspace = _empty(A.device, stream)(plan["workspace_bytes"] // 4, dtype=torch.float32,
+                                             device=A.device)
     ws_ptr = workspace.data_ptr() if workspace is not None else 0
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     if stream is None:
@@ -666,7 +674,7 @@ def _launch(fn, where: str, device, stream, args) -> None:
 
 def _mx_out(out, shape, dtype, device, stream):
     if out is None:
-        return _empty(shape, dtype, device, stream)
+        return _empty(device, stream)(shape, dtype=dtype, device=device)
     if out.dtype != dtype or tuple(out.shape) != tuple(shape) or out.device != device:
         raise TypeError(f"out must be a {dtype} tensor of shape {tuple(shape)} on {device}")
     return out
@@ -682,11 +690,13 @@ def mx_quantize(X, along: str = "rows", out=None, stream=None):
     rows, K = X.shape
     if way == 1:
         rows, K = K, rows
-    _fits(rows, K, ldx)
+    if max(rows, K, ldx) > _INT_MAX:
+        _fits(rows, K, ldx)
     if out is None:
         c, s = (K + 31) // 32 * 16, (K + 511) // 512 * 16
-        codes = _empty((rows, c), torch.uint8, device, stream)
-        scales = _empty((rows, s), torch.uint8, device, stream)
+        empty = _empty(device, stream)
+        codes = empty((rows, c), dtype=torch.uint8, device=device)
+        scales = empty((rows, s), dtype=torch.uint8, device=device)
         out = MxTensor(codes, scales, K)
         args = codes.data_ptr(), c or 16, scales.data_ptr(), s or 16
     else:
@@ -710,10 +720,10 @@ def mx_dequantize(q, dtype=torch.float32, along: str = "rows", out=None, stream=
     device, way = q.codes.device, _along(along)
     args = _mx_args(q, "q", device)
     rows, K = q.codes.shape[0], q.K
-    _fits(rows, K, args[1], args[3])
     out = _mx_out(out, (rows, K) if way == 0 else (K, rows), dtype, device, stream)
     ldy = _pitch(out)
-    _fits(ldy)
+    if max(rows, K, args[1], args[3], ldy) > _INT_MAX:
+        _fits(rows, K, args[1], args[3], ldy)
     _launch(_lib.gemm_mx_dequantize, "gemm_mx_dequantize", device, stream,
             (rows, K, *args, out.data_ptr(), ldy, fmt, way))
     return out
@@ -747,9 +757,10 @@ def matmul_mx(A, B, dtype=torch.float32, out=None, config: int = -1, stream=None
         M, K2 = A.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} and {tuple(B.shape)}")
-    _fits(M, N, K, config, a[1], b[1], b[3], a[3] if mx else 0)
+    if max(M, N, K, config, a[1], b[1], b[3], a[3] if mx else 0) > _INT_MAX:
+        _fits(M, N, K, config, a[1], b[1], b[3], a[3] if mx else 0)
     if out is None:
-        out = _empty((M, N), dtype, device, stream)
+        out = _empty(device, stream)((M, N), dtype=dtype, device=device)
         ldc = N or 1
     else:
         _mx_out(out, (M, N), dtype, device, stream)
@@ -828,22 +839,24 @@ def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None,
     if dtype not in (X.dtype, torch.float32):
         raise TypeError(f"dtype must be {X.dtype} or float32")
     top = int(top)
-    _fits(T, E, top, H, I, ldx, ldr, a1[1], a1[3], a2[1], a2[3])
+    if max(T, E, top, H, I, ldx, ldr, a1[1], a1[3], a2[1], a2[3]) > _INT_MAX:
+        _fits(T, E, top, H, I, ldx, ldr, a1[1], a1[3], a2[1], a2[3])
     need = _lib.gemm_moe_workspace_bytes(T, E, top, H, I)
     if need < 0:
         raise ValueError(f"sizes outside the layer's bounds: {T} tokens, {E} experts, top {top}, "
                          f"widths {H} and {I}")
+    empty = _empty(device, stream)
     if out is None:
-        out = _empty((T, H), dtype, device, stream)
+        out = empty((T, H), dtype=dtype, device=device)
         ldy = H
     else:
         _mx_out(out, (T, H), dtype, device, stream)
         ldy = _pitch(out)
         _fits(ldy)
-    ids = _empty((T, top), torch.int32, device, stream)
-    gates = _empty((T, top), torch.float32, device, stream)
+    ids = empty((T, top), dtype=torch.int32, device=device)
+    gates = empty((T, top), dtype=torch.float32, device=device)
     if workspace is None:
-        workspace = _empty((need,), torch.uint8, device, stream)
+        workspace = empty(need, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise TypeError(f"workspace must be a contiguous tensor on {device}")
     _launch(_lib.gemm_moe, "gemm_moe", device, stream,
