@@ -104,9 +104,10 @@ int gemm_mx_tile(int config, int M, int N, int K, int *BM, int *BN, int *BK, int
 /*
  * gemm_mx_a16 -- C[i][j] = sum_{k<K} A[i][k] B(j, k) with A in 16 bits
  * (row-major M x K in `a_format`, 2-byte aligned, lda in elements) and B MX:
- * weights in 4 bits, activations as they are.  Every A value enters exactly.
- * Made for few rows (up to 64 of them read B once from memory); any M is
- * served.
+ * weights in 4 bits, activations as they are.  Every A value and every value of
+ * B enters exactly.  Made for few rows (up to 32 read B once, up to 64 where N and
+ * K are large; blocks of rows past that read it again, from cache where it holds
+ * it); any M is served.
  */
 int gemm_mx_a16(int M, int N, int K, const void *A, int lda, int a_format,
                 const unsigned char *B, int ldb, const unsigned char *SB, int ldsb, void *C,

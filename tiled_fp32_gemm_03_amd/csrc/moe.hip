@@ -292,11 +292,12 @@ __global__ void __launch_bounds__(kListThreads) moe_list_kernel(MoeProblem p) {
 // are groups enough to fill the chip, more where there are few.  A wave goes
 // through `each` groups, its weights loaded ahead across them.
 //
-// Memory bounds them: the chosen experts' weights once.  First products run at
-// 4.3 to 4.4 TB/s (268 MB of fp16 weights with odd rows 63 us, the same loads
-// alone 59; 285 MB of MX weights 65 us, alone 58), second ones at 3.3 to 3.6 (134
-// MB of fp16 weights 41 us, alone 37: 16 rows of 64 bytes at a time; 142 MB of
-// MX weights 40 us, alone 32: their activations are twice as large).
+// Memory bounds the first: the chosen experts' weights once, at 4.2 to 4.5 TB/s
+// (268 MB of fp16 weights with odd rows 64 us, the same loads alone 59; 285 MB of
+// MX weights 64 us, alone 58).  Second ones run at 2.7 to 3.2 TB/s (134 MB of fp16
+// weights 50 us, alone 37: 16 rows of 64 bytes at a time; 142 MB of MX weights 44
+// us, alone 32): their activations are three terms, of six bytes a value in LDS,
+// which leaves a compute unit eight waves.
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;  // of the first product's workgroups
 constexpr int kMostWaves = 8;                      // of the second one's: 4 or 8

@@ -87,13 +87,16 @@ __global__ void __launch_bounds__(256) mx_direct_kernel(MxProblem p, int tiles_m
 // of a tile are 32-bit from its first row (the launcher checks the pitch).
 // C is at least one tile each way; edge tiles are moved back inside it.
 //
-// 8192 cubed takes 289 us (3.8 PFLOP/s; 4096 cubed with fp32 C 51 us, of which
-// 16 are its launch, first loads and stores).  The matrix unit is busy 0.38 of
-// the time at 2.2 GHz.  Timing copies: without the direct loads 253 us,
-// without the operand reads 296, without both 217.  Measured and not kept: the
-// 32x32x64 instruction (308 us), the next step's first operands read before
-// the barrier (316), non-temporal stores (319), eight waves of 128 x 64 (287; a
-// fifth fewer cycles at a lower clock, and 4096 cubed 57).
+// 8192 cubed takes 279 to 289 us (3.8 to 3.9 PFLOP/s, 2.2 us a step; 4096 cubed
+// with fp32 C 40 us, of which about 5 are its launch, first loads and stores).  The
+// matrix unit is busy 0.38 of the time at 2.2 GHz.  Timing copies: without the
+// direct loads 253 us, without the operand reads 296, without both 217.  Measured
+// and not kept: the 32x32x64 instruction (308 us), the next step's first operands
+// read before the barrier (316), non-temporal stores (319), eight waves of 128 x 64
+// (287; a fifth fewer cycles at a lower clock, and 4096 cubed slower).  Odd sizes
+// with 16-bit C cost more than their steps: 4097 x 4095 x 2049 takes 40 us before
+// its last row, 20 of them its 9 steps (its stores are 32 bytes to a row and
+// instruction at 2-byte alignment, and these forms spill 3 to 5 registers).
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr int kOutside = (int)0x80000000u;  // an offset past every record count

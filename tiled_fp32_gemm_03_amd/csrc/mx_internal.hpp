@@ -39,7 +39,7 @@ struct MxProblem {
   long long ldc;
   int c_format;
 };
-hipError_t launch_mx_thin(const MxProblem &p, hipStream_t s);  // any M, made for up to 64
+hipError_t launch_mx_thin(const MxProblem &p, hipStream_t s);  // any M, 32 rows at a time
 hipError_t launch_mx_gemm(int entry, const MxProblem &p, hipStream_t s);
 
 // C = A B^T with A in 16 bits (pitch in elements) and B MX.
