@@ -13,13 +13,12 @@
  *   y       = sum_s gate[s] W2[e_s] u,   u[i] = silu(W1[e_s][i] . x) *
  *             (W1[e_s][I + i] . x),      silu(v) = v / (1 + exp(-v))
  *
- * Sums and u are held in fp32, and all of u's bits enter the second product;
- * y is rounded once to its format.  Results do not depend on
- * timing.  A token whose row holds an infinity or a NaN may give NaN in its
- * own row of Y and gates, and no other's (a NaN in a row of R: in the rows of
- * the tokens whose sum of exp(z) has it, with `renormalize` those that choose
- * its expert); an infinity among W2's 16-bit
- * weights may give NaN where it enters.
+ * Sums and u are held in fp32, and u's bits down to 2^-133 enter the second
+ * product; y is rounded once to its format.  Results do not depend on timing.
+ * A token whose row holds an infinity or a NaN may give NaN in its own row of Y
+ * and gates, and no other's.  A NaN in a row of R does in the rows of the tokens
+ * whose sum of exp(z) has it (with `renormalize`, those that choose its expert);
+ * an infinity among W2's 16-bit weights may give NaN where it enters.
  *
  * Memory, streams and errors are as for gemm_f32 (gemm_f32.h): device
  * pointers owned by the caller, nothing allocated, asynchronous on `stream`,
