@@ -32,6 +32,16 @@ Raw C-ABI mirrors (same names and argument order as ``include/gemm_f32.h``):
   gemm_moe(T, E, top, H, I, X, ldx, R, ldr, format, W1, ld1, S1, lds1, W2, ld2, S2, lds2, weights,
            renormalize, Y, ldy, y_format, ids, gates, workspace, workspace_bytes, stream),
   gemm_moe_workspace_bytes(T, E, top, H, I)             (include/gemm_moe.h)
+  gemm_moe_route(T, E, top, Z, ldz, format, score, bias, groups, top_groups, group_score,
+                 renormalize, scale, ids, gates, stream),
+  gemm_moe_route_backward(T, E, top, dgates, Z, ldz, format, score, renormalize, scale, ids, dZ,
+                          lddz, stream)                 (include/gemm_route.h)
+  gemm_experts(T, E, top, H, I, X, ldx, ids, gates, format, W1, ld1, S1, lds1, W2, ld2, S2, lds2,
+               weights, Y, ldy, saved, workspace, workspace_bytes, stream),
+  gemm_experts_backward(T, E, top, H, I, dY, lddy, X, ldx, ids, gates, format, W1, ld1, W2, ld2,
+                        saved, dX, lddx, dgates, dW1, lddw1, dW2, lddw2, workspace,
+                        workspace_bytes, stream),
+  gemm_experts_workspace_bytes(T, E, top, H, I, backward)  (include/gemm_experts.h)
 Pointers are device addresses (ints); ``stream`` is a hipStream_t as int
 (0 = null stream).  A non-zero status raises ``GemmError``.
 
@@ -59,6 +69,12 @@ the ``MxTensor`` B, C[i][j] = sum_k A[i][k] B[j][k].
 ``moe_layer(X, router, w1, w2, top)`` is a mixture-of-experts layer for a few
 tokens, the experts' weights being 16-bit tensors or stacks of MX matrices; it
 returns the result, the chosen experts and their gates.
+
+The same in parts, for other routers, any number of tokens and training:
+``moe_route(logits, top)`` chooses experts and gates from logits (softmax or
+sigmoid scores, a bias for balance, groups of experts), ``moe_experts(X, ids,
+gates, w1, w2)`` is the experts' products for a choice, and
+``moe_route_backward`` and ``moe_experts_backward`` are their gradients.
 """
 from __future__ import annotations
 
@@ -83,6 +99,10 @@ __all__ = [
     "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx", "gemm_mx_tile", "gemm_mx_num_configs",
     "gemm_mx_a16", "gemm_mx_code_bytes", "gemm_mx_scale_bytes",
     "gemm_moe", "gemm_moe_workspace_bytes", "moe_layer", "MOE_WEIGHTS",
+    "gemm_moe_route", "gemm_moe_route_backward", "moe_route", "moe_route_backward",
+    "ROUTE_SCORES", "ROUTE_GROUP_SCORES",
+    "gemm_experts", "gemm_experts_backward", "gemm_experts_workspace_bytes", "moe_experts",
+    "moe_experts_backward",
     "library_path",
     "exported_symbols",
 ]
@@ -105,6 +125,7 @@ _lib = ctypes.CDLL(_LIB_PATH)
 
 _i = ctypes.c_int
 _ll = ctypes.c_longlong
+_f = ctypes.c_float
 _p = ctypes.c_void_p
 _ip = ctypes.POINTER(ctypes.c_int)
 
@@ -141,6 +162,13 @@ _SIGS = {
     "gemm_moe_workspace_bytes": ([_i, _i, _i, _i, _i], _ll),
     "gemm_moe": ([_i, _i, _i, _i, _i, _p, _i, _p, _i, _i, _p, _i, _p, _i, _p, _i, _p, _i, _i, _i,
                   _p, _i, _i, _p, _p, _p, _ll, _p], _i),
+    "gemm_moe_route": ([_i, _i, _i, _p, _i, _i, _i, _p, _i, _i, _i, _i, _f, _p, _p, _p], _i),
+    "gemm_moe_route_backward": ([_i, _i, _i, _p, _p, _i, _i, _i, _i, _f, _p, _p, _i, _p], _i),
+    "gemm_experts_workspace_bytes": ([_i, _i, _i, _i, _i, _i], _ll),
+    "gemm_experts": ([_i, _i, _i, _i, _i, _p, _i, _p, _p, _i, _p, _i, _p, _i, _p, _i, _p, _i, _i,
+                      _p, _i, _p, _p, _ll, _p], _i),
+    "gemm_experts_backward": ([_i, _i, _i, _i, _i, _p, _i, _p, _i, _p, _p, _i, _p, _i, _p, _i, _p,
+                               _p, _i, _p, _p, _i, _p, _i, _p, _ll, _p], _i),
     "gemm_f32_probe_lds_bytes": ([_i, _i], _ll),
     "gemm_f32_device_props": ([_i, _ip, _ip, _ip, _ip, _ip], _i),
     "gemm_f32_probe_fused": ([_i, _i, _i, _p, _ll, _p, _p], _i),
@@ -167,6 +195,9 @@ MX_FORMATS = {"bf16": 0, "f16": 1, "f32": 2}
 MX_ALONG = {"rows": 0, "columns": 1}
 # Kinds of expert weights (include/gemm_moe.h).
 MOE_WEIGHTS = {"w16": 0, "mx": 1}
+# Scores of experts and of their groups (include/gemm_route.h).
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+ROUTE_GROUP_SCORES = {"max": 0, "top2": 1}
 _MX_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
@@ -448,6 +479,64 @@ def gemm_moe(T, E, top, H, I, X, ldx, R, ldr, format, W1, ld1, S1, lds1, W2, ld2
                          ids or None, gates or None, workspace or None, int(workspace_bytes),
                          stream or None),
            "gemm_moe")
+
+
+def _named(value, names: dict, what: str) -> int:
+    if isinstance(value, str):
+        try:
+            return names[value]
+        except KeyError:
+            raise ValueError(f"unknown {what} {value!r}; one of {sorted(names)}") from None
+    return int(value)
+
+
+def gemm_moe_route(T, E, top, Z, ldz, format, score, bias, groups, top_groups, group_score,
+                   renormalize, scale, ids, gates, stream=0) -> None:
+    score, group_score = _named(score, ROUTE_SCORES, "score"), _named(group_score, ROUTE_GROUP_SCORES, "group score")
+    _fits(T, E, top, ldz, score, groups, top_groups, group_score)
+    _check(_lib.gemm_moe_route(T, E, top, Z or None, ldz, _mx_format(format), score, bias or None,
+                               groups, top_groups, group_score, int(bool(renormalize)), scale,
+                               ids or None, gates or None, stream or None),
+           "gemm_moe_route")
+
+
+def gemm_moe_route_backward(T, E, top, dgates, Z, ldz, format, score, renormalize, scale, ids, dZ,
+                            lddz, stream=0) -> None:
+    score = _named(score, ROUTE_SCORES, "score")
+    _fits(T, E, top, ldz, score, lddz)
+    _check(_lib.gemm_moe_route_backward(T, E, top, dgates or None, Z or None, ldz,
+                                        _mx_format(format), score, int(bool(renormalize)), scale,
+                                        ids or None, dZ or None, lddz, stream or None),
+           "gemm_moe_route_backward")
+
+
+def gemm_experts_workspace_bytes(T, E, top, H, I, backward=0) -> int:
+    _fits(int(T), int(E), int(top), int(H), int(I))
+    return int(_lib.gemm_experts_workspace_bytes(int(T), int(E), int(top), int(H), int(I),
+                                                 int(bool(backward))))
+
+
+def gemm_experts(T, E, top, H, I, X, ldx, ids, gates, format, W1, ld1, S1, lds1, W2, ld2, S2, lds2,
+                 weights, Y, ldy, saved, workspace, workspace_bytes, stream=0) -> None:
+    weights = _named(weights, MOE_WEIGHTS, "kind of weights")
+    _fits(T, E, top, H, I, ldx, ld1, lds1, ld2, lds2, weights, ldy)
+    _check(_lib.gemm_experts(T, E, top, H, I, X or None, ldx, ids or None, gates or None,
+                             _format(format), W1 or None, ld1, S1 or None, lds1, W2 or None, ld2,
+                             S2 or None, lds2, weights, Y or None, ldy, saved or None,
+                             workspace or None, int(workspace_bytes), stream or None),
+           "gemm_experts")
+
+
+def gemm_experts_backward(T, E, top, H, I, dY, lddy, X, ldx, ids, gates, format, W1, ld1, W2, ld2,
+                          saved, dX, lddx, dgates, dW1, lddw1, dW2, lddw2, workspace,
+                          workspace_bytes, stream=0) -> None:
+    _fits(T, E, top, H, I, lddy, ldx, ld1, ld2, lddx, lddw1, lddw2)
+    _check(_lib.gemm_experts_backward(T, E, top, H, I, dY or None, lddy, X or None, ldx,
+                                      ids or None, gates or None, _format(format), W1 or None, ld1,
+                                      W2 or None, ld2, saved or None, dX or None, lddx,
+                                      dgates or None, dW1 or None, lddw1, dW2 or None, lddw2,
+                                      workspace or None, int(workspace_bytes), stream or None),
+           "gemm_experts_backward")
 
 
 def config_name(variant, config: int = -1, M: int = 1, N: int = 1, K: int = 1) -> str:
@@ -865,3 +954,172 @@ def moe_layer(X, router, w1, w2, top: int, renormalize: bool = True, dtype=None,
              ids.data_ptr(), gates.data_ptr(), workspace.data_ptr(),
              workspace.numel() * workspace.element_size()))
     return out, ids, gates
+
+
+def _choices(ids, gates, name: str, device):
+    """Checks a contiguous (T, top) int32 tensor of ids and its float32 companion."""
+    if ids.dtype != torch.int32 or ids.device != device or ids.dim() != 2 or not ids.is_contiguous():
+        raise TypeError(f"ids must be a contiguous 2-D int32 tensor on {device}")
+    if gates.dtype != torch.float32 or gates.device != device or not gates.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float32 tensor on {device}")
+    if gates.shape != ids.shape:
+        raise ValueError(f"{name} must have the shape of ids, {tuple(ids.shape)}")
+
+
+def _logits(logits):
+    fmt = _MX_DTYPES.get(logits.dtype)
+    if fmt is None or not logits.is_cuda:
+        raise TypeError("logits must be a float32, bfloat16 or float16 CUDA tensor")
+    return fmt, _pitch(logits)
+
+
+def moe_route(logits, top: int, score="softmax", bias=None, groups: int = 1, top_groups: int = 1,
+              group_score="max", renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Chosen experts and their gates from logits (T, E) (include/gemm_route.h): (ids, gates).
+
+    ``score`` is "softmax" or "sigmoid"; ``bias`` (E float32) is added to the scores
+    for the choice alone.  The experts are ``groups`` runs; where ``top_groups`` is
+    less, only experts of that many groups can be chosen, by the largest key in a
+    group (``group_score="max"``) or the sum of its two largest ("top2").  With
+    ``renormalize`` a token's gates add up to ``scale``.  ids are (T, top) int32,
+    gates (T, top) float32.
+    """
+    fmt, ldz = _logits(logits)
+    device = logits.device
+    T, E = logits.shape
+    if bias is not None:
+        if bias.dtype != torch.float32 or bias.device != device or not bias.is_contiguous():
+            raise TypeError(f"bias must be a contiguous float32 tensor on {device}")
+        if tuple(bias.shape) != (E,):
+            raise ValueError(f"bias must have {E} values")
+    top, groups, top_groups = int(top), int(groups), int(top_groups)
+    score = _named(score, ROUTE_SCORES, "score")
+    group_score = _named(group_score, ROUTE_GROUP_SCORES, "group score")
+    _fits(T, E, top, ldz, score, groups, top_groups, group_score)
+    if top < 0:
+        raise ValueError("top must not be negative")
+    empty = _empty(device, stream)
+    ids = empty((T, top), dtype=torch.int32, device=device)
+    gates = empty((T, top), dtype=torch.float32, device=device)
+    _launch(_lib.gemm_moe_route, "gemm_moe_route", device, stream,
+            (T, E, top, logits.data_ptr(), ldz, fmt, score,
+             bias.data_ptr() if bias is not None else None, groups, top_groups, group_score,
+             int(bool(renormalize)), float(scale), ids.data_ptr(), gates.data_ptr()))
+    return ids, gates
+
+
+def moe_route_backward(dgates, logits, ids, score="softmax", renormalize: bool = True,
+                       scale: float = 1.0, out=None, stream=None):
+    """The gradient of moe_route's logits, in their dtype, from that of its gates
+    (T, top): for the ids that it gave and the same score, renormalize and scale."""
+    fmt, ldz = _logits(logits)
+    device = logits.device
+    _choices(ids, dgates, "dgates", device)
+    T, E = logits.shape
+    if ids.shape[0] != T:
+        raise ValueError(f"ids must have {T} rows, not {ids.shape[0]}")
+    score = _named(score, ROUTE_SCORES, "score")
+    out = _mx_out(out, (T, E), logits.dtype, device, stream)
+    lddz = _pitch(out)
+    _fits(T, E, ids.shape[1], ldz, lddz, score)
+    _launch(_lib.gemm_moe_route_backward, "gemm_moe_route_backward", device, stream,
+            (T, E, ids.shape[1], dgates.data_ptr(), logits.data_ptr(), ldz, fmt, score,
+             int(bool(renormalize)), float(scale), ids.data_ptr(), out.data_ptr(), lddz))
+    return out
+
+
+def _workspace(workspace, need: int, empty, device):
+    if workspace is None:
+        return empty(need, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise TypeError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def _experts_sizes(X, ids, gates, w1, w2):
+    if X.dtype not in (torch.bfloat16, torch.float16) or not X.is_cuda:
+        raise TypeError("X must be a bfloat16 or float16 CUDA tensor")
+    device = X.device
+    ldx = _pitch(X)
+    T, H = X.shape
+    _choices(ids, gates, "gates", device)
+    if ids.shape[0] != T:
+        raise ValueError(f"ids must have {T} rows, not {ids.shape[0]}")
+    if isinstance(w1, MxTensor) != isinstance(w2, MxTensor):
+        raise TypeError("w1 and w2 must both be MxTensors or both tensors")
+    if len(w2.shape) != 3:
+        raise ValueError("w2 must have three dimensions: experts, rows, values")
+    E, I = w2.shape[0], w2.shape[2]
+    a1 = _expert_rows(w1, "w1", X.dtype, device, E, 2 * I, H)
+    a2 = _expert_rows(w2, "w2", X.dtype, device, E, H, I)
+    top = ids.shape[1]
+    _fits(T, E, top, H, I, ldx, a1[1], a1[3], a2[1], a2[3])
+    return device, T, E, top, H, I, ldx, a1, a2
+
+
+def _experts_bytes(T, E, top, H, I, backward: int) -> int:
+    need = _lib.gemm_experts_workspace_bytes(T, E, top, H, I, backward)
+    if need < 0:
+        raise ValueError(f"sizes outside the products' bounds: {T} tokens, {E} experts, top {top}, "
+                         f"widths {H} and {I}")
+    return need
+
+
+def moe_experts(X, ids, gates, w1, w2, save: bool = False, out=None, workspace=None, stream=None):
+    """The experts' products for a choice made before (include/gemm_experts.h), y[t] =
+    sum_s gates[t][s] w2[e] u, u = silu(w1[e][:I] x[t]) * (w1[e][I:] x[t]), e = ids[t][s].
+
+    X is (T, H), bfloat16 or float16; ids (T, top) int32, where an id outside 0 .. E - 1
+    is a dropped choice, gates (T, top) float32; w1 is (E, 2 I, H) and w2 (E, H, I),
+    tensors of X's dtype or, up to 256 tokens and without ``save``, stacks of MX matrices.
+    Returns Y, (T, H) in X's dtype; with ``save`` (Y, saved), the second for
+    moe_experts_backward.  ``workspace`` is a uint8 CUDA tensor of at least
+    gemm_experts_workspace_bytes; when None, one is allocated with torch for this call.
+    """
+    device, T, E, top, H, I, ldx, a1, a2 = _experts_sizes(X, ids, gates, w1, w2)
+    mx = isinstance(w2, MxTensor)
+    if mx and (save or T > 256):
+        raise ValueError("MX weights are for up to 256 tokens, without save")
+    need = _experts_bytes(T, E, top, H, I, 0)
+    empty = _empty(device, stream)
+    out = _mx_out(out, (T, H), X.dtype, device, stream)
+    ldy = _pitch(out)
+    _fits(ldy)
+    saved = empty((T * top, 2 * I), dtype=torch.float32, device=device) if save else None
+    workspace = _workspace(workspace, need, empty, device)
+    _launch(_lib.gemm_experts, "gemm_experts", device, stream,
+            (T, E, top, H, I, X.data_ptr(), ldx, ids.data_ptr(), gates.data_ptr(),
+             _MX_DTYPES[X.dtype], *a1, *a2, int(mx), out.data_ptr(), ldy,
+             saved.data_ptr() if save else None, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size()))
+    return (out, saved) if save else out
+
+
+def moe_experts_backward(dY, X, ids, gates, w1, w2, saved, weights: bool = True, workspace=None,
+                         stream=None):
+    """The gradients (dX, dgates, dw1, dw2) of moe_experts from that of its result, with
+    the ``saved`` of the same call; without ``weights`` (dX, dgates) alone."""
+    device, T, E, top, H, I, ldx, a1, a2 = _experts_sizes(X, ids, gates, w1, w2)
+    if isinstance(w2, MxTensor):
+        raise TypeError("w1 and w2 must be tensors")
+    if dY.dtype != X.dtype or dY.device != device or tuple(dY.shape) != (T, H):
+        raise TypeError(f"dY must be a {X.dtype} tensor of shape {(T, H)} on {device}")
+    lddy = _pitch(dY)
+    _fits(lddy)
+    if (saved.dtype != torch.float32 or saved.device != device or not saved.is_contiguous()
+            or tuple(saved.shape) != (T * top, 2 * I)):
+        raise TypeError(f"saved must be a contiguous float32 tensor of shape {(T * top, 2 * I)} on {device}")
+    need = _experts_bytes(T, E, top, H, I, 1)
+    empty = _empty(device, stream)
+    dX = empty((T, H), dtype=X.dtype, device=device)
+    dgates = empty((T, top), dtype=torch.float32, device=device)
+    dw1 = empty((E, 2 * I, H), dtype=X.dtype, device=device) if weights else None
+    dw2 = empty((E, H, I), dtype=X.dtype, device=device) if weights else None
+    workspace = _workspace(workspace, need, empty, device)
+    _launch(_lib.gemm_experts_backward, "gemm_experts_backward", device, stream,
+            (T, E, top, H, I, dY.data_ptr(), lddy, X.data_ptr(), ldx, ids.data_ptr(),
+             gates.data_ptr(), _MX_DTYPES[X.dtype], a1[0], a1[1], a2[0], a2[1], saved.data_ptr(),
+             dX.data_ptr(), H, dgates.data_ptr(), dw1.data_ptr() if weights else None, H,
+             dw2.data_ptr() if weights else None, I, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size()))
+    return (dX, dgates, dw1, dw2) if weights else (dX, dgates)

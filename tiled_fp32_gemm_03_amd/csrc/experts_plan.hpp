@@ -1,0 +1,54 @@
+// Host-only planning of routing, the experts' products and adapters: sizes,
+// argument checks, workspaces and the choice of a kernel.  Plain C++17 with no
+// HIP types, like host_plan.hpp; nothing here touches a GPU.
+#pragma once
+
+#include "mx_plan.hpp"
+
+namespace gemm_f32_impl {
+
+// ---- routing (gemm_route.h) ---------------------------------------------------
+
+constexpr int kRouteMaxTokens = 1 << 22, kRouteMaxExperts = 512, kRouteMaxTop = 16,
+              kRouteMaxGroups = 64;
+constexpr int kSoftmax = 0, kSigmoid = 1;
+constexpr int kGroupMax = 0, kGroupTop2 = 1;
+int route_check_sizes(int T, int E, int top);
+
+// ---- the experts' products (gemm_experts.h) -----------------------------------
+
+constexpr int kExpertsMaxTokens = 1 << 22, kExpertsMaxWidth = 1 << 17;
+int experts_check_sizes(int T, int E, int top, int H, int I);
+
+// A pair is a token's choice, number token * top + choice.  The pairs whose
+// expert is in 0 .. E - 1 are ordered by expert, then by number; a pair's
+// number in that order is its place.
+constexpr int kListPairs = 1024;  // pairs to a workgroup of the listing kernels
+struct ExpertsSpace {
+  long long start;   // int [E + 1]: expert e's places are start[e] .. start[e + 1] - 1
+  long long tiles;   // int [4 + 4 most_tiles]: the number of row tiles, then from the fifth int on
+                     // each one's expert, first place and rows, and 0
+  long long list;    // int [T top]: the pair of each place
+  long long token;   // int [T top]: its token
+  long long where;   // int [T top]: the place of each pair, -1 where it has none
+  long long counts;  // int [list workgroups][E]
+  long long u;       // 16 bits [T top][ipitch], by place: inner values (backward: times their gate)
+  long long part;    // 16 bits [T top][hpitch], by pair: what the pair adds to its token
+  long long dh;      // 16 bits [T top][2 ipitch], by place: gradient of the first product
+  long long dg;      // float [slices][T top], by place: parts of the gates' gradients
+  long long bytes;
+  long long ipitch, hpitch, most_tiles, slices, list_groups;
+};
+// `tile`: rows and columns of a tile.
+ExpertsSpace experts_space(int T, int E, int top, int H, int I, int tile, bool backward);
+// Whether a forward pass without `saved` runs on the thin products of the
+// mixture-of-experts layer.
+bool experts_thin(int T, int E, int top);
+// The tile of a call's products, 256 or 128.
+int experts_tile(int T, int E, int top, int H, int I);
+
+// ---- adapters (gemm_adapters.h) -----------------------------------------------
+
+constexpr int kAdaptersMaxRows = 1 << 24, kAdaptersMaxRank = 512, kAdaptersMaxCount = 1 << 16;
+
+}  // namespace gemm_f32_impl

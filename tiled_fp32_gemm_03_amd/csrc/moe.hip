@@ -192,7 +192,7 @@ __device__ inline void list_pairs(const MoeProblem &p, Route<MAX_PAIRS> &r) {
   for (int c = wave; c < chunks; c += kWaves) {
     const int i = 64 * c + lane, e = i < pairs ? r.chosen[i] : kMoeMaxExperts;
     const unsigned long long same = same_expert(e);
-    if (i < pairs && (same & before) == 0) r.count[c][e] = (unsigned short)__popcll(same);
+    if (e < p.E && (same & before) == 0) r.count[c][e] = (unsigned short)__popcll(same);
   }
   __syncthreads();
   if (wave == 0) {  // where each expert's pairs begin, and the chosen experts
@@ -223,7 +223,7 @@ __device__ inline void list_pairs(const MoeProblem &p, Route<MAX_PAIRS> &r) {
   for (int c = wave; c < chunks; c += kWaves) {
     const int i = 64 * c + lane, e = i < pairs ? r.chosen[i] : kMoeMaxExperts;
     const unsigned long long same = same_expert(e);
-    if (i < pairs) {
+    if (e < p.E) {  // pair i has an expert
       int at = r.start[e] + __popcll(same & before);
       for (int q = 0; q < c; ++q) at += r.count[q][e];
       r.list[at] = (unsigned short)i;
@@ -278,6 +278,26 @@ __global__ void __launch_bounds__(64 * kChooseTokens) moe_choose_kernel(MoeProbl
   write_choice<64 * kChooseTokens>(p, r, t0 * p.top, last * p.top);
 }
 constexpr int kListThreads = 1024;
+// The lists of a choice made before (several tokens): as above, without the pairs
+// that have no expert, which come last.
+__global__ void __launch_bounds__(kListThreads) moe_given_kernel(MoeProblem p) {
+  __shared__ Route<kMoeMaxTokens * kMoeMaxTop> r;
+  __shared__ int valid;
+  const int pairs = p.T * p.top;
+  if (threadIdx.x == 0) valid = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < pairs; i += kListThreads) {
+    const int e = p.given_ids[i];
+    const bool in = e >= 0 && e < p.E;
+    r.chosen[i] = (unsigned short)(in ? e : kMoeMaxExperts);
+    if (in) atomicAdd(&valid, 1);
+  }
+  __syncthreads();
+  list_pairs<kListThreads>(p, r);
+  if (threadIdx.x == 0) r.start[p.E] = (unsigned short)valid;
+  __syncthreads();
+  write_lists<kListThreads>(p, r);
+}
 __global__ void __launch_bounds__(kListThreads) moe_list_kernel(MoeProblem p) {
   __shared__ Route<kMoeMaxTokens * kMoeMaxTop> r;
   for (int i = threadIdx.x; i < p.T * p.top; i += kListThreads)
@@ -309,6 +329,12 @@ constexpr int kMostWaves = 8;                      // of the second one's: 4 or 
 constexpr int kTileLds = 74 * 1024;
 constexpr int kMostLds = 140 * 1024, kCuLds = 160 * 1024;
 
+// The number of pair i's expert in a choice made before, or -1.
+__device__ inline int given_expert(const MoeProblem &p, int i) {
+  const int e = p.given_ids[i];
+  return e >= 0 && e < p.E ? e : -1;
+}
+
 // What the launch chose: waves, waves per group, groups per wave, the tile's LDS.
 struct MoeShape {
   int waves, ks, each, lds;
@@ -320,6 +346,10 @@ struct Expert {
   int e, first, n;  // its number, its first place in the list, its pairs
 };
 __device__ inline bool expert_of(const MoeProblem &p, int a, Expert &x) {
+  if (p.T == 1 && p.given_ids) {
+    x = {given_expert(p, a), a, 1};
+    return x.e >= 0;
+  }
   const int *active = ws_at<int>(p, p.at.active), *start = ws_at<int>(p, p.at.start);
   if (a >= active[0]) return false;
   x.e = active[1 + a];
@@ -428,8 +458,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeProblem p, MoeSh
   __shared__ long long starts[16];  // of the tokens' rows
   Expert x;
   if constexpr (ONE) {
-    const bool writes = blockIdx.x == 0 && blockIdx.y == 0;
-    if (wave_id() == 0) choose_experts<false>(p, route, 0, 0);
+    const bool writes = blockIdx.x == 0 && blockIdx.y == 0 && !p.given_ids;
+    if (p.given_ids && given_expert(p, blockIdx.y) < 0) return;
+    if (wave_id() == 0 && !p.given_ids) choose_experts<false>(p, route, 0, 0);
     if (writes && wave_id() == 1) choose_experts<true>(p, route, 0, 0);  // the same, and the gates
     if (wave_id() >= 2)  // meanwhile the token's first tile
       stage_acts<AF, W, ROWS>(
@@ -445,7 +476,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeProblem p, MoeSh
       }
       if (threadIdx.x == 0) ws_at<int>(p, p.at.active)[0] = p.top;
     }
-    x = {__builtin_amdgcn_readfirstlane(route.chosen[blockIdx.y]), (int)blockIdx.y, 1};
+    x = {p.given_ids ? given_expert(p, blockIdx.y)
+                     : __builtin_amdgcn_readfirstlane(route.chosen[blockIdx.y]),
+         (int)blockIdx.y, 1};
   } else if (!expert_of(p, blockIdx.y, x)) {
     return;
   }
@@ -499,7 +532,8 @@ __global__ void __launch_bounds__(64 * kMostWaves, 2) moe_down_kernel(MoeProblem
     auto row = [&](int r) __attribute__((always_inline)) {
       return p.ws + p.at.u + 4 * (x.first + m0 + r) * p.at.upitch;
     };
-    const int pair = ws_at<int>(p, p.at.list)[x.first + m0 + (l16 < n ? l16 : 0)];
+    const int at = x.first + m0 + (l16 < n ? l16 : 0);
+    const int pair = p.T == 1 ? at : ws_at<int>(p, p.at.list)[at];
     auto done = [&](int c, const f32x4 (&acc)[1]) __attribute__((always_inline)) {
       const long long h = 16LL * c + 4 * g, left = p.H - h;
       store4<kF32>(ws_at<float>(p, p.at.part), pair * p.at.ypitch + h, (int)(left < 4 ? left : 4),
@@ -516,12 +550,14 @@ __global__ void __launch_bounds__(256) moe_sum_kernel(MoeProblem p) {
   const int t = blockIdx.y;
   const long long h = 4LL * (blockIdx.x * 256 + threadIdx.x), left = p.H - h;
   if (left <= 0) return;
-  const float *gates = ws_at<float>(p, p.at.gates) + t * p.top;
+  const float *gates = (p.given_ids ? p.given_gates : ws_at<float>(p, p.at.gates)) + t * p.top;
   const float *part = ws_at<float>(p, p.at.part) + (long long)t * p.top * p.at.ypitch + h;
   f32x4 y{0, 0, 0, 0};
 #pragma unroll 4
-  for (int s = 0; s < p.top; ++s)
+  for (int s = 0; s < p.top; ++s) {
+    if (p.given_ids && given_expert(p, t * p.top + s) < 0) continue;
     y += gates[s] * *reinterpret_cast<const f32x4 *>(part + s * p.at.ypitch);
+  }
   store4_fmt(p.y_format, p.Y, t * p.ldy + h, (int)(left < 4 ? left : 4), y);
 }
 
@@ -635,9 +671,13 @@ hipError_t launch_products(const MoeProblem &p, hipStream_t s) {
 
 hipError_t launch_moe(const MoeProblem &p, hipStream_t s) {
   const bool bf16 = p.format == kBf16;
-  hipError_t e = bf16 ? launch_logits<kBf16>(p, s) : launch_logits<kF16>(p, s);
+  hipError_t e = hipSuccess;
+  if (!p.given_ids) e = bf16 ? launch_logits<kBf16>(p, s) : launch_logits<kF16>(p, s);
   if (e != hipSuccess) return e;
-  if (p.T > 1 && p.T <= kRouteTokens) {
+  if (p.given_ids) {
+    if (p.T > 1) e = launch_kernel(moe_given_kernel, dim3(1), dim3(kListThreads), s, p);
+    if (e != hipSuccess) return e;
+  } else if (p.T > 1 && p.T <= kRouteTokens) {
     e = launch_kernel(moe_route_kernel, dim3(1), dim3(64 * kRouteTokens), s, p);
     if (e != hipSuccess) return e;
   } else if (p.T > 1) {

@@ -178,6 +178,6 @@ extern "C" int gemm_moe(int T, int E, int top, int H, int I, const void *X, int 
                      static_cast<const unsigned char *>(W1), mx ? ld1 : 2LL * ld1, S1, lds1,
                      static_cast<const unsigned char *>(W2), mx ? ld2 : 2LL * ld2, S2, lds2,
                      mx, renormalize != 0, Y, ldy, y_format, ids, gates,
-                     static_cast<unsigned char *>(workspace), at};
+                     static_cast<unsigned char *>(workspace), at, nullptr, nullptr};
   return launch_status(launch_moe(p, static_cast<hipStream_t>(stream)), "moe");
 }

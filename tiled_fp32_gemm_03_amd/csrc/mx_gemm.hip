@@ -6,6 +6,7 @@
 #include "mx_values.hpp"
 #include "addr_math.hpp"
 #include "addr_math16.hpp"
+#include "buffer_lds.hpp"
 #include "w16_tiles.hpp"
 
 
@@ -98,18 +99,6 @@ __global__ void __launch_bounds__(256) mx_direct_kernel(MxProblem p, int tiles_m
 // its last row, 20 of them its 9 steps (its stores are 32 bytes to a row and
 // instruction at 2-byte alignment, and these forms spill 3 to 5 registers).
 
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-constexpr int kOutside = (int)0x80000000u;  // an offset past every record count
-
-// 16 bytes per lane from rsrc[voff + soff] to LDS at lds_addr + 16 lane.
-// M0 holds the LDS destination: see ks_load_to_lds16 (w16_tiles.hpp).
-__device__ inline void mx_load_to_lds16(int voff, rsrc_t rsrc, int soff, unsigned lds_addr) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
-               :
-               : "v"(voff), "s"(rsrc), "s"(lds_addr), "s"(soff)
-               : "memory", "m0");
-}
-
 template <int WT_>
 struct MxTile {
   static constexpr int WT = WT_, BM = 2 * WT_, TB = WT_ / 16;
@@ -189,15 +178,15 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxProblem p, int tiles_m, 
       if constexpr (TAIL) v = W::KB * kk + (c0 ^ (4 * h)) < nb ? v : kOutside;
       const unsigned to = st + (q < W::DMA ? 0 : W::CODES) + (W::DMA * wave + i) * 1024;
       const int soff = 16 * W::KB * kk + (i >> 1) * (q < W::DMA ? a16 : b16);
-      mx_load_to_lds16(v, q < W::DMA ? a.codes : b.codes, soff, to);
+      buffer_load_to_lds16(v, q < W::DMA ? a.codes : b.codes, soff, to);
     }
   };
   auto issue_scales = [&](int buf, const MxSide &a, const MxSide &b, int kk)
       __attribute__((always_inline)) {
     if (W::SROWS == 4 || wave < W::SROWS) {
       const unsigned to = lds_u + 2 * W::STAGE + buf * 2 * W::SCALES + wave * 1024;
-      mx_load_to_lds16(vsa, a.scales, 8 * kk, to);
-      mx_load_to_lds16(vsb, b.scales, 8 * kk, to + W::SCALES);
+      buffer_load_to_lds16(vsa, a.scales, 8 * kk, to);
+      buffer_load_to_lds16(vsb, b.scales, 8 * kk, to + W::SCALES);
     }
   };
 

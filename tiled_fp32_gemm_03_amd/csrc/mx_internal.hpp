@@ -79,6 +79,9 @@ struct MoeProblem {
   float *gates;
   unsigned char *ws;
   MoeSpace at;
+  // A choice made before, [T top] each; else null: the router makes it.
+  const int *given_ids;
+  const float *given_gates;
 };
 hipError_t launch_moe(const MoeProblem &p, hipStream_t s);
 

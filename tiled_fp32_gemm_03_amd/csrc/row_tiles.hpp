@@ -1,0 +1,401 @@
+// Products of 16-bit matrices in tiles whose rows are chosen by a list (gfx950):
+// the experts' products and the adapters'.
+//
+// A tile of 2 WTM x 2 WTN over 4 waves (2 x 2), each with WTM / 16 x WTN / 16
+// blocks of v_mfma_f32_16x16x32, in 64-deep k steps and two LDS stages.  The waves
+// of one column half take the tile's blocks of 16 rows in turn, so that a tile
+// with few rows costs every wave the same, and blocks without rows are passed
+// over.  An operand lies in memory in one of two ways, and in LDS likewise:
+//   * k along its rows (KcSide): rows of 64 k, 8 chunks of 16 bytes, at m16_a_pos;
+//     a lane's operand is one 16-byte read;
+//   * k down its rows (KmSide): rows of W columns in 32-byte slots, at m16_b_slot;
+//     a lane's operand is two transposing reads (mixed16.hip).
+// Rows that are not there, columns past the width and k past the end are zeros.
+//
+// S says how operands come to LDS.  kDirect: by buffer loads straight into it; a
+// lane with nothing to load takes an offset past the buffer's record count.  Needs
+// 16-byte aligned rows, widths of whole 16 bytes and 32-bit offsets.  Else
+// through registers with 64-bit addresses: kByWords: rows that start in the middle
+// of a 4-byte word are read by the words around their values (Eight<kOdd>);
+// kAnyRows: anything.
+#pragma once
+
+#include "addr_math16.hpp"
+#include "buffer_lds.hpp"
+#include "mx_thin.hpp"
+#include "w16_tiles.hpp"
+
+namespace gemm_f32_impl {
+namespace {
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+enum { kDirect, kByWords, kAnyRows };
+constexpr int kStepK = 64;
+constexpr int kMostRecords = 0x7ffffff0;
+constexpr int kNever = 0x7fffffff;
+
+template <int WTM_, int WTN_>
+struct RowTile {
+  static constexpr int WTM = WTM_, WTN = WTN_, BM = 2 * WTM_, BN = 2 * WTN_;
+  static constexpr int TBM = WTM_ / 16, TBN = WTN_ / 16;
+  static constexpr int A_BYTES = BM * kStepK * 2, B_BYTES = BN * kStepK * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int A_LOADS = BM / 32, B_LOADS = BN / 32;  // per wave and step, 1 KB each
+  static_assert(2 * STAGE <= kLdsBytes, "two stages fit in LDS");
+};
+
+__device__ inline rsrc_t buffer_of(const void *p, long long bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<void *>(p), 0, (int)(bytes < kMostRecords ? bytes : kMostRecords), 0x00020000);
+}
+
+// 8 codes from element k of a row of `width` (zeros past it), on their way.
+template <int S>
+struct Chunk {
+  Eight<S == kByWords ? kOdd : kShort> x;
+  long long k;
+  int width;
+  __device__ __forceinline__ void load(const uint16_t *row, long long at, int w) {
+    k = at;
+    width = row ? w : 0;
+    if (width) x.load(reinterpret_cast<const unsigned char *>(row), at, w);
+  }
+  __device__ __forceinline__ u32x4 get() const {
+    if (width == 0) return u32x4{0, 0, 0, 0};
+    u32x4 v = x.get();
+    if (k + 8 > width) v = x.end(v, k, width);
+    return v;
+  }
+};
+
+// An operand with k along its rows, W rows of it.  `row(r)`: row r's first
+// element, or null.  K values to a row; from step `half` on (for rows of two
+// parts, each of whole steps and K values) the second part.
+template <int W, int S>
+struct KcSide {
+  static constexpr bool kDown = false;
+  static constexpr int kLoads = W / 32;
+  rsrc_t rsrc;
+  int voff[S == kDirect ? kLoads : 1];
+  const uint16_t *rows[S == kDirect ? 1 : kLoads];
+  Chunk<S == kDirect ? kAnyRows : S> held[S == kDirect ? 1 : kLoads];
+  int c0, K, half, step, left;
+
+  // `base`, `bytes`: what the rows lie in (kDirect).
+  template <class RowOf>
+  __device__ __forceinline__ void init(const void *base, long long bytes, RowOf row, int K_,
+                                       int half_, int wave, int lane) {
+    K = K_;
+    half = half_;
+    c0 = (lane & 7) ^ (lane >> 4);
+    if constexpr (S == kDirect) rsrc = buffer_of(base, bytes);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const uint16_t *r = row(8 * (kLoads * wave + q) + (lane >> 3));
+      if constexpr (S == kDirect)
+        voff[q] = r ? (int)(reinterpret_cast<const char *>(r) - static_cast<const char *>(base)) +
+                          16 * (c0 ^ (4 * (q & 1)))
+                    : kOutside;
+      else
+        rows[q] = r;
+    }
+  }
+  __device__ __forceinline__ void begin(int kk) {
+    step = kk;
+    left = K - kStepK * (kk >= half ? kk - half : kk);  // values from the step's first on
+  }
+  __device__ __forceinline__ void issue(int q, unsigned stage, int wave) {
+    const int v = 8 * (c0 ^ (4 * (q & 1))) < left ? voff[q] : kOutside;
+    buffer_load_to_lds16(v, rsrc, 2 * kStepK * step, stage + (kLoads * wave + q) * 1024);
+  }
+  __device__ __forceinline__ void load(int q) {
+    const uint16_t *r = rows[q];
+    if (r) r += (long long)kStepK * step - (K - left);
+    held[q].load(r, K - left + 8 * (c0 ^ (4 * (q & 1))), K);
+  }
+  __device__ __forceinline__ u32x4 get(int q) const { return held[q].get(); }
+};
+
+// An operand with k down its rows, `width` (at most W) columns of it: n rows from
+// `first` on, ld elements apart.  From step `half` on the second part: n rows
+// from `second` on.
+template <int W, int S>
+struct KmSide {
+  static constexpr bool kDown = true;
+  static constexpr int kLoads = W / 32, kChunks = W / 8;
+  rsrc_t rsrc;
+  int voff[S == kDirect ? kLoads : 1];
+  Chunk<S == kDirect ? kAnyRows : S> held[S == kDirect ? 1 : kLoads];
+  const uint16_t *first, *second, *at;
+  long long ld;
+  int n, half, width, left;
+
+  static __device__ __forceinline__ int row_of(int q, int wave, int lane) {
+    return (64 * (kLoads * wave + q) + lane) / kChunks;
+  }
+  static __device__ __forceinline__ int column_of(int q, int wave, int lane) {
+    const int pos = lane % kChunks;  // 64 is a multiple of kChunks
+    return 8 * (2 * m16_b_slot(row_of(q, wave, lane), pos >> 1) + (pos & 1));
+  }
+  __device__ __forceinline__ void init(const uint16_t *first_, const uint16_t *second_,
+                                       long long ld_, int n_, int half_, int width_, int wave,
+                                       int lane) {
+    first = first_;
+    second = second_;
+    ld = ld_;
+    n = n_;
+    half = half_;
+    width = width_;
+    if constexpr (S == kDirect)
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) {
+        const int c = column_of(q, wave, lane);
+        voff[q] = c < width ? (int)(2 * (row_of(q, wave, lane) * ld + c)) : kOutside;
+      }
+  }
+  __device__ __forceinline__ void begin(int kk) {
+    const int k0 = kStepK * (kk >= half ? kk - half : kk);
+    left = n - k0;
+    at = (kk >= half ? second : first) + k0 * ld;
+    if constexpr (S == kDirect)  // rows past the end are past the record count
+      rsrc = buffer_of(at, left > 0 ? 2 * ((left - 1) * ld + width) : 0);
+  }
+  __device__ __forceinline__ void issue(int q, unsigned stage, int wave) {
+    buffer_load_to_lds16(voff[q], rsrc, 0, stage + (kLoads * wave + q) * 1024);
+  }
+  __device__ __forceinline__ void load(int q, int wave, int lane) {
+    const int r = row_of(q, wave, lane), c = column_of(q, wave, lane);
+    held[q].load(r < left && c < width ? at + r * ld : nullptr, c, width);
+  }
+  __device__ __forceinline__ u32x4 get(int q) const { return held[q].get(); }
+};
+
+// The same with its rows chosen by a list: row k is row list[k] of `base`.  The list
+// is read a step ahead.
+template <int W, int S>
+struct KmListSide {
+  static constexpr bool kDown = true;
+  static constexpr int kLoads = W / 32, kChunks = W / 8;
+  rsrc_t rsrc;
+  Chunk<S == kDirect ? kAnyRows : S> held[S == kDirect ? 1 : kLoads];
+  const uint16_t *base;
+  const int *list;
+  long long ld;
+  int n, last, width, k0;
+  int now[kLoads], next[kLoads];
+
+  __device__ __forceinline__ void fetch(int kk, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int k = kStepK * kk + KmSide<W, S>::row_of(q, wave, lane);
+      now[q] = next[q];
+      next[q] = list[k < n ? k : last];
+    }
+  }
+  // `list` has a readable place if n is 0.
+  __device__ __forceinline__ void init(const uint16_t *base_, long long bytes, long long ld_,
+                                       const int *list_, int n_, int width_, int wave, int lane) {
+    base = base_;
+    ld = ld_;
+    list = list_;
+    n = n_;
+    last = n > 0 ? n - 1 : 0;
+    width = width_;
+    if constexpr (S == kDirect) rsrc = buffer_of(base_, bytes);
+    fetch(0, wave, lane);
+  }
+  __device__ __forceinline__ void begin(int kk, int wave, int lane) {
+    k0 = kStepK * kk;
+    fetch(kk + 1, wave, lane);
+  }
+  __device__ __forceinline__ void issue(int q, unsigned stage, int wave, int lane) {
+    const int c = KmSide<W, S>::column_of(q, wave, lane);
+    const bool in = k0 + KmSide<W, S>::row_of(q, wave, lane) < n && c < width;
+    buffer_load_to_lds16(in ? (int)(2 * (now[q] * ld + c)) : kOutside, rsrc, 0,
+                         stage + (kLoads * wave + q) * 1024);
+  }
+  __device__ __forceinline__ void load(int q, int wave, int lane) {
+    const int c = KmSide<W, S>::column_of(q, wave, lane);
+    const bool in = k0 + KmSide<W, S>::row_of(q, wave, lane) < n && c < width;
+    held[q].load(in ? base + now[q] * ld : nullptr, c, width);
+  }
+  __device__ __forceinline__ u32x4 get(int q) const { return held[q].get(); }
+};
+
+// One set of calls for all sides.
+template <int W, int S>
+__device__ __forceinline__ void side_begin(KcSide<W, S> &x, int kk, int, int) { x.begin(kk); }
+template <int W, int S>
+__device__ __forceinline__ void side_begin(KmSide<W, S> &x, int kk, int, int) { x.begin(kk); }
+template <int W, int S>
+__device__ __forceinline__ void side_begin(KmListSide<W, S> &x, int kk, int wave, int lane) {
+  x.begin(kk, wave, lane);
+}
+template <int W, int S>
+__device__ __forceinline__ void side_issue(KcSide<W, S> &x, int q, unsigned stage, int wave, int) {
+  x.issue(q, stage, wave);
+}
+template <int W, int S>
+__device__ __forceinline__ void side_issue(KmSide<W, S> &x, int q, unsigned stage, int wave, int) {
+  x.issue(q, stage, wave);
+}
+template <int W, int S>
+__device__ __forceinline__ void side_issue(KmListSide<W, S> &x, int q, unsigned stage, int wave,
+                                           int lane) {
+  x.issue(q, stage, wave, lane);
+}
+template <int W, int S>
+__device__ __forceinline__ void side_load(KcSide<W, S> &x, int q, int, int) { x.load(q); }
+template <int W, int S>
+__device__ __forceinline__ void side_load(KmSide<W, S> &x, int q, int wave, int lane) {
+  x.load(q, wave, lane);
+}
+template <int W, int S>
+__device__ __forceinline__ void side_load(KmListSide<W, S> &x, int q, int wave, int lane) {
+  x.load(q, wave, lane);
+}
+
+// A lane's operand: block `block` of 16 rows (columns), 32-deep group kg.
+template <bool DOWN, int W>
+__device__ __forceinline__ i16x8 read_operand(const char *st, int block, int kg, int lane) {
+  const int l16 = lane & 15, g = lane >> 4;
+  if constexpr (!DOWN) {
+    return *reinterpret_cast<const i16x8 *>(st + 16 * m16_a_pos(16 * block + l16, 4 * kg + g));
+  } else {
+    i16x4 h[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = 32 * kg + 8 * g + 4 * i + (l16 >> 2);
+      const char *at = st + k * (W * 2) + 32 * m16_b_slot(k, block) + 8 * (l16 & 3);
+      h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(at));
+    }
+    return i16x8{h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
+  }
+}
+
+template <int FMT>
+__device__ inline f32x4 mfma_rows(i16x8 b, i16x8 a, f32x4 acc) {
+  if constexpr (FMT == kBf16)
+    return mfma_bf16(__builtin_bit_cast(u32x4, b), __builtin_bit_cast(u32x4, a), acc);
+  else
+    return mfma_f16(__builtin_bit_cast(u32x4, b), __builtin_bit_cast(u32x4, a), acc);
+}
+
+// The products of nk steps onto zero; `blocks` of this wave's blocks of rows have
+// any.  acc[i][j]: lane l has row l % 16 of the wave's row block i (block 2 i +
+// wave / 2 of the tile) and columns 4 (l / 16) .. + 3 of its column block j (block
+// TBN (wave % 2) + j).  On return the LDS may still be read by other waves.
+template <class T, int FMT, int S, class A, class B>
+__device__ __forceinline__ void tile_product(char *lds, A &a, B &b, int nk, int blocks, int wave,
+                                             int lane, f32x4 (&acc)[T::TBM][T::TBN]) {
+  const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t *)lds;
+  const int wm = wave >> 1, wn = wave & 1;
+#pragma unroll
+  for (int i = 0; i < T::TBM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TBN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (nk <= 0) return;  // uniform
+  constexpr int kLoads = T::A_LOADS + T::B_LOADS;
+
+  auto issue = [&](unsigned stage, int q0, int q1) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      if (q < q0 || q >= q1) continue;
+      if (q < T::A_LOADS) side_issue(a, q, stage, wave, lane);
+      else side_issue(b, q - T::A_LOADS, stage + T::A_BYTES, wave, lane);
+    }
+  };
+  auto load = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < T::A_LOADS; ++q) side_load(a, q, wave, lane);
+#pragma unroll
+    for (int q = 0; q < T::B_LOADS; ++q) side_load(b, q, wave, lane);
+  };
+  auto put = [&](char *stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < T::A_LOADS; ++q)
+      *reinterpret_cast<u32x4 *>(stage + 16 * (64 * (T::A_LOADS * wave + q) + lane)) = a.get(q);
+#pragma unroll
+    for (int q = 0; q < T::B_LOADS; ++q)
+      *reinterpret_cast<u32x4 *>(stage + T::A_BYTES + 16 * (64 * (T::B_LOADS * wave + q) + lane)) =
+          b.get(q);
+  };
+
+  side_begin(a, 0, wave, lane);
+  side_begin(b, 0, wave, lane);
+  if constexpr (S == kDirect) {
+    issue(lds_u, 0, kLoads);
+  } else {
+    load();
+    put(lds);
+  }
+  int stage = 0;
+#pragma unroll 1
+  for (int kk = 0; kk < nk; ++kk) {
+    const bool more = kk + 1 < nk;
+    if constexpr (S == kDirect) __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(0));  // own loads
+    ks_lds_barrier();  // everyone's; the other stage is free
+    const char *st = lds + stage * T::STAGE;
+    const unsigned nst = lds_u + (stage ^ 1) * T::STAGE;
+    if (more) {
+      side_begin(a, kk + 1, wave, lane);
+      side_begin(b, kk + 1, wave, lane);
+      if constexpr (S != kDirect) load();
+    }
+    i16x8 fa[2][T::TBM], fb[2][T::TBN];
+    auto read = [&](int kg) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < T::TBN; ++j)
+        fb[kg & 1][j] = read_operand<B::kDown, T::BN>(st + T::A_BYTES, wn * T::TBN + j, kg, lane);
+#pragma unroll
+      for (int i = 0; i < T::TBM; ++i)
+        fa[kg & 1][i] = read_operand<A::kDown, T::BM>(st, 2 * i + wm, kg, lane);
+    };
+    read(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kg = 0; kg < kStepK / 32; ++kg) {
+#pragma unroll
+      for (int i = 0; i < T::TBM; ++i) {
+        if (i < blocks) {  // uniform
+#pragma unroll
+          for (int j = 0; j < T::TBN; ++j)
+            acc[i][j] = mfma_rows<FMT>(fb[kg & 1][j], fa[kg & 1][i], acc[i][j]);
+        }
+        constexpr int kPerRow = 2;
+        const int row = kg * T::TBM + i;
+        if (S == kDirect && row * kPerRow < kLoads) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (more) issue(nst, row * kPerRow, (row + 1) * kPerRow);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (kg + 1 < kStepK / 32 && i == T::TBM / 2 - 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          read(kg + 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+    stage ^= 1;
+    if constexpr (S != kDirect)
+      if (more) put(lds + stage * T::STAGE);
+    if constexpr (T::TBM * T::TBN == 64) {  // accumulation registers (see big16_kernel)
+#pragma unroll
+      for (int i = 0; i < T::TBM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TBN; ++j) asm volatile("" : "+a"(acc[i][j]));
+    }
+  }
+}
+
+// How many of a wave's row blocks have any of n rows.
+__device__ inline int blocks_of(int n, int wm) {
+  const int b = (n + 15) >> 4;
+  return (b - wm + 1) >> 1;
+}
+
+}  // namespace
+}  // namespace gemm_f32_impl
