@@ -15,6 +15,7 @@ namespace {
 // kOneGroup pairs by one workgroup; more in three launches, kListPairs to a
 // workgroup.  Pairs whose expert is not in 0 .. E - 1 get no place.
 
+constexpr int kMostGroups = 1 << 20;
 constexpr int kOneGroup = 8192, kOneThreads = 1024, kListThreads = 256;
 
 __device__ inline int expert_of(const ExpertsProblem &p, long long pair, long long pairs) {

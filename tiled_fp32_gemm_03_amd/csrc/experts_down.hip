@@ -10,79 +10,114 @@ namespace gemm_f32_impl {
 namespace {
 
 template <class T, int FMT, bool GATES>
-__device__ __forceinline__ void store_part(const ExpertsProblem &p, const Rows &r, int h0,
+__device__ __forceinline__ void store_part(const ExpertsProblem &p, const RowJob &j,
                                            const f32x4 (&acc)[T::TBM][T::TBN], int wave, int lane) {
-  const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15, g = lane >> 4;
-  const int *list = ws_at<int>(p, p.at.list);
+  const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15;
+  const int *list = ws_at<int>(p, p.at.list) + j.first;
 #pragma unroll
   for (int i = 0; i < T::TBM; ++i) {
     const int row = 16 * (2 * i + wm) + l16;
-    if (row >= r.n) continue;
-    const long long pair = list[r.first + row];
+    if (16 * (2 * i + wm) >= j.rows) continue;  // uniform
+    const bool in = row < j.rows;
+    const long long pair = list[in ? row : 0];
     const float gate = GATES ? p.gates[pair] : 1.f;
+    uint16_t *part = ws_at<uint16_t>(p, p.at.part) + pair * p.at.hpitch;
 #pragma unroll
-    for (int j = 0; j < T::TBN; ++j) {
-      const int h = h0 + 16 * (wn * T::TBN + j) + 4 * g;
-      if (h >= p.H) continue;
-      const f32x4 v = GATES ? acc[i][j] * gate : acc[i][j];
-      *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.part) + pair * p.at.hpitch + h) =
-          u32x2{pack2<FMT>(v[0], v[1]), pack2<FMT>(v[2], v[3])};
+    for (int m = 0; m < T::TBN; m += 2) {
+      const int h = T::BN * j.tn + 16 * (wn * T::TBN + m);
+      const Eights e = GATES ? eights<FMT>(acc[i][m] * gate, acc[i][m + 1] * gate, lane)
+                             : eights<FMT>(acc[i][m], acc[i][m + 1], lane);
+      if (in && h + e.at < p.H) *reinterpret_cast<u32x4 *>(part + h + e.at) = e.v;
     }
   }
 }
 
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_down_kernel(ExpertsProblem p) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  each_row_tile(p, (int)ceil_div(p.H, T::BN), [&](int tm, int tn) __attribute__((always_inline)) {
-    const Rows r = row_tile(p, tm);
-    const uint16_t *u = ws_at<uint16_t>(p, p.at.u) + r.first * p.at.ipitch;
-    const uint16_t *w = p.W2 + (long long)p.H * r.e * p.ld2;
-    const int h0 = T::BN * tn;
-    KcSide<T::BM, S> a;
-    a.init(u, 2 * r.n * p.at.ipitch,
-           [&](int i) __attribute__((always_inline)) {
-             return i < r.n ? u + i * p.at.ipitch : nullptr;
+struct Down {
+  typedef RowJob Job;
+  typedef KcSide<T::BM, S> A;
+  typedef KcSide<T::BN, S> B;
+  const ExpertsProblem &p;
+  const Share share;
+  const int rows, columns, wave, lane;
+  A a;
+  B b;
+
+  __device__ Job job(int t) const {
+    return row_job(p, share.tile(t), rows, columns, (int)ceil_div(p.I, kStepK));
+  }
+  __device__ __forceinline__ void fetch(const Job &) {}
+  __device__ __forceinline__ void begin(const Job &j) {
+    const uint16_t *u = ws_at<uint16_t>(p, p.at.u) + j.first * p.at.ipitch;
+    a.init(u, 2 * j.rows * p.at.ipitch,
+           [&](int i, int) __attribute__((always_inline)) {
+             return i < j.rows ? u + i * p.at.ipitch : nullptr;
            },
            p.I, kNever, wave, lane);
-    KcSide<T::BN, S> b;
+    const uint16_t *w = p.W2 + (long long)p.H * j.e * p.ld2;
     b.init(w, 2 * ((p.H - 1LL) * p.ld2 + p.I),
-           [&](int j) __attribute__((always_inline)) {
-             return h0 + j < p.H ? w + (h0 + j) * p.ld2 : nullptr;
+           [&](int c, int) __attribute__((always_inline)) {
+             const int h = T::BN * j.tn + c;
+             return h < p.H ? w + h * p.ld2 : nullptr;
            },
            p.I, kNever, wave, lane);
-    f32x4 acc[T::TBM][T::TBN];
-    tile_product<T, FMT, S>(lds, a, b, (int)ceil_div(p.I, kStepK), blocks_of(r.n, wave >> 1), wave,
-                            lane, acc);
-    store_part<T, FMT, true>(p, r, h0, acc, wave, lane);
-  });
-}
+  }
+  __device__ __forceinline__ void store(const Job &j, const f32x4 (&acc)[T::TBM][T::TBN], int wave,
+                                        int lane) const {
+    store_part<T, FMT, true>(p, j, acc, wave, lane);
+  }
+};
 
 // dh's rows are two parts of ipitch values, the gate's and the other factor's; so
 // are W1's rows, I of each.
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_dx_kernel(ExpertsProblem p) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  each_row_tile(p, (int)ceil_div(p.H, T::BN), [&](int tm, int tn) __attribute__((always_inline)) {
-    const Rows r = row_tile(p, tm);
+struct Dx {
+  typedef RowJob Job;
+  typedef KcSide<T::BM, S> A;
+  typedef KmSide<T::BN, S> B;
+  const ExpertsProblem &p;
+  const Share share;
+  const int rows, columns, wave, lane;
+  A a;
+  B b;
+
+  __device__ Job job(int t) const {
+    return row_job(p, share.tile(t), rows, columns, (int)(2 * p.at.ipitch / kStepK));
+  }
+  __device__ __forceinline__ void fetch(const Job &) {}
+  __device__ __forceinline__ void begin(const Job &j) {
     const long long pitch = 2 * p.at.ipitch;
-    const int half = (int)(p.at.ipitch / kStepK), h0 = T::BN * tn;
-    const uint16_t *dh = ws_at<uint16_t>(p, p.at.dh) + r.first * pitch;
-    const uint16_t *w = p.W1 + 2LL * p.I * r.e * p.ld1 + h0;
-    KcSide<T::BM, S> a;
-    a.init(dh, 2 * r.n * pitch,
-           [&](int i) __attribute__((always_inline)) {
-             return i < r.n ? dh + i * pitch : nullptr;
+    const int half = (int)(p.at.ipitch / kStepK), h0 = T::BN * j.tn;
+    const uint16_t *dh = ws_at<uint16_t>(p, p.at.dh) + j.first * pitch;
+    a.init(dh, 2 * j.rows * pitch,
+           [&](int i, int) __attribute__((always_inline)) {
+             return i < j.rows ? dh + i * pitch : nullptr;
            },
            p.I, half, wave, lane);
-    KmSide<T::BN, S> b;
+    const uint16_t *w = p.W1 + 2LL * p.I * j.e * p.ld1 + h0;
     b.init(w, w + p.I * p.ld1, p.ld1, p.I, half, p.H - h0 < T::BN ? p.H - h0 : T::BN, wave, lane);
-    f32x4 acc[T::TBM][T::TBN];
-    tile_product<T, FMT, S>(lds, a, b, 2 * half, blocks_of(r.n, wave >> 1), wave, lane, acc);
-    store_part<T, FMT, false>(p, r, h0, acc, wave, lane);
-  });
+  }
+  __device__ __forceinline__ void store(const Job &j, const f32x4 (&acc)[T::TBM][T::TBN], int wave,
+                                        int lane) const {
+    store_part<T, FMT, false>(p, j, acc, wave, lane);
+  }
+};
+
+template <class T, int FMT, int S, template <class, int, int> class Op>
+__device__ __forceinline__ void part_tiles(const ExpertsProblem &p) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int rows = row_tiles(p), columns = (int)ceil_div(p.H, T::BN);
+  Op<T, FMT, S> op{p, Share(rows * columns), rows, columns, wave, lane, {}, {}};
+  tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
+}
+template <class T, int FMT, int S>
+__global__ void __launch_bounds__(256, kPerSimd<T>) experts_down_kernel(ExpertsProblem p) {
+  part_tiles<T, FMT, S, Down>(p);
+}
+template <class T, int FMT, int S>
+__global__ void __launch_bounds__(256, kPerSimd<T>) experts_dx_kernel(ExpertsProblem p) {
+  part_tiles<T, FMT, S, Dx>(p);
 }
 
 }  // namespace
@@ -93,8 +128,7 @@ hipError_t launch_experts_down(const ExpertsProblem &p, hipStream_t s) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
     const long long tiles = p.at.most_tiles * ceil_div(p.H, T::BN);
-    return p.format == kBf16 ? launch_tiles(experts_down_kernel<T, kBf16, S>, p, tiles, s)
-                             : launch_tiles(experts_down_kernel<T, kF16, S>, p, tiles, s);
+    return GEMM_F32_LAUNCH_ROWS(experts_down_kernel, T, S, tiles);
   });
 }
 
@@ -104,8 +138,7 @@ hipError_t launch_experts_dx(const ExpertsProblem &p, hipStream_t s) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
     const long long tiles = p.at.most_tiles * ceil_div(p.H, T::BN);
-    return p.format == kBf16 ? launch_tiles(experts_dx_kernel<T, kBf16, S>, p, tiles, s)
-                             : launch_tiles(experts_dx_kernel<T, kF16, S>, p, tiles, s);
+    return GEMM_F32_LAUNCH_ROWS(experts_dx_kernel, T, S, tiles);
   });
 }
 

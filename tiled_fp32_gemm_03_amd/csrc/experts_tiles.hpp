@@ -23,19 +23,47 @@ __device__ inline Rows row_tile(const ExpertsProblem &p, int tm) {
           __builtin_amdgcn_readfirstlane(t[2])};
 }
 
-// Calls run(tm, tn) for each of this workgroup's tiles of rows x columns.
-template <class Run>
-__device__ __forceinline__ void each_row_tile(const ExpertsProblem &p, int columns, Run run) {
-  const int rows = __builtin_amdgcn_readfirstlane(*ws_at<int>(p, p.at.tiles));
-  const int total = rows * columns;
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    int tm, tn;
-    tile_coords(xcd_remap(t, total), rows, columns, tm, tn);
-    // (divisions: the compiler forms them in vector registers)
-    run(__builtin_amdgcn_readfirstlane(tm), __builtin_amdgcn_readfirstlane(tn));
-    if (t + (int)gridDim.x < total) ks_lds_barrier();  // the next tile's loads overwrite the LDS
+// A workgroup's share of the tiles: t of `count`, those of one round next to one another
+// and each XCD's too.
+struct Share {
+  int first, step, count;
+  __device__ explicit Share(int total) {
+    const int G = gridDim.x;
+    first = xcd_remap(blockIdx.x, G);
+    step = G;
+    count = __builtin_amdgcn_readfirstlane(first < total ? (total - first + G - 1) / G : 0);
   }
+  __device__ int tile(int t) const { return first + t * step; }
+};
+
+// A product of one expert's rows: tile (tm, tn) of row tiles and columns.
+struct RowJob {
+  int steps, rows;
+  int e, first, tn;
+};
+__device__ inline int row_tiles(const ExpertsProblem &p) {
+  return __builtin_amdgcn_readfirstlane(*ws_at<int>(p, p.at.tiles));
 }
+__device__ inline RowJob row_job(const ExpertsProblem &p, int tile, int rows, int columns, int steps) {
+  int tm, tn;
+  tile_coords(tile, rows, columns, tm, tn);
+  // (divisions: the compiler forms them in vector registers)
+  const Rows r = row_tile(p, __builtin_amdgcn_readfirstlane(tm));
+  return {steps, r.n, r.e, r.first, __builtin_amdgcn_readfirstlane(tn)};
+}
+
+// The tokens of a side's rows, on their way: one to each of a lane's loads.
+template <class Side>
+struct TokenRows {
+  int at[Side::kLoads];
+  __device__ __forceinline__ void fetch(const int *token, int n, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < Side::kLoads; ++q) {
+      const int r = Side::row_of(q, wave, lane);
+      at[q] = token[r < n ? r : n - 1];
+    }
+  }
+};
 
 // Whether a matrix's rows can be loaded directly: 16-byte aligned, of whole 16
 // bytes, and `rows` of them within 32-bit offsets.
@@ -48,13 +76,17 @@ inline bool by_words(const void *p, long long width) {
   return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && width >= 8;
 }
 
-constexpr int kMostGroups = 1 << 20;
-template <class Kernel>
-hipError_t launch_tiles(Kernel kern, const ExpertsProblem &p, long long tiles, hipStream_t s) {
+// KERN on at most `tiles` tiles: as many workgroups as the chip holds at once.
+template <auto KERN>
+hipError_t launch_tiles(const ExpertsProblem &p, long long tiles, hipStream_t s) {
   if (tiles <= 0) return hipSuccess;
-  const unsigned grid = (unsigned)(tiles < kMostGroups ? tiles : kMostGroups);
-  return launch_kernel(kern, dim3(grid), dim3(256), s, p);
+  const long long most = resident_workgroups<KERN, 256>();
+  return launch_kernel(KERN, dim3((unsigned)(tiles < most ? tiles : most)), dim3(256), s, p);
 }
+// KERN<T, format, S, ...> in the call's format.
+#define GEMM_F32_LAUNCH_ROWS(KERN, T, S, ...)                                         \
+  (p.format == kBf16 ? launch_tiles<KERN<T, kBf16, S>>(p, __VA_ARGS__, s)               \
+                     : launch_tiles<KERN<T, kF16, S>>(p, __VA_ARGS__, s))
 
 typedef RowTile<128, 128> Large;
 typedef RowTile<64, 64> Small;

@@ -11,57 +11,89 @@ namespace {
 // of the size of the result's own.  SAVE keeps both factors' sums in fp32, for the
 // backward pass.
 template <class T, int FMT, int S, bool SAVE>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_up_kernel(ExpertsProblem p) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15, g = lane >> 4;
-  constexpr int kU = T::BN / 2;
-  const int *token = ws_at<int>(p, p.at.token);
-  each_row_tile(p, (int)ceil_div(p.I, kU), [&](int tm, int tn) __attribute__((always_inline)) {
-    const Rows r = row_tile(p, tm);
-    const uint16_t *w = p.W1 + 2LL * p.I * r.e * p.ld1;
-    const int i0 = kU * tn;
-    KcSide<T::BM, S> a;
+struct Up {
+  typedef RowJob Job;
+  typedef KcSide<T::BM, S> A;
+  typedef KcSide<T::BN, S> B;
+  static constexpr int kU = T::BN / 2;
+  const ExpertsProblem &p;
+  const Share share;
+  const int rows, columns, wave, lane;
+  A a;
+  B b;
+  TokenRows<A> token;
+
+  __device__ Job job(int t) const {
+    return row_job(p, share.tile(t), rows, columns, (int)ceil_div(p.H, kStepK));
+  }
+  __device__ __forceinline__ void fetch(const Job &j) {
+    token.fetch(ws_at<int>(p, p.at.token) + j.first, j.rows, wave, lane);
+  }
+  __device__ __forceinline__ void begin(const Job &j) {
     a.init(p.X, 2 * ((p.T - 1) * p.ldx + p.H),
-           [&](int i) __attribute__((always_inline)) {
-             return i < r.n ? p.X + token[r.first + i] * p.ldx : nullptr;
+           [&](int i, int q) __attribute__((always_inline)) {
+             return i < j.rows ? p.X + token.at[q] * p.ldx : nullptr;
            },
            p.H, kNever, wave, lane);
-    KcSide<T::BN, S> b;
+    const uint16_t *w = p.W1 + 2LL * p.I * j.e * p.ld1;
     b.init(w, 2 * ((2LL * p.I - 1) * p.ld1 + p.H),
-           [&](int j) __attribute__((always_inline)) {
-             const int i = i0 + 16 * (j >> 5) + (j & 15);
-             return i < p.I ? w + ((j & 16) ? p.I + i : i) * p.ld1 : nullptr;
+           [&](int c, int) __attribute__((always_inline)) {
+             const int i = kU * j.tn + 16 * (c >> 5) + (c & 15);
+             return i < p.I ? w + ((c & 16) ? p.I + i : i) * p.ld1 : nullptr;
            },
            p.H, kNever, wave, lane);
-    f32x4 acc[T::TBM][T::TBN];
-    const int blocks = blocks_of(r.n, wm);
-    tile_product<T, FMT, S>(lds, a, b, (int)ceil_div(p.H, kStepK), blocks, wave, lane, acc);
+  }
+  __device__ __forceinline__ void store(const Job &j, const f32x4 (&acc)[T::TBM][T::TBN], int wave,
+                                        int lane) const {
+    const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int i = 0; i < T::TBM; ++i) {
       const int row = 16 * (2 * i + wm) + l16;
-      if (row >= r.n) continue;
-      const long long place = r.first + row;
+      if (16 * (2 * i + wm) >= j.rows) continue;  // uniform
+      const bool in = row < j.rows;
+      const long long place = j.first + row;
 #pragma unroll
-      for (int q = 0; q < T::TBN / 2; ++q) {
-        const int at = i0 + 16 * (wn * T::TBN / 2 + q) + 4 * g, left = p.I - at;
-        if (at >= p.at.ipitch) continue;
-        const f32x4 x = acc[i][2 * q], y = acc[i][2 * q + 1];
-        f32x4 u;
+      for (int q = 0; q < T::TBN / 2; q += 2) {
+        const int at = kU * j.tn + 16 * (wn * T::TBN / 2 + q);
+        f32x4 u[2];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)  // zeros from I to the pitch
-          u[c] = c < left ? x[c] / (1.f + expf(-x[c])) * y[c] : 0.f;
-        *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.u) + place * p.at.ipitch + at) =
-            u32x2{pack2<FMT>(u[0], u[1]), pack2<FMT>(u[2], u[3])};
-        if constexpr (SAVE) {
-          if (left > 0) {
-            store4<kF32>(p.saved, place * 2 * p.I + at, left, x);
-            store4<kF32>(p.saved, place * 2 * p.I + p.I + at, left, y);
+        for (int h = 0; h < 2; ++h) {
+          const int c0 = at + 16 * h + 4 * g, left = p.I - c0;
+          const f32x4 x = acc[i][2 * (q + h)], y = acc[i][2 * (q + h) + 1];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)  // zeros from I to the pitch
+            u[h][c] = c < left ? x[c] / (1.f + expf(-x[c])) * y[c] : 0.f;
+          if constexpr (SAVE) {
+            if (in && left > 0) {
+              store4<kF32>(p.saved, place * 2 * p.I + c0, left, x);
+              store4<kF32>(p.saved, place * 2 * p.I + p.I + c0, left, y);
+            }
           }
         }
+        const Eights e = eights<FMT>(u[0], u[1], lane);
+        if (in && at < p.at.ipitch)  // whole 64s
+          *reinterpret_cast<u32x4 *>(ws_at<uint16_t>(p, p.at.u) + place * p.at.ipitch + at + e.at) =
+              e.v;
       }
     }
-  });
+  }
+};
+
+template <class T, int FMT, int S, bool SAVE>
+__device__ __forceinline__ void up_tiles(const ExpertsProblem &p) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int rows = row_tiles(p), columns = (int)ceil_div(p.I, T::BN / 2);
+  Up<T, FMT, S, SAVE> op{p, Share(rows * columns), rows, columns, wave, lane, {}, {}, {}};
+  tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
+}
+template <class T, int FMT, int S>
+__global__ void __launch_bounds__(256, kPerSimd<T>) experts_up_kernel(ExpertsProblem p) {
+  up_tiles<T, FMT, S, false>(p);
+}
+template <class T, int FMT, int S>
+__global__ void __launch_bounds__(256, kPerSimd<T>) experts_up_save_kernel(ExpertsProblem p) {
+  up_tiles<T, FMT, S, true>(p);
 }
 
 }  // namespace
@@ -73,11 +105,8 @@ hipError_t launch_experts_up(const ExpertsProblem &p, hipStream_t s) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
     const long long tiles = p.at.most_tiles * ceil_div(p.I, T::BN / 2);
-    if (p.saved)
-      return p.format == kBf16 ? launch_tiles(experts_up_kernel<T, kBf16, S, true>, p, tiles, s)
-                               : launch_tiles(experts_up_kernel<T, kF16, S, true>, p, tiles, s);
-    return p.format == kBf16 ? launch_tiles(experts_up_kernel<T, kBf16, S, false>, p, tiles, s)
-                             : launch_tiles(experts_up_kernel<T, kF16, S, false>, p, tiles, s);
+    return p.saved ? GEMM_F32_LAUNCH_ROWS(experts_up_save_kernel, T, S, tiles)
+                   : GEMM_F32_LAUNCH_ROWS(experts_up_kernel, T, S, tiles);
   });
 }
 

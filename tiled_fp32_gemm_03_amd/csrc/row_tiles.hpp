@@ -47,9 +47,20 @@ struct RowTile {
   static_assert(2 * STAGE <= kLdsBytes, "two stages fit in LDS");
 };
 
-__device__ inline rsrc_t buffer_of(const void *p, long long bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<void *>(p), 0, (int)(bytes < kMostRecords ? bytes : kMostRecords), 0x00020000);
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline const void *uniform(const void *p) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return reinterpret_cast<const void *>((uintptr_t)(uint32_t)uniform((int)(a >> 32)) << 32 |
+                                        (uint32_t)uniform((int)a));
+}
+// (Made again for each step: the compiler may carry what all lanes share in vector
+// registers from one to the next.)
+__device__ inline int records_of(long long bytes) {
+  return (int)(bytes < kMostRecords ? bytes : kMostRecords);
+}
+__device__ inline rsrc_t buffer_of(const void *p, int records) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(uniform(p)), 0, uniform(records),
+                                           0x00020000);
 }
 
 // 8 codes from element k of a row of `width` (zeros past it), on their way.
@@ -71,30 +82,36 @@ struct Chunk {
   }
 };
 
-// An operand with k along its rows, W rows of it.  `row(r)`: row r's first
-// element, or null.  K values to a row; from step `half` on (for rows of two
+// An operand with k along its rows, W rows of it.  `row(r, q)`: row r's first element,
+// or null; q, the number of the load that brings it, row_of its r.  K values to a row; from step `half` on (for rows of two
 // parts, each of whole steps and K values) the second part.
 template <int W, int S>
 struct KcSide {
   static constexpr bool kDown = false;
   static constexpr int kLoads = W / 32;
+  const void *base;
+  int records;
   rsrc_t rsrc;
   int voff[S == kDirect ? kLoads : 1];
   const uint16_t *rows[S == kDirect ? 1 : kLoads];
   Chunk<S == kDirect ? kAnyRows : S> held[S == kDirect ? 1 : kLoads];
   int c0, K, half, step, left;
 
+  static __device__ __forceinline__ int row_of(int q, int wave, int lane) {
+    return 8 * (kLoads * wave + q) + (lane >> 3);
+  }
   // `base`, `bytes`: what the rows lie in (kDirect).
   template <class RowOf>
-  __device__ __forceinline__ void init(const void *base, long long bytes, RowOf row, int K_,
+  __device__ __forceinline__ void init(const void *base_, long long bytes, RowOf row, int K_,
                                        int half_, int wave, int lane) {
     K = K_;
     half = half_;
     c0 = (lane & 7) ^ (lane >> 4);
-    if constexpr (S == kDirect) rsrc = buffer_of(base, bytes);
+    base = base_;
+    records = records_of(bytes);
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
-      const uint16_t *r = row(8 * (kLoads * wave + q) + (lane >> 3));
+      const uint16_t *r = row(row_of(q, wave, lane), q);
       if constexpr (S == kDirect)
         voff[q] = r ? (int)(reinterpret_cast<const char *>(r) - static_cast<const char *>(base)) +
                           16 * (c0 ^ (4 * (q & 1)))
@@ -106,10 +123,11 @@ struct KcSide {
   __device__ __forceinline__ void begin(int kk) {
     step = kk;
     left = K - kStepK * (kk >= half ? kk - half : kk);  // values from the step's first on
+    if constexpr (S == kDirect) rsrc = buffer_of(base, records);
   }
   __device__ __forceinline__ void issue(int q, unsigned stage, int wave) {
     const int v = 8 * (c0 ^ (4 * (q & 1))) < left ? voff[q] : kOutside;
-    buffer_load_to_lds16(v, rsrc, 2 * kStepK * step, stage + (kLoads * wave + q) * 1024);
+    buffer_load_to_lds16(v, rsrc, uniform(2 * kStepK * step), (unsigned)uniform((int)(stage + (kLoads * wave + q) * 1024)));
   }
   __device__ __forceinline__ void load(int q) {
     const uint16_t *r = rows[q];
@@ -161,10 +179,10 @@ struct KmSide {
     left = n - k0;
     at = (kk >= half ? second : first) + k0 * ld;
     if constexpr (S == kDirect)  // rows past the end are past the record count
-      rsrc = buffer_of(at, left > 0 ? 2 * ((left - 1) * ld + width) : 0);
+      rsrc = buffer_of(at, left > 0 ? records_of(2 * ((left - 1) * ld + width)) : 0);
   }
   __device__ __forceinline__ void issue(int q, unsigned stage, int wave) {
-    buffer_load_to_lds16(voff[q], rsrc, 0, stage + (kLoads * wave + q) * 1024);
+    buffer_load_to_lds16(voff[q], rsrc, 0, (unsigned)uniform((int)(stage + (kLoads * wave + q) * 1024)));
   }
   __device__ __forceinline__ void load(int q, int wave, int lane) {
     const int r = row_of(q, wave, lane), c = column_of(q, wave, lane);
@@ -180,6 +198,7 @@ struct KmListSide {
   static constexpr bool kDown = true;
   static constexpr int kLoads = W / 32, kChunks = W / 8;
   rsrc_t rsrc;
+  int records;
   Chunk<S == kDirect ? kAnyRows : S> held[S == kDirect ? 1 : kLoads];
   const uint16_t *base;
   const int *list;
@@ -195,7 +214,7 @@ struct KmListSide {
       next[q] = list[k < n ? k : last];
     }
   }
-  // `list` has a readable place if n is 0.
+  // `list` has a readable place if n is 0.  Before begin(0).
   __device__ __forceinline__ void init(const uint16_t *base_, long long bytes, long long ld_,
                                        const int *list_, int n_, int width_, int wave, int lane) {
     base = base_;
@@ -204,18 +223,19 @@ struct KmListSide {
     n = n_;
     last = n > 0 ? n - 1 : 0;
     width = width_;
-    if constexpr (S == kDirect) rsrc = buffer_of(base_, bytes);
+    records = records_of(bytes);
     fetch(0, wave, lane);
   }
   __device__ __forceinline__ void begin(int kk, int wave, int lane) {
     k0 = kStepK * kk;
+    if constexpr (S == kDirect) rsrc = buffer_of(base, records);
     fetch(kk + 1, wave, lane);
   }
   __device__ __forceinline__ void issue(int q, unsigned stage, int wave, int lane) {
     const int c = KmSide<W, S>::column_of(q, wave, lane);
     const bool in = k0 + KmSide<W, S>::row_of(q, wave, lane) < n && c < width;
     buffer_load_to_lds16(in ? (int)(2 * (now[q] * ld + c)) : kOutside, rsrc, 0,
-                         stage + (kLoads * wave + q) * 1024);
+                         (unsigned)uniform((int)(stage + (kLoads * wave + q) * 1024)));
   }
   __device__ __forceinline__ void load(int q, int wave, int lane) {
     const int c = KmSide<W, S>::column_of(q, wave, lane);
@@ -284,117 +304,181 @@ __device__ inline f32x4 mfma_rows(i16x8 b, i16x8 a, f32x4 acc) {
     return mfma_f16(__builtin_bit_cast(u32x4, b), __builtin_bit_cast(u32x4, a), acc);
 }
 
-// The products of nk steps onto zero; `blocks` of this wave's blocks of rows have
-// any.  acc[i][j]: lane l has row l % 16 of the wave's row block i (block 2 i +
-// wave / 2 of the tile) and columns 4 (l / 16) .. + 3 of its column block j (block
-// TBN (wave % 2) + j).  On return the LDS may still be read by other waves.
-template <class T, int FMT, int S, class A, class B>
-__device__ __forceinline__ void tile_product(char *lds, A &a, B &b, int nk, int blocks, int wave,
-                                             int lane, f32x4 (&acc)[T::TBM][T::TBN]) {
-  const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t *)lds;
-  const int wm = wave >> 1, wn = wave & 1;
-#pragma unroll
-  for (int i = 0; i < T::TBM; ++i)
-#pragma unroll
-    for (int j = 0; j < T::TBN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (nk <= 0) return;  // uniform
-  constexpr int kLoads = T::A_LOADS + T::B_LOADS;
-
-  auto issue = [&](unsigned stage, int q0, int q1) __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-      if (q < q0 || q >= q1) continue;
-      if (q < T::A_LOADS) side_issue(a, q, stage, wave, lane);
-      else side_issue(b, q - T::A_LOADS, stage + T::A_BYTES, wave, lane);
-    }
-  };
-  auto load = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = 0; q < T::A_LOADS; ++q) side_load(a, q, wave, lane);
-#pragma unroll
-    for (int q = 0; q < T::B_LOADS; ++q) side_load(b, q, wave, lane);
-  };
-  auto put = [&](char *stage) __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = 0; q < T::A_LOADS; ++q)
-      *reinterpret_cast<u32x4 *>(stage + 16 * (64 * (T::A_LOADS * wave + q) + lane)) = a.get(q);
-#pragma unroll
-    for (int q = 0; q < T::B_LOADS; ++q)
-      *reinterpret_cast<u32x4 *>(stage + T::A_BYTES + 16 * (64 * (T::B_LOADS * wave + q) + lane)) =
-          b.get(q);
-  };
-
-  side_begin(a, 0, wave, lane);
-  side_begin(b, 0, wave, lane);
-  if constexpr (S == kDirect) {
-    issue(lds_u, 0, kLoads);
-  } else {
-    load();
-    put(lds);
-  }
-  int stage = 0;
-#pragma unroll 1
-  for (int kk = 0; kk < nk; ++kk) {
-    const bool more = kk + 1 < nk;
-    if constexpr (S == kDirect) __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(0));  // own loads
-    ks_lds_barrier();  // everyone's; the other stage is free
-    const char *st = lds + stage * T::STAGE;
-    const unsigned nst = lds_u + (stage ^ 1) * T::STAGE;
-    if (more) {
-      side_begin(a, kk + 1, wave, lane);
-      side_begin(b, kk + 1, wave, lane);
-      if constexpr (S != kDirect) load();
-    }
-    i16x8 fa[2][T::TBM], fb[2][T::TBN];
-    auto read = [&](int kg) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < T::TBN; ++j)
-        fb[kg & 1][j] = read_operand<B::kDown, T::BN>(st + T::A_BYTES, wn * T::TBN + j, kg, lane);
-#pragma unroll
-      for (int i = 0; i < T::TBM; ++i)
-        fa[kg & 1][i] = read_operand<A::kDown, T::BM>(st, 2 * i + wm, kg, lane);
-    };
-    read(0);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int kg = 0; kg < kStepK / 32; ++kg) {
-#pragma unroll
-      for (int i = 0; i < T::TBM; ++i) {
-        if (i < blocks) {  // uniform
-#pragma unroll
-          for (int j = 0; j < T::TBN; ++j)
-            acc[i][j] = mfma_rows<FMT>(fb[kg & 1][j], fa[kg & 1][i], acc[i][j]);
-        }
-        constexpr int kPerRow = 2;
-        const int row = kg * T::TBM + i;
-        if (S == kDirect && row * kPerRow < kLoads) {
-          __builtin_amdgcn_sched_barrier(0);
-          if (more) issue(nst, row * kPerRow, (row + 1) * kPerRow);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (kg + 1 < kStepK / 32 && i == T::TBM / 2 - 1) {
-          __builtin_amdgcn_sched_barrier(0);
-          read(kg + 1);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-    }
-    stage ^= 1;
-    if constexpr (S != kDirect)
-      if (more) put(lds + stage * T::STAGE);
-    if constexpr (T::TBM * T::TBN == 64) {  // accumulation registers (see big16_kernel)
-#pragma unroll
-      for (int i = 0; i < T::TBM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TBN; ++j) asm volatile("" : "+a"(acc[i][j]));
-    }
-  }
-}
-
 // How many of a wave's row blocks have any of n rows.
 __device__ inline int blocks_of(int n, int wm) {
   const int b = (n + 15) >> 4;
   return (b - wm + 1) >> 1;
+}
+
+// Two column blocks' four values of a lane, in 16 bits, as eight of one: lanes of
+// even groups of 16 get theirs of block a, with the next group's, odd ones of block b.
+// So a row's 64 bytes are stored by four lanes, 16 bytes each.
+struct Eights {
+  u32x4 v;
+  int at;  // of 32 columns
+};
+template <int FMT>
+__device__ inline Eights eights(f32x4 a, f32x4 b, int lane) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(pack2<FMT>(a[0], a[1]), pack2<FMT>(b[0], b[1]),
+                                                   false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(pack2<FMT>(a[2], a[3]), pack2<FMT>(b[2], b[3]),
+                                                   false, false);
+  const int g = lane >> 4;
+  return {u32x4{lo[0], hi[0], lo[1], hi[1]}, 16 * (g & 1) + 8 * (g >> 1)};
+}
+// Stored to a row of `left` values, of any alignment.
+__device__ inline void store_eights(uint16_t *row, const Eights &e, int left) {
+  left -= e.at;
+  if (left >= 8) {
+    *reinterpret_cast<u32x4h *>(row + e.at) = e.v;
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 7; ++c)
+    if (c < left) row[e.at + c] = (uint16_t)(e.v[c >> 1] >> (16 * (c & 1)));
+}
+
+// A workgroup's tiles, one after the other.  `Op` has
+//   Job       what a tile is: `steps` of k, `rows` (of the tile's that there are), ...
+//   A, B      the operands' sides, members a and b
+//   job(t)    the job of this workgroup's t-th tile; t < count
+//   fetch(j)  starts the loads that the sides of job j need to begin
+//   begin(j)  makes the sides those of job j
+//   store(j, acc, wave, lane)
+// In store's acc[i][m] lane l has row l % 16 of the wave's row block i (block 2 i +
+// wave / 2 of the tile) and columns 4 (l / 16) .. + 3 of its column block m (block
+// TBN (wave % 2) + m).
+//
+// The loads of a tile's first step are issued under the end of the tile before, so
+// that they are on their way while its results are stored.
+template <class T, int FMT, int S, class Op>
+__device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave, int lane) {
+  if (count <= 0) return;  // uniform
+  const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t *)lds;
+  const int wm = wave >> 1, wn = wave & 1;
+  constexpr int kLoads = T::A_LOADS + T::B_LOADS;
+
+  auto issue = [&](unsigned to, int q0, int q1) __attribute__((always_inline)) {
+    const unsigned stage = (unsigned)uniform((int)to);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      if (q < q0 || q >= q1) continue;
+      if (q < T::A_LOADS) side_issue(op.a, q, stage, wave, lane);
+      else side_issue(op.b, q - T::A_LOADS, stage + T::A_BYTES, wave, lane);
+    }
+  };
+  auto load = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < T::A_LOADS; ++q) side_load(op.a, q, wave, lane);
+#pragma unroll
+    for (int q = 0; q < T::B_LOADS; ++q) side_load(op.b, q, wave, lane);
+  };
+  auto put = [&](char *stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < T::A_LOADS; ++q)
+      *reinterpret_cast<u32x4 *>(stage + 16 * (64 * (T::A_LOADS * wave + q) + lane)) = op.a.get(q);
+#pragma unroll
+    for (int q = 0; q < T::B_LOADS; ++q)
+      *reinterpret_cast<u32x4 *>(stage + T::A_BYTES + 16 * (64 * (T::B_LOADS * wave + q) + lane)) =
+          op.b.get(q);
+  };
+  int stage = 0;
+  // The first step of a job that has one.
+  auto first_step = [&](const typename Op::Job &j) __attribute__((always_inline)) {
+    op.begin(j);
+    side_begin(op.a, 0, wave, lane);
+    side_begin(op.b, 0, wave, lane);
+    if constexpr (S == kDirect) {
+      issue(lds_u + stage * T::STAGE, 0, kLoads);
+    } else {
+      load();
+      put(lds + stage * T::STAGE);
+    }
+  };
+
+  typename Op::Job job = op.job(0);
+  op.fetch(job);
+  if (job.steps > 0) first_step(job);
+#pragma unroll 1
+  for (int t = 0; t < count; ++t) {
+    const bool next = t + 1 < count;
+    typename Op::Job after = job;
+    if (next) after = op.job(t + 1);
+    const int blocks = blocks_of(job.rows, wm), nk = job.steps;
+    f32x4 acc[T::TBM][T::TBN];
+#pragma unroll
+    for (int i = 0; i < T::TBM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::TBN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // A step; MORE: another of this tile follows.
+    auto step = [&](auto more, int kk) __attribute__((always_inline)) {
+      constexpr bool MORE = decltype(more)::value;
+      if constexpr (S == kDirect) __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(0));  // own loads
+      ks_lds_barrier();  // everyone's; the other stage is free
+      const char *st = lds + stage * T::STAGE;
+      stage ^= 1;
+      const unsigned nst = lds_u + stage * T::STAGE;
+      if constexpr (MORE) {
+        side_begin(op.a, kk + 1, wave, lane);
+        side_begin(op.b, kk + 1, wave, lane);
+        if constexpr (S != kDirect) load();
+      } else if (next) {
+        op.fetch(after);
+      }
+      i16x8 fa[2][T::TBM], fb[2][T::TBN];
+      auto read = [&](int kg) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < T::TBN; ++j)
+          fb[kg & 1][j] =
+              read_operand<Op::B::kDown, T::BN>(st + T::A_BYTES, wn * T::TBN + j, kg, lane);
+#pragma unroll
+        for (int i = 0; i < T::TBM; ++i)
+          fa[kg & 1][i] = read_operand<Op::A::kDown, T::BM>(st, 2 * i + wm, kg, lane);
+      };
+      read(0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int kg = 0; kg < kStepK / 32; ++kg) {
+#pragma unroll
+        for (int i = 0; i < T::TBM; ++i) {
+          if (i < blocks) {  // uniform
+#pragma unroll
+            for (int j = 0; j < T::TBN; ++j)
+              acc[i][j] = mfma_rows<FMT>(fb[kg & 1][j], fa[kg & 1][i], acc[i][j]);
+          }
+          constexpr int kPerRow = 2;
+          const int row = kg * T::TBM + i;
+          if (MORE && S == kDirect && row * kPerRow < kLoads) {
+            __builtin_amdgcn_sched_barrier(0);
+            issue(nst, row * kPerRow, (row + 1) * kPerRow);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (kg + 1 < kStepK / 32 && i == T::TBM / 2 - 1) {
+            __builtin_amdgcn_sched_barrier(0);
+            read(kg + 1);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      }
+      if constexpr (S != kDirect && MORE) put(lds + stage * T::STAGE);
+      if constexpr (T::TBM * T::TBN == 64) {  // accumulation registers (see big16_kernel)
+#pragma unroll
+        for (int i = 0; i < T::TBM; ++i)
+#pragma unroll
+          for (int j = 0; j < T::TBN; ++j) asm volatile("" : "+a"(acc[i][j]));
+      }
+    };
+#pragma unroll 1
+    for (int kk = 0; kk + 1 < nk; ++kk) step(std::true_type{}, kk);
+    if (nk > 0) step(std::false_type{}, nk - 1);
+    if (next) {
+      if (nk <= 0) op.fetch(after);
+      if (after.steps > 0) first_step(after);
+    }
+    op.store(job, acc, wave, lane);
+    job = after;
+  }
+  if constexpr (S == kDirect) __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(0));
 }
 
 }  // namespace
