@@ -12,12 +12,12 @@ namespace {
 template <class T, int FMT, bool GATES>
 __device__ __forceinline__ void store_part(const ExpertsProblem &p, const RowJob &j,
                                            const f32x4 (&acc)[T::TBM][T::TBN], int wave, int lane) {
-  const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15;
+  const int wm = wave / T::WGN, wn = wave % T::WGN, l16 = lane & 15;
   const int *list = ws_at<int>(p, p.at.list) + j.first;
 #pragma unroll
   for (int i = 0; i < T::TBM; ++i) {
-    const int row = 16 * (2 * i + wm) + l16;
-    if (16 * (2 * i + wm) >= j.rows) continue;  // uniform
+    const int row = 16 * (T::WGM * i + wm) + l16;
+    if (16 * (T::WGM * i + wm) >= j.rows) continue;  // uniform
     const bool in = row < j.rows;
     const long long pair = list[in ? row : 0];
     const float gate = GATES ? p.gates[pair] : 1.f;
@@ -35,8 +35,8 @@ __device__ __forceinline__ void store_part(const ExpertsProblem &p, const RowJob
 template <class T, int FMT, int S>
 struct Down {
   typedef RowJob Job;
-  typedef KcSide<T::BM, S> A;
-  typedef KcSide<T::BN, S> B;
+  typedef KcSide<T::BM, S, T::WAVES> A;
+  typedef KcSide<T::BN, S, T::WAVES> B;
   const ExpertsProblem &p;
   const Share share;
   const int rows, columns, wave, lane;
@@ -73,8 +73,8 @@ struct Down {
 template <class T, int FMT, int S>
 struct Dx {
   typedef RowJob Job;
-  typedef KcSide<T::BM, S> A;
-  typedef KmSide<T::BN, S> B;
+  typedef KcSide<T::BM, S, T::WAVES> A;
+  typedef KmSide<T::BN, S, T::WAVES> B;
   const ExpertsProblem &p;
   const Share share;
   const int rows, columns, wave, lane;
@@ -112,11 +112,11 @@ __device__ __forceinline__ void part_tiles(const ExpertsProblem &p) {
   tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_down_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, 2) experts_down_kernel(ExpertsProblem p) {
   part_tiles<T, FMT, S, Down>(p);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_dx_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, 2) experts_dx_kernel(ExpertsProblem p) {
   part_tiles<T, FMT, S, Dx>(p);
 }
 

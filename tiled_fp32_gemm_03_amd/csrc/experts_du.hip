@@ -13,8 +13,8 @@ namespace {
 template <class T, int FMT, int S>
 struct Du {
   typedef RowJob Job;
-  typedef KcSide<T::BM, S> A;
-  typedef KmSide<T::BN, S> B;
+  typedef KcSide<T::BM, S, T::WAVES> A;
+  typedef KmSide<T::BN, S, T::WAVES> B;
   const ExpertsProblem &p;
   const Share share;
   const int rows, columns, wave, lane;
@@ -40,13 +40,13 @@ struct Du {
   }
   __device__ __forceinline__ void store(const Job &j, const f32x4 (&acc)[T::TBM][T::TBN], int wave,
                                         int lane) const {
-    const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15, g = lane >> 4;
+    const int wm = wave / T::WGN, wn = wave % T::WGN, l16 = lane & 15, g = lane >> 4;
     const int *list = ws_at<int>(p, p.at.list) + j.first;
-    float *dg = ws_at<float>(p, p.at.dg) + (2LL * j.tn + wn) * p.T * p.top;
+    float *dg = ws_at<float>(p, p.at.dg) + ((long long)T::WGN * j.tn + wn) * p.T * p.top;
 #pragma unroll
     for (int i = 0; i < T::TBM; ++i) {
-      const int row = 16 * (2 * i + wm) + l16;
-      if (16 * (2 * i + wm) >= j.rows) continue;  // uniform
+      const int row = 16 * (T::WGM * i + wm) + l16;
+      if (16 * (T::WGM * i + wm) >= j.rows) continue;  // uniform
       const bool in = row < j.rows;
       const long long place = j.first + (in ? row : 0);
       const float gate = p.gates[list[in ? row : 0]];
@@ -96,7 +96,7 @@ struct Du {
 };
 
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_du_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, 2) experts_du_kernel(ExpertsProblem p) {
   __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int rows = row_tiles(p), columns = (int)ceil_div(p.I, T::BN);

@@ -40,8 +40,8 @@ __device__ inline int at_most(int a, int b) { return a < b ? a : b; }
 template <class T, int FMT, int S>
 struct Dw1 {
   typedef WeightJob Job;
-  typedef KmSide<T::BM, S> A;
-  typedef KmListSide<T::BN, S> B;
+  typedef KmSide<T::BM, S, T::WAVES> A;
+  typedef KmListSide<T::BN, S, T::WAVES> B;
   const ExpertsProblem &p;
   const Share share;
   const int tiles_m, tiles_n, wave, lane;
@@ -62,11 +62,11 @@ struct Dw1 {
   }
   __device__ __forceinline__ void store(const Job &j, const f32x4 (&acc)[T::TBM][T::TBN], int wave,
                                         int lane) const {
-    const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15, ip = (int)p.at.ipitch;
+    const int wm = wave / T::WGN, wn = wave % T::WGN, l16 = lane & 15, ip = (int)p.at.ipitch;
     uint16_t *out = p.dW1 + 2LL * p.I * j.e * p.lddw1;
 #pragma unroll
     for (int i = 0; i < T::TBM; ++i) {
-      const int c = j.m0 + 16 * (2 * i + wm) + l16, second = c >= ip, at = c - (second ? ip : 0);
+      const int c = j.m0 + 16 * (T::WGM * i + wm) + l16, second = c >= ip, at = c - (second ? ip : 0);
       const bool in = c < 2 * ip && at < p.I;
       uint16_t *row = out + ((second ? p.I : 0) + at) * p.lddw1;
 #pragma unroll
@@ -83,8 +83,8 @@ struct Dw1 {
 template <class T, int FMT, int S>
 struct Dw2 {
   typedef WeightJob Job;
-  typedef KmListSide<T::BM, S> A;
-  typedef KmSide<T::BN, S> B;
+  typedef KmListSide<T::BM, S, T::WAVES> A;
+  typedef KmSide<T::BN, S, T::WAVES> B;
   const ExpertsProblem &p;
   const Share share;
   const int tiles_m, tiles_n, wave, lane;
@@ -104,11 +104,11 @@ struct Dw2 {
   }
   __device__ __forceinline__ void store(const Job &j, const f32x4 (&acc)[T::TBM][T::TBN], int wave,
                                         int lane) const {
-    const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15;
+    const int wm = wave / T::WGN, wn = wave % T::WGN, l16 = lane & 15;
     uint16_t *out = p.dW2 + (long long)p.H * j.e * p.lddw2;
 #pragma unroll
     for (int i = 0; i < T::TBM; ++i) {
-      const int h = j.m0 + 16 * (2 * i + wm) + l16;
+      const int h = j.m0 + 16 * (T::WGM * i + wm) + l16;
       uint16_t *row = out + h * p.lddw2;
 #pragma unroll
       for (int m = 0; m < T::TBN; m += 2) {
@@ -129,11 +129,11 @@ __device__ __forceinline__ void weight_tiles(const ExpertsProblem &p, int rows, 
   tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_dw1_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, 2) experts_dw1_kernel(ExpertsProblem p) {
   weight_tiles<T, FMT, S, Dw1>(p, (int)(2 * p.at.ipitch), p.H);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_dw2_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, 2) experts_dw2_kernel(ExpertsProblem p) {
   weight_tiles<T, FMT, S, Dw2>(p, p.H, p.I);
 }
 

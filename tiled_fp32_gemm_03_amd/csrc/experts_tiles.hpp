@@ -77,21 +77,22 @@ inline bool by_words(const void *p, long long width) {
 }
 
 // KERN on at most `tiles` tiles: as many workgroups as the chip holds at once.
-template <auto KERN>
+template <auto KERN, int THREADS>
 hipError_t launch_tiles(const ExpertsProblem &p, long long tiles, hipStream_t s) {
   if (tiles <= 0) return hipSuccess;
-  const long long most = resident_workgroups<KERN, 256>();
-  return launch_kernel(KERN, dim3((unsigned)(tiles < most ? tiles : most)), dim3(256), s, p);
+  const long long most = resident_workgroups<KERN, THREADS>();
+  return launch_kernel(KERN, dim3((unsigned)(tiles < most ? tiles : most)), dim3(THREADS),
+                       s, p);
 }
 // KERN<T, format, S, ...> in the call's format.
 #define GEMM_F32_LAUNCH_ROWS(KERN, T, S, ...)                                         \
-  (p.format == kBf16 ? launch_tiles<KERN<T, kBf16, S>>(p, __VA_ARGS__, s)               \
-                     : launch_tiles<KERN<T, kF16, S>>(p, __VA_ARGS__, s))
+  (p.format == kBf16 ? launch_tiles<KERN<T, kBf16, S>, T::THREADS>(p, __VA_ARGS__, s)               \
+                     : launch_tiles<KERN<T, kF16, S>, T::THREADS>(p, __VA_ARGS__, s))
 
-typedef RowTile<128, 128> Large;
-typedef RowTile<64, 64> Small;
-template <class T>
-constexpr int kPerSimd = T::STAGE > 40 * 1024 ? 1 : 2;  // workgroups to a CU
+// Two waves to a SIMD: eight of one workgroup, or four of each of two.
+typedef RowTile<64, 128, 4, 2> Large;
+typedef RowTile<64, 64, 2, 2> Small;
+static_assert(Large::WGN == 2 && Small::WGN == 2, "slices of ExpertsSpace");
 
 // `make(tile, integral_constant S)` launches.  Large tiles are loaded directly
 // alone (through registers a wave of 128 x 128 has none left for its loads).

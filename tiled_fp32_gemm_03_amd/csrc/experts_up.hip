@@ -13,8 +13,8 @@ namespace {
 template <class T, int FMT, int S, bool SAVE>
 struct Up {
   typedef RowJob Job;
-  typedef KcSide<T::BM, S> A;
-  typedef KcSide<T::BN, S> B;
+  typedef KcSide<T::BM, S, T::WAVES> A;
+  typedef KcSide<T::BN, S, T::WAVES> B;
   static constexpr int kU = T::BN / 2;
   const ExpertsProblem &p;
   const Share share;
@@ -45,11 +45,11 @@ struct Up {
   }
   __device__ __forceinline__ void store(const Job &j, const f32x4 (&acc)[T::TBM][T::TBN], int wave,
                                         int lane) const {
-    const int wm = wave >> 1, wn = wave & 1, l16 = lane & 15, g = lane >> 4;
+    const int wm = wave / T::WGN, wn = wave % T::WGN, l16 = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int i = 0; i < T::TBM; ++i) {
-      const int row = 16 * (2 * i + wm) + l16;
-      if (16 * (2 * i + wm) >= j.rows) continue;  // uniform
+      const int row = 16 * (T::WGM * i + wm) + l16;
+      if (16 * (T::WGM * i + wm) >= j.rows) continue;  // uniform
       const bool in = row < j.rows;
       const long long place = j.first + row;
 #pragma unroll
@@ -88,11 +88,11 @@ __device__ __forceinline__ void up_tiles(const ExpertsProblem &p) {
   tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_up_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, 2) experts_up_kernel(ExpertsProblem p) {
   up_tiles<T, FMT, S, false>(p);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(256, kPerSimd<T>) experts_up_save_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, 2) experts_up_save_kernel(ExpertsProblem p) {
   up_tiles<T, FMT, S, true>(p);
 }
 

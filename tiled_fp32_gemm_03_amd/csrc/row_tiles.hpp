@@ -1,9 +1,9 @@
 // Products of 16-bit matrices in tiles whose rows are chosen by a list (gfx950):
 // the experts' products and the adapters'.
 //
-// A tile of 2 WTM x 2 WTN over 4 waves (2 x 2), each with WTM / 16 x WTN / 16
-// blocks of v_mfma_f32_16x16x32, in 64-deep k steps and two LDS stages.  The waves
-// of one column half take the tile's blocks of 16 rows in turn, so that a tile
+// A tile is WGM x WGN waves of WTM / 16 x WTN / 16 blocks of v_mfma_f32_16x16x32,
+// in 64-deep k steps and two LDS stages.  The waves that share columns
+// take the tile's blocks of 16 rows in turn, so that a tile
 // with few rows costs every wave the same, and blocks without rows are passed
 // over.  An operand lies in memory in one of two ways, and in LDS likewise:
 //   * k along its rows (KcSide): rows of 64 k, 8 chunks of 16 bytes, at m16_a_pos;
@@ -37,13 +37,16 @@ constexpr int kStepK = 64;
 constexpr int kMostRecords = 0x7ffffff0;
 constexpr int kNever = 0x7fffffff;
 
-template <int WTM_, int WTN_>
+// WGM x WGN waves of WTM x WTN.
+template <int WTM_, int WTN_, int WGM_, int WGN_>
 struct RowTile {
-  static constexpr int WTM = WTM_, WTN = WTN_, BM = 2 * WTM_, BN = 2 * WTN_;
+  static constexpr int WTM = WTM_, WTN = WTN_, WGM = WGM_, WGN = WGN_, WAVES = WGM_ * WGN_;
+  static constexpr int BM = WGM_ * WTM_, BN = WGN_ * WTN_, THREADS = 64 * WAVES;
   static constexpr int TBM = WTM_ / 16, TBN = WTN_ / 16;
   static constexpr int A_BYTES = BM * kStepK * 2, B_BYTES = BN * kStepK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int A_LOADS = BM / 32, B_LOADS = BN / 32;  // per wave and step, 1 KB each
+  static constexpr int A_LOADS = BM / 8 / WAVES, B_LOADS = BN / 8 / WAVES;  // per wave and step, 1 KB each
+  static_assert(A_LOADS % 2 == 0 && B_LOADS % 2 == 0, "whole pairs of loads (KcSide)");
   static_assert(2 * STAGE <= kLdsBytes, "two stages fit in LDS");
 };
 
@@ -82,13 +85,13 @@ struct Chunk {
   }
 };
 
-// An operand with k along its rows, W rows of it.  `row(r, q)`: row r's first element,
+// An operand with k along its rows, W rows of it, loaded by NW waves.  `row(r, q)`: row r's first element,
 // or null; q, the number of the load that brings it, row_of its r.  K values to a row; from step `half` on (for rows of two
 // parts, each of whole steps and K values) the second part.
-template <int W, int S>
+template <int W, int S, int NW>
 struct KcSide {
   static constexpr bool kDown = false;
-  static constexpr int kLoads = W / 32;
+  static constexpr int kLoads = W / 8 / NW;
   const void *base;
   int records;
   rsrc_t rsrc;
@@ -140,10 +143,10 @@ struct KcSide {
 // An operand with k down its rows, `width` (at most W) columns of it: n rows from
 // `first` on, ld elements apart.  From step `half` on the second part: n rows
 // from `second` on.
-template <int W, int S>
+template <int W, int S, int NW>
 struct KmSide {
   static constexpr bool kDown = true;
-  static constexpr int kLoads = W / 32, kChunks = W / 8;
+  static constexpr int kLoads = W / 8 / NW, kChunks = W / 8;
   rsrc_t rsrc;
   int voff[S == kDirect ? kLoads : 1];
   Chunk<S == kDirect ? kAnyRows : S> held[S == kDirect ? 1 : kLoads];
@@ -193,10 +196,10 @@ struct KmSide {
 
 // The same with its rows chosen by a list: row k is row list[k] of `base`.  The list
 // is read a step ahead.
-template <int W, int S>
+template <int W, int S, int NW>
 struct KmListSide {
   static constexpr bool kDown = true;
-  static constexpr int kLoads = W / 32, kChunks = W / 8;
+  static constexpr int kLoads = W / 8 / NW, kChunks = W / 8;
   rsrc_t rsrc;
   int records;
   Chunk<S == kDirect ? kAnyRows : S> held[S == kDirect ? 1 : kLoads];
@@ -209,7 +212,7 @@ struct KmListSide {
   __device__ __forceinline__ void fetch(int kk, int wave, int lane) {
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
-      const int k = kStepK * kk + KmSide<W, S>::row_of(q, wave, lane);
+      const int k = kStepK * kk + KmSide<W, S, NW>::row_of(q, wave, lane);
       now[q] = next[q];
       next[q] = list[k < n ? k : last];
     }
@@ -232,49 +235,49 @@ struct KmListSide {
     fetch(kk + 1, wave, lane);
   }
   __device__ __forceinline__ void issue(int q, unsigned stage, int wave, int lane) {
-    const int c = KmSide<W, S>::column_of(q, wave, lane);
-    const bool in = k0 + KmSide<W, S>::row_of(q, wave, lane) < n && c < width;
+    const int c = KmSide<W, S, NW>::column_of(q, wave, lane);
+    const bool in = k0 + KmSide<W, S, NW>::row_of(q, wave, lane) < n && c < width;
     buffer_load_to_lds16(in ? (int)(2 * (now[q] * ld + c)) : kOutside, rsrc, 0,
                          (unsigned)uniform((int)(stage + (kLoads * wave + q) * 1024)));
   }
   __device__ __forceinline__ void load(int q, int wave, int lane) {
-    const int c = KmSide<W, S>::column_of(q, wave, lane);
-    const bool in = k0 + KmSide<W, S>::row_of(q, wave, lane) < n && c < width;
+    const int c = KmSide<W, S, NW>::column_of(q, wave, lane);
+    const bool in = k0 + KmSide<W, S, NW>::row_of(q, wave, lane) < n && c < width;
     held[q].load(in ? base + now[q] * ld : nullptr, c, width);
   }
   __device__ __forceinline__ u32x4 get(int q) const { return held[q].get(); }
 };
 
 // One set of calls for all sides.
-template <int W, int S>
-__device__ __forceinline__ void side_begin(KcSide<W, S> &x, int kk, int, int) { x.begin(kk); }
-template <int W, int S>
-__device__ __forceinline__ void side_begin(KmSide<W, S> &x, int kk, int, int) { x.begin(kk); }
-template <int W, int S>
-__device__ __forceinline__ void side_begin(KmListSide<W, S> &x, int kk, int wave, int lane) {
+template <int W, int S, int NW>
+__device__ __forceinline__ void side_begin(KcSide<W, S, NW> &x, int kk, int, int) { x.begin(kk); }
+template <int W, int S, int NW>
+__device__ __forceinline__ void side_begin(KmSide<W, S, NW> &x, int kk, int, int) { x.begin(kk); }
+template <int W, int S, int NW>
+__device__ __forceinline__ void side_begin(KmListSide<W, S, NW> &x, int kk, int wave, int lane) {
   x.begin(kk, wave, lane);
 }
-template <int W, int S>
-__device__ __forceinline__ void side_issue(KcSide<W, S> &x, int q, unsigned stage, int wave, int) {
+template <int W, int S, int NW>
+__device__ __forceinline__ void side_issue(KcSide<W, S, NW> &x, int q, unsigned stage, int wave, int) {
   x.issue(q, stage, wave);
 }
-template <int W, int S>
-__device__ __forceinline__ void side_issue(KmSide<W, S> &x, int q, unsigned stage, int wave, int) {
+template <int W, int S, int NW>
+__device__ __forceinline__ void side_issue(KmSide<W, S, NW> &x, int q, unsigned stage, int wave, int) {
   x.issue(q, stage, wave);
 }
-template <int W, int S>
-__device__ __forceinline__ void side_issue(KmListSide<W, S> &x, int q, unsigned stage, int wave,
+template <int W, int S, int NW>
+__device__ __forceinline__ void side_issue(KmListSide<W, S, NW> &x, int q, unsigned stage, int wave,
                                            int lane) {
   x.issue(q, stage, wave, lane);
 }
-template <int W, int S>
-__device__ __forceinline__ void side_load(KcSide<W, S> &x, int q, int, int) { x.load(q); }
-template <int W, int S>
-__device__ __forceinline__ void side_load(KmSide<W, S> &x, int q, int wave, int lane) {
+template <int W, int S, int NW>
+__device__ __forceinline__ void side_load(KcSide<W, S, NW> &x, int q, int, int) { x.load(q); }
+template <int W, int S, int NW>
+__device__ __forceinline__ void side_load(KmSide<W, S, NW> &x, int q, int wave, int lane) {
   x.load(q, wave, lane);
 }
-template <int W, int S>
-__device__ __forceinline__ void side_load(KmListSide<W, S> &x, int q, int wave, int lane) {
+template <int W, int S, int NW>
+__device__ __forceinline__ void side_load(KmListSide<W, S, NW> &x, int q, int wave, int lane) {
   x.load(q, wave, lane);
 }
 
@@ -305,9 +308,9 @@ __device__ inline f32x4 mfma_rows(i16x8 b, i16x8 a, f32x4 acc) {
 }
 
 // How many of a wave's row blocks have any of n rows.
+template <class T>
 __device__ inline int blocks_of(int n, int wm) {
-  const int b = (n + 15) >> 4;
-  return (b - wm + 1) >> 1;
+  return (((n + 15) >> 4) - wm + T::WGM - 1) / T::WGM;
 }
 
 // Two column blocks' four values of a lane, in 16 bits, as eight of one: lanes of
@@ -345,9 +348,9 @@ __device__ inline void store_eights(uint16_t *row, const Eights &e, int left) {
 //   fetch(j)  starts the loads that the sides of job j need to begin
 //   begin(j)  makes the sides those of job j
 //   store(j, acc, wave, lane)
-// In store's acc[i][m] lane l has row l % 16 of the wave's row block i (block 2 i +
-// wave / 2 of the tile) and columns 4 (l / 16) .. + 3 of its column block m (block
-// TBN (wave % 2) + m).
+// In store's acc[i][m] lane l has row l % 16 of the wave's row block i (block WGM i +
+// wave / WGN of the tile) and columns 4 (l / 16) .. + 3 of its column block m (block
+// TBN (wave % WGN) + m).
 //
 // The loads of a tile's first step are issued under the end of the tile before, so
 // that they are on their way while its results are stored.
@@ -355,7 +358,7 @@ template <class T, int FMT, int S, class Op>
 __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave, int lane) {
   if (count <= 0) return;  // uniform
   const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t *)lds;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / T::WGN, wn = wave % T::WGN;
   constexpr int kLoads = T::A_LOADS + T::B_LOADS;
 
   auto issue = [&](unsigned to, int q0, int q1) __attribute__((always_inline)) {
@@ -404,15 +407,16 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
     const bool next = t + 1 < count;
     typename Op::Job after = job;
     if (next) after = op.job(t + 1);
-    const int blocks = blocks_of(job.rows, wm), nk = job.steps;
+    const int blocks = blocks_of<T>(job.rows, wm), nk = job.steps;
     f32x4 acc[T::TBM][T::TBN];
 #pragma unroll
     for (int i = 0; i < T::TBM; ++i)
 #pragma unroll
       for (int j = 0; j < T::TBN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // A step; MORE: another of this tile follows.
-    auto step = [&](auto more, int kk) __attribute__((always_inline)) {
-      constexpr bool MORE = decltype(more)::value;
+    // A step; MORE: another of this tile follows; FULL: every row block has rows (a
+    // branch to each block costs a lone wave a tenth of its rate).
+    auto step = [&](auto more, auto full, int kk) __attribute__((always_inline)) {
+      constexpr bool MORE = decltype(more)::value, FULL = decltype(full)::value;
       if constexpr (S == kDirect) __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(0));  // own loads
       ks_lds_barrier();  // everyone's; the other stage is free
       const char *st = lds + stage * T::STAGE;
@@ -425,26 +429,40 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
       } else if (next) {
         op.fetch(after);
       }
-      i16x8 fa[2][T::TBM], fb[2][T::TBN];
+      // One group's operands, or two where there are registers for them.
+      constexpr int kAhead = T::TBM * T::TBN <= 16 ? 1 : 0;
+      i16x8 fa[1 + kAhead][T::TBM], fb[1 + kAhead][T::TBN];
       auto read = [&](int kg) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < T::TBN; ++j)
-          fb[kg & 1][j] =
+          fb[kg & kAhead][j] =
               read_operand<Op::B::kDown, T::BN>(st + T::A_BYTES, wn * T::TBN + j, kg, lane);
 #pragma unroll
         for (int i = 0; i < T::TBM; ++i)
-          fa[kg & 1][i] = read_operand<Op::A::kDown, T::BM>(st, 2 * i + wm, kg, lane);
+          fa[kg & kAhead][i] = read_operand<Op::A::kDown, T::BM>(st, T::WGM * i + wm, kg, lane);
       };
-      read(0);
+      // The first group's in the order of their use.
+      fb[0][0] = read_operand<Op::B::kDown, T::BN>(st + T::A_BYTES, wn * T::TBN, 0, lane);
       __builtin_amdgcn_sched_barrier(0);
+      fa[0][0] = read_operand<Op::A::kDown, T::BM>(st, wm, 0, lane);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 1; j < T::TBN; ++j)
+        fb[0][j] = read_operand<Op::B::kDown, T::BN>(st + T::A_BYTES, wn * T::TBN + j, 0, lane);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 1; i < T::TBM; ++i) {
+        fa[0][i] = read_operand<Op::A::kDown, T::BM>(st, T::WGM * i + wm, 0, lane);
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int kg = 0; kg < kStepK / 32; ++kg) {
 #pragma unroll
         for (int i = 0; i < T::TBM; ++i) {
-          if (i < blocks) {  // uniform
+          if (FULL || i < blocks) {  // uniform
 #pragma unroll
             for (int j = 0; j < T::TBN; ++j)
-              acc[i][j] = mfma_rows<FMT>(fb[kg & 1][j], fa[kg & 1][i], acc[i][j]);
+              acc[i][j] = mfma_rows<FMT>(fb[kg & kAhead][j], fa[kg & kAhead][i], acc[i][j]);
           }
           constexpr int kPerRow = 2;
           const int row = kg * T::TBM + i;
@@ -453,7 +471,7 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
             issue(nst, row * kPerRow, (row + 1) * kPerRow);
             __builtin_amdgcn_sched_barrier(0);
           }
-          if (kg + 1 < kStepK / 32 && i == T::TBM / 2 - 1) {
+          if (kg + 1 < kStepK / 32 && i == (kAhead ? T::TBM / 2 - 1 : T::TBM - 1)) {
             __builtin_amdgcn_sched_barrier(0);
             read(kg + 1);
             __builtin_amdgcn_sched_barrier(0);
@@ -468,9 +486,14 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
           for (int j = 0; j < T::TBN; ++j) asm volatile("" : "+a"(acc[i][j]));
       }
     };
+    if (blocks == T::TBM) {
 #pragma unroll 1
-    for (int kk = 0; kk + 1 < nk; ++kk) step(std::true_type{}, kk);
-    if (nk > 0) step(std::false_type{}, nk - 1);
+      for (int kk = 0; kk + 1 < nk; ++kk) step(std::true_type{}, std::true_type{}, kk);
+    } else {
+#pragma unroll 1
+      for (int kk = 0; kk + 1 < nk; ++kk) step(std::true_type{}, std::false_type{}, kk);
+    }
+    if (nk > 0) step(std::false_type{}, std::false_type{}, nk - 1);
     if (next) {
       if (nk <= 0) op.fetch(after);
       if (after.steps > 0) first_step(after);
