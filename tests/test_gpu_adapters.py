@@ -1,0 +1,155 @@
+"""GPU parity of the projection with low-rank adapters (matmul_adapters) with its
+definition in 64 bits.
+
+Bars, from the arithmetic.  A sum of K terms in fp32 is off by at most (K + 8) 2^-23 of the
+sum of their magnitudes, in whatever order; scale A x is kept in 16 bits, hs (half a step of
+the format) more; B's product of it is off by that, and by its own sum of R terms; the two
+parts are added in fp32 and rounded once to the format."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from experts_util import HALF_STEP, TINY, _mm  # noqa: E402
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+EPS = 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def g():
+    import tiled_fp32_gemm_03_amd as lib
+    return lib
+
+
+def _make(T, N, K, R, count, dtype, ids=None, seed=0):
+    rng = np.random.default_rng(seed + T + 3 * N + 5 * K + 7 * R + 11 * count)
+    dev = torch.device("cuda:0")
+    to = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dev)  # noqa: E731
+    x, w = to(T, K).to(dtype), (to(N, K) / K ** 0.5).to(dtype)
+    a, b = (to(count, R, K) / K ** 0.5).to(dtype), (to(count, N, R) / R ** 0.5).to(dtype)
+    scales = torch.from_numpy((rng.random(count) * 4 - 1).astype(np.float32)).to(dev)
+    if ids is None:
+        ids = rng.integers(-1, count + 1, T)
+    return x, w, a, b, torch.from_numpy(np.asarray(ids).astype(np.int32)).to(dev), scales
+
+
+def reference(x, w, a, b, ids, scales):
+    hs, tiny = HALF_STEP[x.dtype], TINY[x.dtype]
+    K, R = x.shape[1], a.shape[1]
+    xd, wd = x.double(), w.double()
+    y, bar = _mm(xd, wd.t()), (K + 8) * EPS * _mm(xd.abs(), wd.abs().t())
+    for r in range(a.shape[0]):
+        rows = torch.nonzero(ids == r).squeeze(1)
+        if not rows.numel():
+            continue
+        ad, bd, s = a[r].double(), b[r].double(), 1.0 if scales is None else scales[r].double()
+        v, ev = s * _mm(xd[rows], ad.t()), abs(s) * (K + 24) * EPS * _mm(xd[rows].abs(), ad.abs().t())
+        ev = ev + hs * (v.abs() + ev) + tiny
+        y[rows] += _mm(v, bd.t())
+        bar[rows] += _mm(ev, bd.abs().t()) + (R + 8) * EPS * _mm(v.abs() + ev, bd.abs().t())
+    return y, bar + 4 * EPS * y.abs()
+
+
+def check(got, ref, what):
+    value, bound = ref
+    hs, tiny = HALF_STEP[got.dtype], TINY[got.dtype]
+    d = (got.double() - value).abs()
+    assert torch.isfinite(d).all(), what
+    if d.numel():
+        assert float((d - (bound * (1 + hs) + hs * value.abs() + tiny)).max()) <= 0, (what, float(d.max()))
+        assert float(d.norm()) <= (2e-5 + 2 * hs) * float(value.norm()) + 1e-30, what
+
+
+# rows, columns, K, rank, adapters: one of each, thin products of one to four blocks of rows,
+# tiles of 128 and 256, ranks and widths of fewer than 8 values, odd rows
+CASES = [(1, 1, 1, 1, 1), (1, 64, 128, 16, 3), (3, 17, 5, 3, 2), (4, 100, 300, 8, 4), (16, 200, 1000, 33, 5),
+         (17, 130, 257, 7, 511), (31, 1000, 96, 64, 8), (64, 333, 515, 17, 20), (61, 4095, 129, 100, 3), (64, 16, 4096, 512, 2),
+         (65, 70, 64, 8, 3), (65, 9, 7, 5, 4), (200, 129, 333, 40, 9), (300, 264, 520, 16, 64), (513, 1, 65, 1, 1),
+         (1000, 136, 1024, 65, 30), (2100, 72, 40, 12, 511), (9000, 24, 64, 4, 7)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+@pytest.mark.parametrize("case", CASES)
+def test_adapters(g, case, fmt):
+    print(f"case: adapters {case} {fmt}", flush=True)
+    args = _make(*case, DT[fmt])
+    check(g.matmul_adapters(*args), reference(*args), (case, fmt))
+
+
+@pytest.mark.parametrize("case,fmt", [((3000, 4096, 512, 32, 6), "bf16"), ((1500, 8200, 264, 24, 40), "f16")])
+def test_large_tiles(g, case, fmt):
+    print(f"case: adapters large {case} {fmt}", flush=True)
+    args = _make(*case, DT[fmt])
+    check(g.matmul_adapters(*args), reference(*args), (case, fmt))
+
+
+@pytest.mark.parametrize("T", [5, 40, 600])
+def test_which_rows(g, T):
+    """All of one adapter, none of any, runs that end at and inside tiles, ids far outside."""
+    N, K, R, count = 96, 128, 16, 6
+    far = np.array([-2 ** 31, 2 ** 31 - 1, -1, count])
+    for name, ids in {"one": np.full(T, 3), "none": np.full(T, -1), "halves": (np.arange(T) >= T // 2) * 2,
+                      "tiles": np.arange(T) // 128, "far": far[np.arange(T) % 4], "mixed": np.arange(T) % (count + 2) - 1}.items():
+        print(f"case: adapters rows {T} {name}", flush=True)
+        args = _make(T, N, K, R, count, torch.bfloat16, ids=ids)
+        ref = reference(*args)
+        check(g.matmul_adapters(*args), ref, (T, name))
+        x, w, a, b, i, s = args
+        check(g.matmul_adapters(x, w, a, b, i), reference(x, w, a, b, i, None), (T, name, "no scales"))
+        if name == "none":
+            check(g.matmul_adapters(x, w, a[:0], b[:0], i), ref, (T, "no adapters"))
+
+
+@pytest.mark.parametrize("T", [1, 30, 64, 65, 700])
+def test_one_requests_infinities_are_its_own(g, T):
+    """Infinities and NaN in one adapter's A, B and scale, and in one row of x, leave the
+    other rows' results as they are, to the bit."""
+    print(f"case: adapters infinities {T}", flush=True)
+    ids = np.arange(T) % 4
+    x, w, a, b, i, s = _make(T, 200, 256, 24, 4, torch.bfloat16, ids=ids)
+    want = g.matmul_adapters(x, w, a, b, i, s)
+    for broken in ("a", "b", "scale"):
+        a2, b2, s2 = a.clone(), b.clone(), s.clone()
+        if broken == "a":
+            a2[2] = float("nan")
+        elif broken == "b":
+            b2[2, ::2] = float("inf")
+            b2[2, 1::2] = float("nan")
+        else:
+            s2[2] = float("inf")
+        got = g.matmul_adapters(x, w, a2, b2, i, s2)
+        own = i == 2
+        assert torch.equal(got[~own], want[~own]), (T, broken)
+        if own.any():
+            assert not torch.isfinite(got[own]).all(), (T, broken)
+    x2 = x.clone()
+    x2[T // 2] = float("nan")
+    got = g.matmul_adapters(x2, w, a, b, i, s)
+    rest = torch.arange(T, device=x.device) != T // 2
+    assert torch.equal(got[rest], want[rest]) and got[T // 2].isnan().all()
+
+
+@pytest.mark.parametrize("T", [7, 64, 333])
+def test_strides(g, T):
+    for off, pad in ((0, 8), (8, 16), (1, 2)):
+        print(f"case: adapters strides {T} {off} {pad}", flush=True)
+        x, w, a, b, ids, s = _make(T, 120, 136, 24, 3, torch.float16)
+
+        def wide(t):
+            big = torch.full((*t.shape[:-1], t.shape[-1] + off + pad), float("nan"), dtype=t.dtype, device=t.device)
+            v = big[..., off:off + t.shape[-1]]
+            v.copy_(t)
+            return v
+
+        out = torch.full((T + 1, 120 + pad), 5.0, dtype=x.dtype, device=x.device)
+        y = g.matmul_adapters(wide(x), wide(w), wide(a), wide(b), ids, s, out=out[:T, :120])
+        check(y, reference(x, w, a, b, ids, s), (T, off))
+        assert (out[:, 120:] == 5).all() and (out[T] == 5).all()
+
+
+def test_no_rows(g):
+    x, w, a, b, ids, s = _make(4, 16, 32, 8, 2, torch.bfloat16)
+    assert g.matmul_adapters(x[:0], w, a, b, ids[:0], s).shape == (0, 16)

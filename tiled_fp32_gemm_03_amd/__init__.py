@@ -42,6 +42,9 @@ Raw C-ABI mirrors (same names and argument order as ``include/gemm_f32.h``):
                         saved, dX, lddx, dgates, dW1, lddw1, dW2, lddw2, workspace,
                         workspace_bytes, stream),
   gemm_experts_workspace_bytes(T, E, top, H, I, backward)  (include/gemm_experts.h)
+  gemm_adapters(T, N, K, R, count, X, ldx, W, ldw, A, lda, B, ldb, ids, scales, format, Y, ldy,
+                workspace, workspace_bytes, stream),
+  gemm_adapters_workspace_bytes(T, N, K, R, count)      (include/gemm_adapters.h)
 Pointers are device addresses (ints); ``stream`` is a hipStream_t as int
 (0 = null stream).  A non-zero status raises ``GemmError``.
 
@@ -75,6 +78,9 @@ The same in parts, for other routers, any number of tokens and training:
 sigmoid scores, a bias for balance, groups of experts), ``moe_experts(X, ids,
 gates, w1, w2)`` is the experts' products for a choice, and
 ``moe_route_backward`` and ``moe_experts_backward`` are their gradients.
+
+``matmul_adapters(X, w, a, b, ids)`` is a shared projection with low-rank adapters
+of many requests, one to a row or none.
 """
 from __future__ import annotations
 
@@ -103,6 +109,7 @@ __all__ = [
     "ROUTE_SCORES", "ROUTE_GROUP_SCORES",
     "gemm_experts", "gemm_experts_backward", "gemm_experts_workspace_bytes", "moe_experts",
     "moe_experts_backward",
+    "gemm_adapters", "gemm_adapters_workspace_bytes", "matmul_adapters",
     "library_path",
     "exported_symbols",
 ]
@@ -169,6 +176,9 @@ _SIGS = {
                       _p, _i, _p, _p, _ll, _p], _i),
     "gemm_experts_backward": ([_i, _i, _i, _i, _i, _p, _i, _p, _i, _p, _p, _i, _p, _i, _p, _i, _p,
                                _p, _i, _p, _p, _i, _p, _i, _p, _ll, _p], _i),
+    "gemm_adapters_workspace_bytes": ([_i, _i, _i, _i, _i], _ll),
+    "gemm_adapters": ([_i, _i, _i, _i, _i, _p, _i, _p, _i, _p, _i, _p, _i, _p, _p, _i, _p, _i, _p,
+                       _ll, _p], _i),
     "gemm_f32_probe_lds_bytes": ([_i, _i], _ll),
     "gemm_f32_device_props": ([_i, _ip, _ip, _ip, _ip, _ip], _i),
     "gemm_f32_probe_fused": ([_i, _i, _i, _p, _ll, _p, _p], _i),
@@ -537,6 +547,21 @@ def gemm_experts_backward(T, E, top, H, I, dY, lddy, X, ldx, ids, gates, format,
                                       dgates or None, dW1 or None, lddw1, dW2 or None, lddw2,
                                       workspace or None, int(workspace_bytes), stream or None),
            "gemm_experts_backward")
+
+
+def gemm_adapters_workspace_bytes(T, N, K, R, count) -> int:
+    _fits(int(T), int(N), int(K), int(R), int(count))
+    return int(_lib.gemm_adapters_workspace_bytes(int(T), int(N), int(K), int(R), int(count)))
+
+
+def gemm_adapters(T, N, K, R, count, X, ldx, W, ldw, A, lda, B, ldb, ids, scales, format, Y, ldy,
+                  workspace, workspace_bytes, stream=0) -> None:
+    _fits(T, N, K, R, count, ldx, ldw, lda, ldb, ldy)
+    _check(_lib.gemm_adapters(T, N, K, R, count, X or None, ldx, W or None, ldw, A or None, lda,
+                              B or None, ldb, ids or None, scales or None, _format(format),
+                              Y or None, ldy, workspace or None, int(workspace_bytes),
+                              stream or None),
+           "gemm_adapters")
 
 
 def config_name(variant, config: int = -1, M: int = 1, N: int = 1, K: int = 1) -> str:
@@ -1123,3 +1148,57 @@ def moe_experts_backward(dY, X, ids, gates, w1, w2, saved, weights: bool = True,
              dw2.data_ptr() if weights else None, I, workspace.data_ptr(),
              workspace.numel() * workspace.element_size()))
     return (dX, dgates, dw1, dw2) if weights else (dX, dgates)
+
+
+def matmul_adapters(X, w, a, b, ids, scales=None, out=None, workspace=None, stream=None):
+    """A shared projection with low-rank adapters (include/gemm_adapters.h), y[t] = w x[t] +
+    scales[r] b[r] (a[r] x[t]), r = ids[t]; a row whose id is outside 0 .. count - 1 has no
+    adapter.
+
+    X is (T, K) and w (N, K), both bfloat16 or float16; a is (count, R, K) and b (count, N, R)
+    of the same dtype; ids (T,) int32; scales (count,) float32, or None for 1 each.  Returns
+    (T, N) in X's dtype.  ``workspace`` is a uint8 CUDA tensor of at least
+    gemm_adapters_workspace_bytes; when None, one is allocated with torch for this call.
+    """
+    if X.dtype not in (torch.bfloat16, torch.float16) or not X.is_cuda:
+        raise TypeError("X must be a bfloat16 or float16 CUDA tensor")
+    device = X.device
+    if w.dtype != X.dtype or w.device != device:
+        raise TypeError(f"w must be a {X.dtype} tensor on {device}")
+    ldx, ldw = _pitch(X), _pitch(w)
+    T, K = X.shape
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"w must have rows of {K} values, not {w.shape[1]}")
+    if isinstance(a, MxTensor) or isinstance(b, MxTensor):
+        raise TypeError("a and b must be tensors")
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a and b must have three dimensions: adapters, rows, values")
+    count, R = a.shape[0], a.shape[1]
+    pa = _expert_rows(a, "a", X.dtype, device, count, R, K)
+    pb = _expert_rows(b, "b", X.dtype, device, count, N, R)
+    if ids.dtype != torch.int32 or ids.device != device or not ids.is_contiguous():
+        raise TypeError(f"ids must be a contiguous int32 tensor on {device}")
+    if tuple(ids.shape) != (T,):
+        raise ValueError(f"ids must have {T} values")
+    if scales is not None:
+        if scales.dtype != torch.float32 or scales.device != device or not scales.is_contiguous():
+            raise TypeError(f"scales must be a contiguous float32 tensor on {device}")
+        if tuple(scales.shape) != (count,):
+            raise ValueError(f"scales must have {count} values")
+    _fits(T, N, K, R, count, ldx, ldw, pa[1], pb[1])
+    need = _lib.gemm_adapters_workspace_bytes(T, N, K, R, count)
+    if need < 0:
+        raise ValueError(f"sizes outside the product's bounds: {T} rows, {N} x {K}, {count} adapters "
+                         f"of rank {R}")
+    empty = _empty(device, stream)
+    out = _mx_out(out, (T, N), X.dtype, device, stream)
+    ldy = _pitch(out)
+    _fits(ldy)
+    workspace = _workspace(workspace, need, empty, device)
+    _launch(_lib.gemm_adapters, "gemm_adapters", device, stream,
+            (T, N, K, R, count, X.data_ptr(), ldx, w.data_ptr(), ldw, pa[0], pa[1], pb[0], pb[1],
+             ids.data_ptr(), scales.data_ptr() if scales is not None else None,
+             _MX_DTYPES[X.dtype], out.data_ptr(), ldy, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size()))
+    return out

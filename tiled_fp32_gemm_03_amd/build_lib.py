@@ -23,7 +23,8 @@ ARCH = "gfx950"
 
 SOURCES = ["gemm_f32_abi.hip", "naive_tiled.hip", "prod.hip", "w16_vgpr.hip", "valu.hip", "mixed.hip",
            "mixed16.hip", "probes.hip", "mx_abi.hip", "mx_quant.hip", "mx_gemm.hip", "mx_a16.hip", "moe.hip",
-           "rows_abi.hip", "route.hip", "experts.hip", "experts_up.hip", "experts_down.hip", "experts_du.hip", "experts_dw.hip"]
+           "rows_abi.hip", "route.hip", "experts.hip", "experts_up.hip", "experts_down.hip", "experts_du.hip", "experts_dw.hip",
+           "adapters.hip", "adapters_thin.hip"]
 
 # Host-only C++ (no device code): argument checks, launch table, choice model.
 HOST_SOURCES = ["host_plan.cpp", "mx_plan.cpp", "experts_plan.cpp"]

@@ -19,8 +19,9 @@ constexpr int kMostGroups = 1 << 20;
 constexpr int kOneGroup = 8192, kOneThreads = 1024, kListThreads = 256;
 
 __device__ inline int expert_of(const ExpertsProblem &p, long long pair, long long pairs) {
-  const int e = pair < pairs ? p.ids[pair] : -1;
-  return e >= 0 && e < p.E ? e : kMoeMaxExperts;  // kMoeMaxExperts: none
+  if (pair >= pairs) return kMoeMaxExperts;  // none
+  const int e = p.ids[pair], last = p.E - (p.rest ? 1 : 0);
+  return e >= 0 && e < last ? e : p.rest ? p.E - 1 : kMoeMaxExperts;
 }
 
 // Lanes of the wave whose pair has the same expert.
@@ -49,18 +50,18 @@ __device__ inline void count_pairs(const ExpertsProblem &p, int *count, long lon
 
 // Where each expert's places begin, and the row tiles, from the experts' counts
 // `n` of the first kMoeMaxExperts threads.  On return begin[e] is expert e's first place.
-__device__ inline void lay_out(const ExpertsProblem &p, int n, int (*scan)[2][kMoeMaxExperts],
+__device__ inline void lay_out(const ExpertsProblem &p, int n, int (*scan)[3][kMoeMaxExperts],
                                int *begin) {
   const int e = threadIdx.x;
   const bool in = e < kMoeMaxExperts;
-  const int tiles = (n + p.tile - 1) / p.tile;
-  if (in) scan[0][0][e] = n, scan[0][1][e] = tiles;
+  const int tiles = p.rest && e == p.E - 1 ? 0 : (n + p.tile - 1) / p.tile;
+  if (in) scan[0][0][e] = n, scan[0][1][e] = tiles, scan[0][2][e] = n > 0;
   __syncthreads();
   int from = 0;
   for (int d = 1; d < kMoeMaxExperts; d <<= 1) {
     if (in) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < 3; ++q)
         scan[from ^ 1][q][e] = scan[from][q][e] + (e >= d ? scan[from][q][e - d] : 0);
     }
     from ^= 1;
@@ -78,9 +79,16 @@ __device__ inline void lay_out(const ExpertsProblem &p, int n, int (*scan)[2][kM
       at[1] = first + t * p.tile;
       at[2] = n - t * p.tile < p.tile ? n - t * p.tile : p.tile;
     }
+    if (p.rest && n > 0) {
+      const int run = scan[from][2][e] - 1;
+      int *at = ws_at<int>(p, p.at.runs) + 4 + 4 * run, *tile_run = ws_at<int>(p, p.at.tile_run);
+      at[0] = e, at[1] = first, at[2] = n;
+      for (int t = (first + p.run_tile - 1) / p.run_tile; t * p.run_tile < last; ++t) tile_run[t] = run;
+    }
     if (e == p.E - 1) {
       start[p.E] = last;
       table[0] = t0 + tiles;
+      if (p.rest) *ws_at<int>(p, p.at.runs) = scan[from][2][e];
     }
   }
   __syncthreads();
@@ -125,7 +133,7 @@ __device__ inline void place_pairs(const ExpertsProblem &p, int *begin,
 }
 
 __global__ void __launch_bounds__(kOneThreads) experts_list_kernel(ExpertsProblem p) {
-  __shared__ int scan[2][2][kMoeMaxExperts];
+  __shared__ int scan[2][3][kMoeMaxExperts];
   __shared__ int begin[kMoeMaxExperts];
   __shared__ unsigned short count[kOneThreads / 64][kMoeMaxExperts];
   const long long pairs = (long long)p.T * p.top;
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(kListThreads) experts_count_kernel(ExpertsProb
 
 // One workgroup: each group's counts become the places of its first pairs.
 __global__ void __launch_bounds__(kMoeMaxExperts) experts_scan_kernel(ExpertsProblem p) {
-  __shared__ int scan[2][2][kMoeMaxExperts];
+  __shared__ int scan[2][3][kMoeMaxExperts];
   __shared__ int begin[kMoeMaxExperts];
   int *counts = ws_at<int>(p, p.at.counts) + threadIdx.x;
   int n = 0;
@@ -177,6 +185,8 @@ __global__ void __launch_bounds__(kListThreads) experts_place_kernel(ExpertsProb
   place_pairs<kListThreads>(p, begin, count, from, to, pairs);
 }
 
+}  // namespace
+
 hipError_t launch_list(const ExpertsProblem &p, hipStream_t s) {
   if ((long long)p.T * p.top <= kOneGroup)
     return launch_kernel(experts_list_kernel, dim3(1), dim3(kOneThreads), s, p);
@@ -187,6 +197,8 @@ hipError_t launch_list(const ExpertsProblem &p, hipStream_t s) {
   if (e != hipSuccess) return e;
   return launch_kernel(experts_place_kernel, groups, dim3(kListThreads), s, p);
 }
+
+namespace {
 
 // ---- sums over a token's pairs --------------------------------------------------
 

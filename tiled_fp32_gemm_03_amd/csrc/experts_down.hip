@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(T::THREADS, 2) experts_dx_kernel(ExpertsProble
 }  // namespace
 
 hipError_t launch_experts_down(const ExpertsProblem &p, hipStream_t s) {
-  return choose_tiles(p, direct(p.W2, p.ld2, p.I, p.H), by_words(p.W2, p.I),
+  return choose_tiles(p.tile, direct(p.W2, p.ld2, p.I, p.H), by_words(p.W2, p.I),
                       [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
@@ -133,7 +133,7 @@ hipError_t launch_experts_down(const ExpertsProblem &p, hipStream_t s) {
 }
 
 hipError_t launch_experts_dx(const ExpertsProblem &p, hipStream_t s) {
-  return choose_tiles(p, direct(p.W1, p.ld1, p.H, kStepK), by_words(p.W1, p.H),
+  return choose_tiles(p.tile, direct(p.W1, p.ld1, p.H, kStepK), by_words(p.W1, p.H),
                       [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;

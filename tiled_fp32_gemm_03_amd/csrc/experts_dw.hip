@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(T::THREADS, 2) experts_dw2_kernel(ExpertsProbl
 
 hipError_t launch_experts_dw(const ExpertsProblem &p, hipStream_t s) {
   hipError_t e = hipSuccess;
-  if (p.dW1) e = choose_tiles(p, direct(p.X, p.ldx, p.H, p.T), by_words(p.X, p.H),
+  if (p.dW1) e = choose_tiles(p.tile, direct(p.X, p.ldx, p.H, p.T), by_words(p.X, p.H),
                                     [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
@@ -149,7 +149,7 @@ hipError_t launch_experts_dw(const ExpertsProblem &p, hipStream_t s) {
     return GEMM_F32_LAUNCH_ROWS(experts_dw1_kernel, T, S, tiles);
   });
   if (e != hipSuccess || !p.dW2) return e;
-  return choose_tiles(p, direct(p.dY, p.lddy, p.H, p.T), by_words(p.dY, p.H),
+  return choose_tiles(p.tile, direct(p.dY, p.lddy, p.H, p.T), by_words(p.dY, p.H),
                       [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;

@@ -34,7 +34,13 @@ struct ExpertsProblem {
   long long lddw2;
   unsigned char *ws;
   ExpertsSpace at;
+  // Rows by adapter: pairs with no expert are expert E - 1's, which has no row tiles;
+  // and rows of the product's tiles.
+  int rest, run_tile;
 };
+
+// The order of the pairs by expert, in the workspace.
+hipError_t launch_list(const ExpertsProblem &p, hipStream_t s);
 
 hipError_t launch_experts_forward(const ExpertsProblem &p, hipStream_t s);
 hipError_t launch_experts_backward(const ExpertsProblem &p, hipStream_t s);
@@ -45,5 +51,26 @@ hipError_t launch_experts_down(const ExpertsProblem &p, hipStream_t s);  // u, W
 hipError_t launch_experts_du(const ExpertsProblem &p, hipStream_t s);    // dY, W2, saved -> dh, u, dg
 hipError_t launch_experts_dx(const ExpertsProblem &p, hipStream_t s);    // dh, W1 -> part
 hipError_t launch_experts_dw(const ExpertsProblem &p, hipStream_t s);    // dh, X -> dW1; dY, u -> dW2
+
+// A shared projection with adapters (gemm_adapters.h).
+struct AdaptersProblem {
+  int T, N, K, R, count, format;
+  const uint16_t *X;
+  long long ldx;
+  const uint16_t *W;
+  long long ldw;
+  const uint16_t *A;
+  long long lda;
+  const uint16_t *B;
+  long long ldb;
+  const int *ids;
+  const float *scales;  // may be null
+  uint16_t *Y;
+  long long ldy;
+  unsigned char *ws;
+  AdaptersSpace at;
+};
+hipError_t launch_adapters_thin(const AdaptersProblem &p, hipStream_t s);   // T <= kAdaptersThin
+hipError_t launch_adapters_tiles(const AdaptersProblem &p, hipStream_t s);  // more
 
 }  // namespace gemm_f32_impl

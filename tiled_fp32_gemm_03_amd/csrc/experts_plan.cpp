@@ -57,6 +57,53 @@ ExpertsSpace experts_space(int T, int E, int top, int H, int I, int tile, bool b
   w.part = take(2 * pairs * w.hpitch);
   w.dh = backward ? take(4 * pairs * w.ipitch) : at;
   w.dg = backward ? take(4 * pairs * w.slices) : at;
+  w.runs = w.tile_run = at;
+  w.bytes = at;
+  return w;
+}
+
+int adapters_check_sizes(int T, int N, int K, int R, int count) {
+  if (T < 0 || count < 0 || N < 1 || K < 1 || R < 1) return kInvalidDim;
+  if (T > kAdaptersMaxRows || N > kAdaptersMaxWidth || K > kAdaptersMaxWidth ||
+      R > kAdaptersMaxRank || count > kAdaptersMaxCount)
+    return kBadArg;
+  return kOk;
+}
+
+AdaptersSpace adapters_space(int T, int N, int K, int R, int count) {
+  AdaptersSpace w{};
+  long long at = 0;
+  auto take = [&at](long long bytes) {
+    const long long from = at;
+    at += ceil_div(bytes, 256) * 256;
+    return from;
+  };
+  w.rpitch = ceil_div(R, 64) * 64;
+  w.v = take(2 * T * w.rpitch);
+  w.splits = 1;
+  w.chunk = K;
+  if (T > kAdaptersThin) {
+    w.tile = ceil_div(T, 256) * ceil_div(N, 256) >= 192 ? 256 : 128;
+    // The products with A: row tiles of kAdaptersRows, K in parts until there are
+    // two workgroups to a compute unit, of 256 values at least.
+    const long long tiles = (ceil_div(T, kAdaptersRows) + count / 2) * ceil_div(R, kAdaptersRows);
+    while (tiles * w.splits < 512 && ceil_div(K, 2 * w.splits) >= 256) w.splits *= 2;
+    w.chunk = (int)(ceil_div(ceil_div(K, w.splits), 64) * 64);
+    w.splits = (int)ceil_div(K, w.chunk);
+    w.part = take(4LL * w.splits * T * w.rpitch);
+    const int E = count + 1;
+    ExpertsSpace &o = w.order;
+    o.most_tiles = T / kAdaptersRows + (E < T ? E : T);
+    o.list_groups = ceil_div(T, kListPairs);
+    o.start = take(4LL * (E + 1));
+    o.tiles = take(16 + 16 * o.most_tiles);
+    o.list = take(4LL * T);
+    o.token = take(4LL * T);
+    o.where = take(4LL * T);
+    o.counts = take(4 * o.list_groups * E);
+    o.runs = take(16 + 16LL * (E < T ? E : T));
+    o.tile_run = take(4 * ceil_div(T, w.tile));
+  }
   w.bytes = at;
   return w;
 }

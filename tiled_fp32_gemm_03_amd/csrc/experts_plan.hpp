@@ -36,6 +36,11 @@ struct ExpertsSpace {
   long long part;    // 16 bits [T top][hpitch], by pair: what the pair adds to its token
   long long dh;      // 16 bits [T top][2 ipitch], by place: gradient of the first product
   long long dg;      // float [slices][T top], by place: parts of the gates' gradients
+  // Of rows by adapter alone: the runs of one adapter (or none) that there are, as
+  // `tiles` has the row tiles, and the number of the run in which each row tile of
+  // the product begins.
+  long long runs;
+  long long tile_run;
   long long bytes;
   long long ipitch, hpitch, most_tiles, slices, list_groups;
 };
@@ -49,6 +54,24 @@ int experts_tile(int T, int E, int top, int H, int I);
 
 // ---- adapters (gemm_adapters.h) -----------------------------------------------
 
-constexpr int kAdaptersMaxRows = 1 << 24, kAdaptersMaxRank = 512, kAdaptersMaxCount = 1 << 16;
+constexpr int kAdaptersMaxRows = 1 << 22, kAdaptersMaxWidth = 1 << 17, kAdaptersMaxRank = 512,
+              kAdaptersMaxCount = 511;
+// Up to this many rows: thin products, which read W once; and the rows of a tile of
+// the products with A.
+constexpr int kAdaptersThin = 64, kAdaptersRows = 64;
+int adapters_check_sizes(int T, int N, int K, int R, int count);
+
+// Rows by adapter: as pairs by expert (ExpertsSpace), with the rows without one as
+// the last of count + 1.
+struct AdaptersSpace {
+  ExpertsSpace order;  // u, part, dh and dg: none
+  long long part;      // float [splits][T][rpitch], by place: A x in parts of K
+  long long v;         // 16 bits [T][rpitch], by place (thin: by row): scale A x
+  long long bytes;
+  long long rpitch;
+  int tile;            // rows and columns of the product's tiles
+  int splits, chunk;   // parts of K, of `chunk` values each
+};
+AdaptersSpace adapters_space(int T, int N, int K, int R, int count);
 
 }  // namespace gemm_f32_impl

@@ -77,8 +77,8 @@ inline bool by_words(const void *p, long long width) {
 }
 
 // KERN on at most `tiles` tiles: as many workgroups as the chip holds at once.
-template <auto KERN, int THREADS>
-hipError_t launch_tiles(const ExpertsProblem &p, long long tiles, hipStream_t s) {
+template <auto KERN, int THREADS, class P>
+hipError_t launch_tiles(const P &p, long long tiles, hipStream_t s) {
   if (tiles <= 0) return hipSuccess;
   const long long most = resident_workgroups<KERN, THREADS>();
   return launch_kernel(KERN, dim3((unsigned)(tiles < most ? tiles : most)), dim3(THREADS),
@@ -97,9 +97,9 @@ static_assert(Large::WGN == 2 && Small::WGN == 2, "slices of ExpertsSpace");
 // `make(tile, integral_constant S)` launches.  Large tiles are loaded directly
 // alone (through registers a wave of 128 x 128 has none left for its loads).
 template <class Make>
-hipError_t choose_tiles(const ExpertsProblem &p, bool direct_loads, bool words, Make make) {
+hipError_t choose_tiles(int tile, bool direct_loads, bool words, Make make) {
   if (direct_loads) {
-    if (p.tile == Large::BM) return make(Large{}, std::integral_constant<int, kDirect>{});
+    if (tile == Large::BM) return make(Large{}, std::integral_constant<int, kDirect>{});
     return make(Small{}, std::integral_constant<int, kDirect>{});
   }
   if (words) return make(Small{}, std::integral_constant<int, kByWords>{});

@@ -124,8 +124,15 @@ struct KcSide {
     }
   }
   __device__ __forceinline__ void begin(int kk) {
+    turn(kk);
+    seal();
+  }
+  // In two parts, for steps that may be of different rows.
+  __device__ __forceinline__ void turn(int kk) {
     step = kk;
     left = K - kStepK * (kk >= half ? kk - half : kk);  // values from the step's first on
+  }
+  __device__ __forceinline__ void seal() {
     if constexpr (S == kDirect) rsrc = buffer_of(base, records);
   }
   __device__ __forceinline__ void issue(int q, unsigned stage, int wave) {

@@ -1,8 +1,9 @@
-// C-ABI front end of routing (gemm_route.h) and the experts' products
-// (gemm_experts.h): argument checks, in the order sizes, row pitches, formats,
+// C-ABI front end of routing (gemm_route.h), the experts' products
+// (gemm_experts.h) and adapters (gemm_adapters.h): argument checks, in the order sizes, row pitches, formats,
 // pointers, workspace, then the launches.  Every error is returned before
 // anything is enqueued.
 #include "experts_internal.hpp"
+#include "gemm_adapters.h"
 #include "gemm_experts.h"
 #include "gemm_f32.h"
 #include "gemm_internal.hpp"
@@ -23,6 +24,11 @@ static_assert(kRouteMaxTokens == GEMM_ROUTE_MAX_TOKENS && kRouteMaxExperts == GE
 static_assert(kExpertsMaxTokens == GEMM_EXPERTS_MAX_TOKENS &&
                   kExpertsMaxWidth == GEMM_EXPERTS_MAX_WIDTH,
               "bounds of experts_plan.hpp and gemm_experts.h differ");
+static_assert(kAdaptersMaxRows == GEMM_ADAPTERS_MAX_ROWS &&
+                  kAdaptersMaxWidth == GEMM_ADAPTERS_MAX_WIDTH &&
+                  kAdaptersMaxRank == GEMM_ADAPTERS_MAX_RANK &&
+                  kAdaptersMaxCount == GEMM_ADAPTERS_MAX_COUNT,
+              "bounds of experts_plan.hpp and gemm_adapters.h differ");
 
 namespace {
 
@@ -197,4 +203,40 @@ extern "C" int gemm_experts_backward(int T, int E, int top, int H, int I, const 
   p.at = experts_space(T, E, top, H, I, p.tile, true);
   return launch_status(launch_experts_backward(p, static_cast<hipStream_t>(stream)),
                        "experts backward");
+}
+
+// ---- adapters ----------------------------------------------------------------------
+
+extern "C" long long gemm_adapters_workspace_bytes(int T, int N, int K, int R, int count) {
+  return adapters_check_sizes(T, N, K, R, count) == kOk ? adapters_space(T, N, K, R, count).bytes
+                                                        : -1;
+}
+
+extern "C" int gemm_adapters(int T, int N, int K, int R, int count, const void *X, int ldx,
+                             const void *W, int ldw, const void *A, int lda, const void *B, int ldb,
+                             const int *ids, const float *scales, int format, void *Y, int ldy,
+                             void *workspace, long long workspace_bytes, void *stream) {
+  int rc = adapters_check_sizes(T, N, K, R, count);
+  if (rc != kOk) return rc;
+  if (!is_16(format)) return kBadArg;
+  if (ldx < K || ldw < K || ldy < N || (count > 0 && (lda < K || ldb < R))) return kInvalidLd;
+  if (T == 0) return kOk;
+  rc = check_plain_pointer(X, format);
+  if (rc == kOk) rc = check_plain_pointer(W, format);
+  if (rc == kOk && count > 0) rc = check_plain_pointer(A, format);
+  if (rc == kOk && count > 0) rc = check_plain_pointer(B, format);
+  if (rc == kOk) rc = check_words(ids);
+  if (rc == kOk && scales) rc = check_words(scales);
+  if (rc == kOk) rc = check_plain_pointer(Y, format);
+  if (rc != kOk) return rc;
+  const AdaptersSpace at = adapters_space(T, N, K, R, count);
+  if (bad_workspace(workspace, workspace_bytes, at.bytes)) return GEMM_F32_BAD_WORKSPACE;
+  const AdaptersProblem p{T, N, K, R, count, format, static_cast<const uint16_t *>(X), ldx,
+                          static_cast<const uint16_t *>(W), ldw, static_cast<const uint16_t *>(A),
+                          lda, static_cast<const uint16_t *>(B), ldb, ids, scales,
+                          static_cast<uint16_t *>(Y), ldy, static_cast<unsigned char *>(workspace),
+                          at};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return launch_status(T <= kAdaptersThin ? launch_adapters_thin(p, s) : launch_adapters_tiles(p, s),
+                       "adapters");
 }
