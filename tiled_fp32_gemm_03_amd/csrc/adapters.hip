@@ -76,7 +76,7 @@ struct Low {
       const int row = 16 * (T::WGM * i + wm) + l16;
       if (row >= j.rows) continue;
 #pragma unroll
-      for (int m = 0; m < T::TBN; ++m)  // rpitch: whole tiles; zeros from R on
+      for (int m = 0; m < T::TBN; ++m)  // rpitch: whole tiles
         *reinterpret_cast<f32x4 *>(part + (j.first + row) * p.at.rpitch + T::BN * j.tn +
                                    16 * (wn * T::TBN + m) + 4 * g) = acc[i][m];
     }
@@ -105,6 +105,10 @@ __global__ void __launch_bounds__(256) adapters_join_kernel(AdaptersProblem p) {
     sum += *reinterpret_cast<const f32x4 *>(part + s * p.T * p.at.rpitch);
   const int r = p.ids[ws_at<int>(p, p.at.order.list)[place]];
   if (p.scales) sum *= p.scales[r];
+  const int left = p.R - 4 * (int)(i - (long long)place * per);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c >= left) sum[c] = 0.f;
   *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.v) + 4 * i) =
       u32x2{pack2<FMT>(sum[0], sum[1]), pack2<FMT>(sum[2], sum[3])};
 }

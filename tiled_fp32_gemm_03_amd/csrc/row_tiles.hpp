@@ -15,9 +15,9 @@
 // S says how operands come to LDS.  kDirect: by buffer loads straight into it; a
 // lane with nothing to load takes an offset past the buffer's record count.  Needs
 // 16-byte aligned rows, widths of whole 16 bytes and 32-bit offsets.  Else
-// through registers with 64-bit addresses: kByWords: rows that start in the middle
-// of a 4-byte word are read by the words around their values (Eight<kOdd>);
-// kAnyRows: anything.
+// through registers with 64-bit addresses: kByWords: rows that may start in the middle
+// of a 4-byte word, of 8 values at least, in a matrix that starts on one; kAnyRows:
+// anything.
 #pragma once
 
 #include "addr_math16.hpp"
@@ -66,27 +66,54 @@ __device__ inline rsrc_t buffer_of(const void *p, int records) {
                                            0x00020000);
 }
 
-// 8 codes from element k of a row of `width` (zeros past it), on their way.
+// 8 codes on their way through registers, in memory order along the lanes of a row.
+// kByWords: the words around them, from 2 bytes before the first on where that is in
+// the middle of one (the row before, or its padding: only rows after the first can be,
+// because the matrix starts on a word); the last code is the first of the next lane's
+// words, or `last`.  In a step that passes the end of the rows (`tail`, the same for all
+// lanes) the 8 codes that end there at the latest, moved into place when they are put
+// to LDS, each lane with a `last` of its own.
 template <int S>
 struct Chunk {
-  Eight<S == kByWords ? kOdd : kShort> x;
-  long long k;
-  int width;
-  __device__ __forceinline__ void load(const uint16_t *row, long long at, int w) {
-    k = at;
-    width = row ? w : 0;
-    if (width) x.load(reinterpret_cast<const unsigned char *>(row), at, w);
+  u32x4 v;
+  uint32_t last;
+  int shift, drop;
+  // Codes k .. k + 7 of `row`, of which there are `width`; the lane that holds the
+  // row's last chunk of the step ends at `end`.
+  __device__ __forceinline__ void load(const uint16_t *row, int k, int width, int end, bool tail) {
+    if constexpr (S == kByWords) {
+      int from = k, stop = end - 1;
+      if (tail) {  // uniform
+        from = k < width - 8 ? k : width - 8;
+        drop = k - from;
+        stop = from + 7;
+      }
+      const uint16_t *at = row + from;
+      const uintptr_t odd = reinterpret_cast<uintptr_t>(at) & 2;
+      v = *reinterpret_cast<const u32x4w *>(reinterpret_cast<const char *>(at) - odd);
+      last = row[stop];
+      shift = 8 * (int)odd;
+    } else {
+      v = load_guarded(reinterpret_cast<const unsigned char *>(row), k < width ? k : width, width);
+    }
   }
-  __device__ __forceinline__ u32x4 get() const {
-    if (width == 0) return u32x4{0, 0, 0, 0};
-    u32x4 v = x.get();
-    if (k + 8 > width) v = x.end(v, k, width);
-    return v;
+  __device__ __forceinline__ u32x4 get(bool ends, bool tail) const {
+    if constexpr (S != kByWords) return v;
+    const uint32_t next =
+        (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[0], 0x101, 0xf, 0xf, true);  // lane + 1's
+    const uint32_t word = ends || tail ? last : next;
+    u32x4 x{__builtin_amdgcn_alignbit(v[1], v[0], (uint32_t)shift),
+            __builtin_amdgcn_alignbit(v[2], v[1], (uint32_t)shift),
+            __builtin_amdgcn_alignbit(v[3], v[2], (uint32_t)shift),
+            __builtin_amdgcn_alignbit(word, v[3], (uint32_t)shift)};
+    if (tail) x = drop_first(x, drop);
+    return x;
   }
 };
 
 // An operand with k along its rows, W rows of it, loaded by NW waves.  `row(r, q)`: row r's first element,
-// or null; q, the number of the load that brings it, row_of its r.  K values to a row; from step `half` on (for rows of two
+// or null (then nothing that is read of the result depends on it); q, the number of
+// the load that brings it, row_of its r.  K values to a row; from step `half` on (for rows of two
 // parts, each of whole steps and K values) the second part.
 template <int W, int S, int NW>
 struct KcSide {
@@ -120,7 +147,7 @@ struct KcSide {
                           16 * (c0 ^ (4 * (q & 1)))
                     : kOutside;
       else
-        rows[q] = r;
+        rows[q] = r ? r : static_cast<const uint16_t *>(base);
     }
   }
   __device__ __forceinline__ void begin(int kk) {
@@ -139,13 +166,23 @@ struct KcSide {
     const int v = 8 * (c0 ^ (4 * (q & 1))) < left ? voff[q] : kOutside;
     buffer_load_to_lds16(v, rsrc, uniform(2 * kStepK * step), (unsigned)uniform((int)(stage + (kLoads * wave + q) * 1024)));
   }
-  __device__ __forceinline__ void load(int q) {
-    const uint16_t *r = rows[q];
-    if (r) r += (long long)kStepK * step - (K - left);
-    held[q].load(r, K - left + 8 * (c0 ^ (4 * (q & 1))), K);
+  __device__ __forceinline__ bool tail() const { return left < kStepK; }
+  __device__ __forceinline__ void load(int q, int, int lane) {
+    const int k0 = K - left;
+    held[q].load(rows[q] + (kStepK * step - k0), k0 + 8 * (lane & 7), K, k0 + kStepK, tail());
   }
-  __device__ __forceinline__ u32x4 get(int q) const { return held[q].get(); }
+  __device__ __forceinline__ void put(char *st, int q, int wave, int lane) const {
+    *reinterpret_cast<u32x4 *>(st + 16 * m16_a_pos(row_of(q, wave, lane), lane & 7)) =
+        held[q].get((lane & 7) == 7, tail());
+  }
 };
+
+// Chunk c of k row r, to where side_issue's loads would bring it; zeros where it is not `in`.
+template <int W>
+__device__ __forceinline__ void put_down(char *st, int r, int c, u32x4 v, bool in) {
+  *reinterpret_cast<u32x4 *>(st + r * (2 * W) + 32 * m16_b_slot(r, c >> 1) + 16 * (c & 1)) =
+      in ? v : u32x4{0, 0, 0, 0};
+}
 
 // An operand with k down its rows, `width` (at most W) columns of it: n rows from
 // `first` on, ld elements apart.  From step `half` on the second part: n rows
@@ -194,11 +231,15 @@ struct KmSide {
   __device__ __forceinline__ void issue(int q, unsigned stage, int wave) {
     buffer_load_to_lds16(voff[q], rsrc, 0, (unsigned)uniform((int)(stage + (kLoads * wave + q) * 1024)));
   }
+  __device__ __forceinline__ bool tail() const { return left < kStepK || width < W; }
   __device__ __forceinline__ void load(int q, int wave, int lane) {
-    const int r = row_of(q, wave, lane), c = column_of(q, wave, lane);
-    held[q].load(r < left && c < width ? at + r * ld : nullptr, c, width);
+    const int r = row_of(q, wave, lane);  // (width - 8 may be negative: columns before the tile's)
+    held[q].load(at + (r < left ? r : left - 1) * ld, 8 * (lane % kChunks), width, W, tail());
   }
-  __device__ __forceinline__ u32x4 get(int q) const { return held[q].get(); }
+  __device__ __forceinline__ void put(char *st, int q, int wave, int lane) const {
+    const int r = row_of(q, wave, lane);
+    put_down<W>(st, r, lane % kChunks, held[q].get(lane % kChunks == kChunks - 1, tail()), r < left);
+  }
 };
 
 // The same with its rows chosen by a list: row k is row list[k] of `base`.  The list
@@ -247,12 +288,15 @@ struct KmListSide {
     buffer_load_to_lds16(in ? (int)(2 * (now[q] * ld + c)) : kOutside, rsrc, 0,
                          (unsigned)uniform((int)(stage + (kLoads * wave + q) * 1024)));
   }
-  __device__ __forceinline__ void load(int q, int wave, int lane) {
-    const int c = KmSide<W, S, NW>::column_of(q, wave, lane);
-    const bool in = k0 + KmSide<W, S, NW>::row_of(q, wave, lane) < n && c < width;
-    held[q].load(in ? base + now[q] * ld : nullptr, c, width);
+  __device__ __forceinline__ bool tail() const { return k0 + kStepK > n || width < W; }
+  __device__ __forceinline__ void load(int q, int, int lane) {
+    held[q].load(base + now[q] * ld, 8 * (lane % kChunks), width, W, tail());
   }
-  __device__ __forceinline__ u32x4 get(int q) const { return held[q].get(); }
+  __device__ __forceinline__ void put(char *st, int q, int wave, int lane) const {
+    const int r = KmSide<W, S, NW>::row_of(q, wave, lane);
+    put_down<W>(st, r, lane % kChunks, held[q].get(lane % kChunks == kChunks - 1, tail()),
+                k0 + r < n);
+  }
 };
 
 // One set of calls for all sides.
@@ -277,17 +321,6 @@ __device__ __forceinline__ void side_issue(KmListSide<W, S, NW> &x, int q, unsig
                                            int lane) {
   x.issue(q, stage, wave, lane);
 }
-template <int W, int S, int NW>
-__device__ __forceinline__ void side_load(KcSide<W, S, NW> &x, int q, int, int) { x.load(q); }
-template <int W, int S, int NW>
-__device__ __forceinline__ void side_load(KmSide<W, S, NW> &x, int q, int wave, int lane) {
-  x.load(q, wave, lane);
-}
-template <int W, int S, int NW>
-__device__ __forceinline__ void side_load(KmListSide<W, S, NW> &x, int q, int wave, int lane) {
-  x.load(q, wave, lane);
-}
-
 // A lane's operand: block `block` of 16 rows (columns), 32-deep group kg.
 template <bool DOWN, int W>
 __device__ __forceinline__ i16x8 read_operand(const char *st, int block, int kg, int lane) {
@@ -379,18 +412,15 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
   };
   auto load = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < T::A_LOADS; ++q) side_load(op.a, q, wave, lane);
+    for (int q = 0; q < T::A_LOADS; ++q) op.a.load(q, wave, lane);
 #pragma unroll
-    for (int q = 0; q < T::B_LOADS; ++q) side_load(op.b, q, wave, lane);
+    for (int q = 0; q < T::B_LOADS; ++q) op.b.load(q, wave, lane);
   };
   auto put = [&](char *stage) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < T::A_LOADS; ++q)
-      *reinterpret_cast<u32x4 *>(stage + 16 * (64 * (T::A_LOADS * wave + q) + lane)) = op.a.get(q);
+    for (int q = 0; q < T::A_LOADS; ++q) op.a.put(stage, q, wave, lane);
 #pragma unroll
-    for (int q = 0; q < T::B_LOADS; ++q)
-      *reinterpret_cast<u32x4 *>(stage + T::A_BYTES + 16 * (64 * (T::B_LOADS * wave + q) + lane)) =
-          op.b.get(q);
+    for (int q = 0; q < T::B_LOADS; ++q) op.b.put(stage + T::A_BYTES, q, wave, lane);
   };
   int stage = 0;
   // The first step of a job that has one.
@@ -437,7 +467,7 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
         op.fetch(after);
       }
       // One group's operands, or two where there are registers for them.
-      constexpr int kAhead = T::TBM * T::TBN <= 16 ? 1 : 0;
+      constexpr int kAhead = S == kDirect && T::TBM * T::TBN <= 16 ? 1 : 0;
       i16x8 fa[1 + kAhead][T::TBM], fb[1 + kAhead][T::TBN];
       auto read = [&](int kg) __attribute__((always_inline)) {
 #pragma unroll
