@@ -3,8 +3,7 @@
 // adapter that is asked and 16 of its ranks, and the projection, which reads W once,
 // straight into the matrix instructions' operands (mx_thin.hpp), and the asked
 // adapters' B.
-#include "experts_internal.hpp"
-#include "mx_thin.hpp"
+#include "experts_tiles.hpp"
 
 namespace gemm_f32_impl {
 namespace {
@@ -97,10 +96,205 @@ __global__ void __launch_bounds__(64 * kLowWaves) adapters_low_thin_kernel(Adapt
 }
 
 // ---- the projection ----------------------------------------------------------------------
-// RB blocks of 16 rows, in the order of their adapters, by blocks of 16 columns; `ks`
-// waves share a block of columns, taking the pieces of K in turn.  x waits in LDS, the
-// weights of two pieces are on their way while a third is used.
+// Both kernels: RB blocks of 16 rows, in the order of their adapters, by blocks of 16
+// columns; `ks` waves share a block of columns, taking the steps of K in turn.
+
+// The rows in the order of their adapters, those without one first, and the adapters.
+__device__ inline void order_rows(const AdaptersProblem &p, int (&order)[64], int (&ids)[64]) {
+  if (wave_id() != 0) return;
+  const int lane = threadIdx.x & 63, id = adapter_of(p, lane);
+  int at = 0;
+  for (int i = 0; i < p.T; ++i) {
+    const int o = __builtin_amdgcn_readlane(id, i);
+    at += o < id || (o == id && i < lane);
+  }
+  if (lane < p.T) order[at] = lane, ids[at] = id;
+  else order[lane] = 0, ids[lane] = -1;
+}
+
+// Adds B[r] v, four of a block's adapters at a time, whose B is asked for together; the
+// waves that share columns take them in turn.  Each sum is kept by its own rows alone:
+// an infinity in one request's B is none of the others'.
+template <int FMT, int RB>
+__device__ __forceinline__ void add_adapters(const AdaptersProblem &p, const int (&order)[64],
+                                             const int (&ids)[64], int columns, int ks, int first,
+                                             f32x4 (&acc)[RB]) {
+  constexpr int kBatch = 4;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int n = columns + l16 < p.N ? columns + l16 : p.N - 1;
+  const unsigned char *m = bytes_of(p.B + (long long)n * p.ldb);
+  const long long each = 2LL * p.N * p.ldb;  // bytes of an adapter's B
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int id = ids[16 * b + l16];
+    const uint16_t *v = ws_at<uint16_t>(p, p.at.v) + order[16 * b + l16] * p.at.rpitch;
+    const unsigned any = (unsigned)__ballot(id >= 0) & 0xffffu;
+    if (any == 0) continue;  // uniform
+#pragma unroll 1
+    for (int r0 = 0; r0 < p.R; r0 += 64) {
+      const bool two = r0 + 32 < p.R;  // uniform
+      u32x4 xv[2] = {};
+      if (id >= 0) {
+        xv[0] = *reinterpret_cast<const u32x4 *>(v + r0 + 8 * g);
+        if (two) xv[1] = *reinterpret_cast<const u32x4 *>(v + r0 + 32 + 8 * g);
+      }
+      unsigned left = any;
+      int item = 0;
+      while (left) {  // uniform
+        int e[kBatch];
+        u32x4 bv[kBatch][2];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          e[q] = -1;
+          while (left && e[q] < 0) {
+            const int o = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+            left &= ~(unsigned)__ballot(id == o);
+            if (item++ % ks == first) e[q] = o;
+          }
+          const unsigned char *row = m + (e[q] < 0 ? 0 : e[q]) * each;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = r0 + 32 * h + 8 * g;
+            if (e[q] >= 0 && (h == 0 || two))  // uniform
+              bv[q][h] = load_guarded(row, r < p.R ? r : p.R, p.R);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          if (e[q] < 0) break;  // uniform
+          f32x4 sum = mfma_16<FMT>(bv[q][0], xv[0], f32x4{0, 0, 0, 0});
+          if (two) sum = mfma_16<FMT>(bv[q][1], xv[1], sum);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[b][c] += id == e[q] ? sum[c] : 0.f;
+        }
+      }
+    }
+  }
+}
+
+// The sums of the waves that share columns, added in wave order, and stored.
+template <int FMT, int RB>
+__device__ __forceinline__ void store_rows(const AdaptersProblem &p, unsigned char *lds,
+                                           const int (&order)[64], int columns, int ks, int first,
+                                           f32x4 (&acc)[RB]) {
+  const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
+  if (ks > 1) {
+    f32x4 *part = reinterpret_cast<f32x4 *>(lds);
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < RB; ++b) part[(wave * RB + b) * 64 + lane] = acc[b];
+    __syncthreads();
+    if (first != 0) return;
+    for (int o = 1; o < ks; ++o)
+#pragma unroll
+      for (int b = 0; b < RB; ++b) acc[b] += part[((wave + o) * RB + b) * 64 + lane];
+  }
+  const int c0 = columns + 4 * g;
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+    if (16 * b + l16 < p.T)
+      store4<FMT>(p.Y, order[16 * b + l16] * p.ldy + c0, p.N - c0, acc[b]);
+}
+
 constexpr int kThinWaves = 4, kThinThreads = 64 * kThinWaves;
+
+// ---- rows of whole 16 bytes ----------------------------------------------------------------
+// A round is a 64-deep step for each of the KS waves of a block of columns: x's rows and W's
+// of the workgroup's 64 / KS columns come straight into one of STAGES stages, those of
+// the STAGES - 1 rounds ahead on their way.  Every wave asks for as many loads each
+// round, so that their number tells which have come.
+template <int RB, int KS>
+struct Rounds {
+  static constexpr int X = RB * 2048, W = 2048;      // bytes of a wave's step
+  static constexpr int STAGE = KS * X + kThinWaves * W;
+  static constexpr int STAGES = 150 * 1024 / STAGE < 8 ? 150 * 1024 / STAGE : 8;
+  static constexpr int X_LOADS = (2 * RB * KS + kThinWaves - 1) / kThinWaves;  // a wave's, 1 KB each
+  static constexpr int LOADS = X_LOADS + 2;
+  static constexpr int LDS = STAGES * STAGE;
+  static_assert(STAGES >= 3 && LOADS * (STAGES - 2) < 64, "loads that can be counted");
+  static_assert(kThinWaves * RB * 1024 <= LDS, "the waves' sums");
+};
+
+template <int FMT, int RB, int KS>
+__global__ void __launch_bounds__(kThinThreads) adapters_rounds_kernel(AdaptersProblem p) {
+  typedef Rounds<RB, KS> R;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[R::LDS];
+  __shared__ int order[64], ids[64];
+  const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t *)lds;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  order_rows(p, order, ids);
+  const int first = wave % KS;
+  const int columns = 16 * ((int)blockIdx.x * (kThinWaves / KS) + wave / KS);
+  const rsrc_t xs = buffer_of(p.X, records_of(2 * ((p.T - 1) * p.ldx + p.K)));
+  const uint16_t *w0 = p.W + (long long)columns * p.ldw;
+  const int have = p.N - columns < 16 ? p.N - columns : 16;  // columns, or none
+  const rsrc_t ws = buffer_of(have > 0 ? w0 : p.W,
+                              have > 0 ? records_of(2 * ((have - 1) * p.ldw + p.K)) : 0);
+  // A load brings 8 rows of 8 chunks: row l / 8, chunk c0 of even loads (m16_a_pos).
+  const int c0 = (lane & 7) ^ (lane >> 4);
+  int wv[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) wv[h] = (int)(2 * (8 * h + (lane >> 3)) * p.ldw) + 16 * (c0 ^ (4 * h));
+  __syncthreads();
+  // x's loads are dealt to the waves, some twice where they do not come out even.
+  int xv[R::X_LOADS], part[R::X_LOADS], place[R::X_LOADS];
+#pragma unroll
+  for (int q = 0; q < R::X_LOADS; ++q) {
+    const int i = (wave + kThinWaves * q) % (2 * RB * KS), in = i % (2 * RB);
+    const int r = 8 * in + (lane >> 3);
+    part[q] = i / (2 * RB);
+    place[q] = part[q] * R::X + in * 1024;
+    xv[q] = r < p.T ? (int)(2 * order[r] * p.ldx) + 16 * (c0 ^ (4 * (in & 1))) : kOutside;
+  }
+  const int steps = (p.K + kStepK - 1) / kStepK, rounds = (steps + KS - 1) / KS;
+  auto issue = [&](int round, int stage) __attribute__((always_inline)) {
+    const unsigned to = lds_u + stage * R::STAGE;
+#pragma unroll
+    for (int q = 0; q < R::X_LOADS; ++q) {
+      const int k0 = kStepK * (round * KS + part[q]);
+      const int i = (wave + kThinWaves * q) % (2 * RB * KS);
+      const bool in = k0 + 8 * (c0 ^ (4 * (i & 1))) < p.K;
+      buffer_load_to_lds16(in ? xv[q] : kOutside, xs, uniform(2 * k0),
+                           (unsigned)uniform((int)(to + place[q])));
+    }
+    const int k0 = kStepK * (round * KS + first);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = k0 + 8 * (c0 ^ (4 * h)) < p.K;
+      buffer_load_to_lds16(in ? wv[h] : kOutside, ws, uniform(2 * k0),
+                           (unsigned)uniform((int)(to + KS * R::X + wave * R::W + h * 1024)));
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < R::STAGES - 1; ++i) issue(i, i);
+  f32x4 acc[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) acc[b] = f32x4{0, 0, 0, 0};
+  int stage = 0, ahead = R::STAGES - 1;
+#pragma unroll 1
+  for (int i = 0; i < rounds; ++i) {
+    __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(R::LOADS * (R::STAGES - 2)));  // round i's, own
+    ks_lds_barrier();  // everyone's; the stage of round i - 1 is free
+    issue(i + R::STAGES - 1, ahead);  // past the end: zeros
+    const char *st = reinterpret_cast<const char *>(lds) + stage * R::STAGE;
+#pragma unroll
+    for (int kg = 0; kg < 2; ++kg) {
+      const i16x8 wf = read_operand<false, 16>(st + KS * R::X + wave * R::W, 0, kg, lane);
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        acc[b] = mfma_rows<FMT>(wf, read_operand<false, 16>(st + first * R::X, b, kg, lane), acc[b]);
+    }
+    stage = stage + 1 == R::STAGES ? 0 : stage + 1;
+    ahead = ahead + 1 == R::STAGES ? 0 : ahead + 1;
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(0));
+  add_adapters<FMT, RB>(p, order, ids, columns, KS, first, acc);
+  store_rows<FMT, RB>(p, lds, order, columns, KS, first, acc);
+}
+
+// ---- any rows ----------------------------------------------------------------------------------
+// x waits in LDS, the weights of two pieces of 128 values are on their way while a third
+// is used.
 constexpr int kThinLds = 74 * 1024;  // of x: two workgroups to a compute unit
 
 template <int FMT, int RB, int ROWS>
@@ -109,17 +303,7 @@ __global__ void __launch_bounds__(kThinThreads, 2) adapters_thin_kernel(Adapters
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ int order[64], ids[64];  // rows, and their adapters
   const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
-  // Rows by adapter, those without one first.
-  if (wave == 0) {
-    const int id = adapter_of(p, lane);
-    int at = 0;
-    for (int i = 0; i < p.T; ++i) {
-      const int o = __builtin_amdgcn_readlane(id, i);
-      at += o < id || (o == id && i < lane);
-    }
-    if (lane < p.T) order[at] = lane, ids[at] = id;
-    else order[lane] = 0, ids[lane] = -1;
-  }
+  order_rows(p, order, ids);
   __syncthreads();
   const int first = wave & (ks - 1);
   const int columns = 16 * ((int)blockIdx.x * (kThinWaves / ks) + wave / ks);
@@ -175,50 +359,8 @@ __global__ void __launch_bounds__(kThinThreads, 2) adapters_thin_kernel(Adapters
       }
     }
   }
-  // B[r] v, a run of rows with one adapter after the other; the waves that share
-  // columns take them in turn.  Each sum is kept by its own rows alone: an infinity
-  // in one request's B is none of the others'.
-  const int n = columns + l16 < p.N ? columns + l16 : p.N - 1;
-  int item = 0;
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int id = ids[16 * b + l16];
-    const uint16_t *v = ws_at<uint16_t>(p, p.at.v) + order[16 * b + l16] * p.at.rpitch;
-    unsigned left = (unsigned)__ballot(id >= 0) & 0xffffu;
-    while (left) {  // uniform
-      const int e = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-      left &= ~(unsigned)__ballot(id == e);
-      if (item++ % ks != first) continue;
-      const unsigned char *m = bytes_of(p.B + ((long long)p.N * e + n) * p.ldb);
-      f32x4 sum{0, 0, 0, 0};
-#pragma unroll 2
-      for (int r0 = 0; r0 < p.R; r0 += 32) {
-        const int r = r0 + 8 * g;
-        const u32x4 bv = load_guarded(m, r < p.R ? r : p.R, p.R);
-        u32x4 xv{0, 0, 0, 0};
-        if (id == e) xv = *reinterpret_cast<const u32x4 *>(v + r);
-        sum = mfma_16<FMT>(bv, xv, sum);
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[b][c] += id == e ? sum[c] : 0.f;
-    }
-  }
-  if (ks > 1) {  // the waves' sums, added in wave order
-    f32x4 *part = reinterpret_cast<f32x4 *>(lds);
-    __syncthreads();
-#pragma unroll
-    for (int b = 0; b < RB; ++b) part[(wave * RB + b) * 64 + lane] = acc[b];
-    __syncthreads();
-    if (first != 0) return;
-    for (int o = 1; o < ks; ++o)
-#pragma unroll
-      for (int b = 0; b < RB; ++b) acc[b] += part[((wave + o) * RB + b) * 64 + lane];
-  }
-  const int c0 = columns + 4 * g;
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-    if (16 * b + l16 < p.T)
-      store4<FMT>(p.Y, order[16 * b + l16] * p.ldy + c0, p.N - c0, acc[b]);
+  add_adapters<FMT, RB>(p, order, ids, columns, ks, first, acc);
+  store_rows<FMT, RB>(p, lds, order, columns, ks, first, acc);
 }
 
 template <int FMT, int RB, int ROWS>
@@ -238,6 +380,20 @@ hipError_t launch_thin(const AdaptersProblem &p, hipStream_t s) {
                          dim3((unsigned)ceil_div(groups, kThinWaves / ks)), dim3(kThinThreads), args,
                          (size_t)lds, s);
 }
+template <int FMT, int RB, int KS>
+hipError_t launch_rounds(const AdaptersProblem &p, hipStream_t s) {
+  return launch_kernel(adapters_rounds_kernel<FMT, RB, KS>,
+                       dim3((unsigned)ceil_div(p.N, 16 * kThinWaves / KS)), dim3(kThinThreads), s, p);
+}
+// Waves to a block of columns: until there is a workgroup to each compute unit.
+template <int FMT, int RB>
+hipError_t launch_direct(const AdaptersProblem &p, hipStream_t s) {
+  const long long groups = ceil_div(p.N, 16);
+  if (groups >= 4 * 256) return launch_rounds<FMT, RB, 1>(p, s);
+  if (groups >= 2 * 256) return launch_rounds<FMT, RB, 2>(p, s);
+  return launch_rounds<FMT, RB, 4>(p, s);
+}
+
 template <int FMT, int ROWS>
 hipError_t launch_both(const AdaptersProblem &p, hipStream_t s) {
   if (p.count > 0) {
@@ -246,6 +402,10 @@ hipError_t launch_both(const AdaptersProblem &p, hipStream_t s) {
         launch_kernel(adapters_low_thin_kernel<FMT, ROWS>,
                       dim3((unsigned)p.T, (unsigned)(2 * ceil_div(p.R, 32))), dim3(64 * kLowWaves), s, p);
     if (e != hipSuccess) return e;
+  }
+  if (direct(p.X, p.ldx, p.K, p.T) && direct(p.W, p.ldw, p.K, 16)) {
+    if (p.T <= 16) return launch_direct<FMT, 1>(p, s);
+    return p.T <= 32 ? launch_direct<FMT, 2>(p, s) : launch_direct<FMT, 4>(p, s);
   }
   if (p.T <= 16) return launch_thin<FMT, 1, ROWS>(p, s);
   if (p.T <= 32) return launch_thin<FMT, 2, ROWS>(p, s);
