@@ -12,11 +12,12 @@ namespace {
 
 // ---- the order of the pairs ----------------------------------------------------
 // A stable sort by expert: counts, their sums, then each pair's place.  Up to
-// kOneGroup pairs by one workgroup; more in three launches, kListPairs to a
-// workgroup.  Pairs whose expert is not in 0 .. E - 1 get no place.
+// kOneLaunch pairs in one launch, whose workgroups each count all pairs, and take
+// kListPairs of them; more in three launches (16,384 pairs, 64 experts: 8.3 us
+// against 15.3 in three).  Pairs whose expert is not in 0 .. E - 1 get no place.
 
 constexpr int kMostGroups = 1 << 20;
-constexpr int kOneGroup = 8192, kOneThreads = 1024, kListThreads = 256;
+constexpr int kOneLaunch = 1 << 16, kOneThreads = kListPairs, kListThreads = 256;
 
 __device__ inline int expert_of(const ExpertsProblem &p, long long pair, long long pairs) {
   if (pair >= pairs) return kMoeMaxExperts;  // none
@@ -50,8 +51,9 @@ __device__ inline void count_pairs(const ExpertsProblem &p, int *count, long lon
 
 // Where each expert's places begin, and the row tiles, from the experts' counts
 // `n` of the first kMoeMaxExperts threads.  On return begin[e] is expert e's first place.
+// `writes`: into the workspace too.
 __device__ inline void lay_out(const ExpertsProblem &p, int n, int (*scan)[3][kMoeMaxExperts],
-                               int *begin) {
+                               int *begin, bool writes = true) {
   const int e = threadIdx.x;
   const bool in = e < kMoeMaxExperts;
   const int tiles = p.rest && e == p.E - 1 ? 0 : (n + p.tile - 1) / p.tile;
@@ -67,10 +69,10 @@ __device__ inline void lay_out(const ExpertsProblem &p, int n, int (*scan)[3][kM
     from ^= 1;
     __syncthreads();
   }
-  if (in && e < p.E) {
+  if (in && e < p.E) begin[e] = scan[from][0][e] - n;
+  if (writes && in && e < p.E) {
     const int last = scan[from][0][e], first = last - n;
     int *start = ws_at<int>(p, p.at.start), *table = ws_at<int>(p, p.at.tiles);
-    begin[e] = first;
     start[e] = first;
     const int t0 = scan[from][1][e] - tiles;
     for (int t = 0; t < tiles; ++t) {
@@ -132,16 +134,38 @@ __device__ inline void place_pairs(const ExpertsProblem &p, int *begin,
   }
 }
 
+// Counts are kept in kCopies, by lane, so that a wave's pairs of one expert do not
+// wait for one another.
+constexpr int kCopies = 8;
 __global__ void __launch_bounds__(kOneThreads) experts_list_kernel(ExpertsProblem p) {
   __shared__ int scan[2][3][kMoeMaxExperts];
   __shared__ int begin[kMoeMaxExperts];
+  __shared__ int counts[2][kCopies][kMoeMaxExperts];  // of the pairs before this workgroup's; of the others
   __shared__ unsigned short count[kOneThreads / 64][kMoeMaxExperts];
-  const long long pairs = (long long)p.T * p.top;
-  count_pairs<kOneThreads>(p, begin, 0, pairs, pairs);
-  const int n = (int)threadIdx.x < p.E ? begin[threadIdx.x] : 0;
+  const int pairs = p.T * p.top, from = kListPairs * (int)blockIdx.x;
+  const int copy = threadIdx.x & (kCopies - 1);
+  for (int i = threadIdx.x; i < 2 * kCopies * kMoeMaxExperts; i += kOneThreads)
+    counts[0][0][i] = 0;
   __syncthreads();
-  lay_out(p, n, scan, begin);
-  place_pairs<kOneThreads>(p, begin, count, 0, pairs, pairs);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < pairs; i += kOneThreads) {
+    const int e = expert_of(p, i, pairs);
+    if (e < p.E) atomicAdd(&counts[i >= from][copy][e], 1);
+  }
+  __syncthreads();
+  int before = 0, n = 0;
+  if ((int)threadIdx.x < p.E)
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      before += counts[0][c][threadIdx.x];
+      n += counts[1][c][threadIdx.x];
+    }
+  n += before;
+  lay_out(p, n, scan, begin, blockIdx.x == 0);
+  if ((int)threadIdx.x < p.E) begin[threadIdx.x] += before;
+  __syncthreads();
+  place_pairs<kOneThreads>(p, begin, count, from, from + kListPairs < pairs ? from + kListPairs : pairs,
+                           pairs);
 }
 
 __global__ void __launch_bounds__(kListThreads) experts_count_kernel(ExpertsProblem p) {
@@ -188,9 +212,9 @@ __global__ void __launch_bounds__(kListThreads) experts_place_kernel(ExpertsProb
 }  // namespace
 
 hipError_t launch_list(const ExpertsProblem &p, hipStream_t s) {
-  if ((long long)p.T * p.top <= kOneGroup)
-    return launch_kernel(experts_list_kernel, dim3(1), dim3(kOneThreads), s, p);
-  const dim3 groups((unsigned)p.at.list_groups);
+  const dim3 groups((unsigned)(p.at.list_groups > 0 ? p.at.list_groups : 1));
+  if ((long long)p.T * p.top <= kOneLaunch)
+    return launch_kernel(experts_list_kernel, groups, dim3(kOneThreads), s, p);
   hipError_t e = launch_kernel(experts_count_kernel, groups, dim3(kListThreads), s, p);
   if (e != hipSuccess) return e;
   e = launch_kernel(experts_scan_kernel, dim3(1), dim3(kMoeMaxExperts), s, p);
