@@ -216,3 +216,72 @@ def test_pitch_and_no_tokens(g):
     ids, gates = g.moe_route(big[:0, 3:20], 4)
     assert ids.shape == (0, 4) and gates.shape == (0, 4)
     assert g.moe_route_backward(gates, big[:0, 3:20], ids).shape == (0, 17)
+
+
+# ---- many tokens: several to a wave ---------------------------------------------------------
+
+MANY = [(2049, 63, 6, 1, 1), (2048, 16, 2, 4, 2), (4097, 5, 5, 1, 1), (10241, 256, 8, 8, 4), (5500, 128, 8, 16, 3),
+        (2100, 512, 16, 2, 1), (4444, 100, 10, 10, 2), (4050, 64, 4, 32, 4), (2060, 30, 3, 15, 14), (3001, 256, 8, 8, 4)]
+
+
+def _route_many(z, top, score, bias, groups, keep, by, renorm):
+    """`route` without its loop over tokens."""
+    T, E = z.shape
+    s = _scores(z, score)
+    masked = np.isneginf(z)
+    by_score = bias is not None or (keep < groups and by == "top2")
+    key = np.where(masked, -1e300, s + (bias if bias is not None else 0.0) if by_score else z)
+    if keep < groups:
+        part = -np.sort(-key.reshape(T, groups, -1), axis=2)
+        total = part[:, :, 0].copy()
+        if by == "top2" and part.shape[2] > 1:
+            total += np.where(part[:, :, 1] > -1e300, part[:, :, 1], 0.0)
+        kept = np.argsort(-total, axis=1, kind="stable")[:, :keep]
+        allowed = np.zeros((T, groups), bool)
+        np.put_along_axis(allowed, kept, True, 1)
+        key = np.where(np.repeat(allowed, E // groups, 1), key, -np.inf)
+    ids = np.argsort(-key, axis=1, kind="stable")[:, :top]
+    gates = np.where(np.take_along_axis(masked, ids, 1), 0.0, np.take_along_axis(s, ids, 1))
+    if renorm:
+        if score == "softmax":
+            zc = np.take_along_axis(z, ids, 1)
+            m = zc.max(axis=1, keepdims=True)
+            gates = np.where(np.isneginf(zc), 0.0, np.exp(zc - np.where(np.isfinite(m), m, 0.0)))
+        total = gates.sum(axis=1, keepdims=True)
+        gates = gates / np.where(total > 0, total, 1.0)
+    return ids, gates
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("case", MANY)
+def test_route_many_tokens(g, case, score):
+    T, E, top, groups, keep = case
+    print(f"case: route many {case} {score}", flush=True)
+    rng = np.random.default_rng(sum(case) + 7)
+    dev = torch.device("cuda:0")
+    for fmt, ties, mask in (("f32", False, 0.0), ("bf16", True, 0.3), ("f16", False, 0.6)):
+        t, z = _logits(rng, T, E, fmt, ties, mask)
+        z[5], z[T - 1] = -np.inf, -np.inf
+        t = torch.from_numpy(z.astype(np.float32)).to(DT[fmt])
+        for bias in (None, np.round(rng.standard_normal(E) * 4).astype(np.float32) / 8):
+            for by in ("max", "top2") if groups > 1 else ("max",):
+                for renorm in (False, True):
+                    ids, gates = _route_many(z, top, score, bias, groups, keep, by, renorm)
+                    gi, gg = g.moe_route(t.to(dev), top, score=score, bias=None if bias is None else torch.from_numpy(bias).to(dev),
+                                         groups=groups, top_groups=keep, group_score=by, renormalize=renorm)
+                    what = (case, score, fmt, bias is not None, by, renorm)
+                    assert np.array_equal(gi.cpu().numpy(), ids), what
+                    assert (np.abs(gg.double().cpu().numpy() - gates) <= 2.0 ** -23 * gates).all(), what
+
+
+def test_many_tokens_with_nan_and_infinities(g):
+    """The same rows as a few tokens give."""
+    dev = torch.device("cuda:0")
+    inf, nan = float("inf"), float("nan")
+    few = torch.tensor([[0.0, inf, 1.0, inf, -2.0], [nan, 0.0, 1.0, -inf, 0.5], [-inf] * 5, [nan] * 5, [3.0, 2.0, nan, -inf, 1.0]], device=dev)
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            want = g.moe_route(few, 3, score=score, renormalize=renorm)
+            got = g.moe_route(few.repeat(500, 1), 3, score=score, renormalize=renorm)
+            assert torch.equal(got[0], want[0].repeat(500, 1))
+            assert torch.equal(got[1].nan_to_num(-1.0), want[1].repeat(500, 1).nan_to_num(-1.0))
