@@ -153,3 +153,42 @@ def test_strides(g, T):
 def test_no_rows(g):
     x, w, a, b, ids, s = _make(4, 16, 32, 8, 2, torch.bfloat16)
     assert g.matmul_adapters(x[:0], w, a, b, ids[:0], s).shape == (0, 16)
+
+
+# more rows than thin products take: tiles, with K whole and in parts, and rows of every alignment
+TILES = [(513, 9, 7, 5, 4), (520, 70, 64, 8, 3), (530, 100, 2049, 17, 8), (600, 130, 4096, 16, 5), (700, 264, 520, 16, 64),
+         (560, 129, 333, 40, 9), (900, 300, 1026, 100, 511), (1300, 520, 2056, 24, 12), (300, 4100, 4104, 32, 9), (200, 4095, 3001, 9, 30)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+@pytest.mark.parametrize("case", TILES)
+def test_tiles(g, case, fmt):
+    print(f"case: adapters tiles {case} {fmt}", flush=True)
+    args = _make(*case, DT[fmt])
+    check(g.matmul_adapters(*args), reference(*args), (case, fmt))
+
+
+@pytest.mark.parametrize("K", [136, 1032])
+def test_strides_of_tiles(g, K):
+    for off, pad in ((0, 8), (8, 16), (1, 2), (2, 2)):
+        print(f"case: adapters strides of tiles {K} {off} {pad}", flush=True)
+        x, w, a, b, ids, s = _make(600, 120, K, 24, 3, torch.float16)
+
+        def wide(t):
+            big = torch.full((*t.shape[:-1], t.shape[-1] + off + pad), float("nan"), dtype=t.dtype, device=t.device)
+            v = big[..., off:off + t.shape[-1]]
+            v.copy_(t)
+            return v
+
+        out = torch.full((601, 120 + pad), 5.0, dtype=x.dtype, device=x.device)
+        y = g.matmul_adapters(wide(x), wide(w), wide(a), wide(b), ids, s, out=out[:600, :120])
+        check(y, reference(x, w, a, b, ids, s), (K, off))
+        assert (out[:, 120:] == 5).all() and (out[600] == 5).all()
+
+
+@pytest.mark.parametrize("case", [(70, 24, 72, 8, 3), (200, 300, 1000, 17, 40), (512, 250, 257, 33, 100)])
+def test_thin_products_of_more_than_64_rows(g, case):
+    print(f"case: adapters thin {case}", flush=True)
+    for dtype in DT.values():
+        args = _make(*case, dtype)
+        check(g.matmul_adapters(*args), reference(*args), case)

@@ -83,8 +83,8 @@ struct Low {
   }
 };
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(T::THREADS, 2) adapters_low_kernel(AdaptersProblem p) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+__global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) adapters_low_kernel(AdaptersProblem p) {
+  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int rows = uniform(*ws_at<int>(p, p.at.order.tiles));
   const int columns = (int)ceil_div(p.R, T::BN);
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(256) adapters_join_kernel(AdaptersProblem p) {
 
 struct WideJob {
   int steps, rows;
-  int first, tn, run, runs;
+  int first, tn, run, runs, split;
 };
 template <class T, int FMT, int S>
 struct Wide {
@@ -133,11 +133,13 @@ struct Wide {
 
   __device__ Job job(int t) const {
     int tm, tn;
-    tile_coords(share.tile(t), rows, columns, tm, tn);
+    const int id = share.tile(t), split = uniform(id / (rows * columns));
+    tile_coords(id - split * rows * columns, rows, columns, tm, tn);
     tm = uniform(tm);
     const int *runs = ws_at<int>(p, p.at.order.runs), *of = ws_at<int>(p, p.at.order.tile_run);
     Job j;
-    j.steps = (p.K + kStepK - 1) / kStepK;
+    j.split = split;
+    j.steps = (values(split) + kStepK - 1) / kStepK;
     j.tn = uniform(tn);
     j.first = T::BM * tm;
     j.rows = p.T - j.first < T::BM ? p.T - j.first : T::BM;
@@ -149,24 +151,31 @@ struct Wide {
       if (uniform(runs[4 + 4 * last + 1]) == j.first + j.rows) --last;
     }
     if (uniform(runs[4 + 4 * last]) == p.count) --last;
-    j.runs = last - j.run + 1;
+    j.runs = split == 0 ? last - j.run + 1 : 0;  // the first part of K adds them
     return j;
+  }
+  // of K in a part
+  __device__ int values(int split) const {
+    const int left = p.K - split * p.at.wide_chunk;
+    return left < p.at.wide_chunk ? left : p.at.wide_chunk;
   }
   __device__ __forceinline__ void fetch(const Job &j) {
     token.fetch(ws_at<int>(p, p.at.order.list) + j.first, j.rows, wave, lane);
   }
   __device__ __forceinline__ void begin(const Job &j) {
-    a.init(p.X, 2 * ((p.T - 1) * p.ldx + p.K),
+    const int k0 = j.split * p.at.wide_chunk, n = values(j.split);
+    const uint16_t *x = p.X + k0, *w = p.W + k0;
+    a.init(x, 2 * ((p.T - 1) * p.ldx + n),
            [&](int i, int q) __attribute__((always_inline)) {
-             return i < j.rows ? p.X + token.at[q] * p.ldx : nullptr;
+             return i < j.rows ? x + token.at[q] * p.ldx : nullptr;
            },
-           p.K, kNever, wave, lane);
-    b.init(p.W, 2 * ((p.N - 1) * p.ldw + p.K),
+           n, kNever, wave, lane);
+    b.init(w, 2 * ((p.N - 1) * p.ldw + n),
            [&](int c, int) __attribute__((always_inline)) {
-             const int n = T::BN * j.tn + c;
-             return n < p.N ? p.W + n * p.ldw : nullptr;
+             const int row = T::BN * j.tn + c;
+             return row < p.N ? w + row * p.ldw : nullptr;
            },
-           p.K, kNever, wave, lane);
+           n, kNever, wave, lane);
   }
   // Adds B[r] v.  The matrix instruction multiplies all 16 rows of a block; the sums
   // of rows that are not the run's are dropped, not multiplied by zeros: an
@@ -211,6 +220,21 @@ struct Wide {
     const int wm = wave / T::WGN, wn = wave % T::WGN, l16 = lane & 15;
 #pragma unroll 1
     for (int run = j.run; run < j.run + j.runs; ++run) add_run(j, run, acc, wave, lane);
+    if (p.at.wide_splits > 1) {
+      float *sums = ws_at<float>(p, p.at.wide_part) + (long long)j.split * p.T * p.at.npitch;
+#pragma unroll
+      for (int i = 0; i < T::TBM; ++i) {
+        const int row = 16 * (T::WGM * i + wm) + l16;
+        if (row >= j.rows) continue;
+#pragma unroll
+        for (int m = 0; m < T::TBN; ++m) {
+          const int n = T::BN * j.tn + 16 * (wn * T::TBN + m) + 4 * (lane >> 4);
+          if (n < p.N)
+            *reinterpret_cast<f32x4 *>(sums + (j.first + row) * p.at.npitch + n) = acc[i][m];
+        }
+      }
+      return;
+    }
     const int *list = ws_at<int>(p, p.at.order.list) + j.first;
 #pragma unroll
     for (int i = 0; i < T::TBM; ++i) {
@@ -228,12 +252,30 @@ struct Wide {
   }
 };
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(T::THREADS, 2) adapters_wide_kernel(AdaptersProblem p) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+__global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) adapters_wide_kernel(AdaptersProblem p) {
+  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int rows = (int)ceil_div(p.T, T::BM), columns = (int)ceil_div(p.N, T::BN);
-  Wide<T, FMT, S> op{p, Share(rows * columns), rows, columns, wave, lane, {}, {}, {}};
+  Wide<T, FMT, S> op{p, Share(rows * columns * p.at.wide_splits), rows, columns, wave, lane, {}, {}, {}};
   tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
+}
+
+// y: the parts of K added in order.  Eight values to a thread.
+template <int FMT>
+__global__ void __launch_bounds__(256) adapters_sum_kernel(AdaptersProblem p) {
+  const int per = (int)(p.at.npitch / 8);
+  const long long i = 256LL * blockIdx.x + threadIdx.x;
+  const int place = (int)(i / per), n = 8 * (int)(i - (long long)place * per);
+  if (place >= p.T) return;
+  const float *part = ws_at<float>(p, p.at.wide_part) + place * p.at.npitch + n;
+  float y[8] = {};
+  for (int s = 0; s < p.at.wide_splits; ++s) {
+    const f32x4 *q = reinterpret_cast<const f32x4 *>(part + s * p.T * p.at.npitch);
+    const f32x4 a = q[0], b = q[1];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] += a[c], y[4 + c] += b[c];
+  }
+  store8<FMT>(p.Y, ws_at<int>(p, p.at.order.list)[place] * p.ldy + n, p.N - n, y);
 }
 
 }  // namespace
@@ -264,12 +306,16 @@ hipError_t launch_adapters_tiles(const AdaptersProblem &p, hipStream_t s) {
   if (e != hipSuccess) return e;
   const bool d = direct(p.X, p.ldx, p.K, p.T) && direct(p.W, p.ldw, p.K, p.N);
   const bool w = by_words(p.X, p.K) && by_words(p.W, p.K);
-  return choose_tiles(p.at.tile, d, w, [&](auto tile, auto how) {
+  const long long all = ceil_div(p.T, p.at.tile) * ceil_div(p.N, p.at.tile) * p.at.wide_splits;
+  e = choose_tiles(p.at.tile, all, d, w, [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
-    const long long tiles = ceil_div(p.T, T::BM) * ceil_div(p.N, T::BN);
-    return GEMM_F32_LAUNCH_ROWS(adapters_wide_kernel, T, S, tiles);
+    return GEMM_F32_LAUNCH_ROWS(adapters_wide_kernel, T, S, all);
   });
+  if (e != hipSuccess || p.at.wide_splits == 1) return e;
+  const dim3 grid((unsigned)ceil_div(p.T * (p.at.npitch / 8), 256));
+  return p.format == kBf16 ? launch_kernel(adapters_sum_kernel<kBf16>, grid, dim3(256), s, p)
+                           : launch_kernel(adapters_sum_kernel<kF16>, grid, dim3(256), s, p);
 }
 
 }  // namespace gemm_f32_impl

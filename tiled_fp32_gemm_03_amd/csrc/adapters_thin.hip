@@ -1,5 +1,5 @@
-// A shared projection with low-rank adapters for up to 64 rows (gemm_adapters.h):
-// single tokens of many requests.  Two launches: scale A[r] x by a workgroup to each
+// A shared projection with low-rank adapters for few rows (gemm_adapters.h), 64 at a
+// time: single tokens of many requests.  Two launches: scale A[r] x by a workgroup to each
 // adapter that is asked and 16 of its ranks, and the projection, which reads W once,
 // straight into the matrix instructions' operands (mx_thin.hpp), and the asked
 // adapters' B.
@@ -20,6 +20,16 @@ __device__ inline f32x4 mfma_16(u32x4 b, u32x4 a, f32x4 acc) {
   if constexpr (FMT == kBf16) return mfma_bf16(b, a, acc);
   else return mfma_f16(b, a, acc);
 }
+// A launch takes 64 rows at a time: those of block b of them.
+__device__ inline AdaptersProblem rows_of(AdaptersProblem p, int b) {
+  const long long from = kAdaptersThin * (long long)b;
+  p.X += from * p.ldx;
+  p.Y += from * p.ldy;
+  p.ids += from;
+  p.at.v += 2 * from * p.at.rpitch;
+  p.T = p.T - from < kAdaptersThin ? (int)(p.T - from) : kAdaptersThin;
+  return p;
+}
 // The adapter of row i, or -1.
 __device__ inline int adapter_of(const AdaptersProblem &p, int i) {
   const int e = i < p.T ? p.ids[i] : -1;
@@ -32,11 +42,12 @@ __device__ inline int adapter_of(const AdaptersProblem &p, int i) {
 // are added in wave order.
 constexpr int kLowWaves = 8;
 template <int FMT, int ROWS>
-__global__ void __launch_bounds__(64 * kLowWaves) adapters_low_thin_kernel(AdaptersProblem p) {
+__global__ void __launch_bounds__(64 * kLowWaves) adapters_low_thin_kernel(AdaptersProblem all) {
+  const AdaptersProblem p = rows_of(all, blockIdx.x / kAdaptersThin);
   __shared__ f32x4 part[kLowWaves][64];
   __shared__ int rows[64];
   const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
-  const int i = blockIdx.x, r0 = 16 * blockIdx.y;
+  const int i = blockIdx.x % kAdaptersThin, r0 = 16 * blockIdx.y;
   const int id = adapter_of(p, lane), e = __builtin_amdgcn_readlane(id, i);
   if (e < 0) return;  // uniform
   const unsigned long long same = __ballot(id == e);
@@ -198,53 +209,107 @@ __device__ __forceinline__ void store_rows(const AdaptersProblem &p, unsigned ch
 
 constexpr int kThinWaves = 4, kThinThreads = 64 * kThinWaves;
 
-// ---- rows of whole 16 bytes ----------------------------------------------------------------
+// ---- matrices that start on a 4-byte word ---------------------------------------------------
 // A round is a 64-deep step for each of the KS waves of a block of columns: x's rows and W's
 // of the workgroup's 64 / KS columns come straight into one of STAGES stages, those of
 // the STAGES - 1 rounds ahead on their way.  Every wave asks for as many loads each
 // round, so that their number tells which have come.
-template <int RB, int KS>
+//
+// Rows of whole 16 bytes lie in LDS by 8 chunks of 16 bytes, as in row_tiles.hpp.  WORDS:
+// rows that may start in the middle of a word, or end inside 16 bytes, by 9 chunks from the
+// word that a row's first value is in (144 bytes: 16 rows meet on no bank); the values
+// are moved into place, and those past K cleared, when they are read.
+template <int RB, int KS, bool WORDS>
 struct Rounds {
-  static constexpr int X = RB * 2048, W = 2048;      // bytes of a wave's step
+  static constexpr int CHUNKS = WORDS ? 9 : 8, ROW = 16 * CHUNKS;
+  static constexpr int X_ALL = (RB * 16 * CHUNKS + 63) / 64;  // loads of a wave's step of x, 1 KB each
+  static constexpr int W_LOADS = (16 * CHUNKS + 63) / 64;
+  static constexpr int X = X_ALL * 1024, W = W_LOADS * 1024;
   static constexpr int STAGE = KS * X + kThinWaves * W;
   static constexpr int STAGES = 150 * 1024 / STAGE < 8 ? 150 * 1024 / STAGE : 8;
-  static constexpr int X_LOADS = (2 * RB * KS + kThinWaves - 1) / kThinWaves;  // a wave's, 1 KB each
-  static constexpr int LOADS = X_LOADS + 2;
+  static constexpr int X_LOADS = (X_ALL * KS + kThinWaves - 1) / kThinWaves;  // a wave's
+  static constexpr int LOADS = X_LOADS + W_LOADS;
   static constexpr int LDS = STAGES * STAGE;
   static_assert(STAGES >= 3 && LOADS * (STAGES - 2) < 64, "loads that can be counted");
   static_assert(kThinWaves * RB * 1024 <= LDS, "the waves' sums");
+
+  // Where position n of a step's chunks comes from: row, and chunk of it.
+  static __device__ __forceinline__ int row_of(int n) { return n / CHUNKS; }
+  static __device__ __forceinline__ int chunk_of(int n) {
+    return WORDS ? n % CHUNKS : (n & 7) ^ ((row_of(n) >> 1) & 7);
+  }
 };
 
-template <int FMT, int RB, int KS>
-__global__ void __launch_bounds__(kThinThreads) adapters_rounds_kernel(AdaptersProblem p) {
-  typedef Rounds<RB, KS> R;
+// A lane's operand: block `block` of 16 rows, group kg of 32; WORDS: of rows that are
+// `shift` bits into their words, the first `left` values of the step.
+template <bool WORDS>
+__device__ __forceinline__ i16x8 read_round(const unsigned char *st, int block, int kg, int lane,
+                                            int shift, int left) {
+  if constexpr (!WORDS) {
+    return read_operand<false, 16>(reinterpret_cast<const char *>(st), block, kg, lane);
+  } else {
+    const int g = lane >> 4;
+    const unsigned char *at = st + (16 * block + (lane & 15)) * 144 + 16 * (4 * kg + g);
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(at);
+    const uint32_t next = *reinterpret_cast<const uint32_t *>(at + 16);
+    u32x4 x{__builtin_amdgcn_alignbit(v[1], v[0], (uint32_t)shift),
+            __builtin_amdgcn_alignbit(v[2], v[1], (uint32_t)shift),
+            __builtin_amdgcn_alignbit(v[3], v[2], (uint32_t)shift),
+            __builtin_amdgcn_alignbit(next, v[3], (uint32_t)shift)};
+    if (left < kStepK) {  // uniform
+      const int keep = left - 32 * kg - 8 * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = keep >= 2 * i + 2 ? x[i] : keep == 2 * i + 1 ? x[i] & 0xffffu : 0u;
+    }
+    return __builtin_bit_cast(i16x8, x);
+  }
+}
+
+template <int FMT, int RB, int KS, bool WORDS>
+__global__ void __launch_bounds__(kThinThreads) adapters_rounds_kernel(AdaptersProblem all) {
+  typedef Rounds<RB, KS, WORDS> R;
+  const AdaptersProblem p = rows_of(all, blockIdx.y);
   __shared__ __attribute__((aligned(16))) unsigned char lds[R::LDS];
   __shared__ int order[64], ids[64];
   const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t *)lds;
-  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15;
   order_rows(p, order, ids);
   const int first = wave % KS;
   const int columns = 16 * ((int)blockIdx.x * (kThinWaves / KS) + wave / KS);
-  const rsrc_t xs = buffer_of(p.X, records_of(2 * ((p.T - 1) * p.ldx + p.K)));
-  const uint16_t *w0 = p.W + (long long)columns * p.ldw;
   const int have = p.N - columns < 16 ? p.N - columns : 16;  // columns, or none
-  const rsrc_t ws = buffer_of(have > 0 ? w0 : p.W,
-                              have > 0 ? records_of(2 * ((have - 1) * p.ldw + p.K)) : 0);
-  // A load brings 8 rows of 8 chunks: row l / 8, chunk c0 of even loads (m16_a_pos).
-  const int c0 = (lane & 7) ^ (lane >> 4);
-  int wv[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) wv[h] = (int)(2 * (8 * h + (lane >> 3)) * p.ldw) + 16 * (c0 ^ (4 * h));
+  // The words that the matrices' values are in; the wave's rows of W from the word of the first.
+  const uintptr_t w_at = reinterpret_cast<uintptr_t>(p.W + (have > 0 ? columns : 0) * p.ldw);
+  const int w_odd = (int)(w_at & 2), x_odd = (int)(reinterpret_cast<uintptr_t>(p.X) & 2);
+  auto words = [](long long bytes) { return records_of((bytes + 3) & ~3LL); };
+  const rsrc_t xs = buffer_of(reinterpret_cast<const char *>(p.X) - x_odd,
+                              words(x_odd + 2 * ((p.T - 1) * p.ldx + p.K)));
+  const rsrc_t ws = buffer_of(reinterpret_cast<const void *>(w_at - w_odd),
+                              have > 0 ? words(w_odd + 2 * ((have - 1) * p.ldw + p.K)) : 0);
+  // Offset of a row's chunk 0, and of the first value in it.
+  auto w_row = [&](int r) __attribute__((always_inline)) { return w_odd + (int)(2 * r * p.ldw); };
   __syncthreads();
+  auto x_row = [&](int r) __attribute__((always_inline)) {
+    return x_odd + (int)(2 * order[r] * p.ldx);
+  };
+  int wv[R::W_LOADS], wk[R::W_LOADS];  // offsets, and the first k of the chunk in the step
+#pragma unroll
+  for (int h = 0; h < R::W_LOADS; ++h) {
+    const int n = 64 * h + lane, r = R::row_of(n), c = R::chunk_of(n), at = w_row(r);
+    wk[h] = 8 * c - (at & 2) / 2;
+    wv[h] = r < have && r < 16 ? (at & ~3) + 16 * c : kOutside;
+  }
   // x's loads are dealt to the waves, some twice where they do not come out even.
-  int xv[R::X_LOADS], part[R::X_LOADS], place[R::X_LOADS];
+  int xv[R::X_LOADS], xk[R::X_LOADS], part[R::X_LOADS], place[R::X_LOADS];
 #pragma unroll
   for (int q = 0; q < R::X_LOADS; ++q) {
-    const int i = (wave + kThinWaves * q) % (2 * RB * KS), in = i % (2 * RB);
-    const int r = 8 * in + (lane >> 3);
-    part[q] = i / (2 * RB);
+    const int i = (wave + kThinWaves * q) % (R::X_ALL * KS), in = i % R::X_ALL;
+    const int n = 64 * in + lane, r = R::row_of(n), c = R::chunk_of(n);
+    const int at = x_row(r < 64 ? r : 0);
+    part[q] = i / R::X_ALL;
     place[q] = part[q] * R::X + in * 1024;
-    xv[q] = r < p.T ? (int)(2 * order[r] * p.ldx) + 16 * (c0 ^ (4 * (in & 1))) : kOutside;
+    xk[q] = 8 * c - (at & 2) / 2;
+    xv[q] = r < p.T && r < 16 * RB ? (at & ~3) + 16 * c : kOutside;
   }
   const int steps = (p.K + kStepK - 1) / kStepK, rounds = (steps + KS - 1) / KS;
   auto issue = [&](int round, int stage) __attribute__((always_inline)) {
@@ -252,37 +317,40 @@ __global__ void __launch_bounds__(kThinThreads) adapters_rounds_kernel(AdaptersP
 #pragma unroll
     for (int q = 0; q < R::X_LOADS; ++q) {
       const int k0 = kStepK * (round * KS + part[q]);
-      const int i = (wave + kThinWaves * q) % (2 * RB * KS);
-      const bool in = k0 + 8 * (c0 ^ (4 * (i & 1))) < p.K;
-      buffer_load_to_lds16(in ? xv[q] : kOutside, xs, uniform(2 * k0),
+      buffer_load_to_lds16(k0 + xk[q] < p.K ? xv[q] : kOutside, xs, uniform(2 * k0),
                            (unsigned)uniform((int)(to + place[q])));
     }
     const int k0 = kStepK * (round * KS + first);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool in = k0 + 8 * (c0 ^ (4 * h)) < p.K;
-      buffer_load_to_lds16(in ? wv[h] : kOutside, ws, uniform(2 * k0),
+    for (int h = 0; h < R::W_LOADS; ++h)
+      buffer_load_to_lds16(k0 + wk[h] < p.K ? wv[h] : kOutside, ws, uniform(2 * k0),
                            (unsigned)uniform((int)(to + KS * R::X + wave * R::W + h * 1024)));
-    }
   };
 #pragma unroll
   for (int i = 0; i < R::STAGES - 1; ++i) issue(i, i);
+  // Bits that a lane's rows are into their words.
+  int ws_shift = 8 * (w_row(l16) & 2), xs_shift[RB];
   f32x4 acc[RB];
 #pragma unroll
-  for (int b = 0; b < RB; ++b) acc[b] = f32x4{0, 0, 0, 0};
+  for (int b = 0; b < RB; ++b) {
+    xs_shift[b] = 8 * (x_row(16 * b + l16) & 2);
+    acc[b] = f32x4{0, 0, 0, 0};
+  }
   int stage = 0, ahead = R::STAGES - 1;
 #pragma unroll 1
   for (int i = 0; i < rounds; ++i) {
     __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(R::LOADS * (R::STAGES - 2)));  // round i's, own
     ks_lds_barrier();  // everyone's; the stage of round i - 1 is free
     issue(i + R::STAGES - 1, ahead);  // past the end: zeros
-    const char *st = reinterpret_cast<const char *>(lds) + stage * R::STAGE;
+    const unsigned char *st = lds + stage * R::STAGE;
+    const int left = p.K - kStepK * (i * KS + first);
 #pragma unroll
     for (int kg = 0; kg < 2; ++kg) {
-      const i16x8 wf = read_operand<false, 16>(st + KS * R::X + wave * R::W, 0, kg, lane);
+      const i16x8 wf = read_round<WORDS>(st + KS * R::X + wave * R::W, 0, kg, lane, ws_shift, left);
 #pragma unroll
       for (int b = 0; b < RB; ++b)
-        acc[b] = mfma_rows<FMT>(wf, read_operand<false, 16>(st + first * R::X, b, kg, lane), acc[b]);
+        acc[b] = mfma_rows<FMT>(
+            wf, read_round<WORDS>(st + first * R::X, b, kg, lane, xs_shift[b], left), acc[b]);
     }
     stage = stage + 1 == R::STAGES ? 0 : stage + 1;
     ahead = ahead + 1 == R::STAGES ? 0 : ahead + 1;
@@ -292,14 +360,15 @@ __global__ void __launch_bounds__(kThinThreads) adapters_rounds_kernel(AdaptersP
   store_rows<FMT, RB>(p, lds, order, columns, KS, first, acc);
 }
 
-// ---- any rows ----------------------------------------------------------------------------------
+// ---- any matrices, also of 2^31 bytes and more ---------------------------------------------
 // x waits in LDS, the weights of two pieces of 128 values are on their way while a third
 // is used.
 constexpr int kThinLds = 74 * 1024;  // of x: two workgroups to a compute unit
 
 template <int FMT, int RB, int ROWS>
-__global__ void __launch_bounds__(kThinThreads, 2) adapters_thin_kernel(AdaptersProblem p, Tile tile,
-                                                                        int ks) {
+__global__ void __launch_bounds__(kThinThreads, 2) adapters_thin_kernel(AdaptersProblem all,
+                                                                        Tile tile, int ks) {
+  const AdaptersProblem p = rows_of(all, blockIdx.y);
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ int order[64], ids[64];  // rows, and their adapters
   const int lane = threadIdx.x & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
@@ -377,21 +446,34 @@ hipError_t launch_thin(const AdaptersProblem &p, hipStream_t s) {
   Tile t = tile;
   void *args[] = {&q, &t, &ks};
   return hipLaunchKernel(reinterpret_cast<const void *>(adapters_thin_kernel<FMT, RB, ROWS>),
-                         dim3((unsigned)ceil_div(groups, kThinWaves / ks)), dim3(kThinThreads), args,
+                         dim3((unsigned)ceil_div(groups, kThinWaves / ks),
+                              (unsigned)ceil_div(p.T, kAdaptersThin)),
+                         dim3(kThinThreads), args,
                          (size_t)lds, s);
 }
-template <int FMT, int RB, int KS>
+// Whether `rows` rows of a matrix that starts on a word are within 32-bit offsets.
+bool on_words(const uint16_t *p, long long ld, long long rows) {
+  return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && 2 * rows * ld + 64 <= kMostRecords;
+}
+template <int FMT, int RB, int KS, bool WORDS>
 hipError_t launch_rounds(const AdaptersProblem &p, hipStream_t s) {
-  return launch_kernel(adapters_rounds_kernel<FMT, RB, KS>,
-                       dim3((unsigned)ceil_div(p.N, 16 * kThinWaves / KS)), dim3(kThinThreads), s, p);
+  return launch_kernel(adapters_rounds_kernel<FMT, RB, KS, WORDS>,
+                       dim3((unsigned)ceil_div(p.N, 16 * kThinWaves / KS),
+                            (unsigned)ceil_div(p.T, kAdaptersThin)),
+                       dim3(kThinThreads), s, p);
 }
 // Waves to a block of columns: until there is a workgroup to each compute unit.
-template <int FMT, int RB>
+template <int FMT, int RB, bool WORDS>
 hipError_t launch_direct(const AdaptersProblem &p, hipStream_t s) {
   const long long groups = ceil_div(p.N, 16);
-  if (groups >= 4 * 256) return launch_rounds<FMT, RB, 1>(p, s);
-  if (groups >= 2 * 256) return launch_rounds<FMT, RB, 2>(p, s);
-  return launch_rounds<FMT, RB, 4>(p, s);
+  if (groups >= 4 * 256) return launch_rounds<FMT, RB, 1, WORDS>(p, s);
+  if (groups >= 2 * 256) return launch_rounds<FMT, RB, 2, WORDS>(p, s);
+  return launch_rounds<FMT, RB, 4, WORDS>(p, s);
+}
+template <int FMT, bool WORDS>
+hipError_t launch_blocks(const AdaptersProblem &p, hipStream_t s) {
+  if (p.T <= 16) return launch_direct<FMT, 1, WORDS>(p, s);
+  return p.T <= 32 ? launch_direct<FMT, 2, WORDS>(p, s) : launch_direct<FMT, 4, WORDS>(p, s);
 }
 
 template <int FMT, int ROWS>
@@ -403,10 +485,10 @@ hipError_t launch_both(const AdaptersProblem &p, hipStream_t s) {
                       dim3((unsigned)p.T, (unsigned)(2 * ceil_div(p.R, 32))), dim3(64 * kLowWaves), s, p);
     if (e != hipSuccess) return e;
   }
-  if (direct(p.X, p.ldx, p.K, p.T) && direct(p.W, p.ldw, p.K, 16)) {
-    if (p.T <= 16) return launch_direct<FMT, 1>(p, s);
-    return p.T <= 32 ? launch_direct<FMT, 2>(p, s) : launch_direct<FMT, 4>(p, s);
-  }
+  if (direct(p.X, p.ldx, p.K, kAdaptersThin) && direct(p.W, p.ldw, p.K, 16))
+    return launch_blocks<FMT, false>(p, s);
+  if (on_words(p.X, p.ldx, kAdaptersThin) && on_words(p.W, p.ldw, 16))
+    return launch_blocks<FMT, true>(p, s);
   if (p.T <= 16) return launch_thin<FMT, 1, ROWS>(p, s);
   if (p.T <= 32) return launch_thin<FMT, 2, ROWS>(p, s);
   return launch_thin<FMT, 4, ROWS>(p, s);

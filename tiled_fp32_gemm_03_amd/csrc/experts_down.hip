@@ -105,25 +105,25 @@ struct Dx {
 
 template <class T, int FMT, int S, template <class, int, int> class Op>
 __device__ __forceinline__ void part_tiles(const ExpertsProblem &p) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int rows = row_tiles(p), columns = (int)ceil_div(p.H, T::BN);
   Op<T, FMT, S> op{p, Share(rows * columns), rows, columns, wave, lane, {}, {}};
   tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(T::THREADS, 2) experts_down_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_down_kernel(ExpertsProblem p) {
   part_tiles<T, FMT, S, Down>(p);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(T::THREADS, 2) experts_dx_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_dx_kernel(ExpertsProblem p) {
   part_tiles<T, FMT, S, Dx>(p);
 }
 
 }  // namespace
 
 hipError_t launch_experts_down(const ExpertsProblem &p, hipStream_t s) {
-  return choose_tiles(p.tile, direct(p.W2, p.ld2, p.I, p.H), by_words(p.W2, p.I),
+  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.H, p.tile), direct(p.W2, p.ld2, p.I, p.H), by_words(p.W2, p.I),
                       [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
@@ -133,7 +133,7 @@ hipError_t launch_experts_down(const ExpertsProblem &p, hipStream_t s) {
 }
 
 hipError_t launch_experts_dx(const ExpertsProblem &p, hipStream_t s) {
-  return choose_tiles(p.tile, direct(p.W1, p.ld1, p.H, kStepK), by_words(p.W1, p.H),
+  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.H, p.tile), direct(p.W1, p.ld1, p.H, kStepK), by_words(p.W1, p.H),
                       [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;

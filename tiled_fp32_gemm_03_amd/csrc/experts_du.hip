@@ -96,8 +96,8 @@ struct Du {
 };
 
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(T::THREADS, 2) experts_du_kernel(ExpertsProblem p) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+__global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_du_kernel(ExpertsProblem p) {
+  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int rows = row_tiles(p), columns = (int)ceil_div(p.I, T::BN);
   Du<T, FMT, S> op{p, Share(rows * columns), rows, columns, wave, lane, {}, {}, {}};
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(T::THREADS, 2) experts_du_kernel(ExpertsProble
 hipError_t launch_experts_du(const ExpertsProblem &p, hipStream_t s) {
   const bool d = direct(p.dY, p.lddy, p.H, p.T) && direct(p.W2, p.ld2, p.I, kStepK);
   const bool w = by_words(p.dY, p.H) && by_words(p.W2, p.I);
-  return choose_tiles(p.tile, d, w, [&](auto tile, auto how) {
+  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.I, p.tile), d, w, [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
     const long long tiles = p.at.most_tiles * ceil_div(p.I, T::BN);

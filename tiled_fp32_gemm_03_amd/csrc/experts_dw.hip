@@ -122,18 +122,18 @@ struct Dw2 {
 
 template <class T, int FMT, int S, template <class, int, int> class Op>
 __device__ __forceinline__ void weight_tiles(const ExpertsProblem &p, int rows, int columns) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int tiles_m = (int)ceil_div(rows, T::BM), tiles_n = (int)ceil_div(columns, T::BN);
   Op<T, FMT, S> op{p, Share(p.E * tiles_m * tiles_n), tiles_m, tiles_n, wave, lane, {}, {}};
   tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(T::THREADS, 2) experts_dw1_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_dw1_kernel(ExpertsProblem p) {
   weight_tiles<T, FMT, S, Dw1>(p, (int)(2 * p.at.ipitch), p.H);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(T::THREADS, 2) experts_dw2_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_dw2_kernel(ExpertsProblem p) {
   weight_tiles<T, FMT, S, Dw2>(p, p.H, p.I);
 }
 
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(T::THREADS, 2) experts_dw2_kernel(ExpertsProbl
 
 hipError_t launch_experts_dw(const ExpertsProblem &p, hipStream_t s) {
   hipError_t e = hipSuccess;
-  if (p.dW1) e = choose_tiles(p.tile, direct(p.X, p.ldx, p.H, p.T), by_words(p.X, p.H),
+  if (p.dW1) e = choose_tiles(p.tile, p.E * ceil_div(2 * p.at.ipitch, p.tile) * ceil_div(p.H, p.tile), direct(p.X, p.ldx, p.H, p.T), by_words(p.X, p.H),
                                     [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
@@ -149,7 +149,7 @@ hipError_t launch_experts_dw(const ExpertsProblem &p, hipStream_t s) {
     return GEMM_F32_LAUNCH_ROWS(experts_dw1_kernel, T, S, tiles);
   });
   if (e != hipSuccess || !p.dW2) return e;
-  return choose_tiles(p.tile, direct(p.dY, p.lddy, p.H, p.T), by_words(p.dY, p.H),
+  return choose_tiles(p.tile, p.E * ceil_div(p.H, p.tile) * ceil_div(p.I, p.tile), direct(p.dY, p.lddy, p.H, p.T), by_words(p.dY, p.H),
                       [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;

@@ -70,7 +70,7 @@ struct AdaptersProblem {
   unsigned char *ws;
   AdaptersSpace at;
 };
-hipError_t launch_adapters_thin(const AdaptersProblem &p, hipStream_t s);   // T <= kAdaptersThin
-hipError_t launch_adapters_tiles(const AdaptersProblem &p, hipStream_t s);  // more
+hipError_t launch_adapters_thin(const AdaptersProblem &p, hipStream_t s);   // adapters_thin
+hipError_t launch_adapters_tiles(const AdaptersProblem &p, hipStream_t s);  // others
 
 }  // namespace gemm_f32_impl

@@ -19,18 +19,45 @@ int experts_check_sizes(int T, int E, int top, int H, int I) {
   return kOk;
 }
 
+// Thin products where an expert has few pairs: they read its weights once for 16 of
+// them.  Thin and tiles, us, by pairs to an expert (experts, widths): 4 (8, 4096 / 2048)
+// 114 and 124, 8 136 and 125, 16 166 and 130; 4 (64, 2048 / 1024) 163 and 171, 8 286
+// and 174; 8 (8, 512 / 512) 21 and 25.
 bool experts_thin(int T, int E, int top) {
   const long long pairs = (long long)T * top;
-  return T <= kMoeMaxTokens && pairs <= 16LL * E;
+  return T <= kMoeMaxTokens && pairs <= 6LL * E;
 }
 
-int experts_tile(int T, int E, int top, int H, int I) {
-  const long long pairs = (long long)T * top;
-  const long long asked = E < pairs ? E : pairs;
-  const long long rows = asked ? ceil_div(pairs, asked) : 0;
-  // 256 x 256 tiles where they can fill most of the chip
-  const long long large = asked * ceil_div(rows, 256) * ceil_div(H < 2 * I ? H : 2 * I, 256);
-  return rows > 64 && large >= 192 ? 256 : 128;
+namespace {
+
+// Microseconds of n tiles of `steps`: rounds of what the chip holds at once (partial
+// ones cost half of what is missing), each step and a tile's start and end.
+double tiles_us(int tile, double n, double steps) {
+  const bool large = tile == 256;
+  const double r = n / (large ? 256 : 512);
+  const double rounds = r <= 1 ? 1 : (r + (double)(long long)(r + 0.999)) / 2;
+  return rounds * (steps * (large ? 2.0 : 1.35) + (large ? 12 : 6));
+}
+
+}  // namespace
+
+// The tile of less modelled time.  128 and 256, us (tokens, experts, choices, widths;
+// forward and training step): 512, 8, 2, 4096 / 2048 153 and 192, 529 and 613; 1,024,
+// the same, 243 and 192, 763 and 678; 4,096, 64, 4, 2048 / 1024 368 and 384, 1,440 and
+// 1,385; 8,192, the same, 620 and 575, 2,250 and 1,992; 8,192, 4, 1, 512 / 2048 108 and
+// 125, 453 and 578; 8,192, 8, 2, 4096 / 4096 2,005 and 1,628.
+int experts_tile(int T, int E, int top, int H, int I, bool trains) {
+  const double pairs = (double)T * top, asked = E < pairs ? E : pairs, rows = asked ? pairs / asked : 0;
+  auto cost = [&](int tile) {
+    const double m = asked * (rows / tile + 0.5);  // experts' last tiles are half full
+    const double h = (double)ceil_div(H, tile), i = (double)ceil_div(I, tile), i2 = (double)ceil_div(2LL * I, tile);
+    double t = tiles_us(tile, m * i2, H / 64.0) + tiles_us(tile, m * h, I / 64.0);
+    if (trains)
+      t += tiles_us(tile, m * i, H / 64.0) + tiles_us(tile, m * h, I / 32.0) +
+           tiles_us(tile, E * i2 * h, rows / 64) + tiles_us(tile, E * h * i, rows / 64);
+    return t;
+  };
+  return cost(256) < cost(128) ? 256 : 128;
 }
 
 ExpertsSpace experts_space(int T, int E, int top, int H, int I, int tile, bool backward) {
@@ -70,6 +97,15 @@ int adapters_check_sizes(int T, int N, int K, int R, int count) {
   return kOk;
 }
 
+// Thin products while 64 rows at a time cost less than the tiles' five launches.  Tiles
+// and thin, us (rows, N x K): 65, 4096 x 4096 51 and 35; 128 56 and 44; 256 52 and 80;
+// 512, 1024 x 1024 35 and 31; 1,024 37 and 58; 256, 8192 x 2048 58 and 83; 200, 2048 x
+// 8192 65 and 60; 192, 16384 x 4096 85 and 113.
+bool adapters_thin(int T, int N, int K) {
+  return T <= kAdaptersThin ||
+         (T <= kAdaptersMostThin && ceil_div(T, kAdaptersThin) * N * K <= 1LL << 25);
+}
+
 AdaptersSpace adapters_space(int T, int N, int K, int R, int count) {
   AdaptersSpace w{};
   long long at = 0;
@@ -80,9 +116,9 @@ AdaptersSpace adapters_space(int T, int N, int K, int R, int count) {
   };
   w.rpitch = ceil_div(R, 64) * 64;
   w.v = take(2 * T * w.rpitch);
-  w.splits = 1;
-  w.chunk = K;
-  if (T > kAdaptersThin) {
+  w.splits = w.wide_splits = 1;
+  w.chunk = w.wide_chunk = K;
+  if (!adapters_thin(T, N, K)) {
     w.tile = ceil_div(T, 256) * ceil_div(N, 256) >= 192 ? 256 : 128;
     // The products with A: row tiles of kAdaptersRows, K in parts until there are
     // two workgroups to a compute unit, of 256 values at least.
@@ -91,6 +127,15 @@ AdaptersSpace adapters_space(int T, int N, int K, int R, int count) {
     w.chunk = (int)(ceil_div(ceil_div(K, w.splits), 64) * 64);
     w.splits = (int)ceil_div(K, w.chunk);
     w.part = take(4LL * w.splits * T * w.rpitch);
+    // The projection: K in parts while there are two to a compute unit at most, of 512
+    // values at least (a compute unit is fed 35 to 45 KB a microsecond, so few tiles
+    // take long however they are scheduled).
+    const long long wide = ceil_div(T, w.tile) * ceil_div(N, w.tile);
+    while (2 * wide * w.wide_splits <= (w.tile == 256 ? 256 : 512) && ceil_div(K, 2 * w.wide_splits) >= 512) w.wide_splits *= 2;
+    w.wide_chunk = (int)(ceil_div(ceil_div(K, w.wide_splits), 64) * 64);
+    w.wide_splits = (int)ceil_div(K, w.wide_chunk);
+    w.npitch = ceil_div(N, 8) * 8;
+    w.wide_part = take(w.wide_splits > 1 ? 4 * w.wide_splits * T * w.npitch : 0);
     const int E = count + 1;
     ExpertsSpace &o = w.order;
     o.most_tiles = T / kAdaptersRows + (E < T ? E : T);

@@ -49,16 +49,18 @@ ExpertsSpace experts_space(int T, int E, int top, int H, int I, int tile, bool b
 // Whether a forward pass without `saved` runs on the thin products of the
 // mixture-of-experts layer.
 bool experts_thin(int T, int E, int top);
-// The tile of a call's products, 256 or 128.
-int experts_tile(int T, int E, int top, int H, int I);
+// The tile of a call's products, 256 or 128; a call that `trains` counts the backward
+// pass's too.
+int experts_tile(int T, int E, int top, int H, int I, bool trains);
 
 // ---- adapters (gemm_adapters.h) -----------------------------------------------
 
 constexpr int kAdaptersMaxRows = 1 << 22, kAdaptersMaxWidth = 1 << 17, kAdaptersMaxRank = 512,
               kAdaptersMaxCount = 511;
-// Up to this many rows: thin products, which read W once; and the rows of a tile of
-// the products with A.
-constexpr int kAdaptersThin = 64, kAdaptersRows = 64;
+// Rows that the thin products take at a time, and the rows of a tile of the products
+// with A.
+constexpr int kAdaptersThin = 64, kAdaptersMostThin = 512, kAdaptersRows = 64;
+bool adapters_thin(int T, int N, int K);
 int adapters_check_sizes(int T, int N, int K, int R, int count);
 
 // Rows by adapter: as pairs by expert (ExpertsSpace), with the rows without one as
@@ -70,7 +72,11 @@ struct AdaptersSpace {
   long long bytes;
   long long rpitch;
   int tile;            // rows and columns of the product's tiles
-  int splits, chunk;   // parts of K, of `chunk` values each
+  int splits, chunk;   // parts of K in the products with A, of `chunk` values each
+  // The same of the projection, where its tiles are few: then their sums.
+  int wide_splits, wide_chunk;
+  long long wide_part;  // float [wide_splits][T][npitch], by place
+  long long npitch;
 };
 AdaptersSpace adapters_space(int T, int N, int K, int R, int count);
 

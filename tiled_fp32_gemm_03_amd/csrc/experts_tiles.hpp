@@ -92,14 +92,28 @@ hipError_t launch_tiles(const P &p, long long tiles, hipStream_t s) {
 // Two waves to a SIMD: eight of one workgroup, or four of each of two.
 typedef RowTile<64, 128, 4, 2> Large;
 typedef RowTile<64, 64, 2, 2> Small;
-static_assert(Large::WGN == 2 && Small::WGN == 2, "slices of ExpertsSpace");
+// One, where tiles are too few for two to a compute unit.
+typedef RowTile<64, 64, 2, 2, 4> Deep;
+static_assert(Large::WGN == 2 && Small::WGN == 2 && Deep::WGN == 2, "slices of ExpertsSpace");
+template <class T>
+constexpr int kWavesPerSimd = T::STAGES > 2 ? 1 : 2;
 
-// `make(tile, integral_constant S)` launches.  Large tiles are loaded directly
+// As many tiles of 128 x 128 as there are compute units.
+constexpr long long kFewTiles = 256;
+// The row tiles that a call's pairs fill where they are spread evenly.
+inline long long even_tiles(const ExpertsProblem &p) {
+  const long long pairs = (long long)p.T * p.top, asked = p.E < pairs ? p.E : pairs;
+  if (asked == 0) return 0;
+  return asked * (pairs / (asked * p.tile)) + ceil_div(asked, 2);
+}
+
+// `make(tile, integral_constant S)` launches, about `tiles` tiles.  Large tiles are loaded directly
 // alone (through registers a wave of 128 x 128 has none left for its loads).
 template <class Make>
-hipError_t choose_tiles(int tile, bool direct_loads, bool words, Make make) {
+hipError_t choose_tiles(int tile, long long tiles, bool direct_loads, bool words, Make make) {
   if (direct_loads) {
     if (tile == Large::BM) return make(Large{}, std::integral_constant<int, kDirect>{});
+    if (tiles <= kFewTiles) return make(Deep{}, std::integral_constant<int, kDirect>{});
     return make(Small{}, std::integral_constant<int, kDirect>{});
   }
   if (words) return make(Small{}, std::integral_constant<int, kByWords>{});

@@ -81,18 +81,18 @@ struct Up {
 
 template <class T, int FMT, int S, bool SAVE>
 __device__ __forceinline__ void up_tiles(const ExpertsProblem &p) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int rows = row_tiles(p), columns = (int)ceil_div(p.I, T::BN / 2);
   Up<T, FMT, S, SAVE> op{p, Share(rows * columns), rows, columns, wave, lane, {}, {}, {}};
   tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(T::THREADS, 2) experts_up_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_up_kernel(ExpertsProblem p) {
   up_tiles<T, FMT, S, false>(p);
 }
 template <class T, int FMT, int S>
-__global__ void __launch_bounds__(T::THREADS, 2) experts_up_save_kernel(ExpertsProblem p) {
+__global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_up_save_kernel(ExpertsProblem p) {
   up_tiles<T, FMT, S, true>(p);
 }
 
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(T::THREADS, 2) experts_up_save_kernel(ExpertsP
 hipError_t launch_experts_up(const ExpertsProblem &p, hipStream_t s) {
   const bool d = direct(p.X, p.ldx, p.H, p.T) && direct(p.W1, p.ld1, p.H, 2LL * p.I);
   const bool w = by_words(p.X, p.H) && by_words(p.W1, p.H);
-  return choose_tiles(p.tile, d, w, [&](auto tile, auto how) {
+  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.I, p.tile / 2), d, w, [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
     const long long tiles = p.at.most_tiles * ceil_div(p.I, T::BN / 2);

@@ -2,7 +2,7 @@
 // the experts' products and the adapters'.
 //
 // A tile is WGM x WGN waves of WTM / 16 x WTN / 16 blocks of v_mfma_f32_16x16x32,
-// in 64-deep k steps and two LDS stages.  The waves that share columns
+// in 64-deep k steps and two or more LDS stages.  The waves that share columns
 // take the tile's blocks of 16 rows in turn, so that a tile
 // with few rows costs every wave the same, and blocks without rows are passed
 // over.  An operand lies in memory in one of two ways, and in LDS likewise:
@@ -37,9 +37,11 @@ constexpr int kStepK = 64;
 constexpr int kMostRecords = 0x7ffffff0;
 constexpr int kNever = 0x7fffffff;
 
-// WGM x WGN waves of WTM x WTN.
-template <int WTM_, int WTN_, int WGM_, int WGN_>
+// WGM x WGN waves of WTM x WTN, and LDS stages: two, or more for tiles that each have a
+// compute unit to themselves (then what bounds a step is how long its loads take).
+template <int WTM_, int WTN_, int WGM_, int WGN_, int STAGES_ = 2>
 struct RowTile {
+  static constexpr int STAGES = STAGES_;
   static constexpr int WTM = WTM_, WTN = WTN_, WGM = WGM_, WGN = WGN_, WAVES = WGM_ * WGN_;
   static constexpr int BM = WGM_ * WTM_, BN = WGN_ * WTN_, THREADS = 64 * WAVES;
   static constexpr int TBM = WTM_ / 16, TBN = WTN_ / 16;
@@ -47,7 +49,8 @@ struct RowTile {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int A_LOADS = BM / 8 / WAVES, B_LOADS = BN / 8 / WAVES;  // per wave and step, 1 KB each
   static_assert(A_LOADS % 2 == 0 && B_LOADS % 2 == 0, "whole pairs of loads (KcSide)");
-  static_assert(2 * STAGE <= kLdsBytes, "two stages fit in LDS");
+  static constexpr int LDS = STAGES * STAGE;
+  static_assert(LDS <= kLdsBytes && (STAGES - 2) * (A_LOADS + B_LOADS) < 64, "the stages");
 };
 
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -381,6 +384,71 @@ __device__ inline void store_eights(uint16_t *row, const Eights &e, int left) {
     if (c < left) row[e.at + c] = (uint16_t)(e.v[c >> 1] >> (16 * (c & 1)));
 }
 
+// tile_loop with more than two stages: the loads of STAGES - 1 steps are on their way.
+template <class T, int FMT, int S, class Op>
+__device__ __forceinline__ void deep_tiles(char *lds, Op &op, int count, int wave, int lane) {
+  static_assert(S == kDirect, "direct loads");
+  constexpr int kLoads = T::A_LOADS + T::B_LOADS, kAhead = T::STAGES - 1;
+  const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t *)lds;
+  const int wm = wave / T::WGN, wn = wave % T::WGN;
+  auto issue = [&](int kk, int at) __attribute__((always_inline)) {
+    const unsigned stage = (unsigned)uniform((int)(lds_u + at * T::STAGE));
+    side_begin(op.a, kk, wave, lane);
+    side_begin(op.b, kk, wave, lane);
+#pragma unroll
+    for (int q = 0; q < T::A_LOADS; ++q) side_issue(op.a, q, stage, wave, lane);
+#pragma unroll
+    for (int q = 0; q < T::B_LOADS; ++q) side_issue(op.b, q, stage + T::A_BYTES, wave, lane);
+  };
+#pragma unroll 1
+  for (int t = 0; t < count; ++t) {
+    const typename Op::Job job = op.job(t);
+    const int nk = job.steps, blocks = blocks_of<T>(job.rows, wm);
+    op.fetch(job);
+    op.begin(job);
+#pragma unroll 1
+    for (int kk = 0; kk < kAhead && kk < nk; ++kk) issue(kk, kk);
+    f32x4 acc[T::TBM][T::TBN];
+#pragma unroll
+    for (int i = 0; i < T::TBM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::TBN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int stage = 0;
+    auto step = [&](auto more, int kk) __attribute__((always_inline)) {
+      constexpr bool MORE = decltype(more)::value;
+      // This step's own loads, which at least those of kAhead - 1 steps follow.
+      __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(MORE ? kLoads * (kAhead - 1) : 0));
+      ks_lds_barrier();  // everyone's; the stage of the step before is free
+      if constexpr (MORE) issue(kk + kAhead, stage == 0 ? kAhead : stage - 1);
+      const char *st = lds + stage * T::STAGE;
+#pragma unroll
+      for (int kg = 0; kg < kStepK / 32; ++kg) {
+        i16x8 fa[T::TBM], fb[T::TBN];
+#pragma unroll
+        for (int j = 0; j < T::TBN; ++j)
+          fb[j] = read_operand<Op::B::kDown, T::BN>(st + T::A_BYTES, wn * T::TBN + j, kg, lane);
+#pragma unroll
+        for (int i = 0; i < T::TBM; ++i)
+          fa[i] = read_operand<Op::A::kDown, T::BM>(st, T::WGM * i + wm, kg, lane);
+#pragma unroll
+        for (int i = 0; i < T::TBM; ++i)
+          if (i < blocks) {  // uniform
+#pragma unroll
+            for (int j = 0; j < T::TBN; ++j) acc[i][j] = mfma_rows<FMT>(fb[j], fa[i], acc[i][j]);
+          }
+      }
+      stage = stage + 1 == T::STAGES ? 0 : stage + 1;
+    };
+    int kk = 0;
+#pragma unroll 1
+    for (; kk + kAhead < nk; ++kk) step(std::true_type{}, kk);
+#pragma unroll 1
+    for (; kk < nk; ++kk) step(std::false_type{}, kk);
+    op.store(job, acc, wave, lane);
+    ks_lds_barrier();  // the next tile's loads overwrite the LDS
+  }
+}
+
 // A workgroup's tiles, one after the other.  `Op` has
 //   Job       what a tile is: `steps` of k, `rows` (of the tile's that there are), ...
 //   A, B      the operands' sides, members a and b
@@ -397,6 +465,10 @@ __device__ inline void store_eights(uint16_t *row, const Eights &e, int left) {
 template <class T, int FMT, int S, class Op>
 __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave, int lane) {
   if (count <= 0) return;  // uniform
+  if constexpr (T::STAGES > 2) {
+    deep_tiles<T, FMT, S>(lds, op, count, wave, lane);
+    return;
+  }
   const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t *)lds;
   const int wm = wave / T::WGN, wn = wave % T::WGN;
   constexpr int kLoads = T::A_LOADS + T::B_LOADS;

@@ -91,10 +91,12 @@ namespace {
 
 long long experts_bytes(int T, int E, int top, int H, int I, bool backward) {
   const long long tiles =
-      experts_space(T, E, top, H, I, experts_tile(T, E, top, H, I), backward).bytes;
-  if (backward || T > kMoeMaxTokens) return tiles;
-  const long long thin = moe_space(T, E, top, H, I).bytes;
-  return thin > tiles ? thin : tiles;
+      experts_space(T, E, top, H, I, experts_tile(T, E, top, H, I, true), backward).bytes;
+  if (backward) return tiles;
+  long long most = experts_space(T, E, top, H, I, experts_tile(T, E, top, H, I, false), false).bytes;
+  if (T <= kMoeMaxTokens && moe_space(T, E, top, H, I).bytes > most)
+    most = moe_space(T, E, top, H, I).bytes;
+  return most > tiles ? most : tiles;
 }
 
 bool bad_workspace(const void *ws, long long bytes, long long need) {
@@ -155,7 +157,7 @@ extern "C" int gemm_experts(int T, int E, int top, int H, int I, const void *X, 
   p.W1 = static_cast<const uint16_t *>(W1), p.ld1 = ld1;
   p.W2 = static_cast<const uint16_t *>(W2), p.ld2 = ld2;
   p.Y = static_cast<uint16_t *>(Y), p.ldy = ldy, p.saved = saved, p.ws = ws;
-  p.tile = experts_tile(T, E, top, H, I);
+  p.tile = experts_tile(T, E, top, H, I, saved != nullptr);
   p.at = experts_space(T, E, top, H, I, p.tile, false);
   return launch_status(launch_experts_forward(p, s), "experts");
 }
@@ -199,7 +201,7 @@ extern "C" int gemm_experts_backward(int T, int E, int top, int H, int I, const 
   p.dW1 = static_cast<uint16_t *>(dW1), p.lddw1 = lddw1;
   p.dW2 = static_cast<uint16_t *>(dW2), p.lddw2 = lddw2;
   p.ws = static_cast<unsigned char *>(workspace);
-  p.tile = experts_tile(T, E, top, H, I);
+  p.tile = experts_tile(T, E, top, H, I, true);
   p.at = experts_space(T, E, top, H, I, p.tile, true);
   return launch_status(launch_experts_backward(p, static_cast<hipStream_t>(stream)),
                        "experts backward");
@@ -237,6 +239,6 @@ extern "C" int gemm_adapters(int T, int N, int K, int R, int count, const void *
                           static_cast<uint16_t *>(Y), ldy, static_cast<unsigned char *>(workspace),
                           at};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return launch_status(T <= kAdaptersThin ? launch_adapters_thin(p, s) : launch_adapters_tiles(p, s),
+  return launch_status(adapters_thin(T, N, K) ? launch_adapters_thin(p, s) : launch_adapters_tiles(p, s),
                        "adapters");
 }
