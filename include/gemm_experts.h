@@ -10,9 +10,9 @@
  * An id outside 0 .. E - 1 is a choice that was dropped: it adds nothing, and its
  * gate's gradient is 0.  The same id twice in a row counts twice.
  *
- * Sums are held in fp32, and results do not depend on timing.  u, each choice's
- * term of y and, in the backward pass, the gradient of h and of x's terms are
- * kept in `format` between the products; values past its range become infinite.
+ * Sums are held in fp32, and results do not depend on timing.  u and, in the
+ * backward pass, gates[t][s] u and the gradient of h are kept in `format` between
+ * the products; values past its range become infinite.
  * (Up to GEMM_MOE_MAX_TOKENS tokens without `saved` they may be kept in fp32.)
  * An infinity or a NaN reaches what is computed from it: a token's own rows, and
  * the weights' gradients of its experts.

@@ -235,16 +235,16 @@ __global__ void __launch_bounds__(256) experts_sum_kernel(ExpertsProblem p, uint
   for (long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y; t < p.T;
        t += (long long)gridDim.x * blockDim.y) {
     const int *ids = p.ids + t * p.top;
-    const uint16_t *part = ws_at<uint16_t>(p, p.at.part) + t * p.top * p.at.hpitch;
+    const float *part = ws_at<float>(p, p.at.part) + t * p.top * p.at.hpitch;
     for (int h = 8 * threadIdx.x; h < p.H; h += 8 * per) {
       float v[8] = {};
 #pragma unroll 4
       for (int s = 0; s < p.top; ++s) {
         if (ids[s] < 0 || ids[s] >= p.E) continue;
-        float w[8];
-        load8<FMT>(part, s * p.at.hpitch + h, 8, w);
+        const f32x4 *w = reinterpret_cast<const f32x4 *>(part + s * p.at.hpitch + h);
+        const f32x4 a = w[0], b = w[1];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] += w[c];
+        for (int c = 0; c < 4; ++c) v[c] += a[c], v[4 + c] += b[c];
       }
       store8<FMT>(out, t * ldo + h, p.H - h, v);
     }

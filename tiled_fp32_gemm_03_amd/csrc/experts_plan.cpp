@@ -81,7 +81,7 @@ ExpertsSpace experts_space(int T, int E, int top, int H, int I, int tile, bool b
   w.where = take(4 * pairs);
   w.counts = take(4 * w.list_groups * E);
   w.u = take(2 * pairs * w.ipitch);
-  w.part = take(2 * pairs * w.hpitch);
+  w.part = take(4 * pairs * w.hpitch);
   w.dh = backward ? take(4 * pairs * w.ipitch) : at;
   w.dg = backward ? take(4 * pairs * w.slices) : at;
   w.runs = w.tile_run = at;

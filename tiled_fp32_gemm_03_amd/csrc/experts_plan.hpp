@@ -33,7 +33,7 @@ struct ExpertsSpace {
   long long where;   // int [T top]: the place of each pair, -1 where it has none
   long long counts;  // int [list workgroups][E]
   long long u;       // 16 bits [T top][ipitch], by place: inner values (backward: times their gate)
-  long long part;    // 16 bits [T top][hpitch], by pair: what the pair adds to its token
+  long long part;    // float [T top][hpitch], by pair: what the pair adds to its token
   long long dh;      // 16 bits [T top][2 ipitch], by place: gradient of the first product
   long long dg;      // float [slices][T top], by place: parts of the gates' gradients
   // Of rows by adapter alone: the runs of one adapter (or none) that there are, as
