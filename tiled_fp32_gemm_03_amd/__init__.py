@@ -492,11 +492,11 @@ def gemm_moe(T, E, top, H, I, X, ldx, R, ldr, format, W1, ld1, S1, lds1, W2, ld2
 
 
 def _named(value, names: dict, what: str) -> int:
+    known = names.get(value)
+    if known is not None:
+        return known
     if isinstance(value, str):
-        try:
-            return names[value]
-        except KeyError:
-            raise ValueError(f"unknown {what} {value!r}; one of {sorted(names)}") from None
+        raise ValueError(f"unknown {what} {value!r}; one of {sorted(names)}")
     return int(value)
 
 
@@ -1020,12 +1020,13 @@ def moe_route(logits, top: int, score="softmax", bias=None, groups: int = 1, top
     top, groups, top_groups = int(top), int(groups), int(top_groups)
     score = _named(score, ROUTE_SCORES, "score")
     group_score = _named(group_score, ROUTE_GROUP_SCORES, "group score")
-    _fits(T, E, top, ldz, score, groups, top_groups, group_score)
-    if top < 0:
-        raise ValueError("top must not be negative")
+    if max(T, E, top, ldz, score, groups, top_groups, group_score) > _INT_MAX or min(
+            top, score, groups, top_groups, group_score) < 0:
+        _fits(T, E, top, ldz, score, groups, top_groups, group_score)
+        raise ValueError("top, groups and top_groups must not be negative")
     empty = _empty(device, stream)
-    ids = empty((T, top), dtype=torch.int32, device=device)
-    gates = empty((T, top), dtype=torch.float32, device=device)
+    ids = empty(T, top, dtype=torch.int32, device=device)
+    gates = empty(T, top, dtype=torch.float32, device=device)
     _launch(_lib.gemm_moe_route, "gemm_moe_route", device, stream,
             (T, E, top, logits.data_ptr(), ldz, fmt, score,
              bias.data_ptr() if bias is not None else None, groups, top_groups, group_score,
@@ -1044,11 +1045,15 @@ def moe_route_backward(dgates, logits, ids, score="softmax", renormalize: bool =
     if ids.shape[0] != T:
         raise ValueError(f"ids must have {T} rows, not {ids.shape[0]}")
     score = _named(score, ROUTE_SCORES, "score")
-    out = _mx_out(out, (T, E), logits.dtype, device, stream)
-    lddz = _pitch(out)
-    _fits(T, E, ids.shape[1], ldz, lddz, score)
+    if out is None:
+        out, lddz = _empty(device, stream)(T, E, dtype=logits.dtype, device=device), E or 1
+    else:
+        lddz = _pitch(_mx_out(out, (T, E), logits.dtype, device, stream))
+    top = ids.shape[1]
+    if max(T, E, top, ldz, lddz, score) > _INT_MAX:
+        _fits(T, E, top, ldz, lddz, score)
     _launch(_lib.gemm_moe_route_backward, "gemm_moe_route_backward", device, stream,
-            (T, E, ids.shape[1], dgates.data_ptr(), logits.data_ptr(), ldz, fmt, score,
+            (T, E, top, dgates.data_ptr(), logits.data_ptr(), ldz, fmt, score,
              int(bool(renormalize)), float(scale), ids.data_ptr(), out.data_ptr(), lddz))
     return out
 
@@ -1078,7 +1083,8 @@ def _experts_sizes(X, ids, gates, w1, w2):
     a1 = _expert_rows(w1, "w1", X.dtype, device, E, 2 * I, H)
     a2 = _expert_rows(w2, "w2", X.dtype, device, E, H, I)
     top = ids.shape[1]
-    _fits(T, E, top, H, I, ldx, a1[1], a1[3], a2[1], a2[3])
+    if max(T, E, top, H, I, ldx, a1[1], a1[3], a2[1], a2[3]) > _INT_MAX:
+        _fits(T, E, top, H, I, ldx, a1[1], a1[3], a2[1], a2[3])
     return device, T, E, top, H, I, ldx, a1, a2
 
 
@@ -1107,10 +1113,12 @@ def moe_experts(X, ids, gates, w1, w2, save: bool = False, out=None, workspace=N
         raise ValueError("MX weights are for up to 256 tokens, without save")
     need = _experts_bytes(T, E, top, H, I, 0)
     empty = _empty(device, stream)
-    out = _mx_out(out, (T, H), X.dtype, device, stream)
-    ldy = _pitch(out)
-    _fits(ldy)
-    saved = empty((T * top, 2 * I), dtype=torch.float32, device=device) if save else None
+    if out is None:
+        out, ldy = empty(T, H, dtype=X.dtype, device=device), H
+    else:
+        ldy = _pitch(_mx_out(out, (T, H), X.dtype, device, stream))
+        _fits(ldy)
+    saved = empty(T * top, 2 * I, dtype=torch.float32, device=device) if save else None
     workspace = _workspace(workspace, need, empty, device)
     _launch(_lib.gemm_experts, "gemm_experts", device, stream,
             (T, E, top, H, I, X.data_ptr(), ldx, ids.data_ptr(), gates.data_ptr(),
@@ -1136,10 +1144,10 @@ def moe_experts_backward(dY, X, ids, gates, w1, w2, saved, weights: bool = True,
         raise TypeError(f"saved must be a contiguous float32 tensor of shape {(T * top, 2 * I)} on {device}")
     need = _experts_bytes(T, E, top, H, I, 1)
     empty = _empty(device, stream)
-    dX = empty((T, H), dtype=X.dtype, device=device)
-    dgates = empty((T, top), dtype=torch.float32, device=device)
-    dw1 = empty((E, 2 * I, H), dtype=X.dtype, device=device) if weights else None
-    dw2 = empty((E, H, I), dtype=X.dtype, device=device) if weights else None
+    dX = empty(T, H, dtype=X.dtype, device=device)
+    dgates = empty(T, top, dtype=torch.float32, device=device)
+    dw1 = empty(E, 2 * I, H, dtype=X.dtype, device=device) if weights else None
+    dw2 = empty(E, H, I, dtype=X.dtype, device=device) if weights else None
     workspace = _workspace(workspace, need, empty, device)
     _launch(_lib.gemm_experts_backward, "gemm_experts_backward", device, stream,
             (T, E, top, H, I, dY.data_ptr(), lddy, X.data_ptr(), ldx, ids.data_ptr(),
@@ -1186,15 +1194,18 @@ def matmul_adapters(X, w, a, b, ids, scales=None, out=None, workspace=None, stre
             raise TypeError(f"scales must be a contiguous float32 tensor on {device}")
         if tuple(scales.shape) != (count,):
             raise ValueError(f"scales must have {count} values")
-    _fits(T, N, K, R, count, ldx, ldw, pa[1], pb[1])
+    if max(T, N, K, R, count, ldx, ldw, pa[1], pb[1]) > _INT_MAX:
+        _fits(T, N, K, R, count, ldx, ldw, pa[1], pb[1])
     need = _lib.gemm_adapters_workspace_bytes(T, N, K, R, count)
     if need < 0:
         raise ValueError(f"sizes outside the product's bounds: {T} rows, {N} x {K}, {count} adapters "
                          f"of rank {R}")
     empty = _empty(device, stream)
-    out = _mx_out(out, (T, N), X.dtype, device, stream)
-    ldy = _pitch(out)
-    _fits(ldy)
+    if out is None:
+        out, ldy = empty(T, N, dtype=X.dtype, device=device), N
+    else:
+        ldy = _pitch(_mx_out(out, (T, N), X.dtype, device, stream))
+        _fits(ldy)
     workspace = _workspace(workspace, need, empty, device)
     _launch(_lib.gemm_adapters, "gemm_adapters", device, stream,
             (T, N, K, R, count, X.data_ptr(), ldx, w.data_ptr(), ldw, pa[0], pa[1], pb[0], pb[1],

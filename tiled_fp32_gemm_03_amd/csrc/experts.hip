@@ -52,29 +52,35 @@ __device__ inline void count_pairs(const ExpertsProblem &p, int *count, long lon
 // Where each expert's places begin, and the row tiles, from the experts' counts
 // `n` of the first kMoeMaxExperts threads.  On return begin[e] is expert e's first place.
 // `writes`: into the workspace too.
-__device__ inline void lay_out(const ExpertsProblem &p, int n, int (*scan)[3][kMoeMaxExperts],
-                               int *begin, bool writes = true) {
-  const int e = threadIdx.x;
+__device__ inline void lay_out(const ExpertsProblem &p, int n, int (*scan)[3], int *begin,
+                               bool writes = true) {
+  const int e = threadIdx.x, lane = e & 63, wave = wave_id();
   const bool in = e < kMoeMaxExperts;
   const int tiles = p.rest && e == p.E - 1 ? 0 : (n + p.tile - 1) / p.tile;
-  if (in) scan[0][0][e] = n, scan[0][1][e] = tiles, scan[0][2][e] = n > 0;
-  __syncthreads();
-  int from = 0;
-  for (int d = 1; d < kMoeMaxExperts; d <<= 1) {
-    if (in) {
+  int upto[3] = {n, tiles, n > 0};  // sums up to this expert: in the wave, then in all
+  if (in) {
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
-        scan[from ^ 1][q][e] = scan[from][q][e] + (e >= d ? scan[from][q][e - d] : 0);
-    }
-    from ^= 1;
-    __syncthreads();
+    for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const int v = __shfl_up(upto[q], d);
+        if (lane >= d) upto[q] += v;
+      }
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (lane == 63) scan[wave][q] = upto[q];
   }
-  if (in && e < p.E) begin[e] = scan[from][0][e] - n;
+  __syncthreads();
+  if (in)
+    for (int w = 0; w < wave; ++w)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) upto[q] += scan[w][q];
+  if (in && e < p.E) begin[e] = upto[0] - n;
   if (writes && in && e < p.E) {
-    const int last = scan[from][0][e], first = last - n;
+    const int last = upto[0], first = last - n;
     int *start = ws_at<int>(p, p.at.start), *table = ws_at<int>(p, p.at.tiles);
     start[e] = first;
-    const int t0 = scan[from][1][e] - tiles;
+    const int t0 = upto[1] - tiles;
     for (int t = 0; t < tiles; ++t) {
       int *at = table + 4 + 4LL * (t0 + t);
       at[0] = e;
@@ -82,7 +88,7 @@ __device__ inline void lay_out(const ExpertsProblem &p, int n, int (*scan)[3][kM
       at[2] = n - t * p.tile < p.tile ? n - t * p.tile : p.tile;
     }
     if (p.rest && n > 0) {
-      const int run = scan[from][2][e] - 1;
+      const int run = upto[2] - 1;
       int *at = ws_at<int>(p, p.at.runs) + 4 + 4 * run, *tile_run = ws_at<int>(p, p.at.tile_run);
       at[0] = e, at[1] = first, at[2] = n;
       for (int t = (first + p.run_tile - 1) / p.run_tile; t * p.run_tile < last; ++t) tile_run[t] = run;
@@ -90,7 +96,7 @@ __device__ inline void lay_out(const ExpertsProblem &p, int n, int (*scan)[3][kM
     if (e == p.E - 1) {
       start[p.E] = last;
       table[0] = t0 + tiles;
-      if (p.rest) *ws_at<int>(p, p.at.runs) = scan[from][2][e];
+      if (p.rest) *ws_at<int>(p, p.at.runs) = upto[2];
     }
   }
   __syncthreads();
@@ -138,7 +144,7 @@ __device__ inline void place_pairs(const ExpertsProblem &p, int *begin,
 // wait for one another.
 constexpr int kCopies = 8;
 __global__ void __launch_bounds__(kOneThreads) experts_list_kernel(ExpertsProblem p) {
-  __shared__ int scan[2][3][kMoeMaxExperts];
+  __shared__ int scan[kMoeMaxExperts / 64][3];
   __shared__ int begin[kMoeMaxExperts];
   __shared__ int counts[2][kCopies][kMoeMaxExperts];  // of the pairs before this workgroup's; of the others
   __shared__ unsigned short count[kOneThreads / 64][kMoeMaxExperts];
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(kListThreads) experts_count_kernel(ExpertsProb
 
 // One workgroup: each group's counts become the places of its first pairs.
 __global__ void __launch_bounds__(kMoeMaxExperts) experts_scan_kernel(ExpertsProblem p) {
-  __shared__ int scan[2][3][kMoeMaxExperts];
+  __shared__ int scan[kMoeMaxExperts / 64][3];
   __shared__ int begin[kMoeMaxExperts];
   int *counts = ws_at<int>(p, p.at.counts) + threadIdx.x;
   int n = 0;
