@@ -281,34 +281,35 @@ __global__ void __launch_bounds__(256) adapters_sum_kernel(AdaptersProblem p) {
 }  // namespace
 
 hipError_t launch_adapters_tiles(const AdaptersProblem &p, hipStream_t s) {
+  const bool d = direct(p.X, p.ldx, p.K, p.T) && direct(p.W, p.ldw, p.K, p.N);
+  const bool w = by_words(p.X, p.K) && by_words(p.W, p.K);
+  const int tile = d ? p.at.tile : Small::BM;
   ExpertsProblem order{};
   order.T = p.T, order.E = p.count + 1, order.top = 1, order.ids = p.ids;
-  order.tile = kAdaptersRows, order.rest = 1, order.run_tile = p.at.tile;
+  order.tile = kAdaptersRows, order.rest = 1, order.run_tile = tile;
   order.ws = p.ws, order.at = p.at.order;
   hipError_t e = launch_list(order, s);
   if (e == hipSuccess && p.count > 0) {
-    const bool d = direct(p.X, p.ldx, p.K, p.T) && direct(p.A, p.lda, p.K, p.R);
-    const bool w = by_words(p.X, p.K) && by_words(p.A, p.K);
+    const bool ad = direct(p.X, p.ldx, p.K, p.T) && direct(p.A, p.lda, p.K, p.R);
+    const bool aw = by_words(p.X, p.K) && by_words(p.A, p.K);
     const long long tiles =
         p.at.order.most_tiles * ceil_div(p.R, Narrow::BN) * p.at.splits;
     auto low = [&](auto how) {
       constexpr int S = decltype(how)::value;
       return GEMM_F32_LAUNCH_ROWS(adapters_low_kernel, Narrow, S, tiles);
     };
-    e = d ? low(std::integral_constant<int, kDirect>{})
-          : w ? low(std::integral_constant<int, kByWords>{})
-              : low(std::integral_constant<int, kAnyRows>{});
+    e = ad ? low(std::integral_constant<int, kDirect>{})
+           : aw ? low(std::integral_constant<int, kByWords>{})
+                : low(std::integral_constant<int, kAnyRows>{});
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)ceil_div(p.T * (p.at.rpitch / 4), 256));
     e = p.format == kBf16 ? launch_kernel(adapters_join_kernel<kBf16>, grid, dim3(256), s, p)
                           : launch_kernel(adapters_join_kernel<kF16>, grid, dim3(256), s, p);
   }
   if (e != hipSuccess) return e;
-  const bool d = direct(p.X, p.ldx, p.K, p.T) && direct(p.W, p.ldw, p.K, p.N);
-  const bool w = by_words(p.X, p.K) && by_words(p.W, p.K);
-  const long long all = ceil_div(p.T, p.at.tile) * ceil_div(p.N, p.at.tile) * p.at.wide_splits;
-  e = choose_tiles(p.at.tile, all, d, w, [&](auto tile, auto how) {
-    typedef decltype(tile) T;
+  const long long all = ceil_div(p.T, tile) * ceil_div(p.N, tile) * p.at.wide_splits;
+  e = choose_tiles(tile, all, d, w, [&](auto tiles, auto how) {
+    typedef decltype(tiles) T;
     constexpr int S = decltype(how)::value;
     return GEMM_F32_LAUNCH_ROWS(adapters_wide_kernel, T, S, all);
   });

@@ -282,14 +282,22 @@ __global__ void __launch_bounds__(256) experts_dgates_kernel(ExpertsProblem p) {
 
 }  // namespace
 
-hipError_t launch_experts_forward(const ExpertsProblem &p, hipStream_t s) {
+// The products of a pass take the list's row tiles, so all of them are of one size.
+hipError_t launch_experts_forward(const ExpertsProblem &call, hipStream_t s) {
+  ExpertsProblem p = call;
+  p.tile = up_direct(p) && down_direct(p) ? experts_tile(p.T, p.E, p.top, p.H, p.I, p.saved != nullptr)
+                                          : Small::BM;
+  p.at = experts_space(p.T, p.E, p.top, p.H, p.I, p.tile, false);
   hipError_t e = launch_list(p, s);
   if (e == hipSuccess) e = launch_experts_up(p, s);
   if (e == hipSuccess) e = launch_experts_down(p, s);
   return e == hipSuccess ? launch_sum(p, p.Y, p.ldy, s) : e;
 }
 
-hipError_t launch_experts_backward(const ExpertsProblem &p, hipStream_t s) {
+hipError_t launch_experts_backward(const ExpertsProblem &call, hipStream_t s) {
+  ExpertsProblem p = call;
+  p.tile = du_direct(p) && dx_direct(p) ? experts_tile(p.T, p.E, p.top, p.H, p.I, true) : Small::BM;
+  p.at = experts_space(p.T, p.E, p.top, p.H, p.I, p.tile, true);
   hipError_t e = launch_list(p, s);
   if (e == hipSuccess && (p.dgates || p.dX || p.dW1 || p.dW2)) e = launch_experts_du(p, s);
   if (e == hipSuccess && p.dgates && p.T > 0)

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_dx_kerne
 }  // namespace
 
 hipError_t launch_experts_down(const ExpertsProblem &p, hipStream_t s) {
-  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.H, p.tile), direct(p.W2, p.ld2, p.I, p.H), by_words(p.W2, p.I),
+  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.H, p.tile), down_direct(p), by_words(p.W2, p.I),
                       [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
@@ -132,7 +132,7 @@ hipError_t launch_experts_down(const ExpertsProblem &p, hipStream_t s) {
 }
 
 hipError_t launch_experts_dx(const ExpertsProblem &p, hipStream_t s) {
-  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.H, p.tile), direct(p.W1, p.ld1, p.H, kStepK), by_words(p.W1, p.H),
+  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.H, p.tile), dx_direct(p), by_words(p.W1, p.H),
                       [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;

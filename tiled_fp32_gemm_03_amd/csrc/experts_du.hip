@@ -107,9 +107,8 @@ __global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_du_kerne
 }  // namespace
 
 hipError_t launch_experts_du(const ExpertsProblem &p, hipStream_t s) {
-  const bool d = direct(p.dY, p.lddy, p.H, p.T) && direct(p.W2, p.ld2, p.I, kStepK);
   const bool w = by_words(p.dY, p.H) && by_words(p.W2, p.I);
-  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.I, p.tile), d, w, [&](auto tile, auto how) {
+  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.I, p.tile), du_direct(p), w, [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
     const long long tiles = p.at.most_tiles * ceil_div(p.I, T::BN);

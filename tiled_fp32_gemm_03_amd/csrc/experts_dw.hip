@@ -141,15 +141,18 @@ __global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_dw2_kern
 
 hipError_t launch_experts_dw(const ExpertsProblem &p, hipStream_t s) {
   hipError_t e = hipSuccess;
-  if (p.dW1) e = choose_tiles(p.tile, p.E * ceil_div(2 * p.at.ipitch, p.tile) * ceil_div(p.H, p.tile), direct(p.X, p.ldx, p.H, p.T), by_words(p.X, p.H),
-                                    [&](auto tile, auto how) {
+  // (These tiles are not the list's: each of the two has its own.)
+  const bool d1 = direct(p.X, p.ldx, p.H, p.T), d2 = direct(p.dY, p.lddy, p.H, p.T);
+  const int t1 = d1 ? p.tile : Small::BM, t2 = d2 ? p.tile : Small::BM;
+  if (p.dW1) e = choose_tiles(t1, p.E * ceil_div(2 * p.at.ipitch, t1) * ceil_div(p.H, t1), d1, by_words(p.X, p.H),
+                              [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
     const long long tiles = p.E * ceil_div(2 * p.at.ipitch, T::BM) * ceil_div(p.H, T::BN);
     return GEMM_F32_LAUNCH_ROWS(experts_dw1_kernel, T, S, tiles);
   });
   if (e != hipSuccess || !p.dW2) return e;
-  return choose_tiles(p.tile, p.E * ceil_div(p.H, p.tile) * ceil_div(p.I, p.tile), direct(p.dY, p.lddy, p.H, p.T), by_words(p.dY, p.H),
+  return choose_tiles(t2, p.E * ceil_div(p.H, t2) * ceil_div(p.I, t2), d2, by_words(p.dY, p.H),
                       [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;

@@ -147,7 +147,7 @@ AdaptersSpace adapters_space(int T, int N, int K, int R, int count) {
     o.where = take(4LL * T);
     o.counts = take(4 * o.list_groups * E);
     o.runs = take(16 + 16LL * (E < T ? E : T));
-    o.tile_run = take(4 * ceil_div(T, w.tile));
+    o.tile_run = take(4 * ceil_div(T, 128));  // (of either tile)
   }
   w.bytes = at;
   return w;

@@ -76,6 +76,16 @@ inline bool by_words(const void *p, long long width) {
   return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && width >= 8;
 }
 
+// The products of a pass whose row tiles are the list's.
+inline bool up_direct(const ExpertsProblem &p) {
+  return direct(p.X, p.ldx, p.H, p.T) && direct(p.W1, p.ld1, p.H, 2LL * p.I);
+}
+inline bool down_direct(const ExpertsProblem &p) { return direct(p.W2, p.ld2, p.I, p.H); }
+inline bool du_direct(const ExpertsProblem &p) {
+  return direct(p.dY, p.lddy, p.H, p.T) && direct(p.W2, p.ld2, p.I, kStepK);
+}
+inline bool dx_direct(const ExpertsProblem &p) { return direct(p.W1, p.ld1, p.H, kStepK); }
+
 // KERN on at most `tiles` tiles: as many workgroups as the chip holds at once.
 template <auto KERN, int THREADS, class P>
 hipError_t launch_tiles(const P &p, long long tiles, hipStream_t s) {
@@ -108,7 +118,8 @@ inline long long even_tiles(const ExpertsProblem &p) {
 }
 
 // `make(tile, integral_constant S)` launches, about `tiles` tiles.  Large tiles are loaded directly
-// alone (through registers a wave of 128 x 128 has none left for its loads).
+// alone (through registers a wave of 128 x 128 has none left for its loads): a call
+// whose row tiles are a list's asks for them only where all its products are.
 template <class Make>
 hipError_t choose_tiles(int tile, long long tiles, bool direct_loads, bool words, Make make) {
   if (direct_loads) {
@@ -116,6 +127,7 @@ hipError_t choose_tiles(int tile, long long tiles, bool direct_loads, bool words
     if (tiles <= kFewTiles) return make(Deep{}, std::integral_constant<int, kDirect>{});
     return make(Small{}, std::integral_constant<int, kDirect>{});
   }
+  if (tile != Small::BM) return hipErrorInvalidValue;
   if (words) return make(Small{}, std::integral_constant<int, kByWords>{});
   return make(Small{}, std::integral_constant<int, kAnyRows>{});
 }

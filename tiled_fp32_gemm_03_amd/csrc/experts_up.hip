@@ -99,9 +99,8 @@ __global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) experts_up_save_
 }  // namespace
 
 hipError_t launch_experts_up(const ExpertsProblem &p, hipStream_t s) {
-  const bool d = direct(p.X, p.ldx, p.H, p.T) && direct(p.W1, p.ld1, p.H, 2LL * p.I);
   const bool w = by_words(p.X, p.H) && by_words(p.W1, p.H);
-  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.I, p.tile / 2), d, w, [&](auto tile, auto how) {
+  return choose_tiles(p.tile, even_tiles(p) * ceil_div(p.I, p.tile / 2), up_direct(p), w, [&](auto tile, auto how) {
     typedef decltype(tile) T;
     constexpr int S = decltype(how)::value;
     const long long tiles = p.at.most_tiles * ceil_div(p.I, T::BN / 2);

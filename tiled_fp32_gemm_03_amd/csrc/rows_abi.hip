@@ -90,13 +90,13 @@ extern "C" int gemm_moe_route_backward(int T, int E, int top, const float *dgate
 namespace {
 
 long long experts_bytes(int T, int E, int top, int H, int I, bool backward) {
-  const long long tiles =
-      experts_space(T, E, top, H, I, experts_tile(T, E, top, H, I, true), backward).bytes;
+  // (of smaller tiles: they need the most)
+  const long long tiles = experts_space(T, E, top, H, I, 128, backward).bytes;
   if (backward) return tiles;
-  long long most = experts_space(T, E, top, H, I, experts_tile(T, E, top, H, I, false), false).bytes;
+  long long most = tiles;
   if (T <= kMoeMaxTokens && moe_space(T, E, top, H, I).bytes > most)
     most = moe_space(T, E, top, H, I).bytes;
-  return most > tiles ? most : tiles;
+  return most;
 }
 
 bool bad_workspace(const void *ws, long long bytes, long long need) {
@@ -157,8 +157,6 @@ extern "C" int gemm_experts(int T, int E, int top, int H, int I, const void *X, 
   p.W1 = static_cast<const uint16_t *>(W1), p.ld1 = ld1;
   p.W2 = static_cast<const uint16_t *>(W2), p.ld2 = ld2;
   p.Y = static_cast<uint16_t *>(Y), p.ldy = ldy, p.saved = saved, p.ws = ws;
-  p.tile = experts_tile(T, E, top, H, I, saved != nullptr);
-  p.at = experts_space(T, E, top, H, I, p.tile, false);
   return launch_status(launch_experts_forward(p, s), "experts");
 }
 
@@ -201,8 +199,6 @@ extern "C" int gemm_experts_backward(int T, int E, int top, int H, int I, const 
   p.dW1 = static_cast<uint16_t *>(dW1), p.lddw1 = lddw1;
   p.dW2 = static_cast<uint16_t *>(dW2), p.lddw2 = lddw2;
   p.ws = static_cast<unsigned char *>(workspace);
-  p.tile = experts_tile(T, E, top, H, I, true);
-  p.at = experts_space(T, E, top, H, I, p.tile, true);
   return launch_status(launch_experts_backward(p, static_cast<hipStream_t>(stream)),
                        "experts backward");
 }
