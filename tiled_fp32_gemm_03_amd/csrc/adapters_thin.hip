@@ -312,8 +312,18 @@ __global__ void __launch_bounds__(kThinThreads) adapters_rounds_kernel(AdaptersP
     xv[q] = r < p.T && r < 16 * RB ? (at & ~3) + 16 * c : kOutside;
   }
   const int steps = (p.K + kStepK - 1) / kStepK, rounds = (steps + KS - 1) / KS;
-  auto issue = [&](int round, int stage) __attribute__((always_inline)) {
+  // A workgroup's n-th round, past the end the one after the last.  Workgroups begin at
+  // places spread over K and go round: rows a power of two apart lie in few channels
+  // of the memory at any one k (64 rows, 16384 x 8192: 104 us from the first round, 90 so; one row,
+  // 4096 x 4096: 16.3 and 15.8).
+  const int shift = (int)((long long)blockIdx.x * rounds / gridDim.x);
+  auto round_of = [&](int n) __attribute__((always_inline)) {
+    const int r = n + shift;
+    return uniform(n >= rounds ? rounds : r < rounds ? r : r - rounds);
+  };
+  auto issue = [&](int n, int stage) __attribute__((always_inline)) {
     const unsigned to = lds_u + stage * R::STAGE;
+    const int round = round_of(n);
 #pragma unroll
     for (int q = 0; q < R::X_LOADS; ++q) {
       const int k0 = kStepK * (round * KS + part[q]);
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(kThinThreads) adapters_rounds_kernel(AdaptersP
     ks_lds_barrier();  // everyone's; the stage of round i - 1 is free
     issue(i + R::STAGES - 1, ahead);  // past the end: zeros
     const unsigned char *st = lds + stage * R::STAGE;
-    const int left = p.K - kStepK * (i * KS + first);
+    const int left = p.K - kStepK * (round_of(i) * KS + first);
 #pragma unroll
     for (int kg = 0; kg < 2; ++kg) {
       const i16x8 wf = read_round<WORDS>(st + KS * R::X + wave * R::W, 0, kg, lane, ws_shift, left);

@@ -120,7 +120,7 @@ struct Chunk {
 // parts, each of whole steps and K values) the second part.
 template <int W, int S, int NW>
 struct KcSide {
-  static constexpr bool kDown = false;
+  static constexpr bool kDown = false, kListed = false;
   static constexpr int kLoads = W / 8 / NW;
   const void *base;
   int records;
@@ -192,7 +192,7 @@ __device__ __forceinline__ void put_down(char *st, int r, int c, u32x4 v, bool i
 // from `second` on.
 template <int W, int S, int NW>
 struct KmSide {
-  static constexpr bool kDown = true;
+  static constexpr bool kDown = true, kListed = false;
   static constexpr int kLoads = W / 8 / NW, kChunks = W / 8;
   rsrc_t rsrc;
   int voff[S == kDirect ? kLoads : 1];
@@ -249,7 +249,7 @@ struct KmSide {
 // is read a step ahead.
 template <int W, int S, int NW>
 struct KmListSide {
-  static constexpr bool kDown = true;
+  static constexpr bool kDown = true, kListed = true;  // (its steps come in order)
   static constexpr int kLoads = W / 8 / NW, kChunks = W / 8;
   rsrc_t rsrc;
   int records;
@@ -384,6 +384,21 @@ __device__ inline void store_eights(uint16_t *row, const Eights &e, int left) {
     if (c < left) row[e.at + c] = (uint16_t)(e.v[c >> 1] >> (16 * (c & 1)));
 }
 
+// The first of a workgroup's n steps: each begins at another place in k and goes round
+// (next_step).  Rows a power of two apart lie in few channels of an L2 at any one k, and of the
+// memory: workgroups of one XCD begin up to three steps apart (what they share is still
+// in its L2), XCDs an eighth of k.  (All from the first step, and so, us: 16,384 pairs of 8
+// experts, 4096 / 4096 1,585 and 1,502; a training step of 64 experts, 2048 / 1024 1,385
+// and 1,373; of 7, 1000 / 517 164 and 166; 8,192 rows with adapters, 4096 x 4096 253 and 255.)
+template <class Op>
+__device__ __forceinline__ int first_of(int n) {
+  if constexpr (Op::A::kListed || Op::B::kListed) return 0;
+  if (n < 4) return 0;  // uniform
+  const int from = n * (int)(blockIdx.x & 7) / 8 + (int)(blockIdx.x >> 3 & 3);
+  return uniform(from < n ? from : from - n);
+}
+__device__ __forceinline__ int next_step(int kk, int n) { return kk + 1 == n ? 0 : kk + 1; }
+
 // tile_loop with more than two stages: the loads of STAGES - 1 steps are on their way.
 template <class T, int FMT, int S, class Op>
 __device__ __forceinline__ void deep_tiles(char *lds, Op &op, int count, int wave, int lane) {
@@ -391,10 +406,12 @@ __device__ __forceinline__ void deep_tiles(char *lds, Op &op, int count, int wav
   constexpr int kLoads = T::A_LOADS + T::B_LOADS, kAhead = T::STAGES - 1;
   const unsigned lds_u = (unsigned)(uintptr_t)(lds_void_t *)lds;
   const int wm = wave / T::WGN, wn = wave % T::WGN;
-  auto issue = [&](int kk, int at) __attribute__((always_inline)) {
+  int place = 0;
+  auto issue = [&](int n, int at) __attribute__((always_inline)) {
     const unsigned stage = (unsigned)uniform((int)(lds_u + at * T::STAGE));
-    side_begin(op.a, kk, wave, lane);
-    side_begin(op.b, kk, wave, lane);
+    side_begin(op.a, place, wave, lane);
+    side_begin(op.b, place, wave, lane);
+    place = next_step(place, n);
 #pragma unroll
     for (int q = 0; q < T::A_LOADS; ++q) side_issue(op.a, q, stage, wave, lane);
 #pragma unroll
@@ -406,20 +423,21 @@ __device__ __forceinline__ void deep_tiles(char *lds, Op &op, int count, int wav
     const int nk = job.steps, blocks = blocks_of<T>(job.rows, wm);
     op.fetch(job);
     op.begin(job);
+    place = first_of<Op>(nk);
 #pragma unroll 1
-    for (int kk = 0; kk < kAhead && kk < nk; ++kk) issue(kk, kk);
+    for (int kk = 0; kk < kAhead && kk < nk; ++kk) issue(nk, kk);
     f32x4 acc[T::TBM][T::TBN];
 #pragma unroll
     for (int i = 0; i < T::TBM; ++i)
 #pragma unroll
       for (int j = 0; j < T::TBN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     int stage = 0;
-    auto step = [&](auto more, int kk) __attribute__((always_inline)) {
+    auto step = [&](auto more) __attribute__((always_inline)) {
       constexpr bool MORE = decltype(more)::value;
       // This step's own loads, which at least those of kAhead - 1 steps follow.
       __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(MORE ? kLoads * (kAhead - 1) : 0));
       ks_lds_barrier();  // everyone's; the stage of the step before is free
-      if constexpr (MORE) issue(kk + kAhead, stage == 0 ? kAhead : stage - 1);
+      if constexpr (MORE) issue(nk, stage == 0 ? kAhead : stage - 1);
       const char *st = lds + stage * T::STAGE;
 #pragma unroll
       for (int kg = 0; kg < kStepK / 32; ++kg) {
@@ -441,9 +459,9 @@ __device__ __forceinline__ void deep_tiles(char *lds, Op &op, int count, int wav
     };
     int kk = 0;
 #pragma unroll 1
-    for (; kk + kAhead < nk; ++kk) step(std::true_type{}, kk);
+    for (; kk + kAhead < nk; ++kk) step(std::true_type{});
 #pragma unroll 1
-    for (; kk < nk; ++kk) step(std::false_type{}, kk);
+    for (; kk < nk; ++kk) step(std::false_type{});
     op.store(job, acc, wave, lane);
     ks_lds_barrier();  // the next tile's loads overwrite the LDS
   }
@@ -494,12 +512,13 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
 #pragma unroll
     for (int q = 0; q < T::B_LOADS; ++q) op.b.put(stage + T::A_BYTES, q, wave, lane);
   };
-  int stage = 0;
+  int stage = 0, place = 0;
   // The first step of a job that has one.
   auto first_step = [&](const typename Op::Job &j) __attribute__((always_inline)) {
     op.begin(j);
-    side_begin(op.a, 0, wave, lane);
-    side_begin(op.b, 0, wave, lane);
+    place = first_of<Op>(j.steps);
+    side_begin(op.a, place, wave, lane);
+    side_begin(op.b, place, wave, lane);
     if constexpr (S == kDirect) {
       issue(lds_u + stage * T::STAGE, 0, kLoads);
     } else {
@@ -524,7 +543,7 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
       for (int j = 0; j < T::TBN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     // A step; MORE: another of this tile follows; FULL: every row block has rows (a
     // branch to each block costs a lone wave a tenth of its rate).
-    auto step = [&](auto more, auto full, int kk) __attribute__((always_inline)) {
+    auto step = [&](auto more, auto full) __attribute__((always_inline)) {
       constexpr bool MORE = decltype(more)::value, FULL = decltype(full)::value;
       if constexpr (S == kDirect) __builtin_amdgcn_s_waitcnt(vmcnt_wait_imm(0));  // own loads
       ks_lds_barrier();  // everyone's; the other stage is free
@@ -532,8 +551,9 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
       stage ^= 1;
       const unsigned nst = lds_u + stage * T::STAGE;
       if constexpr (MORE) {
-        side_begin(op.a, kk + 1, wave, lane);
-        side_begin(op.b, kk + 1, wave, lane);
+        place = next_step(place, nk);
+        side_begin(op.a, place, wave, lane);
+        side_begin(op.b, place, wave, lane);
         if constexpr (S != kDirect) load();
       } else if (next) {
         op.fetch(after);
@@ -599,12 +619,12 @@ __device__ __forceinline__ void tile_loop(char *lds, Op &op, int count, int wave
     };
     if (blocks == T::TBM) {
 #pragma unroll 1
-      for (int kk = 0; kk + 1 < nk; ++kk) step(std::true_type{}, std::true_type{}, kk);
+      for (int kk = 0; kk + 1 < nk; ++kk) step(std::true_type{}, std::true_type{});
     } else {
 #pragma unroll 1
-      for (int kk = 0; kk + 1 < nk; ++kk) step(std::true_type{}, std::false_type{}, kk);
+      for (int kk = 0; kk + 1 < nk; ++kk) step(std::true_type{}, std::false_type{});
     }
-    if (nk > 0) step(std::false_type{}, std::false_type{}, nk - 1);
+    if (nk > 0) step(std::false_type{}, std::false_type{});
     if (next) {
       if (nk <= 0) op.fetch(after);
       if (after.steps > 0) first_step(after);
