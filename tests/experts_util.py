@@ -6,7 +6,7 @@ terms' magnitudes.  With hs half a step of the 16-bit format, s = 1 / (1 + exp(-
   p, q (first product)      ep, eq: that bound
   u = p s q                 |silu'| <= 1.1: (|silu| + 1.1 ep)(|q| + eq) - |silu q|, and 2^-20 |u|
                             for exp, division and products in fp32; kept in 16 bits: hs more
-  a choice's term of y      gate |W2| (error of u), its own fp32 sum, kept in 16 bits: hs
+  a choice's term of y      gate |W2| (error of u), its own fp32 sum, kept in fp32: 2^-24
   v = W2^T dy               ev: the bound of its sum
   dp = gate v q f(p)        f = s (1 + p (1 - s)), |f| <= 1.1, |f'| <= 0.5, and f itself is off by
                             2^-20 at most: gate ((|v| + ev)(|q| + eq)(|f| + 0.5 ep + 2^-20) - |v q f|), hs
@@ -57,7 +57,7 @@ def reference(x, ids, gates, w1, w2, dy=None):
         t, at = _mm(u, a2.t()), a2.abs().t()
         bt = _mm(ru, at) + (I + 8) * eps * _mm(u.abs() + ru, at)
         gt, gb = g * t, g.abs() * bt * (1 + eps)
-        gb = gb + hs * (gt.abs() + gb) + tiny
+        gb = gb + 2.0 ** -24 * (gt.abs() + gb)
         y.index_add_(0, tok, gt)
         by.index_add_(0, tok, gb)
         mag.index_add_(0, tok, gt.abs() + gb)
@@ -75,7 +75,7 @@ def reference(x, ids, gates, w1, w2, dy=None):
         bp, bq = (b + (hs + 2.0 ** -20) * (d.abs() + b) + tiny for b, d in ((bp, dp), (bq, dq)))
         dh, bdh = torch.cat((dp, dq), 1), torch.cat((bp, bq), 1)
         r, br = _mm(dh, a1), _mm(bdh, a1.abs()) + (2 * I + 8) * eps * _mm(dh.abs() + bdh, a1.abs())
-        br = br + hs * (r.abs() + br) + tiny
+        br = br + 2.0 ** -24 * (r.abs() + br)
         dx.index_add_(0, tok, r)
         bdx.index_add_(0, tok, br)
         mdx.index_add_(0, tok, r.abs() + br)
