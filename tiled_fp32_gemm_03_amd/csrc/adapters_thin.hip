@@ -1,8 +1,8 @@
 // A shared projection with low-rank adapters for few rows (gemm_adapters.h), 64 at a
 // time: single tokens of many requests.  Two launches: scale A[r] x by a workgroup to each
 // adapter that is asked and 16 of its ranks, and the projection, which reads W once,
-// straight into the matrix instructions' operands (mx_thin.hpp), and the asked
-// adapters' B.
+// through a ring of LDS stages or, matrices that this cannot address, straight into the
+// matrix instructions' operands (mx_thin.hpp), and the asked adapters' B.
 //
 // 64 rows, 16384 x 8192, 32 adapters of rank 64: 90 us, 4.0 TB/s of W, A and B; x goes
 // through each compute unit's LDS beside W, as many bytes again.
