@@ -1,0 +1,48 @@
+"""The experts' products where a row names an expert more than once, so that one expert has
+more choices than there are tokens, and a token more choices than there are experts; on
+workspaces of NaN.  Bounds in experts_util.py."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from experts_util import check, reference  # noqa: E402
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def g():
+    import tiled_fp32_gemm_03_amd as lib
+    return lib
+
+
+def _check(g, T, E, top, H, I, ids, dtype, weights, what):
+    print(f"case: experts repeats {what}", flush=True)
+    rng = np.random.default_rng(T + 7 * E + 11 * top + 13 * H + 17 * I)
+    dev = torch.device("cuda:0")
+    to = lambda *s, by=1.0: torch.from_numpy((rng.standard_normal(s) / by).astype(np.float32)).to(dev, dtype)  # noqa: E731
+    x, w1, w2 = to(T, H), to(E, 2 * I, H, by=H ** .5), to(E, H, I, by=I ** .5)
+    gates = torch.from_numpy((rng.random((T, top)) - 0.2).astype(np.float32)).to(dev)
+    ids = torch.from_numpy(np.asarray(ids).astype(np.int32)).to(dev)
+    v1, v2 = w1, w2
+    if weights == "mx":
+        q1, q2 = g.mx_quantize(w1.reshape(-1, H)), g.mx_quantize(w2.reshape(-1, I))
+        v1 = g.mx_dequantize(q1, dtype=dtype).reshape(w1.shape)
+        v2 = g.mx_dequantize(q2, dtype=dtype).reshape(w2.shape)
+        w1 = g.MxTensor(q1.codes.reshape(E, 2 * I, -1), q1.scales.reshape(E, 2 * I, -1), H)
+        w2 = g.MxTensor(q2.codes.reshape(E, H, -1), q2.scales.reshape(E, H, -1), I)
+    ws = torch.full((g.gemm_experts_workspace_bytes(T, E, top, H, I, 0),), 255, dtype=torch.uint8, device=dev)
+    ref = reference(x, ids, gates, v1, v2)["y"]
+    check(g.moe_experts(x, ids, gates, w1, w2, workspace=ws), ref, what)
+
+
+@pytest.mark.parametrize("weights", ["w16", "mx"])
+@pytest.mark.parametrize("E,top", [(1, 3), (1, 6), (2, 3), (2, 4), (2, 6), (3, 16), (2, 16), (7, 12)])
+def test_one_token_with_more_choices_than_experts(g, E, top, weights):
+    for fmt, dtype in DT.items():
+        for name, ids in (("in turn", np.arange(top)[None] % E), ("all of one", np.full((1, top), E - 1)),
+                          ("some dropped", (np.arange(top)[None] % (E + 1)) - 1)):
+            _check(g, 1, E, top, 264, 72, ids, dtype, weights, ("one token", E, top, weights, fmt, name))

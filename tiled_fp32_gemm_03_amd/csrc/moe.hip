@@ -620,7 +620,9 @@ MoeShape shape_of(long long experts, int columns, int K, int rows) {
 }
 template <int W, int A, int NB, class Kernel>
 hipError_t launch_experts(Kernel kern, const MoeProblem &p, int columns, int K, hipStream_t s) {
-  const int experts = p.E < p.T * p.top ? p.E : p.T * p.top;
+  // Workgroups to an expert that is asked or, one token, to each of its choices (a choice
+  // made before may name an expert more than once).
+  const int experts = p.T == 1 || p.T * p.top < p.E ? p.T * p.top : p.E;
   MoeShape sh = shape_of<W, A>(experts, columns, K, p.T);
   MoeProblem q = p;
   void *args[] = {&q, &sh};
