@@ -21,11 +21,11 @@ def g():
 
 def _check(g, T, E, top, H, I, ids, dtype, weights, what):
     print(f"case: experts repeats {what}", flush=True)
-    rng = np.random.default_rng(T + 7 * E + 11 * top + 13 * H + 17 * I)
     dev = torch.device("cuda:0")
-    to = lambda *s, by=1.0: torch.from_numpy((rng.standard_normal(s) / by).astype(np.float32)).to(dev, dtype)  # noqa: E731
+    gen = torch.Generator(device=dev).manual_seed(T + 7 * E + 11 * top + 13 * H + 17 * I)
+    to = lambda *s, by=1.0: (torch.randn(s, generator=gen, device=dev) / by).to(dtype)  # noqa: E731
     x, w1, w2 = to(T, H), to(E, 2 * I, H, by=H ** .5), to(E, H, I, by=I ** .5)
-    gates = torch.from_numpy((rng.random((T, top)) - 0.2).astype(np.float32)).to(dev)
+    gates = torch.rand(T, top, generator=gen, device=dev) - 0.2
     ids = torch.from_numpy(np.asarray(ids).astype(np.int32)).to(dev)
     v1, v2 = w1, w2
     if weights == "mx":
@@ -46,3 +46,16 @@ def test_one_token_with_more_choices_than_experts(g, E, top, weights):
         for name, ids in (("in turn", np.arange(top)[None] % E), ("all of one", np.full((1, top), E - 1)),
                           ("some dropped", (np.arange(top)[None] % (E + 1)) - 1)):
             _check(g, 1, E, top, 264, 72, ids, dtype, weights, ("one token", E, top, weights, fmt, name))
+
+
+# an expert with more choices than tokens: in turns of 4, 8 and 16, up to several of each
+@pytest.mark.parametrize("weights", ["w16", "mx"])
+@pytest.mark.parametrize("T,top,H,I", [(2, 3, 2048, 1024), (2, 16, 520, 2048), (3, 2, 2049, 1025), (4, 4, 2048, 2048), (4, 13, 257, 130), (5, 2, 2048, 1024),
+                                       (6, 5, 1000, 2048), (8, 16, 2048, 520), (7, 9, 4097, 65), (9, 4, 2048, 520), (8, 3, 4096, 4096)])
+def test_an_expert_with_more_choices_than_tokens(g, T, top, H, I, weights):
+    E = 24
+    for fmt, dtype in DT.items():
+        most = np.full((T, top), 5)
+        most[0, 0], most[-1, -1] = 7, -1
+        for name, ids in (("all of one", np.full((T, top), E - 1)), ("most of one", most)):
+            _check(g, T, E, top, H, I, ids, dtype, weights, ("few tokens", T, top, H, I, weights, fmt, name))

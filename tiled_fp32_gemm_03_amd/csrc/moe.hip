@@ -335,9 +335,10 @@ __device__ inline int given_expert(const MoeProblem &p, int i) {
   return e >= 0 && e < p.E ? e : -1;
 }
 
-// What the launch chose: waves, waves per group, groups per wave, the tile's LDS.
+// What the launch chose: waves, waves per group, groups per wave, the tile's LDS, and the
+// most rows that it has room for.
 struct MoeShape {
-  int waves, ks, each, lds;
+  int waves, ks, each, lds, rows;
   __host__ __device__ int threads() const { return 64 * waves; }
 };
 
@@ -489,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeProblem p, MoeSh
     w[0] = {p.W1 + r * p.ld1, p.S1 + r * p.lds1};
     w[1] = {p.W1 + (r + p.I) * p.ld1, p.S1 + (r + p.I) * p.lds1};
   };
-  for (int m0 = 0; m0 < x.n; m0 += 16) {
-    const int n = x.n - m0 < 16 ? x.n - m0 : 16;
+  for (int m0 = 0; m0 < x.n; m0 += sh.rows) {
+    const int n = x.n - m0 < sh.rows ? x.n - m0 : sh.rows;
     if ((int)threadIdx.x < n) {
       const int at = x.first + m0 + threadIdx.x;
       const int pair = ONE ? at : ws_at<int>(p, p.at.list)[at];
@@ -527,8 +528,8 @@ __global__ void __launch_bounds__(64 * kMostWaves, 2) moe_down_kernel(MoeProblem
     const long long r = (long long)p.H * x.e + h;
     w[0] = {p.W2 + r * p.ld2, p.S2 + r * p.lds2};
   };
-  for (int m0 = 0; m0 < x.n; m0 += 16) {
-    const int n = x.n - m0 < 16 ? x.n - m0 : 16;
+  for (int m0 = 0; m0 < x.n; m0 += sh.rows) {
+    const int n = x.n - m0 < sh.rows ? x.n - m0 : sh.rows;
     auto row = [&](int r) __attribute__((always_inline)) {
       return p.ws + p.at.u + 4 * (x.first + m0 + r) * p.at.upitch;
     };
@@ -583,7 +584,8 @@ int tile_bytes(int rows, int K, int ks) {
   return most;
 }
 // The shape of a product over `experts` experts, `columns` columns and K, of
-// at most `rows` rows each.
+// at most `rows` rows each.  (Where a choice made before names an expert more than once in
+// a row, it may have more than that: they are taken in turns of as many as the LDS is for.)
 template <int W, int A>
 MoeShape shape_of(long long experts, int columns, int K, int rows) {
   const long long groups = experts * ceil_div(columns, 16);
@@ -597,6 +599,7 @@ MoeShape shape_of(long long experts, int columns, int K, int rows) {
   // bf16 160 and 168; 2, 4000 / 2500, bf16 70 and 67; 20, 8000 / 2100, fp16 202 and 219.
   const long long pieces = ceil_div(K, kPieceK<W>);
   sh.waves = kWaves;
+  sh.rows = tile_rows(rows);
   sh.ks = 1;
   while (sh.ks < kWaves && 2 * sh.ks <= pieces && groups * sh.ks < 4 * 256) sh.ks *= 2;
   if (W != kMx && sh.ks == 1 && groups < 8 * 256 && pieces >= 16) sh.ks = 2;
