@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves<LANES>) route_kernel(RoutePro
     for (int i = 0; i < P; ++i) zmax = max_of(zmax, z[i]);
     zmax = token_max<LANES>(zmax);
   }
-  // The choice: by the scores where a bias or a sum enters, else by the logits.
+  // Keys are scores where a bias or a sum enters, else logits.
   const bool by_score = p.bias != nullptr || (choose_groups && p.group_score == kGroupTop2);
   if (softmax && (by_score || !p.renormalize)) {
     double numbers = 0.0;
@@ -188,7 +188,9 @@ __global__ void __launch_bounds__(64 * kRouteWaves<LANES>) route_kernel(RoutePro
     for (int i = 0; i < P; ++i) {
       const int e = sub + LANES * i, g = (int)(((float)e + 0.5f) * per);
       const bool stays = e < p.E && (kept >> ((e < p.E ? g : 0) * L) & 1);
-      key[i] = stays ? key[i] : kLow;
+      // (without a bias scores are for the groups' sums alone: they may be rounded to 0 or 1)
+      const double mine = p.bias ? key[i] : key_of(z[i]);
+      key[i] = stays ? mine : kLow;
     }
   }
   for (int s = 0; s < p.top; ++s) {
