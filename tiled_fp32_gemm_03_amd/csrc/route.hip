@@ -243,6 +243,13 @@ __global__ void __launch_bounds__(64 * kRouteWaves<LANES>) route_kernel(RoutePro
 //   softmax, renormalised: dz[e] = c r[e] (d[e] - sum_j d[j] r[j]), r = s / sum of the chosen s
 //   sigmoid:               dz[e] = c s[e] (1 - s[e]) d[e]
 //   sigmoid, renormalised: dz[e] = c r[e] (1 - s[e]) (d[e] - sum_j d[j] r[j])
+// A share near 1 leaves little of its difference: with a logit 30 above the others it was
+// off by 3e-4, from 37 on 0.  So 1 - s is 1 / (1 + exp(z)), and tokens with a share above
+// kNear form, over the other choices j (softmax: over other experts, `rest` the share of
+// those not chosen),
+//   d[e] - sum_j d[j] r[j] = sum_j r[j] (d[e] - d[j]) + rest d[e]
+// (for all tokens, 4,097 on 6 of 63 experts, 7.8 us instead of 5.8).
+constexpr double kNear = 1.0 - 0x1p-8;
 template <int FMT, int P>
 __global__ void __launch_bounds__(64 * kRouteWaves<64>) route_backward_kernel(RouteProblem p) {
   const int lane = threadIdx.x & 63;
@@ -251,7 +258,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves<64>) route_backward_kernel(Ro
   const bool softmax = p.score == kSoftmax, all = softmax && !p.renormalize;
   const bool mine = lane < p.top;
   int id = mine ? p.given[t * p.top + lane] : -1;
-  if (id >= p.E) id = -1;
+  if (id < 0 || id >= p.E) id = -1;
   const double d = id >= 0 ? p.scale * (double)p.dgates[t * p.top + lane] : 0.0;
   const double chosen = id >= 0 ? (double)load1<FMT>(p.Z, t * p.ldz + id) : kLow;
   double z[P], zmax = kLow, total = 0.0;
@@ -267,24 +274,52 @@ __global__ void __launch_bounds__(64 * kRouteWaves<64>) route_backward_kernel(Ro
       part += z[i];
     }
     total = token_sum<64>(part);
-    if (total == 0.0) total = 1.0;
   } else if (softmax) {
     zmax = token_max<64>(chosen);
   }
-  // r, the choice's share, and what it is multiplied with
-  double score = 0.0, r = 0.0;
+  double score = 0.0;
   if (id >= 0) score = softmax ? (chosen == kLow ? 0.0 : exp_below(chosen, zmax)) : sigmoid(chosen);
   if (!all) total = p.renormalize ? token_sum<64>(score) : 1.0;
   if (total == 0.0) total = 1.0;
-  r = score / total;
-  const double mean = all || p.renormalize ? token_sum<64>(d * r) : 0.0;
-  const double slope = softmax ? 1.0 : 1.0 - score;
-  const double add = all ? d : r * slope * (d - mean);
+  const double r = id >= 0 ? score / total : 0.0;
+  const double slope = softmax ? 1.0 : sigmoid(-chosen);
+  const bool near = __ballot((all || p.renormalize) && r > kNear) != 0;  // uniform
+  double add, mean = 0.0;
+  unsigned own = 0;  // bit i: `add` is all of the gradient of expert lane + 64 i
+  int of = id;       // -1 where an earlier choice is of the same expert and has its sum
+  if (!near) {
+    if (all || p.renormalize) mean = token_sum<64>(d * r);
+    add = all ? d : r * slope * (d - mean);
+  } else {
+    double sum = d, rest = 0.0;
+    if (all) {
+      sum = 0.0;
+      for (int s = 0; s < p.top; ++s) {
+        const int e = (int)lane_of((uint32_t)id, s);
+        const double v = lane_of(d, s);
+        if (e == id) sum += v;
+        if (e == id && s < lane) of = -1;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if (e == lane + 64 * i) own |= 1u << i;
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) rest += own >> i & 1 ? 0.0 : z[i];
+      rest = token_sum<64>(rest) / total;
+      mean = token_sum<64>(of >= 0 ? sum * r : 0.0);
+    }
+    add = rest > 0.0 ? rest * sum : 0.0;
+    const double share = of >= 0 ? r : 0.0;
+    for (int s = 0; s < p.top; ++s)
+      if ((int)lane_of((uint32_t)of, s) >= 0 && s != lane)
+        add += lane_of(share, s) * (sum - lane_of(sum, s));
+    add *= share * slope;
+  }
   double out[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) out[i] = 0.0;
   for (int s = 0; s < p.top; ++s) {
-    const int e = (int)lane_of((uint32_t)id, s);
+    const int e = (int)lane_of((uint32_t)of, s);
     const double v = lane_of(add, s);
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -294,9 +329,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves<64>) route_backward_kernel(Ro
   for (int i = 0; i < P; ++i) {
     const int e = lane + 64 * i;
     if (e >= p.E) continue;
-    if (all) {
-      out[i] = z[i] / total * (out[i] - mean);
-    }
+    if (all && !(own >> i & 1)) out[i] = z[i] / total * (out[i] - mean);
     store1<FMT>(p.dZ, t * p.lddz + e, (float)out[i]);
   }
 }
