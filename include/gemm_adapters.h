@@ -5,9 +5,11 @@
  * For each of T rows x of X, r = ids[t]:
  *   y = W x + scales[r] B[r] (A[r] x)      r in 0 .. count - 1
  *   y = W x                                any other r: a row without an adapter
- * Sums are held in fp32; scales[r] A[r] x is kept in `format` on its way into the
- * second product (its rounding is of the size of the result's own), and y is rounded
- * once.  Results do not depend on timing.  An infinity or a NaN reaches the rows
+ * Sums are held in fp32, and y is rounded once.  scales[r] A[r] x is rounded to the
+ * precision of `format` on its way into the second product (an error of the size of
+ * the result's own), not to its range: in fp16 each row's values, in groups of up to
+ * 64 ranks, have an exponent of their own (one below 2^-28 of its group's largest may
+ * be lost).  Results do not depend on timing.  An infinity or a NaN reaches the rows
  * that it enters alone: a row's own values, W's, and its own adapter's.
  *
  * Memory, streams and errors are as for gemm_f32 (gemm_f32.h): device

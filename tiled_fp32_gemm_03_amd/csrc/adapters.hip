@@ -5,6 +5,7 @@
 //
 // Bound as any product of such tiles: 8,192 rows, 4096 x 4096, 16 adapters of rank 32 take 255 us,
 // 235 of them in the projection (1.17 PFLOP/s), 16 for A x, 10 for the order, 4 to join.
+#include "adapters_rank.hpp"
 #include "experts_tiles.hpp"
 
 namespace gemm_f32_impl {
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(T::THREADS, kWavesPerSimd<T>) adapters_low_ker
   tile_loop<T, FMT, S>(lds, op, op.share.count, wave, lane);
 }
 
-// v: the parts added in order, times the scale, in 16 bits.  Four values to a thread.
+// v: the parts added in order, times the scale.  Four values to a thread.
 template <int FMT>
 __global__ void __launch_bounds__(256) adapters_join_kernel(AdaptersProblem p) {
   const int per = (int)(p.at.rpitch / 4);
@@ -112,8 +113,7 @@ __global__ void __launch_bounds__(256) adapters_join_kernel(AdaptersProblem p) {
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     if (c >= left) sum[c] = 0.f;
-  *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.v) + 4 * i) =
-      u32x2{pack2<FMT>(sum[0], sum[1]), pack2<FMT>(sum[2], sum[3])};
+  Kept<FMT>::store(ws_at<typename Kept<FMT>::type>(p, p.at.v) + 4 * i, sum);
 }
 
 // ---- the projection -------------------------------------------------------------------
@@ -189,7 +189,7 @@ struct Wide {
     const int *at = ws_at<int>(p, p.at.order.runs) + 4 + 4LL * run;
     const int from = uniform(at[1]) - j.first, to = from + uniform(at[2]);
     const uint16_t *m = p.B + (long long)p.N * uniform(at[0]) * p.ldb;
-    const uint16_t *v = ws_at<uint16_t>(p, p.at.v) + j.first * p.at.rpitch;
+    const auto *v = ws_at<typename Kept<FMT>::type>(p, p.at.v) + j.first * p.at.rpitch;
 #pragma unroll 1
     for (int r0 = 0; r0 < p.R; r0 += 32) {
       const int r = r0 + 8 * g;
@@ -206,14 +206,13 @@ struct Wide {
         const int row0 = 16 * (T::WGM * i + wm);
         if (row0 + 16 <= from || row0 >= to || row0 >= j.rows) continue;  // uniform
         const bool in = row0 + l16 >= from && row0 + l16 < to && row0 + l16 < j.rows;
-        const u32x4 x =
-            *reinterpret_cast<const u32x4 *>(v + (in ? row0 + l16 : row0) * p.at.rpitch + r);
+        const LowRank<FMT, 1> x(v + (in ? row0 + l16 : row0) * p.at.rpitch + r, 1);
 #pragma unroll
         for (int c = 0; c < T::TBN; ++c) {
           const f32x4 sum = mfma_rows<FMT>(__builtin_bit_cast(i16x8, bf[c]),
-                                           __builtin_bit_cast(i16x8, x), f32x4{0, 0, 0, 0});
+                                           __builtin_bit_cast(i16x8, x.v[0]), f32x4{0, 0, 0, 0});
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][c][q] += in ? sum[q] : 0.f;
+          for (int q = 0; q < 4; ++q) acc[i][c][q] += in ? x.back(sum[q]) : 0.f;
         }
       }
     }

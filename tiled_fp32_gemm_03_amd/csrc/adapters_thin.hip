@@ -6,6 +6,7 @@
 //
 // 64 rows, 16384 x 8192, 32 adapters of rank 64: 90 us, 4.0 TB/s of W, A and B; x goes
 // through each compute unit's LDS beside W, as many bytes again.
+#include "adapters_rank.hpp"
 #include "experts_tiles.hpp"
 
 namespace gemm_f32_impl {
@@ -29,7 +30,7 @@ __device__ inline AdaptersProblem rows_of(AdaptersProblem p, int b) {
   p.X += from * p.ldx;
   p.Y += from * p.ldy;
   p.ids += from;
-  p.at.v += 2 * from * p.at.rpitch;
+  p.at.v += 4 * from * p.at.rpitch;
   p.T = p.T - from < kAdaptersThin ? (int)(p.T - from) : kAdaptersThin;
   return p;
 }
@@ -101,9 +102,9 @@ __global__ void __launch_bounds__(64 * kLowWaves) adapters_low_thin_kernel(Adapt
       for (int c = 0; c < 4; ++c)  // zeros from R on
         if (r0 + 4 * g + c >= p.R) acc[c] = 0.f;
       if (m0 + l16 < n)
-        *reinterpret_cast<u32x2 *>(ws_at<uint16_t>(p, p.at.v) + rows[m0 + l16] * p.at.rpitch + r0 +
-                                   4 * g) =
-            u32x2{pack2<FMT>(acc[0], acc[1]), pack2<FMT>(acc[2], acc[3])};
+        Kept<FMT>::store(ws_at<typename Kept<FMT>::type>(p, p.at.v) +
+                             rows[m0 + l16] * p.at.rpitch + r0 + 4 * g,
+                         acc);
     }
     __syncthreads();
   }
@@ -141,17 +142,13 @@ __device__ __forceinline__ void add_adapters(const AdaptersProblem &p, const int
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     const int id = ids[16 * b + l16];
-    const uint16_t *v = ws_at<uint16_t>(p, p.at.v) + order[16 * b + l16] * p.at.rpitch;
+    const auto *v = ws_at<typename Kept<FMT>::type>(p, p.at.v) + order[16 * b + l16] * p.at.rpitch;
     const unsigned any = (unsigned)__ballot(id >= 0) & 0xffffu;
     if (any == 0) continue;  // uniform
 #pragma unroll 1
     for (int r0 = 0; r0 < p.R; r0 += 64) {
       const bool two = r0 + 32 < p.R;  // uniform
-      u32x4 xv[2] = {};
-      if (id >= 0) {
-        xv[0] = *reinterpret_cast<const u32x4 *>(v + r0 + 8 * g);
-        if (two) xv[1] = *reinterpret_cast<const u32x4 *>(v + r0 + 32 + 8 * g);
-      }
+      const LowRank<FMT, 2> x(v + r0 + 8 * g, id < 0 ? 0 : two ? 2 : 1);
       unsigned left = any;
       int item = 0;
       while (left) {  // uniform
@@ -176,10 +173,10 @@ __device__ __forceinline__ void add_adapters(const AdaptersProblem &p, const int
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
           if (e[q] < 0) break;  // uniform
-          f32x4 sum = mfma_16<FMT>(bv[q][0], xv[0], f32x4{0, 0, 0, 0});
-          if (two) sum = mfma_16<FMT>(bv[q][1], xv[1], sum);
+          f32x4 sum = mfma_16<FMT>(bv[q][0], x.v[0], f32x4{0, 0, 0, 0});
+          if (two) sum = mfma_16<FMT>(bv[q][1], x.v[1], sum);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[b][c] += id == e[q] ? sum[c] : 0.f;
+          for (int c = 0; c < 4; ++c) acc[b][c] += id == e[q] ? x.back(sum[c]) : 0.f;
         }
       }
     }

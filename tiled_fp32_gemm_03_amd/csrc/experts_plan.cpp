@@ -115,7 +115,7 @@ AdaptersSpace adapters_space(int T, int N, int K, int R, int count) {
     return from;
   };
   w.rpitch = ceil_div(R, 64) * 64;
-  w.v = take(2 * T * w.rpitch);
+  w.v = take(4LL * T * w.rpitch);
   w.splits = w.wide_splits = 1;
   w.chunk = w.wide_chunk = K;
   if (!adapters_thin(T, N, K)) {

@@ -68,7 +68,7 @@ int adapters_check_sizes(int T, int N, int K, int R, int count);
 struct AdaptersSpace {
   ExpertsSpace order;  // u, part, dh and dg: none
   long long part;      // float [splits][T][rpitch], by place: A x in parts of K
-  long long v;         // 16 bits [T][rpitch], by place (thin: by row): scale A x
+  long long v;         // float (bf16: 16 bits) [T][rpitch], by place (thin: by row): scale A x
   long long bytes;
   long long rpitch;
   int tile;            // rows and columns of the product's tiles
