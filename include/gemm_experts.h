@@ -12,8 +12,11 @@
  *
  * Sums are held in fp32, and results do not depend on timing.  u and, in the
  * backward pass, gates[t][s] u and the gradient of h are kept in `format` between
- * the products; values past its range become infinite.
- * (Up to GEMM_MOE_MAX_TOKENS tokens without `saved` they may be kept in fp32.)
+ * the products: in fp16 values past 65,504 become infinite, and those below 2^-14 lose
+ * bits.  Without `saved`, up to GEMM_MOE_MAX_TOKENS tokens and 6 choices to an expert
+ * (T top <= 6 E, and always for MX weights), u is kept in fp32.  So with `saved`, or
+ * among more tokens, a token's result may differ in its last bits, and in fp16 may be
+ * infinite where it is not otherwise.
  * An infinity or a NaN reaches what is computed from it: a token's own rows, and
  * the weights' gradients of its experts.
  *

@@ -1104,7 +1104,9 @@ def moe_experts(X, ids, gates, w1, w2, save: bool = False, out=None, workspace=N
     is a dropped choice, gates (T, top) float32; w1 is (E, 2 I, H) and w2 (E, H, I),
     tensors of X's dtype or, up to 256 tokens and without ``save``, stacks of MX matrices.
     Returns Y, (T, H) in X's dtype; with ``save`` (Y, saved), the second for
-    moe_experts_backward.  ``workspace`` is a uint8 CUDA tensor of at least
+    moe_experts_backward.  u is kept in X's dtype (in float16 infinite past 65,504) but for a
+    few tokens without ``save`` (T top <= 6 E, T <= 256), where it is kept in float32.
+    ``workspace`` is a uint8 CUDA tensor of at least
     gemm_experts_workspace_bytes; when None, one is allocated with torch for this call.
     """
     device, T, E, top, H, I, ldx, a1, a2 = _experts_sizes(X, ids, gates, w1, w2)
