@@ -25,17 +25,6 @@ __device__ inline int expert_of(const ExpertsProblem &p, long long pair, long lo
   return e >= 0 && e < last ? e : p.rest ? p.E - 1 : kMoeMaxExperts;
 }
 
-// Lanes of the wave whose pair has the same expert.
-__device__ inline unsigned long long same_expert(int e) {
-  unsigned long long same = ~0ULL;
-#pragma unroll
-  for (int b = 0; b < 10; ++b) {
-    const unsigned long long m = __ballot((e >> b) & 1);
-    same &= (e >> b) & 1 ? m : ~m;
-  }
-  return same;
-}
-
 // Counts of pairs from .. from + pairs' by expert, onto zeros in `count`.
 template <int THREADS>
 __device__ inline void count_pairs(const ExpertsProblem &p, int *count, long long from, long long to,

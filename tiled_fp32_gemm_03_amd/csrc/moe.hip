@@ -168,17 +168,6 @@ __device__ inline void choose_experts(const MoeProblem &p, Route<MAX_PAIRS> &r, 
   if (lane < p.top) r.gate[slot * p.top + lane] = (float)(w / total);
 }
 
-// Lanes of the wave whose pair has the same expert as this lane's.
-__device__ inline unsigned long long same_expert(int e) {
-  unsigned long long same = ~0ULL;
-#pragma unroll
-  for (int b = 0; b < 10; ++b) {
-    const unsigned long long m = __ballot((e >> b) & 1);
-    same &= (e >> b) & 1 ? m : ~m;
-  }
-  return same;
-}
-
 // The lists of chosen pairs, from r.chosen.
 template <int THREADS, int MAX_PAIRS>
 __device__ inline void list_pairs(const MoeProblem &p, Route<MAX_PAIRS> &r) {

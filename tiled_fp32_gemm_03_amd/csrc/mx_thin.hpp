@@ -246,6 +246,16 @@ __device__ inline bool widens_fast(uint32_t sb, uint32_t codes) {
 
 // The wave's number in its workgroup, as a scalar.
 __device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+// Lanes of the wave whose expert number (0 .. 1023) is the same as this lane's.
+__device__ inline unsigned long long same_expert(int e) {
+  unsigned long long same = ~0ULL;
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {
+    const unsigned long long m = __ballot((e >> b) & 1);
+    same &= (e >> b) & 1 ? m : ~m;
+  }
+  return same;
+}
 
 // ---- weights -----------------------------------------------------------------
 //
