@@ -119,7 +119,16 @@ AdaptersSpace adapters_space(int T, int N, int K, int R, int count) {
   w.splits = w.wide_splits = 1;
   w.chunk = w.wide_chunk = K;
   if (!adapters_thin(T, N, K)) {
-    w.tile = ceil_div(T, 256) * ceil_div(N, 256) >= 192 ? 256 : 128;
+    // Tiles of 256 where those of 128 are more than the chip holds at once (else they take
+    // K in parts) and the modelled time is less, with a tenth off for the larger ones.  128
+    // and 256, us (rows, N x K): 2,048, 4096 x 1024 41 and 60; 1,280, 6656 x 4096 123 and
+    // 115; 512, 18432 x 8192 289 and 209; 20,000, 300 x 4096 114 and 145; 20,000, 390 x
+    // 4096 166 and 147; 8,192, 1536 x 4096 161 and 127; 4,096, 4096 x 4096 161 and 136;
+    // 100,000, 100 x 4096 481 and 533; 100,000, 160 x 2048 328 and 312.  Of 47 sizes the
+    // rule loses 10% in two: 33,000, 500 x 2048 141 and 156; 30,000, 640 x 1024 106 and 115.
+    const long long wide = ceil_div(T, 128) * ceil_div(N, 128), large = ceil_div(T, 256) * ceil_div(N, 256);
+    const double steps = K / 64.0;
+    w.tile = wide > 512 && 0.9 * tiles_us(256, large, steps) < tiles_us(128, wide, steps) ? 256 : 128;
     // The products with A: row tiles of kAdaptersRows, K in parts until there are
     // two workgroups to a compute unit, of 256 values at least.
     const long long tiles = (ceil_div(T, kAdaptersRows) + count / 2) * ceil_div(R, kAdaptersRows);
@@ -127,11 +136,10 @@ AdaptersSpace adapters_space(int T, int N, int K, int R, int count) {
     w.chunk = (int)(ceil_div(ceil_div(K, w.splits), 64) * 64);
     w.splits = (int)ceil_div(K, w.chunk);
     w.part = take(4LL * w.splits * T * w.rpitch);
-    // The projection: K in parts while there are two to a compute unit at most, of 512
-    // values at least (a compute unit is fed 35 to 45 KB a microsecond, so few tiles
+    // The projection: K in parts while there are two tiles to a compute unit at most, of
+    // 512 values at least (a compute unit is fed 35 to 45 KB a microsecond, so few tiles
     // take long however they are scheduled).
-    const long long wide = ceil_div(T, w.tile) * ceil_div(N, w.tile);
-    while (2 * wide * w.wide_splits <= (w.tile == 256 ? 256 : 512) && ceil_div(K, 2 * w.wide_splits) >= 512) w.wide_splits *= 2;
+    while (2 * wide * w.wide_splits <= 512 && ceil_div(K, 2 * w.wide_splits) >= 512) w.wide_splits *= 2;
     w.wide_chunk = (int)(ceil_div(ceil_div(K, w.wide_splits), 64) * 64);
     w.wide_splits = (int)ceil_div(K, w.wide_chunk);
     w.npitch = ceil_div(N, 8) * 8;
