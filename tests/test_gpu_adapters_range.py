@@ -72,3 +72,25 @@ def test_fp16_range(g, case):
     got = g.matmul_adapters(x, w, a, b, ids, scales)
     off = (got.double() - value).abs() - (bound * (1 + HS) + HS * value.abs() + TINY)
     assert torch.isfinite(got).all() and float(off.max()) <= 0, (case, float(off.max()))
+
+
+@pytest.mark.parametrize("T", [1, 30, 64, 65, 700])
+def test_one_requests_infinities_are_its_own(g, T):
+    """As for bf16 in test_gpu_adapters.py: the other rows' results as they are, to the bit."""
+    import test_gpu_adapters as adapters
+    print(f"case: adapters fp16 infinities {T}", flush=True)
+    x, w, a, b, i, s = adapters._make(T, 200, 256, 70, 4, torch.float16, ids=np.arange(T) % 4)
+    want = g.matmul_adapters(x, w, a, b, i, s)
+    own = i == 2
+    for name in ("a nan", "a inf", "b", "scale", "scale nan"):
+        a2, b2, s2 = a.clone(), b.clone(), s.clone()
+        if name[0] == "a":
+            a2[2, 5] = float(name[2:])
+        elif name == "b":
+            b2[2, ::2] = float("inf")
+            b2[2, 1::2] = float("nan")
+        else:
+            s2[2] = float("inf") if name == "scale" else float("nan")
+        got = g.matmul_adapters(x, w, a2, b2, i, s2)
+        assert torch.equal(got[~own], want[~own]), (T, name)
+        assert not torch.isfinite(got[own]).any() if name != "b" else not own.any() or not torch.isfinite(got[own]).all(), (T, name)
