@@ -40,7 +40,8 @@ long long gemm_adapters_workspace_bytes(int T, int N, int K, int R, int count);
  *   R         the adapters' rank, 1 .. GEMM_ADAPTERS_MAX_RANK
  *   count     adapters, 0 .. GEMM_ADAPTERS_MAX_COUNT (0: A and B are not read)
  *   X, W, Y   T x K, N x K and T x N in `format` (GEMM_MIXED_BF16 or
- *             GEMM_MIXED_F16), 2-byte aligned, pitches in elements
+ *             GEMM_MIXED_F16), 2-byte aligned, pitches in elements.  (Of more than
+ *             2^31 bytes, X or W, many rows take nearly twice as long.)
  *   A         count * R rows of K values: adapter r's rows from R r on
  *   B         count * N rows of R values: adapter r's rows from N r on
  *   ids       T int

@@ -48,7 +48,8 @@ long long gemm_experts_workspace_bytes(int T, int E, int top, int H, int I, int 
  *   E, top    1 .. 512 (GEMM_MOE_MAX_EXPERTS) and 1 .. 16 (GEMM_MOE_MAX_TOP)
  *   H, I      1 .. GEMM_EXPERTS_MAX_WIDTH
  *   X         T x H in `format` (GEMM_MIXED_BF16 or GEMM_MIXED_F16), 2-byte
- *             aligned, pitches in elements
+ *             aligned, pitches in elements.  (Of more than 2^31 bytes, 2 T ldx, a call
+ *             takes half as long again, and so with dY; two calls do not.)
  *   ids       T x top int, gates T x top float, contiguous
  *   W1        E * 2I rows of H values: expert e's rows from 2I e on
  *   W2        E * H rows of I values: expert e's rows from H e on

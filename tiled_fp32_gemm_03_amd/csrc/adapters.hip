@@ -3,8 +3,10 @@
 // parts, then the projection's tiles, which add B[r] of scale A[r] x for each run of
 // rows with one adapter before they are stored.
 //
-// Bound as any product of such tiles: 8,192 rows, 4096 x 4096, 16 adapters of rank 32 take 255 us,
-// 235 of them in the projection (1.17 PFLOP/s), 16 for A x, 10 for the order, 4 to join.
+// Bound as any product of such tiles: 8,192 rows, 4096 x 4096, 16 adapters of rank 32 take 254
+// to 271 us by box, a call among others (1.03 to 1.10 PFLOP/s).  Traced, calls apart from
+// one another take 300: 265 in the projection (238 at least), 18 for A x, 11 for the order,
+// 6 to join.
 #include "adapters_rank.hpp"
 #include "experts_tiles.hpp"
 

@@ -1,8 +1,9 @@
 // A shared projection with low-rank adapters for few rows (gemm_adapters.h), 64 at a
 // time: single tokens of many requests.  Two launches: scale A[r] x by a workgroup to each
 // adapter that is asked and 16 of its ranks, and the projection, which reads W once,
-// through a ring of LDS stages or, matrices that this cannot address, straight into the
-// matrix instructions' operands (mx_thin.hpp), and the asked adapters' B.
+// through a ring of LDS stages or, where a matrix starts in the middle of a word or 16 rows
+// of W (64 of X) pass 2^31 bytes, straight into the matrix instructions' operands
+// (mx_thin.hpp), and the asked adapters' B.
 //
 // 64 rows, 16384 x 8192, 32 adapters of rank 64: 90 us, 4.0 TB/s of W, A and B; x goes
 // through each compute unit's LDS beside W, as many bytes again.
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kThinThreads) adapters_rounds_kernel(AdaptersP
   store_rows<FMT, RB>(p, lds, order, columns, KS, first, acc);
 }
 
-// ---- any matrices, also of 2^31 bytes and more ---------------------------------------------
+// ---- matrices that start in the middle of a word, and pitches past the ring's offsets ------
 // x waits in LDS, the weights of two pieces of 128 values are on their way while a third
 // is used.
 constexpr int kThinLds = 74 * 1024;  // of x: two workgroups to a compute unit

@@ -13,8 +13,13 @@ namespace {
 // ---- the order of the pairs ----------------------------------------------------
 // A stable sort by expert: counts, their sums, then each pair's place.  Up to
 // kOneLaunch pairs in one launch, whose workgroups each count all pairs, and take
-// kListPairs of them; more in three launches (16,384 pairs, 64 experts: 12 us against
-// 15 in three; 3,063 pairs of 7 experts 6).  Pairs whose expert is not in 0 .. E - 1 get no place.
+// kListPairs of them; more in three launches, the sums by one workgroup.  One launch and
+// three, us, by experts (64, 512, 8, 1): 4,096 pairs 5.7, 6.2, 5.6, 7.5 and 11.1, 13.0,
+// 10.5, 11.6; 65,536 16.0, 17.1, 17.5, 52.5 and 16.4, 19.5, 18.6, 35.9; 131,072 26.7,
+// 28.4, 30.3, 99.9 and 22.8, 27.2, 26.2, 60.6.  Three at 2^20 pairs 115, 145, 144, 418; at
+// 2^22 433, 867, 548, 1,655; at 2^26 11,500, 14,800, 10,700, 26,900: linear, and beside
+// 262,144 tokens' products of 7,500 (8 experts, 4096 / 1024) 45.  Pairs whose expert is
+// not in 0 .. E - 1 get no place.
 
 constexpr int kMostGroups = 1 << 20;
 constexpr int kOneLaunch = 1 << 16, kOneThreads = kListPairs, kListThreads = 256;

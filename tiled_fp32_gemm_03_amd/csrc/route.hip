@@ -3,7 +3,7 @@
 // order of experts next to a tie does not depend on how an exponential was rounded.
 //
 // What bounds it is the instructions, half of them the 64-bit exponentials: 16,384
-// tokens, 256 experts, sigmoid scores, a bias, 4 of 8 groups, top 8 take 23 us (their 17
+// tokens, 256 experts, sigmoid scores, a bias, 4 of 8 groups, top 8 take 23 to 26 us by box (their 17
 // MB of logits 3.3).
 #include "launch_util.hpp"
 #include "mx_thin.hpp"
